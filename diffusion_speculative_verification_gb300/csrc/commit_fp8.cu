@@ -1,0 +1,269 @@
+// ssv_commit_fp8: commit of a verification pass into an e4m3 paged cache.
+//
+// Which rows are appended and where is ssv_commit's rule (SimSD summary,
+// section 4 "Speculative decoding pipeline").  Per touched (page, head), K and
+// V apart, with X the rows appended to the page:
+//   s = 2^e, e smallest with max |X| <= 448 2^e;  s = max(s_old, s) if the page
+//   already holds rows of the sequence;  codes = rn_e4m3(X / s), and the rows
+//   already there become rn_e4m3(code * s_old / s) when s grew.
+//
+// Work: one CTA per (chunk of page_size packed rows, head, K or V).  A page is
+// led by the first token appended to it; the tokens' append indices i < N +
+// n_acc are counted along the packed rows from q_off, so a chunk of page_size
+// rows holds one leader per page boundary or sequence start in it, and the
+// number of CTAs follows from total_rows alone, however ragged the batch.
+// The rows of a page stay in registers between the maximum and the rounding:
+// each element is read once and each code written once.  Bound by HBM for
+// prompts, by latency (table, stage map, rows: three dependent rounds) for a
+// decode pass.
+#include "ssv_internal.cuh"
+#include "paged.cuh"
+
+#include <math.h>
+
+namespace ssv {
+namespace {
+
+constexpr int kC8Threads = 256;
+constexpr int kScaleMin = -100;  // exponent of an all-zero page's scale
+
+struct Commit8Params {
+  const uint8_t *k_new, *v_new;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  const int32_t* pages;
+  const ssv_seq* seqs;
+  const int32_t *tau, *n_acc;
+  int32_t *new_len, *dev_status;
+  int64_t k_stride, v_stride;  // bytes
+  int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunks;
+};
+
+// The checks of sequence s that need no loop, na its accepted stages.
+__device__ __forceinline__ bool commit8_sizes(const Commit8Params& p, const ssv_seq& s, int na) {
+  const int B = s.block, N = s.new_len, C = s.cache_len;
+  if (B < 1 || B > 64 || B > p.max_block || N < 0 || N > p.max_new || C < 0 || na < 0 || na > B) return false;
+  if (s.tau_off < 0 || (long long)s.tau_off + B > p.total_slots) return false;
+  if (s.q_off < 0 || (long long)s.q_off + N + 2LL * B > p.total_rows) return false;
+  const long long len = (long long)C + N + na, pages = (len + (1 << p.ps_log2) - 1) >> p.ps_log2;
+  return len <= 0x7fffffffLL && s.kv_off >= 0 && s.kv_off + pages <= p.table_len;
+}
+
+// Whether lane `first` of `step` sees a bad page among the touched ones.
+__device__ __forceinline__ bool commit8_bad_page(const Commit8Params& p, const ssv_seq& s, int na, int first, int step) {
+  const int app = s.new_len + na;
+  if (app == 0) return false;
+  const int j1 = (s.cache_len + app - 1) >> p.ps_log2;
+  bool bad = false;
+  for (int j = (s.cache_len >> p.ps_log2) + first; j <= j1; j += step) {
+    const int page = p.pages[s.kv_off + j];
+    bad |= page < 0 || page >= p.n_pages;
+  }
+  return bad;
+}
+
+// bits of 2^e with e the smallest integer >= kScaleMin such that amax <= 448 * 2^e
+__device__ __forceinline__ float scale_for(float amax) {
+  if (!(amax > 0.f)) return exp2f((float)kScaleMin);
+  int x;
+  const float f = frexpf(amax, &x);  // amax = f 2^x, 448 = 0.875 * 2^9
+  return ldexpf(1.f, max(x - (f <= 0.875f ? 9 : 8), kScaleMin));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kC8Threads) commit_fp8_kernel(const Commit8Params p) {
+  constexpr int VEC = 16 / (int)sizeof(T), LANES = D / VEC;  // threads per row
+  constexpr int ROWS = kC8Threads / LANES;                   // rows per pass
+  constexpr int PASSES = 128 / ROWS;
+  __shared__ int s_lead[128], s_inv[64], s_nlead;
+  __shared__ float s_max[kC8Threads / 32];
+  __shared__ ssv_seq s_seq[kC8Threads];
+  pdl_wait();  // n_acc and the fresh rows may come from the kernels before this one
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ps = 1 << p.ps_log2;
+  if ((int)blockIdx.x >= p.chunks) {
+    // new lengths and statuses: one warp per sequence
+    const int b = (blockIdx.x - p.chunks) * (kC8Threads / 32) + warp;
+    if (b >= p.batch || blockIdx.y > 0) return;
+    const ssv_seq s = p.seqs[b];
+    const int na = p.n_acc[b];
+    int bad = 0;
+    if (!seq_idle(s)) {
+      if (!commit8_sizes(p, s, na)) bad = SSV_ERR_INVALID;
+      else if (!warp_tau_is_permutation(p.tau + s.tau_off, s.block)) bad = SSV_ERR_BAD_TAU;
+      else if (__any_sync(0xffffffffu, commit8_bad_page(p, s, na, lane, 32))) bad = SSV_ERR_INVALID;
+    }
+    if (lane == 0) {
+      if (bad) report(p.dev_status, bad);
+      p.new_len[b] = bad ? -1 : (seq_idle(s) ? s.cache_len : s.cache_len + s.new_len + na);
+    }
+    return;
+  }
+  // ---- leaders of this chunk's rows
+  const bool table = p.batch <= kC8Threads;
+  if (table && (int)threadIdx.x < p.batch) s_seq[threadIdx.x] = p.seqs[threadIdx.x];
+  if (threadIdx.x == 0) s_nlead = 0;
+  __syncthreads();
+  if ((int)threadIdx.x < ps) {
+    const int row = blockIdx.x * ps + threadIdx.x;
+    const int b = row < p.total_rows ? find_seq_by_row(table ? s_seq : p.seqs, p.batch, row) : -1;
+    if (b >= 0) {
+      const ssv_seq s = table ? s_seq[b] : p.seqs[b];
+      const int i = row - s.q_off;
+      const int na = p.n_acc[b];
+      if (!seq_idle(s) && commit8_sizes(p, s, na) && i < s.new_len + na &&
+          (i == 0 || ((s.cache_len + i) & (ps - 1)) == 0))
+        s_lead[atomicAdd(&s_nlead, 1)] = row;
+    }
+  }
+  __syncthreads();
+  const int nlead = s_nlead;
+  const int head = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const uint8_t* fresh = (is_v ? p.v_new : p.k_new) + (int64_t)head * D * sizeof(T);
+  const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  for (int l = 0; l < nlead; ++l) {
+    const int row = s_lead[l];
+    const int b = find_seq_by_row(table ? s_seq : p.seqs, p.batch, row);
+    const ssv_seq s = table ? s_seq[b] : p.seqs[b];
+    const int N = s.new_len, B = s.block, na = p.n_acc[b], i0 = row - s.q_off;
+    // the whole sequence is good, or nothing of it is written
+    int bad = commit8_bad_page(p, s, na, threadIdx.x, kC8Threads);
+    if (warp == 0) bad |= !warp_tau_is_permutation(p.tau + s.tau_off, B);
+    if (__syncthreads_or(bad)) continue;
+    if ((int)threadIdx.x < B) s_inv[p.tau[s.tau_off + threadIdx.x] - 1] = threadIdx.x;  // slot of each stage
+    __syncthreads();
+    const int t0 = s.cache_len + i0, o0 = t0 & (ps - 1);            // first appended row of the page
+    const int n = min(ps - o0, N + na - i0);                        // rows appended to it
+    const int64_t at = (int64_t)p.pages[s.kv_off + (t0 >> p.ps_log2)] * p.Hkv + head;
+    uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + at * ps * D;
+    float* scale = (is_v ? p.v_scale : p.k_scale) + at;
+    const float s_old = o0 > 0 ? *scale : 0.f;
+    const int lr = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    uint4 x[PASSES];
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const int r = k * ROWS + lr;
+      if (r >= n) continue;
+      const int i = i0 + r;
+      const int src = s.q_off + (i < N ? i : N + s_inv[i - N]);
+      x[k] = *reinterpret_cast<const uint4*>(fresh + src * stride + c * 16);
+    }
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      if (k * ROWS + lr >= n) continue;
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          const float a = fabsf(__uint_as_float(w[e]));
+          if (a < INFINITY) amax = fmaxf(amax, a);
+        } else {
+          const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+          if (lo < INFINITY) amax = fmaxf(amax, lo);
+          if (hi < INFINITY) amax = fmaxf(amax, hi);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) s_max[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kC8Threads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    const float sc = fmaxf(scale_for(amax), s_old);
+    const float inv = 1.f / sc;  // a power of two, exact
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const int r = k * ROWS + lr;
+      if (r >= n) continue;
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      float f[VEC];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          f[e] = __uint_as_float(w[e]);
+        } else {
+          f[2 * e] = __uint_as_float(w[e] << 16);
+          f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+      }
+      uint16_t q[VEC / 2];
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        // infinities become NaN (the conversion would clamp them to a finite code)
+        const float lo = fabsf(f[e]) < INFINITY ? f[e] * inv : NAN, hi = fabsf(f[e + 1]) < INFINITY ? f[e + 1] * inv : NAN;
+        q[e / 2] = f32_to_e4m3x2(lo, hi);
+      }
+      uint8_t* dst = cache + (o0 + r) * D + c * VEC;
+      if constexpr (VEC == 8) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
+      } else {
+        *reinterpret_cast<uint32_t*>(dst) = q[0] | (uint32_t)q[1] << 16;
+      }
+    }
+    if (o0 > 0 && sc > s_old) {
+      // the rows already there, 16 codes at a time
+      const float ratio = s_old * inv;
+      for (int v = threadIdx.x; v < o0 * D / 16; v += kC8Threads) {
+        uint4 raw = reinterpret_cast<const uint4*>(cache)[v];
+        uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t out = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t f2 = e4m3x2_to_f16x2((uint16_t)(w[e] >> (16 * h)));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
+            out |= (uint32_t)f32_to_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+          }
+          w[e] = out;
+        }
+        reinterpret_cast<uint4*>(cache)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    if (threadIdx.x == 0) *scale = sc;
+    __syncthreads();  // s_inv, s_max are reused; every thread has read the old scale
+  }
+}
+
+}  // namespace
+}  // namespace ssv
+
+extern "C" ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream) {
+  using namespace ssv;
+  if (!a) return SSV_ERR_INVALID;
+  if (a->batch < 0 || a->total_rows < 0 || a->total_slots < 0 || a->table_len < 0 || a->n_pages < 0 || a->Hkv <= 0 ||
+      a->max_new < 0 || a->max_block < 1 || a->max_block > 64 || !page_size_ok(a->page_size))
+    return SSV_ERR_INVALID;
+  if (a->dtype != SSV_F32 && a->dtype != SSV_BF16) return SSV_ERR_INVALID;
+  if (a->d != 64 && a->d != 128) return SSV_ERR_UNSUPPORTED;
+  if (a->batch == 0) return SSV_OK;
+  if (!a->seqs || !a->n_acc || !a->new_len) return SSV_ERR_INVALID;
+  if (a->total_rows > 0 && (!a->k_new || !a->v_new || !a->tau)) return SSV_ERR_INVALID;
+  if ((a->n_pages > 0 && (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale)) || (a->table_len > 0 && !a->pages))
+    return SSV_ERR_INVALID;
+  if (a->Hkv > 32767 || (long long)a->n_pages * a->page_size > 0x7fffffffLL) return SSV_ERR_INVALID;
+  const int64_t es = a->dtype == SSV_BF16 ? 2 : 4, width = (int64_t)a->Hkv * a->d;
+  const int64_t ks = a->k_stride ? a->k_stride : width, vs = a->v_stride ? a->v_stride : width;
+  if (ks < width || vs < width) return SSV_ERR_INVALID;
+  const uintptr_t al = (uintptr_t)a->k_new | (uintptr_t)a->v_new | (uintptr_t)a->k_cache | (uintptr_t)a->v_cache |
+                       (uintptr_t)(ks * es) | (uintptr_t)(vs * es);
+  if (al & 15u) return SSV_ERR_INVALID;
+  Commit8Params p{static_cast<const uint8_t*>(a->k_new), static_cast<const uint8_t*>(a->v_new),
+                  static_cast<uint8_t*>(a->k_cache), static_cast<uint8_t*>(a->v_cache), a->k_scale, a->v_scale,
+                  a->pages, a->seqs, a->tau, a->n_acc, a->new_len, a->dev_status, ks * es, vs * es, a->Hkv,
+                  ilog2(a->page_size), a->n_pages, a->table_len, a->batch, a->total_rows, a->total_slots, a->max_new,
+                  a->max_block, (int)(((long long)a->total_rows + a->page_size - 1) / a->page_size)};
+  const dim3 grid(p.chunks + (a->batch + 7) / 8, 2 * a->Hkv);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (a->dtype == SSV_BF16)
+    e = a->d == 128 ? launch_pdl(commit_fp8_kernel<__nv_bfloat16, 128>, grid, dim3(kC8Threads), 0, st, p)
+                    : launch_pdl(commit_fp8_kernel<__nv_bfloat16, 64>, grid, dim3(kC8Threads), 0, st, p);
+  else
+    e = a->d == 128 ? launch_pdl(commit_fp8_kernel<float, 128>, grid, dim3(kC8Threads), 0, st, p)
+                    : launch_pdl(commit_fp8_kernel<float, 64>, grid, dim3(kC8Threads), 0, st, p);
+  return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;
+}

@@ -216,6 +216,7 @@ extern "C" const char* ssv_status_string(ssv_status s) {
     case SSV_ERR_BAD_TAU: return "stage map is not a permutation of 1..B";
     case SSV_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case SSV_ERR_NOT_FINITE: return "temperature not finite or negative";
+    case SSV_ERR_NO_PAGES: return "not enough free pages";
   }
   return "unknown status";
 }

@@ -18,6 +18,7 @@ from .build import LIB
 
 SSV_OK, SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED, SSV_ERR_CUDA = 0, 1, 2, 3
 SSV_ERR_TIMEOUT, SSV_ERR_BAD_TAU, SSV_ERR_WORKSPACE, SSV_ERR_NOT_FINITE = 4, 5, 6, 7
+SSV_ERR_NO_PAGES = 8
 SSV_F32, SSV_BF16 = 0, 1
 ARGMAX, GUMBEL, REJECT, GUMBEL_GEN = 0, 1, 2, 3
 
@@ -26,7 +27,8 @@ EXPORTS = ("ssv_rope_copy", "ssv_verify_attn_workspace", "ssv_verify_attn", "ssv
            "ssv_accept", "ssv_accept_noalloc", "ssv_commit", "ssv_lmhead_accept_workspace", "ssv_lmhead_accept",
            "ssv_get_status", "ssv_status_string", "ssv_version", "ssv_bench", "ssv_set_fault_injection",
            "ssv_tree_verify_attn_workspace", "ssv_tree_verify_attn", "ssv_tree_accept_workspace", "ssv_tree_accept",
-           "ssv_stream_read")
+           "ssv_stream_read", "ssv_page_plan", "ssv_norm_rope_copy", "ssv_verify_attn_fp8_workspace",
+           "ssv_verify_attn_fp8", "ssv_commit_fp8")
 FAULT_NONE, FAULT_ATTN, FAULT_ACCEPT, FAULT_LMHEAD = 0, 1, 2, 3
 
 
@@ -107,6 +109,45 @@ class LmheadArgs(C.Structure):
                 ("n_out", C.c_void_p), ("tokens", C.c_void_p), ("dev_status", C.c_void_p)]
 
 
+class PagePlanArgs(C.Structure):
+    _fields_ = [("cache_len", C.c_void_p), ("new_len", C.c_void_p), ("block", C.c_void_p), ("held", C.c_void_p),
+                ("pages", C.c_void_p), ("free_list", C.c_void_p), ("n_free", C.c_void_p), ("batch", C.c_int32),
+                ("max_pages", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("total_rows", C.c_int32), ("seqs", C.c_void_p), ("slot_map", C.c_void_p),
+                ("slot_off", C.c_void_p), ("held_out", C.c_void_p), ("n_free_out", C.c_void_p),
+                ("dev_status", C.c_void_p)]
+
+
+class NormRopeArgs(C.Structure):
+    _fields_ = [("q_in", C.c_void_p), ("k_in", C.c_void_p), ("q_out", C.c_void_p), ("k_out", C.c_void_p),
+                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("q_in_stride", C.c_int64),
+                ("k_in_stride", C.c_int64), ("q_out_stride", C.c_int64), ("k_out_stride", C.c_int64),
+                ("dtype", C.c_int), ("Hq", C.c_int32), ("Hkv", C.c_int32), ("d", C.c_int32), ("eps", C.c_float),
+                ("base", C.c_double), ("seqs", C.c_void_p), ("batch", C.c_int32), ("total_rows", C.c_int32),
+                ("positions", C.c_void_p), ("dev_status", C.c_void_p)]
+
+
+class AttnFp8Args(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k_cache", C.c_void_p), ("v_cache", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("pages", C.c_void_p), ("k_new", C.c_void_p), ("v_new", C.c_void_p),
+                ("o", C.c_void_p), ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("Hq", C.c_int32),
+                ("Hkv", C.c_int32), ("d", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("table_len", C.c_int32), ("scale", C.c_float), ("seqs", C.c_void_p), ("batch", C.c_int32),
+                ("tau", C.c_void_p), ("total_rows", C.c_int32), ("total_slots", C.c_int32),
+                ("max_cache", C.c_int32), ("max_new", C.c_int32), ("max_block", C.c_int32),
+                ("dev_status", C.c_void_p)]
+
+
+class CommitFp8Args(C.Structure):
+    _fields_ = [("k_new", C.c_void_p), ("v_new", C.c_void_p), ("k_cache", C.c_void_p), ("v_cache", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("pages", C.c_void_p), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("dtype", C.c_int), ("Hkv", C.c_int32), ("d", C.c_int32),
+                ("page_size", C.c_int32), ("n_pages", C.c_int32), ("table_len", C.c_int32), ("seqs", C.c_void_p),
+                ("batch", C.c_int32), ("tau", C.c_void_p), ("n_acc", C.c_void_p), ("new_len", C.c_void_p),
+                ("total_rows", C.c_int32), ("total_slots", C.c_int32), ("max_new", C.c_int32),
+                ("max_block", C.c_int32), ("dev_status", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -140,11 +181,18 @@ def lib():
         L.ssv_tree_verify_attn.argtypes = [C.POINTER(TreeAttnArgs), vp, sz, vp]
         L.ssv_tree_accept_workspace.argtypes = [C.POINTER(TreeAcceptArgs), C.POINTER(sz)]
         L.ssv_tree_accept.argtypes = [C.POINTER(TreeAcceptArgs), vp, sz, vp]
+        L.ssv_page_plan.argtypes = [C.POINTER(PagePlanArgs), vp]
+        L.ssv_norm_rope_copy.argtypes = [C.POINTER(NormRopeArgs), vp]
+        L.ssv_verify_attn_fp8_workspace.argtypes = [C.POINTER(AttnFp8Args), C.POINTER(sz)]
+        L.ssv_verify_attn_fp8.argtypes = [C.POINTER(AttnFp8Args), vp, sz, vp]
+        L.ssv_commit_fp8.argtypes = [C.POINTER(CommitFp8Args), vp]
         for name in ("ssv_rope_copy", "ssv_verify_attn_workspace", "ssv_verify_attn", "ssv_verify_step",
                      "ssv_accept_workspace", "ssv_accept", "ssv_accept_noalloc", "ssv_commit",
                      "ssv_lmhead_accept_workspace", "ssv_lmhead_accept", "ssv_get_status", "ssv_bench",
                      "ssv_set_fault_injection", "ssv_tree_verify_attn_workspace", "ssv_tree_verify_attn",
-                     "ssv_tree_accept_workspace", "ssv_tree_accept", "ssv_stream_read"):
+                     "ssv_tree_accept_workspace", "ssv_tree_accept", "ssv_stream_read", "ssv_page_plan",
+                     "ssv_norm_rope_copy", "ssv_verify_attn_fp8_workspace", "ssv_verify_attn_fp8",
+                     "ssv_commit_fp8"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -210,6 +258,18 @@ class Batch:
         self.max_cache = int(h[:, 0].max()) if self.batch else 0
         self.max_new = int(h[:, 1].max()) if self.batch else 0
         self.max_block = int(h[:, 2].max()) if self.batch else 1
+
+    @classmethod
+    def from_device(cls, seqs, total_rows: int, total_slots: int, max_cache: int, max_new: int, max_block: int):
+        """A batch whose table exists on the device only (int32 [batch, 6], as
+        page_plan writes it), with bounds that the caller states: the rows
+        packed, the slots, and the largest C, N and B that any record may
+        have.  For the operators over the paged cache."""
+        x = cls.__new__(cls)
+        x.host, x.dev, x.batch = None, seqs, seqs.shape[0]
+        x.total_rows, x.total_cache, x.total_slots = total_rows, 0, total_slots
+        x.max_cache, x.max_new, x.max_block = max_cache, max_new, max_block
+        return x
 
 
 def _workspace(nbytes: int, device, ws=None):
@@ -469,6 +529,165 @@ def tree_accept(mode, T, logits, seqs, parent, pos, token, noise=None, noise_row
     _check(lib().ssv_tree_accept(C.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
            "ssv_tree_accept")
     return n_acc, path, ep, et
+
+
+# ---------------------------------------------------------------------------
+# the paged 8-bit KV cache
+# ---------------------------------------------------------------------------
+def _rows_strided(t, what: str) -> int:
+    """Row stride (elements) of a [rows, heads, d] tensor whose heads are contiguous."""
+    s = t.stride()
+    if t.dim() != 3 or (t.shape[0] and (s[2] != 1 or (s[1] != t.shape[2] and t.shape[1] > 1))):
+        raise SsvError(SSV_ERR_INVALID, f"{what}: [rows, heads, d] with contiguous heads")
+    return s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what: str):
+    """(Hkv, page_size, d, n_pages) of a paged e4m3 cache, checked."""
+    torch = _torch()
+    for x in (k_cache, v_cache):
+        if x.dtype not in (torch.uint8, torch.float8_e4m3fn) or x.dim() != 4 or not x.is_contiguous():
+            raise SsvError(SSV_ERR_INVALID, f"{what}: caches are contiguous e4m3 [n_pages, Hkv, page_size, d]")
+    n, hkv, ps, d = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: cache shapes differ")
+    for x in (k_scale, v_scale):
+        if x.dtype != torch.float32 or tuple(x.shape) != (n, hkv) or not x.is_contiguous():
+            raise SsvError(SSV_ERR_INVALID, f"{what}: scales are contiguous fp32 [n_pages, Hkv]")
+    _int32(what, pages)
+    return hkv, ps, d, n
+
+
+def _int32(what: str, *tensors):
+    torch = _torch()
+    for t in tensors:
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise SsvError(SSV_ERR_INVALID, f"{what}: index tensors are contiguous int32")
+
+
+def page_plan(cache_len, new_len, block, held, pages, free_list, n_free, page_size: int, total_rows: int, out=None,
+              dev_status=None, stream=None):
+    """Tables of a pass from the requests' lengths (ssv_page_plan).  cache_len
+    [batch] (negative: the request has ended), new_len, block, held [batch],
+    pages [batch, max_pages], free_list [n_pages], n_free [1]: int32 device
+    tensors; pages and free_list are updated in place.  Returns (seqs
+    [batch, 6], slot_map [total_rows], slot_off [batch], held [batch], n_free
+    [1]), new tensors unless given in ``out``."""
+    torch = _torch()
+    _int32("ssv_page_plan", cache_len, new_len, block, held, pages, free_list, n_free, *(out or ()))
+    batch = cache_len.shape[0]
+    if pages.dim() != 2 or any(x.shape[0] != batch for x in (new_len, block, held, pages)) or n_free.numel() != 1:
+        raise SsvError(SSV_ERR_INVALID, "ssv_page_plan: shapes")
+    if out is None:
+        dev = cache_len.device
+        # one allocation: the table, then the offsets, counts and slot map behind it
+        buf = torch.empty(8 * batch + 1 + int(total_rows), dtype=torch.int32, device=dev)
+        seqs, slot_off, held_out, n_out, slot_map = buf.split([6 * batch, batch, batch, 1, int(total_rows)])
+        out = (seqs.view(batch, 6), slot_map, slot_off, held_out, n_out)
+    elif tuple(x.numel() for x in out) != (6 * batch, int(total_rows), batch, batch, 1):
+        raise SsvError(SSV_ERR_INVALID, "ssv_page_plan: output shapes")
+    seqs, slot_map, slot_off, held_out, n_out = out
+    a = PagePlanArgs(cache_len.data_ptr(), new_len.data_ptr(), block.data_ptr(), held.data_ptr(), pages.data_ptr(),
+                     free_list.data_ptr(), n_free.data_ptr(), batch, pages.shape[1], int(page_size),
+                     free_list.shape[0], int(total_rows), seqs.data_ptr(), slot_map.data_ptr(), slot_off.data_ptr(),
+                     held_out.data_ptr(), n_out.data_ptr(), _ptr(dev_status))
+    _check(lib().ssv_page_plan(C.byref(a), _stream_ptr(stream)), "ssv_page_plan")
+    return out
+
+
+def norm_rope_copy(q, k, q_weight, k_weight, batch: Batch, base: float = 10000.0, eps: float = 1e-6, q_out=None,
+                   k_out=None, positions=None, dev_status=None, stream=None):
+    """RMS norm of every head of Q [rows, Hq, d] and K_new [rows, Hkv, d]
+    (weights [d]) and rope_copy's rotation in one pass; in place unless
+    outputs are given.  Rows may be strided (parts of a fused projection).
+    Returns (q_out, k_out)."""
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: shapes")
+    if any(x.dtype != q.dtype for x in (k, q_out, k_out, q_weight, k_weight)):
+        raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: one dtype")
+    if any(tuple(w.shape) != (q.shape[2],) or not w.is_contiguous() for w in (q_weight, k_weight)):
+        raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: weights are [d]")
+    _int32("ssv_norm_rope_copy", batch.dev, positions)
+    if positions is not None and positions.shape[0] < q.shape[0]:
+        raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: one position per row")
+    what = "ssv_norm_rope_copy"
+    a = NormRopeArgs(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), q_weight.data_ptr(),
+                     k_weight.data_ptr(), _rows_strided(q, what), _rows_strided(k, what), _rows_strided(q_out, what),
+                     _rows_strided(k_out, what), _dtype_code(q), q.shape[1], k.shape[1], q.shape[2], float(eps),
+                     float(base), batch.dev.data_ptr(), batch.batch, q.shape[0], _ptr(positions), _ptr(dev_status))
+    _check(lib().ssv_norm_rope_copy(C.byref(a), _stream_ptr(stream)), what)
+    return q_out, k_out
+
+
+def attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch: Batch, tau,
+                  scale: float = 0.0, dev_status=None):
+    torch = _torch()
+    what = "ssv_verify_attn_fp8"
+    hkv, ps, d, n = _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what)
+    if any(x.dtype != torch.bfloat16 for x in (q, k_new, v_new, out)):
+        raise SsvError(SSV_ERR_INVALID, f"{what}: q, fresh rows and output are bf16")
+    if q.dim() != 3 or not q.is_contiguous() or not out.is_contiguous() or out.shape != q.shape or \
+            tuple(k_new.shape) != (q.shape[0], hkv, d) or v_new.shape != k_new.shape or q.shape[2] != d:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
+    _int32(what, batch.dev, tau)
+    return AttnFp8Args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                       pages.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(),
+                       _rows_strided(k_new, what), _rows_strided(v_new, what), q.shape[1], hkv, d, ps, n,
+                       pages.numel(), float(scale), batch.dev.data_ptr(), batch.batch, tau.data_ptr(), q.shape[0],
+                       tau.shape[0], batch.max_cache, batch.max_new, batch.max_block, _ptr(dev_status))
+
+
+def verify_attn_fp8_workspace_bytes(args: AttnFp8Args) -> int:
+    n = C.c_size_t(0)
+    _check(lib().ssv_verify_attn_fp8_workspace(C.byref(args), C.byref(n)), "ssv_verify_attn_fp8_workspace")
+    return int(n.value)
+
+
+def verify_attn_fp8_workspace(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, batch: Batch, tau):
+    """A zeroed workspace for verify_attn_fp8 on these arguments, to be kept
+    for later calls of the same sizes on the same stream."""
+    a = attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, q, batch, tau)
+    return _workspace(verify_attn_fp8_workspace_bytes(a), q.device)
+
+
+def verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, batch: Batch, tau, out=None,
+                    scale: float = 0.0, workspace=None, dev_status=None, stream=None):
+    """Verification attention with the cached keys in e4m3 pages; q, k_new,
+    v_new bf16 (fresh rows may be strided).  Returns O [rows, Hq, d] bf16."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    a = attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch, tau, scale, dev_status)
+    ws = workspace if workspace is not None else _workspace(verify_attn_fp8_workspace_bytes(a), q.device)
+    _check(lib().ssv_verify_attn_fp8(C.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_ptr(stream)),
+           "ssv_verify_attn_fp8")
+    return out
+
+
+def commit_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch: Batch, tau, n_acc, new_len=None,
+               dev_status=None, stream=None):
+    """Quantises and appends each sequence's fresh prompt rows and accepted
+    data rows (stage order) to its pages, in place; returns new_len [batch]
+    int32 device (-1 for a sequence rejected on the device)."""
+    torch = _torch()
+    what = "ssv_commit_fp8"
+    hkv, ps, d, n = _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what)
+    if k_new.dtype != v_new.dtype or tuple(k_new.shape[1:]) != (hkv, d) or v_new.shape != k_new.shape:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: fresh rows")
+    _int32(what, batch.dev, tau, n_acc, new_len)
+    if n_acc.shape[0] != batch.batch or (new_len is not None and new_len.shape[0] != batch.batch):
+        raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
+    if new_len is None:
+        new_len = torch.empty(batch.batch, dtype=torch.int32, device=k_new.device)
+    a = CommitFp8Args(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                      v_scale.data_ptr(), pages.data_ptr(), _rows_strided(k_new, what), _rows_strided(v_new, what),
+                      _dtype_code(k_new), hkv, d, ps, n, pages.numel(), batch.dev.data_ptr(), batch.batch,
+                      tau.data_ptr(), n_acc.data_ptr(), new_len.data_ptr(), k_new.shape[0], tau.shape[0],
+                      batch.max_new, batch.max_block, _ptr(dev_status))
+    _check(lib().ssv_commit_fp8(C.byref(a), _stream_ptr(stream)), what)
+    return new_len
 
 
 def stream_read(buf, out, stream=None):

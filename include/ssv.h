@@ -58,7 +58,8 @@ typedef enum {
   SSV_ERR_TIMEOUT = 4,      /* a bounded on-device wait ran out */
   SSV_ERR_BAD_TAU = 5,      /* stage map of some sequence is not a permutation of 1..B */
   SSV_ERR_WORKSPACE = 6,    /* workspace null, misaligned or smaller than the query */
-  SSV_ERR_NOT_FINITE = 7    /* temperature not finite / negative */
+  SSV_ERR_NOT_FINITE = 7,   /* temperature not finite / negative */
+  SSV_ERR_NO_PAGES = 8      /* the free stack holds fewer pages than the pass needs (ssv_page_plan) */
 } ssv_status;
 
 typedef enum { SSV_F32 = 0, SSV_BF16 = 1 } ssv_dtype;
@@ -607,6 +608,219 @@ typedef struct {
 SSV_API ssv_status ssv_tree_accept_workspace(const ssv_tree_accept_args* a, size_t* bytes);
 SSV_API ssv_status ssv_tree_accept(const ssv_tree_accept_args* a, void* workspace, size_t workspace_bytes,
                                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * The paged 8-bit KV cache: four operators of a serving loop whose cache is
+ * held in e4m3 pages, in the order a pass calls them (SimSD summary, "Main
+ * contributions" 3: the method composes with a KV cache; the pages give no
+ * cache layout, so the layout is this library's own):
+ *   ssv_page_plan       lengths of the requests -> page table, sequence table, slot map
+ *   ssv_norm_rope_copy  RMS norm of every query / key head and ssv_rope_copy in one pass
+ *   ssv_verify_attn_fp8 ssv_verify_attn with the cached keys read from the pages
+ *   ssv_commit_fp8      ssv_commit into the pages, quantising
+ *
+ * Cache: k_cache, v_cache [n_pages, Hkv, page_size, d] device, e4m3 codes
+ * (one byte each); k_scale, v_scale [n_pages, Hkv] device fp32.  A code c of
+ * (page, head) stands for c * scale[page][head].  page_size in {16, 32, 64,
+ * 128}.  Page table: pages [table_len] device int32; token t of sequence b
+ * sits in row t mod page_size of page pages[seqs[b].kv_off + t / page_size].
+ * An all-zero-length record (new_len = block = 0, as ssv_page_plan writes for
+ * an ended or refused request) is idle: ssv_norm_rope_copy,
+ * ssv_verify_attn_fp8 and ssv_commit_fp8 skip it without an error.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * ssv_page_plan -- the tables of a pass from the lengths of its requests,
+ * built on the device (lengths known only there, such as ssv_commit_fp8's
+ * new_len, never travel to the host).
+ * Per request b, in batch order (all arrays device int32):
+ *   cache_len[b] < 0: the request has ended.  The held[b] pages at the front
+ *     of its table row go back to the free stack (table order), held_out = 0,
+ *     no rows, an idle record.
+ *   otherwise C = cache_len, N = new_len, B = block: it needs
+ *     ceil((C + N + B) / page_size) pages, enough for every row the pass may
+ *     commit, and wants those beyond the held[b] it has.  Rows of requests
+ *     are packed: q_off and tau_off (also slot_off) are the sums of N + 2B
+ *     and B over the earlier requests that have not ended.
+ * The free stack is free_list[0 .. n_free) with the released pages pushed on
+ * top; wanted pages are taken from its top in (request, page) order and
+ * entered in the table row.  A request whose wanted pages, with those wanted
+ * before it, exceed the stack is refused (SSV_ERR_NO_PAGES; so is every later
+ * one that wants pages): it keeps its place in the packing and its held
+ * pages, takes none, and gets an idle record.
+ * Outputs: seqs [batch] (kv_off = b * max_pages); slot_map [total_rows]: for
+ * row q_off + j, j < N + B, of a granted request the cache row page *
+ * page_size + offset of token C + j, -1 at mask rows and at every row of
+ * [0, total_rows) that is no granted request's; slot_off [batch]; held_out
+ * [batch]; n_free_out [1].  pages and free_list are updated in place, at
+ * entries that the call does not read otherwise; held and n_free are not
+ * written, so a pass that fails can be planned again from them.
+ * pages [batch, max_pages]; free_list [n_pages]; 1 <= batch <= 4096;
+ * n_pages * page_size < 2^31; page_size in {16, 32, 64, 128}.  held_out and
+ * n_free_out must not overlap any input.  held[b] of an ended request and
+ * the table's entries are trusted to name distinct pages.
+ * Errors: SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED (batch), SSV_ERR_CUDA; on
+ * device SSV_ERR_INVALID for a request with N < 0, B outside 1..64, held
+ * outside 0..max_pages, more than max_pages pages needed, or rows beyond
+ * total_rows (it takes no pages and gets an idle record; unless only its
+ * rows do not fit, it takes no rows either), for n_free outside 0..n_pages
+ * (taken as 0), and for a released stack that outgrows n_pages (the excess is
+ * dropped); SSV_ERR_NO_PAGES.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const int32_t* cache_len;    /* device [batch]; < 0: ended */
+  const int32_t* new_len;      /* device [batch] */
+  const int32_t* block;        /* device [batch] */
+  const int32_t* held;         /* device [batch] */
+  int32_t* pages;              /* device [batch, max_pages], in and out */
+  int32_t* free_list;          /* device [n_pages], in and out */
+  const int32_t* n_free;       /* device [1] */
+  int32_t batch, max_pages, page_size, n_pages, total_rows;
+  ssv_seq* seqs;               /* device [batch], out */
+  int32_t* slot_map;           /* device [total_rows], out */
+  int32_t* slot_off;           /* device [batch], out */
+  int32_t* held_out;           /* device [batch], out */
+  int32_t* n_free_out;         /* device [1], out */
+  int32_t* dev_status;         /* device, may be NULL */
+} ssv_page_plan_args;
+
+SSV_API ssv_status ssv_page_plan(const ssv_page_plan_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * ssv_norm_rope_copy -- RMS norm of each query and key head and the rotation
+ * of ssv_rope_copy, in one pass over the rows.  For head row x of width d:
+ *   y = x / sqrt(mean(x_i^2) + eps) * weight      (weight: q_weight or k_weight)
+ * then the rotation of y at the row's position, as ssv_rope_copy (same
+ * positions, same optional table).  Computed in fp32, rounded once, to dtype;
+ * angles are formed mod one turn in 64-bit fixed point.
+ * q_in, q_out [total_rows, Hq, d], k_in, k_out [total_rows, Hkv, d] device,
+ * dtype; the heads of a row are contiguous, consecutive rows *_stride
+ * elements apart (0: Hq * d or Hkv * d), so that the inputs may be parts of a
+ * fused projection's output.  An output may be its own input (same address
+ * and stride), and overlaps no other argument.
+ * q_weight, k_weight [d] device, dtype.  eps >= 0 finite.  d in {64, 128};
+ * pointers 16-byte aligned, strides a multiple of 16 bytes.
+ * Errors and device checks as ssv_rope_copy (idle records are skipped).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* q_in;
+  const void* k_in;
+  void* q_out;
+  void* k_out;
+  const void* q_weight;
+  const void* k_weight;
+  int64_t q_in_stride, k_in_stride, q_out_stride, k_out_stride;  /* elements; 0: packed */
+  ssv_dtype dtype;
+  int32_t Hq, Hkv, d;
+  float eps;
+  double base;                 /* RoPE base, e.g. 10000 */
+  const ssv_seq* seqs;         /* device */
+  int32_t batch;
+  int32_t total_rows;
+  const int32_t* positions;    /* device [total_rows] or NULL, as ssv_rope_copy */
+  int32_t* dev_status;         /* device, may be NULL */
+} ssv_norm_rope_args;
+
+SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * ssv_verify_attn_fp8 -- ssv_verify_attn (same rows, same mask, same
+ * grouped heads) with the C cached keys and values of a sequence read from
+ * e4m3 pages; the fresh rows k_new, v_new stay bf16.
+ * q, o [total_rows, Hq, d] bf16 device, packed; k_new, v_new [total_rows,
+ * Hkv, d] bf16 device, rows k_stride / v_stride elements apart (0: Hkv * d).
+ * Scores, softmax statistics and the accumulation of O are fp32.
+ * A sequence's own fresh rows must be finite (a masked non-finite value row
+ * still meets a zero weight); rows of other sequences, rows of a page behind
+ * token C - 1 and pages that are not a sequence's own never influence it,
+ * whatever they hold.  scales: positive and finite.
+ * d = 128; Hq % Hkv == 0, Hq / Hkv <= 128; 1 <= B <= 64; n_pages * Hkv *
+ * page_size < 2^31; pointers 16-byte aligned, strides multiples of 8.
+ * max_cache / max_new / max_block as ssv_verify_attn.  scale 0 means
+ * 1/sqrt(d).  o overlaps no input.
+ * Workspace: ssv_verify_attn_fp8_workspace bytes, 256-byte aligned, zero
+ * before its first use (see the conventions).
+ * Errors: SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED (d, heads), SSV_ERR_WORKSPACE,
+ * SSV_ERR_CUDA; on device SSV_ERR_BAD_TAU, SSV_ERR_TIMEOUT, and
+ * SSV_ERR_INVALID for a sequence outside the buffers or with a page outside
+ * [0, n_pages) among its first ceil(C / page_size) (skipped: its rows of o
+ * are unspecified).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* q;
+  const void* k_cache;         /* e4m3 [n_pages, Hkv, page_size, d] */
+  const void* v_cache;
+  const float* k_scale;        /* [n_pages, Hkv] */
+  const float* v_scale;
+  const int32_t* pages;        /* [table_len] */
+  const void* k_new;
+  const void* v_new;
+  void* o;
+  int64_t k_stride, v_stride;  /* elements; 0: packed */
+  int32_t Hq, Hkv, d, page_size, n_pages, table_len;
+  float scale;
+  const ssv_seq* seqs;         /* device [batch]; kv_off: first entry in pages */
+  int32_t batch;
+  const int32_t* tau;          /* device [total_slots] */
+  int32_t total_rows, total_slots;
+  int32_t max_cache, max_new, max_block;
+  int32_t* dev_status;         /* device, may be NULL */
+} ssv_attn_fp8_args;
+
+SSV_API ssv_status ssv_verify_attn_fp8_workspace(const ssv_attn_fp8_args* a, size_t* bytes);
+SSV_API ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * ssv_commit_fp8 -- ssv_commit into the pages: tokens C .. C + N + n_acc - 1
+ * (the fresh prompt rows, then the data rows of stages 1..n_acc in stage
+ * order) are quantised and appended.  For each touched (page, head), K and V
+ * apart:
+ *   s_new = 2^e, e the smallest integer >= -100 with max |x| <= 448 * 2^e over
+ *           the finite x appended to the page
+ *   s     = max(s_old, s_new) where the page already holds tokens of the
+ *           sequence (its first page, C mod page_size > 0), else s_new
+ *   codes of appended rows: x / s rounded to the nearest e4m3 (ties to even),
+ *           NaN and infinities stored as NaN
+ *   codes of rows already there: code * s_old / s rounded likewise, when s grew
+ * A power-of-two scale costs an 8-bit float no precision, makes x / s exact
+ * and a later rescale exact but for values that fall below 2^-6 s.  Rows
+ * behind the last appended token are left as they were.
+ * k_new, v_new [total_rows, Hkv, d] device, dtype (SSV_F32 or SSV_BF16), rows
+ * k_stride / v_stride elements apart (0: Hkv * d).  seqs, tau, n_acc, new_len
+ * and their checks as ssv_commit; kv_off is the sequence's first entry in
+ * pages [table_len].  d in {64, 128}; 1 <= max_new + max_block bounds every
+ * N + B (sizes the grid); pointers 16-byte aligned, strides a multiple of 16
+ * bytes.  No two touched pages may be the same page (not checked).
+ * Errors: SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED (d), SSV_ERR_CUDA; on device
+ * SSV_ERR_BAD_TAU and SSV_ERR_INVALID as ssv_commit, also for a sequence
+ * whose rows leave [0, total_rows), whose N or B exceeds max_new or max_block,
+ * whose touched pages leave the table or name a page outside [0, n_pages):
+ * nothing of that sequence is written and its new_len is -1.  An idle record
+ * gets new_len = cache_len.  No workspace; asynchronous on `stream`.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* k_new;
+  const void* v_new;
+  void* k_cache;               /* e4m3 [n_pages, Hkv, page_size, d], in and out */
+  void* v_cache;
+  float* k_scale;              /* [n_pages, Hkv], in and out */
+  float* v_scale;
+  const int32_t* pages;        /* [table_len] */
+  int64_t k_stride, v_stride;  /* elements; 0: packed */
+  ssv_dtype dtype;
+  int32_t Hkv, d, page_size, n_pages, table_len;
+  const ssv_seq* seqs;         /* device [batch] */
+  int32_t batch;
+  const int32_t* tau;          /* device [total_slots] */
+  const int32_t* n_acc;        /* device [batch] */
+  int32_t* new_len;            /* device [batch], out */
+  int32_t total_rows, total_slots;
+  int32_t max_new, max_block;
+  int32_t* dev_status;         /* device, may be NULL */
+} ssv_commit_fp8_args;
+
+SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
 
 /* ------------------------------------------------------------------------
  * ssv_set_fault_injection -- test support for failure detection.

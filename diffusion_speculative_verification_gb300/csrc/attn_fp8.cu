@@ -1,24 +1,106 @@
-// ssv_verify_attn_fp8: verification attention over cached keys in e4m3 pages.
+// ssv_verify_attn_fp8: verification attention over cached keys in e4m3 pages
+// (head_dim 128, bf16 queries and fresh rows, fp32 accumulation).
 //
-// One warp per (query row, query head), fp32 throughout, online softmax in
-// the log2 domain.  SimSD summary, section 2: the temporal mask is evaluated
-// from tau for the 2B tail keys.
+// SimSD summary, section 2 "Temporal Attention Mask" and section 4
+// "Verification": O = softmax(scale q K^T | allowed) V, the mask evaluated per
+// (row, key) from tau on the fly.
+//
+// Work unit = (sequence, kv head g, UR consecutive query rows) x the G query
+// heads of the group: MT tiles of 128 packed rows, R = 128 / G query rows each
+// (row m of a tile is query row m / G, head m % G; rows behind R * G are
+// empty).  Its keys are cut into blocks of 128: the cached ones (visible to
+// every row), then the fresh ones up to the last a row needs.
+//
+// Arithmetic of a cached block, on the codes themselves:
+//   scores  q = 2^e (hi + lo), hi and lo e4m3, e per row (an element down to
+//           2^-10 of the row's largest is exact, the rest off by 2^-18 of it).
+//           S = hi K^T + lo K^T on the fp8 tensor path, at the cost of one bf16
+//           product and without converting K; the scale of a page enters with
+//           2^e as a factor of the column group.
+//   values  converted to fp16 (exact), P in fp16: P' = exp2(x - m) vs / 2^u with
+//           vs the page's scale and u one exponent per unit, so that O gathers
+//           in units of 2^u; the row sum l adds P' 2^u / vs.  P' is at most
+//           2^15 and is kept to 11 bits down to 2^-14, that is to weights of
+//           2^-21 and less (u follows the largest vs met, as m does the scores);
+//           pages whose scale is 2^16 below the largest lose bits from there on.
+// Fresh blocks: bf16 S and P (P' = exp2(x - m) / 2^u, any exponent).
+//
+// Scheduling: persistent, one CTA per SM; per kv head the units' blocks are
+// cut into contiguous ranges of equal estimated cost, one per CTA; a unit cut
+// across CTAs leaves fp32 partials (O, m, l) in the workspace, merged in CTA
+// order by the CTA that holds its first block (bounded wait on per-row-group
+// counters).  The plan is derived on the device from seqs.
+//
+// Roles of a CTA (10 warps for one tile, 12 for two):
+//   warp 0       page lookups (32 pages ahead, one per lane), TMA of K pages
+//                (swizzled, the operand itself) and V pages (raw) into rings,
+//                fresh rows into two ring stages at once; the pages' scales
+//   warp 1       MMA issue: S into TMEM, O += P V with P from TMEM
+//   warps 2..    softmax, four per tile, one TMEM lane quadrant each
+//   the others   queries into the operand's form; V codes to fp16 (rows behind
+//                the last token become 0, so nothing there is ever multiplied)
+// Every wait is bounded; an expired one raises the CTA's abort flag, copies and
+// MMAs in flight are drained, TMEM is freed and SSV_ERR_TIMEOUT reported.
 #include "ssv_internal.cuh"
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <math.h>
+
+#include <mutex>
+#include <type_traits>
 
 namespace ssv {
 namespace {
 
+using namespace ptx;
+
+constexpr int D = 128;
+constexpr int BN = 128;                     // keys per block
+constexpr int NK = 4;                       // K ring stages
+constexpr int NSC = 8;                      // blocks of page scales in flight
+constexpr uint32_t STAGE = 128 * 128;       // one e4m3 tile, or half a 16-bit one
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_O = 256;              // O_mt at columns 256 + 128 mt; S / P at 128 mt
+constexpr float kLazy = 8.f;                // the running maximum may lag by 2^8
+constexpr float kUnitTop = 7.f;             // vs / 2^u <= 2^7: P' <= 2^15 in fp16
+constexpr float kUnitRoom = 2.f;            // u leaves that much for larger scales to come
+// Estimated costs of the plan, in units of 0.1 us: a block of one / two tiles
+// and a segment's fixed work; a merge of partials costs about kMergeBlocks blocks.
+constexpr int kBlock1 = 7, kBlock2 = 12, kSegCost = 40;
+constexpr int kMergeBlocks = 8;
+
+enum : uint32_t {
+  B_K_FULL = 0,
+  B_K_EMPTY = B_K_FULL + NK,
+  B_R_FULL = B_K_EMPTY + NK,     // raw V ring (at most NK stages)
+  B_R_EMPTY = B_R_FULL + NK,
+  B_V_FULL = B_R_EMPTY + NK,     // 16-bit V, two stages
+  B_V_EMPTY = B_V_FULL + 2,
+  B_C_FULL = B_V_EMPTY + 2,      // scales
+  B_C_EMPTY = B_C_FULL + NSC,
+  B_Q_FULL = B_C_EMPTY + NSC,    // query operand written / its last S complete
+  B_Q_EMPTY = B_Q_FULL + 1,
+  B_X_FULL = B_Q_EMPTY + 1,      // row exponents, two buffers
+  B_X_EMPTY = B_X_FULL + 2,
+  B_S_FULL = B_X_EMPTY + 2,      // + tile (two active tiles)
+  B_P_FULL = B_S_FULL + 2,
+  B_SDB = B_P_FULL + 2,          // + S buffer (one active tile)
+  B_PDB = B_SDB + 2,
+  B_PV_DONE = B_PDB + 2,         // one active tile: each PV complete
+  B_O_FREE = B_PV_DONE + 1,      // + tile
+  B_SEG_DONE = B_O_FREE + 2,
+  B_FINAL = B_SEG_DONE + 1,
+  B_COUNT = B_FINAL + 1
+};
+
 struct AttnFp8Params {
   const __nv_bfloat16* q;
-  const uint8_t *k_cache, *v_cache;
   const float *k_scale, *v_scale;
   const int32_t* pages;
-  const __nv_bfloat16 *k_new, *v_new;
   __nv_bfloat16* o;
-  int64_t k_stride, v_stride;  // elements
   int Hq, Hkv, ps_log2, n_pages, table_len;
   float scale;
   const ssv_seq* seqs;
@@ -26,125 +108,1147 @@ struct AttnFp8Params {
   const int32_t* tau;
   int total_rows, total_slots, max_cache, max_new, max_block;
   int32_t* dev_status;
+  long long wait_budget;
+  int fault_skip;
 };
 
-// Extents of sequence s within the call's buffers and stated maxima.
-__device__ __forceinline__ bool fp8_seq_ok(const AttnFp8Params& p, const ssv_seq& s) {
-  const long long pages = ((long long)s.cache_len + (1 << p.ps_log2) - 1) >> p.ps_log2;
-  return s.cache_len >= 0 && s.new_len >= 0 && s.block >= 1 && s.block <= 64 && s.q_off >= 0 &&
-         (long long)s.q_off + s.new_len + 2LL * s.block <= p.total_rows && s.kv_off >= 0 &&
-         s.kv_off + pages <= p.table_len && s.tau_off >= 0 && (long long)s.tau_off + s.block <= p.total_slots &&
-         s.cache_len <= p.max_cache && s.new_len <= p.max_new && s.block <= p.max_block;
+struct Fp8Maps {
+  CUtensorMap kc, vc, kn, vn;
+};
+
+struct Fp8Work {
+  int32_t* plan;   // [grid][4][batch + 1] planning tables that do not fit shared memory
+  int32_t* cnt;    // [units][MT][4] arrival counters (zero between calls)
+  float* part_ml;  // [grid][MT][128][2]
+  float* part_o;   // [grid][MT][D / 4][128][4]
+};
+
+// Per head: U units of total cost Wc dealt to Pe CTAs; this CTA's head g and
+// its blocks [begin, end), which start at block k0 of unit u0.
+struct PlanHdr {
+  long long Wc;
+  int U, Pe, g, begin, end, u0, k0;
+};
+
+template <int MT>
+struct Cfg {
+  // at most twelve warps, three per scheduler: 168 registers each
+  static constexpr int kSoft = 4 * MT, kConv = MT == 1 ? 4 : 2, kThreads = 32 * (2 + kSoft + kConv);
+  static constexpr int NR = MT == 1 ? 4 : 2;                // raw V stages
+  static constexpr uint32_t SM_Q = 0;                       // per tile: hi, lo; or the bf16 tile
+  static constexpr uint32_t SM_K = SM_Q + MT * 2 * STAGE;
+  static constexpr uint32_t SM_R = SM_K + NK * STAGE;
+  static constexpr uint32_t SM_V = SM_R + NR * STAGE;       // 2 x 32 KB
+  static constexpr uint32_t SM_SC = SM_V + 4 * STAGE;       // [NSC][20]: k factor x 8, log2 v scale x 8, its maximum
+  static constexpr uint32_t SM_X = SM_SC + NSC * 20 * 4;    // [2][MT][128] int8 row exponents
+  static constexpr uint32_t SM_BAR = SM_X + 2 * MT * 128;
+  static constexpr uint32_t SM_PLAN = SM_BAR + 8 * B_COUNT + 16;
+  static constexpr uint32_t SM_TOTAL = (SM_PLAN + sizeof(PlanHdr) + 15) / 16 * 16;  // planning tables follow
+};
+constexpr size_t kMaxSmem = 227 * 1024;
+static_assert(Cfg<2>::SM_TOTAL <= kMaxSmem && Cfg<1>::SM_TOTAL <= kMaxSmem, "shared memory");
+static_assert(Cfg<2>::SM_PLAN % 8 == 0 && Cfg<1>::SM_PLAN % 8 == 0 && Cfg<1>::SM_BAR % 8 == 0, "alignment");
+
+struct Unit {
+  int b, C, N, B, rows, q_off, kv_off, tau_off;
+  int row0, nvalid, mc, cache_blocks, nblocks, full_new;
+};
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-constexpr int kRowWarps = 4;
+__device__ __forceinline__ void red_release_add(int32_t* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool wait_count(const int32_t* p, int target, volatile int* abort, long long budget) {
+  const long long t0 = clock64();
+  while (ld_acquire(p) < target) {
+    if (*abort) return false;
+    if (clock64() - t0 > budget) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 
-__global__ void __launch_bounds__(kRowWarps * 32) attn_fp8_row_kernel(const AttnFp8Params p) {
-  constexpr int D = 128, E = 4, U = 4;
-  pdl_wait();
+// Float4 group c4 of partial row `slot_row` (= slot * 128 + row): the 32 lanes of a warp
+// (consecutive rows) touch 512 contiguous bytes per access.
+__device__ __forceinline__ float4* part_at(float* part_o, size_t slot_row, int c4) {
+  return reinterpret_cast<float4*>(part_o + (slot_row >> 7) * (128 * D)) + (size_t)c4 * 128 + (slot_row & 127);
+}
+
+// bits [0, n) set, n clamped to [0, 32]
+__device__ __forceinline__ uint32_t prefix32(int n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u));
+}
+
+// 32-bit window [t0, t0 + 32) of a 128-bit mask, zero outside [0, 128)
+__device__ __forceinline__ uint32_t window32(const uint32_t (&m)[4], int t0) {
+  if (t0 <= -32 || t0 >= 128) return 0u;
+  auto pick = [&](int i) { return i == 0 ? m[0] : (i == 1 ? m[1] : (i == 2 ? m[2] : (i == 3 ? m[3] : 0u))); };
+  const int w = t0 >> 5, sh = t0 & 31;  // floor division
+  return sh == 0 ? pick(w) : __funnelshift_r(pick(w), pick(w + 1), sh);
+}
+
+// One 128 x 128 x 128 product of e4m3 operands, (hi + lo) K^T: hi at a_desc, lo
+// one stage behind it, both K-major SW128 like b_desc.
+__device__ __forceinline__ void gemm_q8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const uint64_t a = a_desc + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, b = b_desc + (s & 3) * 2;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)(s > 0))
+        : "memory");
+  }
+}
+
+// Instruction descriptors: fp32 accumulator, shape 128 x 128, B K-major or MN-major.
+constexpr uint32_t kIdShape = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdE4m3 = kIdShape;                     // kind::f8f6f4, e4m3 x e4m3
+constexpr uint32_t kIdBf16 = kIdShape | (1u << 7) | (1u << 10);
+constexpr uint32_t kIdPvF16 = kIdShape | (1u << 16);       // kind::f16, f16 x f16, B MN-major
+constexpr uint32_t kIdPvBf16 = kIdBf16 | (1u << 16);
+
+template <int MT>
+__global__ void __launch_bounds__(Cfg<MT>::kThreads, 1)
+attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, const Fp8Work work, int G,
+                int plan_smem) {
+  using C_ = Cfg<MT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C_::SM_BAR + 8 * B_COUNT);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C_::SM_BAR + 8 * B_COUNT + 4);
+  PlanHdr* plan = reinterpret_cast<PlanHdr*>(smem + C_::SM_PLAN);
+  int* s_prefU = plan_smem ? reinterpret_cast<int*>(smem + C_::SM_TOTAL)
+                           : work.plan + (size_t)blockIdx.x * 4 * (p.batch + 1);
+  int* s_prefB = s_prefU + (p.batch + 1);
+  int* s_prefC = s_prefB + (p.batch + 1);
+  int* s_ntile = s_prefC + (p.batch + 1);
+  auto bar = [&](uint32_t i) -> uint32_t { return sbase + C_::SM_BAR + 8u * i; };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long wb = p.wait_budget;
+  const int R = 128 / G, UR = MT * R, ps = 1 << p.ps_log2, ppb = BN >> p.ps_log2;  // pages per block
+  const int cta = blockIdx.x;
+  if (sbase & 1023u) {  // the swizzled tiles need it; dynamic shared memory starts there
+    if (threadIdx.x == 0) report(p.dev_status, SSV_ERR_CUDA);
+    return;
+  }
+
+  auto mc_of = [&](int rows, int row0) -> int { return MT == 2 && min(UR, rows - row0) > R ? 2 : 1; };
+  auto cost_of = [&](int rows, int row0) -> int { return mc_of(rows, row0) == 2 ? kBlock2 : kBlock1; };
+  // key blocks of the unit at row0: the cached ones, then the fresh ones up to its last prompt
+  // row (causal), or all where it holds tail rows
+  auto blocks_of = [&](int C, int N, int rows, int row0) -> int {
+    return cdiv(C, BN) + cdiv(row0 + UR <= N ? row0 + UR : rows, BN);
+  };
+
+  // ------------------------------------------------------------------ plan
+  if (warp == 0) {
+    pdl_wait();
+    int carryU = 0, carryB = 0, carryC = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      int units = 0, blocks = 0, cost = 0;
+      if (b < p.batch) {
+        const ssv_seq s = p.seqs[b];
+        if (!seq_idle(s)) {
+          const long long np = ((long long)s.cache_len + ps - 1) >> p.ps_log2;
+          const bool ok = s.cache_len >= 0 && s.new_len >= 0 && s.block >= 1 && s.block <= 64 && s.q_off >= 0 &&
+                          (long long)s.q_off + s.new_len + 2LL * s.block <= p.total_rows && s.kv_off >= 0 &&
+                          s.kv_off + np <= p.table_len && s.tau_off >= 0 &&
+                          (long long)s.tau_off + s.block <= p.total_slots && s.cache_len <= p.max_cache &&
+                          s.new_len <= p.max_new && s.block <= p.max_block;
+          if (!ok && cta == 0) report(p.dev_status, SSV_ERR_INVALID);
+          const int rows = s.new_len + 2 * s.block;
+          units = ok ? cdiv(rows, UR) : 0;
+          for (int t = 0; t < units; ++t) {
+            const int nb = blocks_of(s.cache_len, s.new_len, rows, t * UR);
+            blocks += nb;
+            cost += kSegCost + cost_of(rows, t * UR) * nb;
+          }
+        }
+        s_ntile[b] = units;
+      }
+      int iu = units, ib = blocks, ic = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int yu = __shfl_up_sync(0xffffffffu, iu, o), yb = __shfl_up_sync(0xffffffffu, ib, o);
+        const int yc = __shfl_up_sync(0xffffffffu, ic, o);
+        if (lane >= o) { iu += yu; ib += yb; ic += yc; }
+      }
+      if (b < p.batch) { s_prefU[b + 1] = carryU + iu; s_prefB[b + 1] = carryB + ib; s_prefC[b + 1] = carryC + ic; }
+      carryU += __shfl_sync(0xffffffffu, iu, 31);
+      carryB += __shfl_sync(0xffffffffu, ib, 31);
+      carryC += __shfl_sync(0xffffffffu, ic, 31);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      s_prefU[0] = s_prefB[0] = s_prefC[0] = 0;
+      PlanHdr h;
+      h.U = carryU;
+      // CTAs per head: all, unless there are no more units than CTAs and one CTA per unit ends
+      // sooner than spreading the blocks and merging
+      const int cap = max((int)gridDim.x / p.Hkv, 1);
+      int ph = cap;
+      if (carryU > 0 && carryU <= cap) {
+        const long long per_unit = (long long)carryB * cap;
+        const long long per_cta = ((long long)carryB + (long long)kMergeBlocks * cap) * carryU;
+        ph = per_cta < per_unit ? cap : carryU;
+      }
+      // every range at least one block wide, so the CTAs holding a unit's blocks are consecutive
+      ph = min(min(ph, max(carryB, 1)), max(carryC / kBlock2, 1));
+      h.Pe = ph;
+      h.g = cta % p.Hkv;
+      h.Wc = carryC;
+      // unit u occupies the costs [c_u, c_u + kSegCost + w n_u), its i-th block sits at
+      // c_u + kSegCost + w i; rank r owns the blocks in [r Wc / Pe, (r + 1) Wc / Pe).
+      // First block at or after cost c, as (block, unit, offset in the unit):
+      auto locate = [&](long long c, int& u_out, int& k_out) -> int {
+        int lo = 0, hi = p.batch - 1, b = 0;
+        while (lo <= hi) {
+          const int mid = (lo + hi) >> 1;
+          if (s_prefC[mid] <= c) { b = mid; lo = mid + 1; } else { hi = mid - 1; }
+        }
+        const ssv_seq s = p.seqs[b];
+        const int rows = s.new_len + 2 * s.block;
+        int xs = s_prefB[b], uu = s_prefU[b];
+        long long cu = s_prefC[b];
+        for (int t = 0;; ++t, ++uu) {
+          const int nb = blocks_of(s.cache_len, s.new_len, rows, t * UR), w = cost_of(rows, t * UR);
+          if (t >= s_ntile[b] - 1 || cu + kSegCost + (long long)w * nb > c) {
+            const long long dd = c - cu - kSegCost;
+            const int i = dd <= 0 ? 0 : (int)min((dd + w - 1) / w, (long long)nb);
+            u_out = (i == nb) ? uu + 1 : uu;
+            k_out = (i == nb) ? 0 : i;
+            return xs + i;
+          }
+          xs += nb;
+          cu += kSegCost + (long long)w * nb;
+        }
+      };
+      const int r = cta / p.Hkv;
+      h.begin = h.end = h.u0 = h.k0 = 0;
+      if (cta < ph * p.Hkv && carryB > 0) {
+        int u1, k1;
+        h.begin = locate(((long long)r * h.Wc) / ph, h.u0, h.k0);
+        h.end = (r + 1 == ph) ? carryB : locate(((long long)(r + 1) * h.Wc) / ph, u1, k1);
+      }
+      *plan = h;
+      *abort = 0;
+      for (uint32_t i = 0; i < B_COUNT; ++i) {
+        uint32_t n = 1;
+        if ((i >= B_R_EMPTY && i < B_V_EMPTY) || i == B_Q_FULL || i == B_X_FULL || i == B_X_FULL + 1) n = C_::kConv;
+        if ((i >= B_C_EMPTY && i < B_Q_FULL) || i == B_X_EMPTY || i == B_X_EMPTY + 1) n = C_::kSoft;
+        if (i == B_P_FULL || i == B_P_FULL + 1 || i == B_PDB || i == B_PDB + 1 || i == B_O_FREE || i == B_O_FREE + 1)
+          n = 4;
+        mbar_init(bar(i), n);
+      }
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  if (w >= (long long)p.total_rows * p.Hq) return;
-  const int row = (int)(w / p.Hq), h = (int)(w % p.Hq);
-  const int b = find_seq_by_row(p.seqs, p.batch, row);
-  if (b < 0) return;
-  const ssv_seq s = p.seqs[b];
-  if (seq_idle(s)) return;
-  const int i = row - s.q_off, B = s.block, N = s.new_len, C = s.cache_len;
-  if (!fp8_seq_ok(p, s)) {
-    if (lane == 0) report(p.dev_status, SSV_ERR_INVALID);
-    return;
-  }
-  if (i >= N + 2 * B) return;
-  const int32_t* tau = p.tau + s.tau_off;
-  if (!warp_tau_is_permutation(tau, B)) {
-    if (lane == 0) report(p.dev_status, SSV_ERR_BAD_TAU);
-    return;
-  }
-  const int ps = 1 << p.ps_log2;
-  bool bad = false;
-  for (int j = lane; j < (C + ps - 1) >> p.ps_log2; j += 32) {
-    const int page = p.pages[s.kv_off + j];
-    bad |= page < 0 || page >= p.n_pages;
-  }
-  if (__any_sync(0xffffffffu, bad)) {
-    if (lane == 0) report(p.dev_status, SSV_ERR_INVALID);
-    return;
-  }
-  const int kvh = h / (p.Hq / p.Hkv);
-  auto wide = [&](const __nv_bfloat16* x, float* out) {
-    const uint2 v = *reinterpret_cast<const uint2*>(x + lane * E);
-    out[0] = __uint_as_float(v.x << 16); out[1] = __uint_as_float(v.x & 0xffff0000u);
-    out[2] = __uint_as_float(v.y << 16); out[3] = __uint_as_float(v.y & 0xffff0000u);
+  const uint32_t tmem = *tmem_slot;
+  const int begin = plan->begin, end = plan->end, Ph = plan->Pe, Uh = plan->U, gh = plan->g;
+  const long long Wc = plan->Wc;
+  const int rank = cta / p.Hkv;
+
+  auto seq_of = [&](int u) -> int {
+    int lo = 0, hi = p.batch - 1, b = 0;
+    while (lo <= hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_prefU[mid] <= u) { b = mid; lo = mid + 1; } else { hi = mid - 1; }
+    }
+    return b;
   };
-  auto codes = [&](const uint8_t* x, float sc, float* out) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(x + lane * E);
-    const uint32_t f01 = e4m3x2_to_f16x2((uint16_t)v), f23 = e4m3x2_to_f16x2((uint16_t)(v >> 16));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&f01));
-    const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&f23));
-    out[0] = a.x * sc; out[1] = a.y * sc; out[2] = c.x * sc; out[3] = c.y * sc;
+  auto decode = [&](int u) -> Unit {
+    Unit x;
+    x.b = seq_of(u);
+    const ssv_seq s = p.seqs[x.b];
+    x.C = s.cache_len; x.N = s.new_len; x.B = s.block;
+    x.q_off = s.q_off; x.kv_off = s.kv_off; x.tau_off = s.tau_off;
+    x.rows = x.N + 2 * x.B;
+    x.row0 = (u - s_prefU[x.b]) * UR;
+    x.nvalid = min(UR, x.rows - x.row0);
+    x.mc = mc_of(x.rows, x.row0);
+    x.cache_blocks = cdiv(x.C, BN);
+    x.nblocks = blocks_of(x.C, x.N, x.rows, x.row0);
+    x.full_new = (x.row0 < x.N) ? (x.row0 + 1) : x.N;  // fresh keys that every row sees
+    return x;
   };
-  float q[E];
-  wide(p.q + ((size_t)row * p.Hq + h) * D, q);
-  const float qs = p.scale * 1.4426950408889634f;
+  auto cost_start = [&](int r) -> long long { return ((long long)r * Wc) / Ph; };
+  auto owner_at = [&](long long c) -> int {  // rank owning the block at cost c
+    int r = (int)((c * Ph) / (Wc > 0 ? Wc : 1));
+    r = min(max(r, 0), Ph - 1);
+    while (r + 1 < Ph && cost_start(r + 1) <= c) ++r;
+    while (r > 0 && cost_start(r) > c) --r;
+    return r;
+  };
+  auto unit_cost = [&](int u) -> long long {  // cost at which unit u starts
+    const int b = seq_of(u);
+    const ssv_seq s = p.seqs[b];
+    const int rows = s.new_len + 2 * s.block;
+    long long c = s_prefC[b];
+    for (int t = 0; t < u - s_prefU[b]; ++t)
+      c += kSegCost + (long long)cost_of(rows, t * UR) * blocks_of(s.cache_len, s.new_len, rows, t * UR);
+    return c;
+  };
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+    const bool w = mbar_wait(b, parity, abort, wb);
+    return __all_sync(0xffffffffu, w);
+  };
+  // ring index n of a ring of S stages: FULL parity of the use, EMPTY parity of the use before
+  auto full_par = [](int n, int S) -> uint32_t { return (uint32_t)(n / S) & 1u; };
+  auto empty_par = [](int n, int S) -> uint32_t { return (uint32_t)(n / S - 1) & 1u; };
+
+  if (warp == 0) {
+    // ============================================================ producer
+    if (begin < end) {
+      if (lane == 0) { tma_prefetch(&maps.kc); tma_prefetch(&maps.vc); tma_prefetch(&maps.kn); tma_prefetch(&maps.vn); }
+      int u = plan->u0, k = plan->k0, remaining = end - begin;
+      int n = 0, nc = 0;  // ring index of K and raw V; cached blocks so far
+      int k_end = 0, v_end = 0;  // behind the last filled stage of either ring
+      bool run = true;
+      auto take = [&](uint32_t empty, int S) -> bool {  // stage n % S is free
+        return n < S || warp_wait(bar(empty + n % S), empty_par(n, S));
+      };
+      const int row_oob = (int)min((long long)p.n_pages * p.Hkv * ps, 0x7fffffffLL);
+      while (run && remaining > 0) {
+        const Unit x = decode(u);
+        const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
+        // pages of the segment: t = 0 .. np, 32 of them per window, one per lane
+        const int np = min(cdiv(x.C, ps), (k + cached) * ppb) - k * ppb;
+        const int32_t* table = p.pages + x.kv_off + (size_t)k * ppb;
+        auto page_at = [&](int w) -> int {  // -1: no such page
+          const int t = 32 * w + lane;
+          if (t >= np) return -1;
+          const int pg = table[t];
+          if (pg >= 0 && pg < p.n_pages) return pg;
+          report(p.dev_status, SSV_ERR_INVALID);
+          return -2;  // read as zeros
+        };
+        auto scales_at = [&](int pg, float& ks, float& vs) {
+          ks = vs = 1.f;
+          if (pg >= 0) {
+            ks = __ldg(p.k_scale + (size_t)pg * p.Hkv + gh);
+            vs = __ldg(p.v_scale + (size_t)pg * p.Hkv + gh);
+          }
+        };
+        int pg0 = page_at(0), pg1 = page_at(1), pg2 = -1;
+        float ks0, vs0, ks1 = 1.f, vs1 = 1.f;
+        scales_at(pg0, ks0, vs0);
+        for (int i = 0; run && i < cached; ++i) {
+          const int t0 = i * ppb, nb = min(ppb, np - t0);
+          if ((t0 & 31) == 0) {
+            if (i > 0) { pg0 = pg1; pg1 = pg2; ks0 = ks1; vs0 = vs1; }
+            scales_at(pg1, ks1, vs1);
+            pg2 = page_at((t0 >> 5) + 2);
+          }
+          const int src = (t0 + lane) & 31;
+          const int pg = __shfl_sync(0xffffffffu, pg0, src);
+          const float ks = __shfl_sync(0xffffffffu, ks0, src), vs = __shfl_sync(0xffffffffu, vs0, src);
+          const int row = pg >= 0 ? (pg * p.Hkv + gh) * ps : row_oob;
+          auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full) {
+            if (lane == 0) mbar_expect_tx(full, nb * ps * 128);
+            __syncwarp();
+            if (lane < nb) tma_load_2d(dst + lane * ps * 128, map, 0, row, full);
+          };
+          if (!take(B_K_EMPTY, NK)) { run = false; break; }
+          if (!(cta == 0 && nc == p.fault_skip))  // test support: this key block's copy is left out
+            load(&maps.kc, sbase + C_::SM_K + (n % NK) * STAGE, bar(B_K_FULL + n % NK));
+          k_end = n + 1;
+          if (!take(B_R_EMPTY, C_::NR)) { run = false; break; }
+          load(&maps.vc, sbase + C_::SM_R + (n % C_::NR) * STAGE, bar(B_R_FULL + n % C_::NR));
+          v_end = n + 1;
+          // the pages' scales, for the softmax warps
+          if (nc >= NSC && !warp_wait(bar(B_C_EMPTY + nc % NSC), empty_par(nc, NSC))) { run = false; break; }
+          float* sc = reinterpret_cast<float*>(smem + C_::SM_SC) + (nc % NSC) * 20;
+          const float lv = lane < nb ? fmaxf(log2f(vs), -126.f) : -126.f;
+          float top = lv;
 #pragma unroll
-  for (int e = 0; e < E; ++e) q[e] *= qs;
-  float m = -INFINITY, l = 0.f, acc[E] = {0.f, 0.f, 0.f, 0.f};
-  const bool tail_row = i >= N;
-  const int r = i - N, tau_r = tail_row ? tau[r % B] : 0;
-  const int total = C + (tail_row ? N + 2 * B : i + 1);
-  for (int j0 = 0; j0 < total; j0 += U) {
-    float sc[U], vv[U][E];
+          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane < ppb) {
+            sc[lane] = lane < nb ? ks * (p.scale * 1.4426950408889634f) : 0.f;
+            sc[8 + lane] = lane < nb ? lv : top;
+          }
+          if (lane == 0) sc[16] = top;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_C_FULL + nc % NSC));
+          ++n;
+          ++nc;
+        }
+        // fresh rows: a 16-bit block takes two stages, from an even one on
+        for (int i = cached; run && i < len; ++i) {
+          if (n & 1) {
+            if (!take(B_K_EMPTY, NK) || !take(B_R_EMPTY, C_::NR)) { run = false; break; }
+            if (lane == 0) { mbar_arrive(bar(B_K_FULL + n % NK)); mbar_arrive(bar(B_R_FULL + n % C_::NR)); }
+            ++n;
+          }
+          const int z = x.q_off + (k + i - x.cache_blocks) * BN;
+          auto pair = [&](const CUtensorMap* map, uint32_t ring, uint32_t full, uint32_t empty, int S) -> bool {
+            if (n >= S && !(warp_wait(bar(empty + n % S), empty_par(n, S)) &&
+                            warp_wait(bar(empty + (n + 1) % S), empty_par(n + 1, S))))
+              return false;
+            if (lane == 0) {
+              const uint32_t f = bar(full + n % S), dst = sbase + ring + (n % S) * STAGE;
+              mbar_expect_tx(f, 2 * STAGE);
+              tma_load_3d(dst, map, 0, gh, z, f);
+              tma_load_3d(dst + STAGE, map, 64, gh, z, f);
+              mbar_arrive(bar(full + (n + 1) % S));
+            }
+            __syncwarp();
+            return true;
+          };
+          if (!pair(&maps.kn, C_::SM_K, B_K_FULL, B_K_EMPTY, NK)) { run = false; break; }
+          k_end = n + 2;
+          if (!pair(&maps.vn, C_::SM_R, B_R_FULL, B_R_EMPTY, C_::NR)) { run = false; break; }
+          v_end = n + 2;
+          n += 2;
+        }
+        remaining -= len;
+        ++u;
+        k = 0;
+      }
+      // drain (bounded, regardless of abort): the copies that may still be in flight
+      auto drain = [&](uint32_t full, int S, int last) {
+        for (int i = max(last - S, 0); i < last; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(bar(full + i % S), full_par(i, S)) && clock64() - t0 < wb) {
+          }
+        }
+      };
+      drain(B_K_FULL, NK, k_end);
+      drain(B_R_FULL, C_::NR, v_end);
+    }
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer
+    if (lane == 0 && begin < end) {
+      int u = plan->u0, k = plan->k0, remaining = end - begin, nseg = 0, nseg1 = 0;
+      int n = 0, nv = 0, nq = 0;       // K ring index, V blocks, query phases
+      int ns = 0, np = 0;              // one-tile blocks whose S / PV have been issued
+      int n2 = 0;                      // two-tile blocks whose PV has been issued
+      bool run = true;
+      const uint64_t dq0 = smem_desc_sw128(sbase + C_::SM_Q, 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(sbase + C_::SM_K, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(sbase + C_::SM_V, STAGE, 1024);
+      auto wait = [&](uint32_t b, uint32_t parity) -> bool { return mbar_wait_poll(bar(b), parity, abort, wb); };
+      while (run && remaining > 0) {
+        const Unit x = decode(u);
+        const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
+        // S of block i, tile mt, into TMEM column col; the first and last tile of a block wait for
+        // and release its keys, the first and last block of a kind its form of the queries
+        auto issue_s = [&](int i, int mt, uint32_t col) -> bool {
+          const bool q8 = i < cached;
+          if (mt == 0) {
+            if ((i == 0 || i == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) return false;
+            if (!q8 && (n & 1)) {  // the stage left out
+              if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
+              mma_commit(bar(B_K_EMPTY + n % NK));
+              ++n;
+            }
+            if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
+            if (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK))) return false;
+          }
+          tc_fence_after();
+          const uint64_t dq = dq0 + mt * (2 * STAGE >> 4), dk = dk0 + (n % NK) * (STAGE >> 4);
+          if (q8) gemm_q8(tmem + col, dq, dk, kIdE4m3);
+          else gemm_ss_k128_probe(tmem + col, dq, dk, kIdBf16, 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
+          if (mt == x.mc - 1) {
+            for (int e = q8 ? 1 : 2; e > 0; --e, ++n) mma_commit(bar(B_K_EMPTY + n % NK));
+            if (i == cached - 1 || i == len - 1) mma_commit(bar(B_Q_EMPTY));
+          }
+          return true;
+        };
+        auto issue_pv = [&](int i, int mt, uint32_t pcol) {
+          tc_fence_after();
+          gemm_ts_k128_probe(tmem + TM_O + mt * 128, tmem + pcol, dv0 + (nv & 1) * (2 * STAGE >> 4),
+                             i < cached ? kIdPvF16 : kIdPvBf16, i > 0 ? 1u : 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
+        };
+        if (x.mc == 1) {
+          // one active tile: S alternates between two buffers, S(i + 2) after PV(i)
+          auto s_db = [&](int i) -> bool {
+            if (!issue_s(i, 0, (ns & 1) * 128)) return false;
+            mma_commit(bar(B_SDB + (ns & 1)));
+            ++ns;
+            return true;
+          };
+          run = s_db(0) && (len == 1 || s_db(1));
+          for (int i = 0; run && i < len; ++i) {
+            if (!wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u) ||
+                !wait(B_PDB + (np & 1), (uint32_t)(np >> 1) & 1u) ||
+                (i == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1))) {
+              run = false;
+              break;
+            }
+            issue_pv(i, 0, (np & 1) * 128);
+            mma_commit(bar(B_PV_DONE));
+            mma_commit(bar(B_V_EMPTY + (nv & 1)));
+            ++nv;
+            ++np;
+            if (i + 2 < len && !s_db(i + 2)) run = false;
+          }
+        } else {
+          // two tiles: per block PV_0(i) S_0(i + 1) PV_1(i) S_1(i + 1)
+          run = issue_s(0, 0, 0);
+          if (run) {
+            mma_commit(bar(B_S_FULL));
+            run = issue_s(0, 1, 128);
+            mma_commit(bar(B_S_FULL + 1));
+          }
+          for (int i = 0; run && i < len; ++i) {
+            if (!wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u)) { run = false; break; }
+            for (int mt = 0; run && mt < 2; ++mt) {
+              if (!wait(B_P_FULL + mt, (uint32_t)n2 & 1u) ||
+                  (i == 0 && (mt ? nseg1 : nseg) > 0 && !wait(B_O_FREE + mt, ((mt ? nseg1 : nseg) - 1) & 1))) {
+                run = false;
+                break;
+              }
+              issue_pv(i, mt, mt * 128);
+              if (i + 1 < len) {
+                if (!issue_s(i + 1, mt, mt * 128)) { run = false; break; }
+                mma_commit(bar(B_S_FULL + mt));
+              }
+            }
+            mma_commit(bar(B_V_EMPTY + (nv & 1)));
+            ++nv;
+            ++n2;
+          }
+          ++nseg1;
+        }
+        if (!run) break;
+        mma_commit(bar(B_SEG_DONE));
+        ++nseg;
+        remaining -= len;
+        ++u;
+        k = 0;
+      }
+    }
+    if (lane == 0) {
+      // every MMA issued by this thread completes before TMEM is released
+      mma_commit(bar(B_FINAL));
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bar(B_FINAL), 0) && clock64() - t0 < wb) {
+      }
+    }
+  } else if (warp >= 2 + C_::kSoft) {
+    // ============================================================ converters
+    const int ct = threadIdx.x - 32 * (2 + C_::kSoft);
+    constexpr int NT = 32 * C_::kConv;
+    int u = plan->u0, k = plan->k0, remaining = end - begin;
+    int n = 0, nv = 0, nq = 0, nx = 0;
+    bool run = true;
+    while (run && remaining > 0) {
+      const Unit x = decode(u);
+      const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
+      // the unit's queries as the operand of the cached (hi, lo) or the fresh blocks (bf16)
+      auto write_q = [&](bool q8) -> bool {
+        for (int m = ct; m < x.mc * 128; m += NT) {
+          const int tile = m >> 7, ml = m & 127, r_local = tile * R + ml / G;
+          uint4 v[16];
+          if (ml < R * G && r_local < x.nvalid) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.q + ((size_t)(x.q_off + x.row0 + r_local) * p.Hq + gh * G + ml % G) * D);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u;
-      bool ok = j < total;
-      float kk[E] = {0.f, 0.f, 0.f, 0.f};
+            for (int c = 0; c < 16; ++c) v[c] = src[c];
+          } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) vv[u][e] = 0.f;
-      if (ok && j < C) {
-        const size_t at = (size_t)p.pages[s.kv_off + (j >> p.ps_log2)] * p.Hkv + kvh;
-        const size_t off = (at * ps + (j & (ps - 1))) * D;
-        codes(p.k_cache + off, p.k_scale[at], kk);
-        codes(p.v_cache + off, p.v_scale[at], vv[u]);
-      } else if (ok) {
-        const int jn = j - C, t = jn - N;
-        if (tail_row && t >= 0) ok = tail_allowed(r, t, B, tau_r, tau[t % B]);
-        if (ok) {
-          wide(p.k_new + (int64_t)(s.q_off + jn) * p.k_stride + kvh * D, kk);
-          wide(p.v_new + (int64_t)(s.q_off + jn) * p.v_stride + kvh * D, vv[u]);
+            for (int c = 0; c < 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+          }
+          if (m == ct) {  // the operand is free once the last S that reads it is complete
+            if (nq > 0 && !warp_wait(bar(B_Q_EMPTY), (uint32_t)(nq - 1) & 1u)) return false;
+            if (q8 && nx > 1 && !warp_wait(bar(B_X_EMPTY + (nx & 1)), (uint32_t)(nx / 2 - 1) & 1u)) return false;
+          }
+          uint8_t* row = smem + C_::SM_Q + tile * 2 * STAGE + ml * 128;
+          const int sw = ml & 7;
+          if (!q8) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              *reinterpret_cast<uint4*>(row + (c >> 3) * STAGE + (((c & 7) ^ sw) << 4)) = v[c];
+            continue;
+          }
+          float amax = 0.f;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+              amax = fmaxf(amax, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
+            }
+          }
+          // smallest e >= -100 with amax <= 448 2^e = 1.75 2^(e + 8); amax holds a bf16 value
+          const uint32_t bits = __float_as_uint(amax);
+          const int ex = max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+          const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
+          (smem + C_::SM_X)[((nx & 1) * MT + tile) * 128 + ml] = (uint8_t)(int8_t)ex;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t h4[4], l4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // four elements: words 2 e, 2 e + 1 of the 16-element group
+              const uint4& s = v[2 * c + (e >> 1)];
+              const uint32_t wa = (e & 1) ? s.z : s.x, wc = (e & 1) ? s.w : s.y;
+              uint16_t hh[2], ll[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t w = i ? wc : wa;
+                const float a = __uint_as_float(w << 16) * f, b = __uint_as_float(w & 0xffff0000u) * f;
+                hh[i] = f32_to_e4m3x2(a, b);
+                const uint32_t back = e4m3x2_to_f16x2(hh[i]);
+                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                ll[i] = f32_to_e4m3x2(a - r.x, b - r.y);
+              }
+              h4[e] = hh[0] | (uint32_t)hh[1] << 16;
+              l4[e] = ll[0] | (uint32_t)ll[1] << 16;
+            }
+            *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+            *reinterpret_cast<uint4*>(row + STAGE + ((c ^ sw) << 4)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_Q_FULL));
+          if (q8) mbar_arrive(bar(B_X_FULL + (nx & 1)));
+        }
+        ++nq;
+        if (q8) ++nx;
+        return true;
+      };
+      auto v_ready = [&]() -> bool {  // the 16-bit stage of V block nv is free
+        return nv < 2 || warp_wait(bar(B_V_EMPTY + (nv & 1)), (uint32_t)((nv >> 1) - 1) & 1u);
+      };
+      auto v_done = [&](int stages) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_V_FULL + (nv & 1)));
+          for (int e = 0; e < stages; ++e) mbar_arrive(bar(B_R_EMPTY + (n + e) % C_::NR));
+        }
+        n += stages;
+        ++nv;
+      };
+      if (cached > 0) {
+        if (!write_q(true)) { run = false; break; }
+        for (int i = 0; i < cached; ++i) {
+          if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) || !v_ready()) { run = false; break; }
+          const uint8_t* raw = smem + C_::SM_R + (n % C_::NR) * STAGE;
+          uint8_t* dst = smem + C_::SM_V + (nv & 1) * 2 * STAGE;
+          const int keys = x.C - (k + i) * BN;  // rows behind it become zeros
+#pragma unroll
+          for (int it = 0; it < 1024 / NT; ++it) {
+            const int idx = it * NT + ct, key = idx >> 3, c = idx & 7;
+            uint4 s = make_uint4(0, 0, 0, 0);
+            if (key < keys) s = *reinterpret_cast<const uint4*>(raw + idx * 16);
+            const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[2 * e] = e4m3x2_to_f16x2((uint16_t)w[e]);
+              h[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(w[e] >> 16));
+            }
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            // 16-byte chunks 2 c, 2 c + 1 of the key's 256 bytes, in two 64-element columns; the lanes of
+            // either column start with another one, so that eight lanes meet eight banks
+            uint8_t* row = dst + (c >> 2) * STAGE + key * 128;
+            const int c0 = (c & 3) * 2, sw = key & 7, first = c >> 2;
+            *reinterpret_cast<uint4*>(row + (((c0 + first) ^ sw) << 4)) = first ? hi : lo;
+            *reinterpret_cast<uint4*>(row + (((c0 + 1 - first) ^ sw) << 4)) = first ? lo : hi;
+          }
+          v_done(1);
         }
       }
-      float part = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) part = fmaf(q[e], kk[e], part);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-      sc[u] = ok ? part : -INFINITY;
+      if (run && len > cached) {
+        if (!write_q(false)) { run = false; break; }
+        for (int i = cached; i < len; ++i) {
+          if (n & 1) {  // the stage left out
+            if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR))) { run = false; break; }
+            if (lane == 0) mbar_arrive(bar(B_R_EMPTY + n % C_::NR));
+            ++n;
+          }
+          if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) ||
+              !warp_wait(bar(B_R_FULL + (n + 1) % C_::NR), full_par(n + 1, C_::NR)) || !v_ready()) {
+            run = false;
+            break;
+          }
+          const uint4* raw = reinterpret_cast<const uint4*>(smem + C_::SM_R + (n % C_::NR) * STAGE);
+          uint4* dst = reinterpret_cast<uint4*>(smem + C_::SM_V + (nv & 1) * 2 * STAGE);
+          const int keys = x.rows - (k + i - x.cache_blocks) * BN;
+#pragma unroll 4
+          for (int idx = ct; idx < 2048; idx += NT)
+            dst[idx] = ((idx & 1023) >> 3) < keys ? raw[idx] : make_uint4(0, 0, 0, 0);
+          v_done(2);
+        }
+      }
+      remaining -= len;
+      ++u;
+      k = 0;
     }
-    float mx = m;
+  } else {
+    // ============================================================ softmax
+    const int mt = (warp - 2) >> 2, q4 = warp & 3, m = q4 * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t tO = tmem + lane_base + TM_O + mt * 128;
+    const float cexp = p.scale * 1.4426950408889634f;
+    int u = plan->u0, k = plan->k0, remaining = end - begin, seg = 0;
+    int n2 = 0, ndb = 0, nc = 0, nx = 0;  // two-tile / one-tile blocks, cached blocks, row exponents
+    bool run = true;
+    auto scales = [&]() { return reinterpret_cast<const float*>(smem + C_::SM_SC) + (nc % NSC) * 20; };
+    auto scales_wait = [&]() -> bool { return warp_wait(bar(B_C_FULL + nc % NSC), full_par(nc, NSC)); };
+    auto scales_done = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_C_EMPTY + nc % NSC));
+      ++nc;
+    };
+    while (run && remaining > 0) {
+      const Unit x = decode(u);
+      const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
+      const bool complete = (k == 0 && len == x.nblocks);
+      float rowf = 1.f;
+      if (cached > 0) {
+        if (!warp_wait(bar(B_X_FULL + (nx & 1)), (uint32_t)(nx >> 1) & 1u)) { run = false; break; }
+        const int ex = reinterpret_cast<const int8_t*>(smem + C_::SM_X)[((nx & 1) * MT + mt) * 128 + m];
+        rowf = exp2f((float)ex);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_X_EMPTY + (nx & 1)));
+        ++nx;
+      }
+      if (mt >= x.mc) {
+        // the second tile's warps of a one-tile unit: give the scales back
+        for (int i = 0; run && i < cached; ++i) {
+          run = scales_wait();
+          if (run) scales_done();
+        }
+      } else {
+        const int r_local = mt * R + m / G, hj = m % G;
+        const int i = x.row0 + r_local;  // local query row
+        const bool valid = m < R * G && r_local < x.nvalid;
+        const bool warp_active = q4 * 32 < R * G && (mt * R + (q4 * 32) / G) < x.nvalid;
+        const bool db = x.mc == 1;
+        const bool prompt = i < x.N;
+        const int r = i - x.N;
+        uint32_t tm[4] = {0u, 0u, 0u, 0u};  // allowed tail keys of this row
+        if (warp_active && len > cached && x.row0 + x.nvalid > x.N) {  // warp-uniform: fresh blocks and tail rows
+          const int32_t* tau = p.tau + x.tau_off;
+          const int ta = lane < x.B ? tau[lane] : 0, tb = lane + 32 < x.B ? tau[lane + 32] : 0;
+          // a bad stage map cannot index out of range below: report only
+          if (!warp_tau_is_permutation(tau, x.B) && lane == 0) report(p.dev_status, SSV_ERR_BAD_TAU);
+          const bool tail_row = valid && !prompt;
+          const int slot_r = tail_row ? (r % x.B) : 0;
+          const int tra = __shfl_sync(0xffffffffu, ta, slot_r & 31), trb = __shfl_sync(0xffffffffu, tb, slot_r & 31);
+          const int tr = slot_r < 32 ? tra : trb;
+          // le / lt: the slots whose stage is <= tr / < tr, one ballot pair per stage
+          unsigned long long acc = 0ull, le = 0ull, lt = 0ull;
+          for (int v = 1; v <= x.B; ++v) {
+            const uint32_t lo = __ballot_sync(0xffffffffu, ta == v), hi = __ballot_sync(0xffffffffu, tb == v);
+            acc |= ((unsigned long long)hi << 32) | lo;
+            if (v == tr - 1) lt = acc;
+            if (v == tr) le = acc;
+          }
+          // a data row sees the data slots of stages <= its own; a mask row the data slots of
+          // earlier stages and the mask slots of its own stage and later ones
+          const unsigned long long bmask = (x.B >= 64) ? ~0ull : ((1ull << x.B) - 1ull);
+          const bool data_row = r < x.B;
+          const unsigned long long lo_part = !tail_row ? 0ull : (data_row ? le : lt);
+          const unsigned long long hi_part = (!tail_row || data_row) ? 0ull : (~lt & bmask);
+          const unsigned long long w01 = lo_part | (x.B < 64 ? (hi_part << x.B) : 0ull);
+          const unsigned long long w23 = x.B < 64 ? (hi_part >> (64 - x.B)) : hi_part;
+          tm[0] = (uint32_t)w01; tm[1] = (uint32_t)(w01 >> 32);
+          tm[2] = (uint32_t)w23; tm[3] = (uint32_t)(w23 >> 32);
+        }
+        // rows without a query follow along unmasked (their queries are zero) and are dropped at the end
+        float m_used = valid ? -INFINITY : 0.f, l_sum = 0.f, unit = 0.f;
+        for (int jj = 0; jj < len; ++jj) {
+          const int j = k + jj;
+          const bool is_cache = jj < cached;
+          const int sb = db ? (ndb & 1) : mt;
+          const uint32_t tS = tmem + lane_base + sb * 128;
+          const uint32_t sparity = db ? ((ndb >> 1) & 1) : (n2 & 1);
+          if (db) ++ndb; else ++n2;
+          if (is_cache && !scales_wait()) { run = false; break; }
+          if (!warp_wait(db ? bar(B_SDB + sb) : bar(B_S_FULL + mt), sparity)) { run = false; break; }
+          if (!warp_active) {
+            if (is_cache) scales_done();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(db ? bar(B_PDB + sb) : bar(B_P_FULL + mt));
+            continue;
+          }
+          tc_fence_after();
+          // ---- which of the 128 keys this row sees
+          const int kbase = is_cache ? j * BN : (j - x.cache_blocks) * BN;
+          const bool full = is_cache ? (kbase + BN <= x.C) : (kbase + BN <= x.full_new);
+          int lim = BN, lim_rows = 0, toff = 0;  // a prefix, and tail bits for columns < lim_rows
+          if (!full) {
+            if (is_cache) {
+              lim = x.C - kbase;
+            } else if (prompt) {
+              lim = min(i + 1, x.rows) - kbase;
+            } else {
+              lim = x.N - kbase;
+              lim_rows = x.rows - kbase;
+              toff = kbase - x.N;
+            }
+          }
+          auto vis32 = [&](int q) -> uint32_t {
+            uint32_t v = prefix32(lim - 32 * q);
+            if (lim_rows > 32 * q) v |= window32(tm, toff + 32 * q) & prefix32(lim_rows - 32 * q);
+            return v;
+          };
+          // ---- the block's scales: factor of a 16-column group's scores, exponent of its weights
+          const float* sc = scales();
+          const int gsh = p.ps_log2 - 4;
+          auto factor = [&](int q) -> float { return is_cache ? fmaxf(rowf * sc[q >> gsh], 1.17549435e-38f) : cexp; };
+          const float top = is_cache ? sc[16] : unit;
+          const bool grow = jj == 0 || top > unit + kUnitTop;  // the unit has to grow (CTA-uniform)
+          auto shift = [&](int q) -> float { return is_cache ? fmaxf(sc[8 + (q >> gsh)] - unit, -80.f) : -unit; };
+          float lsum = 0.f;
+          bool done = false;
+          // ---- steady state: one pass with the running maximum; falls through, S intact, when some
+          // row's maximum has grown past the threshold
+          auto one_pass = [&](auto masked_tag, auto cache_tag) {
+            constexpr bool kMasked = decltype(masked_tag)::value, kCache = decltype(cache_tag)::value;
+            uint32_t b0[16], b1[16], pw[64];
+            float mx = -INFINITY;
+            tmem_ld16(tS, b0);
+            tmem_wait_ld();
 #pragma unroll
-    for (int u = 0; u < U; ++u) mx = fmaxf(mx, sc[u]);
-    if (mx == -INFINITY) continue;
-    const float corr = exp2f(m - mx);
-    l *= corr;
+            for (int q = 0; q < BN / 16; ++q) {
+              uint32_t* cur = (q & 1) ? b1 : b0;
+              uint32_t* nxt = (q & 1) ? b0 : b1;
+              if (q + 1 < BN / 16) tmem_ld16(tS + (q + 1) * 16, nxt);
+              const float c = kCache ? factor(q) : cexp, sh = kCache ? shift(q) : -unit;
+              const float off = sh - m_used;
+              const uint64_t cc2 = pack2(c, c), of2 = pack2(off, off);
+              uint64_t lp0 = 0ull, lp1 = 0ull;
+              float a0 = -INFINITY, a1 = -INFINITY;
+              uint32_t vq = ~0u;
+              if constexpr (kMasked) vq = vis32(q >> 1) >> ((q & 1) * 16);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= corr;
+              for (int e = 0; e < 8; ++e) {
+                float s0 = __uint_as_float(cur[2 * e]), s1 = __uint_as_float(cur[2 * e + 1]);
+                if constexpr (kMasked) {
+                  const uint32_t bits = vq >> (2 * e);
+                  s0 = (bits & 1u) ? s0 : -INFINITY;
+                  s1 = (bits & 2u) ? s1 : -INFINITY;
+                }
+                if (e & 1) a1 = max3(a1, s0, s1); else a0 = max3(a0, s0, s1);
+                float x0, x1;
+                unpack2(ffma2(pack2(s0, s1), cc2, of2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                if constexpr (kCache) {
+                  const __half2 h = __floats2half2_rn(p0, p1);
+                  pw[q * 8 + e] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                  pw[q * 8 + e] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                if (e & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
+              }
+              mx = fmaxf(mx, fmaxf(a0, a1) * c);
+              float y0, y1;
+              unpack2(fadd2(lp0, lp1), y0, y1);
+              lsum = fmaf(y0 + y1, ex2(-sh), lsum);
+              if (q + 1 < BN / 16) tmem_wait_ld();
+            }
+            if (!__any_sync(0xffffffffu, mx > m_used + kLazy)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float pk = exp2f(sc[u] - mx);
-      l += pk;
+              for (int q = 0; q < BN / 32; ++q) tmem_st16(tS + q * 16, pw + q * 16);
+              done = true;
+            } else {
+              lsum = 0.f;
+            }
+          };
+          if (!grow && __all_sync(0xffffffffu, m_used > -INFINITY)) {
+            if (is_cache) {
+              if (full) one_pass(std::false_type{}, std::true_type{});
+              else one_pass(std::true_type{}, std::true_type{});
+            } else {
+              if (full) one_pass(std::false_type{}, std::false_type{});
+              else one_pass(std::true_type{}, std::false_type{});
+            }
+          }
+          if (!done) {
+            // ---- pass 1: row maximum
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < BN / 16; ++q) {
+              uint32_t sr[16];
+              tmem_ld16(tS + q * 16, sr);
+              tmem_wait_ld();
+              const uint32_t vw = vis32(q >> 1) >> ((q & 1) * 16);
+              float a = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(pk, vv[u][e], acc[e]);
+              for (int e = 0; e < 16; ++e) a = fmaxf(a, ((vw >> e) & 1u) ? __uint_as_float(sr[e]) : -INFINITY);
+              mx = fmaxf(mx, a * factor(q));
+            }
+            const bool need = mx > -INFINITY && (m_used == -INFINITY || mx > m_used + kLazy);
+            const float unit_new = !grow ? unit : (is_cache ? ceilf(top) + kUnitRoom - kUnitTop : 0.f);
+            if (jj > 0 && __any_sync(0xffffffffu, need || unit_new != unit)) {
+              // O holds PV of the earlier blocks, which must be complete: two tiles, S(j) was issued
+              // behind PV(j - 1); one tile, wait for that PV (phase ndb - 2, ndb counting this block)
+              if (db && !warp_wait(bar(B_PV_DONE), ndb & 1)) { run = false; break; }
+              tc_fence_after();
+              const float fm = need ? ex2(m_used - mx) : 1.f;
+              const float f = fm * ex2(unit - unit_new);
+              uint32_t raw[32];
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                tmem_ld32(tO + c * 32, raw);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * f);
+                tmem_st32(tO + c * 32, raw);
+              }
+              tmem_wait_st();
+              l_sum *= fm;
+            }
+            unit = unit_new;
+            if (need) m_used = mx;
+            const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+            // ---- pass 2: chunk q reads S columns [16 q, 16 q + 16) and writes P columns [8 q, 8 q + 8),
+            // which lie in S columns already read
+#pragma unroll 1
+            for (int q = 0; q < BN / 32; ++q) {
+              uint32_t sr[32], pw[16];
+              tmem_ld32(tS + q * 32, sr);
+              tmem_wait_ld();
+              const uint32_t vw = vis32(q);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float c = factor(2 * q + h), sh = shift(2 * q + h);
+                float y = 0.f;
+#pragma unroll
+                for (int e = 8 * h; e < 8 * h + 8; ++e) {
+                  const float p0 = ((vw >> (2 * e)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * e]), c, sh - mref)) : 0.f;
+                  const float p1 =
+                      ((vw >> (2 * e + 1)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * e + 1]), c, sh - mref)) : 0.f;
+                  if (is_cache) {
+                    const __half2 hv = __floats2half2_rn(p0, p1);
+                    pw[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                  } else {
+                    const __nv_bfloat162 hv = __floats2bfloat162_rn(p0, p1);
+                    pw[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                  }
+                  y += p0 + p1;
+                }
+                lsum = fmaf(y, ex2(-sh), lsum);
+              }
+              tmem_st16(tS + q * 16, pw);
+            }
+          }
+          tmem_wait_st();
+          l_sum += lsum;
+          if (is_cache) scales_done();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(db ? bar(B_PDB + sb) : bar(B_P_FULL + mt));
+        }
+        if (!run) break;
+        // ---- epilogue: every PV of the segment is complete; O stays in TMEM until O_FREE
+        if (!warp_wait(bar(B_SEG_DONE), seg & 1)) {
+          run = false;
+          break;
+        }
+        if (warp_active) {
+          tc_fence_after();
+          const float of = exp2f(unit);  // O in units of 2^unit
+          __nv_bfloat16* orow = p.o + ((size_t)(x.q_off + i) * p.Hq + gh * G + hj) * D;
+          auto store_chunk = [&](int q, const float* v, float inv) {
+            if (!valid) return;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const __nv_bfloat162 bv = __floats2bfloat162_rn(v[c + 2 * h] * inv, v[c + 2 * h + 1] * inv);
+                w[h] = *reinterpret_cast<const uint32_t*>(&bv);
+              }
+              *reinterpret_cast<uint4*>(orow + q * 32 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          };
+          if (complete) {
+            const float inv = (l_sum > 0.f) ? 1.f / l_sum : 0.f;
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t raw[32];
+              tmem_ld32(tO + q * 32, raw);
+              tmem_wait_ld();
+              float v[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]) * of;
+              store_chunk(q, v, inv);
+            }
+          } else {
+            // ---- a unit cut across ranks c_a .. c_b of the head: c_a holds its first block, at the end of
+            // its own range, and merges; the others publish their partials and move on
+            const long long cu = unit_cost(u) + kSegCost;
+            const int c_a = owner_at(cu);
+            const int c_b = owner_at(cu + (long long)cost_of(x.rows, x.row0) * (x.nblocks - 1));
+            int32_t* counter = work.cnt + (((size_t)gh * Uh + u) * MT + mt) * 4 + q4;
+            auto slot_of = [&](int rr) -> size_t { return ((size_t)(rr * p.Hkv + gh) * MT + mt) * 128 + m; };
+            if (rank != c_a) {
+              const size_t mine = slot_of(rank);
+              __stcg(reinterpret_cast<float2*>(work.part_ml + mine * 2), make_float2(m_used, l_sum));
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t raw[32];
+                tmem_ld32(tO + q * 32, raw);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                  __stcg(part_at(work.part_o, mine, q * 8 + c / 4),
+                         make_float4(__uint_as_float(raw[c]) * of, __uint_as_float(raw[c + 1]) * of,
+                                     __uint_as_float(raw[c + 2]) * of, __uint_as_float(raw[c + 3]) * of));
+              }
+              __syncwarp();
+              if (lane == 0) red_release_add(counter, 1);
+            } else {
+              int ok = 1;
+              if (lane == 0) ok = wait_count(counter, c_b - c_a, abort, wb) ? 1 : 0;
+              ok = __shfl_sync(0xffffffffu, ok, 0);
+              __syncwarp();
+              if (!ok) run = false;
+            }
+            if (rank == c_a && run) {
+              // in CTA order, so that equal inputs give equal bits
+              float M = m_used;
+              for (int cc = c_a + 1; cc <= c_b; ++cc) M = fmaxf(M, __ldcg(work.part_ml + slot_of(cc) * 2));
+              const float f0 = M == -INFINITY ? 0.f : ex2(m_used - M);
+              float L = l_sum * f0;
+              for (int cc = c_a + 1; cc <= c_b; ++cc) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(work.part_ml + slot_of(cc) * 2));
+                if (M > -INFINITY) L += ml.y * ex2(ml.x - M);
+              }
+              const float inv = (L > 0.f) ? 1.f / L : 0.f;
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t raw[32];
+                tmem_ld32(tO + q * 32, raw);
+                tmem_wait_ld();
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]) * (of * f0);
+                for (int cc = c_a + 1; cc <= c_b; ++cc) {
+                  const size_t sl = slot_of(cc);
+                  const float f = (M == -INFINITY) ? 0.f : ex2(__ldcg(work.part_ml + sl * 2) - M);
+                  float4 w4[8];
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) w4[c] = __ldcg(part_at(work.part_o, sl, q * 8 + c));
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) {
+                    v[4 * c] += w4[c].x * f; v[4 * c + 1] += w4[c].y * f;
+                    v[4 * c + 2] += w4[c].z * f; v[4 * c + 3] += w4[c].w * f;
+                  }
+                }
+                store_chunk(q, v, inv);
+              }
+              if (lane == 0) *counter = 0;  // ready for the next call
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_O_FREE + mt));
+      }
+      remaining -= len;
+      ++seg;
+      ++u;
+      k = 0;
     }
-    m = mx;
   }
-  const float inv = 1.f / l;
-  const __nv_bfloat162 o01 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
-  const __nv_bfloat162 o23 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
-  *reinterpret_cast<uint2*>(p.o + ((size_t)row * p.Hq + h) * D + lane * E) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&o01), *reinterpret_cast<const uint32_t*>(&o23));
+  // ------------------------------------------------------------------ teardown
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort && threadIdx.x == 0) report(p.dev_status, SSV_ERR_TIMEOUT);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 fp8_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// [rows, 128] codes, one page of one head per box
+bool encode_pages(CUtensorMap* m, const void* base, long long rows, int page, CUtensorMapSwizzle sw) {
+  const cuuint64_t dims[2] = {128, (cuuint64_t)rows}, strides[1] = {128};
+  const cuuint32_t box[2] = {128, (cuuint32_t)page}, es[2] = {1, 1};
+  return fp8_encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [rows, heads, 128] bf16 rows `stride` elements apart, 64 columns of one head and 128 rows per box
+bool encode_rows(CUtensorMap* m, const void* base, int heads, long long rows, long long stride) {
+  const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {128 * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, BN}, es[3] = {1, 1, 1};
+  return fp8_encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Fp8Layout {
+  size_t plan, cnt, ml, o, total;
+  int grid, mt;
+};
+
+// Two tiles share a unit's keys where some sequence fills more than one.
+bool fp8_layout(const ssv_attn_fp8_args* a, Fp8Layout* L) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&L->grid, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    L->grid = 152;  // no device: the size of a GB300
+  const int G = a->Hq / a->Hkv, R = 128 / G;
+  const long long max_rows = (long long)a->max_new + 2LL * a->max_block;
+  L->mt = max_rows > R ? 2 : 1;
+  const long long tiles = (max_rows + (long long)L->mt * R - 1) / (L->mt * R);
+  const long long blocks = (long long)a->batch * tiles * (a->max_cache / BN + max_rows / BN + 2 + kSegCost / kBlock1 + 1);
+  if (blocks > (1LL << 30) / kBlock2 || a->Hkv > L->grid) return false;  // the plan's sums are 32-bit
+  size_t off = 0;
+  L->plan = off;
+  off = align_up(off + sizeof(int32_t) * (size_t)L->grid * 4 * (a->batch + 1), 256);
+  L->cnt = off;
+  off = align_up(off + sizeof(int32_t) * (size_t)a->batch * a->Hkv * tiles * L->mt * 4, 256);
+  L->ml = off;
+  off = align_up(off + sizeof(float) * 2 * (size_t)L->grid * L->mt * 128, 256);
+  L->o = off;
+  off = align_up(off + sizeof(float) * (size_t)L->grid * L->mt * 128 * D, 256);
+  L->total = off;
+  return true;
 }
 
 ssv_status fp8_check(const ssv_attn_fp8_args* a) {
@@ -168,34 +1272,74 @@ ssv_status fp8_check(const ssv_attn_fp8_args* a) {
   return (al & 15u) ? SSV_ERR_INVALID : SSV_OK;
 }
 
+
+template <int MT>
+cudaError_t launch_fp8(const AttnFp8Params& p, const Fp8Maps& maps, const Fp8Work& w, int G, int grid, cudaStream_t st) {
+  // a merge waits (bounded) on other CTAs' partials: all must be resident at once, one per SM
+  static std::once_flag once;
+  static cudaError_t ready = cudaSuccess;
+  std::call_once(once, [] {
+    ready = cudaFuncSetAttribute(attn_fp8_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+    int per_sm = 0;
+    if (ready == cudaSuccess)
+      ready = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_fp8_kernel<MT>, Cfg<MT>::kThreads, kMaxSmem);
+    if (ready == cudaSuccess && per_sm < 1) ready = cudaErrorCooperativeLaunchTooLarge;
+  });
+  if (ready != cudaSuccess) return ready;
+  const size_t tables = sizeof(int32_t) * 4 * (size_t)(p.batch + 1);
+  const int in_smem = Cfg<MT>::SM_TOTAL + tables <= kMaxSmem ? 1 : 0;
+  const size_t smem = Cfg<MT>::SM_TOTAL + (in_smem ? tables : 0);
+  return launch_pdl(attn_fp8_kernel<MT>, dim3(grid), dim3(Cfg<MT>::kThreads), smem, st, maps, p, w, G, in_smem);
+}
+
 }  // namespace
 }  // namespace ssv
 
 extern "C" ssv_status ssv_verify_attn_fp8_workspace(const ssv_attn_fp8_args* a, size_t* bytes) {
+  using namespace ssv;
   if (!bytes) return SSV_ERR_INVALID;
-  const ssv_status st = ssv::fp8_check(a);
-  if (st == SSV_OK) *bytes = 256;
-  return st;
+  const ssv_status st = fp8_check(a);
+  if (st != SSV_OK) return st;
+  Fp8Layout L;
+  if (!fp8_layout(a, &L)) return SSV_ERR_UNSUPPORTED;
+  *bytes = (a->batch == 0 || a->total_rows == 0) ? 0 : L.total;
+  return SSV_OK;
 }
 
 extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, size_t ws_bytes, void* stream) {
   using namespace ssv;
-  size_t need = 0;
-  const ssv_status st = ssv_verify_attn_fp8_workspace(a, &need);
+  const ssv_status st = fp8_check(a);
   if (st != SSV_OK) return st;
+  Fp8Layout L;
+  if (!fp8_layout(a, &L)) return SSV_ERR_UNSUPPORTED;
   if (a->batch == 0 || a->total_rows == 0) return SSV_OK;
-  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < need) return SSV_ERR_WORKSPACE;
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < L.total) return SSV_ERR_WORKSPACE;
   const int64_t width = (int64_t)a->Hkv * a->d;
-  AttnFp8Params p{static_cast<const __nv_bfloat16*>(a->q), static_cast<const uint8_t*>(a->k_cache),
-                  static_cast<const uint8_t*>(a->v_cache), a->k_scale, a->v_scale, a->pages,
-                  static_cast<const __nv_bfloat16*>(a->k_new), static_cast<const __nv_bfloat16*>(a->v_new),
-                  static_cast<__nv_bfloat16*>(a->o), a->k_stride ? a->k_stride : width,
-                  a->v_stride ? a->v_stride : width, a->Hq, a->Hkv, ilog2(a->page_size), a->n_pages, a->table_len,
+  const FaultSetting f = fault_for(SSV_FAULT_ATTN);
+  AttnFp8Params p{static_cast<const __nv_bfloat16*>(a->q), a->k_scale, a->v_scale, a->pages,
+                  static_cast<__nv_bfloat16*>(a->o), a->Hq, a->Hkv, ilog2(a->page_size), a->n_pages, a->table_len,
                   a->scale > 0.f ? a->scale : (float)(1.0 / sqrt((double)a->d)), a->seqs, a->batch, a->tau,
-                  a->total_rows, a->total_slots, a->max_cache, a->max_new, a->max_block, a->dev_status};
-  const long long grid = ((long long)a->total_rows * a->Hq + kRowWarps - 1) / kRowWarps;
-  if (grid > 0x7fffffffLL) return SSV_ERR_INVALID;
-  const cudaError_t e = launch_pdl(attn_fp8_row_kernel, dim3((unsigned)grid), dim3(kRowWarps * 32), 0,
-                                   static_cast<cudaStream_t>(stream), p);
+                  a->total_rows, a->total_slots, a->n_pages > 0 ? a->max_cache : 0, a->max_new, a->max_block,
+                  a->dev_status, f.budget, f.skip};
+  Fp8Maps maps;
+  if (!fp8_encode_fn()) return SSV_ERR_CUDA;
+  if (!encode_rows(&maps.kn, a->k_new, a->Hkv, a->total_rows, a->k_stride ? a->k_stride : width) ||
+      !encode_rows(&maps.vn, a->v_new, a->Hkv, a->total_rows, a->v_stride ? a->v_stride : width))
+    return SSV_ERR_CUDA;
+  if (a->n_pages > 0) {
+    const long long rows = (long long)a->n_pages * a->Hkv * a->page_size;
+    if (!encode_pages(&maps.kc, a->k_cache, rows, a->page_size, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_pages(&maps.vc, a->v_cache, rows, a->page_size, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return SSV_ERR_CUDA;
+  } else {
+    maps.kc = maps.kn;  // never read: no sequence may have cached keys
+    maps.vc = maps.vn;
+  }
+  char* w = static_cast<char*>(ws);
+  const Fp8Work work{reinterpret_cast<int32_t*>(w + L.plan), reinterpret_cast<int32_t*>(w + L.cnt),
+                     reinterpret_cast<float*>(w + L.ml), reinterpret_cast<float*>(w + L.o)};
+  const int G = a->Hq / a->Hkv;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = L.mt == 2 ? launch_fp8<2>(p, maps, work, G, L.grid, s) : launch_fp8<1>(p, maps, work, G, L.grid, s);
   return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;
 }

@@ -17,13 +17,12 @@
 //           S = hi K^T + lo K^T on the fp8 tensor path, at the cost of one bf16
 //           product and without converting K; the scale of a page enters with
 //           2^e as a factor of the column group.
-//   values  converted to fp16 (exact), P in fp16: P' = exp2(x - m) vs / 2^u with
-//           vs the page's scale and u one exponent per unit, so that O gathers
-//           in units of 2^u; the row sum l adds P' 2^u / vs.  P' is at most
-//           2^15 and is kept to 11 bits down to 2^-14, that is to weights of
-//           2^-21 and less (u follows the largest vs met, as m does the scores);
-//           pages whose scale is 2^16 below the largest lose bits from there on.
-// Fresh blocks: bf16 S and P (P' = exp2(x - m) / 2^u, any exponent).
+//   values  converted to fp16, with the page's scale: code * vs / 2^u, u one
+//           exponent per unit that follows the largest scale met (exact for a
+//           power of two within 2^22 of the largest).  P = 2^7 exp2(x - m) in
+//           fp16: at most 2^15 where the running maximum lags by 2^8, and 11
+//           bits down to weights of 2^-21.  O gathers in units of 2^u.
+// Fresh blocks: bf16 S; V as it is, P = 2^(7-u) exp2(x - m) in bf16.
 //
 // Scheduling: persistent, one CTA per SM; per kv head the units' blocks are
 // cut into contiguous ranges of equal estimated cost, one per CTA; a unit cut
@@ -31,14 +30,20 @@
 // order by the CTA that holds its first block (bounded wait on per-row-group
 // counters).  The plan is derived on the device from seqs.
 //
-// Roles of a CTA (10 warps for one tile, 12 for two):
-//   warp 0       page lookups (32 pages ahead, one per lane), TMA of K pages
-//                (swizzled, the operand itself) and V pages (raw) into rings,
-//                fresh rows into two ring stages at once; the pages' scales
-//   warp 1       MMA issue: S into TMEM, O += P V with P from TMEM
-//   warps 2..    softmax, four per tile, one TMEM lane quadrant each
-//   the others   queries into the operand's form; V codes to fp16 (rows behind
-//                the last token become 0, so nothing there is ever multiplied)
+// Roles of a CTA (16 warps, 128 registers each; warp 3 idles, so that a set's
+// softmax warps meet the four TMEM lane quadrants in order):
+//   warp 0        page lookups (32 pages ahead, one per lane), TMA of K pages
+//                 (swizzled, the operand itself) and V pages (raw) into rings,
+//                 fresh rows into two ring stages at once; the pages' scales
+//   warps 1, 2    MMA issue, one warp per S / P / O set: PV(n), S(n + 2).  The
+//                 work between two products leaves the tensor pipe to the other
+//                 set's warp
+//   warps 4..11   softmax, four per set, one TMEM lane quadrant each.  A unit of
+//                 two tiles gives each its set (job n: block n / 2); a unit of
+//                 one tile gives the sets its blocks in turn (job n: block n),
+//                 and the first set joins both at the end
+//   warps 12..15  queries into the operand's form; V codes to fp16 (rows behind
+//                 the last token become 0, so nothing there is ever multiplied)
 // Every wait is bounded; an expired one raises the CTA's abort flag, copies and
 // MMAs in flight are drained, TMEM is freed and SSV_ERR_TIMEOUT reported.
 #include "ssv_internal.cuh"
@@ -63,10 +68,14 @@ constexpr int NK = 4;                       // K ring stages
 constexpr int NSC = 8;                      // blocks of page scales in flight
 constexpr uint32_t STAGE = 128 * 128;       // one e4m3 tile, or half a 16-bit one
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TM_O = 256;              // O_mt at columns 256 + 128 mt; S / P at 128 mt
+constexpr int kSoft = 8, kConv = 4, kThreads = 512;
+constexpr uint32_t TM_O = 256;              // O of set t at columns 256 + 128 t; S / P at 128 t
 constexpr float kLazy = 8.f;                // the running maximum may lag by 2^8
-constexpr float kUnitTop = 7.f;             // vs / 2^u <= 2^7: P' <= 2^15 in fp16
+constexpr float kWeight = 7.f;              // P holds weights times 2^7
+constexpr float kUnitTop = 7.f;             // vs / 2^u <= 2^7: |code| vs / 2^u < 2^16 in fp16
 constexpr float kUnitRoom = 2.f;            // u leaves that much for larger scales to come
+constexpr int SC = 20;                      // floats of a block's scales: K factor of every 16 keys x 8, log2 of the
+                                            // V scale x 8, u
 // Estimated costs of the plan, in units of 0.1 us: a block of one / two tiles
 // and a segment's fixed work; a merge of partials costs about kMergeBlocks blocks.
 constexpr int kBlock1 = 7, kBlock2 = 12, kSegCost = 40;
@@ -85,14 +94,12 @@ enum : uint32_t {
   B_Q_EMPTY = B_Q_FULL + 1,
   B_X_FULL = B_Q_EMPTY + 1,      // row exponents, two buffers
   B_X_EMPTY = B_X_FULL + 2,
-  B_S_FULL = B_X_EMPTY + 2,      // + tile (two active tiles)
-  B_P_FULL = B_S_FULL + 2,
-  B_SDB = B_P_FULL + 2,          // + S buffer (one active tile)
-  B_PDB = B_SDB + 2,
-  B_PV_DONE = B_PDB + 2,         // one active tile: each PV complete
-  B_O_FREE = B_PV_DONE + 1,      // + tile
-  B_SEG_DONE = B_O_FREE + 2,
-  B_FINAL = B_SEG_DONE + 1,
+  B_S_FULL = B_X_EMPTY + 2,      // + set
+  B_P_FULL = B_S_FULL + 2,       // + set
+  B_SEG_DONE = B_P_FULL + 2,     // + set: every PV of the segment complete
+  B_O_FREE = B_SEG_DONE + 2,     // both sets' O read
+  B_ML_FULL = B_O_FREE + 1,      // the second set's maxima and sums (one tile)
+  B_FINAL = B_ML_FULL + 1,
   B_COUNT = B_FINAL + 1
 };
 
@@ -132,16 +139,15 @@ struct PlanHdr {
 
 template <int MT>
 struct Cfg {
-  // at most twelve warps, three per scheduler: 168 registers each
-  static constexpr int kSoft = 4 * MT, kConv = MT == 1 ? 4 : 2, kThreads = 32 * (2 + kSoft + kConv);
   static constexpr int NR = MT == 1 ? 4 : 2;                // raw V stages
   static constexpr uint32_t SM_Q = 0;                       // per tile: hi, lo; or the bf16 tile
   static constexpr uint32_t SM_K = SM_Q + MT * 2 * STAGE;
   static constexpr uint32_t SM_R = SM_K + NK * STAGE;
   static constexpr uint32_t SM_V = SM_R + NR * STAGE;       // 2 x 32 KB
-  static constexpr uint32_t SM_SC = SM_V + 4 * STAGE;       // [NSC][20]: k factor x 8, log2 v scale x 8, its maximum
-  static constexpr uint32_t SM_X = SM_SC + NSC * 20 * 4;    // [2][MT][128] int8 row exponents
-  static constexpr uint32_t SM_BAR = SM_X + 2 * MT * 128;
+  static constexpr uint32_t SM_SC = SM_V + 4 * STAGE;       // [NSC][SC]
+  static constexpr uint32_t SM_X = SM_SC + NSC * SC * 4;    // [2][MT][128] int8 row exponents
+  static constexpr uint32_t SM_ML = SM_X + 2 * MT * 128;    // [128] (m, l) of the second set; then its u
+  static constexpr uint32_t SM_BAR = SM_ML + 128 * 8 + 8;
   static constexpr uint32_t SM_PLAN = SM_BAR + 8 * B_COUNT + 16;
   static constexpr uint32_t SM_TOTAL = (SM_PLAN + sizeof(PlanHdr) + 15) / 16 * 16;  // planning tables follow
 };
@@ -160,6 +166,10 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void red_release_add(int32_t* p, int v) {
@@ -223,7 +233,7 @@ constexpr uint32_t kIdPvF16 = kIdShape | (1u << 16);       // kind::f16, f16 x f
 constexpr uint32_t kIdPvBf16 = kIdBf16 | (1u << 16);
 
 template <int MT>
-__global__ void __launch_bounds__(Cfg<MT>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, const Fp8Work work, int G,
                 int plan_smem) {
   using C_ = Cfg<MT>;
@@ -351,10 +361,11 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       *abort = 0;
       for (uint32_t i = 0; i < B_COUNT; ++i) {
         uint32_t n = 1;
-        if ((i >= B_R_EMPTY && i < B_V_EMPTY) || i == B_Q_FULL || i == B_X_FULL || i == B_X_FULL + 1) n = C_::kConv;
-        if ((i >= B_C_EMPTY && i < B_Q_FULL) || i == B_X_EMPTY || i == B_X_EMPTY + 1) n = C_::kSoft;
-        if (i == B_P_FULL || i == B_P_FULL + 1 || i == B_PDB || i == B_PDB + 1 || i == B_O_FREE || i == B_O_FREE + 1)
-          n = 4;
+        if ((i >= B_R_EMPTY && i < B_V_EMPTY) || i == B_Q_FULL || i == B_X_FULL || i == B_X_FULL + 1) n = kConv;
+        if (i >= B_C_EMPTY && i < B_Q_FULL) n = kSoft + kConv;
+        if ((i >= B_K_EMPTY && i < B_R_FULL) || i == B_V_EMPTY || i == B_V_EMPTY + 1 || i == B_Q_EMPTY || i == B_FINAL) n = 2;
+        if (i == B_X_EMPTY || i == B_X_EMPTY + 1 || i == B_O_FREE) n = kSoft;
+        if (i == B_P_FULL || i == B_P_FULL + 1 || i == B_ML_FULL) n = 4;
         mbar_init(bar(i), n);
       }
       fence_mbar_init();
@@ -455,6 +466,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         int pg0 = page_at(0), pg1 = page_at(1), pg2 = -1;
         float ks0, vs0, ks1 = 1.f, vs1 = 1.f;
         scales_at(pg0, ks0, vs0);
+        float unit = 0.f;
         for (int i = 0; run && i < cached; ++i) {
           const int t0 = i * ppb, nb = min(ppb, np - t0);
           if ((t0 & 31) == 0) {
@@ -480,16 +492,21 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           v_end = n + 1;
           // the pages' scales, for the softmax warps
           if (nc >= NSC && !warp_wait(bar(B_C_EMPTY + nc % NSC), empty_par(nc, NSC))) { run = false; break; }
-          float* sc = reinterpret_cast<float*>(smem + C_::SM_SC) + (nc % NSC) * 20;
+          float* sc = reinterpret_cast<float*>(smem + C_::SM_SC) + (nc % NSC) * SC;
+          const float kf = lane < nb ? ks * (p.scale * 1.4426950408889634f) : 0.f;
           const float lv = lane < nb ? fmaxf(log2f(vs), -126.f) : -126.f;
           float top = lv;
 #pragma unroll
           for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane < ppb) {
-            sc[lane] = lane < nb ? ks * (p.scale * 1.4426950408889634f) : 0.f;
-            sc[8 + lane] = lane < nb ? lv : top;
+          top = __shfl_sync(0xffffffffu, top, 0);
+          if (i == 0 || top > unit + kUnitTop) unit = ceilf(top) + kUnitRoom - kUnitTop;
+          const int page16 = (lane & 7) >> (p.ps_log2 - 4);  // page of 16 keys
+          const float kf16 = __shfl_sync(0xffffffffu, kf, page16), lv16 = __shfl_sync(0xffffffffu, lv, page16);
+          if (lane < 8) {
+            sc[lane] = kf16;
+            sc[8 + lane] = lv16;
           }
-          if (lane == 0) sc[16] = top;
+          if (lane == 0) sc[16] = unit;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_C_FULL + nc % NSC));
           ++n;
@@ -538,14 +555,15 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       drain(B_K_FULL, NK, k_end);
       drain(B_R_FULL, C_::NR, v_end);
     }
-  } else if (warp == 1) {
-    // ============================================================ MMA issuer
+  } else if (warp == 1 || warp == 2) {
+    // ============================================================ MMA issuers
+    const int set = warp - 1;
     if (lane == 0 && begin < end) {
-      int u = plan->u0, k = plan->k0, remaining = end - begin, nseg = 0, nseg1 = 0;
+      int u = plan->u0, k = plan->k0, remaining = end - begin, nseg = 0;
       int n = 0, nv = 0, nq = 0;       // K ring index, V blocks, query phases
-      int ns = 0, np = 0;              // one-tile blocks whose S / PV have been issued
-      int n2 = 0;                      // two-tile blocks whose PV has been issued
+      uint32_t pph = 0u;               // parity of the set's next P
       bool run = true;
+      const uint32_t tS = tmem + set * 128, tO = tmem + TM_O + set * 128;
       const uint64_t dq0 = smem_desc_sw128(sbase + C_::SM_Q, 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(sbase + C_::SM_K, 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(sbase + C_::SM_V, STAGE, 1024);
@@ -553,88 +571,66 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       while (run && remaining > 0) {
         const Unit x = decode(u);
         const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
-        // S of block i, tile mt, into TMEM column col; the first and last tile of a block wait for
-        // and release its keys, the first and last block of a kind its form of the queries
-        auto issue_s = [&](int i, int mt, uint32_t col) -> bool {
-          const bool q8 = i < cached;
-          if (mt == 0) {
-            if ((i == 0 || i == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) return false;
+        const bool two = x.mc == 2;
+        const int step = two ? 1 : 2, first = two ? 0 : set;   // blocks of this set: first, first + step, ..
+        const uint64_t dq = dq0 + (two ? set : 0) * (2 * STAGE >> 4);
+        int is = 0;        // next block whose keys pass (the other set's included)
+        int iv = 0;        // next block whose values pass
+        bool freed = nseg == 0;
+        auto give = [&](uint32_t b) {  // this set's MMAs so far done with a buffer; in turn, the other set has none
+          mma_commit(bar(b));
+          if (!two) mma_commit(bar(b));
+        };
+        // S of block i (one of this set's), passing over the other set's blocks before it; i == len: only that
+        auto issue_s = [&](int i) -> bool {
+          for (; is < len && is <= i; ++is) {
+            const bool q8 = is < cached;
+            if ((is == 0 || is == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) return false;
             if (!q8 && (n & 1)) {  // the stage left out
-              if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
-              mma_commit(bar(B_K_EMPTY + n % NK));
+              if (set == 0) {
+                if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
+                mbar_arrive_n(bar(B_K_EMPTY + n % NK), 2);
+              }
               ++n;
             }
-            if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
-            if (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK))) return false;
-          }
-          tc_fence_after();
-          const uint64_t dq = dq0 + mt * (2 * STAGE >> 4), dk = dk0 + (n % NK) * (STAGE >> 4);
-          if (q8) gemm_q8(tmem + col, dq, dk, kIdE4m3);
-          else gemm_ss_k128_probe(tmem + col, dq, dk, kIdBf16, 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
-          if (mt == x.mc - 1) {
-            for (int e = q8 ? 1 : 2; e > 0; --e, ++n) mma_commit(bar(B_K_EMPTY + n % NK));
-            if (i == cached - 1 || i == len - 1) mma_commit(bar(B_Q_EMPTY));
+            if (is == i) {
+              if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
+              if (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK))) return false;
+              tc_fence_after();
+              const uint64_t dk = dk0 + (n % NK) * (STAGE >> 4);
+              if (q8) gemm_q8(tS, dq, dk, kIdE4m3);
+              else gemm_ss_k128_probe(tS, dq, dk, kIdBf16, 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
+              mma_commit(bar(B_S_FULL + set));
+              give(B_K_EMPTY + n % NK);
+              if (!q8) give(B_K_EMPTY + (n + 1) % NK);
+            }
+            n += q8 ? 1 : 2;
+            // behind the last S of either form of the queries
+            if (is == cached - 1 || is == len - 1) mma_commit(bar(B_Q_EMPTY));
           }
           return true;
         };
-        auto issue_pv = [&](int i, int mt, uint32_t pcol) {
+        run = issue_s(first);
+        for (int i = first; run && i < len; i += step) {
+          nv += i - iv;
+          iv = i;
+          if (!wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u) || !wait(B_P_FULL + set, pph) ||
+              (!freed && !wait(B_O_FREE, (nseg - 1) & 1))) {
+            run = false;
+            break;
+          }
+          freed = true;
+          pph ^= 1u;
           tc_fence_after();
-          gemm_ts_k128_probe(tmem + TM_O + mt * 128, tmem + pcol, dv0 + (nv & 1) * (2 * STAGE >> 4),
-                             i < cached ? kIdPvF16 : kIdPvBf16, i > 0 ? 1u : 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
-        };
-        if (x.mc == 1) {
-          // one active tile: S alternates between two buffers, S(i + 2) after PV(i)
-          auto s_db = [&](int i) -> bool {
-            if (!issue_s(i, 0, (ns & 1) * 128)) return false;
-            mma_commit(bar(B_SDB + (ns & 1)));
-            ++ns;
-            return true;
-          };
-          run = s_db(0) && (len == 1 || s_db(1));
-          for (int i = 0; run && i < len; ++i) {
-            if (!wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u) ||
-                !wait(B_PDB + (np & 1), (uint32_t)(np >> 1) & 1u) ||
-                (i == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1))) {
-              run = false;
-              break;
-            }
-            issue_pv(i, 0, (np & 1) * 128);
-            mma_commit(bar(B_PV_DONE));
-            mma_commit(bar(B_V_EMPTY + (nv & 1)));
-            ++nv;
-            ++np;
-            if (i + 2 < len && !s_db(i + 2)) run = false;
-          }
-        } else {
-          // two tiles: per block PV_0(i) S_0(i + 1) PV_1(i) S_1(i + 1)
-          run = issue_s(0, 0, 0);
-          if (run) {
-            mma_commit(bar(B_S_FULL));
-            run = issue_s(0, 1, 128);
-            mma_commit(bar(B_S_FULL + 1));
-          }
-          for (int i = 0; run && i < len; ++i) {
-            if (!wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u)) { run = false; break; }
-            for (int mt = 0; run && mt < 2; ++mt) {
-              if (!wait(B_P_FULL + mt, (uint32_t)n2 & 1u) ||
-                  (i == 0 && (mt ? nseg1 : nseg) > 0 && !wait(B_O_FREE + mt, ((mt ? nseg1 : nseg) - 1) & 1))) {
-                run = false;
-                break;
-              }
-              issue_pv(i, mt, mt * 128);
-              if (i + 1 < len) {
-                if (!issue_s(i + 1, mt, mt * 128)) { run = false; break; }
-                mma_commit(bar(B_S_FULL + mt));
-              }
-            }
-            mma_commit(bar(B_V_EMPTY + (nv & 1)));
-            ++nv;
-            ++n2;
-          }
-          ++nseg1;
+          gemm_ts_k128_probe(tO, tS, dv0 + (nv & 1) * (2 * STAGE >> 4), i < cached ? kIdPvF16 : kIdPvBf16,
+                             i > first ? 1u : 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
+          give(B_V_EMPTY + (nv & 1));
+          if (!issue_s(i + step)) run = false;
         }
+        if (run && !freed) run = wait(B_O_FREE, (nseg - 1) & 1);  // a segment without a block of this set
         if (!run) break;
-        mma_commit(bar(B_SEG_DONE));
+        nv += len - iv;
+        mma_commit(bar(B_SEG_DONE + set));
         ++nseg;
         remaining -= len;
         ++u;
@@ -642,18 +638,18 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       }
     }
     if (lane == 0) {
-      // every MMA issued by this thread completes before TMEM is released
+      // every MMA issued by either thread completes before TMEM is released
       mma_commit(bar(B_FINAL));
       const long long t0 = clock64();
       while (!mbar_try_wait(bar(B_FINAL), 0) && clock64() - t0 < wb) {
       }
     }
-  } else if (warp >= 2 + C_::kSoft) {
+  } else if (warp >= 12) {
     // ============================================================ converters
-    const int ct = threadIdx.x - 32 * (2 + C_::kSoft);
-    constexpr int NT = 32 * C_::kConv;
+    const int ct = threadIdx.x - 32 * 12;
+    constexpr int NT = 32 * kConv;
     int u = plan->u0, k = plan->k0, remaining = end - begin;
-    int n = 0, nv = 0, nq = 0, nx = 0;
+    int n = 0, nv = 0, nq = 0, nx = 0, nc = 0;
     bool run = true;
     while (run && remaining > 0) {
       const Unit x = decode(u);
@@ -662,15 +658,23 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       auto write_q = [&](bool q8) -> bool {
         for (int m = ct; m < x.mc * 128; m += NT) {
           const int tile = m >> 7, ml = m & 127, r_local = tile * R + ml / G;
-          uint4 v[16];
-          if (ml < R * G && r_local < x.nvalid) {
-            const uint4* src = reinterpret_cast<const uint4*>(
+          const uint4* src = nullptr;  // the row's 256 bytes; an empty row is zeros
+          if (ml < R * G && r_local < x.nvalid)
+            src = reinterpret_cast<const uint4*>(
                 p.q + ((size_t)(x.q_off + x.row0 + r_local) * p.Hq + gh * G + ml % G) * D);
+          auto chunk = [&](int c) { return src ? __ldg(src + c) : make_uint4(0, 0, 0, 0); };
+          float amax = 0.f;
+          if (q8) {
+#pragma unroll 8
+            for (int c = 0; c < 16; ++c) {
+              const uint4 v = chunk(c);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = src[c];
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+              for (int e = 0; e < 4; ++e) {
+                const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+                amax = fmaxf(amax, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
+              }
+            }
           }
           if (m == ct) {  // the operand is free once the last S that reads it is complete
             if (nq > 0 && !warp_wait(bar(B_Q_EMPTY), (uint32_t)(nq - 1) & 1u)) return false;
@@ -679,39 +683,27 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           uint8_t* row = smem + C_::SM_Q + tile * 2 * STAGE + ml * 128;
           const int sw = ml & 7;
           if (!q8) {
-#pragma unroll
+#pragma unroll 8
             for (int c = 0; c < 16; ++c)
-              *reinterpret_cast<uint4*>(row + (c >> 3) * STAGE + (((c & 7) ^ sw) << 4)) = v[c];
+              *reinterpret_cast<uint4*>(row + (c >> 3) * STAGE + (((c & 7) ^ sw) << 4)) = chunk(c);
             continue;
-          }
-          float amax = 0.f;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-              amax = fmaxf(amax, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
-            }
           }
           // smallest e >= -100 with amax <= 448 2^e = 1.75 2^(e + 8); amax holds a bf16 value
           const uint32_t bits = __float_as_uint(amax);
           const int ex = max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
           const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
           (smem + C_::SM_X)[((nx & 1) * MT + tile) * 128 + ml] = (uint8_t)(int8_t)ex;
-#pragma unroll
+#pragma unroll 2
           for (int c = 0; c < 8; ++c) {
+            const uint4 v0 = chunk(2 * c), v1 = chunk(2 * c + 1);
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
             uint32_t h4[4], l4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              // four elements: words 2 e, 2 e + 1 of the 16-element group
-              const uint4& s = v[2 * c + (e >> 1)];
-              const uint32_t wa = (e & 1) ? s.z : s.x, wc = (e & 1) ? s.w : s.y;
               uint16_t hh[2], ll[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t w = i ? wc : wa;
-                const float a = __uint_as_float(w << 16) * f, b = __uint_as_float(w & 0xffff0000u) * f;
+                const float a = __uint_as_float(w[2 * e + i] << 16) * f, b = __uint_as_float(w[2 * e + i] & 0xffff0000u) * f;
                 hh[i] = f32_to_e4m3x2(a, b);
                 const uint32_t back = e4m3x2_to_f16x2(hh[i]);
                 const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&back));
@@ -750,30 +742,45 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       if (cached > 0) {
         if (!write_q(true)) { run = false; break; }
         for (int i = 0; i < cached; ++i) {
-          if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) || !v_ready()) { run = false; break; }
-          const uint8_t* raw = smem + C_::SM_R + (n % C_::NR) * STAGE;
-          uint8_t* dst = smem + C_::SM_V + (nv & 1) * 2 * STAGE;
+          if (!warp_wait(bar(B_C_FULL + nc % NSC), full_par(nc, NSC)) ||
+              !warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) || !v_ready()) {
+            run = false;
+            break;
+          }
+          const uint8_t* raw = smem + C_::SM_R + (n % C_::NR) * STAGE + ct * 16;
+          const float* sc = reinterpret_cast<const float*>(smem + C_::SM_SC) + (nc % NSC) * SC;
+          const float unit = sc[16];
           const int keys = x.C - (k + i) * BN;  // rows behind it become zeros
+          static_assert(NT == 128, "sixteen keys per round");
+          // this thread: 16 codes (chunk c) of every 16th key; 16-byte chunks 2 c, 2 c + 1 of the key's 256
+          // bytes, in two 64-element columns.  The lanes of either column start with another one, so that
+          // eight lanes meet eight banks.
+          const int c = ct & 7, key0 = ct >> 3, c0 = (c & 3) * 2, sw = key0 & 7, first = c >> 2;
+          uint8_t* dst = smem + C_::SM_V + (nv & 1) * 2 * STAGE + first * STAGE + key0 * 128;
+          uint8_t* dst0 = dst + (((c0 + first) ^ sw) << 4);
+          uint8_t* dst1 = dst + (((c0 + 1 - first) ^ sw) << 4);
+          uint4 s[8];
 #pragma unroll
-          for (int it = 0; it < 1024 / NT; ++it) {
-            const int idx = it * NT + ct, key = idx >> 3, c = idx & 7;
-            uint4 s = make_uint4(0, 0, 0, 0);
-            if (key < keys) s = *reinterpret_cast<const uint4*>(raw + idx * 16);
-            const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+          for (int it = 0; it < 8; ++it) s[it] = *reinterpret_cast<const uint4*>(raw + it * NT * 16);
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            if (it * 16 + key0 >= keys) s[it] = make_uint4(0, 0, 0, 0);
+            const __half2 f = __float2half2_rn(ex2(sc[8 + it] - unit));
+            const uint32_t w[4] = {s[it].x, s[it].y, s[it].z, s[it].w};
             uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[2 * e] = e4m3x2_to_f16x2((uint16_t)w[e]);
-              h[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(w[e] >> 16));
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t v = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), f);
+              h[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
             const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            // 16-byte chunks 2 c, 2 c + 1 of the key's 256 bytes, in two 64-element columns; the lanes of
-            // either column start with another one, so that eight lanes meet eight banks
-            uint8_t* row = dst + (c >> 2) * STAGE + key * 128;
-            const int c0 = (c & 3) * 2, sw = key & 7, first = c >> 2;
-            *reinterpret_cast<uint4*>(row + (((c0 + first) ^ sw) << 4)) = first ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (((c0 + 1 - first) ^ sw) << 4)) = first ? lo : hi;
+            *reinterpret_cast<uint4*>(dst0 + it * 16 * 128) = first ? hi : lo;
+            *reinterpret_cast<uint4*>(dst1 + it * 16 * 128) = first ? lo : hi;
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_C_EMPTY + nc % NSC));
+          ++nc;
           v_done(1);
         }
       }
@@ -803,26 +810,22 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       ++u;
       k = 0;
     }
-  } else {
+  } else if (warp >= 4) {
     // ============================================================ softmax
-    const int mt = (warp - 2) >> 2, q4 = warp & 3, m = q4 * 32 + lane;
+    const int set = (warp - 4) >> 2, q4 = warp & 3, m = q4 * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t tO = tmem + lane_base + TM_O + mt * 128;
+    const uint32_t tS = tmem + lane_base + set * 128, tO = tmem + lane_base + TM_O + set * 128;
     const float cexp = p.scale * 1.4426950408889634f;
     int u = plan->u0, k = plan->k0, remaining = end - begin, seg = 0;
-    int n2 = 0, ndb = 0, nc = 0, nx = 0;  // two-tile / one-tile blocks, cached blocks, row exponents
+    int nc = 0, nx = 0, nml = 0;  // cached blocks, row exponents, joins so far
+    uint32_t sph = 0u;            // parity of this set's next S
     bool run = true;
-    auto scales = [&]() { return reinterpret_cast<const float*>(smem + C_::SM_SC) + (nc % NSC) * 20; };
-    auto scales_wait = [&]() -> bool { return warp_wait(bar(B_C_FULL + nc % NSC), full_par(nc, NSC)); };
-    auto scales_done = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_C_EMPTY + nc % NSC));
-      ++nc;
-    };
     while (run && remaining > 0) {
       const Unit x = decode(u);
       const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
       const bool complete = (k == 0 && len == x.nblocks);
+      const bool two = x.mc == 2;
+      const int mt = two ? set : 0, jobs = two ? 2 * len : len;
       float rowf = 1.f;
       if (cached > 0) {
         if (!warp_wait(bar(B_X_FULL + (nx & 1)), (uint32_t)(nx >> 1) & 1u)) { run = false; break; }
@@ -832,18 +835,11 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         if (lane == 0) mbar_arrive(bar(B_X_EMPTY + (nx & 1)));
         ++nx;
       }
-      if (mt >= x.mc) {
-        // the second tile's warps of a one-tile unit: give the scales back
-        for (int i = 0; run && i < cached; ++i) {
-          run = scales_wait();
-          if (run) scales_done();
-        }
-      } else {
+      {
         const int r_local = mt * R + m / G, hj = m % G;
         const int i = x.row0 + r_local;  // local query row
         const bool valid = m < R * G && r_local < x.nvalid;
         const bool warp_active = q4 * 32 < R * G && (mt * R + (q4 * 32) / G) < x.nvalid;
-        const bool db = x.mc == 1;
         const bool prompt = i < x.N;
         const int r = i - x.N;
         uint32_t tm[4] = {0u, 0u, 0u, 0u};  // allowed tail keys of this row
@@ -877,19 +873,22 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         }
         // rows without a query follow along unmasked (their queries are zero) and are dropped at the end
         float m_used = valid ? -INFINITY : 0.f, l_sum = 0.f, unit = 0.f;
-        for (int jj = 0; jj < len; ++jj) {
-          const int j = k + jj;
-          const bool is_cache = jj < cached;
-          const int sb = db ? (ndb & 1) : mt;
-          const uint32_t tS = tmem + lane_base + sb * 128;
-          const uint32_t sparity = db ? ((ndb >> 1) & 1) : (n2 & 1);
-          if (db) ++ndb; else ++n2;
-          if (is_cache && !scales_wait()) { run = false; break; }
-          if (!warp_wait(db ? bar(B_SDB + sb) : bar(B_S_FULL + mt), sparity)) { run = false; break; }
+        for (int job = set; job < jobs; job += 2) {
+          const int jj = two ? job >> 1 : job, j = k + jj;
+          const bool is_cache = jj < cached, first = job == set;
+          const int e = nc + jj;  // scales of the block
+          if (is_cache && !warp_wait(bar(B_C_FULL + e % NSC), full_par(e, NSC))) { run = false; break; }
+          if (!warp_wait(bar(B_S_FULL + set), sph)) { run = false; break; }
+          sph ^= 1u;
+          // (a block that one set alone works on is given back by it for both)
+          auto scales_done = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive_n(bar(B_C_EMPTY + e % NSC), two ? 1 : 2);
+          };
           if (!warp_active) {
             if (is_cache) scales_done();
             __syncwarp();
-            if (lane == 0) mbar_arrive(db ? bar(B_PDB + sb) : bar(B_P_FULL + mt));
+            if (lane == 0) mbar_arrive(bar(B_P_FULL + set));
             continue;
           }
           tc_fence_after();
@@ -913,14 +912,21 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             if (lim_rows > 32 * q) v |= window32(tm, toff + 32 * q) & prefix32(lim_rows - 32 * q);
             return v;
           };
-          // ---- the block's scales: factor of a 16-column group's scores, exponent of its weights
-          const float* sc = scales();
-          const int gsh = p.ps_log2 - 4;
-          auto factor = [&](int q) -> float { return is_cache ? fmaxf(rowf * sc[q >> gsh], 1.17549435e-38f) : cexp; };
-          const float top = is_cache ? sc[16] : unit;
-          const bool grow = jj == 0 || top > unit + kUnitTop;  // the unit has to grow (CTA-uniform)
-          auto shift = [&](int q) -> float { return is_cache ? fmaxf(sc[8 + (q >> gsh)] - unit, -80.f) : -unit; };
-          float lsum = 0.f;
+          // ---- factors of the scores of every 16 columns; the unit of O at this block
+          float cf[8], unit_new = first ? 0.f : unit;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) cf[q] = cexp;
+          if (is_cache) {
+            const float4* sc = reinterpret_cast<const float4*>(smem + C_::SM_SC) + (e % NSC) * (SC / 4);
+            const float4 c0 = sc[0], c1 = sc[1];
+            const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) cf[q] = fmaxf(rowf * c[q], 1.17549435e-38f);
+            unit_new = reinterpret_cast<const float*>(sc)[16];
+            scales_done();
+          }
+          const float shift = is_cache ? kWeight : kWeight - unit_new;  // P = exp2(x - m + shift)
+          float lsum = 0.f;  // of P
           bool done = false;
           // ---- steady state: one pass with the running maximum; falls through, S intact, when some
           // row's maximum has grown past the threshold
@@ -928,6 +934,9 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             constexpr bool kMasked = decltype(masked_tag)::value, kCache = decltype(cache_tag)::value;
             uint32_t b0[16], b1[16], pw[64];
             float mx = -INFINITY;
+            uint64_t lp0 = 0ull, lp1 = 0ull;
+            const float off = shift - m_used;
+            const uint64_t of2 = pack2(off, off);
             tmem_ld16(tS, b0);
             tmem_wait_ld();
 #pragma unroll
@@ -935,49 +944,45 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               uint32_t* cur = (q & 1) ? b1 : b0;
               uint32_t* nxt = (q & 1) ? b0 : b1;
               if (q + 1 < BN / 16) tmem_ld16(tS + (q + 1) * 16, nxt);
-              const float c = kCache ? factor(q) : cexp, sh = kCache ? shift(q) : -unit;
-              const float off = sh - m_used;
-              const uint64_t cc2 = pack2(c, c), of2 = pack2(off, off);
-              uint64_t lp0 = 0ull, lp1 = 0ull;
-              float a0 = -INFINITY, a1 = -INFINITY;
               uint32_t vq = ~0u;
               if constexpr (kMasked) vq = vis32(q >> 1) >> ((q & 1) * 16);
+              const float c = kCache ? cf[q] : cexp;
+              const uint64_t cc2 = pack2(c, c);
+              float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float s0 = __uint_as_float(cur[2 * e]), s1 = __uint_as_float(cur[2 * e + 1]);
+              for (int v = 0; v < 8; ++v) {
+                float s0 = __uint_as_float(cur[2 * v]), s1 = __uint_as_float(cur[2 * v + 1]);
                 if constexpr (kMasked) {
-                  const uint32_t bits = vq >> (2 * e);
+                  const uint32_t bits = vq >> (2 * v);
                   s0 = (bits & 1u) ? s0 : -INFINITY;
                   s1 = (bits & 2u) ? s1 : -INFINITY;
                 }
-                if (e & 1) a1 = max3(a1, s0, s1); else a0 = max3(a0, s0, s1);
+                if (v & 1) a1 = max3(a1, s0, s1); else a0 = max3(a0, s0, s1);
                 float x0, x1;
                 unpack2(ffma2(pack2(s0, s1), cc2, of2), x0, x1);
                 const float p0 = ex2(x0), p1 = ex2(x1);
                 if constexpr (kCache) {
-                  const __half2 h = __floats2half2_rn(p0, p1);
-                  pw[q * 8 + e] = *reinterpret_cast<const uint32_t*>(&h);
+                  const __half2 w = __floats2half2_rn(p0, p1);
+                  pw[q * 8 + v] = *reinterpret_cast<const uint32_t*>(&w);
                 } else {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                  pw[q * 8 + e] = *reinterpret_cast<const uint32_t*>(&h);
+                  const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
+                  pw[q * 8 + v] = *reinterpret_cast<const uint32_t*>(&w);
                 }
-                if (e & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
+                if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
               }
               mx = fmaxf(mx, fmaxf(a0, a1) * c);
-              float y0, y1;
-              unpack2(fadd2(lp0, lp1), y0, y1);
-              lsum = fmaf(y0 + y1, ex2(-sh), lsum);
               if (q + 1 < BN / 16) tmem_wait_ld();
             }
             if (!__any_sync(0xffffffffu, mx > m_used + kLazy)) {
 #pragma unroll
               for (int q = 0; q < BN / 32; ++q) tmem_st16(tS + q * 16, pw + q * 16);
+              float y0, y1;
+              unpack2(fadd2(lp0, lp1), y0, y1);
+              lsum = y0 + y1;
               done = true;
-            } else {
-              lsum = 0.f;
             }
           };
-          if (!grow && __all_sync(0xffffffffu, m_used > -INFINITY)) {
+          if (!first && unit_new == unit && __all_sync(0xffffffffu, m_used > -INFINITY)) {
             if (is_cache) {
               if (full) one_pass(std::false_type{}, std::true_type{});
               else one_pass(std::true_type{}, std::true_type{});
@@ -989,7 +994,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           if (!done) {
             // ---- pass 1: row maximum
             float mx = -INFINITY;
-#pragma unroll 1
+#pragma unroll
             for (int q = 0; q < BN / 16; ++q) {
               uint32_t sr[16];
               tmem_ld16(tS + q * 16, sr);
@@ -997,16 +1002,12 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               const uint32_t vw = vis32(q >> 1) >> ((q & 1) * 16);
               float a = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) a = fmaxf(a, ((vw >> e) & 1u) ? __uint_as_float(sr[e]) : -INFINITY);
-              mx = fmaxf(mx, a * factor(q));
+              for (int v = 0; v < 16; ++v) a = fmaxf(a, ((vw >> v) & 1u) ? __uint_as_float(sr[v]) : -INFINITY);
+              mx = fmaxf(mx, a * cf[q]);
             }
             const bool need = mx > -INFINITY && (m_used == -INFINITY || mx > m_used + kLazy);
-            const float unit_new = !grow ? unit : (is_cache ? ceilf(top) + kUnitRoom - kUnitTop : 0.f);
-            if (jj > 0 && __any_sync(0xffffffffu, need || unit_new != unit)) {
-              // O holds PV of the earlier blocks, which must be complete: two tiles, S(j) was issued
-              // behind PV(j - 1); one tile, wait for that PV (phase ndb - 2, ndb counting this block)
-              if (db && !warp_wait(bar(B_PV_DONE), ndb & 1)) { run = false; break; }
-              tc_fence_after();
+            if (!first && __any_sync(0xffffffffu, need || unit_new != unit)) {
+              // O of this set holds its earlier PVs; they are complete, as S of this job was issued behind them
               const float fm = need ? ex2(m_used - mx) : 1.f;
               const float f = fm * ex2(unit - unit_new);
               uint32_t raw[32];
@@ -1015,62 +1016,100 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
                 tmem_ld32(tO + c * 32, raw);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * f);
+                for (int v = 0; v < 32; ++v) raw[v] = __float_as_uint(__uint_as_float(raw[v]) * f);
                 tmem_st32(tO + c * 32, raw);
               }
               tmem_wait_st();
               l_sum *= fm;
             }
-            unit = unit_new;
             if (need) m_used = mx;
-            const float mref = (m_used == -INFINITY) ? 0.f : m_used;
-            // ---- pass 2: chunk q reads S columns [16 q, 16 q + 16) and writes P columns [8 q, 8 q + 8),
+            const float off = shift - ((m_used == -INFINITY) ? 0.f : m_used);
+            // ---- pass 2: chunk q reads S columns [32 q, 32 q + 32) and writes P columns [16 q, 16 q + 16),
             // which lie in S columns already read
-#pragma unroll 1
+#pragma unroll
             for (int q = 0; q < BN / 32; ++q) {
               uint32_t sr[32], pw[16];
               tmem_ld32(tS + q * 32, sr);
               tmem_wait_ld();
               const uint32_t vw = vis32(q);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float c = factor(2 * q + h), sh = shift(2 * q + h);
-                float y = 0.f;
-#pragma unroll
-                for (int e = 8 * h; e < 8 * h + 8; ++e) {
-                  const float p0 = ((vw >> (2 * e)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * e]), c, sh - mref)) : 0.f;
-                  const float p1 =
-                      ((vw >> (2 * e + 1)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * e + 1]), c, sh - mref)) : 0.f;
-                  if (is_cache) {
-                    const __half2 hv = __floats2half2_rn(p0, p1);
-                    pw[e] = *reinterpret_cast<const uint32_t*>(&hv);
-                  } else {
-                    const __nv_bfloat162 hv = __floats2bfloat162_rn(p0, p1);
-                    pw[e] = *reinterpret_cast<const uint32_t*>(&hv);
-                  }
-                  y += p0 + p1;
+              for (int v = 0; v < 16; ++v) {
+                const float c = cf[2 * q + (v >> 3)];
+                const float p0 = ((vw >> (2 * v)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * v]), c, off)) : 0.f;
+                const float p1 = ((vw >> (2 * v + 1)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * v + 1]), c, off)) : 0.f;
+                if (is_cache) {
+                  const __half2 w = __floats2half2_rn(p0, p1);
+                  pw[v] = *reinterpret_cast<const uint32_t*>(&w);
+                } else {
+                  const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
+                  pw[v] = *reinterpret_cast<const uint32_t*>(&w);
                 }
-                lsum = fmaf(y, ex2(-sh), lsum);
+                lsum += p0 + p1;
               }
               tmem_st16(tS + q * 16, pw);
             }
           }
+          unit = unit_new;
+          if (!is_cache) lsum *= ex2(unit_new);  // the row sum counts 2^7 exp2(x - m)
           tmem_wait_st();
           l_sum += lsum;
-          if (is_cache) scales_done();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(db ? bar(B_PDB + sb) : bar(B_P_FULL + mt));
+          if (lane == 0) mbar_arrive(bar(B_P_FULL + set));
         }
+        nc += cached;
         if (!run) break;
         // ---- epilogue: every PV of the segment is complete; O stays in TMEM until O_FREE
-        if (!warp_wait(bar(B_SEG_DONE), seg & 1)) {
+        if (!warp_wait(bar(B_SEG_DONE + set), seg & 1)) {
           run = false;
           break;
         }
+        float f0 = exp2f(unit), f1 = 0.f;  // factors of this set's O and, where they are joined, the other's
+        bool join = false;
+        if (!two) {
+          float2* ml = reinterpret_cast<float2*>(smem + C_::SM_ML);
+          float* ml_unit = reinterpret_cast<float*>(smem + C_::SM_ML + 128 * 8);
+          if (set == 1) {
+            // the first set joins both; what it needs besides O:
+            ml[m] = make_float2(m_used, l_sum);
+            if (m == 0) *ml_unit = unit;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(B_ML_FULL));
+              mbar_arrive(bar(B_O_FREE));
+            }
+          } else {
+            if (!warp_wait(bar(B_ML_FULL), (uint32_t)(nml++) & 1u)) { run = false; break; }
+            join = jobs > 1;  // else the second set has had no block, and its O holds nothing
+            if (join) {
+              const float2 o = ml[m];
+              const float M = fmaxf(m_used, o.x);
+              const float g0 = M == -INFINITY ? 0.f : ex2(m_used - M), g1 = M == -INFINITY ? 0.f : ex2(o.x - M);
+              l_sum = l_sum * g0 + o.y * g1;
+              f0 *= g0;
+              f1 = exp2f(*ml_unit) * g1;
+              m_used = M;
+            }
+          }
+        }
+        if (two || set == 0) {
         if (warp_active) {
           tc_fence_after();
-          const float of = exp2f(unit);  // O in units of 2^unit
+          // 32 columns of O, joined, in true units
+          auto load_o = [&](int q, float* v, float f) {
+            uint32_t raw[32];
+            tmem_ld32(tO + q * 32, raw);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(raw[c]) * (f0 * f);
+            if (join) {
+              tmem_ld32(tO + 128 + q * 32, raw);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = fmaf(__uint_as_float(raw[c]), f1 * f, v[c]);
+            }
+          };
           __nv_bfloat16* orow = p.o + ((size_t)(x.q_off + i) * p.Hq + gh * G + hj) * D;
           auto store_chunk = [&](int q, const float* v, float inv) {
             if (!valid) return;
@@ -1089,12 +1128,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             const float inv = (l_sum > 0.f) ? 1.f / l_sum : 0.f;
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
-              uint32_t raw[32];
-              tmem_ld32(tO + q * 32, raw);
-              tmem_wait_ld();
               float v[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]) * of;
+              load_o(q, v, 1.f);
               store_chunk(q, v, inv);
             }
           } else {
@@ -1110,14 +1145,11 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               __stcg(reinterpret_cast<float2*>(work.part_ml + mine * 2), make_float2(m_used, l_sum));
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
-                uint32_t raw[32];
-                tmem_ld32(tO + q * 32, raw);
-                tmem_wait_ld();
+                float v[32];
+                load_o(q, v, 1.f);
 #pragma unroll
                 for (int c = 0; c < 32; c += 4)
-                  __stcg(part_at(work.part_o, mine, q * 8 + c / 4),
-                         make_float4(__uint_as_float(raw[c]) * of, __uint_as_float(raw[c + 1]) * of,
-                                     __uint_as_float(raw[c + 2]) * of, __uint_as_float(raw[c + 3]) * of));
+                  __stcg(part_at(work.part_o, mine, q * 8 + c / 4), make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]));
               }
               __syncwarp();
               if (lane == 0) red_release_add(counter, 1);
@@ -1132,8 +1164,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               // in CTA order, so that equal inputs give equal bits
               float M = m_used;
               for (int cc = c_a + 1; cc <= c_b; ++cc) M = fmaxf(M, __ldcg(work.part_ml + slot_of(cc) * 2));
-              const float f0 = M == -INFINITY ? 0.f : ex2(m_used - M);
-              float L = l_sum * f0;
+              const float g = M == -INFINITY ? 0.f : ex2(m_used - M);
+              float L = l_sum * g;
               for (int cc = c_a + 1; cc <= c_b; ++cc) {
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(work.part_ml + slot_of(cc) * 2));
                 if (M > -INFINITY) L += ml.y * ex2(ml.x - M);
@@ -1141,12 +1173,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               const float inv = (L > 0.f) ? 1.f / L : 0.f;
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
-                uint32_t raw[32];
-                tmem_ld32(tO + q * 32, raw);
-                tmem_wait_ld();
                 float v[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]) * (of * f0);
+                load_o(q, v, g);
                 for (int cc = c_a + 1; cc <= c_b; ++cc) {
                   const size_t sl = slot_of(cc);
                   const float f = (M == -INFINITY) ? 0.f : ex2(__ldcg(work.part_ml + sl * 2) - M);
@@ -1167,7 +1195,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_O_FREE + mt));
+        if (lane == 0) mbar_arrive(bar(B_O_FREE));
+        }
       }
       remaining -= len;
       ++seg;
@@ -1282,14 +1311,14 @@ cudaError_t launch_fp8(const AttnFp8Params& p, const Fp8Maps& maps, const Fp8Wor
     ready = cudaFuncSetAttribute(attn_fp8_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     int per_sm = 0;
     if (ready == cudaSuccess)
-      ready = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_fp8_kernel<MT>, Cfg<MT>::kThreads, kMaxSmem);
+      ready = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_fp8_kernel<MT>, kThreads, kMaxSmem);
     if (ready == cudaSuccess && per_sm < 1) ready = cudaErrorCooperativeLaunchTooLarge;
   });
   if (ready != cudaSuccess) return ready;
   const size_t tables = sizeof(int32_t) * 4 * (size_t)(p.batch + 1);
   const int in_smem = Cfg<MT>::SM_TOTAL + tables <= kMaxSmem ? 1 : 0;
   const size_t smem = Cfg<MT>::SM_TOTAL + (in_smem ? tables : 0);
-  return launch_pdl(attn_fp8_kernel<MT>, dim3(grid), dim3(Cfg<MT>::kThreads), smem, st, maps, p, w, G, in_smem);
+  return launch_pdl(attn_fp8_kernel<MT>, dim3(grid), dim3(kThreads), smem, st, maps, p, w, G, in_smem);
 }
 
 }  // namespace

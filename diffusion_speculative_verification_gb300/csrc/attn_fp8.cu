@@ -30,14 +30,18 @@
 // order by the CTA that holds its first block (bounded wait on per-row-group
 // counters).  The plan is derived on the device from seqs.
 //
-// Roles of a CTA (16 warps, 128 registers each; warp 3 idles, so that a set's
-// softmax warps meet the four TMEM lane quadrants in order):
+// Roles of a CTA (16 warps, 128 registers each; warps 2 and 3 idle, so that a
+// set's softmax warps meet the four TMEM lane quadrants in order):
 //   warp 0        page lookups (32 pages ahead, one per lane), TMA of K pages
 //                 (swizzled, the operand itself) and V pages (raw) into rings,
 //                 fresh rows into two ring stages at once; the pages' scales
-//   warps 1, 2    MMA issue, one warp per S / P / O set: PV(n), S(n + 2).  The
-//                 work between two products leaves the tensor pipe to the other
-//                 set's warp
+//   warp 1        MMA issue for two S / P / O sets in turn: PV(n), S(n + 2), so
+//                 that a set's softmax runs under the other set's products.  The
+//                 whole warp runs the loop on uniform values and one elected
+//                 lane issues: descriptors then stay in uniform registers.  A
+//                 single-lane loop moves them there for every MMA, and beside
+//                 busy softmax warps that took 1640-2400 cycles for the 1025 of
+//                 a PV and an S (1027 as it is).
 //   warps 4..11   softmax, four per set, one TMEM lane quadrant each.  A unit of
 //                 two tiles gives each its set (job n: block n / 2); a unit of
 //                 one tile gives the sets its blocks in turn (job n: block n),
@@ -96,8 +100,8 @@ enum : uint32_t {
   B_X_EMPTY = B_X_FULL + 2,
   B_S_FULL = B_X_EMPTY + 2,      // + set
   B_P_FULL = B_S_FULL + 2,       // + set
-  B_SEG_DONE = B_P_FULL + 2,     // + set: every PV of the segment complete
-  B_O_FREE = B_SEG_DONE + 2,     // both sets' O read
+  B_SEG_DONE = B_P_FULL + 2,     // every PV of the segment complete
+  B_O_FREE = B_SEG_DONE + 1,     // both sets' O read
   B_ML_FULL = B_O_FREE + 1,      // the second set's maxima and sums (one tile)
   B_FINAL = B_ML_FULL + 1,
   B_COUNT = B_FINAL + 1
@@ -211,26 +215,47 @@ __device__ __forceinline__ uint32_t window32(const uint32_t (&m)[4], int t0) {
   return sh == 0 ? pick(w) : __funnelshift_r(pick(w), pick(w + 1), sh);
 }
 
-// One 128 x 128 x 128 product of e4m3 operands, (hi + lo) K^T: hi at a_desc, lo
-// one stage behind it, both K-major SW128 like b_desc.
-__device__ __forceinline__ void gemm_q8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
-#pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    const uint64_t a = a_desc + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, b = b_desc + (s & 3) * 2;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)(s > 0))
-        : "memory");
-  }
-}
-
 // Instruction descriptors: fp32 accumulator, shape 128 x 128, B K-major or MN-major.
 constexpr uint32_t kIdShape = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdE4m3 = kIdShape;                     // kind::f8f6f4, e4m3 x e4m3
 constexpr uint32_t kIdBf16 = kIdShape | (1u << 7) | (1u << 10);
 constexpr uint32_t kIdPvF16 = kIdShape | (1u << 16);       // kind::f16, f16 x f16, B MN-major
 constexpr uint32_t kIdPvBf16 = kIdBf16 | (1u << 16);
+
+// Tensor operations issued by one elected lane of a converged warp.
+#define FP8_ELECT "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t@e tcgen05.mma.cta_group::1.kind::"
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(FP8_ELECT "f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(FP8_ELECT "f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(FP8_ELECT "f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+#undef FP8_ELECT
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// 128 x 128 x 128 products.  (hi + lo) K^T of e4m3 operands: hi at a, lo one stage behind it, both K-major
+// SW128 like b; bf16 Q K^T, two 64-column halves one stage apart; P V with P in TMEM and V MN-major.
+__device__ __forceinline__ void gemm_q8(uint32_t d, uint64_t a, uint64_t b) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    mma_f8_ss(d, a + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, b + (s & 3) * 2, kIdE4m3, s > 0);
+}
+__device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    mma_f16_ss(d, a + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, b + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, kIdBf16, s > 0);
+}
+__device__ __forceinline__ void gemm_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s) mma_f16_ts(d, a + 8 * s, b + 128 * s, idesc, s > 0 ? 1u : acc);
+}
 
 template <int MT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -363,7 +388,6 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         uint32_t n = 1;
         if ((i >= B_R_EMPTY && i < B_V_EMPTY) || i == B_Q_FULL || i == B_X_FULL || i == B_X_FULL + 1) n = kConv;
         if (i >= B_C_EMPTY && i < B_Q_FULL) n = kSoft + kConv;
-        if ((i >= B_K_EMPTY && i < B_R_FULL) || i == B_V_EMPTY || i == B_V_EMPTY + 1 || i == B_Q_EMPTY || i == B_FINAL) n = 2;
         if (i == B_X_EMPTY || i == B_X_EMPTY + 1 || i == B_O_FREE) n = kSoft;
         if (i == B_P_FULL || i == B_P_FULL + 1 || i == B_ML_FULL) n = 4;
         mbar_init(bar(i), n);
@@ -555,94 +579,89 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       drain(B_K_FULL, NK, k_end);
       drain(B_R_FULL, C_::NR, v_end);
     }
-  } else if (warp == 1 || warp == 2) {
-    // ============================================================ MMA issuers
-    const int set = warp - 1;
-    if (lane == 0 && begin < end) {
-      int u = plan->u0, k = plan->k0, remaining = end - begin, nseg = 0;
-      int n = 0, nv = 0, nq = 0;       // K ring index, V blocks, query phases
-      uint32_t pph = 0u;               // parity of the set's next P
-      bool run = true;
-      const uint32_t tS = tmem + set * 128, tO = tmem + TM_O + set * 128;
-      const uint64_t dq0 = smem_desc_sw128(sbase + C_::SM_Q, 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(sbase + C_::SM_K, 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(sbase + C_::SM_V, STAGE, 1024);
-      auto wait = [&](uint32_t b, uint32_t parity) -> bool { return mbar_wait_poll(bar(b), parity, abort, wb); };
-      while (run && remaining > 0) {
-        const Unit x = decode(u);
-        const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
-        const bool two = x.mc == 2;
-        const int step = two ? 1 : 2, first = two ? 0 : set;   // blocks of this set: first, first + step, ..
-        const uint64_t dq = dq0 + (two ? set : 0) * (2 * STAGE >> 4);
-        int is = 0;        // next block whose keys pass (the other set's included)
-        int iv = 0;        // next block whose values pass
-        bool freed = nseg == 0;
-        auto give = [&](uint32_t b) {  // this set's MMAs so far done with a buffer; in turn, the other set has none
-          mma_commit(bar(b));
-          if (!two) mma_commit(bar(b));
-        };
-        // S of block i (one of this set's), passing over the other set's blocks before it; i == len: only that
-        auto issue_s = [&](int i) -> bool {
-          for (; is < len && is <= i; ++is) {
-            const bool q8 = is < cached;
-            if ((is == 0 || is == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) return false;
-            if (!q8 && (n & 1)) {  // the stage left out
-              if (set == 0) {
-                if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
-                mbar_arrive_n(bar(B_K_EMPTY + n % NK), 2);
-              }
-              ++n;
-            }
-            if (is == i) {
-              if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
-              if (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK))) return false;
-              tc_fence_after();
-              const uint64_t dk = dk0 + (n % NK) * (STAGE >> 4);
-              if (q8) gemm_q8(tS, dq, dk, kIdE4m3);
-              else gemm_ss_k128_probe(tS, dq, dk, kIdBf16, 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
-              mma_commit(bar(B_S_FULL + set));
-              give(B_K_EMPTY + n % NK);
-              if (!q8) give(B_K_EMPTY + (n + 1) % NK);
-            }
-            n += q8 ? 1 : 2;
-            // behind the last S of either form of the queries
-            if (is == cached - 1 || is == len - 1) mma_commit(bar(B_Q_EMPTY));
-          }
-          return true;
-        };
-        run = issue_s(first);
-        for (int i = first; run && i < len; i += step) {
-          nv += i - iv;
-          iv = i;
-          if (!wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u) || !wait(B_P_FULL + set, pph) ||
-              (!freed && !wait(B_O_FREE, (nseg - 1) & 1))) {
-            run = false;
-            break;
-          }
-          freed = true;
-          pph ^= 1u;
-          tc_fence_after();
-          gemm_ts_k128_probe(tO, tS, dv0 + (nv & 1) * (2 * STAGE >> 4), i < cached ? kIdPvF16 : kIdPvBf16,
-                             i > first ? 1u : 0u, bar(B_FINAL), 0, bar(B_FINAL), 0);
-          give(B_V_EMPTY + (nv & 1));
-          if (!issue_s(i + step)) run = false;
-        }
-        if (run && !freed) run = wait(B_O_FREE, (nseg - 1) & 1);  // a segment without a block of this set
-        if (!run) break;
-        nv += len - iv;
-        mma_commit(bar(B_SEG_DONE + set));
-        ++nseg;
-        remaining -= len;
-        ++u;
-        k = 0;
-      }
-    }
-    if (lane == 0) {
-      // every MMA issued by either thread completes before TMEM is released
-      mma_commit(bar(B_FINAL));
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer (converged; see above)
+    auto uni = [](int v) -> int { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t tm = (uint32_t)uni((int)tmem);
+    int u = uni(plan->u0), k = uni(plan->k0), remaining = uni(end - begin), nseg = 0;
+    int n = 0, nv = 0, nq = 0;       // K ring index, V blocks, query phases
+    uint32_t pph0 = 0u, pph1 = 0u;   // parity of the next P of either set
+    bool run = true;
+    const uint64_t dq0 = smem_desc_sw128(sbase + C_::SM_Q, 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(sbase + C_::SM_K, 16, 1024);
+    const uint64_t dv0 = smem_desc_sw128(sbase + C_::SM_V, STAGE, 1024);
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+      if (__all_sync(0xffffffffu, mbar_test_wait(bar(b), parity))) return true;
       const long long t0 = clock64();
-      while (!mbar_try_wait(bar(B_FINAL), 0) && clock64() - t0 < wb) {
+      while (true) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, clock64() - t0 > wb)) {
+          *abort = 1;
+          return false;
+        }
       }
+    };
+    while (run && remaining > 0) {
+      const Unit x = decode(u);
+      const int len = uni(min(x.nblocks - k, remaining)), cached = uni(min(max(x.cache_blocks - k, 0), len));
+      const bool two = uni(x.mc) == 2;
+      const int jobs = two ? 2 * len : len;
+      // S of job j into its set; the first and last job of a block wait for and release its keys,
+      // the first and last of a kind its form of the queries
+      auto issue_s = [&](int j) -> bool {
+        const int t = j & 1, i = two ? j >> 1 : j;
+        const bool q8 = i < cached;
+        if (!two || t == 0) {
+          if ((i == 0 || i == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) return false;
+          if (!q8 && (n & 1)) {  // the stage left out
+            if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
+            commit_elect(bar(B_K_EMPTY + n % NK));
+            ++n;
+          }
+          if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
+          if (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK))) return false;
+        }
+        tc_fence_after();
+        const uint64_t dq = dq0 + (two ? t : 0) * (2 * STAGE >> 4), dk = dk0 + (n % NK) * (STAGE >> 4);
+        if (q8) gemm_q8(tm + t * 128, dq, dk);
+        else gemm_qk(tm + t * 128, dq, dk);
+        commit_elect(bar(B_S_FULL + t));
+        if (!two || t == 1) {
+          for (int e = q8 ? 1 : 2; e > 0; --e, ++n) commit_elect(bar(B_K_EMPTY + n % NK));
+          if (i == cached - 1 || i == len - 1) commit_elect(bar(B_Q_EMPTY));
+        }
+        return true;
+      };
+      run = issue_s(0) && (jobs == 1 || issue_s(1));
+      for (int j = 0; run && j < jobs; ++j) {
+        const int t = j & 1, i = two ? j >> 1 : j;
+        if (((!two || t == 0) && !wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u)) ||
+            (j == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1)) || !wait(B_P_FULL + t, t ? pph1 : pph0)) {
+          run = false;
+          break;
+        }
+        if (t) pph1 ^= 1u; else pph0 ^= 1u;
+        tc_fence_after();
+        gemm_pv(tm + TM_O + t * 128, tm + t * 128, dv0 + (nv & 1) * (2 * STAGE >> 4),
+                i < cached ? kIdPvF16 : kIdPvBf16, j > 1 ? 1u : 0u);
+        if (!two || t == 1) {
+          commit_elect(bar(B_V_EMPTY + (nv & 1)));
+          ++nv;
+        }
+        if (j + 2 < jobs && !issue_s(j + 2)) run = false;
+      }
+      if (!run) break;
+      commit_elect(bar(B_SEG_DONE));
+      ++nseg;
+      remaining -= len;
+      ++u;
+      k = 0;
+    }
+    // every MMA issued completes before TMEM is released
+    commit_elect(bar(B_FINAL));
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar(B_FINAL), 0) && clock64() - t0 < wb) {
     }
   } else if (warp >= 12) {
     // ============================================================ converters
@@ -1060,7 +1079,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         nc += cached;
         if (!run) break;
         // ---- epilogue: every PV of the segment is complete; O stays in TMEM until O_FREE
-        if (!warp_wait(bar(B_SEG_DONE + set), seg & 1)) {
+        if (!warp_wait(bar(B_SEG_DONE), seg & 1)) {
           run = false;
           break;
         }

@@ -222,6 +222,12 @@ constexpr uint32_t kIdBf16 = kIdShape | (1u << 7) | (1u << 10);
 constexpr uint32_t kIdPvF16 = kIdShape | (1u << 16);       // kind::f16, f16 x f16, B MN-major
 constexpr uint32_t kIdPvBf16 = kIdBf16 | (1u << 16);
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Tensor operations issued by one elected lane of a converged warp.
 #define FP8_ELECT "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t@e tcgen05.mma.cta_group::1.kind::"
 __device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -633,21 +639,23 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         }
         return true;
       };
-      run = issue_s(0) && (jobs == 1 || issue_s(1));
-      for (int j = 0; run && j < jobs; ++j) {
-        const int t = j & 1, i = two ? j >> 1 : j;
-        if (((!two || t == 0) && !wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u)) ||
-            (j == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1)) || !wait(B_P_FULL + t, t ? pph1 : pph0)) {
-          run = false;
-          break;
-        }
-        if (t) pph1 ^= 1u; else pph0 ^= 1u;
-        tc_fence_after();
-        gemm_pv(tm + TM_O + t * 128, tm + t * 128, dv0 + (nv & 1) * (2 * STAGE >> 4),
-                i < cached ? kIdPvF16 : kIdPvBf16, j > 1 ? 1u : 0u);
-        if (!two || t == 1) {
-          commit_elect(bar(B_V_EMPTY + (nv & 1)));
-          ++nv;
+#pragma unroll 1
+      for (int j = -2; run && j < jobs; ++j) {
+        if (j >= 0) {
+          const int t = j & 1, i = two ? j >> 1 : j;
+          if (((!two || t == 0) && !wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u)) ||
+              (j == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1)) || !wait(B_P_FULL + t, t ? pph1 : pph0)) {
+            run = false;
+            break;
+          }
+          if (t) pph1 ^= 1u; else pph0 ^= 1u;
+          tc_fence_after();
+          gemm_pv(tm + TM_O + t * 128, tm + t * 128, dv0 + (nv & 1) * (2 * STAGE >> 4),
+                  i < cached ? kIdPvF16 : kIdPvBf16, j > 1 ? 1u : 0u);
+          if (!two || t == 1) {
+            commit_elect(bar(B_V_EMPTY + (nv & 1)));
+            ++nv;
+          }
         }
         if (j + 2 < jobs && !issue_s(j + 2)) run = false;
       }
@@ -931,26 +939,24 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             if (lim_rows > 32 * q) v |= window32(tm, toff + 32 * q) & prefix32(lim_rows - 32 * q);
             return v;
           };
-          // ---- factors of the scores of every 16 columns; the unit of O at this block
-          float cf[8], unit_new = first ? 0.f : unit;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) cf[q] = cexp;
-          if (is_cache) {
-            const float4* sc = reinterpret_cast<const float4*>(smem + C_::SM_SC) + (e % NSC) * (SC / 4);
-            const float4 c0 = sc[0], c1 = sc[1];
-            const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-            for (int q = 0; q < 8; ++q) cf[q] = fmaxf(rowf * c[q], 1.17549435e-38f);
-            unit_new = reinterpret_cast<const float*>(sc)[16];
-            scales_done();
-          }
+          // ---- the block's scales: factors of the scores of every 16 columns, the unit of O
+          const float* sc = reinterpret_cast<const float*>(smem + C_::SM_SC) + (e % NSC) * SC;
+          auto factor = [&](int q) -> float { return is_cache ? fmaxf(rowf * sc[q], 1.17549435e-38f) : cexp; };
+          const float unit_new = is_cache ? sc[16] : (first ? 0.f : unit);
           const float shift = is_cache ? kWeight : kWeight - unit_new;  // P = exp2(x - m + shift)
           float lsum = 0.f;  // of P
           bool done = false;
-          // ---- steady state: one pass with the running maximum; falls through, S intact, when some
-          // row's maximum has grown past the threshold
-          auto one_pass = [&](auto masked_tag, auto cache_tag) {
-            constexpr bool kMasked = decltype(masked_tag)::value, kCache = decltype(cache_tag)::value;
+          // ---- steady state, all keys visible: one pass with the running maximum; falls through, S
+          // intact, when some row's maximum has grown past the threshold
+          auto one_pass = [&](auto cache_tag) {
+            constexpr bool kCache = decltype(cache_tag)::value;
+            float cf[8];
+            if constexpr (kCache) {
+              const float4 c0 = reinterpret_cast<const float4*>(sc)[0], c1 = reinterpret_cast<const float4*>(sc)[1];
+              const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+              for (int q = 0; q < 8; ++q) cf[q] = fmaxf(rowf * c[q], 1.17549435e-38f);
+            }
             uint32_t b0[16], b1[16], pw[64];
             float mx = -INFINITY;
             uint64_t lp0 = 0ull, lp1 = 0ull;
@@ -963,19 +969,12 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               uint32_t* cur = (q & 1) ? b1 : b0;
               uint32_t* nxt = (q & 1) ? b0 : b1;
               if (q + 1 < BN / 16) tmem_ld16(tS + (q + 1) * 16, nxt);
-              uint32_t vq = ~0u;
-              if constexpr (kMasked) vq = vis32(q >> 1) >> ((q & 1) * 16);
               const float c = kCache ? cf[q] : cexp;
               const uint64_t cc2 = pack2(c, c);
               float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
               for (int v = 0; v < 8; ++v) {
-                float s0 = __uint_as_float(cur[2 * v]), s1 = __uint_as_float(cur[2 * v + 1]);
-                if constexpr (kMasked) {
-                  const uint32_t bits = vq >> (2 * v);
-                  s0 = (bits & 1u) ? s0 : -INFINITY;
-                  s1 = (bits & 2u) ? s1 : -INFINITY;
-                }
+                const float s0 = __uint_as_float(cur[2 * v]), s1 = __uint_as_float(cur[2 * v + 1]);
                 if (v & 1) a1 = max3(a1, s0, s1); else a0 = max3(a0, s0, s1);
                 float x0, x1;
                 unpack2(ffma2(pack2(s0, s1), cc2, of2), x0, x1);
@@ -1001,19 +1000,14 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               done = true;
             }
           };
-          if (!first && unit_new == unit && __all_sync(0xffffffffu, m_used > -INFINITY)) {
-            if (is_cache) {
-              if (full) one_pass(std::false_type{}, std::true_type{});
-              else one_pass(std::true_type{}, std::true_type{});
-            } else {
-              if (full) one_pass(std::false_type{}, std::false_type{});
-              else one_pass(std::true_type{}, std::false_type{});
-            }
+          if (!first && full && unit_new == unit && __all_sync(0xffffffffu, m_used > -INFINITY)) {
+            if (is_cache) one_pass(std::true_type{});
+            else one_pass(std::false_type{});
           }
           if (!done) {
             // ---- pass 1: row maximum
             float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < BN / 16; ++q) {
               uint32_t sr[16];
               tmem_ld16(tS + q * 16, sr);
@@ -1022,7 +1016,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               float a = -INFINITY;
 #pragma unroll
               for (int v = 0; v < 16; ++v) a = fmaxf(a, ((vw >> v) & 1u) ? __uint_as_float(sr[v]) : -INFINITY);
-              mx = fmaxf(mx, a * cf[q]);
+              mx = fmaxf(mx, a * factor(q));
             }
             const bool need = mx > -INFINITY && (m_used == -INFINITY || mx > m_used + kLazy);
             if (!first && __any_sync(0xffffffffu, need || unit_new != unit)) {
@@ -1043,17 +1037,17 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             }
             if (need) m_used = mx;
             const float off = shift - ((m_used == -INFINITY) ? 0.f : m_used);
-            // ---- pass 2: chunk q reads S columns [32 q, 32 q + 32) and writes P columns [16 q, 16 q + 16),
+            // ---- pass 2: chunk q reads S columns [16 q, 16 q + 16) and writes P columns [8 q, 8 q + 8),
             // which lie in S columns already read
-#pragma unroll
-            for (int q = 0; q < BN / 32; ++q) {
-              uint32_t sr[32], pw[16];
-              tmem_ld32(tS + q * 32, sr);
+#pragma unroll 1
+            for (int q = 0; q < BN / 16; ++q) {
+              uint32_t sr[16], pw[8];
+              tmem_ld16(tS + q * 16, sr);
               tmem_wait_ld();
-              const uint32_t vw = vis32(q);
+              const uint32_t vw = vis32(q >> 1) >> ((q & 1) * 16);
+              const float c = factor(q);
 #pragma unroll
-              for (int v = 0; v < 16; ++v) {
-                const float c = cf[2 * q + (v >> 3)];
+              for (int v = 0; v < 8; ++v) {
                 const float p0 = ((vw >> (2 * v)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * v]), c, off)) : 0.f;
                 const float p1 = ((vw >> (2 * v + 1)) & 1u) ? ex2(fmaf(__uint_as_float(sr[2 * v + 1]), c, off)) : 0.f;
                 if (is_cache) {
@@ -1065,9 +1059,10 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
                 }
                 lsum += p0 + p1;
               }
-              tmem_st16(tS + q * 16, pw);
+              tmem_st8(tS + q * 8, pw);
             }
           }
+          if (is_cache) scales_done();
           unit = unit_new;
           if (!is_cache) lsum *= ex2(unit_new);  // the row sum counts 2^7 exp2(x - m)
           tmem_wait_st();

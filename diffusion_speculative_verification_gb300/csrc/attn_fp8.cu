@@ -228,39 +228,57 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
-// Tensor operations issued by one elected lane of a converged warp.
-#define FP8_ELECT "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t@e tcgen05.mma.cta_group::1.kind::"
-__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(FP8_ELECT "f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// Tensor operations issued by one elected lane of a converged warp: 128 x 128 x 128 products as eight MMAs,
+// the first of which accumulates iff acc.
+//   gemm_q8: (hi + lo) K^T of e4m3 operands, hi at a, lo 1024 descriptor units behind it, both K-major SW128 like b
+//   gemm_qk: bf16 Q K^T, two 64-column halves of either operand 1024 units apart
+//   gemm_pv: P V, P in TMEM (two elements per column), V MN-major
+#define FP8_MMA8(FIRST, STEP)                                                                                    \
+  "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a, b;\n\t.reg .b32 ta;\n\telect.sync _|e, 0xffffffff;\n\t"                \
+  "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t" FIRST STEP "}"
+#define FP8_SS(KIND, OA, OB) \
+  "add.s64 a, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\t@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, q;\n\t"
+#define FP8_TS(OA, OB) \
+  "add.u32 ta, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %3, q;\n\t"
+__device__ __forceinline__ void gemm_q8(uint32_t d, uint64_t a, uint64_t b) {
+  asm volatile(FP8_MMA8("@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t",
+                        FP8_SS("f8f6f4", 2, 2) FP8_SS("f8f6f4", 4, 4) FP8_SS("f8f6f4", 6, 6) FP8_SS("f8f6f4", 1024, 0)
+                        FP8_SS("f8f6f4", 1026, 2) FP8_SS("f8f6f4", 1028, 4) FP8_SS("f8f6f4", 1030, 6))
+               ::"r"(d), "l"(a), "l"(b), "r"(kIdE4m3), "r"(0) : "memory");
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(FP8_ELECT "f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+__device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
+  asm volatile(FP8_MMA8("@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t",
+                        FP8_SS("f16", 2, 2) FP8_SS("f16", 4, 4) FP8_SS("f16", 6, 6) FP8_SS("f16", 1024, 1024)
+                        FP8_SS("f16", 1026, 1026) FP8_SS("f16", 1028, 1028) FP8_SS("f16", 1030, 1030))
+               ::"r"(d), "l"(a), "l"(b), "r"(kIdBf16), "r"(0) : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(FP8_ELECT "f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+__device__ __forceinline__ void gemm_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(FP8_MMA8("@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t",
+                        FP8_TS(8, 128) FP8_TS(16, 256) FP8_TS(24, 384) FP8_TS(32, 512) FP8_TS(40, 640) FP8_TS(48, 768)
+                        FP8_TS(56, 896))
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
-#undef FP8_ELECT
+#undef FP8_MMA8
+#undef FP8_SS
+#undef FP8_TS
 __device__ __forceinline__ void commit_elect(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-// 128 x 128 x 128 products.  (hi + lo) K^T of e4m3 operands: hi at a, lo one stage behind it, both K-major
-// SW128 like b; bf16 Q K^T, two 64-column halves one stage apart; P V with P in TMEM and V MN-major.
-__device__ __forceinline__ void gemm_q8(uint32_t d, uint64_t a, uint64_t b) {
-#pragma unroll
-  for (int s = 0; s < 8; ++s)
-    mma_f8_ss(d, a + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, b + (s & 3) * 2, kIdE4m3, s > 0);
-}
-__device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
-#pragma unroll
-  for (int s = 0; s < 8; ++s)
-    mma_f16_ss(d, a + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, b + (s >> 2) * (STAGE >> 4) + (s & 3) * 2, kIdBf16, s > 0);
-}
-__device__ __forceinline__ void gemm_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-#pragma unroll
-  for (int s = 0; s < 8; ++s) mma_f16_ts(d, a + 8 * s, b + 128 * s, idesc, s > 0 ? 1u : acc);
+// 32 lanes x 16 columns and the largest of each lane's 16 values
+__device__ __forceinline__ float tmem_max16(uint32_t taddr) {
+  uint32_t r[16];
+  float mx;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, %16, [%17];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=f"(mx)
+      : "r"(taddr)
+      : "memory");
+  return mx;
 }
 
 template <int MT>
@@ -786,24 +804,27 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           uint8_t* dst = smem + C_::SM_V + (nv & 1) * 2 * STAGE + first * STAGE + key0 * 128;
           uint8_t* dst0 = dst + (((c0 + first) ^ sw) << 4);
           uint8_t* dst1 = dst + (((c0 + 1 - first) ^ sw) << 4);
-          uint4 s[8];
+#pragma unroll 1
+          for (int g = 0; g < 8; g += 4) {
+            uint4 s[4];
 #pragma unroll
-          for (int it = 0; it < 8; ++it) s[it] = *reinterpret_cast<const uint4*>(raw + it * NT * 16);
+            for (int it = 0; it < 4; ++it) s[it] = *reinterpret_cast<const uint4*>(raw + (g + it) * NT * 16);
 #pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            if (it * 16 + key0 >= keys) s[it] = make_uint4(0, 0, 0, 0);
-            const __half2 f = __float2half2_rn(ex2(sc[8 + it] - unit));
-            const uint32_t w[4] = {s[it].x, s[it].y, s[it].z, s[it].w};
-            uint32_t h[8];
+            for (int it = 0; it < 4; ++it) {
+              if ((g + it) * 16 + key0 >= keys) s[it] = make_uint4(0, 0, 0, 0);
+              const __half2 f = __float2half2_rn(ex2(sc[8 + g + it] - unit));
+              const uint32_t w[4] = {s[it].x, s[it].y, s[it].z, s[it].w};
+              uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t v = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), f);
-              h[e] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t v = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), f);
+                h[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+              *reinterpret_cast<uint4*>(dst0 + (g + it) * 16 * 128) = first ? hi : lo;
+              *reinterpret_cast<uint4*>(dst1 + (g + it) * 16 * 128) = first ? lo : hi;
             }
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4*>(dst0 + it * 16 * 128) = first ? hi : lo;
-            *reinterpret_cast<uint4*>(dst1 + it * 16 * 128) = first ? lo : hi;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_C_EMPTY + nc % NSC));
@@ -945,68 +966,19 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           const float unit_new = is_cache ? sc[16] : (first ? 0.f : unit);
           const float shift = is_cache ? kWeight : kWeight - unit_new;  // P = exp2(x - m + shift)
           float lsum = 0.f;  // of P
-          bool done = false;
-          // ---- steady state, all keys visible: one pass with the running maximum; falls through, S
-          // intact, when some row's maximum has grown past the threshold
-          auto one_pass = [&](auto cache_tag) {
-            constexpr bool kCache = decltype(cache_tag)::value;
-            float cf[8];
-            if constexpr (kCache) {
-              const float4 c0 = reinterpret_cast<const float4*>(sc)[0], c1 = reinterpret_cast<const float4*>(sc)[1];
-              const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          // ---- the row's maximum over the block
+          float mx = -INFINITY;
+          if (full) {
+#pragma unroll 1
+            for (int q = 0; q < BN / 16; q += 4) {
+              float a[4];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) cf[q] = fmaxf(rowf * c[q], 1.17549435e-38f);
+              for (int h = 0; h < 4; ++h) a[h] = tmem_max16(tS + (q + h) * 16);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < 4; ++h) mx = fmaxf(mx, a[h] * factor(q + h));
             }
-            uint32_t b0[16], b1[16], pw[64];
-            float mx = -INFINITY;
-            uint64_t lp0 = 0ull, lp1 = 0ull;
-            const float off = shift - m_used;
-            const uint64_t of2 = pack2(off, off);
-            tmem_ld16(tS, b0);
-            tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < BN / 16; ++q) {
-              uint32_t* cur = (q & 1) ? b1 : b0;
-              uint32_t* nxt = (q & 1) ? b0 : b1;
-              if (q + 1 < BN / 16) tmem_ld16(tS + (q + 1) * 16, nxt);
-              const float c = kCache ? cf[q] : cexp;
-              const uint64_t cc2 = pack2(c, c);
-              float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                const float s0 = __uint_as_float(cur[2 * v]), s1 = __uint_as_float(cur[2 * v + 1]);
-                if (v & 1) a1 = max3(a1, s0, s1); else a0 = max3(a0, s0, s1);
-                float x0, x1;
-                unpack2(ffma2(pack2(s0, s1), cc2, of2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                if constexpr (kCache) {
-                  const __half2 w = __floats2half2_rn(p0, p1);
-                  pw[q * 8 + v] = *reinterpret_cast<const uint32_t*>(&w);
-                } else {
-                  const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
-                  pw[q * 8 + v] = *reinterpret_cast<const uint32_t*>(&w);
-                }
-                if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
-              }
-              mx = fmaxf(mx, fmaxf(a0, a1) * c);
-              if (q + 1 < BN / 16) tmem_wait_ld();
-            }
-            if (!__any_sync(0xffffffffu, mx > m_used + kLazy)) {
-#pragma unroll
-              for (int q = 0; q < BN / 32; ++q) tmem_st16(tS + q * 16, pw + q * 16);
-              float y0, y1;
-              unpack2(fadd2(lp0, lp1), y0, y1);
-              lsum = y0 + y1;
-              done = true;
-            }
-          };
-          if (!first && full && unit_new == unit && __all_sync(0xffffffffu, m_used > -INFINITY)) {
-            if (is_cache) one_pass(std::true_type{});
-            else one_pass(std::false_type{});
-          }
-          if (!done) {
-            // ---- pass 1: row maximum
-            float mx = -INFINITY;
+          } else {
 #pragma unroll 1
             for (int q = 0; q < BN / 16; ++q) {
               uint32_t sr[16];
@@ -1018,27 +990,75 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               for (int v = 0; v < 16; ++v) a = fmaxf(a, ((vw >> v) & 1u) ? __uint_as_float(sr[v]) : -INFINITY);
               mx = fmaxf(mx, a * factor(q));
             }
-            const bool need = mx > -INFINITY && (m_used == -INFINITY || mx > m_used + kLazy);
-            if (!first && __any_sync(0xffffffffu, need || unit_new != unit)) {
-              // O of this set holds its earlier PVs; they are complete, as S of this job was issued behind them
-              const float fm = need ? ex2(m_used - mx) : 1.f;
-              const float f = fm * ex2(unit - unit_new);
-              uint32_t raw[32];
+          }
+          // ---- the reference may lag behind it; O is brought to a new one, or to a new unit
+          const bool need = mx > -INFINITY && (m_used == -INFINITY || mx > m_used + kLazy);
+          if (!first && __any_sync(0xffffffffu, need || unit_new != unit)) {
+            // O of this set holds its earlier PVs; they are complete, as S of this job was issued behind them
+            const float fm = need ? ex2(m_used - mx) : 1.f;
+            const float f = fm * ex2(unit - unit_new);
+            uint32_t raw[32];
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                tmem_ld32(tO + c * 32, raw);
-                tmem_wait_ld();
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_ld32(tO + c * 32, raw);
+              tmem_wait_ld();
 #pragma unroll
-                for (int v = 0; v < 32; ++v) raw[v] = __float_as_uint(__uint_as_float(raw[v]) * f);
-                tmem_st32(tO + c * 32, raw);
-              }
-              tmem_wait_st();
-              l_sum *= fm;
+              for (int v = 0; v < 32; ++v) raw[v] = __float_as_uint(__uint_as_float(raw[v]) * f);
+              tmem_st32(tO + c * 32, raw);
             }
-            if (need) m_used = mx;
-            const float off = shift - ((m_used == -INFINITY) ? 0.f : m_used);
-            // ---- pass 2: chunk q reads S columns [16 q, 16 q + 16) and writes P columns [8 q, 8 q + 8),
-            // which lie in S columns already read
+            tmem_wait_st();
+            l_sum *= fm;
+          }
+          if (need) m_used = mx;
+          const float off = shift - ((m_used == -INFINITY) ? 0.f : m_used);
+          // ---- P = exp2(x - m + shift) over S: chunk q reads S columns [32 q, 32 q + 32) and writes P columns
+          // [16 q, 16 q + 16), which lie in S columns already read
+          auto exps = [&](auto cache_tag) {
+            constexpr bool kCache = decltype(cache_tag)::value;
+            const uint64_t of2 = pack2(off, off);
+            uint64_t lp0 = 0ull, lp1 = 0ull;
+            uint32_t b0[32], b1[32];
+            tmem_ld32(tS, b0);
+            tmem_wait_ld();
+            auto chunk = [&](int q, uint32_t* cur) {
+              uint32_t pw[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float c = kCache ? factor(2 * q + h) : cexp;
+                const uint64_t cc2 = pack2(c, c);
+#pragma unroll
+                for (int v = 8 * h; v < 8 * h + 8; ++v) {
+                  float x0, x1;
+                  unpack2(ffma2(pack2(__uint_as_float(cur[2 * v]), __uint_as_float(cur[2 * v + 1])), cc2, of2), x0, x1);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  if constexpr (kCache) {
+                    const __half2 w = __floats2half2_rn(p0, p1);
+                    pw[v] = *reinterpret_cast<const uint32_t*>(&w);
+                  } else {
+                    const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
+                    pw[v] = *reinterpret_cast<const uint32_t*>(&w);
+                  }
+                  if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
+                }
+              }
+              tmem_wait_ld();  // the next chunk is here, so this one's P may go over it
+              tmem_st16(tS + q * 16, pw);
+            };
+#pragma unroll 1
+            for (int q = 0; q < BN / 32; q += 2) {
+              tmem_ld32(tS + (q + 1) * 32, b1);
+              chunk(q, b0);
+              if (q + 2 < BN / 32) tmem_ld32(tS + (q + 2) * 32, b0);
+              chunk(q + 1, b1);
+            }
+            float y0, y1;
+            unpack2(fadd2(lp0, lp1), y0, y1);
+            lsum = y0 + y1;
+          };
+          if (full) {
+            if (is_cache) exps(std::true_type{});
+            else exps(std::false_type{});
+          } else {
 #pragma unroll 1
             for (int q = 0; q < BN / 16; ++q) {
               uint32_t sr[16], pw[8];

@@ -16,7 +16,8 @@
 //           2^-10 of the row's largest is exact, the rest off by 2^-18 of it).
 //           S = hi K^T + lo K^T on the fp8 tensor path, at the cost of one bf16
 //           product and without converting K; the scale of a page enters with
-//           2^e as a factor of the column group.
+//           2^e as a factor of the column group.  A small kernel before this one
+//           writes hi, lo and 2^e of every query row to the workspace.
 //   values  converted to fp16, with the page's scale: code * vs / 2^u, u one
 //           exponent per unit that follows the largest scale met (exact for a
 //           power of two within 2^22 of the largest).  P = 2^7 exp2(x - m) in
@@ -30,8 +31,8 @@
 // order by the CTA that holds its first block (bounded wait on per-row-group
 // counters).  The plan is derived on the device from seqs.
 //
-// Roles of a CTA (16 warps, 128 registers each; warps 2 and 3 idle, so that a
-// set's softmax warps meet the four TMEM lane quadrants in order):
+// Roles of a CTA (16 warps, 128 registers each; warp 3 idles, so that a set's
+// softmax warps meet the four TMEM lane quadrants in order):
 //   warp 0        page lookups (32 pages ahead, one per lane), TMA of K pages
 //                 (swizzled, the operand itself) and V pages (raw) into rings,
 //                 fresh rows into two ring stages at once; the pages' scales
@@ -42,12 +43,15 @@
 //                 single-lane loop moves them there for every MMA, and beside
 //                 busy softmax warps that took 1640-2400 cycles for the 1025 of
 //                 a PV and an S (1027 as it is).
+//   warp 2        query tiles, in the form of the cached and of the fresh blocks
 //   warps 4..11   softmax, four per set, one TMEM lane quadrant each.  A unit of
 //                 two tiles gives each its set (job n: block n / 2); a unit of
 //                 one tile gives the sets its blocks in turn (job n: block n),
 //                 and the first set joins both at the end
-//   warps 12..15  queries into the operand's form; V codes to fp16 (rows behind
-//                 the last token become 0, so nothing there is ever multiplied)
+//   warps 12..15  V codes to fp16, fresh V copied (rows behind the last token
+//                 become 0, so nothing there is ever multiplied)
+// The instruction cache bounds how much code a block may pass through: unrolled
+// variants of these loops (250 KB of code) ran the mixed batch at half this speed.
 // Every wait is bounded; an expired one raises the CTA's abort flag, copies and
 // MMAs in flight are drained, TMEM is freed and SSV_ERR_TIMEOUT reported.
 #include "ssv_internal.cuh"
@@ -94,11 +98,9 @@ enum : uint32_t {
   B_V_EMPTY = B_V_FULL + 2,
   B_C_FULL = B_V_EMPTY + 2,      // scales
   B_C_EMPTY = B_C_FULL + NSC,
-  B_Q_FULL = B_C_EMPTY + NSC,    // query operand written / its last S complete
+  B_Q_FULL = B_C_EMPTY + NSC,    // query operand here / its last S complete
   B_Q_EMPTY = B_Q_FULL + 1,
-  B_X_FULL = B_Q_EMPTY + 1,      // row exponents, two buffers
-  B_X_EMPTY = B_X_FULL + 2,
-  B_S_FULL = B_X_EMPTY + 2,      // + set
+  B_S_FULL = B_Q_EMPTY + 1,      // + set
   B_P_FULL = B_S_FULL + 2,       // + set
   B_SEG_DONE = B_P_FULL + 2,     // every PV of the segment complete
   B_O_FREE = B_SEG_DONE + 1,     // both sets' O read
@@ -108,7 +110,7 @@ enum : uint32_t {
 };
 
 struct AttnFp8Params {
-  const __nv_bfloat16* q;
+  const float* q_scale;  // [total_rows][Hq]: 2^e of the split queries
   const float *k_scale, *v_scale;
   const int32_t* pages;
   __nv_bfloat16* o;
@@ -121,10 +123,11 @@ struct AttnFp8Params {
   int32_t* dev_status;
   long long wait_budget;
   int fault_skip;
+  int early;  // the kernel before this one is the query split, which writes nothing but what warps 2 and 4..11 wait for
 };
 
 struct Fp8Maps {
-  CUtensorMap kc, vc, kn, vn;
+  CUtensorMap kc, vc, kn, vn, q, qhi, qlo;
 };
 
 struct Fp8Work {
@@ -149,8 +152,7 @@ struct Cfg {
   static constexpr uint32_t SM_R = SM_K + NK * STAGE;
   static constexpr uint32_t SM_V = SM_R + NR * STAGE;       // 2 x 32 KB
   static constexpr uint32_t SM_SC = SM_V + 4 * STAGE;       // [NSC][SC]
-  static constexpr uint32_t SM_X = SM_SC + NSC * SC * 4;    // [2][MT][128] int8 row exponents
-  static constexpr uint32_t SM_ML = SM_X + 2 * MT * 128;    // [128] (m, l) of the second set; then its u
+  static constexpr uint32_t SM_ML = SM_SC + NSC * SC * 4;   // [128] (m, l) of the second set; then its u
   static constexpr uint32_t SM_BAR = SM_ML + 128 * 8 + 8;
   static constexpr uint32_t SM_PLAN = SM_BAR + 8 * B_COUNT + 16;
   static constexpr uint32_t SM_TOTAL = (SM_PLAN + sizeof(PlanHdr) + 15) / 16 * 16;  // planning tables follow
@@ -317,7 +319,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
 
   // ------------------------------------------------------------------ plan
   if (warp == 0) {
-    pdl_wait();
+    if (!p.early) pdl_wait();
     int carryU = 0, carryB = 0, carryC = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
@@ -410,9 +412,9 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       *abort = 0;
       for (uint32_t i = 0; i < B_COUNT; ++i) {
         uint32_t n = 1;
-        if ((i >= B_R_EMPTY && i < B_V_EMPTY) || i == B_Q_FULL || i == B_X_FULL || i == B_X_FULL + 1) n = kConv;
+        if (i >= B_R_EMPTY && i < B_V_EMPTY) n = kConv;
         if (i >= B_C_EMPTY && i < B_Q_FULL) n = kSoft + kConv;
-        if (i == B_X_EMPTY || i == B_X_EMPTY + 1 || i == B_O_FREE) n = kSoft;
+        if (i == B_O_FREE) n = kSoft;
         if (i == B_P_FULL || i == B_P_FULL + 1 || i == B_ML_FULL) n = 4;
         mbar_init(bar(i), n);
       }
@@ -689,88 +691,48 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     const long long t0 = clock64();
     while (!mbar_try_wait(bar(B_FINAL), 0) && clock64() - t0 < wb) {
     }
+  } else if (warp == 2) {
+    // ============================================================ query tiles
+    if (lane == 0 && begin < end) {
+      tma_prefetch(&maps.q); tma_prefetch(&maps.qhi); tma_prefetch(&maps.qlo);
+      int u = plan->u0, k = plan->k0, remaining = end - begin, nq = 0;
+      bool run = true;
+      pdl_wait();  // the split queries come from the kernel before this one
+      const uint32_t tile_bytes = R * G * 256;
+      while (run && remaining > 0) {
+        const Unit x = decode(u);
+        const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
+        for (int form = cached > 0 ? 0 : 1; form < (len > cached ? 2 : 1); ++form, ++nq) {
+          // the tile is free once the last S of the form before is complete
+          if (nq > 0 && !mbar_wait(bar(B_Q_EMPTY), (uint32_t)(nq - 1) & 1u, abort, wb)) { run = false; break; }
+          mbar_expect_tx(bar(B_Q_FULL), x.mc * tile_bytes);
+          for (int t = 0; t < x.mc; ++t) {
+            const uint32_t dst = sbase + C_::SM_Q + t * 2 * STAGE;
+            const int z = x.q_off + x.row0 + t * R;
+            tma_load_3d(dst, form ? &maps.q : &maps.qhi, 0, gh * G, z, bar(B_Q_FULL));
+            tma_load_3d(dst + STAGE, form ? &maps.q : &maps.qlo, form ? 64 : 0, gh * G, z, bar(B_Q_FULL));
+          }
+        }
+        remaining -= len;
+        ++u;
+        k = 0;
+      }
+      if (nq > 0) {  // drain (bounded): the last tiles may still be in flight
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar(B_Q_FULL), (uint32_t)(nq - 1) & 1u) && clock64() - t0 < wb) {
+        }
+      }
+    }
   } else if (warp >= 12) {
     // ============================================================ converters
     const int ct = threadIdx.x - 32 * 12;
     constexpr int NT = 32 * kConv;
     int u = plan->u0, k = plan->k0, remaining = end - begin;
-    int n = 0, nv = 0, nq = 0, nx = 0, nc = 0;
+    int n = 0, nv = 0, nc = 0;
     bool run = true;
     while (run && remaining > 0) {
       const Unit x = decode(u);
       const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
-      // the unit's queries as the operand of the cached (hi, lo) or the fresh blocks (bf16)
-      auto write_q = [&](bool q8) -> bool {
-        for (int m = ct; m < x.mc * 128; m += NT) {
-          const int tile = m >> 7, ml = m & 127, r_local = tile * R + ml / G;
-          const uint4* src = nullptr;  // the row's 256 bytes; an empty row is zeros
-          if (ml < R * G && r_local < x.nvalid)
-            src = reinterpret_cast<const uint4*>(
-                p.q + ((size_t)(x.q_off + x.row0 + r_local) * p.Hq + gh * G + ml % G) * D);
-          auto chunk = [&](int c) { return src ? __ldg(src + c) : make_uint4(0, 0, 0, 0); };
-          float amax = 0.f;
-          if (q8) {
-#pragma unroll 8
-            for (int c = 0; c < 16; ++c) {
-              const uint4 v = chunk(c);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-                amax = fmaxf(amax, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
-              }
-            }
-          }
-          if (m == ct) {  // the operand is free once the last S that reads it is complete
-            if (nq > 0 && !warp_wait(bar(B_Q_EMPTY), (uint32_t)(nq - 1) & 1u)) return false;
-            if (q8 && nx > 1 && !warp_wait(bar(B_X_EMPTY + (nx & 1)), (uint32_t)(nx / 2 - 1) & 1u)) return false;
-          }
-          uint8_t* row = smem + C_::SM_Q + tile * 2 * STAGE + ml * 128;
-          const int sw = ml & 7;
-          if (!q8) {
-#pragma unroll 8
-            for (int c = 0; c < 16; ++c)
-              *reinterpret_cast<uint4*>(row + (c >> 3) * STAGE + (((c & 7) ^ sw) << 4)) = chunk(c);
-            continue;
-          }
-          // smallest e >= -100 with amax <= 448 2^e = 1.75 2^(e + 8); amax holds a bf16 value
-          const uint32_t bits = __float_as_uint(amax);
-          const int ex = max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-          const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
-          (smem + C_::SM_X)[((nx & 1) * MT + tile) * 128 + ml] = (uint8_t)(int8_t)ex;
-#pragma unroll 2
-          for (int c = 0; c < 8; ++c) {
-            const uint4 v0 = chunk(2 * c), v1 = chunk(2 * c + 1);
-            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-            uint32_t h4[4], l4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint16_t hh[2], ll[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float a = __uint_as_float(w[2 * e + i] << 16) * f, b = __uint_as_float(w[2 * e + i] & 0xffff0000u) * f;
-                hh[i] = f32_to_e4m3x2(a, b);
-                const uint32_t back = e4m3x2_to_f16x2(hh[i]);
-                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                ll[i] = f32_to_e4m3x2(a - r.x, b - r.y);
-              }
-              h4[e] = hh[0] | (uint32_t)hh[1] << 16;
-              l4[e] = ll[0] | (uint32_t)ll[1] << 16;
-            }
-            *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-            *reinterpret_cast<uint4*>(row + STAGE + ((c ^ sw) << 4)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(B_Q_FULL));
-          if (q8) mbar_arrive(bar(B_X_FULL + (nx & 1)));
-        }
-        ++nq;
-        if (q8) ++nx;
-        return true;
-      };
       auto v_ready = [&]() -> bool {  // the 16-bit stage of V block nv is free
         return nv < 2 || warp_wait(bar(B_V_EMPTY + (nv & 1)), (uint32_t)((nv >> 1) - 1) & 1u);
       };
@@ -785,7 +747,6 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         ++nv;
       };
       if (cached > 0) {
-        if (!write_q(true)) { run = false; break; }
         for (int i = 0; i < cached; ++i) {
           if (!warp_wait(bar(B_C_FULL + nc % NSC), full_par(nc, NSC)) ||
               !warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) || !v_ready()) {
@@ -833,7 +794,6 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         }
       }
       if (run && len > cached) {
-        if (!write_q(false)) { run = false; break; }
         for (int i = cached; i < len; ++i) {
           if (n & 1) {  // the stage left out
             if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR))) { run = false; break; }
@@ -865,29 +825,22 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     const uint32_t tS = tmem + lane_base + set * 128, tO = tmem + lane_base + TM_O + set * 128;
     const float cexp = p.scale * 1.4426950408889634f;
     int u = plan->u0, k = plan->k0, remaining = end - begin, seg = 0;
-    int nc = 0, nx = 0, nml = 0;  // cached blocks, row exponents, joins so far
+    int nc = 0, nml = 0;  // cached blocks, joins so far
     uint32_t sph = 0u;            // parity of this set's next S
     bool run = true;
+    pdl_wait();  // the row factors come from the kernel before this one
     while (run && remaining > 0) {
       const Unit x = decode(u);
       const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
       const bool complete = (k == 0 && len == x.nblocks);
       const bool two = x.mc == 2;
       const int mt = two ? set : 0, jobs = two ? 2 * len : len;
-      float rowf = 1.f;
-      if (cached > 0) {
-        if (!warp_wait(bar(B_X_FULL + (nx & 1)), (uint32_t)(nx >> 1) & 1u)) { run = false; break; }
-        const int ex = reinterpret_cast<const int8_t*>(smem + C_::SM_X)[((nx & 1) * MT + mt) * 128 + m];
-        rowf = exp2f((float)ex);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_X_EMPTY + (nx & 1)));
-        ++nx;
-      }
       {
         const int r_local = mt * R + m / G, hj = m % G;
         const int i = x.row0 + r_local;  // local query row
         const bool valid = m < R * G && r_local < x.nvalid;
         const bool warp_active = q4 * 32 < R * G && (mt * R + (q4 * 32) / G) < x.nvalid;
+        const float rowf = cached > 0 && valid ? __ldg(p.q_scale + (size_t)(x.q_off + i) * p.Hq + gh * G + hj) : 1.f;
         const bool prompt = i < x.N;
         const int r = i - x.N;
         uint32_t tm[4] = {0u, 0u, 0u, 0u};  // allowed tail keys of this row
@@ -919,7 +872,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           tm[0] = (uint32_t)w01; tm[1] = (uint32_t)(w01 >> 32);
           tm[2] = (uint32_t)w23; tm[3] = (uint32_t)(w23 >> 32);
         }
-        // rows without a query follow along unmasked (their queries are zero) and are dropped at the end
+        // rows without a query follow along unmasked, whatever their tile rows hold, and are dropped at the end
         float m_used = valid ? -INFINITY : 0.f, l_sum = 0.f, unit = 0.f;
         for (int job = set; job < jobs; job += 2) {
           const int jj = two ? job >> 1 : job, j = k + jj;
@@ -1240,6 +1193,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
   }
   // ------------------------------------------------------------------ teardown
   __syncwarp();
+  pdl_wait();  // this grid never completes before the one it follows
   tc_fence_before();
   __syncthreads();
   if (*abort && threadIdx.x == 0) report(p.dev_status, SSV_ERR_TIMEOUT);
@@ -1247,6 +1201,50 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
+}
+
+// ---------------------------------------------------------------------------
+// The queries of a pass as 2^e (hi + lo): sixteen lanes per (row, head), eight elements each; one read of Q
+// and one write of the same bytes.
+// ---------------------------------------------------------------------------
+constexpr int kSplitThreads = 256;
+
+__global__ void __launch_bounds__(kSplitThreads) query_split_kernel(const uint4* q, uint2* hi, uint2* lo, float* scale,
+                                                                    long long heads) {
+  pdl_wait();
+  pdl_trigger();  // every kernel before this one is complete: the next may read what they wrote
+  const long long h = ((long long)blockIdx.x * kSplitThreads + threadIdx.x) >> 4;
+  const int c = threadIdx.x & 15;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (h < heads) v = __ldg(q + h * 16 + c);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float x[8], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  // smallest e >= -100 with amax <= 448 2^e = 1.75 2^(e + 8)
+  const uint32_t bits = __float_as_uint(amax);
+  const int ex = max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+  const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
+  uint16_t hh[4], ll[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i] * f, b = x[2 * i + 1] * f;
+    hh[i] = f32_to_e4m3x2(a, b);
+    const uint32_t back = e4m3x2_to_f16x2(hh[i]);
+    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&back));
+    ll[i] = f32_to_e4m3x2(a - r.x, b - r.y);
+  }
+  if (h >= heads) return;
+  hi[h * 16 + c] = make_uint2(hh[0] | (uint32_t)hh[1] << 16, hh[2] | (uint32_t)hh[3] << 16);
+  lo[h * 16 + c] = make_uint2(ll[0] | (uint32_t)ll[1] << 16, ll[2] | (uint32_t)ll[3] << 16);
+  if (c == 0) scale[h] = __uint_as_float((uint32_t)(127 + ex) << 23);
 }
 
 // ---------------------------------------------------------------------------
@@ -1274,18 +1272,20 @@ bool encode_pages(CUtensorMap* m, const void* base, long long rows, int page, CU
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [rows, heads, 128] bf16 rows `stride` elements apart, 64 columns of one head and 128 rows per box
-bool encode_rows(CUtensorMap* m, const void* base, int heads, long long rows, long long stride) {
+// [rows, heads, 128] elements of `es` bytes (bf16 or e4m3), rows `stride` elements apart; a box is 128 bytes of
+// box_heads heads of box_rows rows
+bool encode_rows(CUtensorMap* m, const void* base, int es, int heads, long long rows, long long stride, int box_heads,
+                 int box_rows) {
   const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {128 * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64, 1, BN}, es[3] = {1, 1, 1};
-  return fp8_encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+  const cuuint64_t strides[2] = {(cuuint64_t)(128 * es), (cuuint64_t)(stride * es)};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_heads, (cuuint32_t)box_rows}, steps[3] = {1, 1, 1};
+  return fp8_encode_fn()(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, steps,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Fp8Layout {
-  size_t plan, cnt, ml, o, total;
+  size_t plan, cnt, ml, o, q, qs, total;
   int grid, mt;
 };
 
@@ -1310,6 +1310,12 @@ bool fp8_layout(const ssv_attn_fp8_args* a, Fp8Layout* L) {
   off = align_up(off + sizeof(float) * 2 * (size_t)L->grid * L->mt * 128, 256);
   L->o = off;
   off = align_up(off + sizeof(float) * (size_t)L->grid * L->mt * 128 * D, 256);
+  // the split queries, where keys may be cached
+  const size_t heads = a->max_cache > 0 ? (size_t)a->total_rows * a->Hq : 0;
+  L->q = off;
+  off = align_up(off + heads * 2 * D, 256);
+  L->qs = off;
+  off = align_up(off + heads * sizeof(float), 256);
   L->total = off;
   return true;
 }
@@ -1379,30 +1385,41 @@ extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, 
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < L.total) return SSV_ERR_WORKSPACE;
   const int64_t width = (int64_t)a->Hkv * a->d;
   const FaultSetting f = fault_for(SSV_FAULT_ATTN);
-  AttnFp8Params p{static_cast<const __nv_bfloat16*>(a->q), a->k_scale, a->v_scale, a->pages,
+  char* w = static_cast<char*>(ws);
+  const int G = a->Hq / a->Hkv, max_cache = a->n_pages > 0 ? a->max_cache : 0;
+  AttnFp8Params p{reinterpret_cast<const float*>(w + L.qs), a->k_scale, a->v_scale, a->pages,
                   static_cast<__nv_bfloat16*>(a->o), a->Hq, a->Hkv, ilog2(a->page_size), a->n_pages, a->table_len,
                   a->scale > 0.f ? a->scale : (float)(1.0 / sqrt((double)a->d)), a->seqs, a->batch, a->tau,
-                  a->total_rows, a->total_slots, a->n_pages > 0 ? a->max_cache : 0, a->max_new, a->max_block,
-                  a->dev_status, f.budget, f.skip};
+                  a->total_rows, a->total_slots, max_cache, a->max_new, a->max_block, a->dev_status, f.budget, f.skip,
+                  max_cache > 0 ? 1 : 0};
   Fp8Maps maps;
   if (!fp8_encode_fn()) return SSV_ERR_CUDA;
-  if (!encode_rows(&maps.kn, a->k_new, a->Hkv, a->total_rows, a->k_stride ? a->k_stride : width) ||
-      !encode_rows(&maps.vn, a->v_new, a->Hkv, a->total_rows, a->v_stride ? a->v_stride : width))
+  if (!encode_rows(&maps.kn, a->k_new, 2, a->Hkv, a->total_rows, a->k_stride ? a->k_stride : width, 1, BN) ||
+      !encode_rows(&maps.vn, a->v_new, 2, a->Hkv, a->total_rows, a->v_stride ? a->v_stride : width, 1, BN) ||
+      !encode_rows(&maps.q, a->q, 2, a->Hq, a->total_rows, (int64_t)a->Hq * D, G, 128 / G))
     return SSV_ERR_CUDA;
-  if (a->n_pages > 0) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (max_cache > 0) {
     const long long rows = (long long)a->n_pages * a->Hkv * a->page_size;
     if (!encode_pages(&maps.kc, a->k_cache, rows, a->page_size, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_pages(&maps.vc, a->v_cache, rows, a->page_size, CU_TENSOR_MAP_SWIZZLE_NONE))
       return SSV_ERR_CUDA;
+    const long long heads = (long long)a->total_rows * a->Hq, blocks = (heads * 16 + kSplitThreads - 1) / kSplitThreads;
+    char *hi = w + L.q, *lo = hi + heads * D;
+    if (!encode_rows(&maps.qhi, hi, 1, a->Hq, a->total_rows, (int64_t)a->Hq * D, G, 128 / G) ||
+        !encode_rows(&maps.qlo, lo, 1, a->Hq, a->total_rows, (int64_t)a->Hq * D, G, 128 / G))
+      return SSV_ERR_CUDA;
+    if (blocks > 0x7fffffffLL) return SSV_ERR_INVALID;
+    if (launch_pdl(query_split_kernel, dim3((unsigned)blocks), dim3(kSplitThreads), 0, s,
+                   static_cast<const uint4*>(a->q), reinterpret_cast<uint2*>(hi), reinterpret_cast<uint2*>(lo),
+                   reinterpret_cast<float*>(w + L.qs), heads) != cudaSuccess)
+      return SSV_ERR_CUDA;
   } else {
-    maps.kc = maps.kn;  // never read: no sequence may have cached keys
+    maps.kc = maps.qhi = maps.qlo = maps.q;  // never read: no sequence may have cached keys
     maps.vc = maps.vn;
   }
-  char* w = static_cast<char*>(ws);
   const Fp8Work work{reinterpret_cast<int32_t*>(w + L.plan), reinterpret_cast<int32_t*>(w + L.cnt),
                      reinterpret_cast<float*>(w + L.ml), reinterpret_cast<float*>(w + L.o)};
-  const int G = a->Hq / a->Hkv;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = L.mt == 2 ? launch_fp8<2>(p, maps, work, G, L.grid, s) : launch_fp8<1>(p, maps, work, G, L.grid, s);
   return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;
 }

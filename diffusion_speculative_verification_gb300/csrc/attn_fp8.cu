@@ -31,11 +31,10 @@
 // order by the CTA that holds its first block (bounded wait on per-row-group
 // counters).  The plan is derived on the device from seqs.
 //
-// Roles of a CTA (16 warps, 128 registers each; warp 3 idles, so that a set's
-// softmax warps meet the four TMEM lane quadrants in order):
+// Roles of a CTA (16 warps, 128 registers each):
 //   warp 0        page lookups (32 pages ahead, one per lane), TMA of K pages
 //                 (swizzled, the operand itself) and V pages (raw) into rings,
-//                 fresh rows into two ring stages at once; the pages' scales
+//                 fresh rows into two ring stages at once
 //   warp 1        MMA issue for two S / P / O sets in turn: PV(n), S(n + 2), so
 //                 that a set's softmax runs under the other set's products.  The
 //                 whole warp runs the loop on uniform values and one elected
@@ -44,6 +43,7 @@
 //                 busy softmax warps that took 1640-2400 cycles for the 1025 of
 //                 a PV and an S (1027 as it is).
 //   warp 2        query tiles, in the form of the cached and of the fresh blocks
+//   warp 3        the scales of the pages, and with them the unit u
 //   warps 4..11   softmax, four per set, one TMEM lane quadrant each.  A unit of
 //                 two tiles gives each its set (job n: block n / 2); a unit of
 //                 one tile gives the sets its blocks in turn (job n: block n),
@@ -82,8 +82,8 @@ constexpr float kLazy = 8.f;                // the running maximum may lag by 2^
 constexpr float kWeight = 7.f;              // P holds weights times 2^7
 constexpr float kUnitTop = 7.f;             // vs / 2^u <= 2^7: |code| vs / 2^u < 2^16 in fp16
 constexpr float kUnitRoom = 2.f;            // u leaves that much for larger scales to come
-constexpr int SC = 20;                      // floats of a block's scales: K factor of every 16 keys x 8, log2 of the
-                                            // V scale x 8, u
+constexpr int SC = 20;                      // words of a block's scales: K factor of every 16 keys x 8, vs / 2^u of
+                                            // every 16 keys as an fp16 pair x 8, u
 // Estimated costs of the plan, in units of 0.1 us: a block of one / two tiles
 // and a segment's fixed work; a merge of partials costs about kMergeBlocks blocks.
 constexpr int kBlock1 = 7, kBlock2 = 12, kSegCost = 40;
@@ -476,6 +476,16 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     const bool w = mbar_wait(b, parity, abort, wb);
     return __all_sync(0xffffffffu, w);
   };
+  // page of lane `lane` of window w (32 pages) of a segment that starts at block k and holds np pages:
+  // -1 behind the last one, -2 where the table names none (reported; read as zeros)
+  auto page_at = [&](const Unit& x, int k, int np, int w) -> int {
+    const int t = 32 * w + lane;
+    if (t >= np) return -1;
+    const int pg = p.pages[x.kv_off + (size_t)k * ppb + t];
+    if (pg >= 0 && pg < p.n_pages) return pg;
+    report(p.dev_status, SSV_ERR_INVALID);
+    return -2;
+  };
   // ring index n of a ring of S stages: FULL parity of the use, EMPTY parity of the use before
   auto full_par = [](int n, int S) -> uint32_t { return (uint32_t)(n / S) & 1u; };
   auto empty_par = [](int n, int S) -> uint32_t { return (uint32_t)(n / S - 1) & 1u; };
@@ -485,7 +495,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     if (begin < end) {
       if (lane == 0) { tma_prefetch(&maps.kc); tma_prefetch(&maps.vc); tma_prefetch(&maps.kn); tma_prefetch(&maps.vn); }
       int u = plan->u0, k = plan->k0, remaining = end - begin;
-      int n = 0, nc = 0;  // ring index of K and raw V; cached blocks so far
+      int n = 0;                 // ring index of K and raw V
       int k_end = 0, v_end = 0;  // behind the last filled stage of either ring
       bool run = true;
       auto take = [&](uint32_t empty, int S) -> bool {  // stage n % S is free
@@ -497,36 +507,15 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
         // pages of the segment: t = 0 .. np, 32 of them per window, one per lane
         const int np = min(cdiv(x.C, ps), (k + cached) * ppb) - k * ppb;
-        const int32_t* table = p.pages + x.kv_off + (size_t)k * ppb;
-        auto page_at = [&](int w) -> int {  // -1: no such page
-          const int t = 32 * w + lane;
-          if (t >= np) return -1;
-          const int pg = table[t];
-          if (pg >= 0 && pg < p.n_pages) return pg;
-          report(p.dev_status, SSV_ERR_INVALID);
-          return -2;  // read as zeros
-        };
-        auto scales_at = [&](int pg, float& ks, float& vs) {
-          ks = vs = 1.f;
-          if (pg >= 0) {
-            ks = __ldg(p.k_scale + (size_t)pg * p.Hkv + gh);
-            vs = __ldg(p.v_scale + (size_t)pg * p.Hkv + gh);
-          }
-        };
-        int pg0 = page_at(0), pg1 = page_at(1), pg2 = -1;
-        float ks0, vs0, ks1 = 1.f, vs1 = 1.f;
-        scales_at(pg0, ks0, vs0);
-        float unit = 0.f;
+        int pg0 = page_at(x, k, np, 0), pg1 = page_at(x, k, np, 1);
+#pragma unroll 1
         for (int i = 0; run && i < cached; ++i) {
           const int t0 = i * ppb, nb = min(ppb, np - t0);
-          if ((t0 & 31) == 0) {
-            if (i > 0) { pg0 = pg1; pg1 = pg2; ks0 = ks1; vs0 = vs1; }
-            scales_at(pg1, ks1, vs1);
-            pg2 = page_at((t0 >> 5) + 2);
+          if (i > 0 && (t0 & 31) == 0) {
+            pg0 = pg1;
+            pg1 = page_at(x, k, np, (t0 >> 5) + 1);
           }
-          const int src = (t0 + lane) & 31;
-          const int pg = __shfl_sync(0xffffffffu, pg0, src);
-          const float ks = __shfl_sync(0xffffffffu, ks0, src), vs = __shfl_sync(0xffffffffu, vs0, src);
+          const int pg = __shfl_sync(0xffffffffu, pg0, (t0 + lane) & 31);
           const int row = pg >= 0 ? (pg * p.Hkv + gh) * ps : row_oob;
           auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full) {
             if (lane == 0) mbar_expect_tx(full, nb * ps * 128);
@@ -534,33 +523,13 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             if (lane < nb) tma_load_2d(dst + lane * ps * 128, map, 0, row, full);
           };
           if (!take(B_K_EMPTY, NK)) { run = false; break; }
-          if (!(cta == 0 && nc == p.fault_skip))  // test support: this key block's copy is left out
+          if (!(cta == 0 && n == p.fault_skip))  // test support: this key block's copy is left out
             load(&maps.kc, sbase + C_::SM_K + (n % NK) * STAGE, bar(B_K_FULL + n % NK));
           k_end = n + 1;
           if (!take(B_R_EMPTY, C_::NR)) { run = false; break; }
           load(&maps.vc, sbase + C_::SM_R + (n % C_::NR) * STAGE, bar(B_R_FULL + n % C_::NR));
           v_end = n + 1;
-          // the pages' scales, for the softmax warps
-          if (nc >= NSC && !warp_wait(bar(B_C_EMPTY + nc % NSC), empty_par(nc, NSC))) { run = false; break; }
-          float* sc = reinterpret_cast<float*>(smem + C_::SM_SC) + (nc % NSC) * SC;
-          const float kf = lane < nb ? ks * (p.scale * 1.4426950408889634f) : 0.f;
-          const float lv = lane < nb ? fmaxf(log2f(vs), -126.f) : -126.f;
-          float top = lv;
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          top = __shfl_sync(0xffffffffu, top, 0);
-          if (i == 0 || top > unit + kUnitTop) unit = ceilf(top) + kUnitRoom - kUnitTop;
-          const int page16 = (lane & 7) >> (p.ps_log2 - 4);  // page of 16 keys
-          const float kf16 = __shfl_sync(0xffffffffu, kf, page16), lv16 = __shfl_sync(0xffffffffu, lv, page16);
-          if (lane < 8) {
-            sc[lane] = kf16;
-            sc[8 + lane] = lv16;
-          }
-          if (lane == 0) sc[16] = unit;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_C_FULL + nc % NSC));
           ++n;
-          ++nc;
         }
         // fresh rows: a 16-bit block takes two stages, from an even one on
         for (int i = cached; run && i < len; ++i) {
@@ -633,51 +602,56 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       const int len = uni(min(x.nblocks - k, remaining)), cached = uni(min(max(x.cache_blocks - k, 0), len));
       const bool two = uni(x.mc) == 2;
       const int jobs = two ? 2 * len : len;
-      // S of job j into its set; the first and last job of a block wait for and release its keys,
-      // the first and last of a kind its form of the queries
-      auto issue_s = [&](int j) -> bool {
-        const int t = j & 1, i = two ? j >> 1 : j;
-        const bool q8 = i < cached;
-        if (!two || t == 0) {
-          if ((i == 0 || i == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) return false;
+      // Round j: PV of job j and S of job j + 2, of the same set.  What does not hang on the weights is waited
+      // for first, so that between the weights' arrival and the products there is only their issue.
+#pragma unroll 1
+      for (int j = -2; run && j < jobs; ++j) {
+        const int t = j & 1, js = j + 2, i = two ? js >> 1 : js;  // S: block i
+        const bool has_s = js < jobs, q8 = i < cached, last = !two || t == 1;
+        if (has_s && (!two || t == 0)) {  // the first job of block i
+          if ((i == 0 || i == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) { run = false; break; }
           if (!q8 && (n & 1)) {  // the stage left out
-            if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
+            if (!wait(B_K_FULL + n % NK, full_par(n, NK))) { run = false; break; }
             commit_elect(bar(B_K_EMPTY + n % NK));
             ++n;
           }
-          if (!wait(B_K_FULL + n % NK, full_par(n, NK))) return false;
-          if (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK))) return false;
+          if (!wait(B_K_FULL + n % NK, full_par(n, NK)) || (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK)))) {
+            run = false;
+            break;
+          }
         }
-        tc_fence_after();
         const uint64_t dq = dq0 + (two ? t : 0) * (2 * STAGE >> 4), dk = dk0 + (n % NK) * (STAGE >> 4);
-        if (q8) gemm_q8(tm + t * 128, dq, dk);
-        else gemm_qk(tm + t * 128, dq, dk);
-        commit_elect(bar(B_S_FULL + t));
-        if (!two || t == 1) {
-          for (int e = q8 ? 1 : 2; e > 0; --e, ++n) commit_elect(bar(B_K_EMPTY + n % NK));
-          if (i == cached - 1 || i == len - 1) commit_elect(bar(B_Q_EMPTY));
-        }
-        return true;
-      };
-#pragma unroll 1
-      for (int j = -2; run && j < jobs; ++j) {
+        const uint64_t dv = dv0 + (nv & 1) * (2 * STAGE >> 4);
+        const uint32_t tS = tm + t * 128, k_empty = bar(B_K_EMPTY + n % NK), v_empty = bar(B_V_EMPTY + (nv & 1));
+        const bool q_last = i == cached - 1 || i == len - 1;
+        const uint32_t id_pv = (two ? j >> 1 : j) < cached ? kIdPvF16 : kIdPvBf16;
         if (j >= 0) {
-          const int t = j & 1, i = two ? j >> 1 : j;
           if (((!two || t == 0) && !wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u)) ||
               (j == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1)) || !wait(B_P_FULL + t, t ? pph1 : pph0)) {
             run = false;
             break;
           }
-          if (t) pph1 ^= 1u; else pph0 ^= 1u;
           tc_fence_after();
-          gemm_pv(tm + TM_O + t * 128, tm + t * 128, dv0 + (nv & 1) * (2 * STAGE >> 4),
-                  i < cached ? kIdPvF16 : kIdPvBf16, j > 1 ? 1u : 0u);
-          if (!two || t == 1) {
-            commit_elect(bar(B_V_EMPTY + (nv & 1)));
-            ++nv;
+          gemm_pv(tS + TM_O, tS, dv, id_pv, j > 1 ? 1u : 0u);
+          if (t) pph1 ^= 1u; else pph0 ^= 1u;
+        } else {
+          tc_fence_after();
+        }
+        if (has_s) {
+          if (q8) gemm_q8(tS, dq, dk);
+          else gemm_qk(tS, dq, dk);
+          commit_elect(bar(B_S_FULL + t));
+          if (last) {
+            commit_elect(k_empty);
+            if (!q8) commit_elect(bar(B_K_EMPTY + (n + 1) % NK));
+            if (q_last) commit_elect(bar(B_Q_EMPTY));
+            n += q8 ? 1 : 2;
           }
         }
-        if (j + 2 < jobs && !issue_s(j + 2)) run = false;
+        if (j >= 0 && last) {
+          commit_elect(v_empty);
+          ++nv;
+        }
       }
       if (!run) break;
       commit_elect(bar(B_SEG_DONE));
@@ -723,6 +697,55 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         }
       }
     }
+  } else if (warp == 3) {
+    // ============================================================ scales
+    int u = plan->u0, k = plan->k0, remaining = end - begin, nc = 0;
+    bool run = true;
+    while (run && remaining > 0) {
+      const Unit x = decode(u);
+      const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
+      const int np = min(cdiv(x.C, ps), (k + cached) * ppb) - k * ppb;
+      float unit = 0.f, kf = 0.f, lv = -126.f, ks1, vs1;
+      auto fetch = [&](int w) {
+        const int pg = page_at(x, k, np, w);
+        ks1 = vs1 = 0.f;
+        if (pg >= 0) {
+          ks1 = __ldg(p.k_scale + (size_t)pg * p.Hkv + gh);
+          vs1 = __ldg(p.v_scale + (size_t)pg * p.Hkv + gh);
+        }
+      };
+      if (cached > 0) fetch(0);
+#pragma unroll 1
+      for (int i = 0; i < cached; ++i) {
+        const int t0 = i * ppb, nb = min(ppb, np - t0);
+        if ((t0 & 31) == 0) {  // the window's pages, and the loads of the next
+          kf = ks1 * (p.scale * 1.4426950408889634f);
+          lv = fmaxf(log2f(vs1), -126.f);
+          fetch((t0 >> 5) + 1);
+        }
+        // lane < 8: its 16 keys' page (the last one again behind it)
+        const int src = t0 + min((lane & 7) >> (p.ps_log2 - 4), nb - 1);
+        const float kf16 = __shfl_sync(0xffffffffu, kf, src & 31), lv16 = __shfl_sync(0xffffffffu, lv, src & 31);
+        float top = lv16;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (i == 0 || top > unit + kUnitTop) unit = ceilf(top) + kUnitRoom - kUnitTop;
+        if (nc >= NSC && !warp_wait(bar(B_C_EMPTY + nc % NSC), empty_par(nc, NSC))) { run = false; break; }
+        float* sc = reinterpret_cast<float*>(smem + C_::SM_SC) + (nc % NSC) * SC;
+        if (lane < 8) {
+          const __half2 f = __float2half2_rn(ex2(lv16 - unit));
+          sc[lane] = kf16;
+          reinterpret_cast<uint32_t*>(sc)[8 + lane] = *reinterpret_cast<const uint32_t*>(&f);
+        }
+        if (lane == 0) sc[16] = unit;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_C_FULL + nc % NSC));
+        ++nc;
+      }
+      remaining -= len;
+      ++u;
+      k = 0;
+    }
   } else if (warp >= 12) {
     // ============================================================ converters
     const int ct = threadIdx.x - 32 * 12;
@@ -753,38 +776,40 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             run = false;
             break;
           }
-          const uint8_t* raw = smem + C_::SM_R + (n % C_::NR) * STAGE + ct * 16;
           const float* sc = reinterpret_cast<const float*>(smem + C_::SM_SC) + (nc % NSC) * SC;
-          const float unit = sc[16];
           const int keys = x.C - (k + i) * BN;  // rows behind it become zeros
           static_assert(NT == 128, "sixteen keys per round");
-          // this thread: 16 codes (chunk c) of every 16th key; 16-byte chunks 2 c, 2 c + 1 of the key's 256
-          // bytes, in two 64-element columns.  The lanes of either column start with another one, so that
-          // eight lanes meet eight banks.
-          const int c = ct & 7, key0 = ct >> 3, c0 = (c & 3) * 2, sw = key0 & 7, first = c >> 2;
-          uint8_t* dst = smem + C_::SM_V + (nv & 1) * 2 * STAGE + first * STAGE + key0 * 128;
-          uint8_t* dst0 = dst + (((c0 + first) ^ sw) << 4);
-          uint8_t* dst1 = dst + (((c0 + 1 - first) ^ sw) << 4);
+          // this thread: 16 codes (chunk c) of a key in sixteen, which become 16-byte chunks 2 c, 2 c + 1 of the key's
+          // 256 bytes in two 64-element columns.  Eight lanes read chunks 0..3 of one key and 4..7 of its
+          // neighbour, so that both their reads and their writes (swizzled by the key) meet all banks.
+          const int c = ct & 7, key0 = (ct >> 3) ^ (c >> 2), c0 = (c & 3) * 2, sw = key0 & 7;
+          const uint8_t* raw = smem + C_::SM_R + (n % C_::NR) * STAGE + key0 * 128 + c * 16;
+          uint8_t* dst = smem + C_::SM_V + (nv & 1) * 2 * STAGE + (c >> 2) * STAGE + key0 * 128;
+          uint8_t *dst0 = dst + ((c0 ^ sw) << 4), *dst1 = dst + (((c0 + 1) ^ sw) << 4);
 #pragma unroll 1
           for (int g = 0; g < 8; g += 4) {
             uint4 s[4];
 #pragma unroll
-            for (int it = 0; it < 4; ++it) s[it] = *reinterpret_cast<const uint4*>(raw + (g + it) * NT * 16);
+            for (int it = 0; it < 4; ++it) s[it] = *reinterpret_cast<const uint4*>(raw + (g + it) * 16 * 128);
+            if (keys < BN) {
+#pragma unroll
+              for (int it = 0; it < 4; ++it)
+                if ((g + it) * 16 + key0 >= keys) s[it] = make_uint4(0, 0, 0, 0);
+            }
+            const uint4 f4 = reinterpret_cast<const uint4*>(sc)[2 + (g >> 2)];
+            const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-              if ((g + it) * 16 + key0 >= keys) s[it] = make_uint4(0, 0, 0, 0);
-              const __half2 f = __float2half2_rn(ex2(sc[8 + g + it] - unit));
               const uint32_t w[4] = {s[it].x, s[it].y, s[it].z, s[it].w};
               uint32_t h[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const uint32_t v = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), f);
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&f[it]));
                 h[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
-              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-              *reinterpret_cast<uint4*>(dst0 + (g + it) * 16 * 128) = first ? hi : lo;
-              *reinterpret_cast<uint4*>(dst1 + (g + it) * 16 * 128) = first ? lo : hi;
+              *reinterpret_cast<uint4*>(dst0 + (g + it) * 16 * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(dst1 + (g + it) * 16 * 128) = make_uint4(h[4], h[5], h[6], h[7]);
             }
           }
           __syncwarp();
@@ -878,16 +903,25 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           const int jj = two ? job >> 1 : job, j = k + jj;
           const bool is_cache = jj < cached, first = job == set;
           const int e = nc + jj;  // scales of the block
-          if (is_cache && !warp_wait(bar(B_C_FULL + e % NSC), full_par(e, NSC))) { run = false; break; }
+          // ---- the block's scales: factors of the scores of every 16 columns, the unit of O
+          float cf[8], unit_new = first ? 0.f : unit;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) cf[q] = cexp;
+          if (is_cache) {
+            if (!warp_wait(bar(B_C_FULL + e % NSC), full_par(e, NSC))) { run = false; break; }
+            const float4* sc = reinterpret_cast<const float4*>(smem + C_::SM_SC) + (e % NSC) * (SC / 4);
+            const float4 c0 = sc[0], c1 = sc[1];
+            const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) cf[q] = fmaxf(rowf * c[q], 1.17549435e-38f);
+            unit_new = reinterpret_cast<const float*>(sc)[16];
+            __syncwarp();
+            // (a block that one set alone works on is given back by it for both)
+            if (lane == 0) mbar_arrive_n(bar(B_C_EMPTY + e % NSC), two ? 1 : 2);
+          }
           if (!warp_wait(bar(B_S_FULL + set), sph)) { run = false; break; }
           sph ^= 1u;
-          // (a block that one set alone works on is given back by it for both)
-          auto scales_done = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive_n(bar(B_C_EMPTY + e % NSC), two ? 1 : 2);
-          };
           if (!warp_active) {
-            if (is_cache) scales_done();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_P_FULL + set));
             continue;
@@ -913,23 +947,24 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             if (lim_rows > 32 * q) v |= window32(tm, toff + 32 * q) & prefix32(lim_rows - 32 * q);
             return v;
           };
-          // ---- the block's scales: factors of the scores of every 16 columns, the unit of O
-          const float* sc = reinterpret_cast<const float*>(smem + C_::SM_SC) + (e % NSC) * SC;
-          auto factor = [&](int q) -> float { return is_cache ? fmaxf(rowf * sc[q], 1.17549435e-38f) : cexp; };
-          const float unit_new = is_cache ? sc[16] : (first ? 0.f : unit);
+          auto factor = [&](int q) -> float {  // cf[q], q not known when compiling
+            const float a = (q & 1) ? ((q & 2) ? cf[3] : cf[1]) : ((q & 2) ? cf[2] : cf[0]);
+            const float b = (q & 1) ? ((q & 2) ? cf[7] : cf[5]) : ((q & 2) ? cf[6] : cf[4]);
+            return (q & 4) ? b : a;
+          };
           const float shift = is_cache ? kWeight : kWeight - unit_new;  // P = exp2(x - m + shift)
           float lsum = 0.f;  // of P
           // ---- the row's maximum over the block
           float mx = -INFINITY;
           if (full) {
 #pragma unroll 1
-            for (int q = 0; q < BN / 16; q += 4) {
+            for (int g = 0; g < 2; ++g) {
               float a[4];
 #pragma unroll
-              for (int h = 0; h < 4; ++h) a[h] = tmem_max16(tS + (q + h) * 16);
+              for (int h = 0; h < 4; ++h) a[h] = tmem_max16(tS + g * 64 + h * 16);
               tmem_wait_ld();
 #pragma unroll
-              for (int h = 0; h < 4; ++h) mx = fmaxf(mx, a[h] * factor(q + h));
+              for (int h = 0; h < 4; ++h) mx = fmaxf(mx, a[h] * (g ? cf[4 + h] : cf[h]));
             }
           } else {
 #pragma unroll 1
@@ -973,11 +1008,11 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             uint32_t b0[32], b1[32];
             tmem_ld32(tS, b0);
             tmem_wait_ld();
-            auto chunk = [&](int q, uint32_t* cur) {
+            auto chunk = [&](int q, const uint32_t* cur, float ca, float cb) {
               uint32_t pw[16];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float c = kCache ? factor(2 * q + h) : cexp;
+                const float c = kCache ? (h ? cb : ca) : cexp;
                 const uint64_t cc2 = pack2(c, c);
 #pragma unroll
                 for (int v = 8 * h; v < 8 * h + 8; ++v) {
@@ -998,11 +1033,11 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               tmem_st16(tS + q * 16, pw);
             };
 #pragma unroll 1
-            for (int q = 0; q < BN / 32; q += 2) {
-              tmem_ld32(tS + (q + 1) * 32, b1);
-              chunk(q, b0);
-              if (q + 2 < BN / 32) tmem_ld32(tS + (q + 2) * 32, b0);
-              chunk(q + 1, b1);
+            for (int g = 0; g < 2; ++g) {
+              tmem_ld32(tS + (2 * g + 1) * 32, b1);
+              chunk(2 * g, b0, g ? cf[4] : cf[0], g ? cf[5] : cf[1]);
+              if (g == 0) tmem_ld32(tS + 64, b0);
+              chunk(2 * g + 1, b1, g ? cf[6] : cf[2], g ? cf[7] : cf[3]);
             }
             float y0, y1;
             unpack2(fadd2(lp0, lp1), y0, y1);
@@ -1035,7 +1070,6 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               tmem_st8(tS + q * 8, pw);
             }
           }
-          if (is_cache) scales_done();
           unit = unit_new;
           if (!is_cache) lsum *= ex2(unit_new);  // the row sum counts 2^7 exp2(x - m)
           tmem_wait_st();

@@ -34,7 +34,7 @@
 // Roles of a CTA (16 warps, 128 registers each):
 //   warp 0        page lookups (32 pages ahead, one per lane), TMA of K pages
 //                 (swizzled, the operand itself) and V pages (raw) into rings,
-//                 fresh keys into two stages at once
+//                 fresh rows into two ring stages at once
 //   warp 1        MMA issue for two S / P / O sets in turn: PV(n), S(n + 2), so
 //                 that a set's softmax runs under the other set's products.  The
 //                 whole warp runs the loop on uniform values and one elected
@@ -72,6 +72,7 @@ using namespace ptx;
 
 constexpr int D = 128;
 constexpr int BN = 128;                     // keys per block
+constexpr int NK = 4;                       // K ring stages
 constexpr int NSC = 8;                      // blocks of page scales in flight
 constexpr uint32_t STAGE = 128 * 128;       // one e4m3 tile, or half a 16-bit one
 constexpr uint32_t TMEM_COLS = 512;
@@ -90,10 +91,10 @@ constexpr int kMergeBlocks = 8;
 
 enum : uint32_t {
   B_K_FULL = 0,
-  B_K_EMPTY = B_K_FULL + 4,
-  B_R_FULL = B_K_EMPTY + 4,      // raw V ring
-  B_R_EMPTY = B_R_FULL + 4,
-  B_V_FULL = B_R_EMPTY + 4,      // 16-bit V, two stages
+  B_K_EMPTY = B_K_FULL + NK,
+  B_R_FULL = B_K_EMPTY + NK,     // raw V ring (at most NK stages)
+  B_R_EMPTY = B_R_FULL + NK,
+  B_V_FULL = B_R_EMPTY + NK,     // 16-bit V, two stages
   B_V_EMPTY = B_V_FULL + 2,
   B_C_FULL = B_V_EMPTY + 2,      // scales
   B_C_EMPTY = B_C_FULL + NSC,
@@ -104,16 +105,13 @@ enum : uint32_t {
   B_SEG_DONE = B_P_FULL + 2,     // every PV of the segment complete
   B_O_FREE = B_SEG_DONE + 1,     // both sets' O read
   B_ML_FULL = B_O_FREE + 1,      // the second set's maxima and sums (one tile)
-  B_NONE = B_ML_FULL + 1,        // committed to where a round has nothing to give back; nobody waits
-  B_FINAL = B_NONE + 1,
+  B_FINAL = B_ML_FULL + 1,
   B_COUNT = B_FINAL + 1
 };
 
 struct AttnFp8Params {
   const float* q_scale;  // [total_rows][Hq]: 2^e of the split queries
   const float *k_scale, *v_scale;
-  const __nv_bfloat16* v_new;
-  int64_t v_stride;      // elements
   const int32_t* pages;
   __nv_bfloat16* o;
   int Hq, Hkv, ps_log2, n_pages, table_len;
@@ -129,7 +127,7 @@ struct AttnFp8Params {
 };
 
 struct Fp8Maps {
-  CUtensorMap kc, vc, kn, q, qhi, qlo;
+  CUtensorMap kc, vc, kn, vn, q, qhi, qlo;
 };
 
 struct Fp8Work {
@@ -146,23 +144,9 @@ struct PlanHdr {
   int U, Pe, g, begin, end, u0, k0;
 };
 
-// Position in a ring of S stages: the stage, and the parity of its current use (a stage is free for its first
-// use: a wait for the other parity of a barrier's first phase returns at once).
-template <int S>
-struct Ring {
-  int s = 0;
-  uint32_t ph = 0u;
-  __device__ __forceinline__ void next() {
-    if (++s == S) {
-      s = 0;
-      ph ^= 1u;
-    }
-  }
-};
-
 template <int MT>
 struct Cfg {
-  static constexpr int NK = 4, NR = MT == 1 ? 4 : 2;        // stages of the K and of the raw V ring
+  static constexpr int NR = MT == 1 ? 4 : 2;                // raw V stages
   static constexpr uint32_t SM_Q = 0;                       // per tile: hi, lo; or the bf16 tile
   static constexpr uint32_t SM_K = SM_Q + MT * 2 * STAGE;
   static constexpr uint32_t SM_R = SM_K + NK * STAGE;
@@ -285,16 +269,6 @@ __device__ __forceinline__ void commit_elect(uint32_t bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void commit3_elect(uint32_t a, uint32_t b, uint32_t c) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%2];\n\t}" ::"r"(a),
-      "r"(b), "r"(c)
-      : "memory");
-}
-
 // 32 lanes x 16 columns and the largest of each lane's 16 values
 __device__ __forceinline__ float tmem_max16(uint32_t taddr) {
   uint32_t r[16];
@@ -314,7 +288,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, const Fp8Work work, int G,
                 int plan_smem) {
   using C_ = Cfg<MT>;
-  constexpr int NK = C_::NK, NR = C_::NR;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C_::SM_BAR + 8 * B_COUNT);
@@ -520,12 +493,14 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
   if (warp == 0) {
     // ============================================================ producer
     if (begin < end) {
-      if (lane == 0) { tma_prefetch(&maps.kc); tma_prefetch(&maps.vc); tma_prefetch(&maps.kn); }
+      if (lane == 0) { tma_prefetch(&maps.kc); tma_prefetch(&maps.vc); tma_prefetch(&maps.kn); tma_prefetch(&maps.vn); }
       int u = plan->u0, k = plan->k0, remaining = end - begin;
-      int count = 0;             // cached blocks so far
-      Ring<NK> kr;
-      Ring<NR> vr;
+      int n = 0;                 // ring index of K and raw V
+      int k_end = 0, v_end = 0;  // behind the last filled stage of either ring
       bool run = true;
+      auto take = [&](uint32_t empty, int S) -> bool {  // stage n % S is free
+        return n < S || warp_wait(bar(empty + n % S), empty_par(n, S));
+      };
       const int row_oob = (int)min((long long)p.n_pages * p.Hkv * ps, 0x7fffffffLL);
       while (run && remaining > 0) {
         const Unit x = decode(u);
@@ -534,7 +509,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         const int np = min(cdiv(x.C, ps), (k + cached) * ppb) - k * ppb;
         int pg0 = page_at(x, k, np, 0), pg1 = page_at(x, k, np, 1);
 #pragma unroll 1
-        for (int i = 0; i < cached; ++i, ++count) {
+        for (int i = 0; run && i < cached; ++i) {
           const int t0 = i * ppb, nb = min(ppb, np - t0);
           if (i > 0 && (t0 & 31) == 0) {
             pg0 = pg1;
@@ -547,135 +522,135 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             __syncwarp();
             if (lane < nb) tma_load_2d(dst + lane * ps * 128, map, 0, row, full);
           };
-          if (!warp_wait(bar(B_K_EMPTY + kr.s), kr.ph ^ 1u)) { run = false; break; }
-          if (!(cta == 0 && count == p.fault_skip))  // test support: this key block's copy is left out
-            load(&maps.kc, sbase + C_::SM_K + kr.s * STAGE, bar(B_K_FULL + kr.s));
-          kr.next();
-          if (!warp_wait(bar(B_R_EMPTY + vr.s), vr.ph ^ 1u)) { run = false; break; }
-          load(&maps.vc, sbase + C_::SM_R + vr.s * STAGE, bar(B_R_FULL + vr.s));
-          vr.next();
+          if (!take(B_K_EMPTY, NK)) { run = false; break; }
+          if (!(cta == 0 && n == p.fault_skip))  // test support: this key block's copy is left out
+            load(&maps.kc, sbase + C_::SM_K + (n % NK) * STAGE, bar(B_K_FULL + n % NK));
+          k_end = n + 1;
+          if (!take(B_R_EMPTY, C_::NR)) { run = false; break; }
+          load(&maps.vc, sbase + C_::SM_R + (n % C_::NR) * STAGE, bar(B_R_FULL + n % C_::NR));
+          v_end = n + 1;
+          ++n;
         }
-        // fresh keys: a 16-bit block takes two stages in a row
+        // fresh rows: a 16-bit block takes two stages, from an even one on
         for (int i = cached; run && i < len; ++i) {
-          if (kr.s == NK - 1) {  // one stage is left out
-            if (!warp_wait(bar(B_K_EMPTY + kr.s), kr.ph ^ 1u)) { run = false; break; }
-            if (lane == 0) mbar_arrive(bar(B_K_FULL + kr.s));
-            kr.next();
+          if (n & 1) {
+            if (!take(B_K_EMPTY, NK) || !take(B_R_EMPTY, C_::NR)) { run = false; break; }
+            if (lane == 0) { mbar_arrive(bar(B_K_FULL + n % NK)); mbar_arrive(bar(B_R_FULL + n % C_::NR)); }
+            ++n;
           }
-          if (!warp_wait(bar(B_K_EMPTY + kr.s), kr.ph ^ 1u) || !warp_wait(bar(B_K_EMPTY + kr.s + 1), kr.ph ^ 1u)) {
-            run = false;
-            break;
-          }
-          if (lane == 0) {
-            const int z = x.q_off + (k + i - x.cache_blocks) * BN;
-            const uint32_t f = bar(B_K_FULL + kr.s), dst = sbase + C_::SM_K + kr.s * STAGE;
-            mbar_expect_tx(f, 2 * STAGE);
-            tma_load_3d(dst, &maps.kn, 0, gh, z, f);
-            tma_load_3d(dst + STAGE, &maps.kn, 64, gh, z, f);
-            mbar_arrive(bar(B_K_FULL + kr.s + 1));
-          }
-          __syncwarp();
-          kr.next();
-          kr.next();
+          const int z = x.q_off + (k + i - x.cache_blocks) * BN;
+          auto pair = [&](const CUtensorMap* map, uint32_t ring, uint32_t full, uint32_t empty, int S) -> bool {
+            if (n >= S && !(warp_wait(bar(empty + n % S), empty_par(n, S)) &&
+                            warp_wait(bar(empty + (n + 1) % S), empty_par(n + 1, S))))
+              return false;
+            if (lane == 0) {
+              const uint32_t f = bar(full + n % S), dst = sbase + ring + (n % S) * STAGE;
+              mbar_expect_tx(f, 2 * STAGE);
+              tma_load_3d(dst, map, 0, gh, z, f);
+              tma_load_3d(dst + STAGE, map, 64, gh, z, f);
+              mbar_arrive(bar(full + (n + 1) % S));
+            }
+            __syncwarp();
+            return true;
+          };
+          if (!pair(&maps.kn, C_::SM_K, B_K_FULL, B_K_EMPTY, NK)) { run = false; break; }
+          k_end = n + 2;
+          if (!pair(&maps.vn, C_::SM_R, B_R_FULL, B_R_EMPTY, C_::NR)) { run = false; break; }
+          v_end = n + 2;
+          n += 2;
         }
         remaining -= len;
         ++u;
         k = 0;
       }
-      // drain (bounded, regardless of abort): the copies that may still be in flight are those of each stage's
-      // last use, the one before the ring's position
-      auto drain = [&](uint32_t full, int stages, int s, uint32_t ph) {
-        for (int i = 0; i < stages; ++i) {
+      // drain (bounded, regardless of abort): the copies that may still be in flight
+      auto drain = [&](uint32_t full, int S, int last) {
+        for (int i = max(last - S, 0); i < last; ++i) {
           const long long t0 = clock64();
-          while (!mbar_try_wait(bar(full + i), i < s ? ph : ph ^ 1u) && clock64() - t0 < wb) {
+          while (!mbar_try_wait(bar(full + i % S), full_par(i, S)) && clock64() - t0 < wb) {
           }
         }
       };
-      drain(B_K_FULL, NK, kr.s, kr.ph);
-      drain(B_R_FULL, NR, vr.s, vr.ph);
+      drain(B_K_FULL, NK, k_end);
+      drain(B_R_FULL, C_::NR, v_end);
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer (converged; see above)
     auto uni = [](int v) -> int { return __shfl_sync(0xffffffffu, v, 0); };
     const uint32_t tm = (uint32_t)uni((int)tmem);
     int u = uni(plan->u0), k = uni(plan->k0), remaining = uni(end - begin), nseg = 0;
-    int nv = 0, nq = 0;              // V blocks, query phases
+    int n = 0, nv = 0, nq = 0;       // K ring index, V blocks, query phases
     uint32_t pph0 = 0u, pph1 = 0u;   // parity of the next P of either set
-    Ring<NK> kr;
     bool run = true;
     const uint64_t dq0 = smem_desc_sw128(sbase + C_::SM_Q, 16, 1024);
     const uint64_t dk0 = smem_desc_sw128(sbase + C_::SM_K, 16, 1024);
     const uint64_t dv0 = smem_desc_sw128(sbase + C_::SM_V, STAGE, 1024);
-    // all three phases complete (one vote: a round waits once)
-    auto wait3 = [&](uint32_t b1, uint32_t par1, uint32_t b2, uint32_t par2, uint32_t b3, uint32_t par3) -> bool {
-      if (__all_sync(0xffffffffu, mbar_test_wait(b1, par1) & mbar_test_wait(b2, par2) & mbar_test_wait(b3, par3)))
-        return true;
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+      if (__all_sync(0xffffffffu, mbar_test_wait(bar(b), parity))) return true;
       const long long t0 = clock64();
       while (true) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(b1, par1) && mbar_try_wait(b2, par2) && mbar_try_wait(b3, par3)))
-          return true;
-        if (__any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > wb)) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, clock64() - t0 > wb)) {
           *abort = 1;
           return false;
         }
       }
     };
-    auto wait = [&](uint32_t b, uint32_t par) -> bool { return wait3(bar(b), par, bar(b), par, bar(b), par); };
     while (run && remaining > 0) {
       const Unit x = decode(u);
       const int len = uni(min(x.nblocks - k, remaining)), cached = uni(min(max(x.cache_blocks - k, 0), len));
       const bool two = uni(x.mc) == 2;
       const int jobs = two ? 2 * len : len;
-      // Round j: PV of job j and S of job j + 2, of the same set.
+      // Round j: PV of job j and S of job j + 2, of the same set.  What does not hang on the weights is waited
+      // for first, so that between the weights' arrival and the products there is only their issue.
 #pragma unroll 1
       for (int j = -2; run && j < jobs; ++j) {
         const int t = j & 1, js = j + 2, i = two ? js >> 1 : js;  // S: block i
-        const bool has_s = js < jobs, q8 = i < cached, last = !two || t == 1, new_k = has_s && (!two || t == 0);
-        if (new_k && (i == 0 || i == cached || (!q8 && kr.s == NK - 1))) {
-          // the first block of a form of the queries; a stage left out
-          run = (i > 0 && i != cached) || wait(B_Q_FULL, (uint32_t)(nq++) & 1u);
-          if (run && !q8 && kr.s == NK - 1) {
-            run = wait(B_K_FULL + kr.s, kr.ph);
-            commit_elect(bar(B_K_EMPTY + kr.s));
-            kr.next();
+        const bool has_s = js < jobs, q8 = i < cached, last = !two || t == 1;
+        if (has_s && (!two || t == 0)) {  // the first job of block i
+          if ((i == 0 || i == cached) && !wait(B_Q_FULL, (uint32_t)(nq++) & 1u)) { run = false; break; }
+          if (!q8 && (n & 1)) {  // the stage left out
+            if (!wait(B_K_FULL + n % NK, full_par(n, NK))) { run = false; break; }
+            commit_elect(bar(B_K_EMPTY + n % NK));
+            ++n;
           }
-          if (!run) break;
+          if (!wait(B_K_FULL + n % NK, full_par(n, NK)) || (!q8 && !wait(B_K_FULL + (n + 1) % NK, full_par(n + 1, NK)))) {
+            run = false;
+            break;
+          }
         }
-        const uint32_t k_bar = bar(B_K_FULL + kr.s), p_bar = bar(B_P_FULL + t);
-        const uint32_t p_par = t ? pph1 : pph0, none = bar(B_NONE);
-        const uint64_t dq = dq0 + (two ? t : 0) * (2 * STAGE >> 4), dk = dk0 + kr.s * (STAGE >> 4);
+        const uint64_t dq = dq0 + (two ? t : 0) * (2 * STAGE >> 4), dk = dk0 + (n % NK) * (STAGE >> 4);
         const uint64_t dv = dv0 + (nv & 1) * (2 * STAGE >> 4);
-        const uint32_t tS = tm + t * 128, v_empty = j >= 0 && last ? bar(B_V_EMPTY + (nv & 1)) : none;
-        const uint32_t k_empty = has_s && last ? bar(B_K_EMPTY + kr.s) : none;
+        const uint32_t tS = tm + t * 128, k_empty = bar(B_K_EMPTY + n % NK), v_empty = bar(B_V_EMPTY + (nv & 1));
         const bool q_last = i == cached - 1 || i == len - 1;
-        // the keys of S; the values of PV's block, and P
-        const uint32_t v_bar = bar(B_V_FULL + (nv & 1)), v_par = (uint32_t)(nv >> 1) & 1u;
-        if (!(j < 0 ? (!has_s || wait3(k_bar, kr.ph, k_bar, kr.ph, k_bar, kr.ph))
-                    : (new_k ? wait3(k_bar, kr.ph, v_bar, v_par, p_bar, p_par)
-                             : wait3(v_bar, v_par, v_bar, v_par, p_bar, p_par))) ||
-            (j == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1))) {
-          run = false;
-          break;
-        }
-        if (new_k && !q8 && !wait(B_K_FULL + kr.s + 1, kr.ph)) { run = false; break; }
-        tc_fence_after();
+        const uint32_t id_pv = (two ? j >> 1 : j) < cached ? kIdPvF16 : kIdPvBf16;
         if (j >= 0) {
-          gemm_pv(tS + TM_O, tS, dv, (two ? j >> 1 : j) < cached ? kIdPvF16 : kIdPvBf16, j > 1 ? 1u : 0u);
+          if (((!two || t == 0) && !wait(B_V_FULL + (nv & 1), (uint32_t)(nv >> 1) & 1u)) ||
+              (j == 0 && nseg > 0 && !wait(B_O_FREE, (nseg - 1) & 1)) || !wait(B_P_FULL + t, t ? pph1 : pph0)) {
+            run = false;
+            break;
+          }
+          tc_fence_after();
+          gemm_pv(tS + TM_O, tS, dv, id_pv, j > 1 ? 1u : 0u);
           if (t) pph1 ^= 1u; else pph0 ^= 1u;
-          if (last) ++nv;
+        } else {
+          tc_fence_after();
         }
         if (has_s) {
           if (q8) gemm_q8(tS, dq, dk);
           else gemm_qk(tS, dq, dk);
-        }
-        commit3_elect(has_s ? bar(B_S_FULL + t) : none, k_empty, v_empty);
-        if (has_s && last) {
-          if (!q8) {
-            commit_elect(bar(B_K_EMPTY + kr.s + 1));
-            kr.next();
+          commit_elect(bar(B_S_FULL + t));
+          if (last) {
+            commit_elect(k_empty);
+            if (!q8) commit_elect(bar(B_K_EMPTY + (n + 1) % NK));
+            if (q_last) commit_elect(bar(B_Q_EMPTY));
+            n += q8 ? 1 : 2;
           }
-          kr.next();
-          if (q_last) commit_elect(bar(B_Q_EMPTY));
+        }
+        if (j >= 0 && last) {
+          commit_elect(v_empty);
+          ++nv;
         }
       }
       if (!run) break;
@@ -773,34 +748,44 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     }
   } else if (warp >= 12) {
     // ============================================================ converters
-    // A thread converts 16 codes (chunk c) of a key in sixteen, which become the 16-byte chunks 2 c, 2 c + 1 of the
-    // key's 256 bytes in two 64-element columns.  Eight lanes read chunks 0..3 of one key and 4..7 of its
-    // neighbour, so that both their reads and their writes (swizzled by the key) meet all banks.
+    const int ct = threadIdx.x - 32 * 12;
     constexpr int NT = 32 * kConv;
-    static_assert(NT == 128, "sixteen keys per round");
-    const int ct = threadIdx.x - 32 * 12, c = ct & 7, key0 = (ct >> 3) ^ (c >> 2), c0 = (c & 3) * 2, sw = key0 & 7;
-    const uint8_t* raw0 = smem + C_::SM_R + key0 * 128 + c * 16;
-    uint8_t* dst = smem + C_::SM_V + (c >> 2) * STAGE + key0 * 128;
-    uint8_t *dst0 = dst + ((c0 ^ sw) << 4), *dst1 = dst + (((c0 + 1) ^ sw) << 4);
     int u = plan->u0, k = plan->k0, remaining = end - begin;
-    int nv = 0, nc = 0;  // blocks, cached blocks
-    Ring<NR> vr;
+    int n = 0, nv = 0, nc = 0;
     bool run = true;
     while (run && remaining > 0) {
       const Unit x = decode(u);
       const int len = min(x.nblocks - k, remaining), cached = min(max(x.cache_blocks - k, 0), len);
-#pragma unroll 1
-      for (int i = 0; i < len; ++i, ++nv) {
-        const uint32_t stage = (nv & 1) * 2 * STAGE;
-        if (nv >= 2 && !warp_wait(bar(B_V_EMPTY + (nv & 1)), (uint32_t)((nv >> 1) - 1) & 1u)) { run = false; break; }
-        if (i < cached) {
-          if (!warp_wait(bar(B_C_FULL + nc % NSC), full_par(nc, NSC)) || !warp_wait(bar(B_R_FULL + vr.s), vr.ph)) {
+      auto v_ready = [&]() -> bool {  // the 16-bit stage of V block nv is free
+        return nv < 2 || warp_wait(bar(B_V_EMPTY + (nv & 1)), (uint32_t)((nv >> 1) - 1) & 1u);
+      };
+      auto v_done = [&](int stages) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_V_FULL + (nv & 1)));
+          for (int e = 0; e < stages; ++e) mbar_arrive(bar(B_R_EMPTY + (n + e) % C_::NR));
+        }
+        n += stages;
+        ++nv;
+      };
+      if (cached > 0) {
+        for (int i = 0; i < cached; ++i) {
+          if (!warp_wait(bar(B_C_FULL + nc % NSC), full_par(nc, NSC)) ||
+              !warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) || !v_ready()) {
             run = false;
             break;
           }
-          const uint4* sc = reinterpret_cast<const uint4*>(smem + C_::SM_SC) + (nc % NSC) * (SC / 4);
-          const uint8_t* raw = raw0 + vr.s * STAGE;
+          const float* sc = reinterpret_cast<const float*>(smem + C_::SM_SC) + (nc % NSC) * SC;
           const int keys = x.C - (k + i) * BN;  // rows behind it become zeros
+          static_assert(NT == 128, "sixteen keys per round");
+          // this thread: 16 codes (chunk c) of a key in sixteen, which become 16-byte chunks 2 c, 2 c + 1 of the key's
+          // 256 bytes in two 64-element columns.  Eight lanes read chunks 0..3 of one key and 4..7 of its
+          // neighbour, so that both their reads and their writes (swizzled by the key) meet all banks.
+          const int c = ct & 7, key0 = (ct >> 3) ^ (c >> 2), c0 = (c & 3) * 2, sw = key0 & 7;
+          const uint8_t* raw = smem + C_::SM_R + (n % C_::NR) * STAGE + key0 * 128 + c * 16;
+          uint8_t* dst = smem + C_::SM_V + (nv & 1) * 2 * STAGE + (c >> 2) * STAGE + key0 * 128;
+          uint8_t *dst0 = dst + ((c0 ^ sw) << 4), *dst1 = dst + (((c0 + 1) ^ sw) << 4);
 #pragma unroll 1
           for (int g = 0; g < 8; g += 4) {
             uint4 s[4];
@@ -811,7 +796,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               for (int it = 0; it < 4; ++it)
                 if ((g + it) * 16 + key0 >= keys) s[it] = make_uint4(0, 0, 0, 0);
             }
-            const uint4 f4 = sc[2 + (g >> 2)];
+            const uint4 f4 = reinterpret_cast<const uint4*>(sc)[2 + (g >> 2)];
             const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
@@ -823,33 +808,35 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
                 const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&f[it]));
                 h[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
-              *reinterpret_cast<uint4*>(dst0 + stage + (g + it) * 16 * 128) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(dst1 + stage + (g + it) * 16 * 128) = make_uint4(h[4], h[5], h[6], h[7]);
+              *reinterpret_cast<uint4*>(dst0 + (g + it) * 16 * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(dst1 + (g + it) * 16 * 128) = make_uint4(h[4], h[5], h[6], h[7]);
             }
           }
-        } else {
-          const int r0 = (k + i - x.cache_blocks) * BN, ch = ct & 15;
-          const __nv_bfloat16* rows = p.v_new + (int64_t)(x.q_off + r0) * p.v_stride + gh * D;
-#pragma unroll 8
-          for (int key = ct >> 4; key < BN; key += NT / 16) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r0 + key < x.rows) v = __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)key * p.v_stride) + ch);
-            *reinterpret_cast<uint4*>(smem + C_::SM_V + stage + (ch >> 3) * STAGE + key * 128 +
-                                      (((ch & 7) ^ (key & 7)) << 4)) = v;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(B_V_FULL + (nv & 1)));
-          if (i < cached) {
-            mbar_arrive(bar(B_R_EMPTY + vr.s));
-            mbar_arrive(bar(B_C_EMPTY + nc % NSC));
-          }
-        }
-        if (i < cached) {
-          vr.next();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_C_EMPTY + nc % NSC));
           ++nc;
+          v_done(1);
+        }
+      }
+      if (run && len > cached) {
+        for (int i = cached; i < len; ++i) {
+          if (n & 1) {  // the stage left out
+            if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR))) { run = false; break; }
+            if (lane == 0) mbar_arrive(bar(B_R_EMPTY + n % C_::NR));
+            ++n;
+          }
+          if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) ||
+              !warp_wait(bar(B_R_FULL + (n + 1) % C_::NR), full_par(n + 1, C_::NR)) || !v_ready()) {
+            run = false;
+            break;
+          }
+          const uint4* raw = reinterpret_cast<const uint4*>(smem + C_::SM_R + (n % C_::NR) * STAGE);
+          uint4* dst = reinterpret_cast<uint4*>(smem + C_::SM_V + (nv & 1) * 2 * STAGE);
+          const int keys = x.rows - (k + i - x.cache_blocks) * BN;
+#pragma unroll 4
+          for (int idx = ct; idx < 2048; idx += NT)
+            dst[idx] = ((idx & 1023) >> 3) < keys ? raw[idx] : make_uint4(0, 0, 0, 0);
+          v_done(2);
         }
       }
       remaining -= len;
@@ -1012,45 +999,45 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           }
           if (need) m_used = mx;
           const float off = shift - ((m_used == -INFINITY) ? 0.f : m_used);
-          // ---- P = exp2(x - m + shift) over S: chunk q reads S columns [16 q, 16 q + 16) and writes P columns
-          // [8 q, 8 q + 8), which lie in S columns already read
+          // ---- P = exp2(x - m + shift) over S: chunk q reads S columns [32 q, 32 q + 32) and writes P columns
+          // [16 q, 16 q + 16), which lie in S columns already read
           auto exps = [&](auto cache_tag) {
             constexpr bool kCache = decltype(cache_tag)::value;
             const uint64_t of2 = pack2(off, off);
             uint64_t lp0 = 0ull, lp1 = 0ull;
-            uint32_t b0[16], b1[16];
-            tmem_ld16(tS, b0);
+            uint32_t b0[32], b1[32];
+            tmem_ld32(tS, b0);
             tmem_wait_ld();
-            auto chunk = [&](int q, const uint32_t* cur, float c) {
-              uint32_t pw[8];
-              const uint64_t cc2 = pack2(kCache ? c : cexp, kCache ? c : cexp);
+            auto chunk = [&](int q, const uint32_t* cur, float ca, float cb) {
+              uint32_t pw[16];
 #pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                float x0, x1;
-                unpack2(ffma2(pack2(__uint_as_float(cur[2 * v]), __uint_as_float(cur[2 * v + 1])), cc2, of2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                if constexpr (kCache) {
-                  const __half2 w = __floats2half2_rn(p0, p1);
-                  pw[v] = *reinterpret_cast<const uint32_t*>(&w);
-                } else {
-                  const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
-                  pw[v] = *reinterpret_cast<const uint32_t*>(&w);
+              for (int h = 0; h < 2; ++h) {
+                const float c = kCache ? (h ? cb : ca) : cexp;
+                const uint64_t cc2 = pack2(c, c);
+#pragma unroll
+                for (int v = 8 * h; v < 8 * h + 8; ++v) {
+                  float x0, x1;
+                  unpack2(ffma2(pack2(__uint_as_float(cur[2 * v]), __uint_as_float(cur[2 * v + 1])), cc2, of2), x0, x1);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  if constexpr (kCache) {
+                    const __half2 w = __floats2half2_rn(p0, p1);
+                    pw[v] = *reinterpret_cast<const uint32_t*>(&w);
+                  } else {
+                    const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
+                    pw[v] = *reinterpret_cast<const uint32_t*>(&w);
+                  }
+                  if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
                 }
-                if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
               }
               tmem_wait_ld();  // the next chunk is here, so this one's P may go over it
-              tmem_st8(tS + q * 8, pw);
+              tmem_st16(tS + q * 16, pw);
             };
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
-              tmem_ld16(tS + (4 * g + 1) * 16, b1);
-              chunk(4 * g, b0, g ? cf[4] : cf[0]);
-              tmem_ld16(tS + (4 * g + 2) * 16, b0);
-              chunk(4 * g + 1, b1, g ? cf[5] : cf[1]);
-              tmem_ld16(tS + (4 * g + 3) * 16, b1);
-              chunk(4 * g + 2, b0, g ? cf[6] : cf[2]);
-              if (g == 0) tmem_ld16(tS + 64, b0);
-              chunk(4 * g + 3, b1, g ? cf[7] : cf[3]);
+              tmem_ld32(tS + (2 * g + 1) * 32, b1);
+              chunk(2 * g, b0, g ? cf[4] : cf[0], g ? cf[5] : cf[1]);
+              if (g == 0) tmem_ld32(tS + 64, b0);
+              chunk(2 * g + 1, b1, g ? cf[6] : cf[2], g ? cf[7] : cf[3]);
             }
             float y0, y1;
             unpack2(fadd2(lp0, lp1), y0, y1);
@@ -1434,8 +1421,7 @@ extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, 
   const FaultSetting f = fault_for(SSV_FAULT_ATTN);
   char* w = static_cast<char*>(ws);
   const int G = a->Hq / a->Hkv, max_cache = a->n_pages > 0 ? a->max_cache : 0;
-  AttnFp8Params p{reinterpret_cast<const float*>(w + L.qs), a->k_scale, a->v_scale,
-                  static_cast<const __nv_bfloat16*>(a->v_new), a->v_stride ? a->v_stride : width, a->pages,
+  AttnFp8Params p{reinterpret_cast<const float*>(w + L.qs), a->k_scale, a->v_scale, a->pages,
                   static_cast<__nv_bfloat16*>(a->o), a->Hq, a->Hkv, ilog2(a->page_size), a->n_pages, a->table_len,
                   a->scale > 0.f ? a->scale : (float)(1.0 / sqrt((double)a->d)), a->seqs, a->batch, a->tau,
                   a->total_rows, a->total_slots, max_cache, a->max_new, a->max_block, a->dev_status, f.budget, f.skip,
@@ -1443,6 +1429,7 @@ extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, 
   Fp8Maps maps;
   if (!fp8_encode_fn()) return SSV_ERR_CUDA;
   if (!encode_rows(&maps.kn, a->k_new, 2, a->Hkv, a->total_rows, a->k_stride ? a->k_stride : width, 1, BN) ||
+      !encode_rows(&maps.vn, a->v_new, 2, a->Hkv, a->total_rows, a->v_stride ? a->v_stride : width, 1, BN) ||
       !encode_rows(&maps.q, a->q, 2, a->Hq, a->total_rows, (int64_t)a->Hq * D, G, 128 / G))
     return SSV_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1463,7 +1450,7 @@ extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, 
       return SSV_ERR_CUDA;
   } else {
     maps.kc = maps.qhi = maps.qlo = maps.q;  // never read: no sequence may have cached keys
-    maps.vc = maps.q;
+    maps.vc = maps.vn;
   }
   const Fp8Work work{reinterpret_cast<int32_t*>(w + L.plan), reinterpret_cast<int32_t*>(w + L.cnt),
                      reinterpret_cast<float*>(w + L.ml), reinterpret_cast<float*>(w + L.o)};

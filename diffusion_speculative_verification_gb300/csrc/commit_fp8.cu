@@ -7,15 +7,16 @@
 //   already holds rows of the sequence;  codes = rn_e4m3(X / s), and the rows
 //   already there become rn_e4m3(code * s_old / s) when s grew.
 //
-// Work: one CTA per (chunk of page_size packed rows, head, K or V).  A page is
-// led by the first token appended to it; the tokens' append indices i < N +
-// n_acc are counted along the packed rows from q_off, so a chunk of page_size
-// rows holds one leader per page boundary or sequence start in it, and the
-// number of CTAs follows from total_rows alone, however ragged the batch.
-// The rows of a page stay in registers between the maximum and the rounding:
-// each element is read once and each code written once.  Bound by HBM for
-// prompts, by latency (table, stage map, rows: three dependent rounds) for a
-// decode pass.
+// Work: one CTA per (chunk of page_size packed rows, group of heads of K or V).
+// A page is led by the first token appended to it; the tokens' append indices
+// i < N + n_acc are counted along the packed rows from q_off, so a chunk of
+// page_size rows holds one leader per page boundary or sequence start in it, and
+// the number of CTAs follows from total_rows alone, however ragged the batch.
+// Per leader, page_size / 16 warps take one (page, head): sixteen rows each, in
+// registers between the maximum and the rounding, so that each element is read
+// once and each code written once.  Bound by HBM for prompts, by latency
+// (sequences; table and stage map; rows: three dependent rounds) for a decode
+// pass, which is why a CTA's warps serve different heads of the same page.
 #include "ssv_internal.cuh"
 #include "paged.cuh"
 
@@ -71,11 +72,10 @@ __device__ __forceinline__ float scale_for(float amax) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kC8Threads) commit_fp8_kernel(const Commit8Params p) {
-  constexpr int VEC = 16 / (int)sizeof(T), LANES = D / VEC;  // threads per row
-  constexpr int ROWS = kC8Threads / LANES;                   // rows per pass
-  constexpr int PASSES = 128 / ROWS;
-  __shared__ int s_lead[128], s_inv[64], s_nlead;
+__global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8_kernel(const Commit8Params p) {
+  constexpr int VEC = 16 / (int)sizeof(T), LANES = D / VEC;  // lanes per row
+  constexpr int RPP = 32 / LANES, PASSES = 16 / RPP;         // rows per pass of a warp, passes over its sixteen
+  __shared__ int s_lead[128], s_inv[64], s_nlead, s_na[kC8Threads];
   __shared__ float s_max[kC8Threads / 32];
   __shared__ ssv_seq s_seq[kC8Threads];
   pdl_wait();  // n_acc and the fresh rows may come from the kernels before this one
@@ -101,7 +101,10 @@ __global__ void __launch_bounds__(kC8Threads) commit_fp8_kernel(const Commit8Par
   }
   // ---- leaders of this chunk's rows
   const bool table = p.batch <= kC8Threads;
-  if (table && (int)threadIdx.x < p.batch) s_seq[threadIdx.x] = p.seqs[threadIdx.x];
+  if (table && (int)threadIdx.x < p.batch) {
+    s_seq[threadIdx.x] = p.seqs[threadIdx.x];
+    s_na[threadIdx.x] = p.n_acc[threadIdx.x];
+  }
   if (threadIdx.x == 0) s_nlead = 0;
   __syncthreads();
   if ((int)threadIdx.x < ps) {
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kC8Threads) commit_fp8_kernel(const Commit8Par
     if (b >= 0) {
       const ssv_seq s = table ? s_seq[b] : p.seqs[b];
       const int i = row - s.q_off;
-      const int na = p.n_acc[b];
+      const int na = table ? s_na[b] : p.n_acc[b];
       if (!seq_idle(s) && commit8_sizes(p, s, na) && i < s.new_len + na &&
           (i == 0 || ((s.cache_len + i) & (ps - 1)) == 0))
         s_lead[atomicAdd(&s_nlead, 1)] = row;
@@ -118,113 +121,121 @@ __global__ void __launch_bounds__(kC8Threads) commit_fp8_kernel(const Commit8Par
   }
   __syncthreads();
   const int nlead = s_nlead;
-  const int head = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
+  // this warp: rows [16 part, 16 part + 16) of head `head` of K or V
+  const int parts = ps >> 4, unit = blockIdx.y * ((kC8Threads / 32) / parts) + warp / parts, part = warp & (parts - 1);
+  const bool mine = unit < 2 * p.Hkv, is_v = unit >= p.Hkv;
+  const int head = is_v ? unit - p.Hkv : unit;
   const uint8_t* fresh = (is_v ? p.v_new : p.k_new) + (int64_t)head * D * sizeof(T);
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
   for (int l = 0; l < nlead; ++l) {
     const int row = s_lead[l];
     const int b = find_seq_by_row(table ? s_seq : p.seqs, p.batch, row);
     const ssv_seq s = table ? s_seq[b] : p.seqs[b];
-    const int N = s.new_len, B = s.block, na = p.n_acc[b], i0 = row - s.q_off;
+    const int N = s.new_len, B = s.block, na = table ? s_na[b] : p.n_acc[b], i0 = row - s.q_off;
+    const int t0 = s.cache_len + i0, o0 = t0 & (ps - 1);            // first appended row of the page
+    const int n = min(ps - o0, N + na - i0);                        // rows appended to it
+    const int page = p.pages[s.kv_off + (t0 >> p.ps_log2)];
     // the whole sequence is good, or nothing of it is written
     int bad = commit8_bad_page(p, s, na, threadIdx.x, kC8Threads);
     if (warp == 0) bad |= !warp_tau_is_permutation(p.tau + s.tau_off, B);
+    int stage = 0;
+    if ((int)threadIdx.x < B) stage = p.tau[s.tau_off + threadIdx.x];
     if (__syncthreads_or(bad)) continue;
-    if ((int)threadIdx.x < B) s_inv[p.tau[s.tau_off + threadIdx.x] - 1] = threadIdx.x;  // slot of each stage
+    if ((int)threadIdx.x < B) s_inv[stage - 1] = threadIdx.x;  // slot of each stage
     __syncthreads();
-    const int t0 = s.cache_len + i0, o0 = t0 & (ps - 1);            // first appended row of the page
-    const int n = min(ps - o0, N + na - i0);                        // rows appended to it
-    const int64_t at = (int64_t)p.pages[s.kv_off + (t0 >> p.ps_log2)] * p.Hkv + head;
+    const int64_t at = (int64_t)page * p.Hkv + head;
     uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + at * ps * D;
     float* scale = (is_v ? p.v_scale : p.k_scale) + at;
-    const float s_old = o0 > 0 ? *scale : 0.f;
-    const int lr = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    const int r0 = part * 16 + lane / LANES, c = lane % LANES;  // of the appended rows
     uint4 x[PASSES];
-    float amax = 0.f;
+    float s_old = 0.f, amax = 0.f;
+    if (mine) {
+      if (o0 > 0) s_old = *scale;
 #pragma unroll
-    for (int k = 0; k < PASSES; ++k) {
-      const int r = k * ROWS + lr;
-      if (r >= n) continue;
-      const int i = i0 + r;
-      const int src = s.q_off + (i < N ? i : N + s_inv[i - N]);
-      x[k] = *reinterpret_cast<const uint4*>(fresh + src * stride + c * 16);
-    }
-#pragma unroll
-    for (int k = 0; k < PASSES; ++k) {
-      if (k * ROWS + lr >= n) continue;
-      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 4) {
-          const float a = fabsf(__uint_as_float(w[e]));
-          if (a < INFINITY) amax = fmaxf(amax, a);
-        } else {
-          const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-          if (lo < INFINITY) amax = fmaxf(amax, lo);
-          if (hi < INFINITY) amax = fmaxf(amax, hi);
-        }
+      for (int k = 0; k < PASSES; ++k) {
+        const int r = r0 + k * RPP;
+        if (r >= n) continue;
+        const int i = i0 + r;
+        const int src = s.q_off + (i < N ? i : N + s_inv[i - N]);
+        x[k] = *reinterpret_cast<const uint4*>(fresh + src * stride + c * 16);
       }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (lane == 0) s_max[warp] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kC8Threads / 32; ++w) amax = fmaxf(amax, s_max[w]);
-    const float sc = fmaxf(scale_for(amax), s_old);
-    const float inv = 1.f / sc;  // a power of two, exact
-#pragma unroll
-    for (int k = 0; k < PASSES; ++k) {
-      const int r = k * ROWS + lr;
-      if (r >= n) continue;
-      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-      float f[VEC];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 4) {
-          f[e] = __uint_as_float(w[e]);
-        } else {
-          f[2 * e] = __uint_as_float(w[e] << 16);
-          f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
-      }
-      uint16_t q[VEC / 2];
-#pragma unroll
-      for (int e = 0; e < VEC; e += 2) {
-        // infinities become NaN (the conversion would clamp them to a finite code)
-        const float lo = fabsf(f[e]) < INFINITY ? f[e] * inv : NAN, hi = fabsf(f[e + 1]) < INFINITY ? f[e + 1] * inv : NAN;
-        q[e / 2] = f32_to_e4m3x2(lo, hi);
-      }
-      uint8_t* dst = cache + (o0 + r) * D + c * VEC;
-      if constexpr (VEC == 8) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
-      } else {
-        *reinterpret_cast<uint32_t*>(dst) = q[0] | (uint32_t)q[1] << 16;
-      }
-    }
-    if (o0 > 0 && sc > s_old) {
-      // the rows already there, 16 codes at a time
-      const float ratio = s_old * inv;
-      for (int v = threadIdx.x; v < o0 * D / 16; v += kC8Threads) {
-        uint4 raw = reinterpret_cast<const uint4*>(cache)[v];
-        uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      for (int k = 0; k < PASSES; ++k) {
+        if (r0 + k * RPP >= n) continue;
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t out = 0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t f2 = e4m3x2_to_f16x2((uint16_t)(w[e] >> (16 * h)));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
-            out |= (uint32_t)f32_to_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+          if constexpr (sizeof(T) == 4) {
+            const float a = fabsf(__uint_as_float(w[e]));
+            if (a < INFINITY) amax = fmaxf(amax, a);
+          } else {
+            const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+            if (lo < INFINITY) amax = fmaxf(amax, lo);
+            if (hi < INFINITY) amax = fmaxf(amax, hi);
           }
-          w[e] = out;
         }
-        reinterpret_cast<uint4*>(cache)[v] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (lane == 0) s_max[warp] = amax;
     }
-    if (threadIdx.x == 0) *scale = sc;
-    __syncthreads();  // s_inv, s_max are reused; every thread has read the old scale
+    __syncthreads();  // (every warp of the page has read its old scale, too)
+    if (mine) {
+      for (int w = 0; w < parts; ++w) amax = fmaxf(amax, s_max[warp - part + w]);
+      const float sc = fmaxf(scale_for(amax), s_old);
+      const float inv = 1.f / sc;  // a power of two, exact
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k) {
+        const int r = r0 + k * RPP;
+        if (r >= n) continue;
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        float f[VEC];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (sizeof(T) == 4) {
+            f[e] = __uint_as_float(w[e]);
+          } else {
+            f[2 * e] = __uint_as_float(w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+          }
+        }
+        uint16_t q[VEC / 2];
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          // infinities become NaN (the conversion would clamp them to a finite code)
+          const float lo = fabsf(f[e]) < INFINITY ? f[e] * inv : NAN, hi = fabsf(f[e + 1]) < INFINITY ? f[e + 1] * inv : NAN;
+          q[e / 2] = f32_to_e4m3x2(lo, hi);
+        }
+        uint8_t* dst = cache + (o0 + r) * D + c * VEC;
+        if constexpr (VEC == 8) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
+        } else {
+          *reinterpret_cast<uint32_t*>(dst) = q[0] | (uint32_t)q[1] << 16;
+        }
+      }
+      if (o0 > 0 && sc > s_old) {
+        // the rows already there, 16 codes at a time
+        const float ratio = s_old * inv;
+        for (int v = part * 32 + lane; v < o0 * D / 16; v += parts * 32) {
+          const uint4 raw = reinterpret_cast<const uint4*>(cache)[v];
+          uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t out = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t f2 = e4m3x2_to_f16x2((uint16_t)(w[e] >> (16 * h)));
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
+              out |= (uint32_t)f32_to_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+            }
+            w[e] = out;
+          }
+          reinterpret_cast<uint4*>(cache)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (part == 0 && lane == 0) *scale = sc;
+    }
+    __syncthreads();  // s_inv, s_max are reused
   }
 }
 
@@ -256,7 +267,8 @@ extern "C" ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream)
                   a->pages, a->seqs, a->tau, a->n_acc, a->new_len, a->dev_status, ks * es, vs * es, a->Hkv,
                   ilog2(a->page_size), a->n_pages, a->table_len, a->batch, a->total_rows, a->total_slots, a->max_new,
                   a->max_block, (int)(((long long)a->total_rows + a->page_size - 1) / a->page_size)};
-  const dim3 grid(p.chunks + (a->batch + 7) / 8, 2 * a->Hkv);
+  const int per_cta = (kC8Threads / 32) / (a->page_size / 16);  // heads of K or V per CTA
+  const dim3 grid(p.chunks + (a->batch + 7) / 8, (2 * a->Hkv + per_cta - 1) / per_cta);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->dtype == SSV_BF16)

@@ -11,11 +11,15 @@
 // Angles: theta_i / (2 pi) is given as a 64-bit fixed-point fraction F_i of a
 // turn; pos * F_i mod 2^64 is the angle mod one turn exactly, in one integer
 // multiplication (the fp64 pipe of this part is far slower).  Error: that of F_i,
-// 2^-53 relative, times pos -- 3e-9 turns at position 2^24 -- and the
+// at most 3 * 2^-53, times pos -- 6e-9 turns at position 2^24 -- and the
 // rounding of the fraction to fp32.
 //
-// Bound by HBM.  A CTA takes kRows rows (one in a small batch, so that all SMs
-// load); the first loads are issued before the positions are known.
+// Bound by HBM.  A lane holds one 16-byte chunk of either half; the lanes of a
+// warp are 32 / CHUNKS rows of one head, so that a lane's cosines, sines and
+// weights serve all heads of its row, and a CTA's eight warps take every eighth
+// head.  In a small batch (fewer rows than fill the SMs) a CTA has one row, and a
+// warp 32 / CHUNKS heads of it.  The first loads are issued before the positions
+// are known.
 #include "ssv_internal.cuh"
 #include "paged.cuh"
 
@@ -24,9 +28,8 @@
 namespace ssv {
 namespace {
 
-constexpr int kNormRows = 4;
-constexpr int kNormThreads = 256;
-constexpr int kNormPre = 5;  // items per thread in flight
+constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
+constexpr int kNormPre = 5;  // heads per thread in flight
 
 struct NormTheta {
   uint64_t turn[64];  // theta_i / (2 pi) in units of 2^-64 turns
@@ -99,40 +102,37 @@ __device__ __forceinline__ int row_position(const NormParams& p, const ssv_seq& 
   return pos;
 }
 
-template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kNormThreads, 4)
+template <typename T, int D, bool kOneRow>
+__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 2 : 3)
 norm_rope_kernel(const NormParams p, const __grid_constant__ NormTheta th) {
-  constexpr int HALF = D / 2, VEC = kVec<T>, CHUNKS = HALF / VEC;
-  __shared__ float s_cos[ROWS][HALF], s_sin[ROWS][HALF];
+  constexpr int HALF = D / 2, VEC = kVec<T>, CHUNKS = HALF / VEC, GROUPS = 32 / CHUNKS;
+  constexpr int ROWS = kOneRow ? 1 : GROUPS;
+  constexpr int STEP = kOneRow ? kNormWarps * GROUPS : kNormWarps;  // heads between two of a lane's
+  __shared__ __align__(16) float s_cos[ROWS][HALF], s_sin[ROWS][HALF];
   __shared__ int s_pos[ROWS];
   __shared__ ssv_seq s_seq[kNormThreads];
   pdl_wait();  // the rows come from the kernel before this one
   pdl_trigger();
-  const int row0 = blockIdx.x * ROWS, heads = p.Hq + p.Hkv, items = ROWS * heads * CHUNKS;
-  const int ch = threadIdx.x % CHUNKS;  // the same for all of a thread's items
-  // item -> local row lr, head hh of the row (queries, then keys)
-  auto place = [&](int it, int& lr, int& hh) -> bool {
-    hh = (it / CHUNKS) % heads;
-    lr = it / (CHUNKS * heads);
-    return it < items && row0 + lr < p.total_rows;
-  };
-  auto in_at = [&](int lr, int hh) -> const T* {
-    const int64_t row = row0 + lr;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = lane % CHUNKS, g = lane / CHUNKS;
+  const int row0 = blockIdx.x * ROWS, lr = kOneRow ? 0 : g, heads = p.Hq + p.Hkv;
+  const int64_t row = row0 + lr;
+  const bool here = row < p.total_rows;
+  const int head0 = kOneRow ? warp * GROUPS + g : warp;
+  auto in_at = [&](int hh) -> const T* {
     return (hh < p.Hq ? static_cast<const T*>(p.q_in) + row * p.qis + hh * D
                       : static_cast<const T*>(p.k_in) + row * p.kis + (hh - p.Hq) * D) + ch * VEC;
   };
-  auto out_at = [&](int lr, int hh) -> T* {
-    const int64_t row = row0 + lr;
+  auto out_at = [&](int hh) -> T* {
     return (hh < p.Hq ? static_cast<T*>(p.q_out) + row * p.qos + hh * D
                       : static_cast<T*>(p.k_out) + row * p.kos + (hh - p.Hq) * D) + ch * VEC;
   };
   uint4 ra[kNormPre], rb[kNormPre];
-  auto fetch = [&](int it0) {
+  auto fetch = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kNormPre; ++k) {
-      int lr, hh;
-      if (place(it0 + k * kNormThreads, lr, hh)) {
-        const T* x = in_at(lr, hh);
+      const int hh = h0 + k * STEP;
+      if (here && hh < heads) {
+        const T* x = in_at(hh);
         ra[k] = *reinterpret_cast<const uint4*>(x);
         rb[k] = *reinterpret_cast<const uint4*>(x + HALF);
       } else {
@@ -140,56 +140,61 @@ norm_rope_kernel(const NormParams p, const __grid_constant__ NormTheta th) {
       }
     }
   };
-  fetch(threadIdx.x);
+  fetch(head0);
+  const T *wq = static_cast<const T*>(p.q_w) + ch * VEC, *wk = static_cast<const T*>(p.k_w) + ch * VEC;
+  const uint4 wq1 = __ldg(reinterpret_cast<const uint4*>(wq)), wq2 = __ldg(reinterpret_cast<const uint4*>(wq + HALF));
+  const uint4 wk1 = __ldg(reinterpret_cast<const uint4*>(wk)), wk2 = __ldg(reinterpret_cast<const uint4*>(wk + HALF));
   const bool table = p.batch <= kNormThreads;
   if (table && threadIdx.x < p.batch) s_seq[threadIdx.x] = p.seqs[threadIdx.x];
   __syncthreads();
   if (threadIdx.x < ROWS) {
-    const int row = row0 + threadIdx.x;
+    const int r = row0 + threadIdx.x;
     int pos = -1;
-    if (row < p.total_rows) {
-      const int b = find_seq_by_row(table ? s_seq : p.seqs, p.batch, row);
-      if (b >= 0) pos = row_position(p, table ? s_seq[b] : p.seqs[b], row);
+    if (r < p.total_rows) {
+      const int b = find_seq_by_row(table ? s_seq : p.seqs, p.batch, r);
+      if (b >= 0) pos = row_position(p, table ? s_seq[b] : p.seqs[b], r);
     }
     s_pos[threadIdx.x] = pos;
   }
   __syncthreads();
   for (int t = threadIdx.x; t < ROWS * HALF; t += kNormThreads) {
-    const int lr = t / HALF, i = t % HALF;
+    const int r = t / HALF, i = t % HALF;
     // the angle mod one turn, as a signed fraction of half a turn
-    const uint64_t a = (uint64_t)(uint32_t)max(s_pos[lr], 0) * th.turn[i];
-    sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s_sin[lr][i], &s_cos[lr][i]);
+    const uint64_t a = (uint64_t)(uint32_t)max(s_pos[r], 0) * th.turn[i];
+    sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s_sin[r][i], &s_cos[r][i]);
   }
   __syncthreads();
-  for (int it0 = threadIdx.x; it0 - (int)threadIdx.x < items; it0 += kNormPre * kNormThreads) {
-    if (it0 >= kNormPre * kNormThreads) fetch(it0);
+  const bool live = here && s_pos[lr] >= 0;
+  float c[VEC], s[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; v += 4) {
+    *reinterpret_cast<float4*>(c + v) = *reinterpret_cast<const float4*>(&s_cos[lr][ch * VEC + v]);
+    *reinterpret_cast<float4*>(s + v) = *reinterpret_cast<const float4*>(&s_sin[lr][ch * VEC + v]);
+  }
+#pragma unroll 1
+  for (int h0 = head0; h0 - head0 < heads; h0 += kNormPre * STEP) {
+    if (h0 != head0) fetch(h0);
 #pragma unroll
     for (int k = 0; k < kNormPre; ++k) {
-      const int it = it0 + k * kNormThreads;
-      if (it - (int)threadIdx.x >= items) break;  // CTA-uniform
-      int lr, hh;
-      const bool here = place(it, lr, hh);
-      float x1[VEC], x2[VEC], ss = 0.f;
+      const int hh = h0 + k * STEP;
+      float x1[VEC], x2[VEC], w1[VEC], w2[VEC], ss = 0.f;
       widen<T>(ra[k], x1);
       widen<T>(rb[k], x2);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) ss = fmaf(x1[v], x1[v], fmaf(x2[v], x2[v], ss));
 #pragma unroll
       for (int o = CHUNKS / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (!here || s_pos[lr] < 0) continue;
+      if (!live || hh >= heads) continue;
       const float r = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-      const T* w = static_cast<const T*>(hh < p.Hq ? p.q_w : p.k_w) + ch * VEC;
-      float w1[VEC], w2[VEC];
-      widen<T>(__ldg(reinterpret_cast<const uint4*>(w)), w1);
-      widen<T>(__ldg(reinterpret_cast<const uint4*>(w + HALF)), w2);
+      widen<T>(hh < p.Hq ? wq1 : wk1, w1);
+      widen<T>(hh < p.Hq ? wq2 : wk2, w2);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float c = s_cos[lr][ch * VEC + v], s = s_sin[lr][ch * VEC + v];
         const float y1 = x1[v] * r * w1[v], y2 = x2[v] * r * w2[v];
-        x1[v] = y1 * c - y2 * s;
-        x2[v] = y2 * c + y1 * s;
+        x1[v] = y1 * c[v] - y2 * s[v];
+        x2[v] = y2 * c[v] + y1 * s[v];
       }
-      T* o = out_at(lr, hh);
+      T* o = out_at(hh);
       *reinterpret_cast<uint4*>(o) = narrow<T>(x1);
       *reinterpret_cast<uint4*>(o + HALF) = narrow<T>(x2);
     }
@@ -198,14 +203,15 @@ norm_rope_kernel(const NormParams p, const __grid_constant__ NormTheta th) {
 
 template <typename T, int D>
 cudaError_t launch_norm(const NormParams& p, const NormTheta& th, cudaStream_t st) {
+  constexpr int ROWS = 32 / (D / 2 / kVec<T>);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if ((long long)p.total_rows < (long long)kNormRows * sms)
-    return launch_pdl(norm_rope_kernel<T, D, 1>, dim3(p.total_rows), dim3(kNormThreads), 0, st, p, th);
-  return launch_pdl(norm_rope_kernel<T, D, kNormRows>, dim3((p.total_rows + kNormRows - 1) / kNormRows),
-                    dim3(kNormThreads), 0, st, p, th);
+  if ((long long)p.total_rows < (long long)ROWS * sms)
+    return launch_pdl(norm_rope_kernel<T, D, true>, dim3(p.total_rows), dim3(kNormThreads), 0, st, p, th);
+  return launch_pdl(norm_rope_kernel<T, D, false>, dim3((p.total_rows + ROWS - 1) / ROWS), dim3(kNormThreads), 0, st, p,
+                    th);
 }
 
 }  // namespace
@@ -221,7 +227,7 @@ extern "C" ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stre
   if (a->d != 64 && a->d != 128) return SSV_ERR_UNSUPPORTED;
   if (a->dtype != SSV_F32 && a->dtype != SSV_BF16) return SSV_ERR_INVALID;
   if (!(a->base > 1.0) || !isfinite(a->base) || !(a->eps >= 0.f) || !isfinite(a->eps)) return SSV_ERR_INVALID;
-  if ((long long)(a->Hq + (long long)a->Hkv) * a->d * kNormRows > 0x3fffffffLL) return SSV_ERR_INVALID;
+  if (((long long)a->Hq + a->Hkv) * a->d > 0x3fffffffLL) return SSV_ERR_INVALID;
   const int64_t es = a->dtype == SSV_BF16 ? 2 : 4, qw = (int64_t)a->Hq * a->d, kw = (int64_t)a->Hkv * a->d;
   NormParams p{a->q_in, a->k_in, a->q_weight, a->k_weight, a->q_out, a->k_out,
                a->q_in_stride ? a->q_in_stride : qw, a->k_in_stride ? a->k_in_stride : kw,
@@ -233,10 +239,10 @@ extern "C" ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stre
                        (uintptr_t)(p.kis * es) | (uintptr_t)(p.qos * es) | (uintptr_t)(p.kos * es);
   if (al & 15u) return SSV_ERR_INVALID;
   NormTheta th;
-  for (int i = 0; i < 64; ++i) {
-    const double turns = i < a->d / 2 ? pow(a->base, -2.0 * i / a->d) * 0.15915494309189535 : 0.0;  // / (2 pi)
-    th.turn[i] = (uint64_t)ldexp(turns, 64);
-  }
+  // theta_i / (2 pi) by repeated products: i roundings on a theta_i that falls, at most 3 * 2^-53 turns per position
+  const double ratio = pow(a->base, -2.0 / a->d);
+  double turns = 0.15915494309189535;
+  for (int i = 0; i < 64; ++i, turns *= ratio) th.turn[i] = i < a->d / 2 ? (uint64_t)(turns * 18446744073709551616.0) : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->dtype == SSV_BF16)

@@ -18,6 +18,8 @@
 #include "ssv_internal.cuh"
 #include "paged.cuh"
 
+#include <mutex>
+
 namespace ssv {
 namespace {
 
@@ -191,17 +193,27 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     p.pages[(size_t)b * p.max_pages + s_held[b] + (i - s_w[b])] = stack(A - 1 - i);
   }
   for (int i = n_free + tid; i < A - taken; i += step) p.free_list[i] = stack(i);
-  const int mask = (1 << p.ps_log2) - 1;
-  for (int row = tid; row < p.total_rows; row += step) {
-    const int b = last_le(s_q, n, row), j = row - s_q[b];
-    int slot = -1;
-    if (j < s_nb[b]) {
-      const int t = s_c[b] + j, idx = t >> p.ps_log2;
-      const int page = idx < s_held[b] ? p.pages[(size_t)b * p.max_pages + idx]
-                                       : stack(A - 1 - (s_w[b] + idx - s_held[b]));
-      slot = (page << p.ps_log2) + (t & mask);
+  // the slot map: one row per thread while that covers it, else four per thread and step (one search, then along
+  // the requests), so that their loads are in flight together
+  const int mask = (1 << p.ps_log2) - 1, per_row = p.total_rows > step ? 4 : 1;
+  for (int row = per_row * tid; row < p.total_rows; row += per_row * step) {
+    int b = last_le(s_q, n, row), slot[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= per_row) break;
+      while (b + 1 < n && s_q[b + 1] <= row + k) ++b;
+      const int j = row + k - s_q[b];
+      slot[k] = -1;
+      if (j < s_nb[b]) {
+        const int t = s_c[b] + j, idx = t >> p.ps_log2;
+        const int page = idx < s_held[b] ? p.pages[(size_t)b * p.max_pages + idx]
+                                         : stack(A - 1 - (s_w[b] + idx - s_held[b]));
+        slot[k] = (page << p.ps_log2) + (t & mask);
+      }
     }
-    p.slot_map[row] = slot;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < per_row && row + k < p.total_rows) p.slot_map[row + k] = slot[k];
   }
 }
 
@@ -239,8 +251,13 @@ extern "C" ssv_status ssv_page_plan(const ssv_page_plan_args* a, void* stream) {
                a->slot_map, a->slot_off, a->held_out, a->n_free_out, a->dev_status, a->batch, a->max_pages,
                ilog2(a->page_size), a->n_pages, a->total_rows};
   const size_t smem = sizeof(int) * 6 * (size_t)a->batch;
-  SSV_CUDA_CHECK(cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)(sizeof(int) * 6 * kPlanMaxBatch)));
+  static std::once_flag once;
+  static cudaError_t ready = cudaSuccess;
+  std::call_once(once, [] {
+    ready = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(sizeof(int) * 6 * kPlanMaxBatch));
+  });
+  SSV_CUDA_CHECK(ready);
   const int grid = min(152, max(1, (a->total_rows + kPlanRows - 1) / kPlanRows));
   const cudaError_t e =
       launch_pdl(page_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(stream), p);

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -534,34 +535,71 @@ def tree_accept(mode, T, logits, seqs, parent, pos, token, noise=None, noise_row
 # ---------------------------------------------------------------------------
 # the paged 8-bit KV cache
 # ---------------------------------------------------------------------------
+# A serving loop calls these once per layer and pass, and the smallest of their kernels take a few
+# microseconds: the argument block is packed in one go (the layout of the ctypes structure of the
+# same name) instead of field by field, and the stream is read by its handle.
+_CODES = {C.c_void_p: "P", C.c_int: "i", C.c_int32: "i", C.c_int64: "q", C.c_float: "f", C.c_double: "d"}
+
+
+def _packer(cls):
+    return struct.Struct("@" + "".join(_CODES[f] for _, f in cls._fields_)).pack
+
+
+_pack_plan, _pack_norm = _packer(PagePlanArgs), _packer(NormRopeArgs)
+_pack_attn, _pack_commit = _packer(AttnFp8Args), _packer(CommitFp8Args)
+_entries = {}
+
+
+def _entry(name: str, workspace: bool = False):
+    """Entry point `name` on packed argument blocks."""
+    f = _entries.get(name)
+    if f is None:
+        types = [C.c_char_p] + ([C.c_void_p, C.c_size_t] if workspace else []) + [C.c_void_p]
+        f = _entries[name] = C.CFUNCTYPE(C.c_int, *types)((name, lib()))
+    return f
+
+
+def _stream_of(stream, t) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
 def _rows_strided(t, what: str) -> int:
-    """Row stride (elements) of a [rows, heads, d] tensor whose heads are contiguous."""
-    s = t.stride()
-    if t.dim() != 3 or (t.shape[0] and (s[2] != 1 or (s[1] != t.shape[2] and t.shape[1] > 1))):
+    """Row stride (elements) of a [rows, heads, d] tensor whose heads are contiguous; 0: packed."""
+    if t.dim() != 3:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: [rows, heads, d]")
+    if t.is_contiguous():
+        return 0
+    (rows, heads, d), s = t.shape, t.stride()
+    if rows and (s[2] != 1 or (s[1] != d and heads > 1)):
         raise SsvError(SSV_ERR_INVALID, f"{what}: [rows, heads, d] with contiguous heads")
-    return s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return s[0] if rows > 1 else heads * d
 
 
 def _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what: str):
     """(Hkv, page_size, d, n_pages) of a paged e4m3 cache, checked."""
     torch = _torch()
+    shape = k_cache.shape
     for x in (k_cache, v_cache):
-        if x.dtype not in (torch.uint8, torch.float8_e4m3fn) or x.dim() != 4 or not x.is_contiguous():
+        if x.dtype not in (torch.uint8, torch.float8_e4m3fn) or x.dim() != 4 or not x.is_contiguous() or \
+                x.shape != shape:
             raise SsvError(SSV_ERR_INVALID, f"{what}: caches are contiguous e4m3 [n_pages, Hkv, page_size, d]")
-    n, hkv, ps, d = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise SsvError(SSV_ERR_INVALID, f"{what}: cache shapes differ")
+    n, hkv, ps, d = shape
     for x in (k_scale, v_scale):
-        if x.dtype != torch.float32 or tuple(x.shape) != (n, hkv) or not x.is_contiguous():
+        if x.dtype != torch.float32 or x.shape != (n, hkv) or not x.is_contiguous():
             raise SsvError(SSV_ERR_INVALID, f"{what}: scales are contiguous fp32 [n_pages, Hkv]")
-    _int32(what, pages)
     return hkv, ps, d, n
 
 
 def _int32(what: str, *tensors):
-    torch = _torch()
+    i32 = _torch().int32
     for t in tensors:
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+        if t is not None and (t.dtype != i32 or not t.is_contiguous()):
             raise SsvError(SSV_ERR_INVALID, f"{what}: index tensors are contiguous int32")
 
 
@@ -578,20 +616,21 @@ def page_plan(cache_len, new_len, block, held, pages, free_list, n_free, page_si
     batch = cache_len.shape[0]
     if pages.dim() != 2 or any(x.shape[0] != batch for x in (new_len, block, held, pages)) or n_free.numel() != 1:
         raise SsvError(SSV_ERR_INVALID, "ssv_page_plan: shapes")
+    total_rows = int(total_rows)
     if out is None:
-        dev = cache_len.device
-        # one allocation: the table, then the offsets, counts and slot map behind it
-        buf = torch.empty(8 * batch + 1 + int(total_rows), dtype=torch.int32, device=dev)
-        seqs, slot_off, held_out, n_out, slot_map = buf.split([6 * batch, batch, batch, 1, int(total_rows)])
+        # one allocation: the table, the offsets, the counts, the stack height, the slot map
+        seqs, slot_off, held_out, n_out, slot_map = torch.empty(
+            8 * batch + 1 + total_rows, dtype=torch.int32, device=cache_len.device).split_with_sizes(
+                [6 * batch, batch, batch, 1, total_rows])
         out = (seqs.view(batch, 6), slot_map, slot_off, held_out, n_out)
-    elif tuple(x.numel() for x in out) != (6 * batch, int(total_rows), batch, batch, 1):
+    elif tuple(x.numel() for x in out) != (6 * batch, total_rows, batch, batch, 1):
         raise SsvError(SSV_ERR_INVALID, "ssv_page_plan: output shapes")
     seqs, slot_map, slot_off, held_out, n_out = out
-    a = PagePlanArgs(cache_len.data_ptr(), new_len.data_ptr(), block.data_ptr(), held.data_ptr(), pages.data_ptr(),
-                     free_list.data_ptr(), n_free.data_ptr(), batch, pages.shape[1], int(page_size),
-                     free_list.shape[0], int(total_rows), seqs.data_ptr(), slot_map.data_ptr(), slot_off.data_ptr(),
-                     held_out.data_ptr(), n_out.data_ptr(), _ptr(dev_status))
-    _check(lib().ssv_page_plan(C.byref(a), _stream_ptr(stream)), "ssv_page_plan")
+    a = _pack_plan(cache_len.data_ptr(), new_len.data_ptr(), block.data_ptr(), held.data_ptr(), pages.data_ptr(),
+                   free_list.data_ptr(), n_free.data_ptr(), batch, pages.shape[1], int(page_size),
+                   free_list.shape[0], total_rows, seqs.data_ptr(), slot_map.data_ptr(), slot_off.data_ptr(),
+                   held_out.data_ptr(), n_out.data_ptr(), _addr(dev_status))
+    _check(_entry("ssv_page_plan")(a, _stream_of(stream, cache_len)), "ssv_page_plan")
     return out
 
 
@@ -603,40 +642,48 @@ def norm_rope_copy(q, k, q_weight, k_weight, batch: Batch, base: float = 10000.0
     Returns (q_out, k_out)."""
     q_out = q if q_out is None else q_out
     k_out = k if k_out is None else k_out
-    if q_out.shape != q.shape or k_out.shape != k.shape or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    if q.dim() != 3 or k.dim() != 3 or q_out.shape != q.shape or k_out.shape != k.shape or \
+            q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: shapes")
-    if any(x.dtype != q.dtype for x in (k, q_out, k_out, q_weight, k_weight)):
+    what = "ssv_norm_rope_copy"
+    dt = q.dtype
+    if k.dtype != dt or q_out.dtype != dt or k_out.dtype != dt or q_weight.dtype != dt or k_weight.dtype != dt:
         raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: one dtype")
-    if any(tuple(w.shape) != (q.shape[2],) or not w.is_contiguous() for w in (q_weight, k_weight)):
+    if q_weight.shape != q.shape[2:] or k_weight.shape != q.shape[2:] or not q_weight.is_contiguous() or \
+            not k_weight.is_contiguous():
         raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: weights are [d]")
-    _int32("ssv_norm_rope_copy", batch.dev, positions)
+    _int32(what, batch.dev, positions)
     if positions is not None and positions.shape[0] < q.shape[0]:
         raise SsvError(SSV_ERR_INVALID, "ssv_norm_rope_copy: one position per row")
-    what = "ssv_norm_rope_copy"
-    a = NormRopeArgs(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), q_weight.data_ptr(),
-                     k_weight.data_ptr(), _rows_strided(q, what), _rows_strided(k, what), _rows_strided(q_out, what),
-                     _rows_strided(k_out, what), _dtype_code(q), q.shape[1], k.shape[1], q.shape[2], float(eps),
-                     float(base), batch.dev.data_ptr(), batch.batch, q.shape[0], _ptr(positions), _ptr(dev_status))
-    _check(lib().ssv_norm_rope_copy(C.byref(a), _stream_ptr(stream)), what)
+    a = _pack_norm(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), q_weight.data_ptr(),
+                   k_weight.data_ptr(), _rows_strided(q, what), _rows_strided(k, what), _rows_strided(q_out, what),
+                   _rows_strided(k_out, what), _dtype_code(q), q.shape[1], k.shape[1], q.shape[2], eps, base,
+                   batch.dev.data_ptr(), batch.batch, q.shape[0], _addr(positions), _addr(dev_status))
+    _check(_entry(what)(a, _stream_of(stream, q)), what)
     return q_out, k_out
+
+
+def _attn_fp8_fields(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch, tau, scale, dev_status):
+    what = "ssv_verify_attn_fp8"
+    hkv, ps, d, n = _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what)
+    bf16, shape = _torch().bfloat16, q.shape
+    if q.dtype != bf16 or k_new.dtype != bf16 or v_new.dtype != bf16 or out.dtype != bf16:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: q, fresh rows and output are bf16")
+    if q.dim() != 3 or not q.is_contiguous() or not out.is_contiguous() or out.shape != shape or \
+            k_new.shape != (shape[0], hkv, d) or v_new.shape != k_new.shape or shape[2] != d:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
+    _int32(what, pages, batch.dev, tau)
+    return (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            pages.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(), _rows_strided(k_new, what),
+            _rows_strided(v_new, what), shape[1], hkv, d, ps, n, pages.numel(), scale, batch.dev.data_ptr(),
+            batch.batch, tau.data_ptr(), shape[0], tau.shape[0], batch.max_cache, batch.max_new, batch.max_block,
+            _addr(dev_status))
 
 
 def attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch: Batch, tau,
                   scale: float = 0.0, dev_status=None):
-    torch = _torch()
-    what = "ssv_verify_attn_fp8"
-    hkv, ps, d, n = _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what)
-    if any(x.dtype != torch.bfloat16 for x in (q, k_new, v_new, out)):
-        raise SsvError(SSV_ERR_INVALID, f"{what}: q, fresh rows and output are bf16")
-    if q.dim() != 3 or not q.is_contiguous() or not out.is_contiguous() or out.shape != q.shape or \
-            tuple(k_new.shape) != (q.shape[0], hkv, d) or v_new.shape != k_new.shape or q.shape[2] != d:
-        raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
-    _int32(what, batch.dev, tau)
-    return AttnFp8Args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                       pages.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(),
-                       _rows_strided(k_new, what), _rows_strided(v_new, what), q.shape[1], hkv, d, ps, n,
-                       pages.numel(), float(scale), batch.dev.data_ptr(), batch.batch, tau.data_ptr(), q.shape[0],
-                       tau.shape[0], batch.max_cache, batch.max_new, batch.max_block, _ptr(dev_status))
+    return AttnFp8Args(*_attn_fp8_fields(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch, tau,
+                                         float(scale), dev_status))
 
 
 def verify_attn_fp8_workspace_bytes(args: AttnFp8Args) -> int:
@@ -659,10 +706,12 @@ def verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, 
     torch = _torch()
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    a = attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch, tau, scale, dev_status)
-    ws = workspace if workspace is not None else _workspace(verify_attn_fp8_workspace_bytes(a), q.device)
-    _check(lib().ssv_verify_attn_fp8(C.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_ptr(stream)),
-           "ssv_verify_attn_fp8")
+    a = _attn_fp8_fields(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch, tau, float(scale),
+                         dev_status)
+    ws = workspace if workspace is not None else \
+        _workspace(verify_attn_fp8_workspace_bytes(AttnFp8Args(*a)), q.device)
+    _check(_entry("ssv_verify_attn_fp8", True)(_pack_attn(*a), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                               _stream_of(stream, q)), "ssv_verify_attn_fp8")
     return out
 
 
@@ -674,19 +723,20 @@ def commit_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch: B
     torch = _torch()
     what = "ssv_commit_fp8"
     hkv, ps, d, n = _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what)
-    if k_new.dtype != v_new.dtype or tuple(k_new.shape[1:]) != (hkv, d) or v_new.shape != k_new.shape:
+    rows = k_new.shape[0]
+    if k_new.dtype != v_new.dtype or k_new.shape != (rows, hkv, d) or v_new.shape != k_new.shape:
         raise SsvError(SSV_ERR_INVALID, f"{what}: fresh rows")
-    _int32(what, batch.dev, tau, n_acc, new_len)
+    _int32(what, pages, batch.dev, tau, n_acc, new_len)
     if n_acc.shape[0] != batch.batch or (new_len is not None and new_len.shape[0] != batch.batch):
         raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
     if new_len is None:
         new_len = torch.empty(batch.batch, dtype=torch.int32, device=k_new.device)
-    a = CommitFp8Args(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                      v_scale.data_ptr(), pages.data_ptr(), _rows_strided(k_new, what), _rows_strided(v_new, what),
-                      _dtype_code(k_new), hkv, d, ps, n, pages.numel(), batch.dev.data_ptr(), batch.batch,
-                      tau.data_ptr(), n_acc.data_ptr(), new_len.data_ptr(), k_new.shape[0], tau.shape[0],
-                      batch.max_new, batch.max_block, _ptr(dev_status))
-    _check(lib().ssv_commit_fp8(C.byref(a), _stream_ptr(stream)), what)
+    a = _pack_commit(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                     v_scale.data_ptr(), pages.data_ptr(), _rows_strided(k_new, what), _rows_strided(v_new, what),
+                     _dtype_code(k_new), hkv, d, ps, n, pages.numel(), batch.dev.data_ptr(), batch.batch,
+                     tau.data_ptr(), n_acc.data_ptr(), new_len.data_ptr(), rows, tau.shape[0], batch.max_new,
+                     batch.max_block, _addr(dev_status))
+    _check(_entry(what)(a, _stream_of(stream, k_new)), what)
     return new_len
 
 

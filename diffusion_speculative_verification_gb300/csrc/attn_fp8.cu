@@ -140,8 +140,7 @@ struct Fp8Work {
 // Per head: U units of total cost Wc dealt to Pe CTAs; this CTA's head g and
 // its blocks [begin, end), which start at block k0 of unit u0.
 struct PlanHdr {
-  long long Wc;
-  int U, Pe, g, begin, end, u0, k0;
+  int Wc, U, Pe, g, begin, end, u0, k0;
 };
 
 template <int MT>
@@ -168,6 +167,8 @@ struct Unit {
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+// floor(r c / n) of the 32-bit costs c of a head, 0 <= r <= n: rank r's range starts there
+__device__ __forceinline__ int cost_start(int r, int c, int n) { return r * (c / n) + r * (c % n) / n; }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -271,7 +272,7 @@ __device__ __forceinline__ void commit_elect(uint32_t bar) {
 }
 // 32 lanes x 16 columns and the largest of each lane's 16 values
 __device__ __forceinline__ float tmem_max16(uint32_t taddr) {
-  uint32_t r[16];
+  [[maybe_unused]] uint32_t r[16];
   float mx;
   asm volatile(
       "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -375,10 +376,12 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       h.Pe = ph;
       h.g = cta % p.Hkv;
       h.Wc = carryC;
+      // Ranks run against the CTAs' order.  A merge waits on higher ranks, so on CTAs that were dispatched before
+      // the waiting one: where other kernels hold some of the SMs it still ends.
       // unit u occupies the costs [c_u, c_u + kSegCost + w n_u), its i-th block sits at
       // c_u + kSegCost + w i; rank r owns the blocks in [r Wc / Pe, (r + 1) Wc / Pe).
       // First block at or after cost c, as (block, unit, offset in the unit):
-      auto locate = [&](long long c, int& u_out, int& k_out) -> int {
+      auto locate = [&](int c, int& u_out, int& k_out) -> int {
         int lo = 0, hi = p.batch - 1, b = 0;
         while (lo <= hi) {
           const int mid = (lo + hi) >> 1;
@@ -387,40 +390,41 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         const ssv_seq s = p.seqs[b];
         const int rows = s.new_len + 2 * s.block;
         int xs = s_prefB[b], uu = s_prefU[b];
-        long long cu = s_prefC[b];
+        int cu = s_prefC[b];
         for (int t = 0;; ++t, ++uu) {
           const int nb = blocks_of(s.cache_len, s.new_len, rows, t * UR), w = cost_of(rows, t * UR);
-          if (t >= s_ntile[b] - 1 || cu + kSegCost + (long long)w * nb > c) {
-            const long long dd = c - cu - kSegCost;
-            const int i = dd <= 0 ? 0 : (int)min((dd + w - 1) / w, (long long)nb);
+          if (t >= s_ntile[b] - 1 || cu + kSegCost + w * nb > c) {
+            const int dd = c - cu - kSegCost;
+            const int i = dd <= 0 ? 0 : min(w == kBlock2 ? cdiv(dd, kBlock2) : cdiv(dd, kBlock1), nb);
             u_out = (i == nb) ? uu + 1 : uu;
             k_out = (i == nb) ? 0 : i;
             return xs + i;
           }
           xs += nb;
-          cu += kSegCost + (long long)w * nb;
+          cu += kSegCost + w * nb;
         }
       };
-      const int r = cta / p.Hkv;
+      const int r = ph - 1 - cta / p.Hkv;
       h.begin = h.end = h.u0 = h.k0 = 0;
       if (cta < ph * p.Hkv && carryB > 0) {
         int u1, k1;
-        h.begin = locate(((long long)r * h.Wc) / ph, h.u0, h.k0);
-        h.end = (r + 1 == ph) ? carryB : locate(((long long)(r + 1) * h.Wc) / ph, u1, k1);
+        h.begin = locate(cost_start(r, carryC, ph), h.u0, h.k0);
+        h.end = (r + 1 == ph) ? carryB : locate(cost_start(r + 1, carryC, ph), u1, k1);
       }
       *plan = h;
-      *abort = 0;
-      for (uint32_t i = 0; i < B_COUNT; ++i) {
-        uint32_t n = 1;
-        if (i >= B_R_EMPTY && i < B_V_EMPTY) n = kConv;
-        if (i >= B_C_EMPTY && i < B_Q_FULL) n = kSoft + kConv;
-        if (i == B_O_FREE) n = kSoft;
-        if (i == B_P_FULL || i == B_P_FULL + 1 || i == B_ML_FULL) n = 4;
-        mbar_init(bar(i), n);
-      }
-      fence_mbar_init();
     }
-    __syncwarp();
+  } else if (warp == 1) {
+    for (uint32_t i = lane; i < B_COUNT; i += 32) {
+      uint32_t n = 1;
+      if (i >= B_R_EMPTY && i < B_V_EMPTY) n = kConv;
+      if (i >= B_C_EMPTY && i < B_Q_FULL) n = kSoft + kConv;
+      if (i == B_O_FREE) n = kSoft;
+      if (i == B_P_FULL || i == B_P_FULL + 1 || i == B_ML_FULL) n = 4;
+      mbar_init(bar(i), n);
+    }
+    fence_mbar_init();
+    if (lane == 0) *abort = 0;
+  } else if (warp == 2) {
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
   }
   tc_fence_before();
@@ -429,8 +433,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   const int begin = plan->begin, end = plan->end, Ph = plan->Pe, Uh = plan->U, gh = plan->g;
-  const long long Wc = plan->Wc;
-  const int rank = cta / p.Hkv;
+  const int Wc = plan->Wc;
+  const int rank = Ph - 1 - cta / p.Hkv;
 
   auto seq_of = [&](int u) -> int {
     int lo = 0, hi = p.batch - 1, b = 0;
@@ -455,21 +459,20 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     x.full_new = (x.row0 < x.N) ? (x.row0 + 1) : x.N;  // fresh keys that every row sees
     return x;
   };
-  auto cost_start = [&](int r) -> long long { return ((long long)r * Wc) / Ph; };
-  auto owner_at = [&](long long c) -> int {  // rank owning the block at cost c
-    int r = (int)((c * Ph) / (Wc > 0 ? Wc : 1));
+  auto owner_at = [&](int c) -> int {  // rank owning the block at cost c
+    int r = (int)((float)c / (float)max(Wc, 1) * (float)Ph);
     r = min(max(r, 0), Ph - 1);
-    while (r + 1 < Ph && cost_start(r + 1) <= c) ++r;
-    while (r > 0 && cost_start(r) > c) --r;
+    while (r + 1 < Ph && cost_start(r + 1, Wc, Ph) <= c) ++r;
+    while (r > 0 && cost_start(r, Wc, Ph) > c) --r;
     return r;
   };
-  auto unit_cost = [&](int u) -> long long {  // cost at which unit u starts
+  auto unit_cost = [&](int u) -> int {  // cost at which unit u starts
     const int b = seq_of(u);
     const ssv_seq s = p.seqs[b];
     const int rows = s.new_len + 2 * s.block;
-    long long c = s_prefC[b];
+    int c = s_prefC[b];
     for (int t = 0; t < u - s_prefU[b]; ++t)
-      c += kSegCost + (long long)cost_of(rows, t * UR) * blocks_of(s.cache_len, s.new_len, rows, t * UR);
+      c += kSegCost + cost_of(rows, t * UR) * blocks_of(s.cache_len, s.new_len, rows, t * UR);
     return c;
   };
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
@@ -1156,9 +1159,9 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           } else {
             // ---- a unit cut across ranks c_a .. c_b of the head: c_a holds its first block, at the end of
             // its own range, and merges; the others publish their partials and move on
-            const long long cu = unit_cost(u) + kSegCost;
+            const int cu = unit_cost(u) + kSegCost;
             const int c_a = owner_at(cu);
-            const int c_b = owner_at(cu + (long long)cost_of(x.rows, x.row0) * (x.nblocks - 1));
+            const int c_b = owner_at(cu + cost_of(x.rows, x.row0) * (x.nblocks - 1));
             int32_t* counter = work.cnt + (((size_t)gh * Uh + u) * MT + mt) * 4 + q4;
             auto slot_of = [&](int rr) -> size_t { return ((size_t)(rr * p.Hkv + gh) * MT + mt) * 128 + m; };
             if (rank != c_a) {
@@ -1231,7 +1234,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
   tc_fence_before();
   __syncthreads();
   if (*abort && threadIdx.x == 0) report(p.dev_status, SSV_ERR_TIMEOUT);
-  if (warp == 0) {
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }

@@ -37,7 +37,7 @@ struct Commit8Params {
   const int32_t *tau, *n_acc;
   int32_t *new_len, *dev_status;
   int64_t k_stride, v_stride;  // bytes
-  int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunks;
+  int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunks, groups;
 };
 
 // The checks of sequence s that need no loop, na its accepted stages.
@@ -71,9 +71,58 @@ __device__ __forceinline__ float scale_for(float amax) {
   return ldexpf(1.f, max(x - (f <= 0.875f ? 9 : 8), kScaleMin));
 }
 
+// sixteen bytes of fresh elements, as the integers of their bits
+template <typename T> struct Bits;
+template <> struct Bits<float> {
+  static constexpr uint32_t kInf = 0x7f800000u;
+  static __device__ __forceinline__ uint32_t max4(uint32_t top, const uint4& x) {
+    return max(max(max(top, x.x & 0x7fffffffu), x.y & 0x7fffffffu), max(x.z & 0x7fffffffu, x.w & 0x7fffffffu));
+  }
+  static __device__ __forceinline__ uint32_t max4_finite(uint32_t top, uint4& x) {
+    uint32_t* w = &x.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((w[e] & 0x7fffffffu) >= kInf) w[e] = 0x7fc00000u;
+      else top = max(top, w[e] & 0x7fffffffu);
+    }
+    return top;
+  }
+  static __device__ __forceinline__ uint32_t largest(uint32_t top) { return top; }
+  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
+  static __device__ __forceinline__ void pair(const uint32_t* w, int e, float& lo, float& hi) {
+    lo = __uint_as_float(w[2 * e]);
+    hi = __uint_as_float(w[2 * e + 1]);
+  }
+};
+template <> struct Bits<__nv_bfloat16> {  // two to a word
+  static constexpr uint32_t kInf = 0x7f80u;
+  static __device__ __forceinline__ uint32_t max4(uint32_t top, const uint4& x) {
+    return __vmaxu2(__vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu),
+                    __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  }
+  static __device__ __forceinline__ uint32_t max4_finite(uint32_t top, uint4& x) {
+    uint32_t* w = &x.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((w[e] & 0x7fffu) >= kInf) w[e] = (w[e] & 0xffff0000u) | 0x7fc0u;
+      else top = __vmaxu2(top, w[e] & 0x7fffu);
+      if ((w[e] >> 16 & 0x7fffu) >= kInf) w[e] = (w[e] & 0xffffu) | 0x7fc00000u;
+      else top = __vmaxu2(top, w[e] & 0x7fff0000u);
+    }
+    return top;
+  }
+  static __device__ __forceinline__ uint32_t largest(uint32_t top) { return max(top & 0xffffu, top >> 16); }
+  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
+  static __device__ __forceinline__ void pair(const uint32_t* w, int e, float& lo, float& hi) {
+    lo = __uint_as_float(w[e] << 16);
+    hi = __uint_as_float(w[e] & 0xffff0000u);
+  }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8_kernel(const Commit8Params p) {
   constexpr int VEC = 16 / (int)sizeof(T), LANES = D / VEC;  // lanes per row
+  using E = Bits<T>;
   constexpr int RPP = 32 / LANES, PASSES = 16 / RPP;         // rows per pass of a warp, passes over its sixteen
   __shared__ int s_lead[128], s_inv[64], s_nlead, s_na[kC8Threads];
   __shared__ float s_max[kC8Threads / 32];
@@ -81,10 +130,11 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8
   pdl_wait();  // n_acc and the fresh rows may come from the kernels before this one
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ps = 1 << p.ps_log2;
-  if ((int)blockIdx.x >= p.chunks) {
+  const int chunk = blockIdx.x / p.groups, group = blockIdx.x - chunk * p.groups;
+  if (chunk >= p.chunks) {
     // new lengths and statuses: one warp per sequence
-    const int b = (blockIdx.x - p.chunks) * (kC8Threads / 32) + warp;
-    if (b >= p.batch || blockIdx.y > 0) return;
+    const int b = ((int)blockIdx.x - p.chunks * p.groups) * (kC8Threads / 32) + warp;
+    if (b >= p.batch) return;
     const ssv_seq s = p.seqs[b];
     const int na = p.n_acc[b];
     int bad = 0;
@@ -108,7 +158,7 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8
   if (threadIdx.x == 0) s_nlead = 0;
   __syncthreads();
   if ((int)threadIdx.x < ps) {
-    const int row = blockIdx.x * ps + threadIdx.x;
+    const int row = chunk * ps + threadIdx.x;
     const int b = row < p.total_rows ? find_seq_by_row(table ? s_seq : p.seqs, p.batch, row) : -1;
     if (b >= 0) {
       const ssv_seq s = table ? s_seq[b] : p.seqs[b];
@@ -122,7 +172,7 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8
   __syncthreads();
   const int nlead = s_nlead;
   // this warp: rows [16 part, 16 part + 16) of head `head` of K or V
-  const int parts = ps >> 4, unit = blockIdx.y * ((kC8Threads / 32) / parts) + warp / parts, part = warp & (parts - 1);
+  const int parts = ps >> 4, unit = group * ((kC8Threads / 32) / parts) + warp / parts, part = warp & (parts - 1);
   const bool mine = unit < 2 * p.Hkv, is_v = unit >= p.Hkv;
   const int head = is_v ? unit - p.Hkv : unit;
   const uint8_t* fresh = (is_v ? p.v_new : p.k_new) + (int64_t)head * D * sizeof(T);
@@ -159,22 +209,20 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8
         const int src = s.q_off + (i < N ? i : N + s_inv[i - N]);
         x[k] = *reinterpret_cast<const uint4*>(fresh + src * stride + c * 16);
       }
+      // magnitudes as integers, which order alike; what is not finite lies above kInf
+      uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < PASSES; ++k) {
-        if (r0 + k * RPP >= n) continue;
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        if (r0 + k * RPP < n) top = E::max4(top, x[k]);
+      }
+      if (E::largest(top) >= E::kInf) {  // rare: such elements become NaN and do not count
+        top = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (sizeof(T) == 4) {
-            const float a = fabsf(__uint_as_float(w[e]));
-            if (a < INFINITY) amax = fmaxf(amax, a);
-          } else {
-            const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-            if (lo < INFINITY) amax = fmaxf(amax, lo);
-            if (hi < INFINITY) amax = fmaxf(amax, hi);
-          }
+        for (int k = 0; k < PASSES; ++k) {
+          if (r0 + k * RPP < n) top = E::max4_finite(top, x[k]);
         }
       }
+      amax = E::value(E::largest(top));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (lane == 0) s_max[warp] = amax;
@@ -189,22 +237,12 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8
         const int r = r0 + k * RPP;
         if (r >= n) continue;
         const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-        float f[VEC];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (sizeof(T) == 4) {
-            f[e] = __uint_as_float(w[e]);
-          } else {
-            f[2 * e] = __uint_as_float(w[e] << 16);
-            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-          }
-        }
         uint16_t q[VEC / 2];
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) {
-          // infinities become NaN (the conversion would clamp them to a finite code)
-          const float lo = fabsf(f[e]) < INFINITY ? f[e] * inv : NAN, hi = fabsf(f[e + 1]) < INFINITY ? f[e + 1] * inv : NAN;
-          q[e / 2] = f32_to_e4m3x2(lo, hi);
+        for (int e = 0; e < VEC / 2; ++e) {
+          float lo, hi;
+          E::pair(w, e, lo, hi);
+          q[e] = f32_to_e4m3x2(lo * inv, hi * inv);
         }
         uint8_t* dst = cache + (o0 + r) * D + c * VEC;
         if constexpr (VEC == 8) {
@@ -262,13 +300,16 @@ extern "C" ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream)
   const uintptr_t al = (uintptr_t)a->k_new | (uintptr_t)a->v_new | (uintptr_t)a->k_cache | (uintptr_t)a->v_cache |
                        (uintptr_t)(ks * es) | (uintptr_t)(vs * es);
   if (al & 15u) return SSV_ERR_INVALID;
+  const int per_cta = (kC8Threads / 32) / (a->page_size / 16);  // heads of K or V per CTA
   Commit8Params p{static_cast<const uint8_t*>(a->k_new), static_cast<const uint8_t*>(a->v_new),
                   static_cast<uint8_t*>(a->k_cache), static_cast<uint8_t*>(a->v_cache), a->k_scale, a->v_scale,
                   a->pages, a->seqs, a->tau, a->n_acc, a->new_len, a->dev_status, ks * es, vs * es, a->Hkv,
                   ilog2(a->page_size), a->n_pages, a->table_len, a->batch, a->total_rows, a->total_slots, a->max_new,
-                  a->max_block, (int)(((long long)a->total_rows + a->page_size - 1) / a->page_size)};
-  const int per_cta = (kC8Threads / 32) / (a->page_size / 16);  // heads of K or V per CTA
-  const dim3 grid(p.chunks + (a->batch + 7) / 8, (2 * a->Hkv + per_cta - 1) / per_cta);
+                  a->max_block, (int)(((long long)a->total_rows + a->page_size - 1) / a->page_size),
+                  (2 * a->Hkv + per_cta - 1) / per_cta};
+  const long long ctas = (long long)p.chunks * p.groups + (a->batch + 7) / 8;
+  if (ctas > 0x7fffffffLL) return SSV_ERR_INVALID;
+  const dim3 grid((unsigned)ctas);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->dtype == SSV_BF16)

@@ -14,9 +14,16 @@
 // the number of CTAs follows from total_rows alone, however ragged the batch.
 // Per leader, page_size / 16 warps take one (page, head): sixteen rows each, in
 // registers between the maximum and the rounding, so that each element is read
-// once and each code written once.  Bound by HBM for prompts, by latency
-// (sequences; table and stage map; rows: three dependent rounds) for a decode
-// pass, which is why a CTA's warps serve different heads of the same page.
+// once and each code written once.  Groups of one chunk are neighbours in the
+// grid: together they read whole packed rows.
+//
+// Bound: for prompts, HBM and the instructions around it.  4 x 8192 rows of 8
+// heads of 128, bf16: 38.5 us, 5.2 TB/s of the 6.8 TB/s that a copy reaches;
+// maxima taken on the integer bits two at a time, the addresses of whole prompt
+// pages stepped, and the look-ups shared by two groups took it there from 61 us.
+// For a decode pass, latency (sequences; table and stage map; rows: three
+// dependent rounds): 5 us for 16 sequences, which is why a CTA's warps serve
+// different heads of the same page.
 #include "ssv_internal.cuh"
 #include "paged.cuh"
 
@@ -26,6 +33,9 @@ namespace ssv {
 namespace {
 
 constexpr int kC8Threads = 256;
+// A CTA takes several groups of heads of its chunk, one after the other, while that many CTAs remain: three rounds of
+// four per SM.  A prompt of 4 x 8192 rows, 8 heads: 38.5 us with two groups per CTA, 43 us with one or four.
+constexpr int kC8Ctas = 3 * 4 * 152;
 constexpr int kScaleMin = -100;  // exponent of an all-zero page's scale
 
 struct Commit8Params {
@@ -37,7 +47,7 @@ struct Commit8Params {
   const int32_t *tau, *n_acc;
   int32_t *new_len, *dev_status;
   int64_t k_stride, v_stride;  // bytes
-  int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunks, groups;
+  int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunks, groups, ctas_y;
 };
 
 // The checks of sequence s that need no loop, na its accepted stages.
@@ -120,20 +130,21 @@ template <> struct Bits<__nv_bfloat16> {  // two to a word
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8_kernel(const Commit8Params p) {
+__global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 4 : 2) commit_fp8_kernel(const Commit8Params p) {
   constexpr int VEC = 16 / (int)sizeof(T), LANES = D / VEC;  // lanes per row
   using E = Bits<T>;
   constexpr int RPP = 32 / LANES, PASSES = 16 / RPP;         // rows per pass of a warp, passes over its sixteen
-  __shared__ int s_lead[128], s_inv[64], s_nlead, s_na[kC8Threads];
-  __shared__ float s_max[kC8Threads / 32];
+  __shared__ int2 s_lead[128];  // first row, sequence
+  __shared__ int s_inv[64], s_nlead, s_na[kC8Threads];
+  __shared__ float s_max[2][kC8Threads / 32];
   __shared__ ssv_seq s_seq[kC8Threads];
   pdl_wait();  // n_acc and the fresh rows may come from the kernels before this one
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ps = 1 << p.ps_log2;
-  const int chunk = blockIdx.x / p.groups, group = blockIdx.x - chunk * p.groups;
+  const int chunk = blockIdx.x / p.ctas_y, group = blockIdx.x - chunk * p.ctas_y;
   if (chunk >= p.chunks) {
     // new lengths and statuses: one warp per sequence
-    const int b = ((int)blockIdx.x - p.chunks * p.groups) * (kC8Threads / 32) + warp;
+    const int b = ((int)blockIdx.x - p.chunks * p.ctas_y) * (kC8Threads / 32) + warp;
     if (b >= p.batch) return;
     const ssv_seq s = p.seqs[b];
     const int na = p.n_acc[b];
@@ -166,20 +177,17 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8
       const int na = table ? s_na[b] : p.n_acc[b];
       if (!seq_idle(s) && commit8_sizes(p, s, na) && i < s.new_len + na &&
           (i == 0 || ((s.cache_len + i) & (ps - 1)) == 0))
-        s_lead[atomicAdd(&s_nlead, 1)] = row;
+        s_lead[atomicAdd(&s_nlead, 1)] = make_int2(row, b);
     }
   }
   __syncthreads();
   const int nlead = s_nlead;
   // this warp: rows [16 part, 16 part + 16) of head `head` of K or V
-  const int parts = ps >> 4, unit = group * ((kC8Threads / 32) / parts) + warp / parts, part = warp & (parts - 1);
-  const bool mine = unit < 2 * p.Hkv, is_v = unit >= p.Hkv;
-  const int head = is_v ? unit - p.Hkv : unit;
-  const uint8_t* fresh = (is_v ? p.v_new : p.k_new) + (int64_t)head * D * sizeof(T);
-  const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  const int parts = ps >> 4, per_cta = (kC8Threads / 32) / parts, part = warp & (parts - 1);
+  const int r0 = part * 16 + lane / LANES, c = lane % LANES;  // of the appended rows
+  int turn = 0;
   for (int l = 0; l < nlead; ++l) {
-    const int row = s_lead[l];
-    const int b = find_seq_by_row(table ? s_seq : p.seqs, p.batch, row);
+    const int row = s_lead[l].x, b = s_lead[l].y;
     const ssv_seq s = table ? s_seq[b] : p.seqs[b];
     const int N = s.new_len, B = s.block, na = table ? s_na[b] : p.n_acc[b], i0 = row - s.q_off;
     const int t0 = s.cache_len + i0, o0 = t0 & (ps - 1);            // first appended row of the page
@@ -193,87 +201,103 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 3 : 2) commit_fp8
     if (__syncthreads_or(bad)) continue;
     if ((int)threadIdx.x < B) s_inv[stage - 1] = threadIdx.x;  // slot of each stage
     __syncthreads();
-    const int64_t at = (int64_t)page * p.Hkv + head;
-    uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + at * ps * D;
-    float* scale = (is_v ? p.v_scale : p.k_scale) + at;
-    const int r0 = part * 16 + lane / LANES, c = lane % LANES;  // of the appended rows
-    uint4 x[PASSES];
-    float s_old = 0.f, amax = 0.f;
-    if (mine) {
-      if (o0 > 0) s_old = *scale;
+    // sixteen rows in order, as in all of a prompt but its ends: the addresses step
+    const bool prompt = part * 16 + 16 <= min(n, N - i0);
+    for (int y = group; y < p.groups; y += p.ctas_y, turn ^= 1) {
+      const int unit = y * per_cta + warp / parts;
+      const bool mine = unit < 2 * p.Hkv, is_v = unit >= p.Hkv;
+      const int head = is_v ? unit - p.Hkv : unit;
+      const int64_t at = (int64_t)page * p.Hkv + head;
+      uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + at * ps * D;
+      float* scale = (is_v ? p.v_scale : p.k_scale) + at;
+      uint4 x[PASSES];
+      float s_old = 0.f, amax = 0.f;
+      if (mine) {
+        const int64_t stride = is_v ? p.v_stride : p.k_stride;
+        const uint8_t* fresh = (is_v ? p.v_new : p.k_new) + (int64_t)head * D * sizeof(T) + c * 16 + s.q_off * stride;
+        if (o0 > 0) s_old = *scale;
+        if (prompt) {
+          fresh += (i0 + r0) * stride;
 #pragma unroll
-      for (int k = 0; k < PASSES; ++k) {
-        const int r = r0 + k * RPP;
-        if (r >= n) continue;
-        const int i = i0 + r;
-        const int src = s.q_off + (i < N ? i : N + s_inv[i - N]);
-        x[k] = *reinterpret_cast<const uint4*>(fresh + src * stride + c * 16);
-      }
-      // magnitudes as integers, which order alike; what is not finite lies above kInf
-      uint32_t top = 0;
+          for (int k = 0; k < PASSES; ++k) {
+            x[k] = __ldcs(reinterpret_cast<const uint4*>(fresh));
+            fresh += RPP * stride;
+          }
+        } else {
 #pragma unroll
-      for (int k = 0; k < PASSES; ++k) {
-        if (r0 + k * RPP < n) top = E::max4(top, x[k]);
-      }
-      if (E::largest(top) >= E::kInf) {  // rare: such elements become NaN and do not count
-        top = 0;
+          for (int k = 0; k < PASSES; ++k) {
+            const int r = r0 + k * RPP;
+            if (r >= n) continue;
+            const int i = i0 + r;
+            x[k] = *reinterpret_cast<const uint4*>(fresh + (i < N ? i : N + s_inv[i - N]) * stride);
+          }
+        }
+        // magnitudes as integers, which order alike; what is not finite lies above kInf
+        uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < PASSES; ++k) {
-          if (r0 + k * RPP < n) top = E::max4_finite(top, x[k]);
+          if (r0 + k * RPP < n) top = E::max4(top, x[k]);
         }
-      }
-      amax = E::value(E::largest(top));
+        if (E::largest(top) >= E::kInf) {  // rare: such elements become NaN and do not count
+          top = 0;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (lane == 0) s_max[warp] = amax;
-    }
-    __syncthreads();  // (every warp of the page has read its old scale, too)
-    if (mine) {
-      for (int w = 0; w < parts; ++w) amax = fmaxf(amax, s_max[warp - part + w]);
-      const float sc = fmaxf(scale_for(amax), s_old);
-      const float inv = 1.f / sc;  // a power of two, exact
-#pragma unroll
-      for (int k = 0; k < PASSES; ++k) {
-        const int r = r0 + k * RPP;
-        if (r >= n) continue;
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-        uint16_t q[VEC / 2];
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-          float lo, hi;
-          E::pair(w, e, lo, hi);
-          q[e] = f32_to_e4m3x2(lo * inv, hi * inv);
-        }
-        uint8_t* dst = cache + (o0 + r) * D + c * VEC;
-        if constexpr (VEC == 8) {
-          *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
-        } else {
-          *reinterpret_cast<uint32_t*>(dst) = q[0] | (uint32_t)q[1] << 16;
-        }
-      }
-      if (o0 > 0 && sc > s_old) {
-        // the rows already there, 16 codes at a time
-        const float ratio = s_old * inv;
-        for (int v = part * 32 + lane; v < o0 * D / 16; v += parts * 32) {
-          const uint4 raw = reinterpret_cast<const uint4*>(cache)[v];
-          uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t out = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t f2 = e4m3x2_to_f16x2((uint16_t)(w[e] >> (16 * h)));
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
-              out |= (uint32_t)f32_to_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
-            }
-            w[e] = out;
+          for (int k = 0; k < PASSES; ++k) {
+            if (r0 + k * RPP < n) top = E::max4_finite(top, x[k]);
           }
-          reinterpret_cast<uint4*>(cache)[v] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        amax = E::value(E::largest(top));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (lane == 0) s_max[turn][warp] = amax;
       }
-      if (part == 0 && lane == 0) *scale = sc;
+      __syncthreads();  // (every warp of the page has read its old scale, too)
+      if (mine) {
+        for (int w = 0; w < parts; ++w) amax = fmaxf(amax, s_max[turn][warp - part + w]);
+        const float sc = fmaxf(scale_for(amax), s_old);
+        const float inv = 1.f / sc;  // a power of two, exact
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) {
+          const int r = r0 + k * RPP;
+          if (r >= n) continue;
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint16_t q[VEC / 2];
+#pragma unroll
+          for (int e = 0; e < VEC / 2; ++e) {
+            float lo, hi;
+            E::pair(w, e, lo, hi);
+            q[e] = f32_to_e4m3x2(lo * inv, hi * inv);
+          }
+          uint8_t* dst = cache + (o0 + r) * D + c * VEC;
+          if constexpr (VEC == 8) {
+            *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
+          } else {
+            *reinterpret_cast<uint32_t*>(dst) = q[0] | (uint32_t)q[1] << 16;
+          }
+        }
+        if (o0 > 0 && sc > s_old) {
+          // the rows already there, 16 codes at a time
+          const float ratio = s_old * inv;
+          for (int v = part * 32 + lane; v < o0 * D / 16; v += parts * 32) {
+            const uint4 raw = reinterpret_cast<const uint4*>(cache)[v];
+            uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t out = 0;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t f2 = e4m3x2_to_f16x2((uint16_t)(w[e] >> (16 * h)));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
+                out |= (uint32_t)f32_to_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+              }
+              w[e] = out;
+            }
+            reinterpret_cast<uint4*>(cache)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (part == 0 && lane == 0) *scale = sc;
+      }
     }
-    __syncthreads();  // s_inv, s_max are reused
+    __syncthreads();  // s_inv is reused
   }
 }
 
@@ -306,8 +330,10 @@ extern "C" ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream)
                   a->pages, a->seqs, a->tau, a->n_acc, a->new_len, a->dev_status, ks * es, vs * es, a->Hkv,
                   ilog2(a->page_size), a->n_pages, a->table_len, a->batch, a->total_rows, a->total_slots, a->max_new,
                   a->max_block, (int)(((long long)a->total_rows + a->page_size - 1) / a->page_size),
-                  (2 * a->Hkv + per_cta - 1) / per_cta};
-  const long long ctas = (long long)p.chunks * p.groups + (a->batch + 7) / 8;
+                  (2 * a->Hkv + per_cta - 1) / per_cta, 0};
+  const long long turns = (long long)p.chunks * p.groups / kC8Ctas;
+  p.ctas_y = p.groups / (turns < 1 ? 1 : turns > p.groups ? p.groups : (int)turns);
+  const long long ctas = (long long)p.chunks * p.ctas_y + (a->batch + 7) / 8;
   if (ctas > 0x7fffffffLL) return SSV_ERR_INVALID;
   const dim3 grid((unsigned)ctas);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

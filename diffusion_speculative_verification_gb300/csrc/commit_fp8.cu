@@ -7,11 +7,11 @@
 //   already holds rows of the sequence;  codes = rn_e4m3(X / s), and the rows
 //   already there become rn_e4m3(code * s_old / s) when s grew.
 //
-// Work: one CTA per (chunk of page_size packed rows, group of heads of K or V).
-// A page is led by the first token appended to it; the tokens' append indices
-// i < N + n_acc are counted along the packed rows from q_off, so a chunk of
-// page_size rows holds one leader per page boundary or sequence start in it, and
-// the number of CTAs follows from total_rows alone, however ragged the batch.
+// Work: one CTA per (chunk of packed rows, groups of heads of K or V).  A page is
+// led by the first token appended to it; the tokens' append indices i < N + n_acc
+// are counted along the packed rows from q_off, so a chunk holds one leader per
+// page boundary or sequence start in it, and the number of CTAs follows from
+// total_rows alone, however ragged the batch.
 // Per leader, page_size / 16 warps take one (page, head): sixteen rows each, in
 // registers between the maximum and the rounding, so that each element is read
 // once and each code written once.  Groups of one chunk are neighbours in the
@@ -35,6 +35,9 @@ namespace {
 constexpr int kC8Threads = 256;
 // A CTA takes several groups of heads of its chunk, one after the other, while that many CTAs remain: three rounds of
 // four per SM.  A prompt of 4 x 8192 rows, 8 heads: 38.5 us with two groups per CTA, 43 us with one or four.
+// A chunk is a page's rows, or fewer (16 at least) while the CTAs stay within one per SM: pages are written one after the
+// other in a CTA.  11 sequences of one head, pages of 128: 15.8 us with chunks of a page, 7.1 us so.
+constexpr int kC8Few = 152;
 constexpr int kC8Ctas = 3 * 4 * 152;
 constexpr int kScaleMin = -100;  // exponent of an all-zero page's scale
 
@@ -47,7 +50,7 @@ struct Commit8Params {
   const int32_t *tau, *n_acc;
   int32_t *new_len, *dev_status;
   int64_t k_stride, v_stride;  // bytes
-  int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunks, groups, ctas_y;
+  int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunk_rows, chunks, groups, ctas_y;
 };
 
 // The checks of sequence s that need no loop, na its accepted stages.
@@ -168,8 +171,8 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 4 : 2) commit_fp8
   }
   if (threadIdx.x == 0) s_nlead = 0;
   __syncthreads();
-  if ((int)threadIdx.x < ps) {
-    const int row = chunk * ps + threadIdx.x;
+  if ((int)threadIdx.x < p.chunk_rows) {
+    const int row = chunk * p.chunk_rows + threadIdx.x;
     const int b = row < p.total_rows ? find_seq_by_row(table ? s_seq : p.seqs, p.batch, row) : -1;
     if (b >= 0) {
       const ssv_seq s = table ? s_seq[b] : p.seqs[b];
@@ -329,8 +332,11 @@ extern "C" ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream)
                   static_cast<uint8_t*>(a->k_cache), static_cast<uint8_t*>(a->v_cache), a->k_scale, a->v_scale,
                   a->pages, a->seqs, a->tau, a->n_acc, a->new_len, a->dev_status, ks * es, vs * es, a->Hkv,
                   ilog2(a->page_size), a->n_pages, a->table_len, a->batch, a->total_rows, a->total_slots, a->max_new,
-                  a->max_block, (int)(((long long)a->total_rows + a->page_size - 1) / a->page_size),
-                  (2 * a->Hkv + per_cta - 1) / per_cta, 0};
+                  a->max_block, 16, 0, (2 * a->Hkv + per_cta - 1) / per_cta, 0};
+  for (;; p.chunk_rows *= 2) {
+    p.chunks = (int)(((long long)a->total_rows + p.chunk_rows - 1) / p.chunk_rows);
+    if (p.chunk_rows == a->page_size || (long long)p.chunks * p.groups <= kC8Few) break;
+  }
   const long long turns = (long long)p.chunks * p.groups / kC8Ctas;
   p.ctas_y = p.groups / (turns < 1 ? 1 : turns > p.groups ? p.groups : (int)turns);
   const long long ctas = (long long)p.chunks * p.ctas_y + (a->batch + 7) / 8;

@@ -167,6 +167,18 @@ struct Unit {
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+// Bounded wait of a warp that has tried once: out of line, for the sake of the instruction cache (see above).
+__device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, volatile int* abort, long long budget) {
+  const long long t0 = clock64();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > budget)) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
 // floor(r c / n) of the 32-bit costs c of a head, 0 <= r <= n: rank r's range starts there
 __device__ __forceinline__ int cost_start(int r, int c, int n) { return r * (c / n) + r * (c % n) / n; }
 __device__ __forceinline__ float ex2(float x) {
@@ -476,8 +488,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     return c;
   };
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
-    const bool w = mbar_wait(b, parity, abort, wb);
-    return __all_sync(0xffffffffu, w);
+    return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) || warp_wait_more(b, parity, abort, wb);
   };
   // page of lane `lane` of window w (32 pages) of a segment that starts at block k and holds np pages:
   // -1 behind the last one, -2 where the table names none (reported; read as zeros)
@@ -588,18 +599,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     const uint64_t dq0 = smem_desc_sw128(sbase + C_::SM_Q, 16, 1024);
     const uint64_t dk0 = smem_desc_sw128(sbase + C_::SM_K, 16, 1024);
     const uint64_t dv0 = smem_desc_sw128(sbase + C_::SM_V, STAGE, 1024);
-    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-      if (__all_sync(0xffffffffu, mbar_test_wait(bar(b), parity))) return true;
-      const long long t0 = clock64();
-      while (true) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity))) return true;
-        if (__any_sync(0xffffffffu, *abort != 0)) return false;
-        if (__any_sync(0xffffffffu, clock64() - t0 > wb)) {
-          *abort = 1;
-          return false;
-        }
-      }
-    };
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool { return warp_wait(bar(b), parity); };
     while (run && remaining > 0) {
       const Unit x = decode(u);
       const int len = uni(min(x.nblocks - k, remaining)), cached = uni(min(max(x.cache_blocks - k, 0), len));

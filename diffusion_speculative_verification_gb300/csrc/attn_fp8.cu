@@ -248,34 +248,39 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
 //   gemm_q8: (hi + lo) K^T of e4m3 operands, hi at a, lo 1024 descriptor units behind it, both K-major SW128 like b
 //   gemm_qk: bf16 Q K^T, two 64-column halves of either operand 1024 units apart
 //   gemm_pv: P V, P in TMEM (two elements per column), V MN-major
-#define FP8_MMA8(FIRST, STEP)                                                                                    \
-  "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a, b;\n\t.reg .b32 ta;\n\telect.sync _|e, 0xffffffff;\n\t"                \
-  "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t" FIRST STEP "}"
-#define FP8_SS(KIND, OA, OB) \
-  "add.s64 a, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\t@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, q;\n\t"
-#define FP8_TS(OA, OB) \
-  "add.u32 ta, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %3, q;\n\t"
+__device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdE4m3), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdBf16), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
 __device__ __forceinline__ void gemm_q8(uint32_t d, uint64_t a, uint64_t b) {
-  asm volatile(FP8_MMA8("@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t",
-                        FP8_SS("f8f6f4", 2, 2) FP8_SS("f8f6f4", 4, 4) FP8_SS("f8f6f4", 6, 6) FP8_SS("f8f6f4", 1024, 0)
-                        FP8_SS("f8f6f4", 1026, 2) FP8_SS("f8f6f4", 1028, 4) FP8_SS("f8f6f4", 1030, 6))
-               ::"r"(d), "l"(a), "l"(b), "r"(kIdE4m3), "r"(0) : "memory");
+#pragma unroll
+  for (int s = 0; s < 8; ++s) mma_ss_f8(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s & 3) * 2, s);
 }
 __device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
-  asm volatile(FP8_MMA8("@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t",
-                        FP8_SS("f16", 2, 2) FP8_SS("f16", 4, 4) FP8_SS("f16", 6, 6) FP8_SS("f16", 1024, 1024)
-                        FP8_SS("f16", 1026, 1026) FP8_SS("f16", 1028, 1028) FP8_SS("f16", 1030, 1030))
-               ::"r"(d), "l"(a), "l"(b), "r"(kIdBf16), "r"(0) : "memory");
+#pragma unroll 1  // fresh blocks are few: less code
+  for (int s = 0; s < 8; ++s) mma_ss_bf16(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s >> 2) * 1024 + (s & 3) * 2, s);
 }
 __device__ __forceinline__ void gemm_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(FP8_MMA8("@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t",
-                        FP8_TS(8, 128) FP8_TS(16, 256) FP8_TS(24, 384) FP8_TS(32, 512) FP8_TS(40, 640) FP8_TS(48, 768)
-                        FP8_TS(56, 896))
-               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+#pragma unroll
+  for (int s = 0; s < 8; ++s) mma_ts(d, a + s * 8, b + s * 128, idesc, s | acc);
 }
-#undef FP8_MMA8
-#undef FP8_SS
-#undef FP8_TS
 __device__ __forceinline__ void commit_elect(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -907,26 +912,27 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           const bool is_cache = jj < cached, first = job == set;
           const int e = nc + jj;  // scales of the block
           // ---- the block's scales: factors of the scores of every 16 columns, the unit of O
-          float cf[8], unit_new = first ? 0.f : unit;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) cf[q] = cexp;
+          float unit_new = first ? 0.f : unit;
+          const float* sc = reinterpret_cast<const float*>(smem + C_::SM_SC) + (e % NSC) * SC;
           if (is_cache) {
             if (!warp_wait(bar(B_C_FULL + e % NSC), full_par(e, NSC))) { run = false; break; }
-            const float4* sc = reinterpret_cast<const float4*>(smem + C_::SM_SC) + (e % NSC) * (SC / 4);
-            const float4 c0 = sc[0], c1 = sc[1];
-            const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-            for (int q = 0; q < 8; ++q) cf[q] = fmaxf(rowf * c[q], 1.17549435e-38f);
-            unit_new = reinterpret_cast<const float*>(sc)[16];
-            __syncwarp();
-            // (a block that one set alone works on is given back by it for both)
-            if (lane == 0) mbar_arrive_n(bar(B_C_EMPTY + e % NSC), two ? 1 : 2);
+            unit_new = sc[16];
           }
+          auto factor = [&](int q) -> float {  // of columns [16 q, 16 q + 16)
+            return is_cache ? fmaxf(rowf * sc[q], 1.17549435e-38f) : cexp;
+          };
+          // (a block that one set alone works on is given back by it for both)
+          auto give_back = [&]() {
+            __syncwarp();
+            if (lane == 0) {
+              if (is_cache) mbar_arrive_n(bar(B_C_EMPTY + e % NSC), two ? 1 : 2);
+              mbar_arrive(bar(B_P_FULL + set));
+            }
+          };
           if (!warp_wait(bar(B_S_FULL + set), sph)) { run = false; break; }
           sph ^= 1u;
           if (!warp_active) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P_FULL + set));
+            give_back();
             continue;
           }
           tc_fence_after();
@@ -950,11 +956,6 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             if (lim_rows > 32 * q) v |= window32(tm, toff + 32 * q) & prefix32(lim_rows - 32 * q);
             return v;
           };
-          auto factor = [&](int q) -> float {  // cf[q], q not known when compiling
-            const float a = (q & 1) ? ((q & 2) ? cf[3] : cf[1]) : ((q & 2) ? cf[2] : cf[0]);
-            const float b = (q & 1) ? ((q & 2) ? cf[7] : cf[5]) : ((q & 2) ? cf[6] : cf[4]);
-            return (q & 4) ? b : a;
-          };
           const float shift = is_cache ? kWeight : kWeight - unit_new;  // P = exp2(x - m + shift)
           float lsum = 0.f;  // of P
           // ---- the row's maximum over the block
@@ -962,12 +963,14 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           if (full) {
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
-              float a[4];
+              float a[4], f[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) f[h] = factor(4 * g + h);
 #pragma unroll
               for (int h = 0; h < 4; ++h) a[h] = tmem_max16(tS + g * 64 + h * 16);
               tmem_wait_ld();
 #pragma unroll
-              for (int h = 0; h < 4; ++h) mx = fmaxf(mx, a[h] * (g ? cf[4 + h] : cf[h]));
+              for (int h = 0; h < 4; ++h) mx = fmaxf(mx, a[h] * f[h]);
             }
           } else {
 #pragma unroll 1
@@ -1002,45 +1005,45 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           }
           if (need) m_used = mx;
           const float off = shift - ((m_used == -INFINITY) ? 0.f : m_used);
-          // ---- P = exp2(x - m + shift) over S: chunk q reads S columns [32 q, 32 q + 32) and writes P columns
-          // [16 q, 16 q + 16), which lie in S columns already read
+          // ---- P = exp2(x - m + shift) over S: chunk q reads S columns [16 q, 16 q + 16) and writes P columns
+          // [8 q, 8 q + 8), which lie in S columns already read
           auto exps = [&](auto cache_tag) {
             constexpr bool kCache = decltype(cache_tag)::value;
             const uint64_t of2 = pack2(off, off);
             uint64_t lp0 = 0ull, lp1 = 0ull;
-            uint32_t b0[32], b1[32];
-            tmem_ld32(tS, b0);
+            uint32_t b0[16], b1[16];
+            tmem_ld16(tS, b0);
             tmem_wait_ld();
-            auto chunk = [&](int q, const uint32_t* cur, float ca, float cb) {
-              uint32_t pw[16];
+            auto chunk = [&](int q, const uint32_t* cur, float c) {
+              uint32_t pw[8];
+              const uint64_t cc2 = pack2(c, c);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float c = kCache ? (h ? cb : ca) : cexp;
-                const uint64_t cc2 = pack2(c, c);
-#pragma unroll
-                for (int v = 8 * h; v < 8 * h + 8; ++v) {
-                  float x0, x1;
-                  unpack2(ffma2(pack2(__uint_as_float(cur[2 * v]), __uint_as_float(cur[2 * v + 1])), cc2, of2), x0, x1);
-                  const float p0 = ex2(x0), p1 = ex2(x1);
-                  if constexpr (kCache) {
-                    const __half2 w = __floats2half2_rn(p0, p1);
-                    pw[v] = *reinterpret_cast<const uint32_t*>(&w);
-                  } else {
-                    const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
-                    pw[v] = *reinterpret_cast<const uint32_t*>(&w);
-                  }
-                  if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
+              for (int v = 0; v < 8; ++v) {
+                float x0, x1;
+                unpack2(ffma2(pack2(__uint_as_float(cur[2 * v]), __uint_as_float(cur[2 * v + 1])), cc2, of2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                if constexpr (kCache) {
+                  const __half2 w = __floats2half2_rn(p0, p1);
+                  pw[v] = *reinterpret_cast<const uint32_t*>(&w);
+                } else {
+                  const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
+                  pw[v] = *reinterpret_cast<const uint32_t*>(&w);
                 }
+                if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
               }
               tmem_wait_ld();  // the next chunk is here, so this one's P may go over it
-              tmem_st16(tS + q * 16, pw);
+              tmem_st8(tS + q * 8, pw);
             };
+            float c0 = factor(0), c1 = factor(1);
 #pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-              tmem_ld32(tS + (2 * g + 1) * 32, b1);
-              chunk(2 * g, b0, g ? cf[4] : cf[0], g ? cf[5] : cf[1]);
-              if (g == 0) tmem_ld32(tS + 64, b0);
-              chunk(2 * g + 1, b1, g ? cf[6] : cf[2], g ? cf[7] : cf[3]);
+            for (int q = 0; q < 8; q += 2) {
+              const float n0 = factor((q + 2) & 7), n1 = factor((q + 3) & 7);  // ahead of their use
+              tmem_ld16(tS + (q + 1) * 16, b1);
+              chunk(q, b0, c0);
+              if (q < 6) tmem_ld16(tS + (q + 2) * 16, b0);
+              chunk(q + 1, b1, c1);
+              c0 = n0;
+              c1 = n1;
             }
             float y0, y1;
             unpack2(fadd2(lp0, lp1), y0, y1);
@@ -1078,8 +1081,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           tmem_wait_st();
           l_sum += lsum;
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_P_FULL + set));
+          give_back();
         }
         nc += cached;
         if (!run) break;

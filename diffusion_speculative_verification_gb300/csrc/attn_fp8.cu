@@ -536,18 +536,21 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           }
           const int pg = __shfl_sync(0xffffffffu, pg0, (t0 + lane) & 31);
           const int row = pg >= 0 ? (pg * p.Hkv + gh) * ps : row_oob;
-          auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full) {
-            if (lane == 0) mbar_expect_tx(full, nb * ps * 128);
-            __syncwarp();
-            if (lane < nb) tma_load_2d(dst + lane * ps * 128, map, 0, row, full);
-          };
-          if (!take(B_K_EMPTY, NK)) { run = false; break; }
-          if (!(cta == 0 && n == p.fault_skip))  // test support: this key block's copy is left out
-            load(&maps.kc, sbase + C_::SM_K + (n % NK) * STAGE, bar(B_K_FULL + n % NK));
-          k_end = n + 1;
-          if (!take(B_R_EMPTY, C_::NR)) { run = false; break; }
-          load(&maps.vc, sbase + C_::SM_R + (n % C_::NR) * STAGE, bar(B_R_FULL + n % C_::NR));
-          v_end = n + 1;
+#pragma unroll 1
+          for (int v = 0; run && v < 2; ++v) {  // K, then V
+            const int S = v ? C_::NR : NK, st = n & (S - 1);
+            if (!take(v ? B_R_EMPTY : B_K_EMPTY, S)) { run = false; break; }
+            if (v || cta != 0 || n != p.fault_skip) {  // (test support: this key block's copy is left out)
+              const uint32_t full = bar((v ? B_R_FULL : B_K_FULL) + st);
+              if (lane == 0) mbar_expect_tx(full, nb * ps * 128);
+              __syncwarp();
+              if (lane < nb)
+                tma_load_2d(sbase + (v ? C_::SM_R : C_::SM_K) + st * STAGE + lane * ps * 128, v ? &maps.vc : &maps.kc, 0, row,
+                            full);
+            }
+            (v ? v_end : k_end) = n + 1;
+          }
+          if (!run) break;
           ++n;
         }
         // fresh rows: a 16-bit block takes two stages, from an even one on

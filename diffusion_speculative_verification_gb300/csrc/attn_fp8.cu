@@ -248,39 +248,38 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
 //   gemm_q8: (hi + lo) K^T of e4m3 operands, hi at a, lo 1024 descriptor units behind it, both K-major SW128 like b
 //   gemm_qk: bf16 Q K^T, two 64-column halves of either operand 1024 units apart
 //   gemm_pv: P V, P in TMEM (two elements per column), V MN-major
-__device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdE4m3), "r"(acc)
-      : "memory");
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
 }
-__device__ __forceinline__ void mma_ss_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdBf16), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
+#define FP8_NEXT(KIND, OA, OB) \
+  "add.s64 a, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\ttcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, q;\n\t"
 __device__ __forceinline__ void gemm_q8(uint32_t d, uint64_t a, uint64_t b) {
-#pragma unroll
-  for (int s = 0; s < 8; ++s) mma_ss_f8(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s & 3) * 2, s);
+  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+                 FP8_NEXT("f8f6f4", 2, 2) FP8_NEXT("f8f6f4", 4, 4) FP8_NEXT("f8f6f4", 6, 6) FP8_NEXT("f8f6f4", 1024, 0)
+                 FP8_NEXT("f8f6f4", 1026, 2) FP8_NEXT("f8f6f4", 1028, 4) FP8_NEXT("f8f6f4", 1030, 6) "}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(kIdE4m3) : "memory");
 }
 __device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
-#pragma unroll 1  // fresh blocks are few: less code
-  for (int s = 0; s < 8; ++s) mma_ss_bf16(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s >> 2) * 1024 + (s & 3) * 2, s);
+  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                 FP8_NEXT("f16", 2, 2) FP8_NEXT("f16", 4, 4) FP8_NEXT("f16", 6, 6) FP8_NEXT("f16", 1024, 1024)
+                 FP8_NEXT("f16", 1026, 1026) FP8_NEXT("f16", 1028, 1028) FP8_NEXT("f16", 1030, 1030) "}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(kIdBf16) : "memory");
 }
+#undef FP8_NEXT
+#define FP8_NEXT(OA, OB) \
+  "add.u32 a, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
 __device__ __forceinline__ void gemm_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-#pragma unroll
-  for (int s = 0; s < 8; ++s) mma_ts(d, a + s * 8, b + s * 128, idesc, s | acc);
+  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 FP8_NEXT(8, 128) FP8_NEXT(16, 256) FP8_NEXT(24, 384) FP8_NEXT(32, 512) FP8_NEXT(40, 640) FP8_NEXT(48, 768)
+                 FP8_NEXT(56, 896) "}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
+#undef FP8_NEXT
 __device__ __forceinline__ void commit_elect(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -493,7 +492,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     return c;
   };
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) || warp_wait_more(b, parity, abort, wb);
+    return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) || __all_sync(0xffffffffu, warp_wait_more(b, parity, abort, wb));
   };
   // page of lane `lane` of window w (32 pages) of a segment that starts at block k and holds np pages:
   // -1 behind the last one, -2 where the table names none (reported; read as zeros)
@@ -633,7 +632,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         }
         const uint64_t dq = dq0 + (two ? t : 0) * (2 * STAGE >> 4), dk = dk0 + (n % NK) * (STAGE >> 4);
         const uint64_t dv = dv0 + (nv & 1) * (2 * STAGE >> 4);
-        const uint32_t tS = tm + t * 128, k_empty = bar(B_K_EMPTY + n % NK), v_empty = bar(B_V_EMPTY + (nv & 1));
+        const uint32_t tS = tm + t * 128;
         const bool q_last = i == cached - 1 || i == len - 1;
         const uint32_t id_pv = (two ? j >> 1 : j) < cached ? kIdPvF16 : kIdPvBf16;
         if (j >= 0) {
@@ -642,27 +641,26 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             run = false;
             break;
           }
-          tc_fence_after();
-          gemm_pv(tS + TM_O, tS, dv, id_pv, j > 1 ? 1u : 0u);
           if (t) pph1 ^= 1u; else pph0 ^= 1u;
-        } else {
-          tc_fence_after();
         }
-        if (has_s) {
-          if (q8) gemm_q8(tS, dq, dk);
-          else gemm_qk(tS, dq, dk);
-          commit_elect(bar(B_S_FULL + t));
-          if (last) {
-            commit_elect(k_empty);
-            if (!q8) commit_elect(bar(B_K_EMPTY + (n + 1) % NK));
-            if (q_last) commit_elect(bar(B_Q_EMPTY));
-            n += q8 ? 1 : 2;
+        tc_fence_after();
+        if (elect_one()) {
+          if (j >= 0) gemm_pv(tS + TM_O, tS, dv, id_pv, j > 1 ? 1u : 0u);
+          if (has_s) {
+            if (q8) gemm_q8(tS, dq, dk);
+            else gemm_qk(tS, dq, dk);
+            mma_commit(bar(B_S_FULL + t));
+            if (last) {
+              mma_commit(bar(B_K_EMPTY + n % NK));
+              if (!q8) mma_commit(bar(B_K_EMPTY + (n + 1) % NK));
+              if (q_last) mma_commit(bar(B_Q_EMPTY));
+            }
           }
+          if (j >= 0 && last) mma_commit(bar(B_V_EMPTY + (nv & 1)));
         }
-        if (j >= 0 && last) {
-          commit_elect(v_empty);
-          ++nv;
-        }
+        __syncwarp();
+        if (has_s && last) n += q8 ? 1 : 2;
+        if (j >= 0 && last) ++nv;
       }
       if (!run) break;
       commit_elect(bar(B_SEG_DONE));
@@ -891,6 +889,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           const int tr = slot_r < 32 ? tra : trb;
           // le / lt: the slots whose stage is <= tr / < tr, one ballot pair per stage
           unsigned long long acc = 0ull, le = 0ull, lt = 0ull;
+#pragma unroll 1
           for (int v = 1; v <= x.B; ++v) {
             const uint32_t lo = __ballot_sync(0xffffffffu, ta == v), hi = __ballot_sync(0xffffffffu, tb == v);
             acc |= ((unsigned long long)hi << 32) | lo;

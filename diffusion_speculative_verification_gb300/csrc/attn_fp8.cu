@@ -222,12 +222,11 @@ __device__ __forceinline__ uint32_t prefix32(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u));
 }
 
-// 32-bit window [t0, t0 + 32) of a 128-bit mask, zero outside [0, 128)
-__device__ __forceinline__ uint32_t window32(const uint32_t (&m)[4], int t0) {
+// 32-bit window [t0, t0 + 32) of the 128-bit mask m[1..4], zero outside [0, 128); m[0] = m[5] = 0
+__device__ __forceinline__ uint32_t window32(const uint32_t* m, int t0) {
   if (t0 <= -32 || t0 >= 128) return 0u;
-  auto pick = [&](int i) { return i == 0 ? m[0] : (i == 1 ? m[1] : (i == 2 ? m[2] : (i == 3 ? m[3] : 0u))); };
-  const int w = t0 >> 5, sh = t0 & 31;  // floor division
-  return sh == 0 ? pick(w) : __funnelshift_r(pick(w), pick(w + 1), sh);
+  const int w = t0 >> 5;  // floor division
+  return __funnelshift_r(m[w + 1], m[w + 2], t0 & 31);
 }
 
 // Instruction descriptors: fp32 accumulator, shape 128 x 128, B K-major or MN-major.
@@ -353,6 +352,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           if (!ok && cta == 0) report(p.dev_status, SSV_ERR_INVALID);
           const int rows = s.new_len + 2 * s.block;
           units = ok ? cdiv(rows, UR) : 0;
+#pragma unroll 1
           for (int t = 0; t < units; ++t) {
             const int nb = blocks_of(s.cache_len, s.new_len, rows, t * UR);
             blocks += nb;
@@ -487,6 +487,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     const ssv_seq s = p.seqs[b];
     const int rows = s.new_len + 2 * s.block;
     int c = s_prefC[b];
+#pragma unroll 1
     for (int t = 0; t < u - s_prefU[b]; ++t)
       c += kSegCost + cost_of(rows, t * UR) * blocks_of(s.cache_len, s.new_len, rows, t * UR);
     return c;
@@ -553,6 +554,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           ++n;
         }
         // fresh rows: a 16-bit block takes two stages, from an even one on
+#pragma unroll 1
         for (int i = cached; run && i < len; ++i) {
           if (n & 1) {
             if (!take(B_K_EMPTY, NK) || !take(B_R_EMPTY, C_::NR)) { run = false; break; }
@@ -586,6 +588,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       }
       // drain (bounded, regardless of abort): the copies that may still be in flight
       auto drain = [&](uint32_t full, int S, int last) {
+#pragma unroll 1
         for (int i = max(last - S, 0); i < last; ++i) {
           const long long t0 = clock64();
           while (!mbar_try_wait(bar(full + i % S), full_par(i, S)) && clock64() - t0 < wb) {
@@ -689,6 +692,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           // the tile is free once the last S of the form before is complete
           if (nq > 0 && !mbar_wait(bar(B_Q_EMPTY), (uint32_t)(nq - 1) & 1u, abort, wb)) { run = false; break; }
           mbar_expect_tx(bar(B_Q_FULL), x.mc * tile_bytes);
+#pragma unroll 1
           for (int t = 0; t < x.mc; ++t) {
             const uint32_t dst = sbase + C_::SM_Q + t * 2 * STAGE;
             const int z = x.q_off + x.row0 + t * R;
@@ -779,6 +783,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         ++nv;
       };
       if (cached > 0) {
+#pragma unroll 1
         for (int i = 0; i < cached; ++i) {
           if (!warp_wait(bar(B_C_FULL + nc % NSC), full_par(nc, NSC)) ||
               !warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR)) || !v_ready()) {
@@ -828,6 +833,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         }
       }
       if (run && len > cached) {
+#pragma unroll 1
         for (int i = cached; i < len; ++i) {
           if (n & 1) {  // the stage left out
             if (!warp_wait(bar(B_R_FULL + n % C_::NR), full_par(n, C_::NR))) { run = false; break; }
@@ -877,25 +883,26 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         const float rowf = cached > 0 && valid ? __ldg(p.q_scale + (size_t)(x.q_off + i) * p.Hq + gh * G + hj) : 1.f;
         const bool prompt = i < x.N;
         const int r = i - x.N;
-        uint32_t tm[4] = {0u, 0u, 0u, 0u};  // allowed tail keys of this row
+        uint32_t tm[6] = {0u, 0u, 0u, 0u, 0u, 0u};  // allowed tail keys of this row (in local memory: seldom read)
         if (warp_active && len > cached && x.row0 + x.nvalid > x.N) {  // warp-uniform: fresh blocks and tail rows
           const int32_t* tau = p.tau + x.tau_off;
           const int ta = lane < x.B ? tau[lane] : 0, tb = lane + 32 < x.B ? tau[lane + 32] : 0;
-          // a bad stage map cannot index out of range below: report only
-          if (!warp_tau_is_permutation(tau, x.B) && lane == 0) report(p.dev_status, SSV_ERR_BAD_TAU);
           const bool tail_row = valid && !prompt;
           const int slot_r = tail_row ? (r % x.B) : 0;
           const int tra = __shfl_sync(0xffffffffu, ta, slot_r & 31), trb = __shfl_sync(0xffffffffu, tb, slot_r & 31);
           const int tr = slot_r < 32 ? tra : trb;
           // le / lt: the slots whose stage is <= tr / < tr, one ballot pair per stage
           unsigned long long acc = 0ull, le = 0ull, lt = 0ull;
+          bool bad = false;  // (a bad stage map cannot index out of range: report only)
 #pragma unroll 1
           for (int v = 1; v <= x.B; ++v) {
             const uint32_t lo = __ballot_sync(0xffffffffu, ta == v), hi = __ballot_sync(0xffffffffu, tb == v);
             acc |= ((unsigned long long)hi << 32) | lo;
+            bad |= __popc(lo) + __popc(hi) != 1;
             if (v == tr - 1) lt = acc;
             if (v == tr) le = acc;
           }
+          if (bad && lane == 0) report(p.dev_status, SSV_ERR_BAD_TAU);
           // a data row sees the data slots of stages <= its own; a mask row the data slots of
           // earlier stages and the mask slots of its own stage and later ones
           const unsigned long long bmask = (x.B >= 64) ? ~0ull : ((1ull << x.B) - 1ull);
@@ -904,11 +911,12 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           const unsigned long long hi_part = (!tail_row || data_row) ? 0ull : (~lt & bmask);
           const unsigned long long w01 = lo_part | (x.B < 64 ? (hi_part << x.B) : 0ull);
           const unsigned long long w23 = x.B < 64 ? (hi_part >> (64 - x.B)) : hi_part;
-          tm[0] = (uint32_t)w01; tm[1] = (uint32_t)(w01 >> 32);
-          tm[2] = (uint32_t)w23; tm[3] = (uint32_t)(w23 >> 32);
+          tm[1] = (uint32_t)w01; tm[2] = (uint32_t)(w01 >> 32);
+          tm[3] = (uint32_t)w23; tm[4] = (uint32_t)(w23 >> 32);
         }
         // rows without a query follow along unmasked, whatever their tile rows hold, and are dropped at the end
         float m_used = valid ? -INFINITY : 0.f, l_sum = 0.f, unit = 0.f;
+#pragma unroll 1
         for (int job = set; job < jobs; job += 2) {
           const int jj = two ? job >> 1 : job, j = k + jj;
           const bool is_cache = jj < cached, first = job == set;
@@ -1191,9 +1199,11 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             if (rank == c_a && run) {
               // in CTA order, so that equal inputs give equal bits
               float M = m_used;
+#pragma unroll 1
               for (int cc = c_a + 1; cc <= c_b; ++cc) M = fmaxf(M, __ldcg(work.part_ml + slot_of(cc) * 2));
               const float g = M == -INFINITY ? 0.f : ex2(m_used - M);
               float L = l_sum * g;
+#pragma unroll 1
               for (int cc = c_a + 1; cc <= c_b; ++cc) {
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(work.part_ml + slot_of(cc) * 2));
                 if (M > -INFINITY) L += ml.y * ex2(ml.x - M);
@@ -1203,6 +1213,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
               for (int q = 0; q < D / 32; ++q) {
                 float v[32];
                 load_o(q, v, g);
+#pragma unroll 1
                 for (int cc = c_a + 1; cc <= c_b; ++cc) {
                   const size_t sl = slot_of(cc);
                   const float f = (M == -INFINITY) ? 0.f : ex2(__ldcg(work.part_ml + sl * 2) - M);

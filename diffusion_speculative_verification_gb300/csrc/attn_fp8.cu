@@ -85,9 +85,13 @@ constexpr float kUnitRoom = 2.f;            // u leaves that much for larger sca
 constexpr int SC = 20;                      // words of a block's scales: K factor of every 16 keys x 8, vs / 2^u of
                                             // every 16 keys as an fp16 pair x 8, u
 // Estimated costs of the plan, in units of 0.1 us: a block of one / two tiles
-// and a segment's fixed work; a merge of partials costs about kMergeBlocks blocks.
+// and a segment's fixed work.  (Blocks of one tile take 0.5 of two when alone; 7 : 12 and 40 measured best of 4..10 : 12
+// and 20..160 over ragged batches.)
 constexpr int kBlock1 = 7, kBlock2 = 12, kSegCost = 40;
-constexpr int kMergeBlocks = 8;
+// Units cut across CTAs, where there are CTAs to spare: a merge costs about kMergeFixed blocks, and kMergePart for each
+// part (they are read one after the other), so parts of sqrt(kMergePart n) blocks end a unit of n soonest.  One head
+// of K, one sequence of 16384 keys: 169 us over all CTAs, 38 us so; kMergePart of 0.8 or 2 gives 39 us.
+constexpr float kMergeFixed = 4.f, kMergePart = 1.2f;
 
 enum : uint32_t {
   B_K_FULL = 0,
@@ -336,7 +340,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
   // ------------------------------------------------------------------ plan
   if (warp == 0) {
     if (!p.early) pdl_wait();
-    int carryU = 0, carryB = 0, carryC = 0;
+    int carryU = 0, carryB = 0, carryC = 0, top = 0;  // top: blocks of the longest unit
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
       int units = 0, blocks = 0, cost = 0;
@@ -356,6 +360,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           for (int t = 0; t < units; ++t) {
             const int nb = blocks_of(s.cache_len, s.new_len, rows, t * UR);
             blocks += nb;
+            top = max(top, nb);
             cost += kSegCost + cost_of(rows, t * UR) * nb;
           }
         }
@@ -373,6 +378,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       carryB += __shfl_sync(0xffffffffu, ib, 31);
       carryC += __shfl_sync(0xffffffffu, ic, 31);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     __syncwarp();
     if (lane == 0) {
       s_prefU[0] = s_prefB[0] = s_prefC[0] = 0;
@@ -383,9 +390,11 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
       const int cap = max((int)gridDim.x / p.Hkv, 1);
       int ph = cap;
       if (carryU > 0 && carryU <= cap) {
-        const long long per_unit = (long long)carryB * cap;
-        const long long per_cta = ((long long)carryB + (long long)kMergeBlocks * cap) * carryU;
-        ph = per_cta < per_unit ? cap : carryU;
+        const float B = (float)carryB, longest = (float)top;
+        const float w = sqrtf(kMergePart * longest);  // blocks per CTA that part and merge a unit soonest
+        ph = min(max((int)(B / w + 0.5f), carryU), cap);
+        const float each = B / (float)ph;
+        if (longest <= each + kMergeFixed + kMergePart * longest / each) ph = carryU;
       }
       // every range at least one block wide, so the CTAs holding a unit's blocks are consecutive
       ph = min(min(ph, max(carryB, 1)), max(carryC / kBlock2, 1));

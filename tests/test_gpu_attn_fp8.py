@@ -237,3 +237,32 @@ def test_refused_sequences():
     tau = x.tau.copy()
     tau[4:12] = 2
     broken(ssv.SSV_ERR_BAD_TAU, tau=tau)
+
+
+@pytest.mark.parametrize("C,hkv", [([1500], 1), ([20011], 1), ([30001], 2), ([9000, 300, 2500], 1), ([5000, 700, 0, 6400], 8)])
+def test_units_cut_into_many_parts(C, hkv):
+    """Few units and many CTAs: a unit's keys are dealt to several of them, as many as its length is worth."""
+    n = len(C)
+    check(PagedBatch(C, [1] + [0] * (n - 1), [8, 3, 16, 5][:n], 4 * hkv, hkv, 128, 64, seed=sum(C)))
+
+
+@pytest.mark.parametrize("skip", [0, 5])
+def test_wait_runs_out(skip):
+    """One key block's copy is left out: the wait for it ends after its budget, with an error code; other CTAs wait for
+    that part in vain, too.  The workspace once cleared serves a normal call."""
+    x = PagedBatch([6000, 5000], [0, 40], [8, 4], 2, 1, 128, 64, seed=17)
+    t = x.device()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.empty(x.q.shape, dtype=torch.bfloat16, device="cuda")
+    try:
+        ssv.set_fault_injection(ssv.FAULT_ATTN, skip, 200_000)
+        call(t, out, dev_status=status, workspace=ws)
+        assert ssv.get_status(status) == ssv.SSV_ERR_TIMEOUT
+    finally:
+        ssv.set_fault_injection(None)
+    ws.zero_()
+    call(t, out, dev_status=status, workspace=ws)
+    assert ssv.get_status(status) == ssv.SSV_OK
+    o, tol = reference(x)
+    assert (np.abs(out.double().cpu().numpy() - o) <= tol).all()

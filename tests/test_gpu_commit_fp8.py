@@ -181,3 +181,9 @@ def test_graph_replay():
     torch.cuda.synchronize()
     same({k: t[k].cpu().numpy() for k in want}, want)
     assert np.array_equal(nl.cpu().numpy(), n)
+
+
+@pytest.mark.parametrize("hkv,rows", [(16, 15000), (5, 71000)])
+def test_prompts_long_enough_for_ctas_with_several_groups(hkv, rows):
+    """More chunks of rows than CTAs at once: a CTA takes several groups of heads in turn, also unevenly many."""
+    check(PagedBatch([0, 77], [rows, 300], [3, 2], hkv, hkv, 64, 128, seed=rows))

@@ -559,10 +559,23 @@ def _entry(name: str, workspace: bool = False):
     return f
 
 
-def _stream_of(stream, t) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+def _launch(what: str, tensors, block, stream, workspace=None):
+    """Calls entry point `what` on the packed `block`, on the given stream or
+    the current one of the device that holds the first of `tensors`; the others
+    (None: left out) have to be there, too."""
+    cuda = _torch()._C
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise SsvError(SSV_ERR_INVALID, f"{what}: tensors of one CUDA device")
+    if cuda._cuda_getDevice() != dev:
+        with _torch().cuda.device(dev):
+            return _launch(what, tensors, block, stream, workspace)
+    s = cuda._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if workspace is None:
+        _check(_entry(what)(block, s), what)
+    else:
+        _check(_entry(what, True)(block, workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), what)
 
 
 def _addr(t) -> int:
@@ -630,7 +643,7 @@ def page_plan(cache_len, new_len, block, held, pages, free_list, n_free, page_si
                    free_list.data_ptr(), n_free.data_ptr(), batch, pages.shape[1], int(page_size),
                    free_list.shape[0], total_rows, seqs.data_ptr(), slot_map.data_ptr(), slot_off.data_ptr(),
                    held_out.data_ptr(), n_out.data_ptr(), _addr(dev_status))
-    _check(_entry("ssv_page_plan")(a, _stream_of(stream, cache_len)), "ssv_page_plan")
+    _launch("ssv_page_plan", (cache_len, new_len, block, held, pages, free_list, n_free, *out, dev_status), a, stream)
     return out
 
 
@@ -659,7 +672,7 @@ def norm_rope_copy(q, k, q_weight, k_weight, batch: Batch, base: float = 10000.0
                    k_weight.data_ptr(), _rows_strided(q, what), _rows_strided(k, what), _rows_strided(q_out, what),
                    _rows_strided(k_out, what), _dtype_code(q), q.shape[1], k.shape[1], q.shape[2], eps, base,
                    batch.dev.data_ptr(), batch.batch, q.shape[0], _addr(positions), _addr(dev_status))
-    _check(_entry(what)(a, _stream_of(stream, q)), what)
+    _launch(what, (q, k, q_out, k_out, q_weight, k_weight, batch.dev, positions, dev_status), a, stream)
     return q_out, k_out
 
 
@@ -710,8 +723,8 @@ def verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, 
                          dev_status)
     ws = workspace if workspace is not None else \
         _workspace(verify_attn_fp8_workspace_bytes(AttnFp8Args(*a)), q.device)
-    _check(_entry("ssv_verify_attn_fp8", True)(_pack_attn(*a), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                               _stream_of(stream, q)), "ssv_verify_attn_fp8")
+    _launch("ssv_verify_attn_fp8", (q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch.dev, tau, ws,
+                                    dev_status), _pack_attn(*a), stream, ws)
     return out
 
 
@@ -736,7 +749,8 @@ def commit_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch: B
                      _dtype_code(k_new), hkv, d, ps, n, pages.numel(), batch.dev.data_ptr(), batch.batch,
                      tau.data_ptr(), n_acc.data_ptr(), new_len.data_ptr(), rows, tau.shape[0], batch.max_new,
                      batch.max_block, _addr(dev_status))
-    _check(_entry(what)(a, _stream_of(stream, k_new)), what)
+    _launch(what, (k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch.dev, tau, n_acc, new_len, dev_status),
+            a, stream)
     return new_len
 
 

@@ -148,3 +148,21 @@ def test_binding_refuses_wrong_tensors():
     refused(ssv.page_plan, i2, i2, i2.long(), i2, torch.zeros((2, 4), dtype=torch.int32), i2, i2[:1], 16, 10)
     refused(ssv.page_plan, i2, i2, i2, i2, torch.zeros((3, 4), dtype=torch.int32), i2, i2[:1], 16, 10)
     assert np.array_equal(cache.numpy(), np.zeros_like(cache.numpy()))
+
+
+def test_binding_refuses_host_tensors():
+    """Tensors that are right but for where they are: no host address reaches a kernel."""
+    seqs = torch.zeros((2, 6), dtype=torch.int32)
+    batch = ssv.Batch.from_device(seqs, 8, 4, 10, 0, 2)
+    tau, acc = torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    cache, scale = torch.zeros((3, 2, 16, 128), dtype=torch.uint8), torch.zeros((3, 2))
+    pages, w = torch.zeros(6, dtype=torch.int32), torch.ones(128, dtype=torch.bfloat16)
+    rows, q = torch.zeros((8, 2, 128), dtype=torch.bfloat16), torch.zeros((8, 4, 128), dtype=torch.bfloat16)
+    i2 = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: ssv.commit_fp8(rows, rows, cache, cache, scale, scale, pages, batch, tau, acc),
+                 lambda: ssv.verify_attn_fp8(q, cache, cache, scale, scale, pages, rows, rows, batch, tau,
+                                             workspace=torch.zeros(1 << 24, dtype=torch.uint8)),
+                 lambda: ssv.norm_rope_copy(q, rows, w, w, batch),
+                 lambda: ssv.page_plan(i2, i2, i2, i2, torch.zeros((2, 4), dtype=torch.int32), i2, i2[:1], 16, 10)):
+        with pytest.raises(ssv.SsvError, match="one CUDA device"):
+            call()

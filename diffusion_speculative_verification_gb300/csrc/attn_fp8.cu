@@ -37,11 +37,11 @@
 //                 fresh rows into two ring stages at once
 //   warp 1        MMA issue for two S / P / O sets in turn: PV(n), S(n + 2), so
 //                 that a set's softmax runs under the other set's products.  The
-//                 whole warp runs the loop on uniform values and one elected
-//                 lane issues: descriptors then stay in uniform registers.  A
-//                 single-lane loop moves them there for every MMA, and beside
-//                 busy softmax warps that took 1640-2400 cycles for the 1025 of
-//                 a PV and an S (1027 as it is).
+//                 whole warp waits, and one elected lane issues a round's
+//                 products and commits in one branch; a predicate on every MMA
+//                 took twice the instructions (mixed batch 268 us, 249 us so),
+//                 and a loop run by a single lane 1640-2400 cycles for the 1025
+//                 of a PV and an S beside busy softmax warps
 //   warp 2        query tiles, in the form of the cached and of the fresh blocks
 //   warp 3        the scales of the pages, and with them the unit u
 //   warps 4..11   softmax, four per set, one TMEM lane quadrant each.  A unit of
@@ -50,8 +50,18 @@
 //                 and the first set joins both at the end
 //   warps 12..15  V codes to fp16, fresh V copied (rows behind the last token
 //                 become 0, so nothing there is ever multiplied)
-// The instruction cache bounds how much code a block may pass through: unrolled
-// variants of these loops (250 KB of code) ran the mixed batch at half this speed.
+// Bounds.  A block of two tiles takes about 3800 cycles of an SM: its products
+// alone 2050 (the tensor pipe is 42-50% busy), its two softmaxes alone 1650, and
+// each set's S - softmax - P - PV chain leaves gaps that the other does not fill,
+// as S, P and O of two sets fill the 512 TMEM columns and no S can be ahead.
+// Among the sixteen warps the instruction cache is the other bound: 57 misses per
+// product pair with 130 KB of code, and softmax loops at half their speed alone.
+// Rolled cold loops, waits beyond the first try out of line and softmax chunks of
+// sixteen columns brought 20, and the mixed batch from 308 to 242 us.  Measured:
+//   8 x 1024 cached keys, 16 / 8 heads             19 us   (bytes: 2.7 us)
+//   64 sequences of 256..8192, 32 / 8 heads       242 us   2.5 TB/s, 610 TFLOP/s
+//   3 sequences of 90001..110007, pages of 16     282 us   2.3 TB/s, 604 TFLOP/s
+//   4 prompts of 2048 over 4096..6200 cached      742 us   1160 TFLOP/s
 // Every wait is bounded; an expired one raises the CTA's abort flag, copies and
 // MMAs in flight are drained, TMEM is freed and SSV_ERR_TIMEOUT reported.
 #include "ssv_internal.cuh"

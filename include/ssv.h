@@ -733,7 +733,9 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * A sequence's own fresh rows must be finite (a masked non-finite value row
  * still meets a zero weight); rows of other sequences, rows of a page behind
  * token C - 1 and pages that are not a sequence's own never influence it,
- * whatever they hold.  scales: positive and finite.
+ * whatever they hold.  scales: positive and finite; a value scale enters as a
+ * 16-bit float beside the largest met so far in its unit of work, exactly for
+ * the powers of two within 2^22 of it that ssv_commit_fp8 writes.
  * d = 128; Hq % Hkv == 0, Hq / Hkv <= 128; 1 <= B <= 64; n_pages * Hkv *
  * page_size < 2^31; pointers 16-byte aligned, strides multiples of 8.
  * max_cache / max_new / max_block as ssv_verify_attn.  scale 0 means
@@ -745,6 +747,8 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * SSV_ERR_INVALID for a sequence outside the buffers or with a page outside
  * [0, n_pages) among its first ceil(C / page_size) (skipped: its rows of o
  * are unspecified).
+ * Scheduling as ssv_verify_attn: one CTA per SM, and where a unit of work is
+ * split the CTA with its first key block waits (bounded) for the others.
  * ---------------------------------------------------------------------- */
 typedef struct {
   const void* q;
@@ -826,7 +830,8 @@ SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
  * ssv_set_fault_injection -- test support for failure detection.
  * The pages have no counterpart: this lets a test make a bounded device wait
  * run out without faulting, trapping or hanging the GPU.  For the chosen
- * kernel -- the tensor-core attention (SSV_FAULT_ATTN), the streaming
+ * kernel -- the tensor-core attentions (SSV_FAULT_ATTN: ssv_verify_attn and
+ * ssv_verify_attn_fp8, where the copy is that of a key block), the streaming
  * acceptance reduce (SSV_FAULT_ACCEPT) or the fused LM head's GEMM
  * (SSV_FAULT_LMHEAD) -- every bounded wait gives up after
  * wait_budget_cycles SM cycles instead of about one second, and, if

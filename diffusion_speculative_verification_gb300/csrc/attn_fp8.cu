@@ -72,6 +72,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -1350,8 +1351,8 @@ bool encode_rows(CUtensorMap* m, const void* base, int es, int heads, long long 
   const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)(128 * es), (cuuint64_t)(stride * es)};
   const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_heads, (cuuint32_t)box_rows}, steps[3] = {1, 1, 1};
-  return fp8_encode_fn()(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, steps,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fp8_encode_fn()(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                         const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1412,20 +1413,21 @@ ssv_status fp8_check(const ssv_attn_fp8_args* a) {
   return (al & 15u) ? SSV_ERR_INVALID : SSV_OK;
 }
 
-
 template <int MT>
 cudaError_t launch_fp8(const AttnFp8Params& p, const Fp8Maps& maps, const Fp8Work& w, int G, int grid, cudaStream_t st) {
-  // a merge waits (bounded) on other CTAs' partials: all must be resident at once, one per SM
-  static std::once_flag once;
-  static cudaError_t ready = cudaSuccess;
-  std::call_once(once, [] {
-    ready = cudaFuncSetAttribute(attn_fp8_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
-    int per_sm = 0;
-    if (ready == cudaSuccess)
-      ready = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_fp8_kernel<MT>, kThreads, kMaxSmem);
-    if (ready == cudaSuccess && per_sm < 1) ready = cudaErrorCooperativeLaunchTooLarge;
-  });
-  if (ready != cudaSuccess) return ready;
+  // a merge waits (bounded) on other CTAs' partials: all must be resident at once, one per SM (asked once per device)
+  static std::atomic<unsigned long long> ready{0};
+  int dev = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(attn_fp8_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_fp8_kernel<MT>, kThreads, kMaxSmem);
+    if (e == cudaSuccess && per_sm < 1) e = cudaErrorCooperativeLaunchTooLarge;
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready |= 1ull << dev;
+  }
   const size_t tables = sizeof(int32_t) * 4 * (size_t)(p.batch + 1);
   const int in_smem = Cfg<MT>::SM_TOTAL + tables <= kMaxSmem ? 1 : 0;
   const size_t smem = Cfg<MT>::SM_TOTAL + (in_smem ? tables : 0);
@@ -1455,6 +1457,14 @@ extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, 
   if (a->batch == 0 || a->total_rows == 0) return SSV_OK;
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < L.total) return SSV_ERR_WORKSPACE;
   const int64_t width = (int64_t)a->Hkv * a->d;
+  // other CTAs still read the rows while the first ones write o
+  auto meets_o = [&](const void* x, int64_t stride, int64_t cols) {
+    const uintptr_t o = (uintptr_t)a->o, y = (uintptr_t)x;
+    return o < y + 2 * ((a->total_rows - 1) * stride + cols) && y < o + 2 * (int64_t)a->total_rows * a->Hq * D;
+  };
+  if (meets_o(a->q, (int64_t)a->Hq * D, (int64_t)a->Hq * D) || meets_o(a->k_new, a->k_stride ? a->k_stride : width, width) ||
+      meets_o(a->v_new, a->v_stride ? a->v_stride : width, width))
+    return SSV_ERR_INVALID;
   const FaultSetting f = fault_for(SSV_FAULT_ATTN);
   char* w = static_cast<char*>(ws);
   const int G = a->Hq / a->Hkv, max_cache = a->n_pages > 0 ? a->max_cache : 0;

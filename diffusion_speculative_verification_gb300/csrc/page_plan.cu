@@ -19,7 +19,7 @@
 #include "ssv_internal.cuh"
 #include "paged.cuh"
 
-#include <mutex>
+#include <atomic>
 
 namespace ssv {
 namespace {
@@ -252,13 +252,14 @@ extern "C" ssv_status ssv_page_plan(const ssv_page_plan_args* a, void* stream) {
                a->slot_map, a->slot_off, a->held_out, a->n_free_out, a->dev_status, a->batch, a->max_pages,
                ilog2(a->page_size), a->n_pages, a->total_rows};
   const size_t smem = sizeof(int) * 6 * (size_t)a->batch;
-  static std::once_flag once;
-  static cudaError_t ready = cudaSuccess;
-  std::call_once(once, [] {
-    ready = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(sizeof(int) * 6 * kPlanMaxBatch));
-  });
-  SSV_CUDA_CHECK(ready);
+  static std::atomic<unsigned long long> ready{0};  // bit per device
+  int dev = 0;
+  SSV_CUDA_CHECK(cudaGetDevice(&dev));
+  if (dev >= 64 || !(ready.load() >> dev & 1)) {
+    SSV_CUDA_CHECK(cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)(sizeof(int) * 6 * kPlanMaxBatch)));
+    if (dev < 64) ready |= 1ull << dev;
+  }
   const int grid = min(152, max(1, (a->total_rows + kPlanRows - 1) / kPlanRows));
   const cudaError_t e =
       launch_pdl(page_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(stream), p);

@@ -739,7 +739,7 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * d = 128; Hq % Hkv == 0, Hq / Hkv <= 128; 1 <= B <= 64; n_pages * Hkv *
  * page_size < 2^31; pointers 16-byte aligned, strides multiples of 8.
  * max_cache / max_new / max_block as ssv_verify_attn.  scale 0 means
- * 1/sqrt(d).  o overlaps no input.
+ * 1/sqrt(d).  o overlaps no input (checked for q, k_new and v_new).
  * Workspace: ssv_verify_attn_fp8_workspace bytes, 256-byte aligned, zero
  * before its first use (see the conventions).
  * Errors: SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED (d, heads), SSV_ERR_WORKSPACE,

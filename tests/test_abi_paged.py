@@ -150,6 +150,14 @@ def test_binding_refuses_wrong_tensors():
     assert np.array_equal(cache.numpy(), np.zeros_like(cache.numpy()))
 
 
+def test_attn_output_over_its_inputs(L):
+    """o written over rows that other CTAs still read."""
+    rows, wide = 40, 3 * 8 * 128   # K and V as parts of a fused projection
+    for kw in (dict(o=M), dict(o=7 * M), dict(o=M + 2 * rows * 32 * 128 - 16), dict(o=8 * M - 2 * rows * 32 * 128 + 16),
+               dict(o=7 * M + 2 * (rows - 1) * wide + 2 * 8 * 128 - 16, k_stride=wide)):
+        assert L.ssv_verify_attn_fp8(C.byref(_attn(**kw)), 64 * M, 1 << 40, None) == ssv.SSV_ERR_INVALID, kw
+
+
 def test_binding_refuses_host_tensors():
     """Tensors that are right but for where they are: no host address reaches a kernel."""
     seqs = torch.zeros((2, 6), dtype=torch.int32)

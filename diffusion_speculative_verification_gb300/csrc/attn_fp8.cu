@@ -267,33 +267,36 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
 }
-#define FP8_NEXT(KIND, OA, OB) \
-  "add.s64 a, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\ttcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, q;\n\t"
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(kIdE4m3), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(kIdBf16), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
 __device__ __forceinline__ void gemm_q8(uint32_t d, uint64_t a, uint64_t b) {
-  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-                 FP8_NEXT("f8f6f4", 2, 2) FP8_NEXT("f8f6f4", 4, 4) FP8_NEXT("f8f6f4", 6, 6) FP8_NEXT("f8f6f4", 1024, 0)
-                 FP8_NEXT("f8f6f4", 1026, 2) FP8_NEXT("f8f6f4", 1028, 4) FP8_NEXT("f8f6f4", 1030, 6) "}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(kIdE4m3) : "memory");
+#pragma unroll 4
+  for (uint32_t s = 0; s < 8; ++s) mma_f8(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s & 3) * 2, s);
 }
 __device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
-  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-                 FP8_NEXT("f16", 2, 2) FP8_NEXT("f16", 4, 4) FP8_NEXT("f16", 6, 6) FP8_NEXT("f16", 1024, 1024)
-                 FP8_NEXT("f16", 1026, 1026) FP8_NEXT("f16", 1028, 1028) FP8_NEXT("f16", 1030, 1030) "}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(kIdBf16) : "memory");
+#pragma unroll 4
+  for (uint32_t s = 0; s < 8; ++s) mma_bf16(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s >> 2) * 1024 + (s & 3) * 2, s);
 }
-#undef FP8_NEXT
-#define FP8_NEXT(OA, OB) \
-  "add.u32 a, %1, " #OA ";\n\tadd.s64 b, %2, " #OB ";\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
 __device__ __forceinline__ void gemm_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-                 FP8_NEXT(8, 128) FP8_NEXT(16, 256) FP8_NEXT(24, 384) FP8_NEXT(32, 512) FP8_NEXT(40, 640) FP8_NEXT(48, 768)
-                 FP8_NEXT(56, 896) "}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+#pragma unroll 4
+  for (uint32_t s = 0; s < 8; ++s) mma_pv(d, a + s * 8, b + s * 128, idesc, s | acc);
 }
-#undef FP8_NEXT
 __device__ __forceinline__ void commit_elect(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"

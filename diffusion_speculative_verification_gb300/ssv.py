@@ -563,19 +563,28 @@ def _launch(what: str, tensors, block, stream, workspace=None):
     """Calls entry point `what` on the packed `block`, on the given stream or
     the current one of the device that holds the first of `tensors`; the others
     (None: left out) have to be there, too."""
-    cuda = _torch()._C
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
+        if t is not None and t.get_device() != dev:
             raise SsvError(SSV_ERR_INVALID, f"{what}: tensors of one CUDA device")
+    _launch_on(what, dev, block, stream, workspace)
+
+
+def _launch_on(what: str, dev: int, block, stream, workspace=None):
+    if dev < 0:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: tensors of one CUDA device")
+    cuda = _torch()._C
     if cuda._cuda_getDevice() != dev:
         with _torch().cuda.device(dev):
-            return _launch(what, tensors, block, stream, workspace)
+            return _launch_on(what, dev, block, stream, workspace)
     s = cuda._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if workspace is None:
-        _check(_entry(what)(block, s), what)
+        code = (_entries.get(what) or _entry(what))(block, s)
     else:
-        _check(_entry(what, True)(block, workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), what)
+        code = (_entries.get(what) or _entry(what, True))(block, workspace.data_ptr(),
+                                                          workspace.numel() * workspace.element_size(), s)
+    if code:
+        _check(code, what)
 
 
 def _addr(t) -> int:
@@ -625,25 +634,33 @@ def page_plan(cache_len, new_len, block, held, pages, free_list, n_free, page_si
     [batch, 6], slot_map [total_rows], slot_off [batch], held [batch], n_free
     [1]), new tensors unless given in ``out``."""
     torch = _torch()
-    _int32("ssv_page_plan", cache_len, new_len, block, held, pages, free_list, n_free, *(out or ()))
-    batch = cache_len.shape[0]
-    if pages.dim() != 2 or any(x.shape[0] != batch for x in (new_len, block, held, pages)) or n_free.numel() != 1:
-        raise SsvError(SSV_ERR_INVALID, "ssv_page_plan: shapes")
+    what, i32, dev = "ssv_page_plan", torch.int32, cache_len.get_device()
+    for t in (cache_len, new_len, block, held, pages, free_list, n_free) + (out or ()) + \
+            (() if dev_status is None else (dev_status,)):
+        if t.dtype != i32 or not t.is_contiguous():
+            raise SsvError(SSV_ERR_INVALID, f"{what}: index tensors are contiguous int32")
+        if t.get_device() != dev:
+            raise SsvError(SSV_ERR_INVALID, f"{what}: tensors of one CUDA device")
+    batch = cache_len.numel()
+    if cache_len.dim() != 1 or new_len.numel() != batch or block.numel() != batch or held.numel() != batch or \
+            pages.dim() != 2 or pages.shape[0] != batch or n_free.numel() != 1:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
     total_rows = int(total_rows)
     if out is None:
         # one allocation: the table, the offsets, the counts, the stack height, the slot map
-        seqs, slot_off, held_out, n_out, slot_map = torch.empty(
-            8 * batch + 1 + total_rows, dtype=torch.int32, device=cache_len.device).split_with_sizes(
-                [6 * batch, batch, batch, 1, total_rows])
+        buf = torch.empty(8 * batch + 1 + total_rows, dtype=i32, device=cache_len.device)
+        seqs, slot_off, held_out, n_out, slot_map = buf.split_with_sizes([6 * batch, batch, batch, 1, total_rows])
         out = (seqs.view(batch, 6), slot_map, slot_off, held_out, n_out)
-    elif tuple(x.numel() for x in out) != (6 * batch, total_rows, batch, batch, 1):
-        raise SsvError(SSV_ERR_INVALID, "ssv_page_plan: output shapes")
-    seqs, slot_map, slot_off, held_out, n_out = out
+        at = buf.data_ptr()
+        outs = (at, at + 32 * batch + 4, at + 24 * batch, at + 28 * batch, at + 32 * batch)
+    else:
+        if tuple(x.numel() for x in out) != (6 * batch, total_rows, batch, batch, 1):
+            raise SsvError(SSV_ERR_INVALID, f"{what}: output shapes")
+        outs = tuple(x.data_ptr() for x in out)
     a = _pack_plan(cache_len.data_ptr(), new_len.data_ptr(), block.data_ptr(), held.data_ptr(), pages.data_ptr(),
-                   free_list.data_ptr(), n_free.data_ptr(), batch, pages.shape[1], int(page_size),
-                   free_list.shape[0], total_rows, seqs.data_ptr(), slot_map.data_ptr(), slot_off.data_ptr(),
-                   held_out.data_ptr(), n_out.data_ptr(), _addr(dev_status))
-    _launch("ssv_page_plan", (cache_len, new_len, block, held, pages, free_list, n_free, *out, dev_status), a, stream)
+                   free_list.data_ptr(), n_free.data_ptr(), batch, pages.shape[1], int(page_size), free_list.numel(),
+                   total_rows, *outs, _addr(dev_status))
+    _launch_on(what, dev, a, stream)
     return out
 
 

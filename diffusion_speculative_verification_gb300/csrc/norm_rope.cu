@@ -23,8 +23,8 @@
 //
 // Measured: 4 x 8192 rows of 32 + 8 heads of 128, bf16, out of a fused projection:
 // 120 us, 5.6 TB/s of the 6.8 TB/s that a copy reaches (158 us with one head per
-// warp); 37 ragged sequences, fp32, heads of 64: 16.4 us, 3.7 TB/s of mostly one
-// wave of CTAs; 8 sequences of 16 rows: 3.5 us, latency.
+// warp); 37 ragged sequences, fp32, heads of 64: 13.1 us, 4.7 TB/s of little more
+// than one wave of CTAs; 8 sequences of 16 rows: 3.5 us, latency.
 #include "ssv_internal.cuh"
 #include "paged.cuh"
 
@@ -34,7 +34,9 @@ namespace ssv {
 namespace {
 
 constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
-constexpr int kNormPre = 5;  // heads per thread in flight
+// heads per thread in flight (fp32: 2 with four CTAs per SM 13.1 us in the ragged case above, 5 with three 16.2 us)
+template <typename T>
+constexpr int kNormPre = sizeof(T) == 2 ? 5 : 2;
 
 struct NormTheta {
   uint64_t turn[64];  // theta_i / (2 pi) in units of 2^-64 turns
@@ -108,7 +110,7 @@ __device__ __forceinline__ int row_position(const NormParams& p, const ssv_seq& 
 }
 
 template <typename T, int D, bool kOneRow>
-__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 2 : 3)
+__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 2 : 4)
 norm_rope_kernel(const NormParams p, const __grid_constant__ NormTheta th) {
   constexpr int HALF = D / 2, VEC = kVec<T>, CHUNKS = HALF / VEC, GROUPS = 32 / CHUNKS;
   constexpr int ROWS = kOneRow ? 1 : GROUPS;
@@ -131,10 +133,10 @@ norm_rope_kernel(const NormParams p, const __grid_constant__ NormTheta th) {
     return (hh < p.Hq ? static_cast<T*>(p.q_out) + row * p.qos + hh * D
                       : static_cast<T*>(p.k_out) + row * p.kos + (hh - p.Hq) * D) + ch * VEC;
   };
-  uint4 ra[kNormPre], rb[kNormPre];
+  uint4 ra[kNormPre<T>], rb[kNormPre<T>];
   auto fetch = [&](int h0) {
 #pragma unroll
-    for (int k = 0; k < kNormPre; ++k) {
+    for (int k = 0; k < kNormPre<T>; ++k) {
       const int hh = h0 + k * STEP;
       if (here && hh < heads) {
         const T* x = in_at(hh);
@@ -177,10 +179,10 @@ norm_rope_kernel(const NormParams p, const __grid_constant__ NormTheta th) {
     *reinterpret_cast<float4*>(s + v) = *reinterpret_cast<const float4*>(&s_sin[lr][ch * VEC + v]);
   }
 #pragma unroll 1
-  for (int h0 = head0; h0 - head0 < heads; h0 += kNormPre * STEP) {
+  for (int h0 = head0; h0 - head0 < heads; h0 += kNormPre<T> * STEP) {
     if (h0 != head0) fetch(h0);
 #pragma unroll
-    for (int k = 0; k < kNormPre; ++k) {
+    for (int k = 0; k < kNormPre<T>; ++k) {
       const int hh = h0 + k * STEP;
       float x1[VEC], x2[VEC], w1[VEC], w2[VEC], ss = 0.f;
       widen<T>(ra[k], x1);

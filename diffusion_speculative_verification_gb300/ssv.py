@@ -661,6 +661,10 @@ def page_plan(cache_len, new_len, block, held, pages, free_list, n_free, page_si
                    free_list.data_ptr(), n_free.data_ptr(), batch, pages.shape[1], int(page_size), free_list.numel(),
                    total_rows, *outs, _addr(dev_status))
     _launch_on(what, dev, a, stream)
+    if batch == 0:  # the call writes nothing: no rows, and the stack as it was
+        with torch.cuda.stream(stream):
+            out[1].fill_(-1)
+            out[4].copy_(n_free)
     return out
 
 

@@ -655,7 +655,8 @@ SSV_API ssv_status ssv_tree_accept(const ssv_tree_accept_args* a, void* workspac
  * [batch]; n_free_out [1].  pages and free_list are updated in place, at
  * entries that the call does not read otherwise; held and n_free are not
  * written, so a pass that fails can be planned again from them.
- * pages [batch, max_pages]; free_list [n_pages]; 1 <= batch <= 4096;
+ * pages [batch, max_pages]; free_list [n_pages]; 1 <= batch <= 4096 (a call
+ * with batch 0 writes nothing);
  * n_pages * page_size < 2^31; page_size in {16, 32, 64, 128}.  held_out and
  * n_free_out must not overlap any input.  held[b] of an ended request and
  * the table's entries are trusted to name distinct pages.

@@ -142,3 +142,16 @@ def test_side_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert np.array_equal(out[1].cpu().numpy(), want["slot_map"]) and np.array_equal(out[0].cpu().numpy(), want["seqs"])
+
+
+def test_empty_batch():
+    """No request: no row is anyone's, and the stack is as high as it was."""
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    free, n_free = torch.arange(5, dtype=torch.int32, device="cuda"), torch.tensor([3], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        seqs, slot_map, slot_off, held, left = ssv.page_plan(e, e, e, e, e.view(0, 4), free, n_free, 16, 7, stream=stream)
+        torch.cuda.synchronize()
+        assert seqs.shape == (0, 6) and slot_off.numel() == held.numel() == 0
+        assert slot_map.tolist() == [-1] * 7 and left.tolist() == [3] and free.tolist() == [0, 1, 2, 3, 4]

@@ -96,3 +96,27 @@ def test_passes_of_a_serving_loop(page):
         assert np.array_equal(g["C"].cpu().numpy(), n)
         C = n.astype(np.int32)
         assert ssv.get_status(status) == ssv.SSV_OK
+
+
+def test_passes_without_rows_or_pages():
+    """Empty calls of the other three, and attention where nothing is cached and no page exists: as over a flat cache."""
+    def z(*s, dt=torch.int32):
+        return torch.zeros(s, dtype=dt, device="cuda")
+
+    bf, status = torch.bfloat16, z(1)
+    none = ssv.Batch.from_device(z(0, 6), 0, 0, 0, 0, 1)
+    codes, scale, w = z(4, 2, 16, 128, dt=torch.uint8), z(4, 2, dt=torch.float32), torch.ones(128, dtype=bf, device="cuda")
+    q0, k0 = z(0, 4, 128, dt=bf), z(0, 2, 128, dt=bf)
+    assert ssv.verify_attn_fp8(q0, codes, codes, scale, scale, z(0), k0, k0, none, z(0), dev_status=status).shape == q0.shape
+    assert ssv.commit_fp8(k0, k0, codes, codes, scale, scale, z(0), none, z(0), z(0), dev_status=status).numel() == 0
+    ssv.norm_rope_copy(q0, k0, w, w, none, dev_status=status)
+    seqs = np.array([[0, 3, 4, 0, 0, 0]], np.int32)
+    batch = ssv.Batch.from_device(torch.from_numpy(seqs).cuda(), 11, 4, 0, 3, 4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn(11, h, 128, device="cuda", generator=g).to(bf) for h in (4, 2, 2))
+    tau = torch.tensor([2, 1, 4, 3], dtype=torch.int32, device="cuda")
+    o = ssv.verify_attn_fp8(q, codes[:0], codes[:0], scale[:0], scale[:0], z(0), k, v, batch, tau, dev_status=status)
+    flat = ssv.verify_attn(q, k0, k0, k, v, ssv.Batch(seqs), tau)
+    assert ssv.get_status(status) == ssv.SSV_OK
+    # bf16 weights and a bf16 result on either side: 2 (2^-8 + 2^-7) of at most max |v|
+    assert float((o.float() - flat.float()).abs().max()) <= 2 * (2 ** -8 + 2 ** -7) * float(v.abs().max())

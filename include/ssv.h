@@ -789,8 +789,10 @@ SSV_API ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* workspa
  *           NaN and infinities stored as NaN
  *   codes of rows already there: code * s_old / s rounded likewise, when s grew
  * A power-of-two scale costs an 8-bit float no precision, makes x / s exact
- * and a later rescale exact but for values that fall below 2^-6 s.  Rows
- * behind the last appended token are left as they were.
+ * and a later rescale exact but for values that fall below 2^-6 s.  Where the
+ * caller has left another positive scale, x * (1 / s) and code * (s_old / s)
+ * are formed in fp32 before they are rounded.  Rows behind the last appended
+ * token are left as they were.
  * k_new, v_new [total_rows, Hkv, d] device, dtype (SSV_F32 or SSV_BF16), rows
  * k_stride / v_stride elements apart (0: Hkv * d).  seqs, tau, n_acc, new_len
  * and their checks as ssv_commit; kv_off is the sequence's first entry in

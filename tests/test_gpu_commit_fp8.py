@@ -187,3 +187,32 @@ def test_graph_replay():
 def test_prompts_long_enough_for_ctas_with_several_groups(hkv, rows):
     """More chunks of rows than CTAs at once: a CTA takes several groups of heads in turn, also unevenly many."""
     check(PagedBatch([0, 77], [rows, 300], [3, 2], hkv, hkv, 64, 128, seed=rows))
+
+
+def test_scales_that_are_no_powers_of_two():
+    """Scales that the caller has put there: kept where they suffice, and each code within a rounding of its value.  An
+    e4m3 rounding is off by at most 2^-4 of the value, or 2^-10 of the scale below the normal range; x (1 / s), or
+    code (s_old / s), by at most 2^-22 of it before."""
+    x = PagedBatch([5, 300, 77, 129], [0, 3, 40, 1], [8, 4, 16, 64], 2, 2, 128, 64, seed=21, spread=5)
+    old = [s.copy() for s in x.scale]
+    for s in x.scale:
+        s *= np.float32(1.37)
+    got, nl, st = run(x)
+    assert st == ssv.SSV_OK
+    want, n = expect(x)
+    assert np.array_equal(nl, n)
+    grown = kept = 0
+    for i, c in enumerate("kv"):
+        s = got[c + "_scale"]
+        assert np.array_equal(s, want[c + "_scale"], equal_nan=True)
+        a = opaged.e4m3_values(got[c + "_cache"]) * s[:, :, None, None].astype(np.float64)
+        b = opaged.e4m3_values(want[c + "_cache"]) * s[:, :, None, None].astype(np.float64)
+        live = ~np.isnan(b)
+        assert np.array_equal(np.isnan(a), ~live)
+        # both are roundings of one value: apart by at most two half steps
+        step = 2 * (2.0 ** -4 * np.maximum(np.abs(a), np.abs(b)) * (1 + 2.0 ** -4) + 2.0 ** -10 * s[:, :, None, None])
+        assert (np.abs(a - b) <= step)[live].all()
+        assert (a != b)[live].mean() < 1e-3   # and the same code but near a tie
+        grown += int((s > old[i] * np.float32(1.37)).sum())
+        kept += int((s == old[i] * np.float32(1.37)).sum())
+    assert grown > 0 and kept > 0

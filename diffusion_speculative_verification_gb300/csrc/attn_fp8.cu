@@ -286,7 +286,7 @@ __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 __device__ __forceinline__ void gemm_q8(uint32_t d, uint64_t a, uint64_t b) {
-#pragma unroll 4
+#pragma unroll
   for (uint32_t s = 0; s < 8; ++s) mma_f8(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s & 3) * 2, s);
 }
 __device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
@@ -294,7 +294,7 @@ __device__ __forceinline__ void gemm_qk(uint32_t d, uint64_t a, uint64_t b) {
   for (uint32_t s = 0; s < 8; ++s) mma_bf16(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s >> 2) * 1024 + (s & 3) * 2, s);
 }
 __device__ __forceinline__ void gemm_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-#pragma unroll 4
+#pragma unroll
   for (uint32_t s = 0; s < 8; ++s) mma_pv(d, a + s * 8, b + s * 128, idesc, s | acc);
 }
 __device__ __forceinline__ void commit_elect(uint32_t bar) {
@@ -994,7 +994,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           // ---- the row's maximum over the block
           float mx = -INFINITY;
           if (full) {
-#pragma unroll 1
+#pragma unroll
             for (int g = 0; g < 2; ++g) {
               float a[4], f[4];
 #pragma unroll
@@ -1038,20 +1038,21 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
           }
           if (need) m_used = mx;
           const float off = shift - ((m_used == -INFINITY) ? 0.f : m_used);
-          // ---- P = exp2(x - m + shift) over S: chunk q reads S columns [16 q, 16 q + 16) and writes P columns
-          // [8 q, 8 q + 8), which lie in S columns already read
+          // ---- P = exp2(x - m + shift) over S: chunk q reads S columns [32 q, 32 q + 32) and writes P columns
+          // [16 q, 16 q + 16), which lie in S columns already read
           auto exps = [&](auto cache_tag) {
             constexpr bool kCache = decltype(cache_tag)::value;
             const uint64_t of2 = pack2(off, off);
             uint64_t lp0 = 0ull, lp1 = 0ull;
-            uint32_t b0[16], b1[16];
-            tmem_ld16(tS, b0);
+            uint32_t b0[32], b1[32];
+            tmem_ld32(tS, b0);
             tmem_wait_ld();
-            auto chunk = [&](int q, const uint32_t* cur, float c) {
-              uint32_t pw[8];
-              const uint64_t cc2 = pack2(c, c);
+            auto chunk = [&](int q, const uint32_t* cur, float ca, float cb) {
+              uint32_t pw[16];
 #pragma unroll
-              for (int v = 0; v < 8; ++v) {
+              for (int v = 0; v < 16; ++v) {
+                const float c = v < 8 ? ca : cb;
+                const uint64_t cc2 = pack2(c, c);
                 float x0, x1;
                 unpack2(ffma2(pack2(__uint_as_float(cur[2 * v]), __uint_as_float(cur[2 * v + 1])), cc2, of2), x0, x1);
                 const float p0 = ex2(x0), p1 = ex2(x1);
@@ -1065,18 +1066,15 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
                 if (v & 1) lp1 = fadd2(lp1, pack2(p0, p1)); else lp0 = fadd2(lp0, pack2(p0, p1));
               }
               tmem_wait_ld();  // the next chunk is here, so this one's P may go over it
-              tmem_st8(tS + q * 8, pw);
+              tmem_st16(tS + q * 16, pw);
             };
-            float c0 = factor(0), c1 = factor(1);
 #pragma unroll 1
-            for (int q = 0; q < 8; q += 2) {
-              const float n0 = factor((q + 2) & 7), n1 = factor((q + 3) & 7);  // ahead of their use
-              tmem_ld16(tS + (q + 1) * 16, b1);
-              chunk(q, b0, c0);
-              if (q < 6) tmem_ld16(tS + (q + 2) * 16, b0);
-              chunk(q + 1, b1, c1);
-              c0 = n0;
-              c1 = n1;
+            for (int q = 0; q < 4; q += 2) {
+              const float f[4] = {factor(2 * q), factor(2 * q + 1), factor(2 * q + 2), factor(2 * q + 3)};
+              tmem_ld32(tS + (q + 1) * 32, b1);
+              chunk(q, b0, f[0], f[1]);
+              if (q < 2) tmem_ld32(tS + (q + 2) * 32, b0);
+              chunk(q + 1, b1, f[2], f[3]);
             }
             float y0, y1;
             unpack2(fadd2(lp0, lp1), y0, y1);

@@ -50,18 +50,19 @@
 //                 and the first set joins both at the end
 //   warps 12..15  V codes to fp16, fresh V copied (rows behind the last token
 //                 become 0, so nothing there is ever multiplied)
-// Bounds.  A block of two tiles takes about 3800 cycles of an SM: its products
+// Bounds.  A block of two tiles takes about 3700 cycles of an SM: its products
 // alone 2050 (the tensor pipe is 42-50% busy), its two softmaxes alone 1650, and
 // each set's S - softmax - P - PV chain leaves gaps that the other does not fill,
 // as S, P and O of two sets fill the 512 TMEM columns and no S can be ahead.
 // Among the sixteen warps the instruction cache is the other bound: 57 misses per
 // product pair with 130 KB of code, and softmax loops at half their speed alone.
-// Rolled cold loops, waits beyond the first try out of line and softmax chunks of
-// sixteen columns brought 20, and the mixed batch from 308 to 242 us.  Measured:
+// Rolled cold loops and waits beyond the first try out of line brought 20, and the
+// mixed batch from 308 to 242 us; with 100 KB the softmax could be unrolled again
+// (chunks of 32 columns instead of 16): 232 us.  Measured:
 //   8 x 1024 cached keys, 16 / 8 heads             19 us   (bytes: 2.7 us)
-//   64 sequences of 256..8192, 32 / 8 heads       242 us   2.5 TB/s, 610 TFLOP/s
-//   3 sequences of 90001..110007, pages of 16     282 us   2.3 TB/s, 604 TFLOP/s
-//   4 prompts of 2048 over 4096..6200 cached      742 us   1160 TFLOP/s
+//   64 sequences of 256..8192, 32 / 8 heads       232 us   2.6 TB/s, 636 TFLOP/s
+//   3 sequences of 90001..110007, pages of 16     268 us   2.4 TB/s, 636 TFLOP/s
+//   4 prompts of 2048 over 4096..6200 cached      724 us   1190 TFLOP/s
 // Every wait is bounded; an expired one raises the CTA's abort flag, copies and
 // MMAs in flight are drained, TMEM is freed and SSV_ERR_TIMEOUT reported.
 #include "ssv_internal.cuh"

@@ -146,17 +146,19 @@ struct Fp8Maps {
   CUtensorMap kc, vc, kn, vn, q, qhi, qlo;
 };
 
+// The counters lie at the front of the workspace, in an area whose size no argument of a call changes, and nothing else
+// is ever written there: zero again after a call of any sizes, they are zero before a call of any other.
 struct Fp8Work {
+  int32_t* cnt;    // [grid][2][4] arrival counters of the unit that a CTA merges (zero between calls)
   int32_t* plan;   // [grid][4][batch + 1] planning tables that do not fit shared memory
-  int32_t* cnt;    // [units][MT][4] arrival counters (zero between calls)
   float* part_ml;  // [grid][MT][128][2]
   float* part_o;   // [grid][MT][D / 4][128][4]
 };
 
-// Per head: U units of total cost Wc dealt to Pe CTAs; this CTA's head g and
+// Per head: units of total cost Wc dealt to Pe CTAs; this CTA's head g and
 // its blocks [begin, end), which start at block k0 of unit u0.
 struct PlanHdr {
-  int Wc, U, Pe, g, begin, end, u0, k0;
+  int Wc, Pe, g, begin, end, u0, k0;
 };
 
 template <int MT>
@@ -399,7 +401,6 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
     if (lane == 0) {
       s_prefU[0] = s_prefB[0] = s_prefC[0] = 0;
       PlanHdr h;
-      h.U = carryU;
       // CTAs per head: all, unless there are no more units than CTAs and one CTA per unit ends
       // sooner than spreading the blocks and merging
       const int cap = max((int)gridDim.x / p.Hkv, 1);
@@ -472,7 +473,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  const int begin = plan->begin, end = plan->end, Ph = plan->Pe, Uh = plan->U, gh = plan->g;
+  const int begin = plan->begin, end = plan->end, Ph = plan->Pe, gh = plan->g;
   const int Wc = plan->Wc;
   const int rank = Ph - 1 - cta / p.Hkv;
 
@@ -1196,7 +1197,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             const int cu = unit_cost(u) + kSegCost;
             const int c_a = owner_at(cu);
             const int c_b = owner_at(cu + cost_of(x.rows, x.row0) * (x.nblocks - 1));
-            int32_t* counter = work.cnt + (((size_t)gh * Uh + u) * MT + mt) * 4 + q4;
+            // (a cut unit ends c_a's range, so a CTA merges one unit at most, and its counters serve that one)
+            int32_t* counter = work.cnt + ((c_a * p.Hkv + gh) * 2 + mt) * 4 + q4;
             auto slot_of = [&](int rr) -> size_t { return ((size_t)(rr * p.Hkv + gh) * MT + mt) * 128 + m; };
             if (rank != c_a) {
               const size_t mine = slot_of(rank);
@@ -1359,7 +1361,7 @@ bool encode_rows(CUtensorMap* m, const void* base, int es, int heads, long long 
 }
 
 struct Fp8Layout {
-  size_t plan, cnt, ml, o, q, qs, total;
+  size_t cnt, plan, ml, o, q, qs, total;
   int grid, mt;
 };
 
@@ -1376,10 +1378,10 @@ bool fp8_layout(const ssv_attn_fp8_args* a, Fp8Layout* L) {
   const long long blocks = (long long)a->batch * tiles * (a->max_cache / BN + max_rows / BN + 2 + kSegCost / kBlock1 + 1);
   if (blocks > (1LL << 30) / kBlock2 || a->Hkv > L->grid) return false;  // the plan's sums are 32-bit
   size_t off = 0;
+  L->cnt = off;  // first, and of one size: see Fp8Work
+  off = align_up(off + sizeof(int32_t) * (size_t)L->grid * 2 * 4, 256);
   L->plan = off;
   off = align_up(off + sizeof(int32_t) * (size_t)L->grid * 4 * (a->batch + 1), 256);
-  L->cnt = off;
-  off = align_up(off + sizeof(int32_t) * (size_t)a->batch * a->Hkv * tiles * L->mt * 4, 256);
   L->ml = off;
   off = align_up(off + sizeof(float) * 2 * (size_t)L->grid * L->mt * 128, 256);
   L->o = off;
@@ -1501,7 +1503,7 @@ extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, 
     maps.kc = maps.qhi = maps.qlo = maps.q;  // never read: no sequence may have cached keys
     maps.vc = maps.vn;
   }
-  const Fp8Work work{reinterpret_cast<int32_t*>(w + L.plan), reinterpret_cast<int32_t*>(w + L.cnt),
+  const Fp8Work work{reinterpret_cast<int32_t*>(w + L.cnt), reinterpret_cast<int32_t*>(w + L.plan),
                      reinterpret_cast<float*>(w + L.ml), reinterpret_cast<float*>(w + L.o)};
   const cudaError_t e = L.mt == 2 ? launch_fp8<2>(p, maps, work, G, L.grid, s) : launch_fp8<1>(p, maps, work, G, L.grid, s);
   return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;

@@ -728,7 +728,7 @@ def verify_attn_fp8_workspace_bytes(args: AttnFp8Args) -> int:
 
 def verify_attn_fp8_workspace(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, batch: Batch, tau):
     """A zeroed workspace for verify_attn_fp8 on these arguments, to be kept
-    for later calls of the same sizes on the same stream."""
+    for later calls on the same stream, of any sizes that ask for no more."""
     a = attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, q, batch, tau)
     return _workspace(verify_attn_fp8_workspace_bytes(a), q.device)
 

@@ -742,7 +742,9 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * max_cache / max_new / max_block as ssv_verify_attn.  scale 0 means
  * 1/sqrt(d).  o overlaps no input (checked for q, k_new and v_new).
  * Workspace: ssv_verify_attn_fp8_workspace bytes, 256-byte aligned, zero
- * before its first use (see the conventions).
+ * before its first use (see the conventions).  Its counters lie at a place
+ * and in an extent that no argument changes: one workspace, at least as large
+ * as each call asks for, serves calls of any sizes one after the other.
  * Errors: SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED (d, heads), SSV_ERR_WORKSPACE,
  * SSV_ERR_CUDA; on device SSV_ERR_BAD_TAU, SSV_ERR_TIMEOUT, and
  * SSV_ERR_INVALID for a sequence outside the buffers or with a page outside

@@ -110,15 +110,18 @@ struct TcMaps {
   CUtensorMap q, kc, vc, kn, vn;
 };
 
+// The counters lie at the front of the workspace, in an area whose size no
+// argument of a call changes, and nothing else is ever written there: zero
+// again after a call of any sizes, they are zero before a call of any other.
 struct TcWork {
+  int32_t* cnt;    // [grid][2][4] arrival counters of the unit that a CTA merges (zero between calls)
   int32_t* plan;   // [grid][4][batch + 1] per-CTA planning tables
-  int32_t* cnt;    // [units][MT][4] arrival counters (zero between calls)
   float* part_ml;  // [2 * grid][MT][128][2]  running max (log2 domain), sum
   float* part_o;   // [2 * grid][MT][D / 4][128][4] unnormalised O (see part_o_at)
 };
 
 // Release increment (no return value, so no round trip) and a bounded
-// acquire poll for the per-(unit, tile, row group) arrival counters.
+// acquire poll for the per-(merging CTA, tile, row group) arrival counters.
 __device__ __forceinline__ void red_release_add(int32_t* p, int v) {
   asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -148,12 +151,12 @@ __device__ __forceinline__ float4* part_o_at(float* part_o, size_t slot_row, int
   return reinterpret_cast<float4*>(part_o + (slot_row >> 7) * (128 * D)) + (size_t)c4 * 128 + (slot_row & 127);
 }
 
-// Per head: W key blocks, U units, Pe owning CTAs and Wc cost units; this
+// Per head: W key blocks, Pe owning CTAs and Wc cost units; this
 // CTA's head g and its range [begin, end) of the head's blocks, which starts
 // at block k0 of unit u0.
 struct PlanHdr {
   long long Wc;
-  int W, U, Pe, g, begin, end, u0, k0;
+  int W, Pe, g, begin, end, u0, k0;
 };
 static_assert(8 * B_COUNT + 8 + sizeof(PlanHdr) <= 256, "barrier area overflow");
 
@@ -290,7 +293,6 @@ attn_tc_kernel(const __grid_constant__ TcMaps maps, const AttnParams p, const Tc
       s_prefC[0] = 0;
       PlanHdr h;
       h.W = carryB;  // key blocks per head
-      h.U = carryU;  // units per head
       // CTAs per head: all of them, unless there are no more units than CTAs and one CTA
       // per unit finishes sooner than spreading the head's blocks over all of them, which
       // splits units and costs a merge (about kMergeBlocks key blocks of time).
@@ -366,7 +368,7 @@ attn_tc_kernel(const __grid_constant__ TcMaps maps, const AttnParams p, const Tc
   // own predecessor before letting this one start, is the only one running.
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  const int begin = plan->begin, end = plan->end, Ph = plan->Pe, Uh = plan->U;
+  const int begin = plan->begin, end = plan->end, Ph = plan->Pe;
   const long long Wc = plan->Wc;
   const int gh = plan->g;           // kv head served by this CTA
   const int rank = cta / p.Hkv;     // rank among the CTAs of head gh
@@ -1015,7 +1017,8 @@ attn_tc_kernel(const __grid_constant__ TcMaps maps, const AttnParams p, const Tc
             const int c_a = owner_at(cu + kSegCost);                                   // ranks of head gh holding
             const int c_b = owner_at(cu + kSegCost + (long long)unit_weight(x.rows, x.row0, UR, R, MT) *
                                                           (x.nblocks - 1));                 // the first, last block
-            int32_t* counter = work.cnt + (((size_t)gh * Uh + u) * MT + mt) * 4 + q4;
+            // (a cut unit ends c_a's range, so a CTA merges one unit at most)
+            int32_t* counter = work.cnt + ((c_a * p.Hkv + gh) * 2 + mt) * 4 + q4;
             // partial slot of rank rr (> c_a): its piece is the first segment of its range
             auto slot_of = [&](int rr) -> size_t { return ((size_t)((rr * p.Hkv + gh) * 2) * MT + mt) * 128 + m; };
             if (rank != c_a) {
@@ -1219,23 +1222,19 @@ static int choose_mt(const AttnParams& p) {
 }
 
 struct WsLayout {
-  size_t plan, cnt, ml, o, total;
-  int grid, mt, units;
+  size_t cnt, plan, ml, o, total;
+  int grid, mt;
 };
 
 static WsLayout ws_layout(const AttnParams& p) {
   WsLayout L;
-  const int G = p.Hq / p.Hkv;
   L.mt = choose_mt(p);
-  const int UR = L.mt * (128 / G);
-  const long long max_rows = (long long)p.max_new + (p.prompt_only ? 1LL : 2LL) * p.max_block;
-  L.units = (int)((long long)p.batch * p.Hkv * ((max_rows + UR - 1) / UR));
   L.grid = sm_count();
   size_t off = 0;
+  L.cnt = off;  // first, and of one size: see TcWork
+  off = align_up(off + sizeof(int32_t) * (size_t)L.grid * 2 * 4, 256);
   L.plan = off;
   off = align_up(off + sizeof(int32_t) * (size_t)L.grid * 4 * (p.batch + 1), 256);
-  L.cnt = off;
-  off = align_up(off + sizeof(int32_t) * (size_t)L.units * L.mt * 4, 256);
   L.ml = off;
   off = align_up(off + sizeof(float) * 2 * (size_t)(2 * L.grid) * L.mt * 128, 256);
   L.o = off;

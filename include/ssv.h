@@ -20,7 +20,13 @@
  *    paths.  Scratch space is caller-provided ("workspace"), sized by the
  *    matching *_workspace query, 256-byte aligned, and must be all-zero
  *    when first used: each call leaves the zero-initialised counter area
- *    zero again on exit.
+ *    zero again on exit.  The attention entry points (ssv_verify_attn,
+ *    ssv_tree_verify_attn, ssv_verify_attn_fp8) keep their counters at a
+ *    place and in an extent that no argument changes, the same for the three:
+ *    one workspace, at least as large as each call asks for, serves them with
+ *    any sizes, one after the other.  ssv_accept and ssv_lmhead_accept lay
+ *    theirs out by the call: clear a workspace before calls of another batch,
+ *    total_slots, V, hidden or mode, or of another entry point, use it.
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls are
  *    asynchronous on it.  Host-side validation errors return synchronously
  *    and launch nothing.
@@ -742,9 +748,8 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * max_cache / max_new / max_block as ssv_verify_attn.  scale 0 means
  * 1/sqrt(d).  o overlaps no input (checked for q, k_new and v_new).
  * Workspace: ssv_verify_attn_fp8_workspace bytes, 256-byte aligned, zero
- * before its first use (see the conventions).  Its counters lie at a place
- * and in an extent that no argument changes: one workspace, at least as large
- * as each call asks for, serves calls of any sizes one after the other.
+ * before its first use; it serves calls of any sizes that ask for no more
+ * (see the conventions).
  * Errors: SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED (d, heads), SSV_ERR_WORKSPACE,
  * SSV_ERR_CUDA; on device SSV_ERR_BAD_TAU, SSV_ERR_TIMEOUT, and
  * SSV_ERR_INVALID for a sequence outside the buffers or with a page outside

@@ -47,7 +47,7 @@ struct Commit8Params {
   float *k_scale, *v_scale;
   const int32_t* pages;
   const ssv_seq* seqs;
-  const int32_t *tau, *n_acc;
+  const int32_t *tau, *n_acc, *cache_len;
   int32_t *new_len, *dev_status;
   int64_t k_stride, v_stride;  // bytes
   int Hkv, ps_log2, n_pages, table_len, batch, total_rows, total_slots, max_new, max_block, chunk_rows, chunks, groups, ctas_y;
@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(kC8Threads, sizeof(T) == 2 ? 4 : 2) commit_fp8
     }
     if (lane == 0) {
       if (bad) report(p.dev_status, bad);
-      p.new_len[b] = bad ? -1 : (seq_idle(s) ? s.cache_len : s.cache_len + s.new_len + na);
+      if (!bad && !seq_idle(s)) p.new_len[b] = s.cache_len + s.new_len + na;
+      else if (p.cache_len) p.new_len[b] = p.cache_len[b];  // (which may be new_len itself)
+      else p.new_len[b] = bad ? -1 : s.cache_len;
     }
     return;
   }
@@ -330,7 +332,7 @@ extern "C" ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream)
   const int per_cta = (kC8Threads / 32) / (a->page_size / 16);  // heads of K or V per CTA
   Commit8Params p{static_cast<const uint8_t*>(a->k_new), static_cast<const uint8_t*>(a->v_new),
                   static_cast<uint8_t*>(a->k_cache), static_cast<uint8_t*>(a->v_cache), a->k_scale, a->v_scale,
-                  a->pages, a->seqs, a->tau, a->n_acc, a->new_len, a->dev_status, ks * es, vs * es, a->Hkv,
+                  a->pages, a->seqs, a->tau, a->n_acc, a->cache_len, a->new_len, a->dev_status, ks * es, vs * es, a->Hkv,
                   ilog2(a->page_size), a->n_pages, a->table_len, a->batch, a->total_rows, a->total_slots, a->max_new,
                   a->max_block, 16, 0, (2 * a->Hkv + per_cta - 1) / per_cta, 0};
   for (;; p.chunk_rows *= 2) {

@@ -146,7 +146,7 @@ class CommitFp8Args(C.Structure):
                 ("page_size", C.c_int32), ("n_pages", C.c_int32), ("table_len", C.c_int32), ("seqs", C.c_void_p),
                 ("batch", C.c_int32), ("tau", C.c_void_p), ("n_acc", C.c_void_p), ("new_len", C.c_void_p),
                 ("total_rows", C.c_int32), ("total_slots", C.c_int32), ("max_new", C.c_int32),
-                ("max_block", C.c_int32), ("dev_status", C.c_void_p)]
+                ("max_block", C.c_int32), ("dev_status", C.c_void_p), ("cache_len", C.c_void_p)]
 
 
 _lib = None
@@ -750,18 +750,22 @@ def verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, 
 
 
 def commit_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch: Batch, tau, n_acc, new_len=None,
-               dev_status=None, stream=None):
+               dev_status=None, stream=None, cache_len=None):
     """Quantises and appends each sequence's fresh prompt rows and accepted
     data rows (stage order) to its pages, in place; returns new_len [batch]
-    int32 device (-1 for a sequence rejected on the device)."""
+    int32 device.  cache_len: the lengths that page_plan was given, which the
+    requests that it left idle and the sequences rejected here keep (a loop
+    passes them; without them such a sequence gets its record's cache_len, 0
+    in page_plan's idle records, or -1)."""
     torch = _torch()
     what = "ssv_commit_fp8"
     hkv, ps, d, n = _paged_cache(k_cache, v_cache, k_scale, v_scale, pages, what)
     rows = k_new.shape[0]
     if k_new.dtype != v_new.dtype or k_new.shape != (rows, hkv, d) or v_new.shape != k_new.shape:
         raise SsvError(SSV_ERR_INVALID, f"{what}: fresh rows")
-    _int32(what, pages, batch.dev, tau, n_acc, new_len)
-    if n_acc.shape[0] != batch.batch or (new_len is not None and new_len.shape[0] != batch.batch):
+    _int32(what, pages, batch.dev, tau, n_acc, new_len, cache_len)
+    if n_acc.shape[0] != batch.batch or (new_len is not None and new_len.shape[0] != batch.batch) or \
+            (cache_len is not None and cache_len.shape[0] != batch.batch):
         raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
     if new_len is None:
         new_len = torch.empty(batch.batch, dtype=torch.int32, device=k_new.device)
@@ -769,9 +773,9 @@ def commit_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch: B
                      v_scale.data_ptr(), pages.data_ptr(), _rows_strided(k_new, what), _rows_strided(v_new, what),
                      _dtype_code(k_new), hkv, d, ps, n, pages.numel(), batch.dev.data_ptr(), batch.batch,
                      tau.data_ptr(), n_acc.data_ptr(), new_len.data_ptr(), rows, tau.shape[0], batch.max_new,
-                     batch.max_block, _addr(dev_status))
-    _launch(what, (k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch.dev, tau, n_acc, new_len, dev_status),
-            a, stream)
+                     batch.max_block, _addr(dev_status), _addr(cache_len))
+    _launch(what, (k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch.dev, tau, n_acc, new_len, dev_status,
+                   cache_len), a, stream)
     return new_len
 
 

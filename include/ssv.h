@@ -638,7 +638,8 @@ SSV_API ssv_status ssv_tree_accept(const ssv_tree_accept_args* a, void* workspac
 /* ------------------------------------------------------------------------
  * ssv_page_plan -- the tables of a pass from the lengths of its requests,
  * built on the device (lengths known only there, such as ssv_commit_fp8's
- * new_len, never travel to the host).
+ * new_len, never travel to the host; ssv_commit_fp8 is then given cache_len,
+ * from which the requests that this call leaves idle keep their lengths).
  * Per request b, in batch order (all arrays device int32):
  *   cache_len[b] < 0: the request has ended.  The held[b] pages at the front
  *     of its table row go back to the free stack (table order), held_out = 0,
@@ -810,8 +811,15 @@ SSV_API ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* workspa
  * SSV_ERR_BAD_TAU and SSV_ERR_INVALID as ssv_commit, also for a sequence
  * whose rows leave [0, total_rows), whose N or B exceeds max_new or max_block,
  * whose touched pages leave the table or name a page outside [0, n_pages):
- * nothing of that sequence is written and its new_len is -1.  An idle record
- * gets new_len = cache_len.  No workspace; asynchronous on `stream`.
+ * nothing of that sequence is written.
+ * new_len[b]: C + N + n_acc of a sequence that was appended to.  Of any other
+ * -- an idle record, a rejected sequence -- cache_len[b] where the lengths
+ * that ssv_page_plan was given are passed on (device [batch], may be new_len
+ * itself): a request that got no pages keeps its length, an ended one stays
+ * ended, and a rejected one keeps its tokens (dev_status tells).  Without
+ * them: the record's cache_len (0 in ssv_page_plan's idle records) and -1; a
+ * loop that feeds new_len to its next ssv_page_plan has to pass them.
+ * No workspace; asynchronous on `stream`.
  * ---------------------------------------------------------------------- */
 typedef struct {
   const void* k_new;
@@ -832,6 +840,7 @@ typedef struct {
   int32_t total_rows, total_slots;
   int32_t max_new, max_block;
   int32_t* dev_status;         /* device, may be NULL */
+  const int32_t* cache_len;    /* device [batch], may be NULL: lengths before the pass */
 } ssv_commit_fp8_args;
 
 SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);

@@ -151,16 +151,17 @@ def gather_cache(seq, pages, codes, scale):
     return out
 
 
-def commit_pages(seqs, pages, tau_all, n_acc, fresh, codes, scale):
+def commit_pages(seqs, pages, tau_all, n_acc, fresh, codes, scale, cache_len=None):
     """Appends rows of `fresh` (float64 [rows, Hkv, d]) to one of K / V;
-    returns (codes, scale, new_len).  Idle records keep their length."""
+    returns (codes, scale, new_len).  Idle records keep their length, that of
+    `cache_len` where it is given."""
     codes, scale = codes.copy(), scale.copy()
     ps = codes.shape[2]
     new_len = np.zeros(len(seqs), np.int64)
     for b, s in enumerate(np.asarray(seqs)):
         C, N, B, q_off, kv, t_off = (int(v) for v in s)
         if N == 0 and B == 0:
-            new_len[b] = C
+            new_len[b] = C if cache_len is None else cache_len[b]
             continue
         rows = committed_rows(N, B, tau_all[t_off:t_off + B], int(n_acc[b]))
         new_len[b] = C + len(rows)

@@ -26,3 +26,14 @@ def test_attn_workspace_counters_have_one_place(L):
     assert need(max_new=2048) == need(max_new=100)
     if not torch.cuda.is_available():
         assert need(batch=47) - need(batch=31) == 152 * 16 * 16
+
+
+def test_commit_refuses_lengths_of_another_batch():
+    seqs = torch.zeros((2, 6), dtype=torch.int32)
+    batch = ssv.Batch.from_device(seqs, 8, 4, 10, 0, 2)
+    tau, acc = torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    cache, scale = torch.zeros((3, 2, 16, 128), dtype=torch.uint8), torch.zeros((3, 2))
+    pages, rows = torch.zeros(6, dtype=torch.int32), torch.zeros((8, 2, 128), dtype=torch.bfloat16)
+    for bad in (acc[:1], acc.long(), torch.zeros(4, dtype=torch.int32)[::2]):
+        with pytest.raises(ssv.SsvError, match="shapes|contiguous int32"):
+            ssv.commit_fp8(rows, rows, cache, cache, scale, scale, pages, batch, tau, acc, cache_len=bad)

@@ -94,6 +94,9 @@ constexpr float kLazy = 8.f;                // the running maximum may lag by 2^
 constexpr float kWeight = 7.f;              // P holds weights times 2^7
 constexpr float kUnitTop = 7.f;             // vs / 2^u <= 2^7: |code| vs / 2^u < 2^16 in fp16
 constexpr float kUnitRoom = 2.f;            // u leaves that much for larger scales to come
+// u goes no lower, however small the cached values are (2^-100 is the scale of zero pages): weights of fresh keys are
+// then at most 2^(7 + 8 + 64), and O in units of 2^u holds sums of weights times fresh values up to 2^48.
+constexpr float kUnitMin = -64.f;
 constexpr int SC = 20;                      // words of a block's scales: K factor of every 16 keys x 8, vs / 2^u of
                                             // every 16 keys as an fp16 pair x 8, u
 // Estimated costs of the plan, in units of 0.1 us: a block of one / two tiles
@@ -767,7 +770,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         float top = lv16;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (i == 0 || top > unit + kUnitTop) unit = ceilf(top) + kUnitRoom - kUnitTop;
+        if (i == 0 || top > unit + kUnitTop) unit = fmaxf(ceilf(top) + kUnitRoom - kUnitTop, kUnitMin);
         if (nc >= NSC && !warp_wait(bar(B_C_EMPTY + nc % NSC), empty_par(nc, NSC))) { run = false; break; }
         float* sc = reinterpret_cast<float*>(smem + C_::SM_SC) + (nc % NSC) * SC;
         if (lane < 8) {

@@ -742,8 +742,12 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * still meets a zero weight); rows of other sequences, rows of a page behind
  * token C - 1 and pages that are not a sequence's own never influence it,
  * whatever they hold.  scales: positive and finite; a value scale enters as a
- * 16-bit float beside the largest met so far in its unit of work, exactly for
- * the powers of two within 2^22 of it that ssv_commit_fp8 writes.
+ * 16-bit float beside the largest met so far in its unit of work, or beside
+ * 2^-59 where that is larger, exactly for the powers of two within 2^22 of it
+ * that ssv_commit_fp8 writes.  Beside value scales above 2^96, weights of
+ * fresh keys below 2^-42 of the row's largest count as none (below 2^-11 at
+ * the largest scale, 2^127).  Sums of weights times fresh values beside cached
+ * values of less than 2^-59 have to stay below 2^48.
  * d = 128; Hq % Hkv == 0, Hq / Hkv <= 128; 1 <= B <= 64; n_pages * Hkv *
  * page_size < 2^31; pointers 16-byte aligned, strides multiples of 8.
  * max_cache / max_new / max_block as ssv_verify_attn.  scale 0 means

@@ -567,6 +567,8 @@ def _launch(what: str, tensors, block, stream, workspace=None):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise SsvError(SSV_ERR_INVALID, f"{what}: tensors of one CUDA device")
+    if workspace is not None and not workspace.is_contiguous():
+        raise SsvError(SSV_ERR_WORKSPACE, f"{what}: the workspace is contiguous")
     _launch_on(what, dev, block, stream, workspace)
 
 
@@ -600,6 +602,8 @@ def _rows_strided(t, what: str) -> int:
     (rows, heads, d), s = t.shape, t.stride()
     if rows and (s[2] != 1 or (s[1] != d and heads > 1)):
         raise SsvError(SSV_ERR_INVALID, f"{what}: [rows, heads, d] with contiguous heads")
+    if rows > 1 and s[0] < heads * d:  # one row repeated (stride 0, which the library reads as packed), or rows that overlap
+        raise SsvError(SSV_ERR_INVALID, f"{what}: rows that do not overlap")
     return s[0] if rows > 1 else heads * d
 
 

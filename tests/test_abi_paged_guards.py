@@ -37,3 +37,40 @@ def test_commit_refuses_lengths_of_another_batch():
     for bad in (acc[:1], acc.long(), torch.zeros(4, dtype=torch.int32)[::2]):
         with pytest.raises(ssv.SsvError, match="shapes|contiguous int32"):
             ssv.commit_fp8(rows, rows, cache, cache, scale, scale, pages, batch, tau, acc, cache_len=bad)
+
+
+def test_rows_that_share_memory_are_refused():
+    """One row expanded over all (row stride 0) or rows that overlap: the library would read rows that are not there."""
+    seqs = torch.zeros((2, 6), dtype=torch.int32)
+    batch = ssv.Batch.from_device(seqs, 8, 4, 10, 0, 2)
+    tau, acc = torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    cache, scale = torch.zeros((3, 2, 16, 128), dtype=torch.uint8), torch.zeros((3, 2))
+    pages, w = torch.zeros(6, dtype=torch.int32), torch.ones(128, dtype=torch.bfloat16)
+    rows, q = torch.zeros((8, 2, 128), dtype=torch.bfloat16), torch.zeros((8, 4, 128), dtype=torch.bfloat16)
+    c = (cache, cache, scale, scale, pages)
+
+    def shared(heads):
+        yield torch.zeros((1, heads, 128), dtype=torch.bfloat16).expand(8, heads, 128)
+        yield torch.zeros((4096,), dtype=torch.bfloat16).as_strided((8, heads, 128), (128, 128, 1))
+
+    for r in shared(2):
+        for f in (lambda: ssv.norm_rope_copy(q, r, w, w, batch, k_out=rows),
+                  lambda: ssv.norm_rope_copy(q, r, w, w, batch),
+                  lambda: ssv.norm_rope_copy(q, rows, w, w, batch, k_out=r),
+                  lambda: ssv.verify_attn_fp8(q, *c, r, rows, batch, tau),
+                  lambda: ssv.verify_attn_fp8(q, *c, rows, r, batch, tau),
+                  lambda: ssv.commit_fp8(r, rows, *c, batch, tau, acc),
+                  lambda: ssv.commit_fp8(rows, r, *c, batch, tau, acc)):
+            with pytest.raises(ssv.SsvError, match="rows that do not overlap"):
+                f()
+    for r in shared(4):
+        with pytest.raises(ssv.SsvError, match="rows that do not overlap"):
+            ssv.norm_rope_copy(r, rows, w, w, batch, q_out=q)
+    assert ssv._rows_strided(rows[:1].expand(1, 2, 128), "") == 0       # a single row is itself
+    assert ssv._rows_strided(torch.zeros((8, 6, 128))[:, 2:4], "") == 6 * 128
+
+
+def test_workspace_of_one_element_expanded_is_refused():
+    q = torch.zeros((8, 4, 128), dtype=torch.bfloat16)
+    with pytest.raises(ssv.SsvError, match="the workspace is contiguous"):
+        ssv._launch("ssv_verify_attn_fp8", (q,), b"", None, torch.zeros(1, dtype=torch.uint8).expand(1 << 24))

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import struct
+from contextlib import nullcontext
 from typing import Optional
 
 import numpy as np
@@ -235,6 +236,14 @@ def _stream_ptr(stream) -> Optional[int]:
     return s.cuda_stream
 
 
+def _on(stream):
+    """Where a call makes its outputs and its scratch: on the stream that it
+    runs on.  They are then filled in that stream's order, and their memory goes
+    back to that stream's allocations; like any tensor of that stream they are
+    waited for before another one uses them."""
+    return nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.float32:
@@ -332,10 +341,11 @@ def verify_attn(q, k_cache, v_cache, k_new, v_new, batch: Batch, tau, out=None, 
                 scale: float = 0.0, workspace=None, dev_status=None, stream=None):
     """Verification attention; returns O [rows, Hq, d]."""
     torch = _torch()
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-    a = attn_args(q, k_cache, v_cache, k_new, v_new, out, batch, tau, scale, dev_status)
-    ws = _workspace(verify_attn_workspace_bytes(a), q.device, workspace)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        a = attn_args(q, k_cache, v_cache, k_new, v_new, out, batch, tau, scale, dev_status)
+        ws = _workspace(verify_attn_workspace_bytes(a), q.device, workspace)
     _check(lib().ssv_verify_attn(C.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
            "ssv_verify_attn")
     return out
@@ -364,13 +374,15 @@ def accept(mode, T, logits, draft_tokens, tau, block, gamma, slot_off, draft_log
     torch = _torch()
     dev = logits.device
     if out is None:
-        out = (torch.empty(block.shape[0], dtype=torch.int32, device=dev),
-               torch.empty(block.shape[0], dtype=torch.int32, device=dev),
-               torch.empty(draft_tokens.shape[0], dtype=torch.int32, device=dev))
+        with _on(stream):
+            out = (torch.empty(block.shape[0], dtype=torch.int32, device=dev),
+                   torch.empty(block.shape[0], dtype=torch.int32, device=dev),
+                   torch.empty(draft_tokens.shape[0], dtype=torch.int32, device=dev))
     n_acc, n_out, tokens = out
     a = accept_args(mode, T, logits, draft_tokens, tau, block, gamma, slot_off, n_acc, n_out, tokens,
                     draft_logits, noise, noise_row, u_accept, u_sample, max_block, dev_status, noise_seed)
-    ws = _workspace(accept_workspace_bytes(a), dev, workspace)
+    with _on(stream):
+        ws = _workspace(accept_workspace_bytes(a), dev, workspace)
     _check(lib().ssv_accept(C.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
            "ssv_accept")
     return n_acc, n_out, tokens
@@ -385,9 +397,10 @@ def accept_noalloc(mode, T, logits, draft_tokens, tau, block, gamma, slot_off, d
     torch = _torch()
     dev = logits.device
     if out is None:
-        out = (torch.empty(block.shape[0], dtype=torch.int32, device=dev),
-               torch.empty(block.shape[0], dtype=torch.int32, device=dev),
-               torch.empty(draft_tokens.shape[0], dtype=torch.int32, device=dev))
+        with _on(stream):
+            out = (torch.empty(block.shape[0], dtype=torch.int32, device=dev),
+                   torch.empty(block.shape[0], dtype=torch.int32, device=dev),
+                   torch.empty(draft_tokens.shape[0], dtype=torch.int32, device=dev))
     n_acc, n_out, tokens = out
     a = accept_args(mode, T, logits, draft_tokens, tau, block, gamma, slot_off, n_acc, n_out, tokens,
                     draft_logits, noise, noise_row, u_accept, u_sample, max_block, dev_status, noise_seed)
@@ -414,7 +427,8 @@ def commit(k_new, v_new, k_dst, v_dst, batch: Batch, tau, n_acc, dst_off, dst_ca
     if tuple(k_dst.shape[1:]) != tuple(k_new.shape[1:]) or v_dst.shape != k_dst.shape or v_new.shape != k_new.shape:
         raise SsvError(SSV_ERR_INVALID, "ssv_commit: row shapes differ")
     if new_len is None:
-        new_len = torch.empty(batch.batch, dtype=torch.int32, device=k_new.device)
+        with _on(stream):
+            new_len = torch.empty(batch.batch, dtype=torch.int32, device=k_new.device)
     a = commit_args(k_new, v_new, k_dst, v_dst, batch, tau, n_acc, dst_off, dst_cap, new_len, dev_status)
     _check(lib().ssv_commit(C.byref(a), _stream_ptr(stream)), "ssv_commit")
     return new_len
@@ -445,13 +459,15 @@ def lmhead_accept(mode, T, hidden_states, lm_head, draft_tokens, tau, block, gam
         raise SsvError(SSV_ERR_INVALID, "ssv_lmhead_accept: shapes")
     dev = hidden_states.device
     if out is None:
-        out = (torch.empty(block.shape[0], dtype=torch.int32, device=dev),
-               torch.empty(block.shape[0], dtype=torch.int32, device=dev),
-               torch.empty(draft_tokens.shape[0], dtype=torch.int32, device=dev))
+        with _on(stream):
+            out = (torch.empty(block.shape[0], dtype=torch.int32, device=dev),
+                   torch.empty(block.shape[0], dtype=torch.int32, device=dev),
+                   torch.empty(draft_tokens.shape[0], dtype=torch.int32, device=dev))
     n_acc, n_out, tokens = out
     a = lmhead_args(mode, T, hidden_states, lm_head, draft_tokens, tau, block, gamma, slot_off, n_acc, n_out,
                     tokens, noise, noise_row, dev_status)
-    ws = _workspace(lmhead_accept_workspace_bytes(a), dev, workspace)
+    with _on(stream):
+        ws = _workspace(lmhead_accept_workspace_bytes(a), dev, workspace)
     _check(lib().ssv_lmhead_accept(C.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
            "ssv_lmhead_accept")
     return n_acc, n_out, tokens
@@ -491,11 +507,12 @@ def tree_verify_attn(q, k_cache, v_cache, k_new, v_new, seqs, parent, pos, total
     uint8 device tensor of tree_verify_attn_workspace_bytes (allocated here
     when not given)."""
     torch = _torch()
-    if out is None:
-        out = torch.zeros((int(total_out), q.shape[1], q.shape[2]), dtype=out_dtype or q.dtype, device=q.device)
-    a = tree_attn_args(q, k_cache, v_cache, k_new, v_new, out, seqs, parent, pos, total_out, max_cache, scale,
-                       dev_status)
-    ws = _workspace(tree_verify_attn_workspace_bytes(a), q.device, workspace)
+    with _on(stream):
+        if out is None:
+            out = torch.zeros((int(total_out), q.shape[1], q.shape[2]), dtype=out_dtype or q.dtype, device=q.device)
+        a = tree_attn_args(q, k_cache, v_cache, k_new, v_new, out, seqs, parent, pos, total_out, max_cache, scale,
+                           dev_status)
+        ws = _workspace(tree_verify_attn_workspace_bytes(a), q.device, workspace)
     _check(lib().ssv_tree_verify_attn(C.byref(a), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                                       _stream_ptr(stream)), "ssv_tree_verify_attn")
     return out
@@ -518,15 +535,17 @@ def tree_accept(mode, T, logits, seqs, parent, pos, token, noise=None, noise_row
     torch = _torch()
     dev = logits.device
     b = seqs.shape[0]
-    n_acc = torch.empty(b, dtype=torch.int32, device=dev)
-    path = torch.empty((b, 64), dtype=torch.int32, device=dev)
-    ep = torch.empty(b, dtype=torch.int32, device=dev)
-    et = torch.empty(b, dtype=torch.int32, device=dev)
+    with _on(stream):
+        n_acc = torch.empty(b, dtype=torch.int32, device=dev)
+        path = torch.empty((b, 64), dtype=torch.int32, device=dev)
+        ep = torch.empty(b, dtype=torch.int32, device=dev)
+        et = torch.empty(b, dtype=torch.int32, device=dev)
     a = tree_accept_args(mode, T, logits, seqs, parent, pos, token, n_acc, path, ep, et, noise, noise_row, pos_off,
                          dev_status)
     n = C.c_size_t(0)
     _check(lib().ssv_tree_accept_workspace(C.byref(a), C.byref(n)), "ssv_tree_accept_workspace")
-    ws = _workspace(int(n.value), dev, workspace)
+    with _on(stream):
+        ws = _workspace(int(n.value), dev, workspace)
     _check(lib().ssv_tree_accept(C.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
            "ssv_tree_accept")
     return n_acc, path, ep, et
@@ -652,7 +671,8 @@ def page_plan(cache_len, new_len, block, held, pages, free_list, n_free, page_si
     total_rows = int(total_rows)
     if out is None:
         # one allocation: the table, the offsets, the counts, the stack height, the slot map
-        buf = torch.empty(8 * batch + 1 + total_rows, dtype=i32, device=cache_len.device)
+        with _on(stream):
+            buf = torch.empty(8 * batch + 1 + total_rows, dtype=i32, device=cache_len.device)
         seqs, slot_off, held_out, n_out, slot_map = buf.split_with_sizes([6 * batch, batch, batch, 1, total_rows])
         out = (seqs.view(batch, 6), slot_map, slot_off, held_out, n_out)
         at = buf.data_ptr()
@@ -666,7 +686,7 @@ def page_plan(cache_len, new_len, block, held, pages, free_list, n_free, page_si
                    total_rows, *outs, _addr(dev_status))
     _launch_on(what, dev, a, stream)
     if batch == 0:  # the call writes nothing: no rows, and the stack as it was
-        with torch.cuda.stream(stream):
+        with _on(stream):
             out[1].fill_(-1)
             out[4].copy_(n_free)
     return out
@@ -730,11 +750,13 @@ def verify_attn_fp8_workspace_bytes(args: AttnFp8Args) -> int:
     return int(n.value)
 
 
-def verify_attn_fp8_workspace(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, batch: Batch, tau):
+def verify_attn_fp8_workspace(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, batch: Batch, tau,
+                              stream=None):
     """A zeroed workspace for verify_attn_fp8 on these arguments, to be kept
     for later calls on the same stream, of any sizes that ask for no more."""
     a = attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, q, batch, tau)
-    return _workspace(verify_attn_fp8_workspace_bytes(a), q.device)
+    with _on(stream):
+        return _workspace(verify_attn_fp8_workspace_bytes(a), q.device)
 
 
 def verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, batch: Batch, tau, out=None,
@@ -743,11 +765,14 @@ def verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, 
     v_new bf16 (fresh rows may be strided).  Returns O [rows, Hq, d] bf16."""
     torch = _torch()
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     a = _attn_fp8_fields(q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch, tau, float(scale),
                          dev_status)
-    ws = workspace if workspace is not None else \
-        _workspace(verify_attn_fp8_workspace_bytes(AttnFp8Args(*a)), q.device)
+    ws = workspace
+    if ws is None:
+        with _on(stream):
+            ws = _workspace(verify_attn_fp8_workspace_bytes(AttnFp8Args(*a)), q.device)
     _launch("ssv_verify_attn_fp8", (q, k_cache, v_cache, k_scale, v_scale, pages, k_new, v_new, out, batch.dev, tau, ws,
                                     dev_status), _pack_attn(*a), stream, ws)
     return out
@@ -772,7 +797,8 @@ def commit_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch: B
             (cache_len is not None and cache_len.shape[0] != batch.batch):
         raise SsvError(SSV_ERR_INVALID, f"{what}: shapes")
     if new_len is None:
-        new_len = torch.empty(batch.batch, dtype=torch.int32, device=k_new.device)
+        with _on(stream):
+            new_len = torch.empty(batch.batch, dtype=torch.int32, device=k_new.device)
     a = _pack_commit(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                      v_scale.data_ptr(), pages.data_ptr(), _rows_strided(k_new, what), _rows_strided(v_new, what),
                      _dtype_code(k_new), hkv, d, ps, n, pages.numel(), batch.dev.data_ptr(), batch.batch,

@@ -74,3 +74,47 @@ def test_workspace_of_one_element_expanded_is_refused():
     q = torch.zeros((8, 4, 128), dtype=torch.bfloat16)
     with pytest.raises(ssv.SsvError, match="the workspace is contiguous"):
         ssv._launch("ssv_verify_attn_fp8", (q,), b"", None, torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
+
+
+def test_outputs_and_scratch_are_made_on_the_stream_of_the_call(L, monkeypatch):
+    """Tensors that a call makes itself are made under the stream that it was given."""
+    made, entered = [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            entered.append(self.stream)
+
+        def __exit__(self, *a):
+            entered.pop()
+
+    def spy(f):
+        def g(*a, **kw):
+            made.append(entered[-1] if entered else None)
+            return f(*a, **kw)
+        return g
+
+    seqs = torch.zeros((2, 6), dtype=torch.int32)
+    batch = ssv.Batch.from_device(seqs, 8, 4, 10, 0, 2)
+    tau, acc = torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    cache, scale = torch.zeros((3, 2, 16, 128), dtype=torch.uint8), torch.zeros((3, 2))
+    pages, i2, table = torch.zeros(6, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int32)
+    rows, q = torch.zeros((8, 2, 128), dtype=torch.bfloat16), torch.zeros((8, 4, 128), dtype=torch.bfloat16)
+    c = (cache, cache, scale, scale, pages)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch, "empty", spy(torch.empty))
+    monkeypatch.setattr(torch, "zeros", spy(torch.zeros))
+    s = object()
+    for call, n in ((lambda: ssv.verify_attn_fp8(q, *c, rows, rows, batch, tau, stream=s), 2),
+                    (lambda: ssv.verify_attn_fp8(q, *c, rows, rows, batch, tau, stream=s, workspace=ws), 1),
+                    (lambda: ssv.commit_fp8(rows, rows, *c, batch, tau, acc, stream=s), 1),
+                    (lambda: ssv.page_plan(i2, i2, i2, i2, table, i2, i2[:1], 16, 10, stream=s), 1)):
+        made.clear()
+        with pytest.raises(ssv.SsvError, match="one CUDA device"):
+            call()
+        assert made == [s] * n
+    made.clear()
+    assert ssv.verify_attn_fp8_workspace(q, *c, rows, rows, batch, tau, stream=s).numel() and made == [s]

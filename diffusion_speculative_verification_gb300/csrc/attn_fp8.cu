@@ -908,7 +908,8 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
         const int i = x.row0 + r_local;  // local query row
         const bool valid = m < R * G && r_local < x.nvalid;
         const bool warp_active = q4 * 32 < R * G && (mt * R + (q4 * 32) / G) < x.nvalid;
-        const float rowf = cached > 0 && valid ? __ldg(p.q_scale + (size_t)(x.q_off + i) * p.Hq + gh * G + hj) : 1.f;
+        // (the kernel that writes the factors may have run beside this one's start: not read as constant data)
+        const float rowf = cached > 0 && valid ? __ldcg(p.q_scale + (size_t)(x.q_off + i) * p.Hq + gh * G + hj) : 1.f;
         const bool prompt = i < x.N;
         const int r = i - x.N;
         uint32_t tm[6] = {0u, 0u, 0u, 0u, 0u, 0u};  // allowed tail keys of this row (in local memory: seldom read)
@@ -1295,7 +1296,7 @@ __global__ void __launch_bounds__(kSplitThreads) query_split_kernel(const uint4*
   const long long h = ((long long)blockIdx.x * kSplitThreads + threadIdx.x) >> 4;
   const int c = threadIdx.x & 15;
   uint4 v = make_uint4(0, 0, 0, 0);
-  if (h < heads) v = __ldg(q + h * 16 + c);
+  if (h < heads) v = __ldcg(q + h * 16 + c);  // (nor here: the kernel before may write q while this one starts)
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float x[8], amax = 0.f;
 #pragma unroll

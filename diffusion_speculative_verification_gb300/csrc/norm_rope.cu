@@ -149,8 +149,9 @@ norm_rope_kernel(const NormParams p, const __grid_constant__ NormTheta th) {
   };
   fetch(head0);
   const T *wq = static_cast<const T*>(p.q_w) + ch * VEC, *wk = static_cast<const T*>(p.k_w) + ch * VEC;
-  const uint4 wq1 = __ldg(reinterpret_cast<const uint4*>(wq)), wq2 = __ldg(reinterpret_cast<const uint4*>(wq + HALF));
-  const uint4 wk1 = __ldg(reinterpret_cast<const uint4*>(wk)), wk2 = __ldg(reinterpret_cast<const uint4*>(wk + HALF));
+  // plain loads, which stay behind the wait above: the kernel before may write the weights, too
+  const uint4 wq1 = *reinterpret_cast<const uint4*>(wq), wq2 = *reinterpret_cast<const uint4*>(wq + HALF);
+  const uint4 wk1 = *reinterpret_cast<const uint4*>(wk), wk2 = *reinterpret_cast<const uint4*>(wk + HALF);
   const bool table = p.batch <= kNormThreads;
   if (table && threadIdx.x < p.batch) s_seq[threadIdx.x] = p.seqs[threadIdx.x];
   __syncthreads();

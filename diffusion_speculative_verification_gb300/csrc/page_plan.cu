@@ -195,15 +195,18 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
   }
   for (int i = n_free + tid; i < A - taken; i += step) p.free_list[i] = stack(i);
   // the slot map: one row per thread while that covers it, else four per thread and step (one search, then along
-  // the requests), so that their loads are in flight together
+  // the requests), so that their loads are in flight together.  Rows are unsigned: the step behind the last of 2^31 - 1
+  // stays in range.
   const int mask = (1 << p.ps_log2) - 1, per_row = p.total_rows > step ? 4 : 1;
-  for (int row = per_row * tid; row < p.total_rows; row += per_row * step) {
+  const uint32_t total = p.total_rows;
+  for (uint32_t row = per_row * tid; row < total; row += per_row * step) {
     int b = last_le(s_q, n, row), slot[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (k >= per_row) break;
-      while (b + 1 < n && s_q[b + 1] <= row + k) ++b;
-      const int j = row + k - s_q[b];
+      if (k >= per_row || row + k >= total) break;
+      const int r = row + k;
+      while (b + 1 < n && s_q[b + 1] <= r) ++b;
+      const int j = r - s_q[b];
       slot[k] = -1;
       if (j < s_nb[b]) {
         const int t = s_c[b] + j, idx = t >> p.ps_log2;
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k < per_row && row + k < p.total_rows) p.slot_map[row + k] = slot[k];
+      if (k < per_row && row + k < total) p.slot_map[row + k] = slot[k];
   }
 }
 
@@ -260,7 +263,7 @@ extern "C" ssv_status ssv_page_plan(const ssv_page_plan_args* a, void* stream) {
                                         (int)(sizeof(int) * 6 * kPlanMaxBatch)));
     if (dev < 64) ready |= 1ull << dev;
   }
-  const int grid = min(152, max(1, (a->total_rows + kPlanRows - 1) / kPlanRows));
+  const int grid = min(152, max(1, a->total_rows / kPlanRows + (a->total_rows % kPlanRows > 0)));
   const cudaError_t e =
       launch_pdl(page_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;

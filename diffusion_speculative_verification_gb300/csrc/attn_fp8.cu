@@ -1188,7 +1188,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
             }
           };
           if (complete) {
-            const float inv = (l_sum > 0.f) ? 1.f / l_sum : 0.f;
+            const float inv = (l_sum > 0.f) ? 1.f / l_sum : NAN;  // (every row sees its own key)
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               float v[32];
@@ -1236,7 +1236,7 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(work.part_ml + slot_of(cc) * 2));
                 if (M > -INFINITY) L += ml.y * ex2(ml.x - M);
               }
-              const float inv = (L > 0.f) ? 1.f / L : 0.f;
+              const float inv = (L > 0.f) ? 1.f / L : NAN;
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
                 float v[32];
@@ -1305,7 +1305,10 @@ __global__ void __launch_bounds__(kSplitThreads) query_split_kernel(const uint4*
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+  for (int i = 0; i < 8; ++i) {
+    if (fabsf(x[i]) < INFINITY) amax = fmaxf(amax, fabsf(x[i]));
+    else x[i] = NAN;  // an infinity would be clamped
+  }
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   // smallest e >= -100 with amax <= 448 2^e = 1.75 2^(e + 8)

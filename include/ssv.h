@@ -739,9 +739,11 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * Hkv, d] bf16 device, rows k_stride / v_stride elements apart (0: Hkv * d).
  * Scores, softmax statistics and the accumulation of O are fp32.
  * A sequence's own fresh rows must be finite (a masked non-finite value row
- * still meets a zero weight); rows of other sequences, rows of a page behind
- * token C - 1 and pages that are not a sequence's own never influence it,
- * whatever they hold.  scales: positive and finite; a value scale enters as a
+ * still meets a zero weight).  A query (row, head) with an infinity or NaN
+ * gives NaN in its own row of o alone.  Rows of other sequences, rows of a
+ * page behind token C - 1 and pages that are not a sequence's own never
+ * influence it, whatever they hold.  scales: positive and finite; a value
+ * scale enters as a
  * 16-bit float beside the largest met so far in its unit of work, or beside
  * 2^-59 where that is larger, exactly for the powers of two within 2^22 of it
  * that ssv_commit_fp8 writes.  Beside value scales above 2^96, weights of

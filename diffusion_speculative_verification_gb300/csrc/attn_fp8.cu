@@ -73,6 +73,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <type_traits>
@@ -143,6 +144,7 @@ struct AttnFp8Params {
   long long wait_budget;
   int fault_skip;
   int early;  // the kernel before this one is the query split, which writes nothing but what warps 2 and 4..11 wait for
+  int ordered;  // the plan's sums are known to fit 32 bits only for sequences that share no rows: see fp8_layout
 };
 
 struct Fp8Maps {
@@ -361,31 +363,42 @@ attn_fp8_kernel(const __grid_constant__ Fp8Maps maps, const AttnFp8Params p, con
   if (warp == 0) {
     if (!p.early) pdl_wait();
     int carryU = 0, carryB = 0, carryC = 0, top = 0;  // top: blocks of the longest unit
+    int carryE = 0;                                   // end of the rows so far
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
       int units = 0, blocks = 0, cost = 0;
-      if (b < p.batch) {
-        const ssv_seq s = p.seqs[b];
-        if (!seq_idle(s)) {
-          const long long np = ((long long)s.cache_len + ps - 1) >> p.ps_log2;
-          const bool ok = s.cache_len >= 0 && s.new_len >= 0 && s.block >= 1 && s.block <= 64 && s.q_off >= 0 &&
-                          (long long)s.q_off + s.new_len + 2LL * s.block <= p.total_rows && s.kv_off >= 0 &&
-                          s.kv_off + np <= p.table_len && s.tau_off >= 0 &&
-                          (long long)s.tau_off + s.block <= p.total_slots && s.cache_len <= p.max_cache &&
-                          s.new_len <= p.max_new && s.block <= p.max_block;
-          if (!ok && cta == 0) report(p.dev_status, SSV_ERR_INVALID);
-          const int rows = s.new_len + 2 * s.block;
-          units = ok ? cdiv(rows, UR) : 0;
-#pragma unroll 1
-          for (int t = 0; t < units; ++t) {
-            const int nb = blocks_of(s.cache_len, s.new_len, rows, t * UR);
-            blocks += nb;
-            top = max(top, nb);
-            cost += kSegCost + cost_of(rows, t * UR) * nb;
-          }
+      ssv_seq s{};
+      if (b < p.batch) s = p.seqs[b];
+      const bool idle = seq_idle(s);
+      const int rows = s.new_len + 2 * s.block;
+      const long long np = ((long long)s.cache_len + ps - 1) >> p.ps_log2;
+      bool ok = s.cache_len >= 0 && s.new_len >= 0 && s.block >= 1 && s.block <= 64 && s.q_off >= 0 &&
+                (long long)s.q_off + s.new_len + 2LL * s.block <= p.total_rows && s.kv_off >= 0 &&
+                s.kv_off + np <= p.table_len && s.tau_off >= 0 && (long long)s.tau_off + s.block <= p.total_slots &&
+                s.cache_len <= p.max_cache && s.new_len <= p.max_new && s.block <= p.max_block;
+      if (p.ordered) {  // (behind a sequence whose rows it shares: refused)
+        int e = ok ? s.q_off + rows : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, e, o);
+          if (lane >= o) e = max(e, y);
         }
-        s_ntile[b] = units;
+        const int before = __shfl_up_sync(0xffffffffu, e, 1);
+        ok = ok && s.q_off >= (lane ? max(before, carryE) : carryE);
+        carryE = max(carryE, __shfl_sync(0xffffffffu, e, 31));
       }
+      if (!ok && !idle && cta == 0) report(p.dev_status, SSV_ERR_INVALID);
+      if (ok) {
+        units = cdiv(rows, UR);
+#pragma unroll 1
+        for (int t = 0; t < units; ++t) {
+          const int nb = blocks_of(s.cache_len, s.new_len, rows, t * UR);
+          blocks += nb;
+          top = max(top, nb);
+          cost += kSegCost + cost_of(rows, t * UR) * nb;
+        }
+      }
+      if (b < p.batch) s_ntile[b] = units;
       int iu = units, ib = blocks, ic = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -1369,7 +1382,7 @@ bool encode_rows(CUtensorMap* m, const void* base, int es, int heads, long long 
 
 struct Fp8Layout {
   size_t cnt, plan, ml, o, q, qs, total;
-  int grid, mt;
+  int grid, mt, ordered;
 };
 
 // Two tiles share a unit's keys where some sequence fills more than one.
@@ -1382,8 +1395,12 @@ bool fp8_layout(const ssv_attn_fp8_args* a, Fp8Layout* L) {
   const long long max_rows = (long long)a->max_new + 2LL * a->max_block;
   L->mt = max_rows > R ? 2 : 1;
   const long long tiles = (max_rows + (long long)L->mt * R - 1) / (L->mt * R);
-  const long long blocks = (long long)a->batch * tiles * (a->max_cache / BN + max_rows / BN + 2 + kSegCost / kBlock1 + 1);
-  if (blocks > (1LL << 30) / kBlock2 || a->Hkv > L->grid) return false;  // the plan's sums are 32-bit
+  // The plan's sums are 32-bit.  They hold for any records where every sequence may be as long as the longest; where
+  // not, sequences that share no rows have total_rows between them, which the kernel then checks of them.
+  const long long most = (1LL << 30) / kBlock2, per = a->max_cache / BN + max_rows / BN + 2 + kSegCost / kBlock1 + 1;
+  const long long units = std::min(a->batch * tiles, a->total_rows / ((long long)L->mt * R) + a->batch);
+  if (units > most / per || a->Hkv > L->grid) return false;
+  L->ordered = a->batch * tiles > most / per ? 1 : 0;
   size_t off = 0;
   L->cnt = off;  // first, and of one size: see Fp8Work
   off = align_up(off + sizeof(int32_t) * (size_t)L->grid * 2 * 4, 256);
@@ -1483,7 +1500,7 @@ extern "C" ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* ws, 
                   static_cast<__nv_bfloat16*>(a->o), a->Hq, a->Hkv, ilog2(a->page_size), a->n_pages, a->table_len,
                   a->scale > 0.f ? a->scale : (float)(1.0 / sqrt((double)a->d)), a->seqs, a->batch, a->tau,
                   a->total_rows, a->total_slots, max_cache, a->max_new, a->max_block, a->dev_status, f.budget, f.skip,
-                  max_cache > 0 ? 1 : 0};
+                  max_cache > 0 ? 1 : 0, L.ordered};
   Fp8Maps maps;
   if (!fp8_encode_fn()) return SSV_ERR_CUDA;
   if (!encode_rows(&maps.kn, a->k_new, 2, a->Hkv, a->total_rows, a->k_stride ? a->k_stride : width, 1, BN) ||

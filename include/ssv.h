@@ -761,7 +761,11 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * SSV_ERR_CUDA; on device SSV_ERR_BAD_TAU, SSV_ERR_TIMEOUT, and
  * SSV_ERR_INVALID for a sequence outside the buffers or with a page outside
  * [0, n_pages) among its first ceil(C / page_size) (skipped: its rows of o
- * are unspecified).
+ * are unspecified).  SSV_ERR_UNSUPPORTED also where the plan could pass 32
+ * bits: more than 2^30 / 12 blocks for total_rows / 64 + batch tiles of rows (64
+ * at a group of four) of the longest sequence that max_cache, max_new and
+ * max_block allow.  Where batch such sequences would pass it, sequences have
+ * to be in order without shared rows, which is then checked on the device.
  * Scheduling as ssv_verify_attn: one CTA per SM, and where a unit of work is
  * split the CTA with its first key block waits (bounded) for the others.
  * ---------------------------------------------------------------------- */

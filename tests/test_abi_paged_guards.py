@@ -118,3 +118,13 @@ def test_outputs_and_scratch_are_made_on_the_stream_of_the_call(L, monkeypatch):
         assert made == [s] * n
     made.clear()
     assert ssv.verify_attn_fp8_workspace(q, *c, rows, rows, batch, tau, stream=s).numel() and made == [s]
+
+
+def test_attn_bounds_of_many_requests_and_a_long_prompt(L):
+    """Units follow the rows there are, not batch times the longest: 1000 decoding requests beside a prompt of 32768."""
+    n = C.c_size_t(0)
+    big = dict(batch=1000, total_rows=33 * 1000 + 32768, total_slots=16000, max_cache=32768, max_new=32768, max_block=16)
+    assert L.ssv_verify_attn_fp8_workspace(C.byref(_attn(**big)), C.byref(n)) == ssv.SSV_OK
+    assert n.value < 2 << 30
+    big.update(total_rows=1 << 28, max_cache=1 << 20)
+    assert L.ssv_verify_attn_fp8_workspace(C.byref(_attn(**big)), C.byref(n)) == ssv.SSV_ERR_UNSUPPORTED

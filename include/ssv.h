@@ -658,8 +658,11 @@ SSV_API ssv_status ssv_tree_accept(const ssv_tree_accept_args* a, void* workspac
  * Outputs: seqs [batch] (kv_off = b * max_pages); slot_map [total_rows]: for
  * row q_off + j, j < N + B, of a granted request the cache row page *
  * page_size + offset of token C + j, -1 at mask rows and at every row of
- * [0, total_rows) that is no granted request's; slot_off [batch]; held_out
- * [batch]; n_free_out [1].  pages and free_list are updated in place, at
+ * [0, total_rows) that is no granted request's (tokens are appended in stage
+ * order: the entry at j = N + s - 1 is where ssv_commit_fp8 puts the data row
+ * of stage s, not that of slot s; a caller that stores rows itself looks up
+ * slot k at j = N + tau(k) - 1); slot_off [batch]; held_out [batch];
+ * n_free_out [1].  pages and free_list are updated in place, at
  * entries that the call does not read otherwise; held and n_free are not
  * written, so a pass that fails can be planned again from them.
  * pages [batch, max_pages]; free_list [n_pages]; 1 <= batch <= 4096 (a call

@@ -124,3 +124,30 @@ def test_lengths_without_those_of_the_plan():
     n = ssv.commit_fp8(t["k_new"], t["v_new"], t["k_cache"], t["v_cache"], t["k_scale"], t["v_scale"], t["pages"],
                        t["batch"], t["tau"], t["n_acc"])
     assert n.tolist() == [20 + 1 + int(x.n_acc[0]), -1, 0]
+
+
+def test_slot_map_names_the_rows_that_the_commit_fills():
+    """By stage, not by slot: row N + s - 1 of a request's entries is where the data row of stage s goes."""
+    s = Loop(2, 20, 4)
+    s.run([37, 5], [3, 2])
+    N, B = [3, 0], [6, 8]
+    table, held = s.g["pages"], s.g["held"]
+    seqs, slot_map, _, held, _ = ssv.page_plan(s.g["C"], s.ints(N), s.ints(B), held, table, s.g["free"], s.g["n_free"],
+                                               PAGE, 31)
+    rows, tau = 31, np.array([3, 1, 6, 2, 5, 4, 8, 1, 7, 2, 6, 3, 5, 4], np.int32)
+    k = torch.zeros(rows, HKV, D, dtype=torch.bfloat16, device="cuda")
+    k[:, 0, :rows] = 448 * torch.eye(rows, device="cuda").to(k)            # each row is one of its own
+    batch = ssv.Batch.from_device(seqs, rows, 14, 320, 3, 8)
+    cache, sc = [torch.zeros_like(c) for c in s.cache], [torch.ones_like(y) for y in s.sc]
+    ssv.commit_fp8(k, k, *cache, *sc, table, batch, s.ints(tau), s.ints(B), cache_len=s.g["C"])
+    at = slot_map.cpu().numpy()
+    codes, scale = cache[0].cpu().numpy(), sc[0].cpu().numpy()
+    row0 = 0
+    for b in range(2):
+        t = tau[6 * b: 6 * b + B[b]]
+        for j in range(N[b] + B[b]):
+            row = row0 + (j if j < N[b] else N[b] + int(np.flatnonzero(t == j - N[b] + 1)[0]))
+            page, o = divmod(int(at[row0 + j]), PAGE)
+            got = opaged.e4m3_values(codes[page, 0, o]) * scale[page, 0]
+            assert got[row] == 448 and got.sum() == 448
+        row0 += N[b] + 2 * B[b]

@@ -19,10 +19,11 @@
 //           2^e as a factor of the column group.  A small kernel before this one
 //           writes hi, lo and 2^e of every query row to the workspace.
 //   values  converted to fp16, with the page's scale: code * vs / 2^u, u one
-//           exponent per unit that follows the largest scale met (exact for a
-//           power of two within 2^22 of the largest).  P = 2^7 exp2(x - m) in
-//           fp16: at most 2^15 where the running maximum lags by 2^8, and 11
-//           bits down to weights of 2^-21.  O gathers in units of 2^u.
+//           exponent per unit that follows the largest scale met, from -64 up
+//           (a scale that is a power of two is exact down to 2^-20 of the
+//           largest).  P = 2^7 exp2(x - m) in fp16: at most 2^15 where the
+//           running maximum lags by 2^8, and 11 bits down to weights of 2^-21.
+//           O gathers in units of 2^u.
 // Fresh blocks: bf16 S; V as it is, P = 2^(7-u) exp2(x - m) in bf16.
 //
 // Scheduling: persistent, one CTA per SM; per kv head the units' blocks are
@@ -58,11 +59,13 @@
 // product pair with 130 KB of code, and softmax loops at half their speed alone.
 // Rolled cold loops and waits beyond the first try out of line brought 20, and the
 // mixed batch from 308 to 242 us; with 100 KB the softmax could be unrolled again
-// (chunks of 32 columns instead of 16): 232 us.  Measured:
+// (chunks of 32 columns instead of 16): 232 us.  Rows that do not fill a tile
+// cost whole ones: 1.57 (mixed) and 1.94 (long) times the products needed below.
+// Measured:
 //   8 x 1024 cached keys, 16 / 8 heads             19 us   (bytes: 2.7 us)
 //   64 sequences of 256..8192, 32 / 8 heads       232 us   2.6 TB/s, 636 TFLOP/s
-//   3 sequences of 90001..110007, pages of 16     268 us   2.4 TB/s, 636 TFLOP/s
-//   4 prompts of 2048 over 4096..6200 cached      724 us   1190 TFLOP/s
+//   3 sequences of 90001..110007, pages of 16     267 us   2.4 TB/s, 637 TFLOP/s
+//   4 prompts of 2048 over 4096..6200 cached      723 us   1193 TFLOP/s
 // Every wait is bounded; an expired one raises the CTA's abort flag, copies and
 // MMAs in flight are drained, TMEM is freed and SSV_ERR_TIMEOUT reported.
 #include "ssv_internal.cuh"

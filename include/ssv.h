@@ -740,16 +740,20 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * e4m3 pages; the fresh rows k_new, v_new stay bf16.
  * q, o [total_rows, Hq, d] bf16 device, packed; k_new, v_new [total_rows,
  * Hkv, d] bf16 device, rows k_stride / v_stride elements apart (0: Hkv * d).
- * Scores, softmax statistics and the accumulation of O are fp32.
+ * Scores, softmax statistics and the accumulation of O are fp32.  Rounded to
+ * fewer bits on the way: the queries of cached keys, to two e4m3 parts (2^-18
+ * of a row's largest element); the weights, to fp16 over cached keys (2^-11)
+ * and bf16 over fresh ones (2^-8), the sum that divides them being that of the
+ * unrounded ones; a cached value times its scale, to fp16 (below).
  * A sequence's own fresh rows must be finite (a masked non-finite value row
  * still meets a zero weight).  A query (row, head) with an infinity or NaN
  * gives NaN in its own row of o alone.  Rows of other sequences, rows of a
  * page behind token C - 1 and pages that are not a sequence's own never
- * influence it, whatever they hold.  scales: positive and finite; a value
- * scale enters as a
- * 16-bit float beside the largest met so far in its unit of work, or beside
- * 2^-59 where that is larger, exactly for the powers of two within 2^22 of it
- * that ssv_commit_fp8 writes.  Beside value scales above 2^96, weights of
+ * influence it, whatever they hold.  scales: positive and finite.  A cached
+ * value times its scale enters as a 16-bit float beside the largest scale met
+ * so far in its unit of work, or beside 2^-59 where that is larger: exactly
+ * for scales that are powers of two, as ssv_commit_fp8 writes them, down to
+ * 2^-20 of it, within 2^-30 of it below.  Beside value scales above 2^96, weights of
  * fresh keys below 2^-42 of the row's largest count as none (below 2^-11 at
  * the largest scale, 2^127).  Sums of weights times fresh values beside cached
  * values of less than 2^-59 have to stay below 2^48.
@@ -817,7 +821,7 @@ SSV_API ssv_status ssv_verify_attn_fp8(const ssv_attn_fp8_args* a, void* workspa
  * k_new, v_new [total_rows, Hkv, d] device, dtype (SSV_F32 or SSV_BF16), rows
  * k_stride / v_stride elements apart (0: Hkv * d).  seqs, tau, n_acc, new_len
  * and their checks as ssv_commit; kv_off is the sequence's first entry in
- * pages [table_len].  d in {64, 128}; 1 <= max_new + max_block bounds every
+ * pages [table_len].  d in {64, 128} (ssv_verify_attn_fp8 reads 128 alone); 1 <= max_new + max_block bounds every
  * N + B (sizes the grid); pointers 16-byte aligned, strides a multiple of 16
  * bytes.  No two touched pages may be the same page (not checked).
  * Errors: SSV_ERR_INVALID, SSV_ERR_UNSUPPORTED (d), SSV_ERR_CUDA; on device

@@ -742,9 +742,10 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * Hkv, d] bf16 device, rows k_stride / v_stride elements apart (0: Hkv * d).
  * Scores, softmax statistics and the accumulation of O are fp32.  Rounded to
  * fewer bits on the way: the queries of cached keys, to two e4m3 parts (2^-18
- * of a row's largest element); the weights, to fp16 over cached keys (2^-11)
- * and bf16 over fresh ones (2^-8), the sum that divides them being that of the
- * unrounded ones; a cached value times its scale, to fp16 (below).
+ * of a row's largest element); the weights, to fp16 over cached keys (2^-11,
+ * or 2^-32 of the row's largest where that is more) and bf16 over fresh ones
+ * (2^-8), the sum that divides them being that of the unrounded ones; a cached
+ * value times its scale, to fp16 (below).
  * A sequence's own fresh rows must be finite (a masked non-finite value row
  * still meets a zero weight).  A query (row, head) with an infinity or NaN
  * gives NaN in its own row of o alone.  Rows of other sequences, rows of a
@@ -753,10 +754,10 @@ SSV_API ssv_status ssv_norm_rope_copy(const ssv_norm_rope_args* a, void* stream)
  * value times its scale enters as a 16-bit float beside the largest scale met
  * so far in its unit of work, or beside 2^-59 where that is larger: exactly
  * for scales that are powers of two, as ssv_commit_fp8 writes them, down to
- * 2^-20 of it, within 2^-30 of it below.  Beside value scales above 2^96, weights of
- * fresh keys below 2^-42 of the row's largest count as none (below 2^-11 at
- * the largest scale, 2^127).  Sums of weights times fresh values beside cached
- * values of less than 2^-59 have to stay below 2^48.
+ * 2^-20 of it, within 2^-30 of it below.  Beside value scales above 2^96,
+ * weights of fresh keys below 2^-42 of the row's largest count as none (below
+ * 2^-11 at the largest scale, 2^127).  Sums of weights times fresh values beside
+ * cached values of less than 2^-59 have to stay below 2^48.
  * d = 128; Hq % Hkv == 0, Hq / Hkv <= 128; 1 <= B <= 64; n_pages * Hkv *
  * page_size < 2^31; pointers 16-byte aligned, strides multiples of 8.
  * max_cache / max_new / max_block as ssv_verify_attn.  scale 0 means

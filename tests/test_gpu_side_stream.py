@@ -30,7 +30,7 @@ def beside_a_busy_stream(run):
     done = torch.cuda.Event()
     host, dev = torch.empty(1 << 30, dtype=torch.uint8, pin_memory=True), torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
-    for _ in range(40):                                 # about 0.2 s of copies, which leave the SMs free
+    for _ in range(100):                                # about 0.5 s of copies, which leave the SMs free
         dev.copy_(host, non_blocking=True)
     done.record()
     out = run(side)

@@ -152,14 +152,16 @@ def prepare(case, seed):
     s |= dict(logits=z, token=token, logp=logp, weight=torch.where(idle, 0.0, w), rest=case["rest"])
     if case["op"] == "distill":
         return s | dict(grad=case["grad"])
-    # a training step keeps the statistics of its forward pass
+    # a training step keeps the statistics of its forward pass: the log-sum-exp of each row, and the logarithm of the
+    # share of it that the target's tokens leave
     stats = torch.empty(n, 2, device="cuda")
     for i in range(0, n, step):
         y = z[i:i + step].double() / case["temp"]
-        stats[i:i + step, 0] = torch.logsumexp(y, 1).float()
+        lse = torch.logsumexp(y, 1)
+        stats[i:i + step, 0] = lse.float()
         own_rows, c = (token[i:i + step] >= 0).nonzero(as_tuple=True)
         y[own_rows, token[i:i + step][own_rows, c].long()] = float("-inf")
-        stats[i:i + step, 1] = torch.logsumexp(y, 1).float()
+        stats[i:i + step, 1] = (torch.logsumexp(y, 1) - lse).float()
     return s | dict(stats=stats, grad_loss=torch.randn(n, generator=g, device="cuda"))
 
 
@@ -256,11 +258,10 @@ def _others(y, there, token):
     return y
 
 
-def _gradient(y, there, token, p, r, total, lse, lse_rest, factor, temp):
+def _gradient(y, there, token, p, r, total, lse, log_u, factor, temp):
     """factor / temp * (total q - p) at the target's tokens; their own softmax times (total u - r) at the others."""
     p, r, total = p.float(), r.float(), total.float()
-    u = (lse_rest - lse).exp()
-    grad = (y - lse_rest).exp() * (total * u - r)
+    grad = (y - (lse + log_u)).exp() * (total * log_u.exp() - r)
     at_top = total * (y.gather(1, token) - lse).exp() - p
     own_rows, c = there.nonzero(as_tuple=True)
     grad[own_rows, token[own_rows, c]] = at_top[own_rows, c]
@@ -285,11 +286,11 @@ def _distill(s):
         log_rest = ((z - mr) / s["temp"]).exp().sum(1, keepdim=True).double().log()
         m, mr = m.double() / s["temp"], mr.double() / s["temp"]
         loss = torch.where(p > 0, p * (t - (x.gather(1, token).double() / s["temp"] - m - log)), 0.0).sum(1)
-        rest = torch.where(r > 0, r * (r.log() - (mr - m + log_rest - log)), 0.0)[:, 0]
+        log_u = mr - m + log_rest - log
+        rest = torch.where(r > 0, r * (r.log() - log_u), 0.0)[:, 0]
         out["loss"][c] = torch.where(w != 0, w * (loss + rest), 0.0).float()
-        y, lse, lse_rest = x / s["temp"], (m + log).float(), (mr + log_rest).float()
         if s["grad"]:
-            grad = _gradient(y, there, token, p, r, total, lse, lse_rest, w, s["temp"])
+            grad = _gradient(x / s["temp"], there, token, p, r, total, (m + log).float(), log_u.float(), w, s["temp"])
             out["grad"][c] = torch.where((w != 0)[:, None], grad, 0.0).to(s["logits"].dtype)
     return out
 

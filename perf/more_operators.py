@@ -152,16 +152,17 @@ def prepare(case, seed):
     s |= dict(logits=z, token=token, logp=logp, weight=torch.where(idle, 0.0, w), rest=case["rest"])
     if case["op"] == "distill":
         return s | dict(grad=case["grad"])
-    # a training step keeps the statistics of its forward pass: the log-sum-exp of each row, and the logarithm of the
-    # share of it that the target's tokens leave
-    stats = torch.empty(n, 2, device="cuda")
+    # a training step keeps the statistics of its forward pass: maximum and sum, relative to it, of exp(z / T), over the
+    # row and over the tokens that are not the target's
+    stats = torch.empty(n, 4, device="cuda")
     for i in range(0, n, step):
-        y = z[i:i + step].double() / case["temp"]
-        lse = torch.logsumexp(y, 1)
-        stats[i:i + step, 0] = lse.float()
-        own_rows, c = (token[i:i + step] >= 0).nonzero(as_tuple=True)
-        y[own_rows, token[i:i + step][own_rows, c].long()] = float("-inf")
-        stats[i:i + step, 1] = (torch.logsumexp(y, 1) - lse).float()
+        y = z[i:i + step].double()
+        for j in (0, 2):
+            m = y.amax(1)
+            stats[i:i + step, j] = m.float()
+            stats[i:i + step, j + 1] = ((y - m[:, None]) / case["temp"]).exp().sum(1).float()
+            own_rows, c = (token[i:i + step] >= 0).nonzero(as_tuple=True)
+            y[own_rows, token[i:i + step][own_rows, c].long()] = float("-inf")
     return s | dict(stats=stats, grad_loss=torch.randn(n, generator=g, device="cuda"))
 
 
@@ -258,11 +259,13 @@ def _others(y, there, token):
     return y
 
 
-def _gradient(y, there, token, p, r, total, lse, log_u, factor, temp):
+def _gradient(x, there, token, p, r, total, sums, factor, temp):
     """factor / temp * (total q - p) at the target's tokens; their own softmax times (total u - r) at the others."""
     p, r, total = p.float(), r.float(), total.float()
-    grad = (y - (lse + log_u)).exp() * (total * log_u.exp() - r)
-    at_top = total * (y.gather(1, token) - lse).exp() - p
+    m, s, mr, sr = sums
+    u = (((mr - m) / temp).double().exp() * sr / s).float()
+    grad = ((x - mr) / temp).exp() * ((total * u - r) / sr)
+    at_top = total * (((x.gather(1, token) - m) / temp).exp() / s) - p
     own_rows, c = there.nonzero(as_tuple=True)
     grad[own_rows, token[own_rows, c]] = at_top[own_rows, c]
     return grad * (factor[:, None] / temp)
@@ -282,15 +285,15 @@ def _distill(s):
         m = x.amax(1, keepdim=True)
         z = _others(x, there, token)
         mr = z.amax(1, keepdim=True)
-        log = ((x - m) / s["temp"]).exp().sum(1, keepdim=True).double().log()
-        log_rest = ((z - mr) / s["temp"]).exp().sum(1, keepdim=True).double().log()
-        m, mr = m.double() / s["temp"], mr.double() / s["temp"]
-        loss = torch.where(p > 0, p * (t - (x.gather(1, token).double() / s["temp"] - m - log)), 0.0).sum(1)
-        log_u = mr - m + log_rest - log
+        total_e = ((x - m) / s["temp"]).exp().sum(1, keepdim=True)
+        rest_e = ((z - mr) / s["temp"]).exp().sum(1, keepdim=True)
+        log = total_e.double().log()
+        loss = torch.where(p > 0, p * (t - ((x.gather(1, token) - m).double() / s["temp"] - log)), 0.0).sum(1)
+        log_u = (mr - m).double() / s["temp"] + rest_e.double().log() - log
         rest = torch.where(r > 0, r * (r.log() - log_u), 0.0)[:, 0]
         out["loss"][c] = torch.where(w != 0, w * (loss + rest), 0.0).float()
         if s["grad"]:
-            grad = _gradient(x / s["temp"], there, token, p, r, total, (m + log).float(), log_u.float(), w, s["temp"])
+            grad = _gradient(x, there, token, p, r, total, (m, total_e, mr, rest_e), w, s["temp"])
             out["grad"][c] = torch.where((w != 0)[:, None], grad, 0.0).to(s["logits"].dtype)
     return out
 
@@ -299,11 +302,10 @@ def _backward(s):
     n, v = s["logits"].shape
     grad = torch.empty(n, v, dtype=s["logits"].dtype, device=s["weight"].device)
     for c in _chunks(n, v):
-        y = s["logits"][c].float() / s["temp"]
         there, p, _, r, total = _target(s, c)
         w = s["weight"][c]
-        x = _gradient(y, there, s["token"][c].long().clamp(min=0), p, r, total, s["stats"][c, :1], s["stats"][c, 1:],
-                      w * s["grad_loss"][c], s["temp"])
+        x = _gradient(s["logits"][c].float(), there, s["token"][c].long().clamp(min=0), p, r, total,
+                      s["stats"][c].split(1, 1), w * s["grad_loss"][c], s["temp"])
         grad[c] = torch.where((w != 0)[:, None], x, 0.0).to(grad.dtype)
     return dict(grad=grad)
 

@@ -30,7 +30,8 @@ EXPORTS = ("ssv_rope_copy", "ssv_verify_attn_workspace", "ssv_verify_attn", "ssv
            "ssv_get_status", "ssv_status_string", "ssv_version", "ssv_bench", "ssv_set_fault_injection",
            "ssv_tree_verify_attn_workspace", "ssv_tree_verify_attn", "ssv_tree_accept_workspace", "ssv_tree_accept",
            "ssv_stream_read", "ssv_page_plan", "ssv_norm_rope_copy", "ssv_verify_attn_fp8_workspace",
-           "ssv_verify_attn_fp8", "ssv_commit_fp8")
+           "ssv_verify_attn_fp8", "ssv_commit_fp8", "ssv_logprobs", "ssv_distill", "ssv_distill_backward")
+RENORM, REST = 0, 1
 FAULT_NONE, FAULT_ATTN, FAULT_ACCEPT, FAULT_LMHEAD = 0, 1, 2, 3
 
 
@@ -150,6 +151,22 @@ class CommitFp8Args(C.Structure):
                 ("max_block", C.c_int32), ("dev_status", C.c_void_p), ("cache_len", C.c_void_p)]
 
 
+class LogprobsArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("logits_stride", C.c_int64), ("dtype", C.c_int), ("V", C.c_int32),
+                ("total_rows", C.c_int32), ("rows", C.c_void_p), ("tokens", C.c_void_p), ("n", C.c_int32),
+                ("top_k", C.c_int32), ("T", C.c_float), ("logprob", C.c_void_p), ("rank", C.c_void_p),
+                ("entropy", C.c_void_p), ("lse", C.c_void_p), ("top_logprob", C.c_void_p),
+                ("top_token", C.c_void_p), ("dev_status", C.c_void_p)]
+
+
+class DistillArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("logits_stride", C.c_int64), ("dtype", C.c_int), ("V", C.c_int32),
+                ("n", C.c_int32), ("K", C.c_int32), ("teacher_token", C.c_void_p), ("teacher_logprob", C.c_void_p),
+                ("T", C.c_float), ("mode", C.c_int), ("weight", C.c_void_p), ("loss", C.c_void_p),
+                ("stats", C.c_void_p), ("grad_loss", C.c_void_p), ("grad", C.c_void_p), ("grad_stride", C.c_int64),
+                ("dev_status", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -188,13 +205,16 @@ def lib():
         L.ssv_verify_attn_fp8_workspace.argtypes = [C.POINTER(AttnFp8Args), C.POINTER(sz)]
         L.ssv_verify_attn_fp8.argtypes = [C.POINTER(AttnFp8Args), vp, sz, vp]
         L.ssv_commit_fp8.argtypes = [C.POINTER(CommitFp8Args), vp]
+        L.ssv_logprobs.argtypes = [C.POINTER(LogprobsArgs), vp]
+        L.ssv_distill.argtypes = [C.POINTER(DistillArgs), vp]
+        L.ssv_distill_backward.argtypes = [C.POINTER(DistillArgs), vp]
         for name in ("ssv_rope_copy", "ssv_verify_attn_workspace", "ssv_verify_attn", "ssv_verify_step",
                      "ssv_accept_workspace", "ssv_accept", "ssv_accept_noalloc", "ssv_commit",
                      "ssv_lmhead_accept_workspace", "ssv_lmhead_accept", "ssv_get_status", "ssv_bench",
                      "ssv_set_fault_injection", "ssv_tree_verify_attn_workspace", "ssv_tree_verify_attn",
                      "ssv_tree_accept_workspace", "ssv_tree_accept", "ssv_stream_read", "ssv_page_plan",
                      "ssv_norm_rope_copy", "ssv_verify_attn_fp8_workspace", "ssv_verify_attn_fp8",
-                     "ssv_commit_fp8"):
+                     "ssv_commit_fp8", "ssv_logprobs", "ssv_distill", "ssv_distill_backward"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -566,6 +586,7 @@ def _packer(cls):
 
 _pack_plan, _pack_norm = _packer(PagePlanArgs), _packer(NormRopeArgs)
 _pack_attn, _pack_commit = _packer(AttnFp8Args), _packer(CommitFp8Args)
+_pack_logprobs, _pack_distill = _packer(LogprobsArgs), _packer(DistillArgs)
 _entries = {}
 
 
@@ -807,6 +828,151 @@ def commit_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch: B
     _launch(what, (k_new, v_new, k_cache, v_cache, k_scale, v_scale, pages, batch.dev, tau, n_acc, new_len, dev_status,
                    cache_len), a, stream)
     return new_len
+
+
+# ---------------------------------------------------------------------------
+# log-probabilities and distillation
+# ---------------------------------------------------------------------------
+def _logit_rows(t, what: str) -> int:
+    """Row stride (elements) of [rows, V] logits whose elements are contiguous; 0: packed."""
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: logits are [rows, V]")
+    if t.is_contiguous():
+        return 0
+    (rows, v), s = t.shape, t.stride()
+    if v > 1 and s[1] != 1:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: the logits of a row are contiguous")
+    if rows > 1 and s[0] < v:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: rows that do not overlap")
+    return s[0] if rows > 1 else 0
+
+
+def _like(what: str, shape, dtype, *tensors):
+    for t in tensors:
+        if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+            raise SsvError(SSV_ERR_INVALID, f"{what}: contiguous {dtype} {list(shape)}")
+
+
+def logprobs(logits, tokens=None, top_k: int = 0, T: float = 1.0, rows=None, out=None, dev_status=None, stream=None):
+    """Log-probabilities of tokens (int32 [n], -1: none) under softmax(logits
+    / T), their ranks, the rows' entropies and log-sum-exps, and each row's
+    top_k alternatives.  logits [rows, V] fp32 or bf16 (rows may be strided);
+    entry i has logits row rows[i] (int32 [n]; without it row i).  Returns
+    (logprob [n], rank [n], entropy [n], lse [n], top_logprob [n, top_k],
+    top_token [n, top_k]); logprob and rank are None without tokens, the
+    last two with top_k 0.  ``out``: six tensors (or None) of those shapes."""
+    torch = _torch()
+    what, f32, i32 = "ssv_logprobs", torch.float32, torch.int32
+    stride, dt = _logit_rows(logits, what), _dtype_code(logits)
+    _int32(what, tokens, rows)
+    for t in (tokens, rows):
+        if t is not None and t.dim() != 1:
+            raise SsvError(SSV_ERR_INVALID, f"{what}: one token and one row per entry")
+    n = (tokens if tokens is not None else rows if rows is not None else logits).shape[0]
+    if rows is not None and rows.shape[0] != n:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: one token and one row per entry")
+    top_k = int(top_k)
+    if top_k < 0:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: top_k")
+    if out is None:
+        with _on(stream):
+            # one allocation: four values per entry, then its alternatives
+            buf = torch.empty(n * (4 + 2 * top_k), dtype=f32, device=logits.device)
+        at, nk = buf.data_ptr(), n * top_k
+        lp, rank, ent, lse, tl, tt = buf.split_with_sizes([n, n, n, n, nk, nk])
+        out = (lp, rank.view(i32), ent, lse, tl.view(n, top_k), tt.view(i32).view(n, top_k))
+        ptrs = [at, at + 4 * n, at + 8 * n, at + 12 * n, at + 16 * n, at + 16 * n + 4 * nk]
+        if tokens is None:
+            out, ptrs[0], ptrs[1] = (None, None) + out[2:], 0, 0
+        if not top_k:
+            out, ptrs[4], ptrs[5] = out[:4] + (None, None), 0, 0
+    else:
+        _like(what, (n,), f32, out[0], out[2], out[3])
+        _like(what, (n,), i32, out[1])
+        _like(what, (n, top_k), f32, out[4])
+        _like(what, (n, top_k), i32, out[5])
+        ptrs = [_addr(t) for t in out]
+    a = _pack_logprobs(logits.data_ptr(), stride, dt, logits.shape[1], logits.shape[0], _addr(rows), _addr(tokens), n,
+                       top_k, T, *ptrs, _addr(dev_status))
+    _launch(what, (logits, rows, tokens, dev_status) + out, a, stream)
+    return out
+
+
+def _distill_fields(what, logits, teacher_token, teacher_logprob, T, mode, weight, loss, stats, grad_loss, grad, dev_status):
+    torch = _torch()
+    f32, n = torch.float32, logits.shape[0]
+    stride, dt = _logit_rows(logits, what), _dtype_code(logits)
+    if teacher_token.dim() != 2 or teacher_token.shape[0] != n:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: the target's tokens are [rows, K]")
+    _int32(what, teacher_token)
+    _like(what, teacher_token.shape, f32, teacher_logprob)
+    _like(what, (n,), f32, weight, loss, grad_loss)
+    _like(what, (n, 4), f32, stats)
+    grad_stride = 0
+    if grad is not None:
+        if grad.dtype != logits.dtype or grad.shape != logits.shape:
+            raise SsvError(SSV_ERR_INVALID, f"{what}: the gradient is as the logits")
+        grad_stride = _logit_rows(grad, what)
+    return _pack_distill(logits.data_ptr(), stride, dt, logits.shape[1], n, teacher_token.shape[1],
+                         teacher_token.data_ptr(), teacher_logprob.data_ptr(), T, mode, _addr(weight), _addr(loss),
+                         _addr(stats), _addr(grad_loss), _addr(grad), grad_stride, _addr(dev_status))
+
+
+def _empty_rows(logits):
+    """An uninitialised tensor of the logits' shape whose rows lie to 32-byte boundaries as theirs do, where that
+    costs little memory."""
+    torch = _torch()
+    n, v = logits.shape
+    s = logits.stride(0) if n > 1 else v
+    lead = (logits.data_ptr() % 32) // logits.element_size()
+    if (s == v and lead == 0) or not v <= s <= v + 64:
+        return torch.empty((n, v), dtype=logits.dtype, device=logits.device)
+    return torch.empty(n * s + lead, dtype=logits.dtype, device=logits.device).as_strided((n, v), (s, 1), lead)
+
+
+def distill(logits, teacher_token, teacher_logprob, T: float = 1.0, mode: int = RENORM, weight=None, grad=False,
+            loss=None, stats=None, dev_status=None, stream=None):
+    """Distillation loss of a drafter's logits [n, V] (fp32 or bf16; rows may
+    be strided) against the target's alternatives (teacher_token int32,
+    teacher_logprob fp32 [n, K], as logprobs returns them; token -1: absent),
+    times weight [n].  Returns (loss [n], stats [n, 4], grad); grad is None
+    unless it is asked for (True) or given (a tensor like the logits, which may
+    be the logits themselves).  stats is what distill_backward takes."""
+    torch = _torch()
+    what = "ssv_distill"
+    if logits.dim() != 2:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: logits are [rows, V]")
+    n = logits.shape[0]
+    with _on(stream):
+        if loss is None:
+            loss = torch.empty(n, dtype=torch.float32, device=logits.device)
+        if stats is None:
+            stats = torch.empty((n, 4), dtype=torch.float32, device=logits.device)
+        if grad is True:
+            grad = _empty_rows(logits)
+    if grad is False:
+        grad = None
+    a = _distill_fields(what, logits, teacher_token, teacher_logprob, T, mode, weight, loss, stats, None, grad, dev_status)
+    _launch(what, (logits, teacher_token, teacher_logprob, weight, loss, stats, grad, dev_status), a, stream)
+    return loss, stats, grad
+
+
+def distill_backward(logits, teacher_token, teacher_logprob, stats, grad_loss=None, T: float = 1.0, mode: int = RENORM,
+                     weight=None, grad=None, dev_status=None, stream=None):
+    """Gradient of sum(grad_loss * loss) for distill's losses on the same
+    arguments, from the statistics that it returned; grad_loss [n] fp32 (None:
+    ones).  grad: a tensor like the logits, which may be the logits themselves
+    (allocated here when not given).  Returns grad."""
+    what = "ssv_distill_backward"
+    if logits.dim() != 2:
+        raise SsvError(SSV_ERR_INVALID, f"{what}: logits are [rows, V]")
+    if grad is None:
+        with _on(stream):
+            grad = _empty_rows(logits)
+    a = _distill_fields(what, logits, teacher_token, teacher_logprob, T, mode, weight, None, stats, grad_loss, grad,
+                        dev_status)
+    _launch(what, (logits, teacher_token, teacher_logprob, weight, stats, grad_loss, grad, dev_status), a, stream)
+    return grad
 
 
 def stream_read(buf, out, stream=None):

@@ -864,6 +864,143 @@ typedef struct {
 SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
 
 /* ------------------------------------------------------------------------
+ * What else a pass's logits give.  ssv_accept decides on the target's rows;
+ * the three entry points below return the log-probabilities that a server
+ * reports beside the tokens, and train a drafter on the target's answers (the
+ * SPOT review's order predictor reads the top 32 probabilities and summary
+ * statistics per slot; the DFlash review weighs a draft position's loss by
+ * exp(-(k - 1) / gamma), section 3.1; neither page gives an interface).
+ * Rows: logits [rows, V] device, SSV_F32 or SSV_BF16, rows logits_stride
+ * elements apart (0: V; at least V), at any element-aligned address; rows that
+ * start on 32-byte boundaries are fastest.  1 <= V <= 524288.  T: positive
+ * and finite.  No workspace; sums and results are the same from call to call.
+ * -inf marks a token that cannot be: it has probability 0.  A result beyond
+ * fp32's range (the lse of a row at the type's lowest number, T < 1) is infinite.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * ssv_logprobs -- log-probabilities of given tokens under softmax(l / T), their
+ * ranks, each row's entropy and its top alternatives.
+ * Entry i (0 <= i < n) has the logits row rows[i] (NULL: i) and the token
+ * tokens[i] (NULL: none is asked for).  An entry with token -1 (as ssv_accept
+ * leaves behind the last emitted token) or row -1 is idle: its row is not read,
+ * and logprob, rank, entropy, lse are 0, its alternatives absent.
+ *   lse[i]     = ln sum_v exp(l_v / T)
+ *   logprob[i] = l_t / T - lse
+ *   rank[i]    = 1 + number of tokens before t in the order of the logits
+ *                (descending, equal ones by index)
+ *   entropy[i] = - sum_v p_v ln p_v (nats; tokens of probability 0 add nothing)
+ *   top_token[i][0..top_k), top_logprob[i][..]: the first top_k tokens of that
+ *                order with logits above -inf, and their log-probabilities;
+ *                where there are fewer, -1 and -inf.
+ * Tokens in the order of the stages, as ssv_accept writes them, have the row
+ * of slot k at entry slot_off + tau(k) - 1.
+ * Sums are fp32, per thread and joined in a fixed order; logarithms of sums and
+ * the results are formed in 64 bits and rounded once (top_logprob in 32).
+ * A row with a NaN or +inf gives NaN in logprob, entropy, lse and top_logprob;
+ * NaN logits are in no order (never listed, never before another; the rank of
+ * such a token is 0).  A row of nothing but -inf gives lse = logprob = -inf,
+ * entropy 0 and no alternatives.
+ * tokens given: logprob is not NULL; not given: logprob and rank are NULL.
+ * rank, entropy, lse may be NULL.  0 <= top_k <= 128; top_logprob, top_token
+ * [n, top_k] (NULL for 0).  Outputs overlap no input.
+ * Errors: SSV_ERR_INVALID, SSV_ERR_NOT_FINITE (T), SSV_ERR_UNSUPPORTED (V,
+ * top_k), SSV_ERR_CUDA; on device SSV_ERR_INVALID for a row outside
+ * [-1, total_rows) or a token outside [-1, V) (that entry is taken as idle).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* logits;          /* [total_rows, V] */
+  int64_t logits_stride;       /* elements; 0: V */
+  ssv_dtype dtype;
+  int32_t V;
+  int32_t total_rows;
+  const int32_t* rows;         /* device [n] or NULL */
+  const int32_t* tokens;       /* device [n] or NULL */
+  int32_t n;
+  int32_t top_k;
+  float T;
+  float* logprob;              /* device [n] */
+  int32_t* rank;               /* device [n] or NULL */
+  float* entropy;              /* device [n] or NULL */
+  float* lse;                  /* device [n] or NULL */
+  float* top_logprob;          /* device [n, top_k] */
+  int32_t* top_token;          /* device [n, top_k] */
+  int32_t* dev_status;         /* device, may be NULL */
+} ssv_logprobs_args;
+
+SSV_API ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * ssv_distill, ssv_distill_backward -- distillation of a drafter from the
+ * target's top alternatives: the loss, or the loss and its gradient in one
+ * call, and the gradient for given upstream gradients.
+ * Row i: drafter logits z [V], weight w = weight[i] (NULL: 1), and K listed
+ * tokens teacher_token[i][j] with values t_j = teacher_logprob[i][j], as
+ * ssv_logprobs writes them (at the same T).  Token -1 is absent; one listed
+ * more than once counts with the sum of its probabilities.
+ *   SSV_DISTILL_RENORM: p_j = exp(t_j) / sum exp(t), r = 0 (so that logits
+ *                       divided by T serve as well as log-probabilities)
+ *   SSV_DISTILL_REST:   p_j = exp(t_j), r = max(0, 1 - sum p): the target's
+ *                       probability of all other tokens together (where u = 0, an
+ *                       r below 2^-20, left by the roundings of t, counts as 0)
+ *   q = softmax(z / T), u = sum of q over the tokens that are not listed
+ *   loss[i] = w [ sum_j p_j (ln p_j - ln q_j) + r (ln r - ln u) ]
+ * (terms of probability 0 add nothing), the divergence of q from p with the
+ * other tokens as one; its gradient with P = sum p + r:
+ *   d loss / d z_v = (w / T) (P q_v - p_v)            v listed
+ *                    (w / T) (P q_v - r q_v / u)      v not listed
+ * ssv_distill: writes loss [n]; stats [n, 4] (may be NULL), each row's
+ * (m, S, m', S'): m = max z, S = sum exp((z - m) / T), and the same over the
+ * tokens that are not listed (lse = m / T + ln S; -inf and 0 where there is
+ * nothing above -inf); and, where grad is given, the gradient of
+ * sum_i loss[i].  grad_loss is NULL.
+ * ssv_distill_backward: takes stats as written by ssv_distill on the same
+ * arguments and grad_loss [n] (NULL: 1), writes grad, row i times grad_loss[i].
+ * loss is not used (may be NULL).
+ * grad [n, V] device in the logits' dtype, rows grad_stride elements apart
+ * (0: V).  It may be the logits themselves (same address and stride), and
+ * overlaps no other argument; fastest where its rows lie to 32-byte boundaries
+ * as the logits' do.  Elements between rows are not written.
+ * A row of weight 0 is not read: its loss, statistics and gradient are 0.
+ * A row with a NaN (or +inf) in its logits, or a NaN in its target, gives NaN in its loss and
+ * gradient.  A listed token with p > 0 and logit -inf, or r > 0 with u = 0,
+ * gives the loss +inf (the gradient stays finite); so does a row of nothing but
+ * -inf, whose gradient is 0.  A row whose listed tokens are all absent has the
+ * loss and gradient 0.
+ * Sums over a row are fp32; u is summed from the tokens that are not listed;
+ * the loss's few logarithms and products are in 64 bits.  The gradient is
+ * formed in fp32 and rounded once.
+ * 1 <= K <= 128.
+ * Errors: SSV_ERR_INVALID, SSV_ERR_NOT_FINITE (T), SSV_ERR_UNSUPPORTED (V, K),
+ * SSV_ERR_CUDA; on device SSV_ERR_INVALID for a listed token outside [-1, V)
+ * (taken as absent).
+ * ---------------------------------------------------------------------- */
+typedef enum { SSV_DISTILL_RENORM = 0, SSV_DISTILL_REST = 1 } ssv_distill_mode;
+
+typedef struct {
+  const void* logits;          /* [n, V] */
+  int64_t logits_stride;       /* elements; 0: V */
+  ssv_dtype dtype;
+  int32_t V;
+  int32_t n;
+  int32_t K;
+  const int32_t* teacher_token;    /* device [n, K] */
+  const float* teacher_logprob;    /* device [n, K] */
+  float T;
+  ssv_distill_mode mode;
+  const float* weight;         /* device [n] or NULL */
+  float* loss;                 /* device [n] */
+  float* stats;                /* device [n, 4] */
+  const float* grad_loss;      /* device [n] or NULL (ssv_distill_backward) */
+  void* grad;                  /* [n, V], dtype */
+  int64_t grad_stride;         /* elements; 0: V */
+  int32_t* dev_status;         /* device, may be NULL */
+} ssv_distill_args;
+
+SSV_API ssv_status ssv_distill(const ssv_distill_args* a, void* stream);
+SSV_API ssv_status ssv_distill_backward(const ssv_distill_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
  * ssv_set_fault_injection -- test support for failure detection.
  * The pages have no counterpart: this lets a test make a bounded device wait
  * run out without faulting, trapping or hanging the GPU.  For the chosen

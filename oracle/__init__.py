@@ -27,6 +27,10 @@ What it computes, plainly and slowly, in float64 (numpy):
 * ``lmhead.accept_lmhead``    the LM head over the mask slots (l = W h, exact,
                               rounded once to fp32) followed by the acceptance
                               above (SimSD summary section 4; SPOT review).
+* ``logprobs.logprobs_batch`` / ``distill.distill_batch``  log-probabilities of
+                              a pass's logits, and the loss that trains a drafter
+                              on them with its gradient (definitions in
+                              include/ssv.h; no interface on the pages).
 
 Pins (``tests/test_oracle_*.py``, marked ``not gpu``) tie each function to
 something other than itself: a hand-worked mask from the rule's text, mask
@@ -38,4 +42,4 @@ invariance, brute-force laws of the Gumbel-max and rejection samplers.
 The attention *values* at full size carry no printed example on the pages
 and rest on those reductions.
 """
-from . import mask, rope, attention, accept, commit, lmhead  # noqa: F401
+from . import mask, rope, attention, accept, commit, lmhead, logprobs, distill  # noqa: F401

@@ -30,8 +30,7 @@ struct DistillParams {
   int V, K, mode;
   const int32_t* token;
   const float* logp;
-  float sc;  // log2(e) / T
-  double inv_T;
+  Scale T;
   const float* weight;
   float* loss;
   float* stats;             // [n, 4]: Sums of each row (written by the forward, read by the backward)
@@ -144,8 +143,9 @@ struct Sums {
   __device__ __forceinline__ bool none() const { return mr == -INFINITY && Sr == 0.f; }  // nothing is left to the others
   __device__ __forceinline__ bool empty() const { return none() && S == 0.f; }           // the row is all -inf
   // ln of the others' share
-  __device__ __forceinline__ double ln_u(double inv_T) const {
-    return none() ? -(double)INFINITY : ((double)mr - (double)m) * inv_T + log_sum(Sr) - log_sum(S);
+  __device__ __forceinline__ Pair ln_u(const Scale& T) const {
+    if (none()) return {-INFINITY, 0.f};
+    return two_sum(mr, -m) * Pair{T.hi, T.lo} + (log_sum(Sr) + -log_sum(S));
   }
 };
 
@@ -155,12 +155,12 @@ struct Slope {
   float wT;
 };
 
-__device__ __forceinline__ Slope slope_of(const Sums& s, const Target& tg, double inv_T, double w) {
+__device__ __forceinline__ Slope slope_of(const Sums& s, const Target& tg, const Scale& T, float w) {
   const float rest = rest_of(tg, s.none()), P = tg.sum + rest;
   Slope k;
-  k.wT = (float)(w * inv_T);
+  k.wT = w * T.hi;
   k.ref = s.none() ? 0.f : s.mr;
-  k.coef = s.none() ? 0.f : k.wT * (P * expf((float)s.ln_u(inv_T)) - rest) / s.Sr;
+  k.coef = s.none() ? 0.f : k.wT * (P * expf(value_of(s.ln_u(T))) - rest) / s.Sr;
   k.top = s.m;
   k.share = P / s.S;
   return k;
@@ -174,7 +174,7 @@ __device__ __forceinline__ void write_gradient(const DistillParams& p, const Row
   const int v_lo = max(0, row.first(g0)), v_hi = min(row.V, row.first(g1));
   if (p.vec) {
     char* to = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(31));
-    const float2 sc2 = make_float2(p.sc, p.sc), ref2 = make_float2(-k.ref, -k.ref), c2 = make_float2(k.coef, k.coef);
+    const float2 sc2 = make_float2(p.T.sc, p.T.sc), ref2 = make_float2(-k.ref, -k.ref), c2 = make_float2(k.coef, k.coef);
     for (int gb = g0 + tid; gb < g1; gb += NT * kBatch) {
       Raw x[kBatch];
 #pragma unroll
@@ -198,19 +198,19 @@ __device__ __forceinline__ void write_gradient(const DistillParams& p, const Row
           for (int e = 0; e < kGroup<T>; ++e) {
             const int v = row.first(g) + e;
             if (v >= 0 && v < row.V)
-              out[v] = Elem<T>::from_f32(ex2((load_element(row.row + v) - k.ref) * p.sc) * k.coef);
+              out[v] = Elem<T>::from_f32(ex2((load_element(row.row + v) - k.ref) * p.T.sc) * k.coef);
           }
         }
       }
     }
   } else {
     for (int v = v_lo + tid; v < v_hi; v += NT)
-      out[v] = Elem<T>::from_f32(ex2((load_element(row.row + v) - k.ref) * p.sc) * k.coef);
+      out[v] = Elem<T>::from_f32(ex2((load_element(row.row + v) - k.ref) * p.T.sc) * k.coef);
   }
   __syncthreads();
   for (int j = tid; j < p.K; j += NT) {
     const int v = tg.token[j];
-    if (v >= v_lo && v < v_hi) out[v] = Elem<T>::from_f32(k.wT * (k.share * ex2((tg.z[j] - k.top) * p.sc) - tg.p[j]));
+    if (v >= v_lo && v < v_hi) out[v] = Elem<T>::from_f32(k.wT * (k.share * ex2((tg.z[j] - k.top) * p.T.sc) - tg.p[j]));
   }
 }
 
@@ -246,7 +246,7 @@ struct Shared {
   Target tg;
   Part part[kMaxCluster];
   float red[kLogitsThreads / 32], redS[kLogitsThreads / 32];
-  double redL[4];
+  Pair redL[kLogitsMaxTop / 32];
 };
 
 template <typename T, bool GRAD>
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
 
   // ------------------------------------------------------------ the other tokens
   float m = -INFINITY, S = 0.f;
-  const float2 sc2 = make_float2(p.sc, p.sc);
+  const float2 sc2 = make_float2(p.T.sc, p.T.sc);
   for (int gb = g0 + tid; gb < g1; gb += NT * kBatch) {
     Raw x[kBatch];
 #pragma unroll
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
       mx = fmaxf(mx, group_max<T>(x[u]));
     }
     if (mx > m) {
-      S *= ex2(shift_of(m, mx, p.sc));
+      S *= ex2(shift_of(m, mx, p.T.sc));
       m = mx;
     }
     const float mm = m == -INFINITY ? 0.f : m;  // nothing but -inf and NaN so far
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
   }
   const float M = cta_max(m, sm.red);
   {
-    const float Sw = warp_sum(ex2(shift_of(m, M, p.sc)) * S);
+    const float Sw = warp_sum(ex2(shift_of(m, M, p.T.sc)) * S);
     if (lane == 0) sm.redS[warp] = Sw;
   }
   __syncthreads();
@@ -359,42 +359,49 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
   float mr = -INFINITY;
   for (int i = 0; i < c; ++i) mr = fmaxf(mr, sm.part[i].m);
   float Sr = 0.f;
-  for (int i = 0; i < c; ++i) Sr += ex2(shift_of(sm.part[i].m, mr, p.sc)) * sm.part[i].S;
+  for (int i = 0; i < c; ++i) Sr += ex2(shift_of(sm.part[i].m, mr, p.T.sc)) * sm.part[i].S;
   float mt = -INFINITY;
   for (int j = tid; j < p.K; j += NT)
     if (tg.token[j] >= 0) mt = fmaxf(mt, tg.z[j]);
   const float m_all = fmaxf(mr, cta_max(mt, sm.red));
   float st = 0.f;
   for (int j = tid; j < p.K; j += NT)
-    if (tg.token[j] >= 0) st += ex2((tg.z[j] - (m_all == -INFINITY ? 0.f : m_all)) * p.sc);
+    if (tg.token[j] >= 0) st += ex2((tg.z[j] - (m_all == -INFINITY ? 0.f : m_all)) * p.T.sc);
   st = warp_sum(st);
   if (lane == 0) sm.redS[warp] = st;
   __syncthreads();
-  const float shift = shift_of(mr, m_all, p.sc);
+  const float shift = shift_of(mr, m_all, p.T.sc);
   float S_all = ex2(shift) * Sr;
   for (int i = 0; i < nw; ++i) S_all += sm.redS[i];
   const Sums sums = {m_all, S_all, mr, Sr};
   if (rank == 0) {
-    const double lnS = log_sum(S_all);
-    double part = 0.0;
+    const Pair lnS = log_sum(S_all), inv = {p.T.hi, p.T.lo};
+    Pair part = {0.f, 0.f};
     for (int j = tid; j < p.K; j += NT) {
       const float pj = tg.p[j];
-      if (pj > 0.f || pj != pj)
-        part += (double)pj * ((double)tg.t[j] - (((double)tg.z[j] - (double)m_all) * p.inv_T - lnS));
+      if (pj > 0.f || pj != pj) {
+        // ln p - ln q, a small difference of large numbers: rounded once
+        const Pair q = two_sum(tg.z[j], -m_all) * inv + -lnS;
+        const float d = value_of(Pair{tg.t[j], 0.f} + -q);
+        part = part + Pair{pj, 0.f} * Pair{d, 0.f};
+      }
     }
     if (warp < kLogitsMaxTop / 32) {
-      part = warp_sum(part);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        part = part + Pair{__shfl_xor_sync(0xffffffffu, part.hi, o), __shfl_xor_sync(0xffffffffu, part.lo, o)};
       if (lane == 0) sm.redL[warp] = part;
     }
     __syncthreads();
     if (tid == 0) {
       const float rest = rest_of(tg, sums.none()), P = tg.sum + rest;
-      double loss = 0.0;
-      for (int i = 0; i < min(nw, kLogitsMaxTop / 32); ++i) loss += sm.redL[i];
-      if (rest > 0.f) loss += (double)rest * ((double)logf(rest) - sums.ln_u(p.inv_T));
-      if (S_all != S_all) loss = (double)S_all;
-      if (sums.empty()) loss = P == 0.f ? 0.0 : (double)P * (double)INFINITY;  // no token of the target has a chance
-      p.loss[entry] = (float)((double)w * loss);
+      Pair loss = {0.f, 0.f};
+      for (int i = 0; i < min(nw, kLogitsMaxTop / 32); ++i) loss = loss + sm.redL[i];
+      if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(Pair{logf(rest), 0.f} + -sums.ln_u(p.T)), 0.f};
+      float l = w * value_of(loss);
+      if (S_all != S_all) l = S_all;
+      if (sums.empty()) l = P == 0.f ? 0.f : w * INFINITY;  // no token of the target has a chance
+      p.loss[entry] = l;
       if (p.stats) {
         float* to = p.stats + 4 * (size_t)entry;
         to[0] = m_all;
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
     if (sums.empty())
       write_zeros<T>(p, row, out, g0, g1);
     else
-      write_gradient<T>(p, row, out, g0, g1, slope_of(sums, tg, p.inv_T, (double)w), tg);
+      write_gradient<T>(p, row, out, g0, g1, slope_of(sums, tg, p.T, w), tg);
   }
 }
 
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_backward_kernel(con
   if (sums.empty())
     write_zeros<T>(p, row, out, g0, g1);
   else
-    write_gradient<T>(p, row, out, g0, g1, slope_of(sums, tg, p.inv_T, (double)w * (double)up), tg);
+    write_gradient<T>(p, row, out, g0, g1, slope_of(sums, tg, p.T, w * up), tg);
 }
 
 // The gradient's rows apart from the logits', or on them exactly.
@@ -462,7 +469,7 @@ ssv_status distill_check(const ssv_distill_args* a, DistillParams& p) {
   if (!logits_shape_ok(a->logits, a->logits_stride, a->dtype, a->V, a->n) || a->K < 1 ||
       (a->mode != SSV_DISTILL_RENORM && a->mode != SSV_DISTILL_REST))
     return SSV_ERR_INVALID;
-  if (!logits_scale(a->T, &p.sc)) return SSV_ERR_NOT_FINITE;
+  if (!logits_scale(a->T, &p.T)) return SSV_ERR_NOT_FINITE;
   if (a->V > kLogitsMaxVocab || a->K > kLogitsMaxTop) return SSV_ERR_UNSUPPORTED;
   if (a->n == 0) return SSV_OK;
   if (!a->logits || !a->teacher_token || !a->teacher_logprob) return SSV_ERR_INVALID;
@@ -473,7 +480,6 @@ ssv_status distill_check(const ssv_distill_args* a, DistillParams& p) {
   p.mode = a->mode;
   p.token = a->teacher_token;
   p.logp = a->teacher_logprob;
-  p.inv_T = 1.0 / (double)a->T;
   p.weight = a->weight;
   p.loss = a->loss;
   p.stats = a->stats;

@@ -24,7 +24,7 @@ constexpr int kLogitsMaxVocab = 1 << 19;  // largest V
 constexpr int kLogitsMaxTop = 128;        // most alternatives of a row
 constexpr int kBatch = 4;                 // groups in flight per thread
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLn2 = 0.69314718055994530942;
+constexpr float kLn2 = 0.693147180559945309f;
 
 struct Raw {  // one group
   uint32_t w[8];
@@ -239,12 +239,36 @@ __device__ __forceinline__ float cta_max(float x, float* red) {
   return m;
 }
 
-// ln S of a positive sum, in 64 bits: the exponent apart, so that only the mantissa's logarithm is rounded to 32
-__device__ __forceinline__ double log_sum(float s) {
-  if (!(s > 0.f) || isinf(s)) return (double)logf(s);
+// A value hi + lo of about 48 bits: the logarithms and products that results are differences of.  (The fp64 pipe
+// of this part would take a microsecond for them.)
+struct Pair {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Pair two_sum(float a, float b) {  // exact
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return {s.hi, s.lo + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Pair operator-(Pair a) { return {-a.hi, -a.lo}; }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  return {p, fmaf(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi)};
+}
+// rounded once; infinities and NaN as the leading part has them
+__device__ __forceinline__ float value_of(Pair a) { return fabsf(a.hi) < INFINITY ? a.hi + a.lo : a.hi; }
+
+// ln S of a sum: the exponent apart, so that only the mantissa's logarithm is rounded to 32 bits
+__device__ __forceinline__ Pair log_sum(float s) {
+  if (!(s > 0.f) || isinf(s)) return {logf(s), 0.f};
   int e;
   const float f = frexpf(s, &e);
-  return e * kLn2 + (double)logf(f);
+  // ln 2 = 355 / 512 - 2.1219444005469058e-4; e * 355 / 512 is exact
+  const Pair y = two_sum((float)e * 0.693359375f, logf(f));
+  return {y.hi, y.lo + (float)e * -2.1219444005469058e-4f};
 }
 
 // 2^y on the scale of exp2 for partial sums: f = 2^((from - to) sc); 0 where `from` is -inf
@@ -284,11 +308,20 @@ inline int most_groups(int V, int element_size) { return (V * element_size + 31)
 
 RowSplit split_rows(int rows, int V, int element_size);
 
-// scale of the exponents, log2(e) / T; false where T is not positive or the scale leaves the normal numbers
-inline bool logits_scale(float T, float* sc) {
+// T as the kernels take it
+struct Scale {
+  float sc;          // log2(e) / T, of exponents
+  float hi, lo;      // 1 / T
+};
+
+// false where T is not positive or the scale leaves the normal numbers
+inline bool logits_scale(float T, Scale* s) {
   if (!isfinite(T) || !(T > 0.f)) return false;
-  *sc = (float)(1.4426950408889634 / (double)T);
-  return isfinite(*sc) && *sc >= FLT_MIN;
+  const double inv = 1.0 / (double)T;
+  s->sc = (float)(1.4426950408889634 * inv);
+  s->hi = (float)inv;
+  s->lo = (float)(inv - (double)s->hi);
+  return isfinite(s->sc) && s->sc >= FLT_MIN && s->hi >= FLT_MIN;
 }
 
 // [rows, V] with `stride` elements between rows

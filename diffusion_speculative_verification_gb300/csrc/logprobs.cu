@@ -35,8 +35,7 @@ struct LogprobsParams {
   int V, total_rows, K;
   const int32_t* rows;
   const int32_t* tokens;
-  float sc;       // log2(e) / T
-  double inv_T;
+  Scale T;
   float* logprob;
   int32_t* rank;
   float* entropy;
@@ -78,19 +77,54 @@ __device__ __forceinline__ unsigned long long element_key(float x, int v) {
   return ((unsigned long long)order_bits(x) << 32) | (0xFFFFFFFFu - (uint32_t)v);
 }
 
-// Elements before token t (logit lt) among those of a group.
+// The given token and how elements compare with it: of groups in front of its own an element is before it when no
+// smaller, that is, greater than the next number below; of those behind when greater.
 template <typename T>
-__device__ __noinline__ int count_before(const Raw r, int v0, float lt, int t) {
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < kGroup<T> / 2; ++i) {
-    const float2 x = pair_of<T>(r, i);
-    const int v = v0 + 2 * i;  // below 0: in front of the row
-    n += (x.x > lt || (x.x == lt && v >= 0 && v < t)) ? 1 : 0;
-    n += (x.y > lt || (x.y == lt && v + 1 >= 0 && v + 1 < t)) ? 1 : 0;
+struct Given {
+  int t, group, below;  // below: lt's next lower number as bits of T
+  float lt;
+
+  __device__ __forceinline__ void set(const RowView<T>& row, int token, bool there) {
+    t = token;
+    group = (row.lead + token) / kGroup<T>;
+    lt = there ? load_element(row.row + token) : NAN;  // without a token nothing compares
+    uint32_t b = __float_as_uint(lt) >> (sizeof(T) == 2 ? 16 : 0);
+    const uint32_t sign = sizeof(T) == 2 ? 0x8000u : 0x80000000u;
+    below = (int)((b & ~sign) == 0 ? sign | 1u : (b & sign) ? b + 1 : b - 1);
   }
-  return n;
-}
+
+  // Elements of group g that are before the token.  lt is above -inf.
+  __device__ __forceinline__ int before(const Raw& r, int g, const RowView<T>& row) const {
+    if (g == group) return among(r, row.first(g));
+    int n = 0;
+    if (sizeof(T) == 2) {
+      const uint32_t b = g < group ? (uint32_t)below : __float_as_uint(lt) >> 16, both = b << 16 | b;
+      const __nv_bfloat162 than = *reinterpret_cast<const __nv_bfloat162*>(&both);
+      __nv_bfloat162 c = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c = __hadd2(c, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&r.w[i]), than));
+      n = (int)(__low2float(c) + __high2float(c));
+    } else {
+      const float than = g < group ? __uint_as_float((uint32_t)below) : lt;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += __uint_as_float(r.w[i]) > than ? 1 : 0;
+    }
+    return n;
+  }
+
+  // The same, element by element, for the token's own group and for tokens at -inf.
+  __device__ __noinline__ int among(const Raw r, int v0) const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kGroup<T> / 2; ++i) {
+      const float2 x = pair_of<T>(r, i);
+      const int v = v0 + 2 * i;  // below 0: in front of the row
+      n += (x.x > lt || (x.x == lt && v >= 0 && v < t)) ? 1 : 0;
+      n += (x.y > lt || (x.y == lt && v + 1 >= 0 && v + 1 < t)) ? 1 : 0;
+    }
+    return n;
+  }
+};
 
 // Whole CTA: keys of the row that are >= key.
 template <typename T>
@@ -150,6 +184,29 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
   __syncthreads();
 }
 
+// A bound that the k largest of x[0, n) reach and, but for equal ones, no more: by bisection over the order of the
+// values up to `most`, which ends where exactly k are left.  One warp; -inf where there are fewer.
+__device__ __forceinline__ float nth_largest(const float* x, int n, int k, float most) {
+  constexpr int kPer = kLogitsThreads / 32;
+  uint32_t b[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = (threadIdx.x & 31) + 32 * i;
+    b[i] = j < n ? order_bits(x[j]) : 0u;
+  }
+  uint32_t lo = order_bits(-INFINITY), hi = order_bits(most);  // at least k are >= lo, or lo is -inf's
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    int cnt = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) cnt += b[i] >= mid ? 1 : 0;
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (cnt >= k) lo = mid; else hi = mid - 1;
+    if (cnt == k) break;
+  }
+  return from_order(lo);
+}
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const LogprobsParams p) {
   extern __shared__ float group_top[];  // largest number of every group of this CTA (TOP)
@@ -190,12 +247,14 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
   }
   const RowView<T> row(static_cast<const T*>(p.logits) + (int64_t)r * p.stride, p.V);
   const int g0 = (int)((long long)row.n * rank / c), g1 = (int)((long long)row.n * (rank + 1) / c);
-  const float lt = p.tokens ? load_element(row.row + t) : NAN;  // without a token nothing compares
+  Given<T> given;
+  given.set(row, t, p.tokens != nullptr);
+  const float lt = given.lt;
 
   // ------------------------------------------------------------ the pass
   float m = -INFINITY, S = 0.f, W = 0.f;
   int before = 0;
-  const float2 sc2 = make_float2(p.sc, p.sc);
+  const float2 sc2 = make_float2(p.T.sc, p.T.sc);
   for (int gb = g0 + tid; gb < g1; gb += NT * kBatch) {
     Raw x[kBatch];
 #pragma unroll
@@ -213,9 +272,10 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if (top[u] >= lt && gb + u * NT < g1) before += count_before<T>(x[u], row.first(gb + u * NT), lt, t);
+      if (top[u] >= lt && gb + u * NT < g1)
+        before += lt == -INFINITY ? given.among(x[u], row.first(gb + u * NT)) : given.before(x[u], gb + u * NT, row);
     if (mx > m) {  // sums so far on the new scale
-      const float d = shift_of(m, mx, p.sc), f = ex2(d);
+      const float d = shift_of(m, mx, p.T.sc), f = ex2(d);
       W = f * (W + d * S);
       S = f * S;
       m = mx;
@@ -243,7 +303,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
   // ------------------------------------------------------------ this CTA's part
   const float M = cta_max(m, sm.red);
   {
-    const float d = shift_of(m, M, p.sc), f = ex2(d);
+    const float d = shift_of(m, M, p.T.sc), f = ex2(d);
     const float Sw = warp_sum(f * S), Ww = warp_sum(f * (W + d * S));
     const int nb = warp_sum(before);
     if (lane == 0) {
@@ -252,22 +312,14 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
       sm.redN[warp] = nb;
     }
     if (TOP) sm.top[tid] = m;
-    if (TOP && tid == 0) sm.kth = sm.share = -INFINITY;
   }
   __syncthreads();
-  if (TOP && m > -INFINITY) {
-    // this thread's place among the maxima
-    int place = 0;
-    for (int i = 0; i < NT; i += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(&sm.top[i]);
-      place += (o.x > m || (o.x == m && i < tid)) ? 1 : 0;
-      place += (o.y > m || (o.y == m && i + 1 < tid)) ? 1 : 0;
-      place += (o.z > m || (o.z == m && i + 2 < tid)) ? 1 : 0;
-      place += (o.w > m || (o.w == m && i + 3 < tid)) ? 1 : 0;
+  // the K-th of the threads' maxima by the first warp, the ceil(K / c)-th by the second (or after it)
+  if (TOP)
+    for (int w = warp; w < 2; w += nw) {
+      const float x = nth_largest(sm.top, NT, w ? (p.K + c - 1) / c : p.K, M);
+      if (lane == 0) (w ? sm.share : sm.kth) = x;
     }
-    if (place == p.K - 1) sm.kth = m;
-    if (place == (p.K + c - 1) / c - 1) sm.share = m;
-  }
   if (TOP) __syncthreads();
   if (tid == 0) {
     Part& me = sm.part[rank];
@@ -350,17 +402,18 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
   int nb = 0;
   for (int i = 0; i < c; ++i) {
     const Part& q = sm.part[i];
-    const float d = shift_of(q.m, Mr, p.sc), f = ex2(d);
+    const float d = shift_of(q.m, Mr, p.T.sc), f = ex2(d);
     St += f * q.S;
     Wt += f * (q.W + d * q.S);
     nb += q.before;
   }
   const bool empty = Mr == -INFINITY && St == 0.f;  // nothing above -inf
-  if (tid == 0) {
-    const double lnS = log_sum(St);
-    if (p.lse) p.lse[entry] = empty ? -INFINITY : (float)((double)Mr * p.inv_T + lnS);
-    if (p.entropy) p.entropy[entry] = empty ? 0.f : (float)(lnS - (double)(Wt / St) * kLn2);
-    if (p.logprob) p.logprob[entry] = empty ? -INFINITY : (float)(((double)lt - (double)Mr) * p.inv_T - lnS);
+  const Pair lnS = log_sum(St);
+  if (tid == NT - 1) {
+    const Pair inv = {p.T.hi, p.T.lo};
+    if (p.lse) p.lse[entry] = empty ? -INFINITY : value_of(Pair{Mr, 0.f} * inv + lnS);
+    if (p.entropy) p.entropy[entry] = empty ? 0.f : value_of(lnS + Pair{-(Wt / St) * kLn2, 0.f});
+    if (p.logprob) p.logprob[entry] = empty ? -INFINITY : value_of(two_sum(lt, -Mr) * inv + -lnS);
     if (p.rank) p.rank[entry] = lt == lt ? nb + 1 : 0;
   }
   if (TOP) {
@@ -370,16 +423,16 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
       bisect_top<T>(row, p.K, least, Mr, sm);
       n = p.K;
     }
-    const float lnS = (float)log_sum(St), inv = (float)p.inv_T;
     float* lp = p.top_logprob + (size_t)entry * p.K;
     int32_t* tk = p.top_token + (size_t)entry * p.K;
+    const float ln = value_of(lnS);
     for (int i = tid; i < n; i += NT) {
       const unsigned long long key = sm.merged[i];
       int place = 0;
       for (int j = 0; j < n; ++j) place += sm.merged[j] > key ? 1 : 0;
       if (place < p.K) {
         const float x = from_order((uint32_t)(key >> 32));
-        lp[place] = (x - Mr) * inv - lnS;
+        lp[place] = (x - Mr) * p.T.hi - ln;
         tk[place] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
       }
     }
@@ -404,7 +457,7 @@ RowSplit split_rows(int rows, int V, int element_size) {
   const int groups = most_groups(V, element_size);
   int c = 1;
   while (c < 8 && (long long)rows * c < 608 && groups > 2 * c * kLogitsThreads) c *= 2;
-  while (c < 8 && groups > c * 8192) c *= 2;  // shared memory: a word per group
+  while (c < 8 && groups > c * 9600) c *= 2;  // shared memory: a word per group
   RowSplit sp;
   sp.ctas = c;
   sp.groups = (groups + c - 1) / c;
@@ -420,7 +473,7 @@ extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
   if (!logits_shape_ok(a->logits, a->logits_stride, a->dtype, a->V, a->total_rows) || a->n < 0 || a->top_k < 0)
     return SSV_ERR_INVALID;
   LogprobsParams p;
-  if (!logits_scale(a->T, &p.sc)) return SSV_ERR_NOT_FINITE;
+  if (!logits_scale(a->T, &p.T)) return SSV_ERR_NOT_FINITE;
   if (a->V > kLogitsMaxVocab || a->top_k > kLogitsMaxTop) return SSV_ERR_UNSUPPORTED;
   if (!a->rows && a->n > a->total_rows) return SSV_ERR_INVALID;
   if (a->n == 0) return SSV_OK;
@@ -435,7 +488,6 @@ extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
   p.K = a->top_k;
   p.rows = a->rows;
   p.tokens = a->tokens;
-  p.inv_T = 1.0 / (double)a->T;
   p.logprob = a->logprob;
   p.rank = a->rank;
   p.entropy = a->entropy;

@@ -11,23 +11,25 @@
 // rescaled when the maximum grows), and counts the elements before the given
 // token, which its group's maximum lets it skip mostly.
 //
-// Top alternatives.  The threads' maxima bound the K-th largest element from
-// below: at least K elements are no smaller than the K-th largest of the maxima of
-// one CTA, or than the least over the cluster's c CTAs of each one's
-// ceil(K / c)-th.  With the larger of the two as threshold, groups whose maximum
-// (kept in shared memory, one word per 32 bytes of the row) passes it are read
-// again from L2, and their elements that pass it, hardly more than K, go to the
-// cluster's first CTA as keys (order of the value above the complemented
+// Top alternatives.  The K-th largest of any K or more elements bounds the row's
+// K-th from below.  Each warp gives the j largest of its lanes' maxima, j so that
+// the cluster's warps give about 2 K; with the K-th of these as threshold, groups
+// whose maximum (kept in shared memory, one word per 32 bytes of the row) passes
+// it are listed, read again from L2, one per thread, and their elements that pass
+// it, hardly more than K, go to the cluster's first CTA as keys (order of the value above the complemented
 // index: equal values in the order of their indices).  It ranks them by counting.
 // Where more pass than its list holds (long runs of equal values), it finds the
 // K-th key by bisection over the row.
 #include "logits.cuh"
+
+#include <algorithm>
 
 namespace ssv {
 namespace {
 
 constexpr int kList = 512;        // keys that a list holds
 constexpr int kMaxCluster = 8;
+constexpr int kPool = 2 * kLogitsMaxTop + 8 * kMaxCluster;  // values of the pool at most: 2 K, and one of each warp
 
 struct LogprobsParams {
   const void* logits;
@@ -44,12 +46,12 @@ struct LogprobsParams {
   int32_t* top_token;
   int32_t* dev_status;
   int ctas;
+  int give;  // lane maxima that a warp gives to the pool
 };
 
 struct Part {  // what a CTA knows of its part of the row
   float m, S, W;
   int before;
-  float kth, share;  // its K-th and ceil(K / c)-th largest thread maximum
 };
 constexpr int kPartWords = sizeof(Part) / 4;
 
@@ -58,12 +60,12 @@ struct Shared {
   float red[kLogitsThreads / 32];
   float redS[kLogitsThreads / 32], redW[kLogitsThreads / 32];
   int redN[kLogitsThreads / 32];
-  float kth, share;
-  int count, total;  // keys listed here, keys sent to the cluster's first CTA
+  int groups, count, total;  // groups and keys listed here, keys sent to the cluster's first CTA
   int at;
-  int sum[2];
-  alignas(16) float top[kLogitsThreads];
-  alignas(16) unsigned long long list[kList], merged[kList];
+  float least;
+  alignas(16) uint32_t pool[kPool];  // order of the largest lane maxima of every warp of the cluster, 0: none
+  int group[kList];
+  unsigned long long merged[kList];
 };
 
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -184,39 +186,21 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
   __syncthreads();
 }
 
-// A bound that the k largest of x[0, n) reach and, but for equal ones, no more: by bisection over the order of the
-// values up to `most`, which ends where exactly k are left.  One warp; -inf where there are fewer.
-__device__ __forceinline__ float nth_largest(const float* x, int n, int k, float most) {
-  constexpr int kPer = kLogitsThreads / 32;
-  uint32_t b[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int j = (threadIdx.x & 31) + 32 * i;
-    b[i] = j < n ? order_bits(x[j]) : 0u;
-  }
-  uint32_t lo = order_bits(-INFINITY), hi = order_bits(most);  // at least k are >= lo, or lo is -inf's
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo + 1) / 2;
-    int cnt = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) cnt += b[i] >= mid ? 1 : 0;
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
-    if (cnt >= k) lo = mid; else hi = mid - 1;
-    if (cnt == k) break;
-  }
-  return from_order(lo);
-}
-
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const LogprobsParams p) {
-  extern __shared__ float group_top[];  // largest number of every group of this CTA (TOP)
+  // TOP: largest number of every group of this CTA; then the keys listed here
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  float* group_top = reinterpret_cast<float*>(dynamic);
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(dynamic);
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
   const int c = p.ctas;
   const int rank = (int)blockIdx.x % c, entry = (int)blockIdx.x / c;
   if (tid == 0) {
+    sm.groups = 0;
     sm.count = 0;
     sm.total = 0;
+    sm.least = -INFINITY;
   }
   __syncthreads();
   if (c > 1) cluster_arrive();  // waited for before the first access to another CTA's shared memory
@@ -286,6 +270,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
     float2 S2 = make_float2(0.f, 0.f), W2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
+      if (u && gb + u * NT >= g1) break;
 #pragma unroll
       for (int i = 0; i < kGroup<T> / 2; ++i) {
         float2 y = mul2(add2(pair_of<T>(x[u], i), nm), sc2);
@@ -301,6 +286,23 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
   }
 
   // ------------------------------------------------------------ this CTA's part
+  const int given_n = nw * p.give;  // values that a CTA gives to the pool
+  if (TOP) {
+    uint32_t* mine = sm.pool + rank * given_n + warp * p.give;
+    uint32_t b = order_bits(m);
+    if (p.give == 32) {
+      mine[lane] = b;
+    } else {
+      for (int i = 0; i < p.give; ++i) {
+        const uint32_t most = __reduce_max_sync(0xffffffffu, b);
+        const int who = __ffs(__ballot_sync(0xffffffffu, b == most)) - 1;
+        if (lane == who) {
+          mine[i] = b;
+          b = 0u;
+        }
+      }
+    }
+  }
   const float M = cta_max(m, sm.red);
   {
     const float d = shift_of(m, M, p.T.sc), f = ex2(d);
@@ -311,16 +313,8 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
       sm.redW[warp] = Ww;
       sm.redN[warp] = nb;
     }
-    if (TOP) sm.top[tid] = m;
   }
   __syncthreads();
-  // the K-th of the threads' maxima by the first warp, the ceil(K / c)-th by the second (or after it)
-  if (TOP)
-    for (int w = warp; w < 2; w += nw) {
-      const float x = nth_largest(sm.top, NT, w ? (p.K + c - 1) / c : p.K, M);
-      if (lane == 0) (w ? sm.share : sm.kth) = x;
-    }
-  if (TOP) __syncthreads();
   if (tid == 0) {
     Part& me = sm.part[rank];
     me.m = M;
@@ -331,8 +325,6 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
       me.W += sm.redW[w];
       me.before += sm.redN[w];
     }
-    me.kth = TOP ? sm.kth : 0.f;
-    me.share = TOP ? sm.share : 0.f;
   }
   __syncthreads();
   if (c > 1) {
@@ -344,6 +336,11 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
       const int dst = i / kPartWords, w = i % kPartWords;
       if (dst != rank) cluster_store(cluster_addr(&sm.part[rank], dst) + 4 * w, mine[w]);
     }
+    if (TOP)
+      for (int i = tid; i < c * given_n; i += NT) {
+        const int dst = i / given_n, w = rank * given_n + i % given_n;
+        if (dst != rank) cluster_store(cluster_addr(&sm.pool[w], dst), sm.pool[w]);
+      }
     cluster_arrive();
     if (!TOP && rank != 0) return;
     cluster_wait();
@@ -354,28 +351,44 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
   // ------------------------------------------------------------ alternatives
   float least = -INFINITY;
   if (TOP) {
-    float share = INFINITY;
-    for (int i = 0; i < c; ++i) {
-      least = fmaxf(least, sm.part[i].kth);
-      share = fminf(share, sm.part[i].share);
+    // the K-th of the pool: every value's place in it
+    const int n = c * given_n;
+    for (int i = tid; i < n; i += NT) {
+      const uint32_t v = sm.pool[i];
+      int place = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const uint32_t o = sm.pool[j];
+        place += (o > v || (o == v && j < i)) ? 1 : 0;
+      }
+      if (place == p.K - 1 && v) sm.least = from_order(v);
     }
-    least = fmaxf(least, share);
-    for (int g = g0 + tid; g < g1; g += NT) {
-      const float gt = group_top[g - g0];
-      if (gt >= least && gt > -INFINITY) {
-        const Raw x = row.load(g);
-        const int v0 = row.first(g);
+    __syncthreads();
+    least = sm.least;
+    // groups that reach it
+    if (m >= least && m > -INFINITY)
+      for (int g = g0 + tid; g < g1; g += NT) {
+        const float gt = group_top[g - g0];
+        if (gt >= least && gt > -INFINITY) {
+          const int at = atomicAdd(&sm.groups, 1);
+          if (at < kList) sm.group[at] = g;
+        }
+      }
+    __syncthreads();
+    // their elements that do; more groups than the list holds are more elements, too
+    const int ng = sm.groups;
+    if (ng > kList && tid == 0) sm.count = ng;
+    for (int i = tid; i < ng && ng <= kList; i += NT) {
+      const int g = sm.group[i];
+      const Raw x = row.load(g);
+      const int v0 = row.first(g);
 #pragma unroll
-        for (int i = 0; i < kGroup<T> / 2; ++i) {
-          const float2 y = pair_of<T>(x, i);
-          if (y.x >= least && y.x > -INFINITY) {
-            const int at = atomicAdd(&sm.count, 1);
-            if (at < kList) sm.list[at] = element_key(y.x, v0 + 2 * i);
-          }
-          if (y.y >= least && y.y > -INFINITY) {
-            const int at = atomicAdd(&sm.count, 1);
-            if (at < kList) sm.list[at] = element_key(y.y, v0 + 2 * i + 1);
-          }
+      for (int e = 0; e < kGroup<T>; ++e) {
+        const float2 y = pair_of<T>(x, e / 2);
+        const float z = (e & 1) ? y.y : y.x;
+        if (z >= least && z > -INFINITY) {
+          const int at = atomicAdd(&sm.count, 1);
+          if (at < kList) list[at] = element_key(z, v0 + e);
         }
       }
     }
@@ -386,12 +399,12 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
       __syncthreads();
       const int at = sm.at;
       if (at + mine <= kList)
-        for (int i = tid; i < mine; i += NT) cluster_store64(cluster_addr(&sm.merged[at + i], 0), sm.list[i]);
+        for (int i = tid; i < mine; i += NT) cluster_store64(cluster_addr(&sm.merged[at + i], 0), list[i]);
       cluster_arrive();
       if (rank != 0) return;
       cluster_wait();
     } else {
-      for (int i = tid; i < min(mine, kList); i += NT) sm.merged[i] = sm.list[i];
+      for (int i = tid; i < min(mine, kList); i += NT) sm.merged[i] = list[i];
       if (tid == 0) sm.total = mine;
       __syncthreads();
     }
@@ -429,6 +442,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
     for (int i = tid; i < n; i += NT) {
       const unsigned long long key = sm.merged[i];
       int place = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) place += sm.merged[j] > key ? 1 : 0;
       if (place < p.K) {
         const float x = from_order((uint32_t)(key >> 32));
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
 template <typename T>
 cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, cudaStream_t st) {
   if (p.K == 0) return launch_rows(logprobs_kernel<T, false>, n, sp, 0, st, p);
-  return launch_rows(logprobs_kernel<T, true>, n, sp, sizeof(float) * (size_t)sp.groups, st, p);
+  return launch_rows(logprobs_kernel<T, true>, n, sp, std::max(sizeof(float) * sp.groups, sizeof(unsigned long long) * kList), st, p);
 }
 
 }  // namespace
@@ -456,7 +470,7 @@ cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, 
 RowSplit split_rows(int rows, int V, int element_size) {
   const int groups = most_groups(V, element_size);
   int c = 1;
-  while (c < 8 && (long long)rows * c < 608 && groups > 2 * c * kLogitsThreads) c *= 2;
+  while (c < 8 && (long long)rows * c * 2 <= 608 && groups > 2 * c * kLogitsThreads) c *= 2;
   while (c < 8 && groups > c * 9600) c *= 2;  // shared memory: a word per group
   RowSplit sp;
   sp.ctas = c;
@@ -497,6 +511,8 @@ extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
   p.dev_status = a->dev_status;
   const RowSplit sp = split_rows(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4);
   p.ctas = sp.ctas;
+  const int warps = sp.ctas * (sp.threads / 32);
+  p.give = std::min(32, (2 * a->top_k + warps - 1) / warps);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = a->dtype == SSV_BF16 ? logprobs_launch<__nv_bfloat16>(p, a->n, sp, st)
                                              : logprobs_launch<float>(p, a->n, sp, st);

@@ -12,17 +12,23 @@
 // target leaves little there.  For that the listed tokens of a CTA's part are
 // bits of a map in shared memory, by which a group drops its listed elements.
 //
-// Forward: one pass over a row for the maximum and sum of the other tokens; the
-// listed ones, K gathers, join at the end.  With the gradient, the cluster's CTAs
-// exchange their sums, and each reads its part of the row again, from L2, and
-// writes the gradient; the listed tokens' entries are then written over.  Backward:
-// the same second pass from the forward's statistics.
+// The loss alone: one pass over a row for the maximum and sum of the other tokens,
+// its vectors coming through a ring; the listed ones, K gathers, join at the end.
+// With the gradient, the CTAs of a cluster hold the row in shared memory,
+// exchange their sums, and write the gradient from there; the listed tokens'
+// entries are then written over.  Each logit is read once and each gradient
+// written once.  Backward: the same second part from the forward's statistics.
 #include "logits.cuh"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace ssv {
 namespace {
 
-constexpr int kMaxCluster = 8;
+constexpr int kParts = 8 * kMaxCluster;        // warps of a cluster
+constexpr int kHash = 2 * kLogitsMaxTop;       // places of the table in which repeated tokens meet
+constexpr int kEach = kLogitsMaxTop / 32;      // listed tokens of a lane
 
 struct DistillParams {
   const void* logits;
@@ -38,103 +44,164 @@ struct DistillParams {
   const float* grad_loss;
   void* grad;
   int32_t* dev_status;
-  int ctas;
-  int vec;  // rows of the gradient lie as those of the logits do to 32-byte boundaries
+  int log_c, log_nt;
+  int slot_bytes;
+  int vec;  // rows of the gradient lie as those of the logits do to 16-byte boundaries
 };
 
-// The target of a row: listed tokens (-1: absent), each once, their probabilities and the logarithms of these.
+struct Mass {
+  float sum, rest;  // sum p, r
+};
+
+// The target of a row: listed tokens (-1: absent), each once, their probabilities and the logarithms of these, and the
+// drafter's logits of them.
 struct Target {
   int token[kLogitsMaxTop];
-  float p[kLogitsMaxTop], t[kLogitsMaxTop];
-  float z[kLogitsMaxTop];  // the drafter's logits of them
-  float sum, rest;         // sum p, r
+  float p[kLogitsMaxTop], t[kLogitsMaxTop], z[kLogitsMaxTop];
+  int hash[kHash];
+  Mass mass;
 };
 
-// Whole CTA: the target of row i.  A token listed more than once counts with the sum of its probabilities.
-__device__ __forceinline__ void load_target(const DistillParams& p, int i, bool tell, Target& tg) {
-  const int tid = threadIdx.x, NT = blockDim.x;
-  for (int j = tid; j < p.K; j += NT) {
-    int v = p.token[(size_t)i * p.K + j];
-    float t = p.logp[(size_t)i * p.K + j];
-    if (v < 0 || v >= p.V) {
-      if (v != -1 && tell) report(p.dev_status, SSV_ERR_INVALID);
-      v = -1;
-      t = -INFINITY;
-    }
-    tg.token[j] = v;
-    tg.t[j] = t;
-  }
-  __syncthreads();
-  if (tid < 32) {
-    // probabilities, by one warp: four entries per lane, the sums in a fixed order
-    float x[kLogitsMaxTop / 32], mx = -INFINITY;
+// Whole CTA: the listed tokens of row i and the given values, in three parts, so that callers can work in between:
+// loads into registers; tokens into shared memory (true where one is listed twice); probabilities.
+struct Listed {
+  int v[kEach];
+  float t[kEach];
+};
+
+template <typename F>
+__device__ __forceinline__ void each_listed(int K, F f) {
+  int n = 0;
+  for (int j = threadIdx.x; j < K; j += blockDim.x) f(n++, j);
+}
+
+__device__ __forceinline__ Listed load_listed(const DistillParams& p, int i, bool tell, Target& tg) {
+  Listed l;
+  const int32_t* token = p.token + (size_t)i * p.K;
+  const float* logp = p.logp + (size_t)i * p.K;
 #pragma unroll
-    for (int k = 0; k < kLogitsMaxTop / 32; ++k) {
-      const int j = tid + 32 * k;
+  for (int n = 0; n < kEach; ++n) {
+    const int j = threadIdx.x + n * blockDim.x;
+    l.v[n] = -1;
+    l.t[n] = -INFINITY;
+    if (j < p.K) {
+      l.v[n] = token[j];
+      l.t[n] = logp[j];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kEach; ++n)
+    if (l.v[n] < 0 || l.v[n] >= p.V) {
+      if (l.v[n] != -1 && tell) report(p.dev_status, SSV_ERR_INVALID);
+      l.v[n] = -1;
+      l.t[n] = -INFINITY;
+    }
+  for (int h = threadIdx.x; h < kHash; h += blockDim.x) tg.hash[h] = -1;
+  return l;
+}
+
+// After a barrier behind load_listed.
+__device__ __forceinline__ bool place_listed(const DistillParams& p, const Listed& l, Target& tg) {
+  bool twice = false;
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const int j = threadIdx.x + n * blockDim.x;
+    if (j >= p.K) break;
+    tg.token[j] = l.v[n];
+    tg.t[j] = l.t[n];
+    if (l.v[n] < 0) continue;
+    // at most K of 2 K places are taken, so that a free one is met within K steps
+    for (uint32_t h = ((uint32_t)l.v[n] * 2654435761u) >> 24, s = 0; s < kHash; ++s, h = (h + 1) % kHash) {
+      const int was = atomicCAS(&tg.hash[h], -1, l.v[n]);
+      if (was == -1) break;
+      if (was == l.v[n]) {
+        twice = true;
+        break;
+      }
+    }
+  }
+  return twice;
+}
+
+// After a barrier behind place_listed; `twice`: of any thread.  Ends with one.
+__device__ __forceinline__ Mass weigh_listed(const DistillParams& p, bool twice, Target& tg) {
+  const bool as_is = p.mode == SSV_DISTILL_REST;
+  if (threadIdx.x < 32) {
+    // four entries per lane, the sums in a fixed order
+    const int lane = threadIdx.x;
+    float x[kEach], mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = lane + 32 * k;
       x[k] = j < p.K ? tg.t[j] : -INFINITY;
       mx = fmaxf(mx, x[k]);
     }
     mx = warp_max(mx);
     // relative to the largest for a softmax; as they are where they are log-probabilities
-    const float ref = p.mode == SSV_DISTILL_REST || mx == -INFINITY ? 0.f : mx;
-    float s = 0.f;
+    const float ref = as_is || mx == -INFINITY ? 0.f : mx;
+    float s = 0.f, e[kEach];
 #pragma unroll
-    for (int k = 0; k < kLogitsMaxTop / 32; ++k) {
+    for (int k = 0; k < kEach; ++k) {
       x[k] -= ref;
-      s += expf(x[k]);
+      e[k] = expf(x[k]);
+      s += e[k];
     }
     s = warp_sum(s);
-    const float norm = p.mode == SSV_DISTILL_REST || s == 0.f ? 1.f : s;
-    const float ln = logf(norm);
+    const float norm = as_is || s == 0.f ? 1.f : s, ln = logf(norm);
 #pragma unroll
-    for (int k = 0; k < kLogitsMaxTop / 32; ++k) {
-      const int j = tid + 32 * k;
+    for (int k = 0; k < kEach; ++k) {
+      const int j = lane + 32 * k;
       if (j < p.K) {
-        tg.p[j] = expf(x[k]) / norm;
+        tg.p[j] = e[k] / norm;
         tg.t[j] = x[k] - ln;
       }
     }
-    if (tid == 0) {
-      tg.sum = p.mode == SSV_DISTILL_REST ? s : (s == 0.f ? 0.f : 1.f);
-      if (s != s) tg.sum = s;
-      tg.rest = p.mode == SSV_DISTILL_REST ? (s > 1.f ? 0.f : 1.f - s) : 0.f;  // NaN stays
+    if (lane == 0) {
+      tg.mass.sum = as_is || s == 0.f || s != s ? s : 1.f;
+      tg.mass.rest = as_is ? (s > 1.f ? 0.f : 1.f - s) : 0.f;  // NaN stays
     }
   }
   __syncthreads();
-  // duplicates: the first of them takes the others' probabilities
-  float p_all[(kLogitsMaxTop + 31) / 32];
-  unsigned twice = 0, later = 0;
-  int n = 0;
-  for (int j = tid; j < p.K; j += NT, ++n) {
-    const int v = tg.token[j];
-    float s = tg.p[j];
-    bool first = true;
-    for (int i2 = 0; i2 < p.K; ++i2) {
-      if (i2 == j || v < 0 || tg.token[i2] != v) continue;
-      if (i2 < j) first = false; else { s += tg.p[i2]; twice |= 1u << n; }
-    }
-    if (!first) later |= 1u << n;
-    if (n < (kLogitsMaxTop + 31) / 32) p_all[n] = s;
+  if (twice) {  // the first of equal tokens takes the others' probabilities
+    float all[kEach];
+    unsigned first = 0, later = 0;
+    each_listed(p.K, [&](int n, int j) {
+      const int v = tg.token[j];
+      float q = tg.p[j];
+      bool leads = true, alone = true;
+      for (int o = 0; o < p.K; ++o) {
+        if (o == j || v < 0 || tg.token[o] != v) continue;
+        alone = false;
+        if (o < j) leads = false; else q += tg.p[o];
+      }
+      if (!leads) later |= 1u << n; else if (!alone) first |= 1u << n;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (k == n) all[k] = q;
+    });
+    __syncthreads();
+    each_listed(p.K, [&](int n, int j) {
+      float q = 0.f;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (k == n) q = all[k];
+      if (later >> n & 1u) {
+        tg.token[j] = -1;
+        tg.p[j] = 0.f;
+        tg.t[j] = -INFINITY;
+      } else if (first >> n & 1u) {
+        tg.p[j] = q;
+        tg.t[j] = logf(q);
+      }
+    });
+    __syncthreads();
   }
-  __syncthreads();
-  n = 0;
-  for (int j = tid; j < p.K; j += NT, ++n) {
-    if (later >> n & 1) {
-      tg.token[j] = -1;
-      tg.p[j] = 0.f;
-      tg.t[j] = -INFINITY;
-    } else if (twice >> n & 1) {
-      tg.p[j] = p_all[n];
-      tg.t[j] = logf(p_all[n]);
-    }
-  }
+  return tg.mass;
 }
 
 // r, where the drafter leaves the other tokens nothing (every one is listed or masked): there, what the roundings of
 // fp32 log-probabilities leave of 1 is no probability of other tokens.
-__device__ __forceinline__ float rest_of(const Target& tg, bool none) {
-  return none && tg.rest < 0x1p-20f ? 0.f : tg.rest;
-}
+__device__ __forceinline__ float rest_of(const Mass& t, bool none) { return none && t.rest < 0x1p-20f ? 0.f : t.rest; }
 
 // What a row's softmax needs: maximum and sum, relative to it, over the row and over the tokens that are not listed.
 struct Sums {
@@ -153,167 +220,205 @@ struct Slope {
   float ref, coef;   // other tokens: coef 2^((z - ref) sc)
   float top, share;  // listed ones: wT (share 2^((z - top) sc) - p)
   float wT;
+  bool empty;
 };
 
-__device__ __forceinline__ Slope slope_of(const Sums& s, const Target& tg, const Scale& T, float w) {
-  const float rest = rest_of(tg, s.none()), P = tg.sum + rest;
+__device__ __forceinline__ Slope slope_of(const Sums& s, const Mass& t, const Scale& T, float w) {
+  const float rest = rest_of(t, s.none()), P = t.sum + rest;
   Slope k;
   k.wT = w * T.hi;
   k.ref = s.none() ? 0.f : s.mr;
   k.coef = s.none() ? 0.f : k.wT * (P * expf(value_of(s.ln_u(T))) - rest) / s.Sr;
   k.top = s.m;
   k.share = P / s.S;
+  k.empty = s.empty();
   return k;
 }
 
-// Gradient over the groups [g0, g1) of a row: of the other tokens, then that of the listed ones over it.
+__device__ __forceinline__ void store_vector(void* p, const uint4& r) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w) : "memory");
+}
+
 template <typename T>
-__device__ __forceinline__ void write_gradient(const DistillParams& p, const RowView<T>& row, T* out, int g0, int g1,
-                                               const Slope& k, const Target& tg) {
+__device__ __forceinline__ uint32_t two_of(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// a vector of eight or four values f(e)
+template <typename T, typename F>
+__device__ __forceinline__ uint4 pack_vector(F f) {
+  uint4 y;
+  if constexpr (sizeof(T) == 2) {
+    y.x = two_of<T>(f(0), f(1));
+    y.y = two_of<T>(f(2), f(3));
+    y.z = two_of<T>(f(4), f(5));
+    y.w = two_of<T>(f(6), f(7));
+  } else {
+    y.x = __float_as_uint(f(0));
+    y.y = __float_as_uint(f(1));
+    y.z = __float_as_uint(f(2));
+    y.w = __float_as_uint(f(3));
+  }
+  return y;
+}
+
+// Vectors of the output, with f(v) for element v, at any offset from a vector of the input.
+template <typename T, typename F>
+__device__ __forceinline__ void write_elements(T* out, int lo, int hi, F f) {
+  const int lead = (int)((reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));
+  char* base = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(15));
+  const int first = (lo + lead) / kVec<T>, end = (hi + lead + kVec<T> - 1) / kVec<T>;
+  for (int i = first + threadIdx.x; i < end; i += blockDim.x) {
+    const int v0 = i * kVec<T> - lead;
+    if (v0 >= lo && v0 + kVec<T> <= hi) {
+      store_vector(base + (size_t)i * 16, pack_vector<T>([&](int e) { return f(v0 + e); }));
+    } else {
+      for (int v = max(v0, lo); v < min(v0 + kVec<T>, hi); ++v) out[v] = Elem<T>::from_f32(f(v));
+    }
+  }
+}
+
+// Gradient of a CTA's part, from its slots: of the other tokens, then that of the listed ones over it.  `aligned`: the
+// output's vectors are those of the input.
+template <typename T>
+__device__ __forceinline__ void write_gradient(const DistillParams& p, const RowView<T>& row, const PartView<T>& part,
+                                               const uint4* slots, T* out, const Slope& k, const Target& tg) {
   const int tid = threadIdx.x, NT = blockDim.x;
-  const int v_lo = max(0, row.first(g0)), v_hi = min(row.V, row.first(g1));
   if (p.vec) {
-    char* to = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(31));
+    char* to = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(15)) + (size_t)part.i0 * 16;
     const float2 sc2 = make_float2(p.T.sc, p.T.sc), ref2 = make_float2(-k.ref, -k.ref), c2 = make_float2(k.coef, k.coef);
-    for (int gb = g0 + tid; gb < g1; gb += NT * kBatch) {
-      Raw x[kBatch];
+    auto gradient = [&](const uint4& x) {
+      float2 y[kVec<T> / 2];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int g = gb + u * NT;
-        if (g < g1 && row.whole(g)) x[u] = load_raw(row.base + (size_t)g * 32);
+      for (int e = 0; e < kVec<T> / 2; ++e) {
+        const float2 a = mul2(add2(pair_of<T>(x, e), ref2), sc2);
+        y[e] = mul2(make_float2(ex2(a.x), ex2(a.y)), c2);
       }
+      return pack_vector<T>([&](int e) { return e & 1 ? y[e / 2].y : y[e / 2].x; });
+    };
+    // whole vectors, kBatch at a time; the row's first and last one by element, each by the thread that has it
+    const int n = part.i1 - part.i0, begin = row.lo > part.i0 ? 1 : 0, end = min(part.i1, row.hi) - part.i0;
+    int i = tid < begin ? tid + NT : tid;
+    const uint4* from = slots + i;
+    to += (size_t)i * 16;
+    for (; i + NT * (kBatch - 1) < end; i += NT * kBatch, from += NT * kBatch, to += (size_t)(NT * kBatch) * 16) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int g = gb + u * NT;
-        if (g >= g1) continue;
-        if (row.whole(g)) {
-          Raw y;
-#pragma unroll
-          for (int i = 0; i < kGroup<T> / 2; ++i) {
-            const float2 a = mul2(add2(pair_of<T>(x[u], i), ref2), sc2);
-            put_pair<T>(y, i, mul2(make_float2(ex2(a.x), ex2(a.y)), c2));
-          }
-          store_raw(to + (size_t)g * 32, y);
-        } else {
-          for (int e = 0; e < kGroup<T>; ++e) {
-            const int v = row.first(g) + e;
-            if (v >= 0 && v < row.V)
-              out[v] = Elem<T>::from_f32(ex2((load_element(row.row + v) - k.ref) * p.T.sc) * k.coef);
-          }
-        }
+      for (int u = 0; u < kBatch; ++u) store_vector(to + (size_t)(NT * 16) * u, gradient(from[NT * u]));
+    }
+    for (; i < end; i += NT, from += NT, to += (size_t)NT * 16) store_vector(to, gradient(*from));
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
+      const int j = q ? n - 1 : 0;
+      if (n > 0 && (q == 0 || n > 1) && !row.whole(part.i0 + j) && tid == (j & (NT - 1))) {
+        const uint4 y = gradient(slots[j]);
+        const T* e = reinterpret_cast<const T*>(&y);
+        for (int v = max(0, row.first(part.i0 + j)); v < min(row.V, row.first(part.i0 + j + 1)); ++v)
+          out[v] = e[v - row.first(part.i0 + j)];
       }
     }
   } else {
-    for (int v = v_lo + tid; v < v_hi; v += NT)
-      out[v] = Elem<T>::from_f32(ex2((load_element(row.row + v) - k.ref) * p.T.sc) * k.coef);
+    __syncthreads();  // every thread's vectors are there
+    const T* in = reinterpret_cast<const T*>(slots) - part.at;
+    write_elements<T>(out, part.lo, part.hi, [&](int v) { return ex2((Elem<T>::to_f32(in[v]) - k.ref) * p.T.sc) * k.coef; });
   }
   __syncthreads();
-  for (int j = tid; j < p.K; j += NT) {
+  each_listed(p.K, [&](int, int j) {
     const int v = tg.token[j];
-    if (v >= v_lo && v < v_hi) out[v] = Elem<T>::from_f32(k.wT * (k.share * ex2((tg.z[j] - k.top) * p.T.sc) - tg.p[j]));
-  }
+    if (v >= part.lo && v < part.hi) out[v] = Elem<T>::from_f32(k.wT * (k.share * ex2((tg.z[j] - k.top) * p.T.sc) - tg.p[j]));
+  });
 }
 
 template <typename T>
-__device__ __forceinline__ void write_zeros(const DistillParams& p, const RowView<T>& row, T* out, int g0, int g1) {
-  const int tid = threadIdx.x, NT = blockDim.x;
-  const int v_lo = max(0, row.first(g0)), v_hi = min(row.V, row.first(g1));
-  if (p.vec) {
-    char* to = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(31));
-    Raw zero;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) zero.w[i] = 0u;
-    for (int g = g0 + tid; g < g1; g += NT) {
-      if (row.whole(g)) {
-        store_raw(to + (size_t)g * 32, zero);
-      } else {
-        for (int e = 0; e < kGroup<T>; ++e) {
-          const int v = row.first(g) + e;
-          if (v >= 0 && v < row.V) out[v] = Elem<T>::from_f32(0.f);
-        }
-      }
-    }
-  } else {
-    for (int v = v_lo + tid; v < v_hi; v += NT) out[v] = Elem<T>::from_f32(0.f);
-  }
+__device__ __forceinline__ void write_zeros(const PartView<T>& part, T* out) {
+  write_elements<T>(out, part.lo, part.hi, [](int) { return 0.f; });
 }
-
-struct Part {
-  float m, S;  // maximum and sum of the other tokens of a CTA's part
-};
 
 struct Shared {
   Target tg;
-  Part part[kMaxCluster];
-  float red[kLogitsThreads / 32], redS[kLogitsThreads / 32];
-  Pair redL[kLogitsMaxTop / 32];
+  Slope slope;
+  uint32_t part[kParts][2];  // of every warp: maximum and sum of its other tokens
 };
+
+// waits until at most n of the thread's copies are on their way (n above 7: until 7 are)
+__device__ __forceinline__ void copy_wait_all_but(int n) {
+  switch (n) {
+    case 0: copy_wait<0>(); break;
+    case 1: copy_wait<1>(); break;
+    case 2: copy_wait<2>(); break;
+    case 3: copy_wait<3>(); break;
+    case 4: copy_wait<4>(); break;
+    case 5: copy_wait<5>(); break;
+    case 6: copy_wait<6>(); break;
+    default: copy_wait<7>(); break;
+  }
+}
 
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const DistillParams p) {
-  extern __shared__ uint32_t listed[];  // a bit per element of this CTA's groups: it is a listed token
+  // slots: a ring, or with the gradient the CTA's whole part; behind them a word per thread and step, whose bit
+  // (vector of the step, element) says that the element is a listed token
+  extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
-  const int c = p.ctas;
-  const int rank = (int)blockIdx.x % c, entry = (int)blockIdx.x / c;
+  const int c = 1 << p.log_c;
+  const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
+  uint4* slots = reinterpret_cast<uint4*>(dynamic);
+  uint32_t* listed = reinterpret_cast<uint32_t*>(dynamic + p.slot_bytes);
   if (c > 1) cluster_arrive();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_trigger();
   const float w = p.weight ? p.weight[entry] : 1.f;
   const RowView<T> row(static_cast<const T*>(p.logits) + (int64_t)entry * p.stride, p.V);
+  const PartView<T> part(row, rank, p.log_c, p.log_nt);
   T* out = GRAD ? static_cast<T*>(p.grad) + (int64_t)entry * p.grad_stride : nullptr;
-  const int g0 = (int)((long long)row.n * rank / c), g1 = (int)((long long)row.n * (rank + 1) / c);
   if (w == 0.f) {  // not read at all
     if (rank == 0 && tid == 0) {
       p.loss[entry] = 0.f;
       if (p.stats)
         for (int i = 0; i < 4; ++i) p.stats[4 * (size_t)entry + i] = 0.f;
     }
-    if (GRAD) write_zeros<T>(p, row, out, g0, g1);
+    if (GRAD) write_zeros<T>(part, out);
     if (c > 1) cluster_wait();
     return;
   }
+  auto step_slots = [&](int k) { return slots + kBatch * (GRAD ? k : k % kStages) * NT + tid; };
+  const int ahead = GRAD ? part.steps : kStages;
+  for (int k = 0; k < ahead; ++k) part.fetch(row, k, step_slots(k));
 
   // ------------------------------------------------------------ the target
   Target& tg = sm.tg;
-  const int words = ((g1 - g0) * kGroup<T> + 31) / 32;
-  for (int i = tid; i < words; i += NT) listed[i] = 0u;
-  load_target(p, entry, rank == 0, tg);
+  const Listed mine = load_listed(p, entry, rank == 0, tg);
+  for (int i = tid; i < part.steps * NT; i += NT) listed[i] = 0u;
   __syncthreads();
-  const int at0 = row.first(g0);
-  for (int j = tid; j < p.K; j += NT) {
-    const int v = tg.token[j];
-    if (v < 0) continue;
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const int j = tid + n * NT, v = mine.v[n];
+    if (j >= p.K || v < 0) continue;
     tg.z[j] = load_element(row.row + v);
-    const int b = v - at0;
-    if (b >= 0 && b < (g1 - g0) * kGroup<T>) atomicOr(&listed[b >> 5], 1u << (b & 31));
+    if (v >= part.lo && v < part.hi) {
+      const int i = (v - part.at) / kVec<T>, e = (v - part.at) % kVec<T>, s = i >> p.log_nt;
+      atomicOr(&listed[s / kBatch * NT + (i & (NT - 1))], 1u << (s % kBatch * kVec<T> + e));
+    }
   }
-  __syncthreads();
+  const bool twice = __syncthreads_or(place_listed(p, mine, tg));
+  const Mass mass = weigh_listed(p, twice, tg);
 
   // ------------------------------------------------------------ the other tokens
   float m = -INFINITY, S = 0.f;
   const float2 sc2 = make_float2(p.T.sc, p.T.sc);
-  for (int gb = g0 + tid; gb < g1; gb += NT * kBatch) {
-    Raw x[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int g = gb + u * NT;
-      if (g < g1) x[u] = row.load(g); else set_none<T>(x[u]);
+  auto step = [&](auto is_full, int k) {
+    constexpr bool FULL = decltype(is_full)::value;
+    uint4* at = step_slots(k);
+    // a listed element counts as -inf from here on (its gradient is written over)
+    for (uint32_t bits = listed[k * NT + tid]; bits; bits &= bits - 1) {
+      const int b = __ffs(bits) - 1;
+      reinterpret_cast<T*>(at + NT * (b / kVec<T>))[b % kVec<T>] = Elem<T>::from_f32(-INFINITY);
     }
-    float mx = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int g = gb + u * NT;
-      if (g < g1) {
-        const int b = (g - g0) * kGroup<T>;
-        unsigned bits = listed[b >> 5] >> (b & 31) & ((1u << kGroup<T>) - 1u);
-        while (bits) {
-          drop_element<T>(x[u], __ffs(bits) - 1);
-          bits &= bits - 1;
-        }
-      }
-      mx = fmaxf(mx, group_max<T>(x[u]));
-    }
+    uint4 x[kBatch];
+    part.template take<FULL>(k, at, x);
+    const float mx = step_max<T>(x);
+    if (!GRAD) part.fetch(row, k + kStages, at);  // into the slots that have just been read
     if (mx > m) {
       S *= ex2(shift_of(m, mx, p.T.sc));
       m = mx;
@@ -323,133 +428,149 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
     float2 S2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
+      if (!FULL && part.i0 + tid + NT * (kBatch * k + u) >= part.i1) break;
 #pragma unroll
-      for (int i = 0; i < kGroup<T> / 2; ++i) {
+      for (int i = 0; i < kVec<T> / 2; ++i) {
         const float2 y = mul2(add2(pair_of<T>(x[u], i), nm), sc2);
         S2 = add2(S2, make_float2(ex2(y.x), ex2(y.y)));
       }
     }
     S += S2.x + S2.y;
+  };
+  for (int k = 0; k < part.steps; ++k) {
+    if (GRAD) copy_wait_all_but(part.steps - 1 - k); else copy_wait<kStages - 1>();
+    if (part.full(k)) step(std::true_type{}, k); else step(std::false_type{}, k);
   }
-  const float M = cta_max(m, sm.red);
+  if (!GRAD) copy_wait<0>();
   {
-    const float Sw = warp_sum(ex2(shift_of(m, M, p.T.sc)) * S);
-    if (lane == 0) sm.redS[warp] = Sw;
+    const float M = warp_max(m), Sw = warp_sum(ex2(shift_of(m, M, p.T.sc)) * S);
+    if (c > 1) cluster_wait();
+    const int me = rank * nw + warp;
+    const uint32_t word = lane & 1 ? __float_as_uint(Sw) : __float_as_uint(M);
+    if (c == 1) {
+      if (lane < 2) sm.part[me][lane] = word;
+    } else if (lane < 2 * (GRAD ? c : 1)) {  // the loss alone is the first CTA's
+      cluster_store(cluster_addr(&sm.part[me][lane & 1], lane >> 1), word);
+    }
   }
-  __syncthreads();
-  if (tid == 0) {
-    float s = 0.f;
-    for (int i = 0; i < nw; ++i) s += sm.redS[i];
-    sm.part[rank].m = M;
-    sm.part[rank].S = s;
-  }
-  __syncthreads();
   if (c > 1) {
-    cluster_wait();
-    const int to = GRAD ? c : 1;  // the loss alone is the first CTA's
-    if (tid < 2 * to && tid / 2 != rank)
-      cluster_store(cluster_addr(&sm.part[rank], tid / 2) + 4 * (tid & 1),
-                    reinterpret_cast<const uint32_t*>(&sm.part[rank])[tid & 1]);
     cluster_arrive();
     if (!GRAD && rank != 0) return;
     cluster_wait();
+  } else {
+    __syncthreads();
   }
+  if (!GRAD && warp != 0) return;
 
-  // ------------------------------------------------------------ the row's statistics
-  float mr = -INFINITY;
-  for (int i = 0; i < c; ++i) mr = fmaxf(mr, sm.part[i].m);
-  float Sr = 0.f;
-  for (int i = 0; i < c; ++i) Sr += ex2(shift_of(sm.part[i].m, mr, p.T.sc)) * sm.part[i].S;
-  float mt = -INFINITY;
-  for (int j = tid; j < p.K; j += NT)
-    if (tg.token[j] >= 0) mt = fmaxf(mt, tg.z[j]);
-  const float m_all = fmaxf(mr, cta_max(mt, sm.red));
-  float st = 0.f;
-  for (int j = tid; j < p.K; j += NT)
-    if (tg.token[j] >= 0) st += ex2((tg.z[j] - (m_all == -INFINITY ? 0.f : m_all)) * p.T.sc);
-  st = warp_sum(st);
-  if (lane == 0) sm.redS[warp] = st;
-  __syncthreads();
-  const float shift = shift_of(mr, m_all, p.T.sc);
-  float S_all = ex2(shift) * Sr;
-  for (int i = 0; i < nw; ++i) S_all += sm.redS[i];
-  const Sums sums = {m_all, S_all, mr, Sr};
-  if (rank == 0) {
-    const Pair lnS = log_sum(S_all), inv = {p.T.hi, p.T.lo};
-    Pair part = {0.f, 0.f};
-    for (int j = tid; j < p.K; j += NT) {
-      const float pj = tg.p[j];
+  // ------------------------------------------------------------ the row's sums, by one warp of each CTA in the same order
+  Sums sums;
+  if (warp == 0) {
+    const int n = c * nw;
+    const float m0 = lane < n ? __uint_as_float(sm.part[lane][0]) : -INFINITY;
+    const float m1 = lane + 32 < n ? __uint_as_float(sm.part[lane + 32][0]) : -INFINITY;
+    sums.mr = warp_max(fmaxf(m0, m1));
+    float s = lane < n ? ex2(shift_of(m0, sums.mr, p.T.sc)) * __uint_as_float(sm.part[lane][1]) : 0.f;
+    if (lane + 32 < n) s += ex2(shift_of(m1, sums.mr, p.T.sc)) * __uint_as_float(sm.part[lane + 32][1]);
+    sums.Sr = warp_sum(s);
+    float mt = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = lane + 32 * k;
+      if (j < p.K && tg.token[j] >= 0) mt = fmaxf(mt, tg.z[j]);
+    }
+    sums.m = fmaxf(sums.mr, warp_max(mt));
+    const float ref = sums.m == -INFINITY ? 0.f : sums.m;
+    float st = 0.f;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = lane + 32 * k;
+      if (j < p.K && tg.token[j] >= 0) st += ex2((tg.z[j] - ref) * p.T.sc);
+    }
+    sums.S = ex2(shift_of(sums.mr, sums.m, p.T.sc)) * sums.Sr + warp_sum(st);
+    if (GRAD) {
+      if (lane == 0) sm.slope = slope_of(sums, mass, p.T, w);
+    }
+  }
+  if (GRAD) __syncthreads();
+  if (rank == 0 && warp == 0) {
+    const Pair lnS = log_sum(sums.S), inv = {p.T.hi, p.T.lo};
+    Pair loss = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = lane + 32 * k;
+      const float pj = j < p.K ? tg.p[j] : 0.f;
       if (pj > 0.f || pj != pj) {
         // ln p - ln q, a small difference of large numbers: rounded once
-        const Pair q = two_sum(tg.z[j], -m_all) * inv + -lnS;
-        const float d = value_of(Pair{tg.t[j], 0.f} + -q);
-        part = part + Pair{pj, 0.f} * Pair{d, 0.f};
+        const Pair q = two_sum(tg.z[j], -sums.m) * inv + -lnS;
+        loss = loss + Pair{pj, 0.f} * Pair{value_of(Pair{tg.t[j], 0.f} + -q), 0.f};
       }
     }
-    if (warp < kLogitsMaxTop / 32) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        part = part + Pair{__shfl_xor_sync(0xffffffffu, part.hi, o), __shfl_xor_sync(0xffffffffu, part.lo, o)};
-      if (lane == 0) sm.redL[warp] = part;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      const float rest = rest_of(tg, sums.none()), P = tg.sum + rest;
-      Pair loss = {0.f, 0.f};
-      for (int i = 0; i < min(nw, kLogitsMaxTop / 32); ++i) loss = loss + sm.redL[i];
+    for (int o = 16; o > 0; o >>= 1)
+      loss = loss + Pair{__shfl_xor_sync(0xffffffffu, loss.hi, o), __shfl_xor_sync(0xffffffffu, loss.lo, o)};
+    if (lane == 0) {
+      const float rest = rest_of(mass, sums.none()), P = mass.sum + rest;
       if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(Pair{logf(rest), 0.f} + -sums.ln_u(p.T)), 0.f};
       float l = w * value_of(loss);
-      if (S_all != S_all) l = S_all;
+      if (sums.S != sums.S) l = sums.S;
       if (sums.empty()) l = P == 0.f ? 0.f : w * INFINITY;  // no token of the target has a chance
       p.loss[entry] = l;
       if (p.stats) {
         float* to = p.stats + 4 * (size_t)entry;
-        to[0] = m_all;
-        to[1] = S_all;
-        to[2] = mr;
-        to[3] = Sr;
+        to[0] = sums.m;
+        to[1] = sums.S;
+        to[2] = sums.mr;
+        to[3] = sums.Sr;
       }
     }
   }
   if (GRAD) {
-    if (sums.empty())
-      write_zeros<T>(p, row, out, g0, g1);
+    if (sm.slope.empty)
+      write_zeros<T>(part, out);
     else
-      write_gradient<T>(p, row, out, g0, g1, slope_of(sums, tg, p.T, w), tg);
+      write_gradient<T>(p, row, part, slots, out, sm.slope, tg);
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kLogitsThreads, 4) distill_backward_kernel(const DistillParams p) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Target tg;
+  __shared__ Slope slope;
   const int tid = threadIdx.x, NT = blockDim.x;
-  const int c = p.ctas;
-  const int rank = (int)blockIdx.x % c, entry = (int)blockIdx.x / c;
+  const int c = 1 << p.log_c;
+  const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
+  uint4* slots = reinterpret_cast<uint4*>(dynamic);
   pdl_wait();
   pdl_trigger();
   const float w = p.weight ? p.weight[entry] : 1.f;
   const RowView<T> row(static_cast<const T*>(p.logits) + (int64_t)entry * p.stride, p.V);
+  const PartView<T> part(row, rank, p.log_c, p.log_nt);
   T* out = static_cast<T*>(p.grad) + (int64_t)entry * p.grad_stride;
-  const int g0 = (int)((long long)row.n * rank / c), g1 = (int)((long long)row.n * (rank + 1) / c);
   if (w == 0.f) {
-    write_zeros<T>(p, row, out, g0, g1);
+    write_zeros<T>(part, out);
     return;
   }
-  load_target(p, entry, rank == 0, tg);
-  __syncthreads();
-  const int v_lo = max(0, row.first(g0)), v_hi = min(row.V, row.first(g1));
-  for (int j = tid; j < p.K; j += NT) {
-    const int v = tg.token[j];
-    tg.z[j] = v >= v_lo && v < v_hi ? load_element(row.row + v) : 0.f;  // others belong to other CTAs
-  }
-  __syncthreads();
+  for (int k = 0; k < part.steps; ++k) part.fetch(row, k, slots + kBatch * k * NT + tid);
+  const Listed mine = load_listed(p, entry, rank == 0, tg);
   const float* from = p.stats_in + 4 * (size_t)entry;
   const Sums sums = {from[0], from[1], from[2], from[3]};
   const float up = p.grad_loss ? p.grad_loss[entry] : 1.f;
-  if (sums.empty())
-    write_zeros<T>(p, row, out, g0, g1);
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const int j = tid + n * NT, v = mine.v[n];
+    if (j < p.K && v >= part.lo && v < part.hi) tg.z[j] = load_element(row.row + v);  // others are other CTAs'
+  }
+  const bool twice = __syncthreads_or(place_listed(p, mine, tg));
+  const Mass mass = weigh_listed(p, twice, tg);
+  if (tid == 0) slope = slope_of(sums, mass, p.T, w * up);
+  __syncthreads();
+  copy_wait<0>();
+  if (slope.empty)
+    write_zeros<T>(part, out);
   else
-    write_gradient<T>(p, row, out, g0, g1, slope_of(sums, tg, p.T, w * up), tg);
+    write_gradient<T>(p, row, part, slots, out, slope, tg);
 }
 
 // The gradient's rows apart from the logits', or on them exactly.
@@ -494,17 +615,43 @@ ssv_status distill_check(const ssv_distill_args* a, DistillParams& p) {
     if (!logits_shape_ok(a->grad, a->grad_stride, a->dtype, a->V, a->n) ||
         !rows_apart(a->logits, a->grad, p.stride, p.grad_stride, a->V, a->n, es))
       return SSV_ERR_INVALID;
-    p.vec = (((uintptr_t)a->logits ^ (uintptr_t)a->grad) & 31u) == 0 &&
-            (a->n == 1 || ((uint64_t)(p.stride - p.grad_stride) * es) % 32 == 0);
+    p.vec = (((uintptr_t)a->logits ^ (uintptr_t)a->grad) & 15u) == 0 &&
+            (a->n == 1 || ((uint64_t)(p.stride - p.grad_stride) * es) % 16 == 0);
   }
   return SSV_OK;
 }
 
+// A row in parts of at most `bytes`, as far as `most` CTAs go; more of them while SMs would have no work and a CTA has
+// more than two batches.
+RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, int threads) {
+  const int vectors = row_vectors(V, element_size);
+  int c = 1;
+  while (c < most && (vectors + c - 1) / c > bytes / 16) c *= 2;
+  while (c < most && (long long)rows * c * 2 <= 608 && vectors > 4 * c * kLogitsThreads) c *= 2;
+  return split_of(vectors, c, threads);
+}
+
+template <typename T, bool GRAD>
+cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
+  static uint64_t done = 0;
+  const RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 48 * 1024 : 1 << 20, kMaxCluster, kLogitsThreads);
+  p.log_c = sp.log_c;
+  p.log_nt = sp.log_nt;
+  p.slot_bytes = 16 * (GRAD ? sp.vectors : kStages * kBatch * sp.threads);
+  const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
+  const cudaError_t e = allow_shared(distill_kernel<T, GRAD>, smem, &done);
+  return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD>, n, sp, smem, st, p);
+}
+
 template <typename T>
-cudaError_t distill_launch(const DistillParams& p, int n, const RowSplit& sp, cudaStream_t st) {
-  const size_t smem = ((size_t)sp.groups * kGroup<T> + 31) / 32 * 4;
-  return p.grad ? launch_rows(distill_kernel<T, true>, n, sp, smem, st, p)
-                : launch_rows(distill_kernel<T, false>, n, sp, smem, st, p);
+cudaError_t backward_launch(DistillParams& p, int n, cudaStream_t st) {
+  static uint64_t done = 0;
+  const RowSplit sp = distill_split(n, p.V, sizeof(T), 48 * 1024, 64, kLogitsThreads);
+  p.log_c = sp.log_c;
+  p.log_nt = sp.log_nt;
+  const size_t smem = 16 * (size_t)sp.vectors;
+  cudaError_t e = allow_shared(distill_backward_kernel<T>, smem, &done);
+  return e != cudaSuccess ? e : launch_rows(distill_backward_kernel<T>, n, sp, smem, st, p);
 }
 
 }  // namespace
@@ -517,11 +664,13 @@ extern "C" ssv_status ssv_distill(const ssv_distill_args* a, void* stream) {
   if (s != SSV_OK) return s;
   if (a->n == 0) return SSV_OK;
   if (!a->loss || a->grad_loss) return SSV_ERR_INVALID;
-  const RowSplit sp = split_rows(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4);
-  p.ctas = sp.ctas;
+  using bf16 = __nv_bfloat16;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->dtype == SSV_BF16 ? distill_launch<__nv_bfloat16>(p, a->n, sp, st)
-                                             : distill_launch<float>(p, a->n, sp, st);
+  cudaError_t e;
+  if (a->grad)
+    e = a->dtype == SSV_BF16 ? distill_launch<bf16, true>(p, a->n, st) : distill_launch<float, true>(p, a->n, st);
+  else
+    e = a->dtype == SSV_BF16 ? distill_launch<bf16, false>(p, a->n, st) : distill_launch<float, false>(p, a->n, st);
   return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;
 }
 
@@ -532,10 +681,8 @@ extern "C" ssv_status ssv_distill_backward(const ssv_distill_args* a, void* stre
   if (s != SSV_OK) return s;
   if (a->n == 0) return SSV_OK;
   if (!a->stats || !a->grad) return SSV_ERR_INVALID;
-  const RowSplit sp = split_rows(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4);
-  p.ctas = sp.ctas;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->dtype == SSV_BF16 ? launch_rows(distill_backward_kernel<__nv_bfloat16>, a->n, sp, 0, st, p)
-                                             : launch_rows(distill_backward_kernel<float>, a->n, sp, 0, st, p);
+  const cudaError_t e =
+      a->dtype == SSV_BF16 ? backward_launch<__nv_bfloat16>(p, a->n, st) : backward_launch<float>(p, a->n, st);
   return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;
 }

@@ -1,15 +1,18 @@
 // Rows of logits, as the kernels on a pass's logits read and write them
 // (ssv_logprobs, ssv_distill, ssv_distill_backward).
 //
-// A row of V elements at any element-aligned address is cut at the 32-byte
-// boundaries of memory into groups: group g holds the elements
-// [g E - lead, (g + 1) E - lead), E = 32 / element size, lead the elements
+// A row of V elements at any element-aligned address is cut at the 16-byte
+// boundaries of memory into vectors: vector i holds the elements
+// [i E - lead, (i + 1) E - lead), E = 16 / element size, lead the elements
 // between the boundary at or below the row's start and that start.  All but the
-// first and the last group lie inside the row and move as one 32-byte access;
-// the edges are read element by element, and what they lack counts as -inf.
+// first and the last lie inside the row and move as one access; the edges are read
+// element by element, and what they lack counts as -inf.
 //
-// A row is shared out over the CTAs of a cluster by contiguous ranges of groups;
-// a CTA's threads take every NT-th group, kBatch of them in flight.
+// A CTA has a range of a row's vectors.  Its threads take every NT-th, kBatch of
+// them at a time, and copy them to shared memory ahead of their use (cp.async,
+// each thread to slots that it reads itself, so that no barrier is needed):
+// either through a ring of kStages batches, for a range of any length, or all at
+// once into a buffer that a second pass reads again.
 #pragma once
 
 #include "ssv_internal.cuh"
@@ -19,32 +22,26 @@
 
 namespace ssv {
 
-constexpr int kLogitsThreads = 256;       // most threads of a CTA
-constexpr int kLogitsMaxVocab = 1 << 19;  // largest V
-constexpr int kLogitsMaxTop = 128;        // most alternatives of a row
-constexpr int kBatch = 4;                 // groups in flight per thread
+constexpr int kLogitsThreads = 256;     // most threads of a CTA
+constexpr int kLogitsMaxVocab = 393216; // largest V: 8 CTAs of a cluster hold it in shared memory, as fp32
+constexpr int kLogitsMaxTop = 128;      // most alternatives of a row
+constexpr int kMaxCluster = 8;
+constexpr int kLogBatch = 2, kBatch = 1 << kLogBatch;  // vectors of a thread in one step
+constexpr int kStages = 2;              // steps in flight (ring)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.693147180559945309f;
 
-struct Raw {  // one group
-  uint32_t w[8];
-};
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 
-template <typename T> constexpr int kGroup = 32 / (int)sizeof(T);
-
-__device__ __forceinline__ Raw load_raw(const void* p) {
-  Raw r;
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
-                 "=r"(r.w[7])
-               : "l"(p));
-  return r;
-}
-
-__device__ __forceinline__ void store_raw(void* p, const Raw& r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]),
-               "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+__device__ __forceinline__ void copy_async(void* shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(shared)), "l"(global)
                : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the last N groups have landed
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -84,98 +81,136 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return y;
 }
 
-// element pair i of a group
+// element pair i of a vector
 template <typename T>
-__device__ __forceinline__ float2 pair_of(const Raw& r, int i) {
-  if (sizeof(T) == 2) return make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
-  return make_float2(__uint_as_float(r.w[(2 * i) & 7]), __uint_as_float(r.w[(2 * i + 1) & 7]));
+__device__ __forceinline__ float2 pair_of(const uint4& r, int i) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if (sizeof(T) == 2) return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return make_float2(__uint_as_float(w[(2 * i) & 3]), __uint_as_float(w[(2 * i + 1) & 3]));
 }
 
 template <typename T>
-__device__ __forceinline__ void put_pair(Raw& r, int i, float2 v) {
-  if (sizeof(T) == 2) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-    r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    r.w[(2 * i) & 7] = __float_as_uint(v.x);
-    r.w[(2 * i + 1) & 7] = __float_as_uint(v.y);
-  }
-}
+__device__ __forceinline__ uint32_t none_bits() { return sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u; }  // -inf
 
+// largest number of kBatch vectors, -inf where there is none (NaN are passed over)
 template <typename T>
-__device__ __forceinline__ void set_none(Raw& r) {
+__device__ __forceinline__ float step_max(const uint4 (&x)[kBatch]) {
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162 h[4 * kBatch];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.w[i] = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
-}
-
-// element e of a group becomes -inf
-template <typename T>
-__device__ __forceinline__ void drop_element(Raw& r, int e) {
+    for (int u = 0; u < kBatch; ++u) {
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (sizeof(T) == 2) {
-      if (e == 2 * i) r.w[i] = (r.w[i] & 0xFFFF0000u) | 0xFF80u;
-      if (e == 2 * i + 1) r.w[i] = (r.w[i] & 0xFFFFu) | 0xFF800000u;
-    } else if (e == i) {
-      r.w[i] = 0xFF800000u;
+      for (int i = 0; i < 4; ++i) h[4 * u + i] = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
     }
-  }
-}
-
-// largest number of a group, -inf where there is none (NaN are passed over)
-template <typename T>
-__device__ __forceinline__ float group_max(const Raw& r) {
-  if (sizeof(T) == 2) {
-    __nv_bfloat162 h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = *reinterpret_cast<const __nv_bfloat162*>(&r.w[i]);
-#pragma unroll
-    for (int s = 4; s > 0; s >>= 1)
+    for (int s = 2 * kBatch; s > 0; s >>= 1)
 #pragma unroll
       for (int i = 0; i < s; ++i) h[i] = __hmax2(h[i], h[i + s]);
     return fmaxf(-INFINITY, fmaxf(__low2float(h[0]), __high2float(h[0])));
-  }
-  float m = -INFINITY;
+  } else {
+    float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, __uint_as_float(r.w[i]));
-  return m;
+    for (int u = 0; u < kBatch; ++u)
+      m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(x[u].x), __uint_as_float(x[u].y))),
+                fmaxf(__uint_as_float(x[u].z), __uint_as_float(x[u].w)));
+    return m;
+  }
 }
 
-// A row, cut into groups.
+// A row, cut into vectors.
 template <typename T>
 struct RowView {
-  const char* base;  // address of group 0 (32-byte boundary at or below the row)
+  const char* base;  // address of vector 0 (16-byte boundary at or below the row)
   const T* row;
-  int lead, V, n;    // n groups, those of [lo, hi) whole
+  int lead, V, n;    // n vectors, those of [lo, hi) whole
   int lo, hi;
 
   __device__ __forceinline__ RowView(const T* p, int V_) : row(p), V(V_) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    base = reinterpret_cast<const char*>(a & ~uintptr_t(31));
-    lead = (int)((a & 31) / sizeof(T));
-    n = (lead + V + kGroup<T> - 1) / kGroup<T>;
+    base = reinterpret_cast<const char*>(a & ~uintptr_t(15));
+    lead = (int)((a & 15) / sizeof(T));
+    n = (lead + V + kVec<T> - 1) / kVec<T>;
     lo = lead ? 1 : 0;
-    hi = (lead + V) / kGroup<T>;
+    hi = (lead + V) / kVec<T>;
   }
-  __device__ __forceinline__ bool whole(int g) const { return g >= lo && g < hi; }
-  __device__ __forceinline__ int first(int g) const { return g * kGroup<T> - lead; }  // element at the group's start
-  __device__ __forceinline__ Raw load(int g) const {
-    if (whole(g)) return load_raw(base + (size_t)g * 32);
-    Raw r;
-    set_none<T>(r);
-    const int v0 = first(g);
+  __device__ __forceinline__ bool whole(int i) const { return i >= lo && i < hi; }
+  __device__ __forceinline__ int first(int i) const { return i * kVec<T> - lead; }  // element at the vector's start
+
+  // an edge, element by element
+  __device__ __noinline__ uint4 edge(int i) const {
+    uint32_t w[4] = {none_bits<T>(), none_bits<T>(), none_bits<T>(), none_bits<T>()};
+    const int v0 = first(i);
 #pragma unroll
-    for (int e = 0; e < kGroup<T>; ++e) {
+    for (int e = 0; e < kVec<T>; ++e) {
       const int v = v0 + e;
       if (v < 0 || v >= V) continue;
       if (sizeof(T) == 2) {
         const uint32_t x = *(reinterpret_cast<const volatile uint16_t*>(row) + v);
-        r.w[(e / 2) & 7] = (e & 1) ? (r.w[(e / 2) & 7] & 0xFFFFu) | (x << 16) : (r.w[(e / 2) & 7] & 0xFFFF0000u) | x;
+        w[(e / 2) & 3] = (e & 1) ? (w[(e / 2) & 3] & 0xFFFFu) | (x << 16) : (w[(e / 2) & 3] & 0xFFFF0000u) | x;
       } else {
-        r.w[e & 7] = *(reinterpret_cast<const volatile uint32_t*>(row) + v);
+        w[e & 3] = *(reinterpret_cast<const volatile uint32_t*>(row) + v);
       }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (!whole(i)) return edge(i);
+    uint4 r;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(base + (size_t)i * 16));
     return r;
+  }
+  // vector i to its slot; read by the thread that asked for it
+  __device__ __forceinline__ void fetch(uint4* slot, int i) const {
+    if (whole(i)) copy_async(slot, base + (size_t)i * 16); else *slot = edge(i);
+  }
+};
+
+// A CTA's part of a row: vectors [i0, i1), elements [lo, hi), the first one's start at element `at`; a step is kBatch
+// vectors of every thread.
+template <typename T>
+struct PartView {
+  int i0, i1, lo, hi, at, steps;
+  int full0, full1;  // steps [full0, full1) are full: every thread has kBatch whole vectors
+
+  // CTA `rank` of 2^log_c, of 2^log_nt threads (no division: eight warps of every CTA would spend more on it than on
+  // some rows)
+  __device__ __forceinline__ PartView(const RowView<T>& row, int rank, int log_c, int log_nt) {
+    i0 = (int)(((long long)row.n * rank) >> log_c);
+    i1 = (int)(((long long)row.n * (rank + 1)) >> log_c);
+    at = row.first(i0);
+    lo = max(0, at);
+    hi = min(row.V, row.first(i1));
+    const int log_per = log_nt + kLogBatch;
+    steps = (i1 - i0 + (1 << log_per) - 1) >> log_per;
+    full0 = i0 < row.lo ? 1 : 0;
+    full1 = max(0, min(i1, row.hi) - i0) >> log_per;
+  }
+  __device__ __forceinline__ bool full(int k) const { return k >= full0 && k < full1; }
+  // the thread's vectors of step k, from `slots` on, NT apart
+  __device__ __forceinline__ void fetch(const RowView<T>& row, int k, uint4* slots) const {
+    const int NT = blockDim.x, i = i0 + (int)threadIdx.x + NT * kBatch * k;
+    if (full(k)) {
+      const char* from = row.base + (size_t)i * 16;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) copy_async(slots + NT * u, from + (size_t)(NT * 16) * u);
+    } else {
+      for (int u = 0; u < kBatch; ++u)
+        if (i + NT * u < i1) row.fetch(slots + NT * u, i + NT * u);
+    }
+    copy_commit();
+  }
+  // the same from the slots, -inf where there is none
+  template <bool FULL>
+  __device__ __forceinline__ void take(int k, const uint4* slots, uint4 (&x)[kBatch]) const {
+    const int NT = blockDim.x, i = i0 + (int)threadIdx.x + NT * kBatch * k;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (FULL || i + NT * u < i1)
+        x[u] = slots[NT * u];
+      else
+        x[u].x = x[u].y = x[u].z = x[u].w = none_bits<T>();
   }
 };
 
@@ -215,7 +250,7 @@ __device__ __forceinline__ int cluster_add(uint32_t addr, int v) {
 }
 
 // ---------------------------------------------------------------------------
-// sums over a CTA, in a fixed order
+// sums over a warp, in a fixed order
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -227,16 +262,6 @@ __device__ __forceinline__ N warp_sum(N x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
-}
-
-// largest of every thread's x; `red` holds a value per warp.  Ends with a barrier before `red` is read alone.
-__device__ __forceinline__ float cta_max(float x, float* red) {
-  x = warp_max(x);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  float m = red[0];
-  for (int w = 1; w < (int)blockDim.x / 32; ++w) m = fmaxf(m, red[w]);
-  return m;
 }
 
 // A value hi + lo of about 48 bits: the logarithms and products that results are differences of.  (The fp64 pipe
@@ -279,11 +304,26 @@ __device__ __forceinline__ float shift_of(float from, float to, float sc) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// CTAs per row and threads per CTA.
+// CTAs per row and threads per CTA, powers of two; most vectors of a CTA.
 struct RowSplit {
-  int ctas, threads, groups;  // groups: most groups of one CTA
+  int ctas, threads, vectors, log_c, log_nt;
+  int batches() const { return (vectors + threads * kBatch - 1) / (threads * kBatch); }
 };
 
+// Dynamic shared memory above the default needs the kernel's leave, once per device.
+template <typename K>
+inline cudaError_t allow_shared(K kernel, size_t bytes, uint64_t* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || bytes <= 40 * 1024) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (__atomic_load_n(done, __ATOMIC_ACQUIRE) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
+  if (e == cudaSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELEASE);
+  return e;
+}
+
+// CTAs of a row are a cluster, up to kMaxCluster of them; more are independent.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_rows(void (*kernel)(KArgs...), int rows, const RowSplit& sp, size_t smem, cudaStream_t st,
                                Args&&... args) {
@@ -296,7 +336,7 @@ inline cudaError_t launch_rows(void (*kernel)(KArgs...), int rows, const RowSpli
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = sp.ctas;
+  attr[1].val.clusterDim.x = sp.ctas <= kMaxCluster ? sp.ctas : 1;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -304,9 +344,19 @@ inline cudaError_t launch_rows(void (*kernel)(KArgs...), int rows, const RowSpli
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-inline int most_groups(int V, int element_size) { return (V * element_size + 31) / 32 + 1; }
+// vectors of a row at most
+inline int row_vectors(int V, int element_size) { return (V * element_size + 15) / 16 + 1; }
 
-RowSplit split_rows(int rows, int V, int element_size);
+// `vectors` of a row over c CTAs
+inline RowSplit split_of(int vectors, int c, int most_threads) {
+  RowSplit sp;
+  sp.ctas = c;
+  sp.vectors = (vectors + c - 1) / c;
+  for (sp.log_c = 0; 1 << sp.log_c < c;) ++sp.log_c;
+  for (sp.log_nt = 5; 1 << sp.log_nt < most_threads && 1 << sp.log_nt < sp.vectors;) ++sp.log_nt;
+  sp.threads = 1 << sp.log_nt;
+  return sp;
+}
 
 // T as the kernels take it
 struct Scale {

@@ -9,27 +9,30 @@
 // One pass over a row.  Every thread keeps the running maximum of its elements
 // and, relative to it, S and W = sum e (l - m) sc in fp32 (sc = log2(e) / T; both
 // rescaled when the maximum grows), and counts the elements before the given
-// token, which its group's maximum lets it skip mostly.
+// token, two at a time where their batch's maximum does not rule them out.  The
+// warps of a cluster send their sums to each other, and every warp that needs them
+// joins them in the same order.
 //
 // Top alternatives.  The K-th largest of any K or more elements bounds the row's
 // K-th from below.  Each warp gives the j largest of its lanes' maxima, j so that
-// the cluster's warps give about 2 K; with the K-th of these as threshold, groups
-// whose maximum (kept in shared memory, one word per 32 bytes of the row) passes
-// it are listed, read again from L2, one per thread, and their elements that pass
-// it, hardly more than K, go to the cluster's first CTA as keys (order of the value above the complemented
-// index: equal values in the order of their indices).  It ranks them by counting.
-// Where more pass than its list holds (long runs of equal values), it finds the
-// K-th key by bisection over the row.
+// the cluster's warps give about 2 K; with the K-th of these as threshold, batches
+// whose maximum (kept in shared memory, rounded up to bf16) passes it are listed,
+// read again from L2, one per thread, and their elements that pass it, hardly
+// more than K, go to the cluster's first CTA as keys (order of the value above
+// the complemented index: equal values in the order of their indices).  It ranks
+// them by counting.  Where more pass than its list holds (long runs of equal
+// values), it finds the K-th key by bisection over the row.
 #include "logits.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace ssv {
 namespace {
 
-constexpr int kList = 512;        // keys that a list holds
-constexpr int kMaxCluster = 8;
+constexpr int kList = 512;                                  // keys that a list holds
 constexpr int kPool = 2 * kLogitsMaxTop + 8 * kMaxCluster;  // values of the pool at most: 2 K, and one of each warp
+constexpr int kParts = 8 * kMaxCluster;                     // warps of a cluster
 
 struct LogprobsParams {
   const void* logits;
@@ -45,27 +48,29 @@ struct LogprobsParams {
   float* top_logprob;
   int32_t* top_token;
   int32_t* dev_status;
-  int ctas;
+  int log_c, log_nt;
   int give;  // lane maxima that a warp gives to the pool
 };
 
-struct Part {  // what a CTA knows of its part of the row
-  float m, S, W;
-  int before;
-};
-constexpr int kPartWords = sizeof(Part) / 4;
+// bytes of the ring, in which the lists have room
+__host__ __device__ constexpr size_t ring_bytes(int threads) {
+  const size_t ring = (size_t)kStages * kBatch * 16 * threads, lists = (2 * 8 + 4) * kList;
+  return ring > lists ? ring : lists;
+}
 
 struct Shared {
-  Part part[kMaxCluster];
-  float red[kLogitsThreads / 32];
-  float redS[kLogitsThreads / 32], redW[kLogitsThreads / 32];
-  int redN[kLogitsThreads / 32];
-  int groups, count, total;  // groups and keys listed here, keys sent to the cluster's first CTA
+  uint32_t part[kParts][4];   // of every warp: maximum, S, W, elements before the token
+  int groups, count, total;   // batches and keys listed here, keys sent to the cluster's first CTA
   int at;
   float least;
-  alignas(16) uint32_t pool[kPool];  // order of the largest lane maxima of every warp of the cluster, 0: none
+  int sum[kLogitsThreads / 32];
+  uint32_t pool[kPool];       // order of the largest lane maxima of every warp of the cluster, 0: none
+};
+
+// What the ring's memory holds after the pass.
+struct Lists {
+  unsigned long long merged[kList], list[kList];
   int group[kList];
-  unsigned long long merged[kList];
 };
 
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -83,42 +88,43 @@ __device__ __forceinline__ unsigned long long element_key(float x, int v) {
 // smaller, that is, greater than the next number below; of those behind when greater.
 template <typename T>
 struct Given {
-  int t, group, below;  // below: lt's next lower number as bits of T
+  int t, own, below;  // own: the token's vector; below: lt's next lower number as bits of T
   float lt;
 
   __device__ __forceinline__ void set(const RowView<T>& row, int token, bool there) {
     t = token;
-    group = (row.lead + token) / kGroup<T>;
+    own = (row.lead + token) / kVec<T>;
     lt = there ? load_element(row.row + token) : NAN;  // without a token nothing compares
     uint32_t b = __float_as_uint(lt) >> (sizeof(T) == 2 ? 16 : 0);
     const uint32_t sign = sizeof(T) == 2 ? 0x8000u : 0x80000000u;
     below = (int)((b & ~sign) == 0 ? sign | 1u : (b & sign) ? b + 1 : b - 1);
   }
 
-  // Elements of group g that are before the token.  lt is above -inf.
-  __device__ __forceinline__ int before(const Raw& r, int g, const RowView<T>& row) const {
-    if (g == group) return among(r, row.first(g));
+  // Elements of vector i that are before the token.  lt is above -inf.
+  __device__ __forceinline__ int before(const uint4& r, int i, const RowView<T>& row) const {
+    if (i == own) return among(r, row.first(i));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     int n = 0;
     if (sizeof(T) == 2) {
-      const uint32_t b = g < group ? (uint32_t)below : __float_as_uint(lt) >> 16, both = b << 16 | b;
+      const uint32_t b = i < own ? (uint32_t)below : __float_as_uint(lt) >> 16, both = b << 16 | b;
       const __nv_bfloat162 than = *reinterpret_cast<const __nv_bfloat162*>(&both);
       __nv_bfloat162 c = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c = __hadd2(c, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&r.w[i]), than));
+      for (int k = 0; k < 4; ++k) c = __hadd2(c, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), than));
       n = (int)(__low2float(c) + __high2float(c));
     } else {
-      const float than = g < group ? __uint_as_float((uint32_t)below) : lt;
+      const float than = i < own ? __uint_as_float((uint32_t)below) : lt;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n += __uint_as_float(r.w[i]) > than ? 1 : 0;
+      for (int k = 0; k < 4; ++k) n += __uint_as_float(w[k]) > than ? 1 : 0;
     }
     return n;
   }
 
-  // The same, element by element, for the token's own group and for tokens at -inf.
-  __device__ __noinline__ int among(const Raw r, int v0) const {
+  // The same, element by element, for the token's own vector and for tokens at -inf.
+  __device__ __noinline__ int among(const uint4 r, int v0) const {
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < kGroup<T> / 2; ++i) {
+    for (int i = 0; i < kVec<T> / 2; ++i) {
       const float2 x = pair_of<T>(r, i);
       const int v = v0 + 2 * i;  // below 0: in front of the row
       n += (x.x > lt || (x.x == lt && v >= 0 && v < t)) ? 1 : 0;
@@ -132,28 +138,44 @@ struct Given {
 template <typename T>
 __device__ int count_keys(const RowView<T>& row, unsigned long long key, Shared& sm) {
   int n = 0;
-  for (int g = threadIdx.x; g < row.n; g += blockDim.x) {
-    const Raw r = row.load(g);
-    const int v0 = row.first(g);
+  for (int i = threadIdx.x; i < row.n; i += blockDim.x) {
+    const uint4 r = row.load(i);
+    const int v0 = row.first(i);
 #pragma unroll
-    for (int i = 0; i < kGroup<T> / 2; ++i) {
-      const float2 x = pair_of<T>(r, i);
-      n += (x.x > -INFINITY && element_key(x.x, v0 + 2 * i) >= key) ? 1 : 0;
-      n += (x.y > -INFINITY && element_key(x.y, v0 + 2 * i + 1) >= key) ? 1 : 0;
+    for (int k = 0; k < kVec<T> / 2; ++k) {
+      const float2 x = pair_of<T>(r, k);
+      n += (x.x > -INFINITY && element_key(x.x, v0 + 2 * k) >= key) ? 1 : 0;
+      n += (x.y > -INFINITY && element_key(x.y, v0 + 2 * k + 1) >= key) ? 1 : 0;
     }
   }
   n = warp_sum(n);
-  if ((threadIdx.x & 31) == 0) sm.redN[threadIdx.x >> 5] = n;
+  if ((threadIdx.x & 31) == 0) sm.sum[threadIdx.x >> 5] = n;
   __syncthreads();
   int sum = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += sm.redN[w];
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += sm.sum[w];
   __syncthreads();
   return sum;
 }
 
-// Whole CTA: the row's K greatest keys into sm.merged (more than K elements are above -inf).
+// Keys of a vector's elements that are >= `key` and not -inf: to keys[0, kList), counted in `count`.
 template <typename T>
-__device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float least, float most, Shared& sm) {
+__device__ __forceinline__ void list_keys(const uint4& r, int v0, unsigned long long key, unsigned long long* keys,
+                                          int* count) {
+#pragma unroll
+  for (int e = 0; e < kVec<T>; ++e) {
+    const float2 y = pair_of<T>(r, e / 2);
+    const float z = (e & 1) ? y.y : y.x;
+    if (z > -INFINITY && element_key(z, v0 + e) >= key) {
+      const int at = atomicAdd(count, 1);
+      if (at < kList) keys[at] = element_key(z, v0 + e);
+    }
+  }
+}
+
+// Whole CTA: the row's K greatest keys into `merged` (more than K elements are above -inf).
+template <typename T>
+__device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float least, float most, Shared& sm,
+                                        unsigned long long* merged) {
   // the largest key that at least K keys reach: first the value, then the index
   uint32_t lo = order_bits(least), hi = order_bits(most);
   while (lo < hi) {  // count(lo) >= K throughout
@@ -168,34 +190,20 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
   const unsigned long long key = ((unsigned long long)lo << 32) | ilo;
   if (threadIdx.x == 0) sm.count = 0;
   __syncthreads();
-  for (int g = threadIdx.x; g < row.n; g += blockDim.x) {
-    const Raw r = row.load(g);
-    const int v0 = row.first(g);
-    for (int e = 0; e < kGroup<T>; ++e) {
-      float2 x = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kGroup<T> / 2; ++i)
-        if (i == e / 2) x = pair_of<T>(r, i);
-      const float y = (e & 1) ? x.y : x.x;
-      if (y > -INFINITY && element_key(y, v0 + e) >= key) {
-        const int at = atomicAdd(&sm.count, 1);
-        if (at < kList) sm.merged[at] = element_key(y, v0 + e);
-      }
-    }
-  }
+  for (int i = threadIdx.x; i < row.n; i += blockDim.x) list_keys<T>(row.load(i), row.first(i), key, merged, &sm.count);
   __syncthreads();
 }
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const LogprobsParams p) {
-  // TOP: largest number of every group of this CTA; then the keys listed here
-  extern __shared__ __align__(16) unsigned char dynamic[];
-  float* group_top = reinterpret_cast<float*>(dynamic);
-  unsigned long long* list = reinterpret_cast<unsigned long long*>(dynamic);
+  extern __shared__ __align__(16) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
-  const int c = p.ctas;
-  const int rank = (int)blockIdx.x % c, entry = (int)blockIdx.x / c;
+  const int c = 1 << p.log_c;
+  const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
+  uint4* ring = reinterpret_cast<uint4*>(dynamic);
+  Lists& lists = *reinterpret_cast<Lists*>(dynamic);
+  __nv_bfloat16* tops = reinterpret_cast<__nv_bfloat16*>(dynamic + ring_bytes(NT));
   if (tid == 0) {
     sm.groups = 0;
     sm.count = 0;
@@ -230,7 +238,10 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
     return;
   }
   const RowView<T> row(static_cast<const T*>(p.logits) + (int64_t)r * p.stride, p.V);
-  const int g0 = (int)((long long)row.n * rank / c), g1 = (int)((long long)row.n * (rank + 1) / c);
+  const PartView<T> part(row, rank, p.log_c, p.log_nt);
+  const int i0 = part.i0, i1 = part.i1, steps = part.steps;
+  auto slots = [&](int k) { return ring + kBatch * (k % kStages) * NT + tid; };
+  for (int k = 0; k < kStages; ++k) part.fetch(row, k, slots(k));
   Given<T> given;
   given.set(row, t, p.tokens != nullptr);
   const float lt = given.lt;
@@ -239,40 +250,35 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
   float m = -INFINITY, S = 0.f, W = 0.f;
   int before = 0;
   const float2 sc2 = make_float2(p.T.sc, p.T.sc);
-  for (int gb = g0 + tid; gb < g1; gb += NT * kBatch) {
-    Raw x[kBatch];
+  auto step = [&](auto is_full, int k) {
+    constexpr bool FULL = decltype(is_full)::value;
+    uint4 x[kBatch];
+    part.template take<FULL>(k, slots(k), x);
+    const float mx = step_max<T>(x);
+    part.fetch(row, k + kStages, slots(k));  // into the slots that have just been read
+    if (TOP) tops[k * NT + tid] = __float2bfloat16_ru(mx);
+    const int ib = i0 + tid + NT * kBatch * k;
+    if (mx >= lt) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int g = gb + u * NT;
-      if (g < g1) x[u] = row.load(g); else set_none<T>(x[u]);
+      for (int u = 0; u < kBatch; ++u)
+        if (FULL || ib + NT * u < i1)
+          before += lt == -INFINITY ? given.among(x[u], row.first(ib + NT * u)) : given.before(x[u], ib + NT * u, row);
     }
-    float top[kBatch], mx = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      top[u] = group_max<T>(x[u]);
-      mx = fmaxf(mx, top[u]);
-      const int g = gb + u * NT;
-      if (TOP && g < g1) group_top[g - g0] = top[u];
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (top[u] >= lt && gb + u * NT < g1)
-        before += lt == -INFINITY ? given.among(x[u], row.first(gb + u * NT)) : given.before(x[u], gb + u * NT, row);
     if (mx > m) {  // sums so far on the new scale
       const float d = shift_of(m, mx, p.T.sc), f = ex2(d);
       W = f * (W + d * S);
       S = f * S;
       m = mx;
     }
-    // A group of nothing but -inf and NaN: relative to 0, so that -inf counts nothing and NaN stays.
+    // Nothing but -inf and NaN so far: relative to 0, so that -inf counts nothing and NaN stays.
     const float mm = m == -INFINITY ? 0.f : m;
     const float2 nm = make_float2(-mm, -mm);
     float2 S2 = make_float2(0.f, 0.f), W2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (u && gb + u * NT >= g1) break;
+      if (!FULL && ib + NT * u >= i1) break;
 #pragma unroll
-      for (int i = 0; i < kGroup<T> / 2; ++i) {
+      for (int i = 0; i < kVec<T> / 2; ++i) {
         float2 y = mul2(add2(pair_of<T>(x[u], i), nm), sc2);
         y.x = max_nan(y.x, -200.f);  // 2^-200 is 0 and 0 * -200 too; -inf would make it NaN
         y.y = max_nan(y.y, -200.f);
@@ -283,114 +289,134 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
     }
     S += S2.x + S2.y;
     W += W2.x + W2.y;
+  };
+  for (int k = 0; k < steps; ++k) {
+    copy_wait<kStages - 1>();
+    if (part.full(k)) step(std::true_type{}, k); else step(std::false_type{}, k);
   }
+  copy_wait<0>();
 
-  // ------------------------------------------------------------ this CTA's part
-  const int given_n = nw * p.give;  // values that a CTA gives to the pool
-  if (TOP) {
-    uint32_t* mine = sm.pool + rank * given_n + warp * p.give;
-    uint32_t b = order_bits(m);
-    if (p.give == 32) {
-      mine[lane] = b;
-    } else {
+  // ------------------------------------------------------------ every warp's part, to every CTA that joins them
+  const int give_all = nw * p.give;  // values that a CTA gives to the pool
+  {
+    const float M = warp_max(m);
+    const float d = shift_of(m, M, p.T.sc), f = ex2(d);
+    const float Sw = warp_sum(f * S), Ww = warp_sum(f * (W + d * S));
+    const int nb = warp_sum(before);
+    const int me = rank * nw + warp;
+    if (c > 1) cluster_wait();
+    const uint32_t word = (lane & 3) == 0   ? __float_as_uint(M)
+                          : (lane & 3) == 1 ? __float_as_uint(Sw)
+                          : (lane & 3) == 2 ? __float_as_uint(Ww)
+                                            : (uint32_t)nb;
+    if (c == 1) {
+      if (lane < 4) sm.part[me][lane] = word;
+    } else if (lane < 4 * (TOP ? c : 1)) {  // without alternatives the first CTA joins them alone
+      cluster_store(cluster_addr(&sm.part[me][lane & 3], lane >> 2), word);
+    }
+    if (TOP) {
+      // this warp's largest lane maxima
+      uint32_t b = order_bits(m);
       for (int i = 0; i < p.give; ++i) {
-        const uint32_t most = __reduce_max_sync(0xffffffffu, b);
-        const int who = __ffs(__ballot_sync(0xffffffffu, b == most)) - 1;
-        if (lane == who) {
-          mine[i] = b;
-          b = 0u;
+        uint32_t most = b;
+        int who = i;
+        if (p.give < 32) {
+          most = __reduce_max_sync(0xffffffffu, b);
+          who = __ffs(__ballot_sync(0xffffffffu, b == most)) - 1;
+        } else {
+          most = __shfl_sync(0xffffffffu, b, i);
+        }
+        if (lane == who) b = 0u;
+        uint32_t* to = &sm.pool[me * p.give + i];
+        if (c == 1) {
+          if (lane == 0) *to = most;
+        } else if (lane < c) {
+          cluster_store(cluster_addr(to, lane), most);
         }
       }
     }
   }
-  const float M = cta_max(m, sm.red);
-  {
-    const float d = shift_of(m, M, p.T.sc), f = ex2(d);
-    const float Sw = warp_sum(f * S), Ww = warp_sum(f * (W + d * S));
-    const int nb = warp_sum(before);
-    if (lane == 0) {
-      sm.redS[warp] = Sw;
-      sm.redW[warp] = Ww;
-      sm.redN[warp] = nb;
-    }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    Part& me = sm.part[rank];
-    me.m = M;
-    me.S = me.W = 0.f;
-    me.before = 0;
-    for (int w = 0; w < nw; ++w) {
-      me.S += sm.redS[w];
-      me.W += sm.redW[w];
-      me.before += sm.redN[w];
-    }
-  }
-  __syncthreads();
   if (c > 1) {
-    // every CTA of the cluster (the first alone, without alternatives) gets every part
-    cluster_wait();
-    const uint32_t* mine = reinterpret_cast<const uint32_t*>(&sm.part[rank]);
-    const int to = TOP ? c : 1;
-    for (int i = tid; i < to * kPartWords; i += NT) {
-      const int dst = i / kPartWords, w = i % kPartWords;
-      if (dst != rank) cluster_store(cluster_addr(&sm.part[rank], dst) + 4 * w, mine[w]);
-    }
-    if (TOP)
-      for (int i = tid; i < c * given_n; i += NT) {
-        const int dst = i / given_n, w = rank * given_n + i % given_n;
-        if (dst != rank) cluster_store(cluster_addr(&sm.pool[w], dst), sm.pool[w]);
-      }
     cluster_arrive();
     if (!TOP && rank != 0) return;
     cluster_wait();
+  } else {
+    __syncthreads();
   }
-  float Mr = -INFINITY;
-  for (int i = 0; i < c; ++i) Mr = fmaxf(Mr, sm.part[i].m);
+  float Mr, St, Wt;
+  int nb;
+  {
+    const int q0 = lane, q1 = lane + 32, n = c * nw;
+    const float m0 = q0 < n ? __uint_as_float(sm.part[q0][0]) : -INFINITY;
+    const float m1 = q1 < n ? __uint_as_float(sm.part[q1][0]) : -INFINITY;
+    Mr = warp_max(fmaxf(m0, m1));
+    float s = 0.f, w = 0.f;
+    nb = 0;
+    if (q0 < n) {
+      const float d = shift_of(m0, Mr, p.T.sc), f = ex2(d), S0 = __uint_as_float(sm.part[q0][1]);
+      s = f * S0;
+      w = f * (__uint_as_float(sm.part[q0][2]) + d * S0);
+      nb = (int)sm.part[q0][3];
+    }
+    if (q1 < n) {
+      const float d = shift_of(m1, Mr, p.T.sc), f = ex2(d), S1 = __uint_as_float(sm.part[q1][1]);
+      s += f * S1;
+      w += f * (__uint_as_float(sm.part[q1][2]) + d * S1);
+      nb += (int)sm.part[q1][3];
+    }
+    St = warp_sum(s);
+    Wt = warp_sum(w);
+    nb = warp_sum(nb);
+  }
+
+  // ------------------------------------------------------------ results (the cluster's first CTA)
+  const bool empty = Mr == -INFINITY && St == 0.f;  // nothing above -inf
+  const Pair lnS = log_sum(St);
+  if (rank == 0 && tid == NT - 1) {
+    const Pair inv = {p.T.hi, p.T.lo};
+    if (p.lse) p.lse[entry] = empty ? -INFINITY : value_of(Pair{Mr, 0.f} * inv + lnS);
+    if (p.entropy) p.entropy[entry] = empty ? 0.f : value_of(lnS + Pair{-(Wt / St) * kLn2, 0.f});
+    if (p.logprob) p.logprob[entry] = empty ? -INFINITY : value_of(two_sum(lt, -Mr) * inv + -lnS);
+    if (p.rank) p.rank[entry] = lt == lt ? nb + 1 : 0;
+  }
 
   // ------------------------------------------------------------ alternatives
-  float least = -INFINITY;
   if (TOP) {
     // the K-th of the pool: every value's place in it
-    const int n = c * given_n;
-    for (int i = tid; i < n; i += NT) {
+    const int pooled = c * give_all;
+    for (int i = tid; i < pooled; i += NT) {
       const uint32_t v = sm.pool[i];
       int place = 0;
 #pragma unroll 4
-      for (int j = 0; j < n; ++j) {
+      for (int j = 0; j < pooled; ++j) {
         const uint32_t o = sm.pool[j];
         place += (o > v || (o == v && j < i)) ? 1 : 0;
       }
       if (place == p.K - 1 && v) sm.least = from_order(v);
     }
     __syncthreads();
-    least = sm.least;
-    // groups that reach it
+    const float least = sm.least;
+    // batches that reach it
     if (m >= least && m > -INFINITY)
-      for (int g = g0 + tid; g < g1; g += NT) {
-        const float gt = group_top[g - g0];
-        if (gt >= least && gt > -INFINITY) {
+      for (int k = 0; k < steps; ++k) {
+        const float top = __bfloat162float(tops[k * NT + tid]);
+        if (top >= least && top > -INFINITY) {
           const int at = atomicAdd(&sm.groups, 1);
-          if (at < kList) sm.group[at] = g;
+          if (at < kList) lists.group[at] = k * NT + tid;
         }
       }
     __syncthreads();
-    // their elements that do; more groups than the list holds are more elements, too
+    // their elements that do
     const int ng = sm.groups;
-    if (ng > kList && tid == 0) sm.count = ng;
-    for (int i = tid; i < ng && ng <= kList; i += NT) {
-      const int g = sm.group[i];
-      const Raw x = row.load(g);
-      const int v0 = row.first(g);
-#pragma unroll
-      for (int e = 0; e < kGroup<T>; ++e) {
-        const float2 y = pair_of<T>(x, e / 2);
-        const float z = (e & 1) ? y.y : y.x;
-        if (z >= least && z > -INFINITY) {
-          const int at = atomicAdd(&sm.count, 1);
-          if (at < kList) list[at] = element_key(z, v0 + e);
-        }
+    const unsigned long long key = (unsigned long long)order_bits(least) << 32;
+    if (ng <= kList) {
+      for (int q = tid; q < ng * kBatch; q += NT) {
+        const int b = lists.group[q / kBatch];
+        const int i = i0 + (b & (NT - 1)) + NT * (kBatch * (b >> p.log_nt) + q % kBatch);
+        if (i < i1) list_keys<T>(row.load(i), row.first(i), key, lists.list, &sm.count);
       }
+    } else if (tid == 0) {
+      sm.count = kList + 1;  // hardly fewer: every batch has one but for the rounding of its maximum
     }
     __syncthreads();
     const int mine = sm.count;
@@ -399,55 +425,32 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
       __syncthreads();
       const int at = sm.at;
       if (at + mine <= kList)
-        for (int i = tid; i < mine; i += NT) cluster_store64(cluster_addr(&sm.merged[at + i], 0), list[i]);
+        for (int i = tid; i < mine; i += NT) cluster_store64(cluster_addr(&lists.merged[at + i], 0), lists.list[i]);
       cluster_arrive();
       if (rank != 0) return;
       cluster_wait();
     } else {
-      for (int i = tid; i < min(mine, kList); i += NT) sm.merged[i] = list[i];
+      for (int i = tid; i < min(mine, kList); i += NT) lists.merged[i] = lists.list[i];
       if (tid == 0) sm.total = mine;
       __syncthreads();
     }
-  }
-
-  // ------------------------------------------------------------ results (the cluster's first CTA)
-  float St = 0.f, Wt = 0.f;
-  int nb = 0;
-  for (int i = 0; i < c; ++i) {
-    const Part& q = sm.part[i];
-    const float d = shift_of(q.m, Mr, p.T.sc), f = ex2(d);
-    St += f * q.S;
-    Wt += f * (q.W + d * q.S);
-    nb += q.before;
-  }
-  const bool empty = Mr == -INFINITY && St == 0.f;  // nothing above -inf
-  const Pair lnS = log_sum(St);
-  if (tid == NT - 1) {
-    const Pair inv = {p.T.hi, p.T.lo};
-    if (p.lse) p.lse[entry] = empty ? -INFINITY : value_of(Pair{Mr, 0.f} * inv + lnS);
-    if (p.entropy) p.entropy[entry] = empty ? 0.f : value_of(lnS + Pair{-(Wt / St) * kLn2, 0.f});
-    if (p.logprob) p.logprob[entry] = empty ? -INFINITY : value_of(two_sum(lt, -Mr) * inv + -lnS);
-    if (p.rank) p.rank[entry] = lt == lt ? nb + 1 : 0;
-  }
-  if (TOP) {
-    const int total = sm.total;
-    int n = total;
-    if (total > kList) {
-      bisect_top<T>(row, p.K, least, Mr, sm);
-      n = p.K;
+    int n = sm.total;
+    if (n > kList) {
+      bisect_top<T>(row, p.K, least, Mr, sm, lists.merged);
+      n = sm.count;
     }
+    const float ln = value_of(lnS);
     float* lp = p.top_logprob + (size_t)entry * p.K;
     int32_t* tk = p.top_token + (size_t)entry * p.K;
-    const float ln = value_of(lnS);
     for (int i = tid; i < n; i += NT) {
-      const unsigned long long key = sm.merged[i];
+      const unsigned long long mine_key = lists.merged[i];
       int place = 0;
 #pragma unroll 4
-      for (int j = 0; j < n; ++j) place += sm.merged[j] > key ? 1 : 0;
+      for (int j = 0; j < n; ++j) place += lists.merged[j] > mine_key ? 1 : 0;
       if (place < p.K) {
-        const float x = from_order((uint32_t)(key >> 32));
+        const float x = from_order((uint32_t)(mine_key >> 32));
         lp[place] = (x - Mr) * p.T.hi - ln;
-        tk[place] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
+        tk[place] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine_key);
       }
     }
     for (int i = n + tid; i < p.K; i += NT) {
@@ -457,28 +460,23 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const Logpr
   }
 }
 
-template <typename T>
+template <typename T, bool TOP>
 cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, cudaStream_t st) {
-  if (p.K == 0) return launch_rows(logprobs_kernel<T, false>, n, sp, 0, st, p);
-  return launch_rows(logprobs_kernel<T, true>, n, sp, std::max(sizeof(float) * sp.groups, sizeof(unsigned long long) * kList), st, p);
+  static uint64_t done = 0;
+  const size_t smem = ring_bytes(sp.threads) + (TOP ? (size_t)sp.batches() * sp.threads * sizeof(__nv_bfloat16) : 0);
+  const cudaError_t e = allow_shared(logprobs_kernel<T, TOP>, smem, &done);
+  return e != cudaSuccess ? e : launch_rows(logprobs_kernel<T, TOP>, n, sp, smem, st, p);
+}
+
+// CTAs per row: as many as SMs have room for at once (four each), while a CTA has more than two batches.
+RowSplit logprobs_split(int rows, int V, int element_size) {
+  const int vectors = row_vectors(V, element_size);
+  int c = 1;
+  while (c < kMaxCluster && (long long)rows * c * 2 <= 608 && vectors > 4 * c * kLogitsThreads) c *= 2;
+  return split_of(vectors, c, kLogitsThreads);
 }
 
 }  // namespace
-
-// CTAs per row: while that leaves SMs without work and a CTA more groups than one
-// batch of its threads.
-RowSplit split_rows(int rows, int V, int element_size) {
-  const int groups = most_groups(V, element_size);
-  int c = 1;
-  while (c < 8 && (long long)rows * c * 2 <= 608 && groups > 2 * c * kLogitsThreads) c *= 2;
-  while (c < 8 && groups > c * 9600) c *= 2;  // shared memory: a word per group
-  RowSplit sp;
-  sp.ctas = c;
-  sp.groups = (groups + c - 1) / c;
-  sp.threads = sp.groups >= kLogitsThreads ? kLogitsThreads : (sp.groups + 31) / 32 * 32;
-  return sp;
-}
-
 }  // namespace ssv
 
 extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
@@ -509,12 +507,17 @@ extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
   p.top_logprob = a->top_logprob;
   p.top_token = a->top_token;
   p.dev_status = a->dev_status;
-  const RowSplit sp = split_rows(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4);
-  p.ctas = sp.ctas;
+  const RowSplit sp = logprobs_split(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4);
+  p.log_c = sp.log_c;
+  p.log_nt = sp.log_nt;
   const int warps = sp.ctas * (sp.threads / 32);
   p.give = std::min(32, (2 * a->top_k + warps - 1) / warps);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->dtype == SSV_BF16 ? logprobs_launch<__nv_bfloat16>(p, a->n, sp, st)
-                                             : logprobs_launch<float>(p, a->n, sp, st);
+  using bf16 = __nv_bfloat16;
+  cudaError_t e;
+  if (a->top_k > 0)
+    e = a->dtype == SSV_BF16 ? logprobs_launch<bf16, true>(p, a->n, sp, st) : logprobs_launch<float, true>(p, a->n, sp, st);
+  else
+    e = a->dtype == SSV_BF16 ? logprobs_launch<bf16, false>(p, a->n, sp, st) : logprobs_launch<float, false>(p, a->n, sp, st);
   return e == cudaSuccess ? SSV_OK : SSV_ERR_CUDA;
 }

@@ -872,7 +872,7 @@ SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
  * exp(-(k - 1) / gamma), section 3.1; neither page gives an interface).
  * Rows: logits [rows, V] device, SSV_F32 or SSV_BF16, rows logits_stride
  * elements apart (0: V; at least V), at any element-aligned address; rows that
- * start on 32-byte boundaries are fastest.  1 <= V <= 524288.  T: positive
+ * start on 16-byte boundaries are fastest.  1 <= V <= 393216.  T: positive
  * and finite.  No workspace; sums and results are the same from call to call.
  * -inf marks a token that cannot be: it has probability 0.  A result beyond
  * fp32's range (the lse of a row at the type's lowest number, T < 1) is infinite.
@@ -959,7 +959,7 @@ SSV_API ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream);
  * loss is not used (may be NULL).
  * grad [n, V] device in the logits' dtype, rows grad_stride elements apart
  * (0: V).  It may be the logits themselves (same address and stride), and
- * overlaps no other argument; fastest where its rows lie to 32-byte boundaries
+ * overlaps no other argument; fastest where its rows lie to 16-byte boundaries
  * as the logits' do.  Elements between rows are not written.
  * A row of weight 0 is not read: its loss, statistics and gradient are 0.
  * A row with a NaN (or +inf) in its logits, or a NaN in its target, gives NaN in its loss and

@@ -28,7 +28,7 @@ def _logprobs(**kw):
 def test_logprobs_validation(L):
     inv = ssv.SSV_ERR_INVALID
     cases = [(dict(logits=None), inv), (dict(logits=M + 1), inv), (dict(dtype=ssv.SSV_F32, logits=M + 2), inv),
-             (dict(dtype=2), inv), (dict(V=0), inv), (dict(V=(1 << 19) + 1), ssv.SSV_ERR_UNSUPPORTED),
+             (dict(dtype=2), inv), (dict(V=0), inv), (dict(V=393217), ssv.SSV_ERR_UNSUPPORTED),
              (dict(logits_stride=999), inv), (dict(logits_stride=-1000), inv), (dict(n=-1), inv), (dict(n=9), inv),
              (dict(total_rows=-1), inv), (dict(top_k=-1), inv), (dict(top_k=129), ssv.SSV_ERR_UNSUPPORTED),
              (dict(top_logprob=None), inv), (dict(top_token=None), inv), (dict(logprob=None), inv),

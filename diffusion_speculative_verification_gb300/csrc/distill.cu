@@ -26,7 +26,7 @@
 namespace ssv {
 namespace {
 
-constexpr int kParts = 8 * kMaxCluster;        // warps of a cluster
+constexpr int kParts = kLogitsThreads / 32 * kMaxCluster;  // warps of a cluster
 constexpr int kHash = 2 * kLogitsMaxTop;       // places of the table in which repeated tokens meet
 constexpr int kEach = kLogitsMaxTop / 32;      // listed tokens of a lane
 
@@ -45,7 +45,7 @@ struct DistillParams {
   void* grad;
   int32_t* dev_status;
   int log_c, log_nt;
-  int slot_bytes;
+  int slot_bytes;  // of the ring
   int vec;  // rows of the gradient lie as those of the logits do to 16-byte boundaries
 };
 
@@ -236,7 +236,7 @@ __device__ __forceinline__ Slope slope_of(const Sums& s, const Mass& t, const Sc
 }
 
 __device__ __forceinline__ void store_vector(void* p, const uint4& r) {
-  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w) : "memory");
+  asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w) : "memory");
 }
 
 template <typename T>
@@ -279,50 +279,65 @@ __device__ __forceinline__ void write_elements(T* out, int lo, int hi, F f) {
   }
 }
 
-// Gradient of a CTA's part, from its slots: of the other tokens, then that of the listed ones over it.  `aligned`: the
-// output's vectors are those of the input.
+// The gradient of the other tokens, of one vector.
 template <typename T>
-__device__ __forceinline__ void write_gradient(const DistillParams& p, const RowView<T>& row, const PartView<T>& part,
-                                               const uint4* slots, T* out, const Slope& k, const Target& tg) {
-  const int tid = threadIdx.x, NT = blockDim.x;
-  if (p.vec) {
-    char* to = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(15)) + (size_t)part.i0 * 16;
-    const float2 sc2 = make_float2(p.T.sc, p.T.sc), ref2 = make_float2(-k.ref, -k.ref), c2 = make_float2(k.coef, k.coef);
-    auto gradient = [&](const uint4& x) {
-      float2 y[kVec<T> / 2];
+struct Gradient {
+  float2 ref2, sc2, c2;
+
+  __device__ __forceinline__ Gradient(const Slope& k, float sc)
+      : ref2(make_float2(-k.ref, -k.ref)), sc2(make_float2(sc, sc)), c2(make_float2(k.coef, k.coef)) {}
+  __device__ __forceinline__ uint4 operator()(const uint4& x) const {
+    float2 y[kVec<T> / 2];
 #pragma unroll
-      for (int e = 0; e < kVec<T> / 2; ++e) {
-        const float2 a = mul2(add2(pair_of<T>(x, e), ref2), sc2);
-        y[e] = mul2(make_float2(ex2(a.x), ex2(a.y)), c2);
-      }
-      return pack_vector<T>([&](int e) { return e & 1 ? y[e / 2].y : y[e / 2].x; });
-    };
-    // whole vectors, kBatch at a time; the row's first and last one by element, each by the thread that has it
-    const int n = part.i1 - part.i0, begin = row.lo > part.i0 ? 1 : 0, end = min(part.i1, row.hi) - part.i0;
-    int i = tid < begin ? tid + NT : tid;
-    const uint4* from = slots + i;
-    to += (size_t)i * 16;
-    for (; i + NT * (kBatch - 1) < end; i += NT * kBatch, from += NT * kBatch, to += (size_t)(NT * kBatch) * 16) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) store_vector(to + (size_t)(NT * 16) * u, gradient(from[NT * u]));
+    for (int e = 0; e < kVec<T> / 2; ++e) {
+      const float2 a = mul2(add2(pair_of<T>(x, e), ref2), sc2);
+      y[e] = mul2(make_float2(ex2(a.x), ex2(a.y)), c2);
     }
-    for (; i < end; i += NT, from += NT, to += (size_t)NT * 16) store_vector(to, gradient(*from));
-#pragma unroll 1
-    for (int q = 0; q < 2; ++q) {
-      const int j = q ? n - 1 : 0;
-      if (n > 0 && (q == 0 || n > 1) && !row.whole(part.i0 + j) && tid == (j & (NT - 1))) {
-        const uint4 y = gradient(slots[j]);
-        const T* e = reinterpret_cast<const T*>(&y);
-        for (int v = max(0, row.first(part.i0 + j)); v < min(row.V, row.first(part.i0 + j + 1)); ++v)
-          out[v] = e[v - row.first(part.i0 + j)];
-      }
-    }
-  } else {
-    __syncthreads();  // every thread's vectors are there
-    const T* in = reinterpret_cast<const T*>(slots) - part.at;
-    write_elements<T>(out, part.lo, part.hi, [&](int v) { return ex2((Elem<T>::to_f32(in[v]) - k.ref) * p.T.sc) * k.coef; });
+    return pack_vector<T>([&](int e) { return e & 1 ? y[e / 2].y : y[e / 2].x; });
   }
-  __syncthreads();
+};
+
+// Step k of the thread's vectors, from its slots to an output whose vectors are those of the input; the row's first and
+// last vectors by element.
+template <typename T>
+__device__ __forceinline__ void write_step(const RowView<T>& row, const PartView<T>& part, int k, const uint4* slots, T* out,
+                                           const Gradient<T>& gradient) {
+  const int NT = blockDim.x, i = part.i0 + (int)threadIdx.x + NT * kBatch * k;
+  char* to = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(15)) + (size_t)i * 16;
+  if (part.full(k)) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) store_vector(to + (size_t)(NT * 16) * u, gradient(slots[NT * u]));
+  } else {
+#pragma unroll 1
+    for (int u = 0; u < kBatch && i + NT * u < part.i1; ++u) {
+      const uint4 y = gradient(slots[NT * u]);
+      if (row.whole(i + NT * u)) {
+        store_vector(to + (size_t)(NT * 16) * u, y);
+      } else {
+        const int v0 = row.first(i + NT * u);
+        for (int e = 0; e < kVec<T>; ++e) {
+          const uint32_t w = e * (int)sizeof(T) < 4 ? y.x : e * (int)sizeof(T) < 8 ? y.y : e * (int)sizeof(T) < 12 ? y.z : y.w;
+          if (v0 + e < 0 || v0 + e >= row.V) continue;
+          if (sizeof(T) == 2)
+            reinterpret_cast<uint16_t*>(out)[v0 + e] = (uint16_t)(e & 1 ? w >> 16 : w);
+          else
+            reinterpret_cast<uint32_t*>(out)[v0 + e] = w;
+        }
+      }
+    }
+  }
+}
+
+// Of an output at any offset from the input, with elements from `in`.
+template <typename T>
+__device__ __forceinline__ void write_apart(const PartView<T>& part, const T* in, T* out, const Slope& k, float sc) {
+  write_elements<T>(out, part.lo, part.hi, [&](int v) { return ex2((Elem<T>::to_f32(in[v]) - k.ref) * sc) * k.coef; });
+}
+
+// The listed tokens' entries, over what is there (after a barrier).
+template <typename T>
+__device__ __forceinline__ void write_listed(const DistillParams& p, const PartView<T>& part, T* out, const Slope& k,
+                                             const Target& tg) {
   each_listed(p.K, [&](int, int j) {
     const int v = tg.token[j];
     if (v >= part.lo && v < part.hi) out[v] = Elem<T>::from_f32(k.wT * (k.share * ex2((tg.z[j] - k.top) * p.T.sc) - tg.p[j]));
@@ -340,24 +355,10 @@ struct Shared {
   uint32_t part[kParts][2];  // of every warp: maximum and sum of its other tokens
 };
 
-// waits until at most n of the thread's copies are on their way (n above 7: until 7 are)
-__device__ __forceinline__ void copy_wait_all_but(int n) {
-  switch (n) {
-    case 0: copy_wait<0>(); break;
-    case 1: copy_wait<1>(); break;
-    case 2: copy_wait<2>(); break;
-    case 3: copy_wait<3>(); break;
-    case 4: copy_wait<4>(); break;
-    case 5: copy_wait<5>(); break;
-    case 6: copy_wait<6>(); break;
-    default: copy_wait<7>(); break;
-  }
-}
-
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const DistillParams p) {
-  // slots: a ring, or with the gradient the CTA's whole part; behind them a word per thread and step, whose bit
-  // (vector of the step, element) says that the element is a listed token
+__global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const DistillParams p) {
+  // a ring of slots; behind it a word per thread and step, whose bit (vector of the step, element) says that the
+  // element is a listed token
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
@@ -382,9 +383,8 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
     if (c > 1) cluster_wait();
     return;
   }
-  auto step_slots = [&](int k) { return slots + kBatch * (GRAD ? k : k % kStages) * NT + tid; };
-  const int ahead = GRAD ? part.steps : kStages;
-  for (int k = 0; k < ahead; ++k) part.fetch(row, k, step_slots(k));
+  auto step_slots = [&](int k) { return slots + kBatch * (k % kStages) * NT + tid; };
+  for (int k = 0; k < kStages; ++k) part.fetch(row, k, step_slots(k));
 
   // ------------------------------------------------------------ the target
   Target& tg = sm.tg;
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
     uint4 x[kBatch];
     part.template take<FULL>(k, at, x);
     const float mx = step_max<T>(x);
-    if (!GRAD) part.fetch(row, k + kStages, at);  // into the slots that have just been read
+    part.fetch(row, k + kStages, at);  // into the slots that have just been read
     if (mx > m) {
       S *= ex2(shift_of(m, mx, p.T.sc));
       m = mx;
@@ -438,10 +438,14 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
     S += S2.x + S2.y;
   };
   for (int k = 0; k < part.steps; ++k) {
-    if (GRAD) copy_wait_all_but(part.steps - 1 - k); else copy_wait<kStages - 1>();
+    copy_wait<kStages - 1>();
     if (part.full(k)) step(std::true_type{}, k); else step(std::false_type{}, k);
   }
-  if (!GRAD) copy_wait<0>();
+  copy_wait<0>();
+  // the gradient takes the row's steps from the last one on: what was read last is the likeliest to be in L2
+  const bool again = GRAD && p.vec;
+  if (again)
+    for (int k = 0; k < kStages; ++k) part.fetch(row, part.steps - 1 - k, step_slots(k));
   {
     const float M = warp_max(m), Sw = warp_sum(ex2(shift_of(m, M, p.T.sc)) * S);
     if (c > 1) cluster_wait();
@@ -466,11 +470,11 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
   Sums sums;
   if (warp == 0) {
     const int n = c * nw;
-    const float m0 = lane < n ? __uint_as_float(sm.part[lane][0]) : -INFINITY;
-    const float m1 = lane + 32 < n ? __uint_as_float(sm.part[lane + 32][0]) : -INFINITY;
-    sums.mr = warp_max(fmaxf(m0, m1));
-    float s = lane < n ? ex2(shift_of(m0, sums.mr, p.T.sc)) * __uint_as_float(sm.part[lane][1]) : 0.f;
-    if (lane + 32 < n) s += ex2(shift_of(m1, sums.mr, p.T.sc)) * __uint_as_float(sm.part[lane + 32][1]);
+    float mx = -INFINITY, s = 0.f;
+    for (int q = lane; q < n; q += 32) mx = fmaxf(mx, __uint_as_float(sm.part[q][0]));
+    sums.mr = warp_max(mx);
+    for (int q = lane; q < n; q += 32)
+      s += ex2(shift_of(__uint_as_float(sm.part[q][0]), sums.mr, p.T.sc)) * __uint_as_float(sm.part[q][1]);
     sums.Sr = warp_sum(s);
     float mt = -INFINITY;
 #pragma unroll
@@ -525,15 +529,30 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_kernel(const Distil
     }
   }
   if (GRAD) {
-    if (sm.slope.empty)
+    const Slope k = sm.slope;
+    if (k.empty) {
+      copy_wait<0>();
       write_zeros<T>(part, out);
-    else
-      write_gradient<T>(p, row, part, slots, out, sm.slope, tg);
+      return;
+    }
+    if (again) {
+      const Gradient<T> gradient(k, p.T.sc);
+      for (int q = 0; q < part.steps; ++q) {
+        copy_wait<kStages - 1>();
+        write_step<T>(row, part, part.steps - 1 - q, step_slots(q), out, gradient);
+        part.fetch(row, part.steps - 1 - q - kStages, step_slots(q));
+      }
+      copy_wait<0>();
+    } else {
+      write_apart<T>(part, row.row, out, k, p.T.sc);
+    }
+    __syncthreads();
+    write_listed<T>(p, part, out, k, tg);
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLogitsThreads, 4) distill_backward_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(128, 8) distill_backward_kernel(const DistillParams p) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Target tg;
   __shared__ Slope slope;
@@ -567,10 +586,19 @@ __global__ void __launch_bounds__(kLogitsThreads, 4) distill_backward_kernel(con
   if (tid == 0) slope = slope_of(sums, mass, p.T, w * up);
   __syncthreads();
   copy_wait<0>();
-  if (slope.empty)
+  if (slope.empty) {
     write_zeros<T>(part, out);
-  else
-    write_gradient<T>(p, row, part, slots, out, slope, tg);
+    return;
+  }
+  if (p.vec) {
+    const Gradient<T> gradient(slope, p.T.sc);
+    for (int k = 0; k < part.steps; ++k) write_step<T>(row, part, k, slots + kBatch * k * NT + tid, out, gradient);
+  } else {
+    __syncthreads();  // every thread's vectors are there
+    write_apart<T>(part, reinterpret_cast<const T*>(slots) - part.at, out, slope, p.T.sc);
+  }
+  __syncthreads();
+  write_listed<T>(p, part, out, slope, tg);
 }
 
 // The gradient's rows apart from the logits', or on them exactly.
@@ -627,17 +655,17 @@ RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, i
   const int vectors = row_vectors(V, element_size);
   int c = 1;
   while (c < most && (vectors + c - 1) / c > bytes / 16) c *= 2;
-  while (c < most && (long long)rows * c * 2 <= 608 && vectors > 4 * c * kLogitsThreads) c *= 2;
+  while (c < most && (long long)rows * c * 2 <= 608 && vectors > 4 * c * threads) c *= 2;
   return split_of(vectors, c, threads);
 }
 
 template <typename T, bool GRAD>
 cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   static uint64_t done = 0;
-  const RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 48 * 1024 : 1 << 20, kMaxCluster, kLogitsThreads);
+  const RowSplit sp = distill_split(n, p.V, sizeof(T), 1 << 20, kMaxCluster, GRAD ? 512 : 256);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
-  p.slot_bytes = 16 * (GRAD ? sp.vectors : kStages * kBatch * sp.threads);
+  p.slot_bytes = 16 * kStages * kBatch * sp.threads;
   const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
   const cudaError_t e = allow_shared(distill_kernel<T, GRAD>, smem, &done);
   return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD>, n, sp, smem, st, p);
@@ -646,7 +674,7 @@ cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
 template <typename T>
 cudaError_t backward_launch(DistillParams& p, int n, cudaStream_t st) {
   static uint64_t done = 0;
-  const RowSplit sp = distill_split(n, p.V, sizeof(T), 48 * 1024, 64, kLogitsThreads);
+  const RowSplit sp = distill_split(n, p.V, sizeof(T), 48 * 1024, 64, 128);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
   const size_t smem = 16 * (size_t)sp.vectors;

@@ -22,7 +22,7 @@
 
 namespace ssv {
 
-constexpr int kLogitsThreads = 256;     // most threads of a CTA
+constexpr int kLogitsThreads = 512;     // most threads of a CTA
 constexpr int kLogitsMaxVocab = 393216; // largest V: 8 CTAs of a cluster hold it in shared memory, as fp32
 constexpr int kLogitsMaxTop = 128;      // most alternatives of a row
 constexpr int kMaxCluster = 8;
@@ -190,6 +190,10 @@ struct PartView {
   __device__ __forceinline__ bool full(int k) const { return k >= full0 && k < full1; }
   // the thread's vectors of step k, from `slots` on, NT apart
   __device__ __forceinline__ void fetch(const RowView<T>& row, int k, uint4* slots) const {
+    if (k < 0) {  // none, but a group of copies all the same
+      copy_commit();
+      return;
+    }
     const int NT = blockDim.x, i = i0 + (int)threadIdx.x + NT * kBatch * k;
     if (full(k)) {
       const char* from = row.base + (size_t)i * 16;

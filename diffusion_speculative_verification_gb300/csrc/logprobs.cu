@@ -63,7 +63,7 @@ struct Shared {
   int groups, count, total;   // batches and keys listed here, keys sent to the cluster's first CTA
   int at;
   float least;
-  int sum[kLogitsThreads / 32];
+  int sum[8];
   uint32_t pool[kPool];       // order of the largest lane maxima of every warp of the cluster, 0: none
 };
 
@@ -195,7 +195,7 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLogitsThreads, 4) logprobs_kernel(const LogprobsParams p) {
+__global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p) {
   extern __shared__ __align__(16) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
@@ -472,8 +472,8 @@ cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, 
 RowSplit logprobs_split(int rows, int V, int element_size) {
   const int vectors = row_vectors(V, element_size);
   int c = 1;
-  while (c < kMaxCluster && (long long)rows * c * 2 <= 608 && vectors > 4 * c * kLogitsThreads) c *= 2;
-  return split_of(vectors, c, kLogitsThreads);
+  while (c < kMaxCluster && (long long)rows * c * 2 <= 608 && vectors > 4 * c * 256) c *= 2;
+  return split_of(vectors, c, 256);
 }
 
 }  // namespace

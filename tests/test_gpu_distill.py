@@ -96,15 +96,12 @@ def check(z, token, value, dtype, mode, T=1.0, weight=None, lead=0, pad=0, grad_
     x, buf = rows()
     loss, stats, none = ssv.distill(x, tok, val, T, mode, wt, dev_status=status)
     assert none is None and ssv.get_status(status) == code
-    near(loss.cpu().numpy(), want[0], tl + EPS * np.abs(np.where(np.isfinite(want[0]), want[0], 0)))
-    got = stats.cpu().numpy()
-    near(got[:, ::2], want[2][:, ::2], 0)
-    near(got[:, 1::2], want[2][:, 1::2], LN * want[2][:, 1::2])
+    _forward(loss, stats, want, tl)
     # loss and gradient
     g, gbuf = (x, buf) if in_place else space()
-    loss2, stats2, grad = ssv.distill(x, tok, val, T, mode, wt, grad=g, dev_status=status)
+    loss, stats, grad = ssv.distill(x, tok, val, T, mode, wt, grad=g, dev_status=status)
     assert ssv.get_status(status) == code
-    assert torch.equal(loss2.view(torch.int32), loss.view(torch.int32)) and torch.equal(stats2.view(torch.int32), stats.view(torch.int32))
+    _forward(loss, stats, want, tl)
     near(grad.float().cpu().numpy(), want[1], tg + half_step(np.where(np.isfinite(want[1]), want[1], 0), dtype))
     _between(gbuf, grad)
     # backward from the statistics, which are the ones that the gradient above was formed from
@@ -116,6 +113,13 @@ def check(z, token, value, dtype, mode, T=1.0, weight=None, lead=0, pad=0, grad_
     up = np.where(w[:, None] == 0, 0.0, up)              # a row of weight 0 has the gradient 0, whatever comes from upstream
     near(grad.float().cpu().numpy(), want[1] * up, tg * np.abs(up) + half_step(want[1] * up, dtype))
     _between(gbuf, grad)
+
+
+def _forward(loss, stats, want, tol):
+    near(loss.cpu().numpy(), want[0], tol + EPS * np.abs(np.where(np.isfinite(want[0]), want[0], 0)))
+    got = stats.cpu().numpy()
+    near(got[:, ::2], want[2][:, ::2], 0)
+    near(got[:, 1::2], want[2][:, 1::2], LN * want[2][:, 1::2])
 
 
 def _between(buf, rows):

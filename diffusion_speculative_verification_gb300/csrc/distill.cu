@@ -60,143 +60,128 @@ struct Target {
   float p[kLogitsMaxTop], t[kLogitsMaxTop], z[kLogitsMaxTop];
   int hash[kHash];
   Mass mass;
+  float top, sum;  // largest of z, sum of exp((z - top) / T)
 };
 
-// Whole CTA: the listed tokens of row i and the given values, in three parts, so that callers can work in between:
-// loads into registers; tokens into shared memory (true where one is listed twice); probabilities.
+// One warp brings a row's target, four entries per lane (j = lane + 32 k), while the others are busy with the row.
 struct Listed {
   int v[kEach];
   float t[kEach];
+
+  __device__ __forceinline__ void load(const DistillParams& p, int row) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = lane + 32 * k;
+      v[k] = j < p.K ? p.token[(size_t)row * p.K + j] : -1;
+      t[k] = j < p.K ? p.logp[(size_t)row * p.K + j] : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ void check(const DistillParams& p, bool tell) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (v[k] < 0 || v[k] >= p.V) {
+        if (v[k] != -1 && tell) report(p.dev_status, SSV_ERR_INVALID);
+        v[k] = -1;
+        t[k] = -INFINITY;
+      }
+  }
 };
 
-template <typename F>
-__device__ __forceinline__ void each_listed(int K, F f) {
-  int n = 0;
-  for (int j = threadIdx.x; j < K; j += blockDim.x) f(n++, j);
-}
-
-__device__ __forceinline__ Listed load_listed(const DistillParams& p, int i, bool tell, Target& tg) {
-  Listed l;
-  const int32_t* token = p.token + (size_t)i * p.K;
-  const float* logp = p.logp + (size_t)i * p.K;
+// The warp's entries to shared memory: `row` their logits, those of [lo, hi) alone (the others are not asked for).
+template <typename T>
+__device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, const T* row, int lo, int hi, Target& tg) {
+  const int lane = threadIdx.x & 31;
+  float z[kEach];
 #pragma unroll
-  for (int n = 0; n < kEach; ++n) {
-    const int j = threadIdx.x + n * blockDim.x;
-    l.v[n] = -1;
-    l.t[n] = -INFINITY;
-    if (j < p.K) {
-      l.v[n] = token[j];
-      l.t[n] = logp[j];
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < kEach; ++n)
-    if (l.v[n] < 0 || l.v[n] >= p.V) {
-      if (l.v[n] != -1 && tell) report(p.dev_status, SSV_ERR_INVALID);
-      l.v[n] = -1;
-      l.t[n] = -INFINITY;
-    }
-  for (int h = threadIdx.x; h < kHash; h += blockDim.x) tg.hash[h] = -1;
-  return l;
-}
-
-// After a barrier behind load_listed.
-__device__ __forceinline__ bool place_listed(const DistillParams& p, const Listed& l, Target& tg) {
+  for (int k = 0; k < kEach; ++k) z[k] = l.v[k] >= lo && l.v[k] < hi ? load_element(row + l.v[k]) : -INFINITY;
+  // tokens listed twice meet in a table
+  for (int h = lane; h < kHash; h += 32) tg.hash[h] = -1;
+  __syncwarp();
   bool twice = false;
 #pragma unroll
-  for (int n = 0; n < kEach; ++n) {
-    const int j = threadIdx.x + n * blockDim.x;
-    if (j >= p.K) break;
-    tg.token[j] = l.v[n];
-    tg.t[j] = l.t[n];
-    if (l.v[n] < 0) continue;
+  for (int k = 0; k < kEach; ++k) {
+    if (32 * k >= p.K) break;
+    if (l.v[k] < 0) continue;
     // at most K of 2 K places are taken, so that a free one is met within K steps
-    for (uint32_t h = ((uint32_t)l.v[n] * 2654435761u) >> 24, s = 0; s < kHash; ++s, h = (h + 1) % kHash) {
-      const int was = atomicCAS(&tg.hash[h], -1, l.v[n]);
-      if (was == -1) break;
-      if (was == l.v[n]) {
-        twice = true;
-        break;
-      }
+    uint32_t h = ((uint32_t)l.v[k] * 2654435761u) >> 24;
+    for (int s = 0; s < kHash; ++s, h = (h + 1) % kHash) {
+      const int was = atomicCAS(&tg.hash[h], -1, l.v[k]);
+      twice |= was == l.v[k];
+      if (was == -1 || was == l.v[k]) break;
     }
   }
-  return twice;
-}
-
-// After a barrier behind place_listed; `twice`: of any thread.  Ends with one.
-__device__ __forceinline__ Mass weigh_listed(const DistillParams& p, bool twice, Target& tg) {
+  twice = __any_sync(0xffffffffu, twice);
+  // probabilities: relative to the largest for a softmax; as they are where they are log-probabilities
   const bool as_is = p.mode == SSV_DISTILL_REST;
-  if (threadIdx.x < 32) {
-    // four entries per lane, the sums in a fixed order
-    const int lane = threadIdx.x;
-    float x[kEach], mx = -INFINITY;
+  float mx = -INFINITY, s = 0.f, e[kEach];
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int j = lane + 32 * k;
-      x[k] = j < p.K ? tg.t[j] : -INFINITY;
-      mx = fmaxf(mx, x[k]);
-    }
-    mx = warp_max(mx);
-    // relative to the largest for a softmax; as they are where they are log-probabilities
-    const float ref = as_is || mx == -INFINITY ? 0.f : mx;
-    float s = 0.f, e[kEach];
+  for (int k = 0; k < kEach; ++k) mx = fmaxf(mx, l.t[k]);
+  mx = warp_max(mx);
+  const float ref = as_is || mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      x[k] -= ref;
-      e[k] = expf(x[k]);
-      s += e[k];
-    }
-    s = warp_sum(s);
-    const float norm = as_is || s == 0.f ? 1.f : s, ln = logf(norm);
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int j = lane + 32 * k;
-      if (j < p.K) {
-        tg.p[j] = e[k] / norm;
-        tg.t[j] = x[k] - ln;
-      }
-    }
-    if (lane == 0) {
-      tg.mass.sum = as_is || s == 0.f || s != s ? s : 1.f;
-      tg.mass.rest = as_is ? (s > 1.f ? 0.f : 1.f - s) : 0.f;  // NaN stays
-    }
+  for (int k = 0; k < kEach; ++k) {
+    e[k] = 32 * k < p.K ? expf(l.t[k] - ref) : 0.f;
+    s += e[k];
   }
-  __syncthreads();
+  s = warp_sum(s);
+  const float norm = as_is || s == 0.f ? 1.f : s, ln = logf(norm);
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    if (32 * k >= p.K) break;
+    e[k] /= norm;
+    l.t[k] = l.t[k] - ref - ln;
+  }
   if (twice) {  // the first of equal tokens takes the others' probabilities
-    float all[kEach];
-    unsigned first = 0, later = 0;
-    each_listed(p.K, [&](int n, int j) {
-      const int v = tg.token[j];
-      float q = tg.p[j];
-      bool leads = true, alone = true;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      tg.token[lane + 32 * k] = l.v[k];
+      tg.p[lane + 32 * k] = e[k];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = lane + 32 * k, v = l.v[k];
+      if (v < 0) continue;
       for (int o = 0; o < p.K; ++o) {
-        if (o == j || v < 0 || tg.token[o] != v) continue;
-        alone = false;
-        if (o < j) leads = false; else q += tg.p[o];
+        if (o == j || tg.token[o] != v) continue;
+        if (o < j) {
+          l.v[k] = -1;
+          break;
+        }
+        e[k] += tg.p[o];
+        l.t[k] = logf(e[k]);
       }
-      if (!leads) later |= 1u << n; else if (!alone) first |= 1u << n;
-#pragma unroll
-      for (int k = 0; k < kEach; ++k)
-        if (k == n) all[k] = q;
-    });
-    __syncthreads();
-    each_listed(p.K, [&](int n, int j) {
-      float q = 0.f;
-#pragma unroll
-      for (int k = 0; k < kEach; ++k)
-        if (k == n) q = all[k];
-      if (later >> n & 1u) {
-        tg.token[j] = -1;
-        tg.p[j] = 0.f;
-        tg.t[j] = -INFINITY;
-      } else if (first >> n & 1u) {
-        tg.p[j] = q;
-        tg.t[j] = logf(q);
+      if (l.v[k] < 0) {
+        e[k] = 0.f;
+        l.t[k] = -INFINITY;
+        z[k] = -INFINITY;
       }
-    });
-    __syncthreads();
+    }
+    __syncwarp();
   }
-  return tg.mass;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int j = lane + 32 * k;
+    tg.token[j] = l.v[k];
+    tg.p[j] = e[k];
+    tg.t[j] = l.t[k];
+    tg.z[j] = z[k];
+    top = fmaxf(top, z[k]);
+  }
+  top = warp_max(top);
+  const float zero = top == -INFINITY ? 0.f : top;  // -inf counts nothing, NaN stays
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (32 * k < p.K) sum += ex2((z[k] - zero) * p.T.sc);
+  sum = warp_sum(sum);
+  if (lane == 0) {
+    tg.mass.sum = as_is || s == 0.f || s != s ? s : 1.f;
+    tg.mass.rest = as_is ? (s > 1.f ? 0.f : 1.f - s) : 0.f;  // NaN stays
+    tg.top = top;
+    tg.sum = sum;
+  }
 }
 
 // r, where the drafter leaves the other tokens nothing (every one is listed or masked): there, what the roundings of
@@ -302,7 +287,7 @@ struct Gradient {
 template <typename T>
 __device__ __forceinline__ void write_step(const RowView<T>& row, const PartView<T>& part, int k, const uint4* slots, T* out,
                                            const Gradient<T>& gradient) {
-  const int NT = blockDim.x, i = part.i0 + (int)threadIdx.x + NT * kBatch * k;
+  const int NT = part.NT, i = part.i0 + (int)threadIdx.x + NT * kBatch * k;
   char* to = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(15)) + (size_t)i * 16;
   if (part.full(k)) {
 #pragma unroll
@@ -338,10 +323,10 @@ __device__ __forceinline__ void write_apart(const PartView<T>& part, const T* in
 template <typename T>
 __device__ __forceinline__ void write_listed(const DistillParams& p, const PartView<T>& part, T* out, const Slope& k,
                                              const Target& tg) {
-  each_listed(p.K, [&](int, int j) {
+  for (int j = threadIdx.x; j < p.K; j += blockDim.x) {
     const int v = tg.token[j];
     if (v >= part.lo && v < part.hi) out[v] = Elem<T>::from_f32(k.wT * (k.share * ex2((tg.z[j] - k.top) * p.T.sc) - tg.p[j]));
-  });
+  }
 }
 
 template <typename T>
@@ -355,16 +340,20 @@ struct Shared {
   uint32_t part[kParts][2];  // of every warp: maximum and sum of its other tokens
 };
 
+// Steps in flight: three with the gradient, which keep the last 30% of a long row for it.
+template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
+
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const DistillParams p) {
   // a ring of slots; behind it a word per thread and step, whose bit (vector of the step, element) says that the
   // element is a listed token
-  extern __shared__ __align__(16) unsigned char dynamic[];
+  extern __shared__ __align__(128) unsigned char dynamic[];
   __shared__ Shared sm;
-  const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
+  // NT threads share the row, and a warp behind them brings its target
+  const int tid = threadIdx.x, NT = 1 << p.log_nt, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
+  const bool streams = warp < nw;
   const int c = 1 << p.log_c;
   const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
-  uint4* slots = reinterpret_cast<uint4*>(dynamic);
   uint32_t* listed = reinterpret_cast<uint32_t*>(dynamic + p.slot_bytes);
   if (c > 1) cluster_arrive();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
@@ -383,26 +372,28 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
     if (c > 1) cluster_wait();
     return;
   }
-  auto step_slots = [&](int k) { return slots + kBatch * (k % kStages) * NT + tid; };
-  for (int k = 0; k < kStages; ++k) part.fetch(row, k, step_slots(k));
+  uint4* slots = part.slots_in(dynamic, row);
+  auto step_slots = [&](int k) { return slots + kBatch * (k % kStages<GRAD>) * NT + tid; };
+  if (streams)
+    for (int k = 0; k < kStages<GRAD>; ++k) part.fetch(row, k, step_slots(k));
 
   // ------------------------------------------------------------ the target
   Target& tg = sm.tg;
-  const Listed mine = load_listed(p, entry, rank == 0, tg);
-  for (int i = tid; i < part.steps * NT; i += NT) listed[i] = 0u;
+  Listed mine;
+  if (!streams) mine.load(p, entry);
+  for (int i = tid; i < part.steps * NT; i += blockDim.x) listed[i] = 0u;
   __syncthreads();
+  if (!streams) {
+    mine.check(p, rank == 0);
 #pragma unroll
-  for (int n = 0; n < kEach; ++n) {
-    const int j = tid + n * NT, v = mine.v[n];
-    if (j >= p.K || v < 0) continue;
-    tg.z[j] = load_element(row.row + v);
-    if (v >= part.lo && v < part.hi) {
+    for (int k = 0; k < kEach; ++k) {
+      const int v = mine.v[k];
+      if (v < part.lo || v >= part.hi) continue;
       const int i = (v - part.at) / kVec<T>, e = (v - part.at) % kVec<T>, s = i >> p.log_nt;
       atomicOr(&listed[s / kBatch * NT + (i & (NT - 1))], 1u << (s % kBatch * kVec<T> + e));
     }
   }
-  const bool twice = __syncthreads_or(place_listed(p, mine, tg));
-  const Mass mass = weigh_listed(p, twice, tg);
+  __syncthreads();
 
   // ------------------------------------------------------------ the other tokens
   float m = -INFINITY, S = 0.f;
@@ -418,7 +409,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
     uint4 x[kBatch];
     part.template take<FULL>(k, at, x);
     const float mx = step_max<T>(x);
-    part.fetch(row, k + kStages, at);  // into the slots that have just been read
+    part.fetch(row, k + kStages<GRAD>, at);  // into the slots that have just been read
     if (mx > m) {
       S *= ex2(shift_of(m, mx, p.T.sc));
       m = mx;
@@ -437,18 +428,18 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
     }
     S += S2.x + S2.y;
   };
-  for (int k = 0; k < part.steps; ++k) {
-    copy_wait<kStages - 1>();
-    if (part.full(k)) step(std::true_type{}, k); else step(std::false_type{}, k);
+  if (streams) {
+    for (int k = 0; k < part.steps; ++k) {
+      copy_wait<kStages<GRAD> - 1>();
+      if (part.full(k)) step(std::true_type{}, k); else step(std::false_type{}, k);
+    }
+    copy_wait<0>();
+  } else {
+    weigh_listed<T>(p, mine, row.row, 0, p.V, tg);
   }
-  copy_wait<0>();
-  // the gradient takes the row's steps from the last one on: what was read last is the likeliest to be in L2
-  const bool again = GRAD && p.vec;
-  if (again)
-    for (int k = 0; k < kStages; ++k) part.fetch(row, part.steps - 1 - k, step_slots(k));
-  {
+  if (c > 1) cluster_wait();
+  if (streams) {
     const float M = warp_max(m), Sw = warp_sum(ex2(shift_of(m, M, p.T.sc)) * S);
-    if (c > 1) cluster_wait();
     const int me = rank * nw + warp;
     const uint32_t word = lane & 1 ? __float_as_uint(Sw) : __float_as_uint(M);
     if (c == 1) {
@@ -464,11 +455,11 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
   } else {
     __syncthreads();
   }
-  if (!GRAD && warp != 0) return;
+  if (!GRAD && streams) return;
 
   // ------------------------------------------------------------ the row's sums, by one warp of each CTA in the same order
   Sums sums;
-  if (warp == 0) {
+  if (!streams) {
     const int n = c * nw;
     float mx = -INFINITY, s = 0.f;
     for (int q = lane; q < n; q += 32) mx = fmaxf(mx, __uint_as_float(sm.part[q][0]));
@@ -476,27 +467,14 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
     for (int q = lane; q < n; q += 32)
       s += ex2(shift_of(__uint_as_float(sm.part[q][0]), sums.mr, p.T.sc)) * __uint_as_float(sm.part[q][1]);
     sums.Sr = warp_sum(s);
-    float mt = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int j = lane + 32 * k;
-      if (j < p.K && tg.token[j] >= 0) mt = fmaxf(mt, tg.z[j]);
-    }
-    sums.m = fmaxf(sums.mr, warp_max(mt));
-    const float ref = sums.m == -INFINITY ? 0.f : sums.m;
-    float st = 0.f;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int j = lane + 32 * k;
-      if (j < p.K && tg.token[j] >= 0) st += ex2((tg.z[j] - ref) * p.T.sc);
-    }
-    sums.S = ex2(shift_of(sums.mr, sums.m, p.T.sc)) * sums.Sr + warp_sum(st);
+    sums.m = fmaxf(sums.mr, tg.top);
+    sums.S = ex2(shift_of(sums.mr, sums.m, p.T.sc)) * sums.Sr + ex2(shift_of(tg.top, sums.m, p.T.sc)) * tg.sum;
     if (GRAD) {
-      if (lane == 0) sm.slope = slope_of(sums, mass, p.T, w);
+      if (lane == 0) sm.slope = slope_of(sums, tg.mass, p.T, w);
     }
   }
   if (GRAD) __syncthreads();
-  if (rank == 0 && warp == 0) {
+  if (rank == 0 && !streams) {
     const Pair lnS = log_sum(sums.S), inv = {p.T.hi, p.T.lo};
     Pair loss = {0.f, 0.f};
 #pragma unroll
@@ -513,7 +491,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
     for (int o = 16; o > 0; o >>= 1)
       loss = loss + Pair{__shfl_xor_sync(0xffffffffu, loss.hi, o), __shfl_xor_sync(0xffffffffu, loss.lo, o)};
     if (lane == 0) {
-      const float rest = rest_of(mass, sums.none()), P = mass.sum + rest;
+      const float rest = rest_of(tg.mass, sums.none()), P = tg.mass.sum + rest;
       if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(Pair{logf(rest), 0.f} + -sums.ln_u(p.T)), 0.f};
       float l = w * value_of(loss);
       if (sums.S != sums.S) l = sums.S;
@@ -531,18 +509,17 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
   if (GRAD) {
     const Slope k = sm.slope;
     if (k.empty) {
-      copy_wait<0>();
       write_zeros<T>(part, out);
       return;
     }
-    if (again) {
+    if (p.vec) {
+      // from the last step on: the last ones are still in the ring, and what was read late is the likeliest to be in L2
       const Gradient<T> gradient(k, p.T.sc);
-      for (int q = 0; q < part.steps; ++q) {
-        copy_wait<kStages - 1>();
-        write_step<T>(row, part, part.steps - 1 - q, step_slots(q), out, gradient);
-        part.fetch(row, part.steps - 1 - q - kStages, step_slots(q));
+      for (int q = streams ? part.steps - 1 : -1; q >= 0; --q) {
+        copy_wait<kStages<GRAD> - 1>();
+        write_step<T>(row, part, q, step_slots(q), out, gradient);
+        part.fetch(row, q - kStages<GRAD>, step_slots(q));
       }
-      copy_wait<0>();
     } else {
       write_apart<T>(part, row.row, out, k, p.T.sc);
     }
@@ -553,13 +530,12 @@ __global__ void __launch_bounds__(kLogitsThreads, 2) distill_kernel(const Distil
 
 template <typename T>
 __global__ void __launch_bounds__(128, 8) distill_backward_kernel(const DistillParams p) {
-  extern __shared__ __align__(16) unsigned char dynamic[];
+  extern __shared__ __align__(128) unsigned char dynamic[];
   __shared__ Target tg;
   __shared__ Slope slope;
   const int tid = threadIdx.x, NT = blockDim.x;
   const int c = 1 << p.log_c;
   const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
-  uint4* slots = reinterpret_cast<uint4*>(dynamic);
   pdl_wait();
   pdl_trigger();
   const float w = p.weight ? p.weight[entry] : 1.f;
@@ -570,20 +546,19 @@ __global__ void __launch_bounds__(128, 8) distill_backward_kernel(const DistillP
     write_zeros<T>(part, out);
     return;
   }
+  uint4* slots = part.slots_in(dynamic, row);
   for (int k = 0; k < part.steps; ++k) part.fetch(row, k, slots + kBatch * k * NT + tid);
-  const Listed mine = load_listed(p, entry, rank == 0, tg);
-  const float* from = p.stats_in + 4 * (size_t)entry;
-  const Sums sums = {from[0], from[1], from[2], from[3]};
-  const float up = p.grad_loss ? p.grad_loss[entry] : 1.f;
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < kEach; ++n) {
-    const int j = tid + n * NT, v = mine.v[n];
-    if (j < p.K && v >= part.lo && v < part.hi) tg.z[j] = load_element(row.row + v);  // others are other CTAs'
+  if (tid < 32) {
+    Listed mine;
+    mine.load(p, entry);
+    const float* from = p.stats_in + 4 * (size_t)entry;
+    const Sums sums = {from[0], from[1], from[2], from[3]};
+    const float up = p.grad_loss ? p.grad_loss[entry] : 1.f;
+    mine.check(p, rank == 0);
+    weigh_listed<T>(p, mine, row.row, part.lo, part.hi, tg);
+    __syncwarp();
+    if (tid == 0) slope = slope_of(sums, tg.mass, p.T, w * up);
   }
-  const bool twice = __syncthreads_or(place_listed(p, mine, tg));
-  const Mass mass = weigh_listed(p, twice, tg);
-  if (tid == 0) slope = slope_of(sums, mass, p.T, w * up);
   __syncthreads();
   copy_wait<0>();
   if (slope.empty) {
@@ -662,13 +637,13 @@ RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, i
 template <typename T, bool GRAD>
 cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   static uint64_t done = 0;
-  const RowSplit sp = distill_split(n, p.V, sizeof(T), 1 << 20, kMaxCluster, GRAD ? 512 : 256);
+  const RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 160 * 1024 : 1 << 20, kMaxCluster, GRAD ? 512 : 256);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
-  p.slot_bytes = 16 * kStages * kBatch * sp.threads;
+  p.slot_bytes = 16 * kStages<GRAD> * kBatch * sp.threads + kSlotSlack;
   const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
   const cudaError_t e = allow_shared(distill_kernel<T, GRAD>, smem, &done);
-  return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD>, n, sp, smem, st, p);
+  return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD>, n, sp, sp.threads + 32, smem, st, p);
 }
 
 template <typename T>
@@ -677,9 +652,9 @@ cudaError_t backward_launch(DistillParams& p, int n, cudaStream_t st) {
   const RowSplit sp = distill_split(n, p.V, sizeof(T), 48 * 1024, 64, 128);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
-  const size_t smem = 16 * (size_t)sp.vectors;
+  const size_t smem = 16 * (size_t)sp.vectors + kSlotSlack;
   cudaError_t e = allow_shared(distill_backward_kernel<T>, smem, &done);
-  return e != cudaSuccess ? e : launch_rows(distill_backward_kernel<T>, n, sp, smem, st, p);
+  return e != cudaSuccess ? e : launch_rows(distill_backward_kernel<T>, n, sp, sp.threads, smem, st, p);
 }
 
 }  // namespace

@@ -172,6 +172,7 @@ struct RowView {
 template <typename T>
 struct PartView {
   int i0, i1, lo, hi, at, steps;
+  int NT;            // threads that share it
   int full0, full1;  // steps [full0, full1) are full: every thread has kBatch whole vectors
 
   // CTA `rank` of 2^log_c, of 2^log_nt threads (no division: eight warps of every CTA would spend more on it than on
@@ -182,10 +183,16 @@ struct PartView {
     at = row.first(i0);
     lo = max(0, at);
     hi = min(row.V, row.first(i1));
+    NT = 1 << log_nt;
     const int log_per = log_nt + kLogBatch;
     steps = (i1 - i0 + (1 << log_per) - 1) >> log_per;
     full0 = i0 < row.lo ? 1 : 0;
     full1 = max(0, min(i1, row.hi) - i0) >> log_per;
+  }
+  // Slots for the part in `memory` (128-byte aligned): placed to the 128-byte lines of shared memory as the vectors are
+  // to those of global memory, without which copies take a fifth longer.
+  __device__ __forceinline__ uint4* slots_in(unsigned char* memory, const RowView<T>& row) const {
+    return reinterpret_cast<uint4*>(memory) + (((uint32_t)(reinterpret_cast<uintptr_t>(row.base) >> 4) + (uint32_t)i0) & 7u);
   }
   __device__ __forceinline__ bool full(int k) const { return k >= full0 && k < full1; }
   // the thread's vectors of step k, from `slots` on, NT apart
@@ -194,7 +201,7 @@ struct PartView {
       copy_commit();
       return;
     }
-    const int NT = blockDim.x, i = i0 + (int)threadIdx.x + NT * kBatch * k;
+    const int i = i0 + (int)threadIdx.x + NT * kBatch * k;
     if (full(k)) {
       const char* from = row.base + (size_t)i * 16;
 #pragma unroll
@@ -208,7 +215,7 @@ struct PartView {
   // the same from the slots, -inf where there is none
   template <bool FULL>
   __device__ __forceinline__ void take(int k, const uint4* slots, uint4 (&x)[kBatch]) const {
-    const int NT = blockDim.x, i = i0 + (int)threadIdx.x + NT * kBatch * k;
+    const int i = i0 + (int)threadIdx.x + NT * kBatch * k;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       if (FULL || i + NT * u < i1)
@@ -329,11 +336,11 @@ inline cudaError_t allow_shared(K kernel, size_t bytes, uint64_t* done) {
 
 // CTAs of a row are a cluster, up to kMaxCluster of them; more are independent.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_rows(void (*kernel)(KArgs...), int rows, const RowSplit& sp, size_t smem, cudaStream_t st,
-                               Args&&... args) {
+inline cudaError_t launch_rows(void (*kernel)(KArgs...), int rows, const RowSplit& sp, int threads, size_t smem,
+                               cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * (unsigned)sp.ctas);
-  cfg.blockDim = dim3(sp.threads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -347,6 +354,8 @@ inline cudaError_t launch_rows(void (*kernel)(KArgs...), int rows, const RowSpli
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+
+constexpr int kSlotSlack = 128;  // bytes that slots_in may leave in front, up to a line
 
 // vectors of a row at most
 inline int row_vectors(int V, int element_size) { return (V * element_size + 15) / 16 + 1; }

@@ -30,6 +30,7 @@
 namespace ssv {
 namespace {
 
+constexpr int kStages = 2;                                  // steps in flight
 constexpr int kList = 512;                                  // keys that a list holds
 constexpr int kPool = 2 * kLogitsMaxTop + 8 * kMaxCluster;  // values of the pool at most: 2 K, and one of each warp
 constexpr int kParts = 8 * kMaxCluster;                     // warps of a cluster
@@ -54,7 +55,7 @@ struct LogprobsParams {
 
 // bytes of the ring, in which the lists have room
 __host__ __device__ constexpr size_t ring_bytes(int threads) {
-  const size_t ring = (size_t)kStages * kBatch * 16 * threads, lists = (2 * 8 + 4) * kList;
+  const size_t ring = (size_t)kStages * kBatch * 16 * threads + kSlotSlack, lists = (2 * 8 + 4) * kList;
   return ring > lists ? ring : lists;
 }
 
@@ -196,12 +197,11 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p) {
-  extern __shared__ __align__(16) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
+  extern __shared__ __align__(128) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
   const int c = 1 << p.log_c;
   const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
-  uint4* ring = reinterpret_cast<uint4*>(dynamic);
   Lists& lists = *reinterpret_cast<Lists*>(dynamic);
   __nv_bfloat16* tops = reinterpret_cast<__nv_bfloat16*>(dynamic + ring_bytes(NT));
   if (tid == 0) {
@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
   const RowView<T> row(static_cast<const T*>(p.logits) + (int64_t)r * p.stride, p.V);
   const PartView<T> part(row, rank, p.log_c, p.log_nt);
   const int i0 = part.i0, i1 = part.i1, steps = part.steps;
+  uint4* ring = part.slots_in(dynamic, row);
   auto slots = [&](int k) { return ring + kBatch * (k % kStages) * NT + tid; };
   for (int k = 0; k < kStages; ++k) part.fetch(row, k, slots(k));
   Given<T> given;
@@ -465,7 +466,7 @@ cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, 
   static uint64_t done = 0;
   const size_t smem = ring_bytes(sp.threads) + (TOP ? (size_t)sp.batches() * sp.threads * sizeof(__nv_bfloat16) : 0);
   const cudaError_t e = allow_shared(logprobs_kernel<T, TOP>, smem, &done);
-  return e != cudaSuccess ? e : launch_rows(logprobs_kernel<T, TOP>, n, sp, smem, st, p);
+  return e != cudaSuccess ? e : launch_rows(logprobs_kernel<T, TOP>, n, sp, sp.threads, smem, st, p);
 }
 
 // CTAs per row: as many as SMs have room for at once (four each), while a CTA has more than two batches.

@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
     }
     uint4 x[kBatch];
     part.template take<FULL>(k, at, x);
-    const float mx = step_max<T>(x);
+    const float2 mx2 = step_max<T>(x);
+    const float mx = fmaxf(mx2.x, mx2.y);
     part.fetch(row, k + kStages<GRAD>, at);  // into the slots that have just been read
     if (mx > m) {
       S *= ex2(shift_of(m, mx, p.T.sc));

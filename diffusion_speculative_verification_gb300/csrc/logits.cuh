@@ -92,9 +92,9 @@ __device__ __forceinline__ float2 pair_of(const uint4& r, int i) {
 template <typename T>
 __device__ __forceinline__ uint32_t none_bits() { return sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u; }  // -inf
 
-// largest number of kBatch vectors, -inf where there is none (NaN are passed over)
+// largest of the even and of the odd elements of kBatch vectors, -inf where there is none (NaN are passed over)
 template <typename T>
-__device__ __forceinline__ float step_max(const uint4 (&x)[kBatch]) {
+__device__ __forceinline__ float2 step_max(const uint4 (&x)[kBatch]) {
   if constexpr (sizeof(T) == 2) {
     __nv_bfloat162 h[4 * kBatch];
 #pragma unroll
@@ -107,13 +107,14 @@ __device__ __forceinline__ float step_max(const uint4 (&x)[kBatch]) {
     for (int s = 2 * kBatch; s > 0; s >>= 1)
 #pragma unroll
       for (int i = 0; i < s; ++i) h[i] = __hmax2(h[i], h[i + s]);
-    return fmaxf(-INFINITY, fmaxf(__low2float(h[0]), __high2float(h[0])));
+    return make_float2(fmaxf(-INFINITY, __low2float(h[0])), fmaxf(-INFINITY, __high2float(h[0])));
   } else {
-    float m = -INFINITY;
+    float2 m = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(x[u].x), __uint_as_float(x[u].y))),
-                fmaxf(__uint_as_float(x[u].z), __uint_as_float(x[u].w)));
+    for (int u = 0; u < kBatch; ++u) {
+      m.x = fmaxf(m.x, fmaxf(__uint_as_float(x[u].x), __uint_as_float(x[u].z)));
+      m.y = fmaxf(m.y, fmaxf(__uint_as_float(x[u].y), __uint_as_float(x[u].w)));
+    }
     return m;
   }
 }

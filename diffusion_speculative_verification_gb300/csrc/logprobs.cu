@@ -15,7 +15,8 @@
 //
 // Top alternatives.  The K-th largest of any K or more elements bounds the row's
 // K-th from below.  Each warp gives the j largest of its lanes' maxima, j so that
-// the cluster's warps give about 2 K; with the K-th of these as threshold, batches
+// the cluster's warps give about 2 K (where lanes are fewer, the maxima of their
+// even and odd elements); with the K-th of these as threshold, batches
 // whose maximum (kept in shared memory, rounded up to bf16) passes it are listed,
 // read again from L2, one per thread, and their elements that pass it, hardly
 // more than K, go to the cluster's first CTA as keys (order of the value above
@@ -32,8 +33,9 @@ namespace {
 
 constexpr int kStages = 2;                                  // steps in flight
 constexpr int kList = 512;                                  // keys that a list holds
-constexpr int kPool = 2 * kLogitsMaxTop + 8 * kMaxCluster;  // values of the pool at most: 2 K, and one of each warp
-constexpr int kParts = 8 * kMaxCluster;                     // warps of a cluster
+constexpr int kThreads = 128;                               // most threads of a CTA
+constexpr int kPool = 2 * kLogitsMaxTop + 4 * kMaxCluster + 4;  // values of the pool: 2 K, one of each warp, and a rest
+constexpr int kParts = 4 * kMaxCluster;                     // warps of a cluster: one lane each joins them
 
 struct LogprobsParams {
   const void* logits;
@@ -50,7 +52,7 @@ struct LogprobsParams {
   int32_t* top_token;
   int32_t* dev_status;
   int log_c, log_nt;
-  int give;  // lane maxima that a warp gives to the pool
+  int give;  // maxima that a warp gives to the pool; 32: of all lanes, 64: of all lanes' even and odd elements
 };
 
 // bytes of the ring, in which the lists have room
@@ -63,9 +65,9 @@ struct Shared {
   uint32_t part[kParts][4];   // of every warp: maximum, S, W, elements before the token
   int groups, count, total;   // batches and keys listed here, keys sent to the cluster's first CTA
   int at;
-  float least;
-  int sum[8];
-  uint32_t pool[kPool];       // order of the largest lane maxima of every warp of the cluster, 0: none
+  uint32_t least[kThreads / 32];
+  int sum[kThreads / 32];
+  alignas(16) uint32_t pool[kPool];  // order of the largest lane maxima of every warp of the cluster, 0: none
 };
 
 // What the ring's memory holds after the pass.
@@ -101,24 +103,36 @@ struct Given {
     below = (int)((b & ~sign) == 0 ? sign | 1u : (b & sign) ? b + 1 : b - 1);
   }
 
-  // Elements of vector i that are before the token.  lt is above -inf.
-  __device__ __forceinline__ int before(const uint4& r, int i, const RowView<T>& row) const {
-    if (i == own) return among(r, row.first(i));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    int n = 0;
-    if (sizeof(T) == 2) {
+  // Elements of a step's vectors, i and every NT-th behind it up to `end`, that are before the token; vectors from
+  // there on are -inf.
+  __device__ __forceinline__ int before(const uint4 (&x)[kBatch], int i, int NT, int end, const RowView<T>& row) const {
+    if (lt == -INFINITY || (i <= own && own <= i + NT * (kBatch - 1))) {
+      int n = 0;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i + NT * u < end) n += among(x[u], row.first(i + NT * u));
+      return n;
+    }
+    if constexpr (sizeof(T) == 2) {
       const uint32_t b = i < own ? (uint32_t)below : __float_as_uint(lt) >> 16, both = b << 16 | b;
       const __nv_bfloat162 than = *reinterpret_cast<const __nv_bfloat162*>(&both);
-      __nv_bfloat162 c = __floats2bfloat162_rn(0.f, 0.f);
+      __nv_bfloat162 c = __floats2bfloat162_rn(0.f, 0.f);  // counts up to 16 are exact
 #pragma unroll
-      for (int k = 0; k < 4; ++k) c = __hadd2(c, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), than));
-      n = (int)(__low2float(c) + __high2float(c));
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c = __hadd2(c, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), than));
+      }
+      return (int)(__low2float(c) + __high2float(c));
     } else {
       const float than = i < own ? __uint_as_float((uint32_t)below) : lt;
+      int n = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) n += __uint_as_float(w[k]) > than ? 1 : 0;
+      for (int u = 0; u < kBatch; ++u)
+        n += (__uint_as_float(x[u].x) > than ? 1 : 0) + (__uint_as_float(x[u].y) > than ? 1 : 0) +
+             (__uint_as_float(x[u].z) > than ? 1 : 0) + (__uint_as_float(x[u].w) > than ? 1 : 0);
+      return n;
     }
-    return n;
   }
 
   // The same, element by element, for the token's own vector and for tokens at -inf.
@@ -196,7 +210,7 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p) {
+__global__ void __launch_bounds__(kThreads, 7) logprobs_kernel(const LogprobsParams p) {
   extern __shared__ __align__(128) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
@@ -204,11 +218,11 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
   const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
   Lists& lists = *reinterpret_cast<Lists*>(dynamic);
   __nv_bfloat16* tops = reinterpret_cast<__nv_bfloat16*>(dynamic + ring_bytes(NT));
+  if (TOP && tid < 4) sm.pool[(nw * p.give << p.log_c & ~3) + tid] = 0u;  // behind the last; the pool may write over it
   if (tid == 0) {
     sm.groups = 0;
     sm.count = 0;
     sm.total = 0;
-    sm.least = -INFINITY;
   }
   __syncthreads();
   if (c > 1) cluster_arrive();  // waited for before the first access to another CTA's shared memory
@@ -249,22 +263,23 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
 
   // ------------------------------------------------------------ the pass
   float m = -INFINITY, S = 0.f, W = 0.f;
+  float even = -INFINITY, odd = -INFINITY;  // m by elements
   int before = 0;
   const float2 sc2 = make_float2(p.T.sc, p.T.sc);
   auto step = [&](auto is_full, int k) {
     constexpr bool FULL = decltype(is_full)::value;
     uint4 x[kBatch];
     part.template take<FULL>(k, slots(k), x);
-    const float mx = step_max<T>(x);
+    const float2 mx2 = step_max<T>(x);
+    const float mx = fmaxf(mx2.x, mx2.y);
+    if (TOP) {
+      even = fmaxf(even, mx2.x);
+      odd = fmaxf(odd, mx2.y);
+    }
     part.fetch(row, k + kStages, slots(k));  // into the slots that have just been read
     if (TOP) tops[k * NT + tid] = __float2bfloat16_ru(mx);
     const int ib = i0 + tid + NT * kBatch * k;
-    if (mx >= lt) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (FULL || ib + NT * u < i1)
-          before += lt == -INFINITY ? given.among(x[u], row.first(ib + NT * u)) : given.before(x[u], ib + NT * u, row);
-    }
+    if (mx >= lt) before += given.before(x, ib, NT, i1, row);
     if (mx > m) {  // sums so far on the new scale
       const float d = shift_of(m, mx, p.T.sc), f = ex2(d);
       W = f * (W + d * S);
@@ -298,7 +313,6 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
   copy_wait<0>();
 
   // ------------------------------------------------------------ every warp's part, to every CTA that joins them
-  const int give_all = nw * p.give;  // values that a CTA gives to the pool
   {
     const float M = warp_max(m);
     const float d = shift_of(m, M, p.T.sc), f = ex2(d);
@@ -316,24 +330,28 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
       cluster_store(cluster_addr(&sm.part[me][lane & 3], lane >> 2), word);
     }
     if (TOP) {
-      // this warp's largest lane maxima
-      uint32_t b = order_bits(m);
-      for (int i = 0; i < p.give; ++i) {
-        uint32_t most = b;
-        int who = i;
-        if (p.give < 32) {
-          most = __reduce_max_sync(0xffffffffu, b);
-          who = __ffs(__ballot_sync(0xffffffffu, b == most)) - 1;
-        } else {
-          most = __shfl_sync(0xffffffffu, b, i);
-        }
-        if (lane == who) b = 0u;
+      auto give = [&](int i, uint32_t v) {  // by every lane
         uint32_t* to = &sm.pool[me * p.give + i];
         if (c == 1) {
-          if (lane == 0) *to = most;
+          if (lane == 0) *to = v;
         } else if (lane < c) {
-          cluster_store(cluster_addr(to, lane), most);
+          cluster_store(cluster_addr(to, lane), v);
         }
+      };
+      uint32_t b = order_bits(m);
+      if (p.give < 32) {  // the largest
+        for (int i = 0; i < p.give; ++i) {
+          const uint32_t most = __reduce_max_sync(0xffffffffu, b);
+          if (lane == __ffs(__ballot_sync(0xffffffffu, b == most)) - 1) b = 0u;
+          give(i, most);
+        }
+      } else {
+        const uint32_t e = order_bits(even), o = order_bits(odd);
+        if (c == 1) {
+          sm.pool[me * p.give + lane] = p.give == 32 ? b : e;
+          if (p.give == 64) sm.pool[me * p.give + 32 + lane] = o;
+        }
+        for (int i = 0; c > 1 && i < p.give; ++i) give(i, __shfl_sync(0xffffffffu, p.give == 32 ? b : i < 32 ? e : o, i & 31));
       }
     }
   }
@@ -347,23 +365,16 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
   float Mr, St, Wt;
   int nb;
   {
-    const int q0 = lane, q1 = lane + 32, n = c * nw;
-    const float m0 = q0 < n ? __uint_as_float(sm.part[q0][0]) : -INFINITY;
-    const float m1 = q1 < n ? __uint_as_float(sm.part[q1][0]) : -INFINITY;
-    Mr = warp_max(fmaxf(m0, m1));
+    const bool there = lane < c * nw;
+    const float ml = there ? __uint_as_float(sm.part[lane][0]) : -INFINITY;
+    Mr = warp_max(ml);
     float s = 0.f, w = 0.f;
     nb = 0;
-    if (q0 < n) {
-      const float d = shift_of(m0, Mr, p.T.sc), f = ex2(d), S0 = __uint_as_float(sm.part[q0][1]);
-      s = f * S0;
-      w = f * (__uint_as_float(sm.part[q0][2]) + d * S0);
-      nb = (int)sm.part[q0][3];
-    }
-    if (q1 < n) {
-      const float d = shift_of(m1, Mr, p.T.sc), f = ex2(d), S1 = __uint_as_float(sm.part[q1][1]);
-      s += f * S1;
-      w += f * (__uint_as_float(sm.part[q1][2]) + d * S1);
-      nb += (int)sm.part[q1][3];
+    if (there) {
+      const float d = shift_of(ml, Mr, p.T.sc), f = ex2(d), Sl = __uint_as_float(sm.part[lane][1]);
+      s = f * Sl;
+      w = f * (__uint_as_float(sm.part[lane][2]) + d * Sl);
+      nb = (int)sm.part[lane][3];
     }
     St = warp_sum(s);
     Wt = warp_sum(w);
@@ -383,20 +394,24 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
 
   // ------------------------------------------------------------ alternatives
   if (TOP) {
-    // the K-th of the pool: every value's place in it
-    const int pooled = c * give_all;
+    // the K-th of the pool: the least value that fewer than K exceed
+    const int pooled = c * nw * p.give;
+    uint32_t mine_least = 0xFFFFFFFFu;
     for (int i = tid; i < pooled; i += NT) {
       const uint32_t v = sm.pool[i];
-      int place = 0;
-#pragma unroll 4
-      for (int j = 0; j < pooled; ++j) {
-        const uint32_t o = sm.pool[j];
-        place += (o > v || (o == v && j < i)) ? 1 : 0;
+      int above = 0;
+      for (int j = 0; j < pooled; j += 4) {  // a multiple of four, or 0 behind the last
+        const uint4 o = *reinterpret_cast<const uint4*>(&sm.pool[j]);
+        above += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
       }
-      if (place == p.K - 1 && v) sm.least = from_order(v);
+      if (above < p.K) mine_least = min(mine_least, v);
     }
+    mine_least = __reduce_min_sync(0xffffffffu, mine_least);
+    if (lane == 0) sm.least[warp] = mine_least;
     __syncthreads();
-    const float least = sm.least;
+    for (int w = 0; w < nw; ++w) mine_least = min(mine_least, sm.least[w]);
+    // fewer values than K bound nothing (0: a lane without elements)
+    const float least = pooled < p.K || mine_least == 0u ? -INFINITY : from_order(mine_least);
     // batches that reach it
     if (m >= least && m > -INFINITY)
       for (int k = 0; k < steps; ++k) {
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(256, 4) logprobs_kernel(const LogprobsParams p
     for (int i = tid; i < n; i += NT) {
       const unsigned long long mine_key = lists.merged[i];
       int place = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < n; ++j) place += lists.merged[j] > mine_key ? 1 : 0;
       if (place < p.K) {
         const float x = from_order((uint32_t)(mine_key >> 32));
@@ -469,12 +484,13 @@ cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, 
   return e != cudaSuccess ? e : launch_rows(logprobs_kernel<T, TOP>, n, sp, sp.threads, smem, st, p);
 }
 
-// CTAs per row: as many as SMs have room for at once (four each), while a CTA has more than two batches.
-RowSplit logprobs_split(int rows, int V, int element_size) {
-  const int vectors = row_vectors(V, element_size);
+// CTAs per row: more of them while they leave SMs without work and a CTA has more than two steps.
+RowSplit logprobs_split(int rows, int V, int element_size, int top_k) {
+  // alternatives are ranked by every thread: none of them less for a short row
+  const int vectors = std::max(row_vectors(V, element_size), top_k > 0 ? kThreads : 1);
   int c = 1;
-  while (c < kMaxCluster && (long long)rows * c * 2 <= 608 && vectors > 4 * c * 256) c *= 2;
-  return split_of(vectors, c, 256);
+  while (c < kMaxCluster && (long long)rows * c * 2 <= 456 && vectors > 2 * c * kThreads * kBatch) c *= 2;
+  return split_of(vectors, c, kThreads);
 }
 
 }  // namespace
@@ -508,11 +524,13 @@ extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
   p.top_logprob = a->top_logprob;
   p.top_token = a->top_token;
   p.dev_status = a->dev_status;
-  const RowSplit sp = logprobs_split(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4);
+  const RowSplit sp = logprobs_split(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4, a->top_k);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
   const int warps = sp.ctas * (sp.threads / 32);
-  p.give = std::min(32, (2 * a->top_k + warps - 1) / warps);
+  p.give = (2 * a->top_k + warps - 1) / warps;
+  // fewer lanes with elements than that: even and odd elements apart (four warps at most, so that the pool holds them)
+  if (p.give > 32 || (warps <= 4 && row_vectors(a->V, a->dtype == SSV_BF16 ? 2 : 4) < 2 * a->top_k)) p.give = 64;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   cudaError_t e;

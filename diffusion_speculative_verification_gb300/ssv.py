@@ -875,25 +875,25 @@ def logprobs(logits, tokens=None, top_k: int = 0, T: float = 1.0, rows=None, out
     if top_k < 0:
         raise SsvError(SSV_ERR_INVALID, f"{what}: top_k")
     if out is None:
+        dev = logits.device
+        lp = rank = tl = tt = None
         with _on(stream):
-            # one allocation: four values per entry, then its alternatives
-            buf = torch.empty(n * (4 + 2 * top_k), dtype=f32, device=logits.device)
-        at, nk = buf.data_ptr(), n * top_k
-        lp, rank, ent, lse, tl, tt = buf.split_with_sizes([n, n, n, n, nk, nk])
-        out = (lp, rank.view(i32), ent, lse, tl.view(n, top_k), tt.view(i32).view(n, top_k))
-        ptrs = [at, at + 4 * n, at + 8 * n, at + 12 * n, at + 16 * n, at + 16 * n + 4 * nk]
-        if tokens is None:
-            out, ptrs[0], ptrs[1] = (None, None) + out[2:], 0, 0
-        if not top_k:
-            out, ptrs[4], ptrs[5] = out[:4] + (None, None), 0, 0
+            if tokens is None:
+                ent, lse = torch.empty((2, n), dtype=f32, device=dev).unbind()
+            else:
+                lp, ent, lse = torch.empty((3, n), dtype=f32, device=dev).unbind()
+                rank = torch.empty(n, dtype=i32, device=dev)
+            if top_k:
+                tl = torch.empty((n, top_k), dtype=f32, device=dev)
+                tt = torch.empty((n, top_k), dtype=i32, device=dev)
+        out = (lp, rank, ent, lse, tl, tt)
     else:
         _like(what, (n,), f32, out[0], out[2], out[3])
         _like(what, (n,), i32, out[1])
         _like(what, (n, top_k), f32, out[4])
         _like(what, (n, top_k), i32, out[5])
-        ptrs = [_addr(t) for t in out]
     a = _pack_logprobs(logits.data_ptr(), stride, dt, logits.shape[1], logits.shape[0], _addr(rows), _addr(tokens), n,
-                       top_k, T, *ptrs, _addr(dev_status))
+                       top_k, T, *map(_addr, out), _addr(dev_status))
     _launch(what, (logits, rows, tokens, dev_status) + out, a, stream)
     return out
 

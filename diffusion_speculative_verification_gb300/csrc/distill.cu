@@ -60,7 +60,8 @@ struct Target {
   float p[kLogitsMaxTop], t[kLogitsMaxTop], z[kLogitsMaxTop];
   int hash[kHash];
   Mass mass;
-  float top, sum;  // largest of z, sum of exp((z - top) / T)
+  float top;  // largest of z
+  Pair sum;   // sum of exp((z - top) / T)
 };
 
 // One warp brings a row's target, four entries per lane (j = lane + 32 k), while the others are busy with the row.
@@ -114,7 +115,8 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   twice = __any_sync(0xffffffffu, twice);
   // probabilities: relative to the largest for a softmax; as they are where they are log-probabilities
   const bool as_is = p.mode == SSV_DISTILL_REST;
-  float mx = -INFINITY, s = 0.f, e[kEach];
+  float mx = -INFINITY, e[kEach];
+  Pair all = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < kEach; ++k) mx = fmaxf(mx, l.t[k]);
   mx = warp_max(mx);
@@ -122,9 +124,10 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     e[k] = 32 * k < p.K ? expf(l.t[k] - ref) : 0.f;
-    s += e[k];
+    all = all + Pair{e[k], 0.f};
   }
-  s = warp_sum(s);
+  all = warp_sum(all);
+  const float s = value_of(all);
   const float norm = as_is || s == 0.f ? 1.f : s, ln = logf(norm);
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
@@ -160,7 +163,8 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
     }
     __syncwarp();
   }
-  float top = -INFINITY, sum = 0.f;
+  float top = -INFINITY;
+  Pair sum = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const int j = lane + 32 * k;
@@ -173,12 +177,16 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   top = warp_max(top);
   const float zero = top == -INFINITY ? 0.f : top;  // -inf counts nothing, NaN stays
 #pragma unroll
-  for (int k = 0; k < kEach; ++k)
-    if (32 * k < p.K) sum += ex2((z[k] - zero) * p.T.sc);
+  for (int k = 0; k < kEach; ++k) {
+    if (32 * k >= p.K) break;
+    const Pair x = two_sum(z[k], -zero) * Pair{p.T.hi, p.T.lo};
+    const float e1 = expf(x.hi);
+    sum = sum + Pair{e1, e1 > 0.f ? e1 * x.lo : 0.f};  // -inf has no low part; NaN stays
+  }
   sum = warp_sum(sum);
   if (lane == 0) {
     tg.mass.sum = as_is || s == 0.f || s != s ? s : 1.f;
-    tg.mass.rest = as_is ? (s > 1.f ? 0.f : 1.f - s) : 0.f;  // NaN stays
+    tg.mass.rest = as_is ? (s > 1.f ? 0.f : value_of(Pair{1.f, 0.f} + -all)) : 0.f;  // NaN stays
     tg.top = top;
     tg.sum = sum;
   }
@@ -189,15 +197,27 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
 __device__ __forceinline__ float rest_of(const Mass& t, bool none) { return none && t.rest < 0x1p-20f ? 0.f : t.rest; }
 
 // What a row's softmax needs: maximum and sum, relative to it, over the row and over the tokens that are not listed.
+// (The sums are of 32 bits, joined in 48: the last few additions would cost a loss, which is a small difference of
+// their logarithms, as much as all before.)
 struct Sums {
   float m, S, mr, Sr;
+  Pair ln, ln_r;  // logarithms of S and Sr
+
+  __device__ __forceinline__ void set(float m_, Pair S_, float mr_, Pair Sr_) {
+    m = m_;
+    S = value_of(S_);
+    mr = mr_;
+    Sr = value_of(Sr_);
+    ln = log_sum(S_);
+    ln_r = log_sum(Sr_);
+  }
 
   __device__ __forceinline__ bool none() const { return mr == -INFINITY && Sr == 0.f; }  // nothing is left to the others
   __device__ __forceinline__ bool empty() const { return none() && S == 0.f; }           // the row is all -inf
   // ln of the others' share
   __device__ __forceinline__ Pair ln_u(const Scale& T) const {
     if (none()) return {-INFINITY, 0.f};
-    return two_sum(mr, -m) * Pair{T.hi, T.lo} + (log_sum(Sr) + -log_sum(S));
+    return two_sum(mr, -m) * Pair{T.hi, T.lo} + (ln_r + -ln);
   }
 };
 
@@ -337,7 +357,7 @@ __device__ __forceinline__ void write_zeros(const PartView<T>& part, T* out) {
 struct Shared {
   Target tg;
   Slope slope;
-  uint32_t part[kParts][2];  // of every warp: maximum and sum of its other tokens
+  uint32_t part[kParts][4];  // of every warp: maximum and sum (a pair) of its other tokens
 };
 
 // Steps in flight: three with the gradient, which keep the last 30% of a long row for it.
@@ -397,7 +417,7 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
 
   // ------------------------------------------------------------ the other tokens
   float m = -INFINITY, S = 0.f;
-  const float2 sc2 = make_float2(p.T.sc, p.T.sc);
+  const float2 sc2 = make_float2(p.T.down, p.T.down), lo2 = make_float2(p.T.rest, p.T.rest);
   auto step = [&](auto is_full, int k) {
     constexpr bool FULL = decltype(is_full)::value;
     uint4* at = step_slots(k);
@@ -423,7 +443,8 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
       if (!FULL && part.i0 + tid + NT * (kBatch * k + u) >= part.i1) break;
 #pragma unroll
       for (int i = 0; i < kVec<T> / 2; ++i) {
-        const float2 y = mul2(add2(pair_of<T>(x[u], i), nm), sc2);
+        // the scale to 48 bits: rounded to 24 it would move every term the same way, by up to 2^-25 of its exponent
+        const float2 d = add2(pair_of<T>(x[u], i), nm), y = fma2(d, lo2, mul2(d, sc2));
         S2 = add2(S2, make_float2(ex2(y.x), ex2(y.y)));
       }
     }
@@ -440,13 +461,14 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
   }
   if (c > 1) cluster_wait();
   if (streams) {
-    const float M = warp_max(m), Sw = warp_sum(ex2(shift_of(m, M, p.T.sc)) * S);
+    const float M = warp_max(m);
+    const Pair Sw = warp_sum(Pair{ex2(shift_of(m, M, p.T.sc)) * S, 0.f});
     const int me = rank * nw + warp;
-    const uint32_t word = lane & 1 ? __float_as_uint(Sw) : __float_as_uint(M);
+    const uint32_t word = (lane & 3) == 0 ? __float_as_uint(M) : __float_as_uint((lane & 3) == 1 ? Sw.hi : Sw.lo);
     if (c == 1) {
-      if (lane < 2) sm.part[me][lane] = word;
-    } else if (lane < 2 * (GRAD ? c : 1)) {  // the loss alone is the first CTA's
-      cluster_store(cluster_addr(&sm.part[me][lane & 1], lane >> 1), word);
+      if (lane < 3) sm.part[me][lane] = word;
+    } else if (lane < 4 * (GRAD ? c : 1)) {  // the loss alone is the first CTA's
+      cluster_store(cluster_addr(&sm.part[me][lane & 3], lane >> 2), word);
     }
   }
   if (c > 1) {
@@ -460,23 +482,30 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
 
   // ------------------------------------------------------------ the row's sums, by one warp of each CTA in the same order
   Sums sums;
+  float listed_share = 0.f;  // 1 - u
   if (!streams) {
     const int n = c * nw;
-    float mx = -INFINITY, s = 0.f;
+    float mx = -INFINITY;
     for (int q = lane; q < n; q += 32) mx = fmaxf(mx, __uint_as_float(sm.part[q][0]));
-    sums.mr = warp_max(mx);
-    for (int q = lane; q < n; q += 32)
-      s += ex2(shift_of(__uint_as_float(sm.part[q][0]), sums.mr, p.T.sc)) * __uint_as_float(sm.part[q][1]);
-    sums.Sr = warp_sum(s);
-    sums.m = fmaxf(sums.mr, tg.top);
-    sums.S = ex2(shift_of(sums.mr, sums.m, p.T.sc)) * sums.Sr + ex2(shift_of(tg.top, sums.m, p.T.sc)) * tg.sum;
+    mx = warp_max(mx);
+    Pair s = {0.f, 0.f};
+    for (int q = lane; q < n; q += 32) {
+      const float f = ex2(shift_of(__uint_as_float(sm.part[q][0]), mx, p.T.sc));
+      s = s + Pair{f * __uint_as_float(sm.part[q][1]), f * __uint_as_float(sm.part[q][2])};
+    }
+    s = warp_sum(s);
+    const float m_all = fmaxf(mx, tg.top);
+    const float fr = ex2(shift_of(mx, m_all, p.T.sc)), ft = ex2(shift_of(tg.top, m_all, p.T.sc));
+    const Pair st = {ft * tg.sum.hi, ft * tg.sum.lo};
+    sums.set(m_all, Pair{fr * s.hi, fr * s.lo} + st, mx, s);
+    listed_share = value_of(st) / sums.S;
     if (GRAD) {
       if (lane == 0) sm.slope = slope_of(sums, tg.mass, p.T, w);
     }
   }
   if (GRAD) __syncthreads();
   if (rank == 0 && !streams) {
-    const Pair lnS = log_sum(sums.S), inv = {p.T.hi, p.T.lo};
+    const Pair inv = {p.T.hi, p.T.lo};
     Pair loss = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
@@ -484,16 +513,16 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
       const float pj = j < p.K ? tg.p[j] : 0.f;
       if (pj > 0.f || pj != pj) {
         // ln p - ln q, a small difference of large numbers: rounded once
-        const Pair q = two_sum(tg.z[j], -sums.m) * inv + -lnS;
+        const Pair q = two_sum(tg.z[j], -sums.m) * inv + -sums.ln;
         loss = loss + Pair{pj, 0.f} * Pair{value_of(Pair{tg.t[j], 0.f} + -q), 0.f};
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      loss = loss + Pair{__shfl_xor_sync(0xffffffffu, loss.hi, o), __shfl_xor_sync(0xffffffffu, loss.lo, o)};
+    loss = warp_sum(loss);
     if (lane == 0) {
       const float rest = rest_of(tg.mass, sums.none()), P = tg.mass.sum + rest;
-      if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(Pair{logf(rest), 0.f} + -sums.ln_u(p.T)), 0.f};
+      // a share of more than half from what is listed: the difference of two logarithms would be off by their rounding
+      const Pair ln_u = listed_share < 0.5f ? Pair{log1pf(-listed_share), 0.f} : sums.ln_u(p.T);
+      if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(Pair{logf(rest), 0.f} + -ln_u), 0.f};
       float l = w * value_of(loss);
       if (sums.S != sums.S) l = sums.S;
       if (sums.empty()) l = P == 0.f ? 0.f : w * INFINITY;  // no token of the target has a chance
@@ -553,7 +582,8 @@ __global__ void __launch_bounds__(128, 8) distill_backward_kernel(const DistillP
     Listed mine;
     mine.load(p, entry);
     const float* from = p.stats_in + 4 * (size_t)entry;
-    const Sums sums = {from[0], from[1], from[2], from[3]};
+    Sums sums;
+    sums.set(from[0], Pair{from[1], 0.f}, from[2], Pair{from[3], 0.f});
     const float up = p.grad_loss ? p.grad_loss[entry] : 1.f;
     mine.check(p, rank == 0);
     weigh_listed<T>(p, mine, row.row, part.lo, part.hi, tg);

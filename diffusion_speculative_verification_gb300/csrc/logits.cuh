@@ -298,6 +298,13 @@ __device__ __forceinline__ Pair operator*(Pair a, Pair b) {
 // rounded once; infinities and NaN as the leading part has them
 __device__ __forceinline__ float value_of(Pair a) { return fabsf(a.hi) < INFINITY ? a.hi + a.lo : a.hi; }
 
+__device__ __forceinline__ Pair warp_sum(Pair x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x = x + Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+  return x;
+}
+
 // ln S of a sum: the exponent apart, so that only the mantissa's logarithm is rounded to 32 bits
 __device__ __forceinline__ Pair log_sum(float s) {
   if (!(s > 0.f) || isinf(s)) return {logf(s), 0.f};
@@ -306,6 +313,12 @@ __device__ __forceinline__ Pair log_sum(float s) {
   // ln 2 = 355 / 512 - 2.1219444005469058e-4; e * 355 / 512 is exact
   const Pair y = two_sum((float)e * 0.693359375f, logf(f));
   return {y.hi, y.lo + (float)e * -2.1219444005469058e-4f};
+}
+
+__device__ __forceinline__ Pair log_sum(Pair s) {
+  const float v = value_of(s);
+  const Pair y = log_sum(v);
+  return v > 0.f && v < INFINITY ? Pair{y.hi, y.lo + ((s.hi - v) + s.lo) / v} : y;
 }
 
 // 2^y on the scale of exp2 for partial sums: f = 2^((from - to) sc); 0 where `from` is -inf
@@ -374,8 +387,10 @@ inline RowSplit split_of(int vectors, int c, int most_threads) {
 
 // T as the kernels take it
 struct Scale {
-  float sc;          // log2(e) / T, of exponents
-  float hi, lo;      // 1 / T
+  float sc;      // log2(e) / T, of exponents
+  float down;    // the same rounded down, and
+  float rest;    // what that leaves, above 0 (so that -inf times either is -inf)
+  float hi, lo;  // 1 / T to 48 bits
 };
 
 // false where T is not positive or the scale leaves the normal numbers
@@ -383,6 +398,9 @@ inline bool logits_scale(float T, Scale* s) {
   if (!isfinite(T) || !(T > 0.f)) return false;
   const double inv = 1.0 / (double)T;
   s->sc = (float)(1.4426950408889634 * inv);
+  const double exact = 1.4426950408889634 * inv;
+  s->down = (double)s->sc > exact ? nextafterf(s->sc, 0.f) : s->sc;
+  s->rest = fmaxf((float)(exact - (double)s->down), FLT_MIN);
   s->hi = (float)inv;
   s->lo = (float)(inv - (double)s->hi);
   return isfinite(s->sc) && s->sc >= FLT_MIN && s->hi >= FLT_MIN;

@@ -149,6 +149,17 @@ def test_large_vocabularies(v, n, K, dtype, mode):
     check(*make(r, n, v, K, T=2.0, absent=0.1), dtype, mode, T=2.0)
 
 
+@pytest.mark.parametrize("T", [0.3, 0.7, 1.1, 1.5, 3.0, 50.0])
+def test_temperatures(T):
+    """Scales that are rounded up and down, beside the -inf around a row and in it."""
+    r = np.random.default_rng(33)
+    for v in (50, 3001):
+        z, token, value = make(r, 3, v, 9, T)
+        z[1, v // 2] = -np.inf
+        for dtype in (W.F32, W.BF16):
+            check(z, token, value, dtype, ssv.REST, T=T, lead=3, pad=2)
+
+
 @pytest.mark.parametrize("n", [700, 1300])
 def test_many_rows(n):
     r = np.random.default_rng(n)

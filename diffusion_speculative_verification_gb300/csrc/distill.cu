@@ -90,7 +90,8 @@ struct Listed {
 };
 
 // The warp's entries to shared memory: `row` their logits, those of [lo, hi) alone (the others are not asked for).
-template <typename T>
+// LOSS: with what a loss needs, the rest to more than 32 bits and the sum over the listed tokens.
+template <bool LOSS, typename T>
 __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, const T* row, int lo, int hi, Target& tg) {
   const int lane = threadIdx.x & 31;
   float z[kEach];
@@ -123,12 +124,16 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   const float ref = as_is || mx == -INFINITY ? 0.f : mx;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    e[k] = 32 * k < p.K ? expf(l.t[k] - ref) : 0.f;
-    all = all + Pair{e[k], 0.f};
+    e[k] = 0.f;
+    if (32 * k >= p.K) continue;
+    e[k] = expf(l.t[k] - ref);
+    // what an exponential rounded to 32 bits is off by, from its logarithm: the rest is what the sum leaves of 1
+    const float off = LOSS && as_is && e[k] > 0.f ? e[k] * value_of(Pair{l.t[k], 0.f} + -log_sum(e[k])) : 0.f;
+    all = all + Pair{e[k], off};
   }
   all = warp_sum(all);
   const float s = value_of(all);
-  const float norm = as_is || s == 0.f ? 1.f : s, ln = logf(norm);
+  const float norm = as_is || s == 0.f ? 1.f : s, ln = as_is || s == 0.f ? 0.f : value_of(log_sum(all));
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     if (32 * k >= p.K) break;
@@ -175,15 +180,17 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
     top = fmaxf(top, z[k]);
   }
   top = warp_max(top);
-  const float zero = top == -INFINITY ? 0.f : top;  // -inf counts nothing, NaN stays
+  if (LOSS) {
+    const float zero = top == -INFINITY ? 0.f : top;  // -inf counts nothing, NaN stays
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    if (32 * k >= p.K) break;
-    const Pair x = two_sum(z[k], -zero) * Pair{p.T.hi, p.T.lo};
-    const float e1 = expf(x.hi);
-    sum = sum + Pair{e1, e1 > 0.f ? e1 * x.lo : 0.f};  // -inf has no low part; NaN stays
+    for (int k = 0; k < kEach; ++k) {
+      if (32 * k >= p.K) break;
+      const Pair x = two_sum(z[k], -zero) * Pair{p.T.hi, p.T.lo};
+      const float e1 = expf(x.hi);
+      sum = sum + Pair{e1, e1 > 0.f ? e1 * x.lo : 0.f};  // -inf has no low part; NaN stays
+    }
+    sum = warp_sum(sum);
   }
-  sum = warp_sum(sum);
   if (lane == 0) {
     tg.mass.sum = as_is || s == 0.f || s != s ? s : 1.f;
     tg.mass.rest = as_is ? (s > 1.f ? 0.f : value_of(Pair{1.f, 0.f} + -all)) : 0.f;  // NaN stays
@@ -197,28 +204,11 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
 __device__ __forceinline__ float rest_of(const Mass& t, bool none) { return none && t.rest < 0x1p-20f ? 0.f : t.rest; }
 
 // What a row's softmax needs: maximum and sum, relative to it, over the row and over the tokens that are not listed.
-// (The sums are of 32 bits, joined in 48: the last few additions would cost a loss, which is a small difference of
-// their logarithms, as much as all before.)
 struct Sums {
   float m, S, mr, Sr;
-  Pair ln, ln_r;  // logarithms of S and Sr
-
-  __device__ __forceinline__ void set(float m_, Pair S_, float mr_, Pair Sr_) {
-    m = m_;
-    S = value_of(S_);
-    mr = mr_;
-    Sr = value_of(Sr_);
-    ln = log_sum(S_);
-    ln_r = log_sum(Sr_);
-  }
 
   __device__ __forceinline__ bool none() const { return mr == -INFINITY && Sr == 0.f; }  // nothing is left to the others
   __device__ __forceinline__ bool empty() const { return none() && S == 0.f; }           // the row is all -inf
-  // ln of the others' share
-  __device__ __forceinline__ Pair ln_u(const Scale& T) const {
-    if (none()) return {-INFINITY, 0.f};
-    return two_sum(mr, -m) * Pair{T.hi, T.lo} + (ln_r + -ln);
-  }
 };
 
 struct Slope {
@@ -233,7 +223,7 @@ __device__ __forceinline__ Slope slope_of(const Sums& s, const Mass& t, const Sc
   Slope k;
   k.wT = w * T.hi;
   k.ref = s.none() ? 0.f : s.mr;
-  k.coef = s.none() ? 0.f : k.wT * (P * expf(value_of(s.ln_u(T))) - rest) / s.Sr;
+  k.coef = s.none() ? 0.f : k.wT * (P * (expf((s.mr - s.m) * T.hi) * (s.Sr / s.S)) - rest) / s.Sr;
   k.top = s.m;
   k.share = P / s.S;
   k.empty = s.empty();
@@ -457,7 +447,7 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
     }
     copy_wait<0>();
   } else {
-    weigh_listed<T>(p, mine, row.row, 0, p.V, tg);
+    weigh_listed<true, T>(p, mine, row.row, 0, p.V, tg);
   }
   if (c > 1) cluster_wait();
   if (streams) {
@@ -481,23 +471,27 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
   if (!GRAD && streams) return;
 
   // ------------------------------------------------------------ the row's sums, by one warp of each CTA in the same order
+  // (The sums are of 32 bits, joined in 48: the last few additions would cost a loss, which is a small difference of
+  // their logarithms, as much as all before.)
   Sums sums;
+  Pair S_all, S_rest;
   float listed_share = 0.f;  // 1 - u
   if (!streams) {
     const int n = c * nw;
     float mx = -INFINITY;
     for (int q = lane; q < n; q += 32) mx = fmaxf(mx, __uint_as_float(sm.part[q][0]));
     mx = warp_max(mx);
-    Pair s = {0.f, 0.f};
+    S_rest = Pair{0.f, 0.f};
     for (int q = lane; q < n; q += 32) {
       const float f = ex2(shift_of(__uint_as_float(sm.part[q][0]), mx, p.T.sc));
-      s = s + Pair{f * __uint_as_float(sm.part[q][1]), f * __uint_as_float(sm.part[q][2])};
+      S_rest = S_rest + Pair{f * __uint_as_float(sm.part[q][1]), f * __uint_as_float(sm.part[q][2])};
     }
-    s = warp_sum(s);
+    S_rest = warp_sum(S_rest);
     const float m_all = fmaxf(mx, tg.top);
     const float fr = ex2(shift_of(mx, m_all, p.T.sc)), ft = ex2(shift_of(tg.top, m_all, p.T.sc));
     const Pair st = {ft * tg.sum.hi, ft * tg.sum.lo};
-    sums.set(m_all, Pair{fr * s.hi, fr * s.lo} + st, mx, s);
+    S_all = Pair{fr * S_rest.hi, fr * S_rest.lo} + st;
+    sums = {m_all, value_of(S_all), mx, value_of(S_rest)};
     listed_share = value_of(st) / sums.S;
     if (GRAD) {
       if (lane == 0) sm.slope = slope_of(sums, tg.mass, p.T, w);
@@ -505,7 +499,7 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
   }
   if (GRAD) __syncthreads();
   if (rank == 0 && !streams) {
-    const Pair inv = {p.T.hi, p.T.lo};
+    const Pair inv = {p.T.hi, p.T.lo}, lnS = log_sum(S_all);
     Pair loss = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
@@ -513,7 +507,7 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
       const float pj = j < p.K ? tg.p[j] : 0.f;
       if (pj > 0.f || pj != pj) {
         // ln p - ln q, a small difference of large numbers: rounded once
-        const Pair q = two_sum(tg.z[j], -sums.m) * inv + -sums.ln;
+        const Pair q = two_sum(tg.z[j], -sums.m) * inv + -lnS;
         loss = loss + Pair{pj, 0.f} * Pair{value_of(Pair{tg.t[j], 0.f} + -q), 0.f};
       }
     }
@@ -521,8 +515,10 @@ __global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const D
     if (lane == 0) {
       const float rest = rest_of(tg.mass, sums.none()), P = tg.mass.sum + rest;
       // a share of more than half from what is listed: the difference of two logarithms would be off by their rounding
-      const Pair ln_u = listed_share < 0.5f ? Pair{log1pf(-listed_share), 0.f} : sums.ln_u(p.T);
-      if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(Pair{logf(rest), 0.f} + -ln_u), 0.f};
+      const Pair ln_u = listed_share < 0.5f ? Pair{log1pf(-listed_share), 0.f}
+                        : sums.none()       ? Pair{-INFINITY, 0.f}
+                                            : two_sum(sums.mr, -sums.m) * inv + (log_sum(S_rest) + -lnS);
+      if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(log_sum(rest) + -ln_u), 0.f};
       float l = w * value_of(loss);
       if (sums.S != sums.S) l = sums.S;
       if (sums.empty()) l = P == 0.f ? 0.f : w * INFINITY;  // no token of the target has a chance
@@ -582,11 +578,10 @@ __global__ void __launch_bounds__(128, 8) distill_backward_kernel(const DistillP
     Listed mine;
     mine.load(p, entry);
     const float* from = p.stats_in + 4 * (size_t)entry;
-    Sums sums;
-    sums.set(from[0], Pair{from[1], 0.f}, from[2], Pair{from[3], 0.f});
+    const Sums sums = {from[0], from[1], from[2], from[3]};
     const float up = p.grad_loss ? p.grad_loss[entry] : 1.f;
     mine.check(p, rank == 0);
-    weigh_listed<T>(p, mine, row.row, part.lo, part.hi, tg);
+    weigh_listed<false, T>(p, mine, row.row, part.lo, part.hi, tg);
     __syncwarp();
     if (tid == 0) slope = slope_of(sums, tg.mass, p.T, w * up);
   }

@@ -305,14 +305,23 @@ __device__ __forceinline__ Pair warp_sum(Pair x) {
   return x;
 }
 
-// ln S of a sum: the exponent apart, so that only the mantissa's logarithm is rounded to 32 bits
+// ln s of a positive number to about 2^-30: s = 2^e f with f in [sqrt(1/2), sqrt(2)), and ln f = 2 atanh((f - 1) / (f + 1))
+// by its series, whose first term alone needs more than 32 bits
 __device__ __forceinline__ Pair log_sum(float s) {
   if (!(s > 0.f) || isinf(s)) return {logf(s), 0.f};
   int e;
-  const float f = frexpf(s, &e);
+  float f = frexpf(s, &e);
+  if (f < 0.70710678f) {
+    f *= 2.f;
+    --e;
+  }
+  const float a = f - 1.f;  // exact
+  const Pair b = two_sum(f, 1.f);
+  const float q = a / b.hi, low = (fmaf(-q, b.hi, a) - q * b.lo) / b.hi, z = q * q;
+  const float series = z * (1.f / 3 + z * (1.f / 5 + z * (1.f / 7 + z * (1.f / 9 + z * (1.f / 11)))));
   // ln 2 = 355 / 512 - 2.1219444005469058e-4; e * 355 / 512 is exact
-  const Pair y = two_sum((float)e * 0.693359375f, logf(f));
-  return {y.hi, y.lo + (float)e * -2.1219444005469058e-4f};
+  const Pair y = two_sum((float)e * 0.693359375f, 2.f * q);
+  return {y.hi, y.lo + (2.f * (low + q * series) + (float)e * -2.1219444005469058e-4f)};
 }
 
 __device__ __forceinline__ Pair log_sum(Pair s) {

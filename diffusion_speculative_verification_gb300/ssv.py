@@ -875,18 +875,13 @@ def logprobs(logits, tokens=None, top_k: int = 0, T: float = 1.0, rows=None, out
     if top_k < 0:
         raise SsvError(SSV_ERR_INVALID, f"{what}: top_k")
     if out is None:
-        dev = logits.device
-        lp = rank = tl = tt = None
+        dev, empty = logits.device, torch.empty
         with _on(stream):
-            if tokens is None:
-                ent, lse = torch.empty((2, n), dtype=f32, device=dev).unbind()
-            else:
-                lp, ent, lse = torch.empty((3, n), dtype=f32, device=dev).unbind()
-                rank = torch.empty(n, dtype=i32, device=dev)
-            if top_k:
-                tl = torch.empty((n, top_k), dtype=f32, device=dev)
-                tt = torch.empty((n, top_k), dtype=i32, device=dev)
-        out = (lp, rank, ent, lse, tl, tt)
+            out = (None if tokens is None else empty(n, dtype=f32, device=dev),
+                   None if tokens is None else empty(n, dtype=i32, device=dev),
+                   empty(n, dtype=f32, device=dev), empty(n, dtype=f32, device=dev),
+                   empty((n, top_k), dtype=f32, device=dev) if top_k else None,
+                   empty((n, top_k), dtype=i32, device=dev) if top_k else None)
     else:
         _like(what, (n,), f32, out[0], out[2], out[3])
         _like(what, (n,), i32, out[1])

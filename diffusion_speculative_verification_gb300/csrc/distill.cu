@@ -26,7 +26,8 @@
 namespace ssv {
 namespace {
 
-constexpr int kParts = kLogitsThreads / 32 * kMaxCluster;  // warps of a cluster
+constexpr int kThreads = 512;                  // most threads that share a row's part
+constexpr int kParts = kThreads / 32 * kMaxCluster;  // warps of a cluster
 constexpr int kHash = 2 * kLogitsMaxTop;       // places of the table in which repeated tokens meet
 constexpr int kEach = kLogitsMaxTop / 32;      // listed tokens of a lane
 
@@ -354,7 +355,7 @@ struct Shared {
 template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kLogitsThreads + 32, 2) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const DistillParams p) {
   // a ring of slots; behind it a word per thread and step, whose bit (vector of the step, element) says that the
   // element is a listed token
   extern __shared__ __align__(128) unsigned char dynamic[];
@@ -693,6 +694,12 @@ extern "C" ssv_status ssv_distill(const ssv_distill_args* a, void* stream) {
   if (s != SSV_OK) return s;
   if (a->n == 0) return SSV_OK;
   if (!a->loss || a->grad_loss) return SSV_ERR_INVALID;
+  const int es = a->dtype == SSV_BF16 ? 2 : 4;
+  if (meets_rows(a->loss, 4 * (size_t)a->n, a->logits, p.stride, a->V, a->n, es) ||
+      meets_rows(a->stats, 16 * (size_t)a->n, a->logits, p.stride, a->V, a->n, es) ||
+      (a->grad && (meets_rows(a->loss, 4 * (size_t)a->n, a->grad, p.grad_stride, a->V, a->n, es) ||
+                   meets_rows(a->stats, 16 * (size_t)a->n, a->grad, p.grad_stride, a->V, a->n, es))))
+    return SSV_ERR_INVALID;
   using bf16 = __nv_bfloat16;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -710,6 +717,8 @@ extern "C" ssv_status ssv_distill_backward(const ssv_distill_args* a, void* stre
   if (s != SSV_OK) return s;
   if (a->n == 0) return SSV_OK;
   if (!a->stats || !a->grad) return SSV_ERR_INVALID;
+  if (meets_rows(a->stats, 16 * (size_t)a->n, a->grad, p.grad_stride, a->V, a->n, a->dtype == SSV_BF16 ? 2 : 4))
+    return SSV_ERR_INVALID;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       a->dtype == SSV_BF16 ? backward_launch<__nv_bfloat16>(p, a->n, st) : backward_launch<float>(p, a->n, st);

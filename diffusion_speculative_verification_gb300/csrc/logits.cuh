@@ -8,11 +8,10 @@
 // first and the last lie inside the row and move as one access; the edges are read
 // element by element, and what they lack counts as -inf.
 //
-// A CTA has a range of a row's vectors.  Its threads take every NT-th, kBatch of
-// them at a time, and copy them to shared memory ahead of their use (cp.async,
-// each thread to slots that it reads itself, so that no barrier is needed):
-// either through a ring of kStages batches, for a range of any length, or all at
-// once into a buffer that a second pass reads again.
+// A CTA has a part of a row's vectors.  Its threads take every NT-th, kBatch of
+// them in a step, and copy them to shared memory ahead of their use (cp.async,
+// each thread to slots that it reads itself, so that no barrier is needed),
+// through a ring of a few steps or, a short part, all at once.
 #pragma once
 
 #include "ssv_internal.cuh"
@@ -22,9 +21,8 @@
 
 namespace ssv {
 
-constexpr int kLogitsThreads = 512;     // most threads of a CTA
-constexpr int kLogitsMaxVocab = 393216; // largest V: 8 CTAs of a cluster hold it in shared memory, as fp32
-constexpr int kLogitsMaxTop = 128;      // most alternatives of a row
+constexpr int kLogitsMaxVocab = 1 << 19;  // largest V
+constexpr int kLogitsMaxTop = 128;        // most alternatives of a row
 constexpr int kMaxCluster = 8;
 constexpr int kLogBatch = 2, kBatch = 1 << kLogBatch;  // vectors of a thread in one step
 constexpr int kStages = 2;              // steps in flight (ring)
@@ -361,6 +359,7 @@ inline cudaError_t allow_shared(K kernel, size_t bytes, uint64_t* done) {
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_rows(void (*kernel)(KArgs...), int rows, const RowSplit& sp, int threads, size_t smem,
                                cudaStream_t st, Args&&... args) {
+  if ((long long)rows * sp.ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * (unsigned)sp.ctas);
   cfg.blockDim = dim3(threads);
@@ -413,6 +412,12 @@ inline bool logits_scale(float T, Scale* s) {
   s->hi = (float)inv;
   s->lo = (float)(inv - (double)s->hi);
   return isfinite(s->sc) && s->sc >= FLT_MIN && s->hi >= FLT_MIN;
+}
+
+// whether `bytes` at p meet a [rows, V] matrix with `stride` elements between rows, gaps included
+inline bool meets_rows(const void* p, size_t bytes, const void* rows_at, int64_t stride, int V, int rows, int es) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(rows_at);
+  return p && bytes && rows > 0 && a < b + ((uintptr_t)(rows - 1) * stride + V) * es && b < a + bytes;
 }
 
 // [rows, V] with `stride` elements between rows

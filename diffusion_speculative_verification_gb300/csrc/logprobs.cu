@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 namespace ssv {
 namespace {
@@ -512,6 +513,12 @@ extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
   if (!a->logprob && !a->entropy && !a->lse && a->top_k == 0) return SSV_ERR_INVALID;
   p.logits = a->logits;
   p.stride = a->logits_stride ? a->logits_stride : a->V;
+  const size_t n4 = 4 * (size_t)a->n, k4 = n4 * a->top_k;
+  const int es = a->dtype == SSV_BF16 ? 2 : 4;
+  for (const auto& o : {std::make_pair((const void*)a->logprob, n4), std::make_pair((const void*)a->rank, n4),
+                        std::make_pair((const void*)a->entropy, n4), std::make_pair((const void*)a->lse, n4),
+                        std::make_pair((const void*)a->top_logprob, k4), std::make_pair((const void*)a->top_token, k4)})
+    if (meets_rows(o.first, o.second, a->logits, p.stride, a->V, a->total_rows, es)) return SSV_ERR_INVALID;
   p.V = a->V;
   p.total_rows = a->total_rows;
   p.K = a->top_k;
@@ -524,13 +531,13 @@ extern "C" ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream) {
   p.top_logprob = a->top_logprob;
   p.top_token = a->top_token;
   p.dev_status = a->dev_status;
-  const RowSplit sp = logprobs_split(a->n, a->V, a->dtype == SSV_BF16 ? 2 : 4, a->top_k);
+  const RowSplit sp = logprobs_split(a->n, a->V, es, a->top_k);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
   const int warps = sp.ctas * (sp.threads / 32);
   p.give = (2 * a->top_k + warps - 1) / warps;
   // fewer lanes with elements than that: even and odd elements apart (four warps at most, so that the pool holds them)
-  if (p.give > 32 || (warps <= 4 && row_vectors(a->V, a->dtype == SSV_BF16 ? 2 : 4) < 2 * a->top_k)) p.give = 64;
+  if (p.give > 32 || (warps <= 4 && row_vectors(a->V, es) < 2 * a->top_k)) p.give = 64;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   cudaError_t e;

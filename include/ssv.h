@@ -872,7 +872,7 @@ SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
  * exp(-(k - 1) / gamma), section 3.1; neither page gives an interface).
  * Rows: logits [rows, V] device, SSV_F32 or SSV_BF16, rows logits_stride
  * elements apart (0: V; at least V), at any element-aligned address; rows that
- * start on 16-byte boundaries are fastest.  1 <= V <= 393216.  T: positive
+ * start on 16-byte boundaries are fastest.  1 <= V <= 524288.  T: positive
  * and finite.  No workspace; sums and results are the same from call to call.
  * -inf marks a token that cannot be: it has probability 0.  A result beyond
  * fp32's range (the lse of a row at the type's lowest number, T < 1) is infinite.
@@ -903,7 +903,8 @@ SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
  * entropy 0 and no alternatives.
  * tokens given: logprob is not NULL; not given: logprob and rank are NULL.
  * rank, entropy, lse may be NULL.  0 <= top_k <= 128; top_logprob, top_token
- * [n, top_k] (NULL for 0).  Outputs overlap no input.
+ * [n, top_k] (NULL for 0).  Outputs overlap no input
+ * (checked for the logits).
  * Errors: SSV_ERR_INVALID, SSV_ERR_NOT_FINITE (T), SSV_ERR_UNSUPPORTED (V,
  * top_k), SSV_ERR_CUDA; on device SSV_ERR_INVALID for a row outside
  * [-1, total_rows) or a token outside [-1, V) (that entry is taken as idle).

@@ -28,11 +28,12 @@ def _logprobs(**kw):
 def test_logprobs_validation(L):
     inv = ssv.SSV_ERR_INVALID
     cases = [(dict(logits=None), inv), (dict(logits=M + 1), inv), (dict(dtype=ssv.SSV_F32, logits=M + 2), inv),
-             (dict(dtype=2), inv), (dict(V=0), inv), (dict(V=393217), ssv.SSV_ERR_UNSUPPORTED),
+             (dict(dtype=2), inv), (dict(V=0), inv), (dict(V=(1 << 19) + 1), ssv.SSV_ERR_UNSUPPORTED),
              (dict(logits_stride=999), inv), (dict(logits_stride=-1000), inv), (dict(n=-1), inv), (dict(n=9), inv),
              (dict(total_rows=-1), inv), (dict(top_k=-1), inv), (dict(top_k=129), ssv.SSV_ERR_UNSUPPORTED),
              (dict(top_logprob=None), inv), (dict(top_token=None), inv), (dict(logprob=None), inv),
              (dict(tokens=None), inv), (dict(tokens=None, logprob=None), inv)]
+    cases += [(dict(lse=M + 100), inv), (dict(top_token=M + 2 * 8 * 1000 - 4), inv), (dict(logprob=M - 16), inv)]   # over the logits
     cases += [(dict(T=t), ssv.SSV_ERR_NOT_FINITE) for t in (0.0, -1.0, float("inf"), float("nan"), 1e-45)]
     cases += [(dict(tokens=None, logprob=None, rank=None, entropy=None, lse=None, top_k=0), inv)]  # nothing is asked for
     for kw, code in cases:
@@ -64,9 +65,10 @@ def test_distill_validation(L):
     for kw, code in both:
         assert L.ssv_distill(C.byref(_distill(**kw)), None) == code, kw
         assert L.ssv_distill_backward(C.byref(_distill(**kw)), None) == code, kw
-    for kw in (dict(loss=None), dict(grad_loss=8 * M)):
+    for kw in (dict(loss=None), dict(grad_loss=8 * M), dict(loss=M + 64), dict(stats=M + 2 * 8 * 1000 - 16), dict(stats=7 * M),
+               dict(loss=7 * M + 400)):
         assert L.ssv_distill(C.byref(_distill(**kw)), None) == inv, kw
-    for kw in (dict(stats=None), dict(grad=None)):
+    for kw in (dict(stats=None), dict(grad=None), dict(stats=7 * M + 256)):
         assert L.ssv_distill_backward(C.byref(_distill(**kw)), None) == inv, kw
     for f in (L.ssv_distill, L.ssv_distill_backward):
         assert f(None, None) == inv

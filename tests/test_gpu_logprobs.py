@@ -76,7 +76,7 @@ def test_large_vocabularies(v, n, top_k, dtype):
 def test_largest_vocabulary():
     r = np.random.default_rng(5)
     for dtype in (W.F32, W.BF16):
-        check(spread(r, 1, 393216), dtype, [12345], top_k=128)
+        check(spread(r, 1, 1 << 19), dtype, [12345], top_k=128)
 
 
 @pytest.mark.parametrize("n", [700, 1300])

@@ -7,17 +7,32 @@
 //   loss = w [ sum_j p_j (ln p_j - ln q_j) + r (ln r - ln u) ]
 //   d loss / d z_v = (w / T) (P q_v - p_v)                       listed v
 //                    (w / T) (q_v / u) (P u - r)                 other v
-// (q_v / u: the softmax among the other tokens, from their own maximum.)  u is summed from
-// the other tokens alone, never as 1 - (listed): a drafter that has learnt its
-// target leaves little there.  For that the listed tokens of a CTA's part are
-// bits of a map in shared memory, by which a group drops its listed elements.
+// (q_v / u: the softmax among the other tokens, from their own maximum.)  u is
+// summed from the other tokens alone, never as 1 - (listed): a drafter that has
+// learnt its target leaves little there.  For that the listed tokens of a CTA's
+// part are bits of a map in shared memory, by which a thread drops its listed
+// elements.
 //
-// The loss alone: one pass over a row for the maximum and sum of the other tokens,
-// its vectors coming through a ring; the listed ones, K gathers, join at the end.
-// With the gradient, the CTAs of a cluster hold the row in shared memory,
-// exchange their sums, and write the gradient from there; the listed tokens'
-// entries are then written over.  Each logit is read once and each gradient
-// written once.  Backward: the same second part from the forward's statistics.
+// ssv_distill.  One pass over a row for the maximum and sum of the other tokens,
+// its vectors coming through a ring; a warp of its own brings the target meanwhile
+// (K gathers, the softmax of the given values, tokens listed twice met in a small
+// table).  The CTAs of a cluster send each other their sums; with the gradient,
+// each then takes its steps again from the last one on -- the last three are still
+// in the ring, the others come from L2 -- and the listed tokens' entries are
+// written over what the others' formula left there.
+// Bound by HBM and by instructions alike: each logit is fetched from HBM once and
+// each gradient written once (4096 rows of 151936 bf16, K = 128: DRAM traffic at the
+// 2.49 GB that there are), 19 instructions per element at 2.6 per cycle.
+// Measured: that case 454 us, 82% of the copy rate (475 us with whole rows per CTA,
+// which outgrow L2: 1.2 times the traffic; 677 us in quarters, whose ring and
+// target are too much for a part; 463 us with a ring of two steps; first steps again
+// first, a row per CTA: 534 us beside 492); 1024 rows of it 109 us (81%); 700 fp32
+// rows of 32003 36.7 us; the loss of 32 rows 6.8 us, latency.
+//
+// ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
+// that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
+// little above a copy (parts of 96 KB 276 us); 2000 rows of 9001 bf16, padded, 11.8
+// us; 32 rows of 151936 bf16 5.6 us.
 #include "logits.cuh"
 
 #include <algorithm>
@@ -194,7 +209,8 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   }
   if (lane == 0) {
     tg.mass.sum = as_is || s == 0.f || s != s ? s : 1.f;
-    tg.mass.rest = as_is ? (s > 1.f ? 0.f : value_of(Pair{1.f, 0.f} + -all)) : 0.f;  // NaN stays
+    const float left = as_is ? value_of(Pair{1.f, 0.f} + -all) : 0.f;
+    tg.mass.rest = left < 0.f ? 0.f : left;  // NaN stays
     tg.top = top;
     tg.sum = sum;
   }
@@ -212,6 +228,7 @@ struct Sums {
   __device__ __forceinline__ bool empty() const { return none() && S == 0.f; }           // the row is all -inf
 };
 
+// The gradient's coefficients.
 struct Slope {
   float ref, coef;   // other tokens: coef 2^((z - ref) sc)
   float top, share;  // listed ones: wT (share 2^((z - top) sc) - p)
@@ -351,7 +368,7 @@ struct Shared {
   uint32_t part[kParts][4];  // of every warp: maximum and sum (a pair) of its other tokens
 };
 
-// Steps in flight: three with the gradient, which keep the last 30% of a long row for it.
+// Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 454 us; two: 463).
 template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
 template <typename T, bool GRAD>
@@ -624,6 +641,9 @@ ssv_status distill_check(const ssv_distill_args* a, DistillParams& p) {
   if (a->V > kLogitsMaxVocab || a->K > kLogitsMaxTop) return SSV_ERR_UNSUPPORTED;
   if (a->n == 0) return SSV_OK;
   if (!a->logits || !a->teacher_token || !a->teacher_logprob) return SSV_ERR_INVALID;
+  if (((uintptr_t)a->teacher_token | (uintptr_t)a->teacher_logprob | (uintptr_t)a->weight | (uintptr_t)a->loss |
+       (uintptr_t)a->stats | (uintptr_t)a->grad_loss | (uintptr_t)a->dev_status) & 3u)
+    return SSV_ERR_INVALID;
   p.logits = a->logits;
   p.stride = a->logits_stride ? a->logits_stride : a->V;
   p.V = a->V;
@@ -651,8 +671,8 @@ ssv_status distill_check(const ssv_distill_args* a, DistillParams& p) {
   return SSV_OK;
 }
 
-// A row in parts of at most `bytes`, as far as `most` CTAs go; more of them while SMs would have no work and a CTA has
-// more than two batches.
+// A row in parts of at most `bytes`, as far as `most` CTAs go; more of them while there are fewer CTAs than 152 SMs hold
+// at four each and a part has more than one step.  (Loss of 32 rows: 6.8 us at this limit, at half of it and at twice.)
 RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, int threads) {
   const int vectors = row_vectors(V, element_size);
   int c = 1;
@@ -664,6 +684,9 @@ RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, i
 template <typename T, bool GRAD>
 cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   static uint64_t done = 0;
+  // With the gradient parts of 160 KB: two CTAs per SM then have 46 MB of rows on their way, which L2 holds, and 512
+  // threads make the most of a part's fixed cost (4096 rows: see above).  The loss alone reads a row once: no limit, and
+  // 256 threads (32 rows: 6.8 us; 512 threads 8.3 us).
   const RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 160 * 1024 : 1 << 20, kMaxCluster, GRAD ? 512 : 256);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
@@ -676,6 +699,8 @@ cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
 template <typename T>
 cudaError_t backward_launch(DistillParams& p, int n, cudaStream_t st) {
   static uint64_t done = 0;
+  // (1500 fp32 rows: 248 us in parts of 48 KB and of 24, 276 us in parts of 96; 265 us with 256 threads, for whom a
+  // part's fixed cost is too much)
   const RowSplit sp = distill_split(n, p.V, sizeof(T), 48 * 1024, 64, 128);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;

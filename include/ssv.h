@@ -895,8 +895,8 @@ SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
  *                where there are fewer, -1 and -inf.
  * Tokens in the order of the stages, as ssv_accept writes them, have the row
  * of slot k at entry slot_off + tau(k) - 1.
- * Sums are fp32, per thread and joined in a fixed order; logarithms of sums and
- * the results are formed in 64 bits and rounded once (top_logprob in 32).
+ * Sums are fp32, per thread and joined in a fixed order; logprob, lse and entropy
+ * are formed from them in 48 bits and rounded once, top_logprob in fp32.
  * A row with a NaN or +inf gives NaN in logprob, entropy, lse and top_logprob;
  * NaN logits are in no order (never listed, never before another; the rank of
  * such a token is 0).  A row of nothing but -inf gives lse = logprob = -inf,
@@ -968,9 +968,10 @@ SSV_API ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream);
  * gives the loss +inf (the gradient stays finite); so does a row of nothing but
  * -inf, whose gradient is 0.  A row whose listed tokens are all absent has the
  * loss and gradient 0.
- * Sums over a row are fp32; u is summed from the tokens that are not listed;
- * the loss's few logarithms and products are in 64 bits.  The gradient is
- * formed in fp32 and rounded once.
+ * Sums over a row are fp32 per thread and joined in 48 bits; u is summed from the
+ * tokens that are not listed; the loss, a small difference of logarithms, is
+ * formed in 48 bits and rounded once.  The gradient is formed in fp32 and
+ * rounded once.
  * 1 <= K <= 128.
  * Errors: SSV_ERR_INVALID, SSV_ERR_NOT_FINITE (T), SSV_ERR_UNSUPPORTED (V, K),
  * SSV_ERR_CUDA; on device SSV_ERR_INVALID for a listed token outside [-1, V)

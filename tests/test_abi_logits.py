@@ -33,6 +33,7 @@ def test_logprobs_validation(L):
              (dict(total_rows=-1), inv), (dict(top_k=-1), inv), (dict(top_k=129), ssv.SSV_ERR_UNSUPPORTED),
              (dict(top_logprob=None), inv), (dict(top_token=None), inv), (dict(logprob=None), inv),
              (dict(tokens=None), inv), (dict(tokens=None, logprob=None), inv)]
+    cases += [({k: a + 2}, inv) for k, a in (("tokens", 2 * M), ("rows", 9 * M), ("lse", 6 * M), ("top_token", 8 * M), ("rank", 4 * M))]
     cases += [(dict(lse=M + 100), inv), (dict(top_token=M + 2 * 8 * 1000 - 4), inv), (dict(logprob=M - 16), inv)]   # over the logits
     cases += [(dict(T=t), ssv.SSV_ERR_NOT_FINITE) for t in (0.0, -1.0, float("inf"), float("nan"), 1e-45)]
     cases += [(dict(tokens=None, logprob=None, rank=None, entropy=None, lse=None, top_k=0), inv)]  # nothing is asked for
@@ -57,6 +58,8 @@ def test_distill_validation(L):
             (dict(n=-1), inv), (dict(mode=2), inv), (dict(logits_stride=500), inv), (dict(grad_stride=999), inv),
             (dict(teacher_token=None), inv), (dict(teacher_logprob=None), inv), (dict(T=0.0), ssv.SSV_ERR_NOT_FINITE),
             (dict(T=float("nan")), ssv.SSV_ERR_NOT_FINITE),
+            (dict(teacher_token=2 * M + 1), inv), (dict(teacher_logprob=3 * M + 2), inv), (dict(weight=4 * M + 2), inv),
+            (dict(stats=6 * M + 2), inv), (dict(loss=5 * M + 1), inv),
             # a gradient over logits that other CTAs still read
             (dict(grad=M + 32), inv), (dict(grad=M, grad_stride=1008), inv), (dict(grad=M - 32), inv),
             (dict(logits_stride=2000, grad_stride=2000, grad=M + 2 * 999), inv),

@@ -11,7 +11,11 @@
 // rescaled when the maximum grows), and counts the elements before the given
 // token, two at a time where their batch's maximum does not rule them out.  The
 // warps of a cluster send their sums to each other, and every warp that needs them
-// joins them in the same order.
+// joins them in the same order, in 48 bits.  Where one token has nearly all the
+// probability, S is 1 and a little, and entropy and log-probability are made of the
+// little: a thread keeps the sum of the step that holds its maximum apart from the
+// others', and a warp whose sum is nearly 1 forms that step's again without the
+// maximum.
 //
 // Top alternatives.  The K-th largest of any K or more elements bounds the row's
 // K-th from below.  Each warp gives the j largest of its lanes' maxima, j so that
@@ -28,12 +32,13 @@
 // exponential, the sum for the entropy, two maxima, the rank) are close behind, by
 // latency in the short ones: one dependent load, the first copies, a step, two
 // cluster barriers and the ranking of the alternatives.  CTAs are small, so
-// that seven on an SM keep copies in flight while some rank.
-// Measured: 8192 rows of 151936 bf16 without alternatives 383 us, 97% of the copy
-// rate (loads into registers 403 us, the ring with 256 threads 417 us); 960 fp32
-// rows, 30% of them idle, with 32 alternatives 77 us, 80% (256 threads 86 us; rows in
-// halves 92 us); 64 rows with 20 alternatives 13.4 us; one row 9.5 us; 300 rows of
-// 9001 fp32, nine tenths masked, with 64 alternatives 12.9 us.
+// that six on an SM keep copies in flight while some rank.
+// Measured: 8192 rows of 151936 bf16 without alternatives 391 us, 95% of the copy
+// rate (383 us without the digits of nearly certain rows; registers for seven CTAs
+// per SM 430 us; with them loads into registers took 403 us, 256 threads 417 us); 960
+// fp32 rows, 30% of them idle, with 32 alternatives 75 us, 82% (256 threads 86 us;
+// rows in halves 92 us); 64 rows with 20 alternatives 13.8 us; one row 9.9 us; 300
+// rows of 9001 fp32, nine tenths masked, with 64 alternatives 14 us.
 #include "logits.cuh"
 
 #include <algorithm>
@@ -74,7 +79,7 @@ __host__ __device__ constexpr size_t ring_bytes(int threads) {
 }
 
 struct Shared {
-  uint32_t part[kParts][4];   // of every warp: maximum, S, W, elements before the token
+  uint32_t part[kParts][8];   // of every warp: maximum, S (a pair), W, elements before the token
   int groups, count, total;   // batches and keys listed here, keys sent to the cluster's first CTA
   int at;
   uint32_t least[kThreads / 32];
@@ -161,6 +166,29 @@ struct Given {
   }
 };
 
+// Sum of a step's vectors, i and every NT-th behind it up to `end`, without their maximum m, once.
+template <typename T>
+__device__ __noinline__ float step_without(const RowView<T>& row, int i, int NT, int end, float m, float sc) {
+  uint4 x[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    x[u].x = x[u].y = x[u].z = x[u].w = none_bits<T>();
+    if (i + NT * u < end) x[u] = row.load(i + NT * u);
+  }
+  float s = 0.f;
+  bool found = false;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) {
+      const float2 y = pair_of<T>(x[u], e / 2);
+      const float z = (e & 1) ? y.y : y.x;
+      if (!found && z == m) found = true; else s += ex2((z - m) * sc);
+    }
+  }
+  return s;
+}
+
 // Whole CTA: keys of the row that are >= key.
 template <typename T>
 __device__ int count_keys(const RowView<T>& row, unsigned long long key, Shared& sm) {
@@ -222,7 +250,7 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 7) logprobs_kernel(const LogprobsParams p) {
+__global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LogprobsParams p) {
   extern __shared__ __align__(128) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
   __shared__ Shared sm;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
@@ -274,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 7) logprobs_kernel(const LogprobsPar
   const float lt = given.lt;
 
   // ------------------------------------------------------------ the pass
-  float m = -INFINITY, S = 0.f, W = 0.f;
+  float m = -INFINITY, S_top = 0.f, S = 0.f, W = 0.f;  // S_top: of step k_top, which holds the maximum; S: of the others
+  int k_top = 0;
   float even = -INFINITY, odd = -INFINITY;  // m by elements
   int before = 0;
   const float2 sc2 = make_float2(p.T.sc, p.T.sc);
@@ -294,9 +323,11 @@ __global__ void __launch_bounds__(kThreads, 7) logprobs_kernel(const LogprobsPar
     if (mx >= lt) before += given.before(x, ib, NT, i1, row);
     if (mx > m) {  // sums so far on the new scale
       const float d = shift_of(m, mx, p.T.sc), f = ex2(d);
+      S += S_top;
       W = f * (W + d * S);
       S = f * S;
       m = mx;
+      k_top = k;
     }
     // Nothing but -inf and NaN so far: relative to 0, so that -inf counts nothing and NaN stays.
     const float mm = m == -INFINITY ? 0.f : m;
@@ -315,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 7) logprobs_kernel(const LogprobsPar
         W2 = fma2(e, y, W2);
       }
     }
-    S += S2.x + S2.y;
+    if (k == k_top) S_top = S2.x + S2.y; else S += S2.x + S2.y;
     W += W2.x + W2.y;
   };
   for (int k = 0; k < steps; ++k) {
@@ -328,18 +359,25 @@ __global__ void __launch_bounds__(kThreads, 7) logprobs_kernel(const LogprobsPar
   {
     const float M = warp_max(m);
     const float d = shift_of(m, M, p.T.sc), f = ex2(d);
-    const float Sw = warp_sum(f * S), Ww = warp_sum(f * (W + d * S));
+    const float Ww = warp_sum(f * (W + d * (S + S_top)));
+    Pair Sw = warp_sum(Pair{f * S_top, f * S});
+    if (M > -INFINITY && value_of(Sw) < 1.f + 0x1p-7f) {  // 1 for the maximum, and the rest again
+      Pair rest = {f * S_top, f * S};
+      if (lane == __ffs(__ballot_sync(0xffffffffu, m == M)) - 1)
+        rest = Pair{S, step_without<T>(row, i0 + tid + NT * kBatch * k_top, NT, i1, M, p.T.sc)};
+      Sw = Pair{1.f, value_of(warp_sum(rest))};
+    }
     const int nb = warp_sum(before);
     const int me = rank * nw + warp;
     if (c > 1) cluster_wait();
-    const uint32_t word = (lane & 3) == 0   ? __float_as_uint(M)
-                          : (lane & 3) == 1 ? __float_as_uint(Sw)
-                          : (lane & 3) == 2 ? __float_as_uint(Ww)
-                                            : (uint32_t)nb;
-    if (c == 1) {
-      if (lane < 4) sm.part[me][lane] = word;
-    } else if (lane < 4 * (TOP ? c : 1)) {  // without alternatives the first CTA joins them alone
-      cluster_store(cluster_addr(&sm.part[me][lane & 3], lane >> 2), word);
+    for (int i = lane; i < 8 * (TOP ? c : 1); i += 32) {  // without alternatives the first CTA joins them alone
+      const int w = i & 7;
+      if (w > 4) continue;
+      const uint32_t word = __float_as_uint(w == 0 ? M : w == 1 ? Sw.hi : w == 2 ? Sw.lo : Ww);
+      if (c == 1)
+        sm.part[me][w] = w == 4 ? (uint32_t)nb : word;
+      else
+        cluster_store(cluster_addr(&sm.part[me][w], i >> 3), w == 4 ? (uint32_t)nb : word);
     }
     if (TOP) {
       auto give = [&](int i, uint32_t v) {  // by every lane
@@ -375,27 +413,31 @@ __global__ void __launch_bounds__(kThreads, 7) logprobs_kernel(const LogprobsPar
     __syncthreads();
   }
   float Mr, St, Wt;
+  Pair S_row;
   int nb;
   {
     const bool there = lane < c * nw;
     const float ml = there ? __uint_as_float(sm.part[lane][0]) : -INFINITY;
     Mr = warp_max(ml);
-    float s = 0.f, w = 0.f;
+    Pair s = {0.f, 0.f};
+    float w = 0.f;
     nb = 0;
     if (there) {
-      const float d = shift_of(ml, Mr, p.T.sc), f = ex2(d), Sl = __uint_as_float(sm.part[lane][1]);
-      s = f * Sl;
-      w = f * (__uint_as_float(sm.part[lane][2]) + d * Sl);
-      nb = (int)sm.part[lane][3];
+      const float d = shift_of(ml, Mr, p.T.sc), f = ex2(d);
+      const Pair Sl = {__uint_as_float(sm.part[lane][1]), __uint_as_float(sm.part[lane][2])};
+      s = Pair{f * Sl.hi, f * Sl.lo};
+      w = f * (__uint_as_float(sm.part[lane][3]) + d * value_of(Sl));
+      nb = (int)sm.part[lane][4];
     }
-    St = warp_sum(s);
+    S_row = warp_sum(s);
+    St = value_of(S_row);
     Wt = warp_sum(w);
     nb = warp_sum(nb);
   }
 
   // ------------------------------------------------------------ results (the cluster's first CTA)
   const bool empty = Mr == -INFINITY && St == 0.f;  // nothing above -inf
-  const Pair lnS = log_sum(St);
+  const Pair lnS = log_sum(S_row);
   if (rank == 0 && tid == NT - 1) {
     const Pair inv = {p.T.hi, p.T.lo};
     if (p.lse) p.lse[entry] = empty ? -INFINITY : value_of(Pair{Mr, 0.f} * inv + lnS);

@@ -191,6 +191,30 @@ def test_certain_rows():
     check(x, W.F32, [0, 0], top_k=3)
 
 
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("v", [3, 60, 700, 9001, 100000])
+def test_nearly_certain_rows(v, dtype):
+    """One token of nearly all the probability: what the others have, not what is left of 1.  Each of their terms is within
+    3 eps |y| ln 2 + 2^-22 of itself (|y| < 30), their sum within 2^-16 with the additions (logits_common), and so are
+    entropy, its two parts both of that sum, and the log-probability of the token, relatively."""
+    r = np.random.default_rng(v)
+    x = r.standard_normal((12, v)) * 0.5
+    top = r.integers(0, v, 12)
+    x[np.arange(12), top] = np.linspace(5, 19, 12) + np.log(v)
+    x[5, (top[5] + 1) % v] = x[5, top[5]] - 4.0
+    ref, t = store(x, dtype)
+    tok = torch.tensor(top, dtype=torch.int32, device="cuda")
+    lp, rank, ent, lse, tl, tt = (o.cpu().numpy().astype(np.float64) for o in ssv.logprobs(t, tok, 2))
+    for i in range(12):
+        y = ref[i] - ref[i].max()
+        rest = np.exp(np.delete(y, top[i]))
+        small = rest.sum()
+        want = np.log1p(small)
+        h = want - (rest * np.delete(y, top[i])).sum() / (1 + small)
+        assert abs(lp[i] + want) <= LN * want and abs(tl[i, 0] + want) <= LN * want
+        assert abs(ent[i] - h) <= 2 * LN * h and rank[i] == 1 and tt[i, 0] == top[i]
+
+
 def test_long_offsets():
     """A row that starts beyond 2^31 elements."""
     r = np.random.default_rng(12)

@@ -109,6 +109,7 @@ struct Listed {
 // LOSS: with what a loss needs, the rest to more than 32 bits and the sum over the listed tokens.
 template <bool LOSS, typename T>
 __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, const T* row, int lo, int hi, Target& tg) {
+  constexpr bool EXACT = LOSS || sizeof(T) == 4;  // a bf16 gradient would not show it
   const int lane = threadIdx.x & 31;
   float z[kEach];
 #pragma unroll
@@ -132,7 +133,7 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   twice = __any_sync(0xffffffffu, twice);
   // probabilities: relative to the largest for a softmax; as they are where they are log-probabilities
   const bool as_is = p.mode == SSV_DISTILL_REST;
-  float mx = -INFINITY, e[kEach];
+  float mx = -INFINITY, e[kEach], off[kEach];
   Pair all = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < kEach; ++k) mx = fmaxf(mx, l.t[k]);
@@ -140,12 +141,13 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   const float ref = as_is || mx == -INFINITY ? 0.f : mx;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    e[k] = 0.f;
+    e[k] = off[k] = 0.f;
     if (32 * k >= p.K) continue;
     e[k] = expf(l.t[k] - ref);
-    // what an exponential rounded to 32 bits is off by, from its logarithm: the rest is what the sum leaves of 1
-    const float off = LOSS && as_is && e[k] > 0.f ? e[k] * value_of(Pair{l.t[k], 0.f} + -log_sum(e[k])) : 0.f;
-    all = all + Pair{e[k], off};
+    // what an exponential rounded to 32 bits is off by, from its logarithm: the rest is what the sum leaves of 1, and a
+    // gradient what a probability leaves of another
+    if (EXACT && e[k] > 0.f) off[k] = e[k] * value_of(two_sum(l.t[k], -ref) + -log_sum(e[k]));
+    all = all + Pair{e[k], off[k]};
   }
   all = warp_sum(all);
   const float s = value_of(all);
@@ -153,7 +155,8 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     if (32 * k >= p.K) break;
-    e[k] /= norm;
+    const float q = e[k] / norm;
+    e[k] = as_is || !(s < INFINITY) ? e[k] + off[k] : q + (fmaf(-q, all.hi, e[k]) + (off[k] - q * all.lo)) / norm;
     l.t[k] = l.t[k] - ref - ln;
   }
   if (twice) {  // the first of equal tokens takes the others' probabilities
@@ -295,15 +298,18 @@ __device__ __forceinline__ void write_elements(T* out, int lo, int hi, F f) {
 // The gradient of the other tokens, of one vector.
 template <typename T>
 struct Gradient {
-  float2 ref2, sc2, c2;
+  float2 ref2, sc2, lo2, c2;
 
-  __device__ __forceinline__ Gradient(const Slope& k, float sc)
-      : ref2(make_float2(-k.ref, -k.ref)), sc2(make_float2(sc, sc)), c2(make_float2(k.coef, k.coef)) {}
+  __device__ __forceinline__ Gradient(const Slope& k, const Scale& T_)
+      : ref2(make_float2(-k.ref, -k.ref)), sc2(make_float2(T_.down, T_.down)), lo2(make_float2(T_.rest, T_.rest)),
+        c2(make_float2(k.coef, k.coef)) {}
   __device__ __forceinline__ uint4 operator()(const uint4& x) const {
     float2 y[kVec<T> / 2];
 #pragma unroll
     for (int e = 0; e < kVec<T> / 2; ++e) {
-      const float2 a = mul2(add2(pair_of<T>(x, e), ref2), sc2);
+      const float2 d = add2(pair_of<T>(x, e), ref2);
+      float2 a = mul2(d, sc2);
+      if (sizeof(T) == 4) a = fma2(d, lo2, a);  // the scale to 48 bits, as in the sums; bf16 would not show it
       y[e] = mul2(make_float2(ex2(a.x), ex2(a.y)), c2);
     }
     return pack_vector<T>([&](int e) { return e & 1 ? y[e / 2].y : y[e / 2].x; });
@@ -343,8 +349,11 @@ __device__ __forceinline__ void write_step(const RowView<T>& row, const PartView
 
 // Of an output at any offset from the input, with elements from `in`.
 template <typename T>
-__device__ __forceinline__ void write_apart(const PartView<T>& part, const T* in, T* out, const Slope& k, float sc) {
-  write_elements<T>(out, part.lo, part.hi, [&](int v) { return ex2((Elem<T>::to_f32(in[v]) - k.ref) * sc) * k.coef; });
+__device__ __forceinline__ void write_apart(const PartView<T>& part, const T* in, T* out, const Slope& k, const Scale& T_) {
+  write_elements<T>(out, part.lo, part.hi, [&](int v) {
+    const float d = Elem<T>::to_f32(in[v]) - k.ref;
+    return ex2(fmaf(d, T_.rest, d * T_.down)) * k.coef;
+  });
 }
 
 // The listed tokens' entries, over what is there (after a barrier).
@@ -353,7 +362,10 @@ __device__ __forceinline__ void write_listed(const DistillParams& p, const PartV
                                              const Target& tg) {
   for (int j = threadIdx.x; j < p.K; j += blockDim.x) {
     const int v = tg.token[j];
-    if (v >= part.lo && v < part.hi) out[v] = Elem<T>::from_f32(k.wT * (k.share * ex2((tg.z[j] - k.top) * p.T.sc) - tg.p[j]));
+    if (v < part.lo || v >= part.hi) continue;
+    const Pair x = two_sum(tg.z[j], -k.top) * Pair{p.T.hi, p.T.lo};
+    const float e = expf(x.hi), q = k.share * (e > 0.f ? fmaf(e, x.lo, e) : e);  // -inf has no low part; NaN stays
+    out[v] = Elem<T>::from_f32(k.wT * (q - tg.p[j]));
   }
 }
 
@@ -558,14 +570,14 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
     }
     if (p.vec) {
       // from the last step on: the last ones are still in the ring, and what was read late is the likeliest to be in L2
-      const Gradient<T> gradient(k, p.T.sc);
+      const Gradient<T> gradient(k, p.T);
       for (int q = streams ? part.steps - 1 : -1; q >= 0; --q) {
         copy_wait<kStages<GRAD> - 1>();
         write_step<T>(row, part, q, step_slots(q), out, gradient);
         part.fetch(row, q - kStages<GRAD>, step_slots(q));
       }
     } else {
-      write_apart<T>(part, row.row, out, k, p.T.sc);
+      write_apart<T>(part, row.row, out, k, p.T);
     }
     __syncthreads();
     write_listed<T>(p, part, out, k, tg);
@@ -610,11 +622,11 @@ __global__ void __launch_bounds__(128, 8) distill_backward_kernel(const DistillP
     return;
   }
   if (p.vec) {
-    const Gradient<T> gradient(slope, p.T.sc);
+    const Gradient<T> gradient(slope, p.T);
     for (int k = 0; k < part.steps; ++k) write_step<T>(row, part, k, slots + kBatch * k * NT + tid, out, gradient);
   } else {
     __syncthreads();  // every thread's vectors are there
-    write_apart<T>(part, reinterpret_cast<const T*>(slots) - part.at, out, slope, p.T.sc);
+    write_apart<T>(part, reinterpret_cast<const T*>(slots) - part.at, out, slope, p.T);
   }
   __syncthreads();
   write_listed<T>(p, part, out, slope, tg);

@@ -406,7 +406,7 @@ inline bool logits_scale(float T, Scale* s) {
   s->sc = (float)(1.4426950408889634 * inv);
   const double exact = 1.4426950408889634 * inv;
   s->down = (double)s->sc > exact ? nextafterf(s->sc, 0.f) : s->sc;
-  s->rest = fmaxf((float)(exact - (double)s->down), FLT_MIN);
+  s->rest = fmaxf((float)(exact - (double)s->down), FLT_TRUE_MIN);
   s->hi = (float)inv;
   s->lo = (float)(inv - (double)s->hi);
   return isfinite(s->sc) && s->sc >= FLT_MIN && s->hi >= FLT_MIN;

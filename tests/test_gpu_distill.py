@@ -160,6 +160,21 @@ def test_temperatures(T):
             check(z, token, value, dtype, ssv.REST, T=T, lead=3, pad=2)
 
 
+@pytest.mark.parametrize("T", [1e30, 3e37])
+def test_temperatures_near_the_largest(T):
+    """Logits of the type's lowest number, about -11 on the scale of the larger T: what 1 / T has beyond 24 bits is next to
+    fp32's smallest numbers there.  The weights bring loss and gradient back to its range."""
+    r = np.random.default_rng(34)
+    for v in (100, 3001):
+        z, token, value = make(r, 3, v, 9)
+        z[1][r.random(v) < 0.5] = -3.3895314e38
+        z[2] = -3.3895314e38 * r.random(v)
+        value = value - 1
+        for dtype in (W.F32, W.BF16):
+            for mode in MODES:
+                check(z, token, value, dtype, mode, T=T, weight=[T / 8] * 3)
+
+
 @pytest.mark.parametrize("n", [700, 1300])
 def test_many_rows(n):
     r = np.random.default_rng(n)

@@ -883,6 +883,9 @@ def logprobs(logits, tokens=None, top_k: int = 0, T: float = 1.0, rows=None, out
                    empty((n, top_k), dtype=f32, device=dev) if top_k else None,
                    empty((n, top_k), dtype=i32, device=dev) if top_k else None)
     else:
+        out = tuple(out)
+        if len(out) != 6:
+            raise SsvError(SSV_ERR_INVALID, f"{what}: six outputs")
         _like(what, (n,), f32, out[0], out[2], out[3])
         _like(what, (n,), i32, out[1])
         _like(what, (n, top_k), f32, out[4])

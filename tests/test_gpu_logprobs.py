@@ -230,6 +230,19 @@ def test_long_offsets():
     assert np.array_equal(tt.cpu().numpy(), want["top_token"]) and np.array_equal(rank.cpu().numpy(), want["rank"])
 
 
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+def test_zeros_and_subnormal_logits(dtype):
+    """The order of numbers next to 0, of both signs: zeros are equal, subnormal numbers are not zeros."""
+    r = np.random.default_rng(17)
+    near_zero = np.array([0.0, -0.0] + [s * 2.0 ** e for s in (1, -1) for e in (-133, -132, -130, -127, -126, -120)])
+    for v, top_k in ((40, 20), (900, 128), (20000, 64)):
+        x = near_zero[r.integers(0, len(near_zero), (8, v))]
+        x[4:] -= (r.random((4, v)) < 0.98) * r.integers(1, 50, (4, v))   # few of them among others, below
+        t = r.integers(0, v, 8)
+        t[6:] = x[6:].argmax(1)
+        check(x, dtype, t, top_k=top_k)
+
+
 def test_given_outputs_and_repeats():
     r = np.random.default_rng(13)
     _, t = store(spread(r, 9, 20000), W.BF16)
@@ -239,6 +252,9 @@ def test_given_outputs_and_repeats():
     assert ssv.logprobs(t, tok, 30, out=out)[4] is out[4]
     for a, b in zip(first, out):
         assert torch.equal(a, b)
+    assert ssv.logprobs(t, tok, 30, out=list(out))[5] is out[5]
+    with pytest.raises(ssv.SsvError):
+        ssv.logprobs(t, tok, 30, out=out[:4])
     only = (out[0].fill_(0), None, None, None, None, None)
     ssv.logprobs(t, tok, out=only)
     assert torch.equal(out[0], first[0])

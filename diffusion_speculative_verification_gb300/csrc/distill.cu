@@ -22,17 +22,17 @@
 // written over what the others' formula left there.
 // Bound by HBM and by instructions alike: each logit is fetched from HBM once and
 // each gradient written once (4096 rows of 151936 bf16, K = 128: DRAM traffic at the
-// 2.49 GB that there are), 19 instructions per element at 2.6 per cycle.
-// Measured: that case 454 us, 82% of the copy rate (475 us with whole rows per CTA,
+// 2.49 GB that there are), 20 instructions per element at 2.6 per cycle.
+// Measured: that case 452 us, 82% of the copy rate (475 us with whole rows per CTA,
 // which outgrow L2: 1.2 times the traffic; 677 us in quarters, whose ring and
 // target are too much for a part; 463 us with a ring of two steps; first steps again
-// first, a row per CTA: 534 us beside 492); 1024 rows of it 109 us (81%); 700 fp32
+// first, a row per CTA: 534 us beside 492); 1024 rows, K = 64, 111 us (79%); 700 fp32
 // rows of 32003 36.7 us; the loss of 32 rows 6.8 us, latency.
 //
 // ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
 // that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
-// little above a copy (parts of 96 KB 276 us); 2000 rows of 9001 bf16, padded, 11.8
-// us; 32 rows of 151936 bf16 5.6 us.
+// little above a copy (parts of 96 KB 276 us); 2000 rows of 9001 bf16, padded, 12.1
+// us; 32 rows of 151936 bf16 5.4 us.
 #include "logits.cuh"
 
 #include <algorithm>
@@ -380,7 +380,7 @@ struct Shared {
   uint32_t part[kParts][4];  // of every warp: maximum and sum (a pair) of its other tokens
 };
 
-// Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 454 us; two: 463).
+// Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 452 us; two: 463).
 template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
 template <typename T, bool GRAD>

@@ -23,11 +23,11 @@
 // Bound by HBM and by instructions alike: each logit is fetched from HBM once and
 // each gradient written once (4096 rows of 151936 bf16, K = 128: DRAM traffic at the
 // 2.49 GB that there are), 20 instructions per element at 2.6 per cycle.
-// Measured: that case 452 us, 82% of the copy rate (475 us with whole rows per CTA,
+// Measured: that case 444 us, 84% of the copy rate (475 us with whole rows per CTA,
 // which outgrow L2: 1.2 times the traffic; 677 us in quarters, whose ring and
 // target are too much for a part; 463 us with a ring of two steps; first steps again
-// first, a row per CTA: 534 us beside 492); 1024 rows, K = 64, 111 us (79%); 700 fp32
-// rows of 32003 36.7 us; the loss of 32 rows 6.8 us, latency.
+// first, a row per CTA: 534 us beside 492); 1024 rows, K = 64, 109 us (81%); 700 fp32
+// rows of 32003 35.7 us; the loss of 32 rows 6.6 us, latency.
 //
 // ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
 // that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
@@ -380,17 +380,20 @@ struct Shared {
   uint32_t part[kParts][4];  // of every warp: maximum and sum (a pair) of its other tokens
 };
 
-// Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 452 us; two: 463).
+// Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 452 us, two 463, before the threads were known to the compiler).
 template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
-template <typename T, bool GRAD>
+// LOG_NT: 2^LOG_NT threads share a row, so that a step's addresses are constants apart (4096 rows 444 us; known at the
+// launch alone, 451 us); 0: as many as the launch says, for rows that are too short for them.
+template <typename T, bool GRAD, int LOG_NT>
 __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const DistillParams p) {
   // a ring of slots; behind it a word per thread and step, whose bit (vector of the step, element) says that the
   // element is a listed token
   extern __shared__ __align__(128) unsigned char dynamic[];
   __shared__ Shared sm;
   // NT threads share the row, and a warp behind them brings its target
-  const int tid = threadIdx.x, NT = 1 << p.log_nt, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
+  const int log_nt = LOG_NT ? LOG_NT : p.log_nt;
+  const int tid = threadIdx.x, NT = 1 << log_nt, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
   const bool streams = warp < nw;
   const int c = 1 << p.log_c;
   const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
   pdl_trigger();
   const float w = p.weight ? p.weight[entry] : 1.f;
   const RowView<T> row(static_cast<const T*>(p.logits) + (int64_t)entry * p.stride, p.V);
-  const PartView<T> part(row, rank, p.log_c, p.log_nt);
+  const PartView<T> part(row, rank, p.log_c, log_nt);
   T* out = GRAD ? static_cast<T*>(p.grad) + (int64_t)entry * p.grad_stride : nullptr;
   if (w == 0.f) {  // not read at all
     if (rank == 0 && tid == 0) {
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
     for (int k = 0; k < kEach; ++k) {
       const int v = mine.v[k];
       if (v < part.lo || v >= part.hi) continue;
-      const int i = (v - part.at) / kVec<T>, e = (v - part.at) % kVec<T>, s = i >> p.log_nt;
+      const int i = (v - part.at) / kVec<T>, e = (v - part.at) % kVec<T>, s = i >> log_nt;
       atomicOr(&listed[s / kBatch * NT + (i & (NT - 1))], 1u << (s % kBatch * kVec<T> + e));
     }
   }
@@ -693,9 +696,15 @@ RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, i
   return split_of(vectors, c, threads);
 }
 
+template <typename T, bool GRAD, int LOG_NT>
+cudaError_t distill_launch_as(const DistillParams& p, int n, const RowSplit& sp, size_t smem, cudaStream_t st) {
+  static uint64_t done = 0;
+  const cudaError_t e = allow_shared(distill_kernel<T, GRAD, LOG_NT>, smem, &done);
+  return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD, LOG_NT>, n, sp, sp.threads + 32, smem, st, p);
+}
+
 template <typename T, bool GRAD>
 cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
-  static uint64_t done = 0;
   // With the gradient parts of 160 KB: two CTAs per SM then have 46 MB of rows on their way, which L2 holds, and 512
   // threads make the most of a part's fixed cost (4096 rows: see above).  The loss alone reads a row once: no limit, and
   // 256 threads (32 rows: 6.8 us; 512 threads 8.3 us).
@@ -704,8 +713,9 @@ cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   p.log_nt = sp.log_nt;
   p.slot_bytes = 16 * kStages<GRAD> * kBatch * sp.threads + kSlotSlack;
   const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
-  const cudaError_t e = allow_shared(distill_kernel<T, GRAD>, smem, &done);
-  return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD>, n, sp, sp.threads + 32, smem, st, p);
+  constexpr int kWide = GRAD ? 9 : 8;
+  return sp.log_nt == kWide ? distill_launch_as<T, GRAD, kWide>(p, n, sp, smem, st)
+                            : distill_launch_as<T, GRAD, 0>(p, n, sp, smem, st);
 }
 
 template <typename T>
@@ -717,7 +727,7 @@ cudaError_t backward_launch(DistillParams& p, int n, cudaStream_t st) {
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
   const size_t smem = 16 * (size_t)sp.vectors + kSlotSlack;
-  cudaError_t e = allow_shared(distill_backward_kernel<T>, smem, &done);
+  const cudaError_t e = allow_shared(distill_backward_kernel<T>, smem, &done);
   return e != cudaSuccess ? e : launch_rows(distill_backward_kernel<T>, n, sp, sp.threads, smem, st, p);
 }
 

@@ -33,11 +33,11 @@
 // latency in the short ones: one dependent load, the first copies, a step, two
 // cluster barriers and the ranking of the alternatives.  CTAs are small, so
 // that six on an SM keep copies in flight while some rank.
-// Measured: 8192 rows of 151936 bf16 without alternatives 391 us, 95% of the copy
-// rate (383 us without the digits of nearly certain rows; registers for seven CTAs
-// per SM 430 us; with them loads into registers took 403 us, 256 threads 417 us); 960
-// fp32 rows, 30% of them idle, with 32 alternatives 75 us, 82% (256 threads 86 us;
-// rows in halves 92 us); 64 rows with 20 alternatives 13.8 us; one row 9.9 us; 300
+// Measured: 8192 rows of 151936 bf16 without alternatives 379 us, 98% of the copy
+// rate (391 us with the threads known at the launch alone; then registers for seven
+// CTAs per SM 430 us, loads into registers 403 us, 256 threads 417 us); 960
+// fp32 rows, 30% of them idle, with 32 alternatives 74 us, 84% (256 threads 86 us;
+// rows in halves 92 us); 64 rows with 20 alternatives 13.6 us; one row 9.7 us; 300
 // rows of 9001 fp32, nine tenths masked, with 64 alternatives 14 us.
 #include "logits.cuh"
 
@@ -249,11 +249,14 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
   __syncthreads();
 }
 
-template <typename T, bool TOP>
+// LOG_NT: 2^LOG_NT threads in a CTA, so that a step's addresses are constants apart (8192 rows 379 us; known at the launch
+// alone, 391 us); 0: as many as the launch says, for short rows.
+template <typename T, bool TOP, int LOG_NT>
 __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LogprobsParams p) {
   extern __shared__ __align__(128) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
   __shared__ Shared sm;
-  const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
+  const int log_nt = LOG_NT ? LOG_NT : p.log_nt;
+  const int tid = threadIdx.x, NT = 1 << log_nt, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
   const int c = 1 << p.log_c;
   const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
   Lists& lists = *reinterpret_cast<Lists*>(dynamic);
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LogprobsPar
     return;
   }
   const RowView<T> row(static_cast<const T*>(p.logits) + (int64_t)r * p.stride, p.V);
-  const PartView<T> part(row, rank, p.log_c, p.log_nt);
+  const PartView<T> part(row, rank, p.log_c, log_nt);
   const int i0 = part.i0, i1 = part.i1, steps = part.steps;
   uint4* ring = part.slots_in(dynamic, row);
   auto slots = [&](int k) { return ring + kBatch * (k % kStages) * NT + tid; };
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LogprobsPar
     if (ng <= kList) {
       for (int q = tid; q < ng * kBatch; q += NT) {
         const int b = lists.group[q / kBatch];
-        const int i = i0 + (b & (NT - 1)) + NT * (kBatch * (b >> p.log_nt) + q % kBatch);
+        const int i = i0 + (b & (NT - 1)) + NT * (kBatch * (b >> log_nt) + q % kBatch);
         if (i < i1) list_keys<T>(row.load(i), row.first(i), key, lists.list, &sm.count);
       }
     } else if (tid == 0) {
@@ -530,12 +533,17 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LogprobsPar
   }
 }
 
-template <typename T, bool TOP>
-cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, cudaStream_t st) {
+template <typename T, bool TOP, int LOG_NT>
+cudaError_t logprobs_launch_as(const LogprobsParams& p, int n, const RowSplit& sp, cudaStream_t st) {
   static uint64_t done = 0;
   const size_t smem = ring_bytes(sp.threads) + (TOP ? (size_t)sp.batches() * sp.threads * sizeof(__nv_bfloat16) : 0);
-  const cudaError_t e = allow_shared(logprobs_kernel<T, TOP>, smem, &done);
-  return e != cudaSuccess ? e : launch_rows(logprobs_kernel<T, TOP>, n, sp, sp.threads, smem, st, p);
+  const cudaError_t e = allow_shared(logprobs_kernel<T, TOP, LOG_NT>, smem, &done);
+  return e != cudaSuccess ? e : launch_rows(logprobs_kernel<T, TOP, LOG_NT>, n, sp, sp.threads, smem, st, p);
+}
+
+template <typename T, bool TOP>
+cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, cudaStream_t st) {
+  return TOP || sp.log_nt == 7 ? logprobs_launch_as<T, TOP, 7>(p, n, sp, st) : logprobs_launch_as<T, TOP, 0>(p, n, sp, st);
 }
 
 // CTAs per row: more of them while they stay below three per SM and a CTA has more than two steps (64 rows of 151936

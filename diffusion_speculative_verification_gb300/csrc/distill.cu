@@ -14,7 +14,7 @@
 // elements.
 //
 // ssv_distill.  One pass over a row for the maximum and sum of the other tokens,
-// its vectors coming through a ring; a warp of its own brings the target meanwhile
+// its vectors coming through a ring; one or two other warps bring the target meanwhile
 // (K gathers, the softmax of the given values, tokens listed twice met in a small
 // table).  The CTAs of a cluster send each other their sums; with the gradient,
 // each then takes its steps again from the last one on -- the last three are still
@@ -22,8 +22,8 @@
 // written over what the others' formula left there.
 // Bound by HBM and by instructions alike: each logit is fetched from HBM once and
 // each gradient written once (4096 rows of 151936 bf16, K = 128: DRAM traffic at the
-// 2.49 GB that there are), 20 instructions per element at 2.6 per cycle.
-// Measured: that case 444 us, 84% of the copy rate (475 us with whole rows per CTA,
+// 2.49 GB that there are), 18 instructions per element at 2.6 per cycle.
+// Measured: that case 428 us, 87% of the copy rate (475 us with whole rows per CTA,
 // which outgrow L2: 1.2 times the traffic; 677 us in quarters, whose ring and
 // target are too much for a part; 463 us with a ring of two steps; first steps again
 // first, a row per CTA: 534 us beside 492); 1024 rows, K = 64, 109 us (81%); 700 fp32
@@ -44,7 +44,7 @@ namespace {
 constexpr int kThreads = 512;                  // most threads that share a row's part
 constexpr int kParts = kThreads / 32 * kMaxCluster;  // warps of a cluster
 constexpr int kHash = 2 * kLogitsMaxTop;       // places of the table in which repeated tokens meet
-constexpr int kEach = kLogitsMaxTop / 32;      // listed tokens of a lane
+constexpr int kTeam = 2;                       // most warps that bring a target beside those that stream the row
 
 struct DistillParams {
   const void* logits;
@@ -76,20 +76,29 @@ struct Target {
   float p[kLogitsMaxTop], t[kLogitsMaxTop], z[kLogitsMaxTop];
   int hash[kHash];
   Mass mass;
-  float top;  // largest of z
-  Pair sum;   // sum of exp((z - top) / T)
+  float top;        // largest of z
+  Pair sum[kTeam];  // sum of exp((z - top) / T), of each warp of the team
+  float team_mx[kTeam], team_top[kTeam];
+  int team_twice[kTeam];
+  Pair team_all[kTeam];
 };
 
-// One warp brings a row's target, four entries per lane (j = lane + 32 k), while the others are busy with the row.
+// TEAM warps bring a row's target while the others are busy with the row: entry 32 (member + TEAM k) + lane is a lane's
+// k-th.
+template <int TEAM>
 struct Listed {
+  static constexpr int kEach = kLogitsMaxTop / (32 * TEAM);
   int v[kEach];
   float t[kEach];
+  int member;
 
-  __device__ __forceinline__ void load(const DistillParams& p, int row) {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ int at(int k) const { return 32 * (member + TEAM * k) + (threadIdx.x & 31); }
+  __device__ __forceinline__ bool none(int k, int K) const { return 32 * (member + TEAM * k) >= K; }  // of any lane
+  __device__ __forceinline__ void load(const DistillParams& p, int row, int member_) {
+    member = member_;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int j = lane + 32 * k;
+      const int j = at(k);
       v[k] = j < p.K ? p.token[(size_t)row * p.K + j] : -1;
       t[k] = j < p.K ? p.logp[(size_t)row * p.K + j] : -INFINITY;
     }
@@ -105,22 +114,29 @@ struct Listed {
   }
 };
 
-// The warp's entries to shared memory: `row` their logits, those of [lo, hi) alone (the others are not asked for).
+template <int TEAM>
+__device__ __forceinline__ void team_sync() {
+  if (TEAM == 1) __syncwarp(); else asm volatile("barrier.sync 1, %0;" ::"n"(32 * TEAM) : "memory");
+}
+
+// The team's entries to shared memory: `row` their logits, those of [lo, hi) alone (the others are not asked for).
 // LOSS: with what a loss needs, the rest to more than 32 bits and the sum over the listed tokens.
-template <bool LOSS, typename T>
-__device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, const T* row, int lo, int hi, Target& tg) {
+template <bool LOSS, typename T, int TEAM>
+__device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM>& l, const T* row, int lo, int hi,
+                                             Target& tg) {
+  constexpr int kEach = Listed<TEAM>::kEach;
   constexpr bool EXACT = LOSS || sizeof(T) == 4;  // a bf16 gradient would not show it
   const int lane = threadIdx.x & 31;
   float z[kEach];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) z[k] = l.v[k] >= lo && l.v[k] < hi ? load_element(row + l.v[k]) : -INFINITY;
   // tokens listed twice meet in a table
-  for (int h = lane; h < kHash; h += 32) tg.hash[h] = -1;
-  __syncwarp();
+  for (int h = lane + 32 * l.member; h < kHash; h += 32 * TEAM) tg.hash[h] = -1;
+  team_sync<TEAM>();
   bool twice = false;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    if (32 * k >= p.K) break;
+    if (l.none(k, p.K)) break;
     if (l.v[k] < 0) continue;
     // at most K of 2 K places are taken, so that a free one is met within K steps
     uint32_t h = ((uint32_t)l.v[k] * 2654435761u) >> 24;
@@ -133,16 +149,34 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   twice = __any_sync(0xffffffffu, twice);
   // probabilities: relative to the largest for a softmax; as they are where they are log-probabilities
   const bool as_is = p.mode == SSV_DISTILL_REST;
-  float mx = -INFINITY, e[kEach], off[kEach];
+  float mx = -INFINITY, top = -INFINITY, e[kEach], off[kEach];
   Pair all = {0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) mx = fmaxf(mx, l.t[k]);
+  for (int k = 0; k < kEach; ++k) {
+    mx = fmaxf(mx, l.t[k]);
+    top = fmaxf(top, z[k]);
+  }
   mx = warp_max(mx);
+  top = warp_max(top);
+  if (TEAM > 1) {
+    if (lane == 0) {
+      tg.team_mx[l.member] = mx;
+      tg.team_top[l.member] = top;
+      tg.team_twice[l.member] = twice;
+    }
+    team_sync<TEAM>();
+#pragma unroll
+    for (int o = 0; o < TEAM; ++o) {
+      mx = fmaxf(mx, tg.team_mx[o]);
+      top = fmaxf(top, tg.team_top[o]);
+      twice |= tg.team_twice[o] != 0;
+    }
+  }
   const float ref = as_is || mx == -INFINITY ? 0.f : mx;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     e[k] = off[k] = 0.f;
-    if (32 * k >= p.K) continue;
+    if (l.none(k, p.K)) continue;
     e[k] = expf(l.t[k] - ref);
     // what an exponential rounded to 32 bits is off by, from its logarithm: the rest is what the sum leaves of 1, and a
     // gradient what a probability leaves of another
@@ -150,11 +184,18 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
     all = all + Pair{e[k], off[k]};
   }
   all = warp_sum(all);
+  if (TEAM > 1) {
+    if (lane == 0) tg.team_all[l.member] = all;
+    team_sync<TEAM>();
+    all = tg.team_all[0];
+#pragma unroll
+    for (int o = 1; o < TEAM; ++o) all = all + tg.team_all[o];
+  }
   const float s = value_of(all);
   const float norm = as_is || s == 0.f ? 1.f : s, ln = as_is || s == 0.f ? 0.f : value_of(log_sum(all));
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    if (32 * k >= p.K) break;
+    if (l.none(k, p.K)) break;
     const float q = e[k] / norm;
     e[k] = as_is || !(s < INFINITY) ? e[k] + off[k] : q + (fmaf(-q, all.hi, e[k]) + (off[k] - q * all.lo)) / norm;
     l.t[k] = l.t[k] - ref - ln;
@@ -162,13 +203,13 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
   if (twice) {  // the first of equal tokens takes the others' probabilities
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      tg.token[lane + 32 * k] = l.v[k];
-      tg.p[lane + 32 * k] = e[k];
+      tg.token[l.at(k)] = l.v[k];
+      tg.p[l.at(k)] = e[k];
     }
-    __syncwarp();
+    team_sync<TEAM>();
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int j = lane + 32 * k, v = l.v[k];
+      const int j = l.at(k), v = l.v[k];
       if (v < 0) continue;
       for (int o = 0; o < p.K; ++o) {
         if (o == j || tg.token[o] != v) continue;
@@ -185,37 +226,34 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed& l, 
         z[k] = -INFINITY;
       }
     }
-    __syncwarp();
+    team_sync<TEAM>();
   }
-  float top = -INFINITY;
   Pair sum = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    const int j = lane + 32 * k;
+    const int j = l.at(k);
     tg.token[j] = l.v[k];
     tg.p[j] = e[k];
     tg.t[j] = l.t[k];
     tg.z[j] = z[k];
-    top = fmaxf(top, z[k]);
   }
-  top = warp_max(top);
   if (LOSS) {
     const float zero = top == -INFINITY ? 0.f : top;  // -inf counts nothing, NaN stays
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      if (32 * k >= p.K) break;
+      if (l.none(k, p.K)) break;
       const Pair x = two_sum(z[k], -zero) * Pair{p.T.hi, p.T.lo};
       const float e1 = expf(x.hi);
       sum = sum + Pair{e1, e1 > 0.f ? e1 * x.lo : 0.f};  // -inf has no low part; NaN stays
     }
     sum = warp_sum(sum);
+    if (lane == 0) tg.sum[l.member] = sum;
   }
-  if (lane == 0) {
+  if (lane == 0 && l.member == 0) {
     tg.mass.sum = as_is || s == 0.f || s != s ? s : 1.f;
     const float left = as_is ? value_of(Pair{1.f, 0.f} + -all) : 0.f;
     tg.mass.rest = left < 0.f ? 0.f : left;  // NaN stays
     tg.top = top;
-    tg.sum = sum;
   }
 }
 
@@ -383,18 +421,18 @@ struct Shared {
 // Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 452 us, two 463, before the threads were known to the compiler).
 template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
-// LOG_NT: 2^LOG_NT threads share a row, so that a step's addresses are constants apart (4096 rows 444 us; known at the
-// launch alone, 451 us); 0: as many as the launch says, for rows that are too short for them.
-template <typename T, bool GRAD, int LOG_NT>
-__global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const DistillParams p) {
+// LOG_NT: 2^LOG_NT threads share a row, so that a step's addresses are constants apart (4096 rows 444 us where known at the
+// launch alone took 451); 0: as many as the launch says, for rows that are too short for them.  TEAM warps bring the target.
+template <typename T, bool GRAD, int LOG_NT, int TEAM>
+__global__ void __launch_bounds__(kThreads + 32 * TEAM, 2) distill_kernel(const DistillParams p) {
   // a ring of slots; behind it a word per thread and step, whose bit (vector of the step, element) says that the
   // element is a listed token
   extern __shared__ __align__(128) unsigned char dynamic[];
   __shared__ Shared sm;
-  // NT threads share the row, and a warp behind them brings its target
+  // NT threads share the row, and the team behind them brings its target; the team's first warp joins the sums
   const int log_nt = LOG_NT ? LOG_NT : p.log_nt;
   const int tid = threadIdx.x, NT = 1 << log_nt, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
-  const bool streams = warp < nw;
+  const bool streams = warp < nw, joins = warp == nw;
   const int c = 1 << p.log_c;
   const int rank = (int)blockIdx.x & (c - 1), entry = (int)blockIdx.x >> p.log_c;
   uint32_t* listed = reinterpret_cast<uint32_t*>(dynamic + p.slot_bytes);
@@ -422,14 +460,14 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
 
   // ------------------------------------------------------------ the target
   Target& tg = sm.tg;
-  Listed mine;
-  if (!streams) mine.load(p, entry);
+  Listed<TEAM> mine;
+  if (!streams) mine.load(p, entry, warp - nw);
   for (int i = tid; i < part.steps * NT; i += blockDim.x) listed[i] = 0u;
   __syncthreads();
   if (!streams) {
     mine.check(p, rank == 0);
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
+    for (int k = 0; k < mine.kEach; ++k) {
       const int v = mine.v[k];
       if (v < part.lo || v >= part.hi) continue;
       const int i = (v - part.at) / kVec<T>, e = (v - part.at) % kVec<T>, s = i >> log_nt;
@@ -480,7 +518,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
     }
     copy_wait<0>();
   } else {
-    weigh_listed<true, T>(p, mine, row.row, 0, p.V, tg);
+    weigh_listed<true>(p, mine, row.row, 0, p.V, tg);
   }
   if (c > 1) cluster_wait();
   if (streams) {
@@ -501,7 +539,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
   } else {
     __syncthreads();
   }
-  if (!GRAD && streams) return;
+  if (!GRAD && !joins) return;
 
   // ------------------------------------------------------------ the row's sums, by one warp of each CTA in the same order
   // (The sums are of 32 bits, joined in 48: the last few additions would cost a loss, which is a small difference of
@@ -509,7 +547,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
   Sums sums;
   Pair S_all, S_rest;
   float listed_share = 0.f;  // 1 - u
-  if (!streams) {
+  if (joins) {
     const int n = c * nw;
     float mx = -INFINITY;
     for (int q = lane; q < n; q += 32) mx = fmaxf(mx, __uint_as_float(sm.part[q][0]));
@@ -522,7 +560,10 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
     S_rest = warp_sum(S_rest);
     const float m_all = fmaxf(mx, tg.top);
     const float fr = ex2(shift_of(mx, m_all, p.T.sc)), ft = ex2(shift_of(tg.top, m_all, p.T.sc));
-    const Pair st = {ft * tg.sum.hi, ft * tg.sum.lo};
+    Pair st = tg.sum[0];
+#pragma unroll
+    for (int o = 1; o < TEAM; ++o) st = st + tg.sum[o];
+    st = Pair{ft * st.hi, ft * st.lo};
     S_all = Pair{fr * S_rest.hi, fr * S_rest.lo} + st;
     sums = {m_all, value_of(S_all), mx, value_of(S_rest)};
     listed_share = value_of(st) / sums.S;
@@ -531,11 +572,11 @@ __global__ void __launch_bounds__(kThreads + 32, 2) distill_kernel(const Distill
     }
   }
   if (GRAD) __syncthreads();
-  if (rank == 0 && !streams) {
+  if (rank == 0 && joins) {
     const Pair inv = {p.T.hi, p.T.lo}, lnS = log_sum(S_all);
     Pair loss = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
+    for (int k = 0; k < kLogitsMaxTop / 32; ++k) {
       const int j = lane + 32 * k;
       const float pj = j < p.K ? tg.p[j] : 0.f;
       if (pj > 0.f || pj != pj) {
@@ -608,13 +649,13 @@ __global__ void __launch_bounds__(128, 8) distill_backward_kernel(const DistillP
   uint4* slots = part.slots_in(dynamic, row);
   for (int k = 0; k < part.steps; ++k) part.fetch(row, k, slots + kBatch * k * NT + tid);
   if (tid < 32) {
-    Listed mine;
-    mine.load(p, entry);
+    Listed<1> mine;
+    mine.load(p, entry, 0);
     const float* from = p.stats_in + 4 * (size_t)entry;
     const Sums sums = {from[0], from[1], from[2], from[3]};
     const float up = p.grad_loss ? p.grad_loss[entry] : 1.f;
     mine.check(p, rank == 0);
-    weigh_listed<false, T>(p, mine, row.row, part.lo, part.hi, tg);
+    weigh_listed<false>(p, mine, row.row, part.lo, part.hi, tg);
     __syncwarp();
     if (tid == 0) slope = slope_of(sums, tg.mass, p.T, w * up);
   }
@@ -696,11 +737,11 @@ RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, i
   return split_of(vectors, c, threads);
 }
 
-template <typename T, bool GRAD, int LOG_NT>
+template <typename T, bool GRAD, int LOG_NT, int TEAM>
 cudaError_t distill_launch_as(const DistillParams& p, int n, const RowSplit& sp, size_t smem, cudaStream_t st) {
   static uint64_t done = 0;
-  const cudaError_t e = allow_shared(distill_kernel<T, GRAD, LOG_NT>, smem, &done);
-  return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD, LOG_NT>, n, sp, sp.threads + 32, smem, st, p);
+  const cudaError_t e = allow_shared(distill_kernel<T, GRAD, LOG_NT, TEAM>, smem, &done);
+  return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD, LOG_NT, TEAM>, n, sp, sp.threads + 32 * TEAM, smem, st, p);
 }
 
 template <typename T, bool GRAD>
@@ -714,8 +755,16 @@ cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   p.slot_bytes = 16 * kStages<GRAD> * kBatch * sp.threads + kSlotSlack;
   const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
   constexpr int kWide = GRAD ? 9 : 8;
-  return sp.log_nt == kWide ? distill_launch_as<T, GRAD, kWide>(p, n, sp, smem, st)
-                            : distill_launch_as<T, GRAD, 0>(p, n, sp, smem, st);
+  // The target is as long on its way as the row's first reading where a warp has four tokens per lane: two warps for more
+  // than 64 tokens (4096 rows, K = 128: 428 us; one warp 444, four 435, whose registers do not suffice), one for fewer (1024
+  // rows, K = 64: 109 us; two 111) and for the loss, of whose 256 threads two take more room (32 rows, K = 32: 6.6 us; two
+  // 7.8).
+  if constexpr (GRAD)
+    if (p.K > 64)
+      return sp.log_nt == kWide ? distill_launch_as<T, GRAD, kWide, 2>(p, n, sp, smem, st)
+                                : distill_launch_as<T, GRAD, 0, 2>(p, n, sp, smem, st);
+  return sp.log_nt == kWide ? distill_launch_as<T, GRAD, kWide, 1>(p, n, sp, smem, st)
+                            : distill_launch_as<T, GRAD, 0, 1>(p, n, sp, smem, st);
 }
 
 template <typename T>

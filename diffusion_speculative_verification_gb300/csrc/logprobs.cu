@@ -28,7 +28,7 @@
 // them by counting.  Where more pass than its list holds (long runs of equal
 // values), it finds the K-th key by bisection over the row.
 //
-// Bound by HBM in the long cases, though 10 instructions per element (the
+// Bound by HBM in the long cases, though 9 instructions per element (the
 // exponential, the sum for the entropy, two maxima, the rank) are close behind, by
 // latency in the short ones: one dependent load, the first copies, a step, two
 // cluster barriers and the ranking of the alternatives.  CTAs are small, so

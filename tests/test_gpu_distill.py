@@ -238,6 +238,23 @@ def test_listed_more_than_once(mode):
 
 
 @pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("K", [64, 65, 96, 97, 127, 128])
+def test_long_lists(K, dtype, mode):
+    """Tokens that are listed far apart, more than once, and absent ones among them, in rows of one and of several CTAs."""
+    r = np.random.default_rng(K)
+    for v in (300, 3001, 60000):
+        z, token, value = make(r, 4, v, K)
+        token[0, K - 1] = token[0, 0]
+        token[0, 33:60] = token[0, 1]
+        token[1, K // 2:] = token[1, :K - K // 2]
+        token[2, r.random(K) < 0.5] = -1
+        token[3] = token[3, 63]
+        value -= np.log(8.0 if mode == ssv.RENORM else 2.0 * K).astype(np.float32)
+        check(z, token, value, dtype, mode, lead=1)
+
+
+@pytest.mark.parametrize("mode", MODES)
 def test_absent_and_refused_tokens(mode):
     r = np.random.default_rng(24)
     z, token, value = make(r, 5, 200, 12)

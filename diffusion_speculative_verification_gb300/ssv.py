@@ -925,6 +925,8 @@ def _empty_rows(logits):
     lead = (logits.data_ptr() % 32) // logits.element_size()
     if (s == v and lead == 0) or not v <= s <= v + 64:
         return torch.empty((n, v), dtype=logits.dtype, device=logits.device)
+    if lead == 0:
+        return torch.empty_strided((n, v), (s, 1), dtype=logits.dtype, device=logits.device)
     return torch.empty(n * s + lead, dtype=logits.dtype, device=logits.device).as_strided((n, v), (s, 1), lead)
 
 

@@ -354,6 +354,20 @@ struct Gradient {
   }
 };
 
+// The elements of a vector that is not whole.
+template <typename T>
+__device__ __noinline__ void write_edge(const RowView<T>& row, int i, const uint4 y, T* out) {
+  const int v0 = row.first(i);
+  for (int e = 0; e < kVec<T>; ++e) {
+    const uint32_t w = e * (int)sizeof(T) < 4 ? y.x : e * (int)sizeof(T) < 8 ? y.y : e * (int)sizeof(T) < 12 ? y.z : y.w;
+    if (v0 + e < 0 || v0 + e >= row.V) continue;
+    if (sizeof(T) == 2)
+      reinterpret_cast<uint16_t*>(out)[v0 + e] = (uint16_t)(e & 1 ? w >> 16 : w);
+    else
+      reinterpret_cast<uint32_t*>(out)[v0 + e] = w;
+  }
+}
+
 // Step k of the thread's vectors, from its slots to an output whose vectors are those of the input; the row's first and
 // last vectors by element.
 template <typename T>
@@ -365,23 +379,11 @@ __device__ __forceinline__ void write_step(const RowView<T>& row, const PartView
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) store_vector(to + (size_t)(NT * 16) * u, gradient(slots[NT * u]));
   } else {
-#pragma unroll 1
-    for (int u = 0; u < kBatch && i + NT * u < part.i1; ++u) {
-      const uint4 y = gradient(slots[NT * u]);
-      if (row.whole(i + NT * u)) {
-        store_vector(to + (size_t)(NT * 16) * u, y);
-      } else {
-        const int v0 = row.first(i + NT * u);
-        for (int e = 0; e < kVec<T>; ++e) {
-          const uint32_t w = e * (int)sizeof(T) < 4 ? y.x : e * (int)sizeof(T) < 8 ? y.y : e * (int)sizeof(T) < 12 ? y.z : y.w;
-          if (v0 + e < 0 || v0 + e >= row.V) continue;
-          if (sizeof(T) == 2)
-            reinterpret_cast<uint16_t*>(out)[v0 + e] = (uint16_t)(e & 1 ? w >> 16 : w);
-          else
-            reinterpret_cast<uint32_t*>(out)[v0 + e] = w;
-        }
-      }
-    }
+    const int end = min(part.i1, row.hi);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (i + NT * u >= row.lo && i + NT * u < end) store_vector(to + (size_t)(NT * 16) * u, gradient(slots[NT * u]));
+    part.edges(row, k, [&](int d, int edge) { write_edge<T>(row, edge, gradient(slots[d]), out); });
   }
 }
 

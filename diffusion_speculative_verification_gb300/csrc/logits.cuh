@@ -158,10 +158,6 @@ struct RowView {
                  : "l"(base + (size_t)i * 16));
     return r;
   }
-  // vector i to its slot; read by the thread that asked for it
-  __device__ __forceinline__ void fetch(uint4* slot, int i) const {
-    if (whole(i)) copy_async(slot, base + (size_t)i * 16); else *slot = edge(i);
-  }
 };
 
 // A CTA's part of a row: vectors [i0, i1), elements [lo, hi), the first one's start at element `at`; a step is kBatch
@@ -192,6 +188,17 @@ struct PartView {
     return reinterpret_cast<uint4*>(memory) + (((uint32_t)(reinterpret_cast<uintptr_t>(row.base) >> 4) + (uint32_t)i0) & 7u);
   }
   __device__ __forceinline__ bool full(int k) const { return k >= full0 && k < full1; }
+  // f(d, i) for the row's first and last vectors that are not whole, where vector i is the thread's in step k, d slots
+  // behind its first (a row of one vector may have it twice)
+  template <typename F>
+  __device__ __forceinline__ void edges(const RowView<T>& row, int k, F f) const {
+    const int j = (int)threadIdx.x + NT * kBatch * k, head = i0 < row.lo && i0 < i1 ? 0 : -1, tail = i1 > row.hi ? row.hi - i0 : -1;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int d = (e ? tail : head) - j;
+      if (d >= 0 && d < NT * kBatch && (d & (NT - 1)) == 0) f(d, i0 + j + d);
+    }
+  }
   // the thread's vectors of step k, from `slots` on, NT apart
   __device__ __forceinline__ void fetch(const RowView<T>& row, int k, uint4* slots) const {
     if (k < 0) {  // none, but a group of copies all the same
@@ -199,13 +206,16 @@ struct PartView {
       return;
     }
     const int i = i0 + (int)threadIdx.x + NT * kBatch * k;
+    const char* from = row.base + (size_t)i * 16;
     if (full(k)) {
-      const char* from = row.base + (size_t)i * 16;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) copy_async(slots + NT * u, from + (size_t)(NT * 16) * u);
-    } else {
+    } else if (k < steps) {
+      const int lowest = row.lo, end = min(i1, row.hi);
+#pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (i + NT * u < i1) row.fetch(slots + NT * u, i + NT * u);
+        if (i + NT * u >= lowest && i + NT * u < end) copy_async(slots + NT * u, from + (size_t)(NT * 16) * u);
+      edges(row, k, [&](int d, int e) { slots[d] = row.edge(e); });
     }
     copy_commit();
   }

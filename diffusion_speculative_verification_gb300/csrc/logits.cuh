@@ -134,21 +134,21 @@ struct RowView {
   __device__ __forceinline__ bool whole(int i) const { return i >= lo && i < hi; }
   __device__ __forceinline__ int first(int i) const { return i * kVec<T> - lead; }  // element at the vector's start
 
-  // an edge, element by element
+  // An edge, element by element.  Its loads depend on nothing, so that they take one way to memory and not one each.
   __device__ __noinline__ uint4 edge(int i) const {
-    uint32_t w[4] = {none_bits<T>(), none_bits<T>(), none_bits<T>(), none_bits<T>()};
     const int v0 = first(i);
+    uint32_t x[kVec<T>], w[4];
 #pragma unroll
     for (int e = 0; e < kVec<T>; ++e) {
-      const int v = v0 + e;
-      if (v < 0 || v >= V) continue;
-      if (sizeof(T) == 2) {
-        const uint32_t x = *(reinterpret_cast<const volatile uint16_t*>(row) + v);
-        w[(e / 2) & 3] = (e & 1) ? (w[(e / 2) & 3] & 0xFFFFu) | (x << 16) : (w[(e / 2) & 3] & 0xFFFF0000u) | x;
-      } else {
-        w[e & 3] = *(reinterpret_cast<const volatile uint32_t*>(row) + v);
-      }
+      const int v = min(max(v0 + e, 0), V - 1);
+      x[e] = sizeof(T) == 2 ? *(reinterpret_cast<const volatile uint16_t*>(row) + v)
+                            : *(reinterpret_cast<const volatile uint32_t*>(row) + v);
     }
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+      if (v0 + e < 0 || v0 + e >= V) x[e] = sizeof(T) == 2 ? none_bits<T>() & 0xFFFFu : none_bits<T>();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = sizeof(T) == 2 ? x[(2 * k) % kVec<T>] | x[(2 * k + 1) % kVec<T>] << 16 : x[k];
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ uint4 load(int i) const {

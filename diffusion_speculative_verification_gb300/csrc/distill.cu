@@ -23,11 +23,11 @@
 // Bound by HBM and by instructions alike: each logit is fetched from HBM once and
 // each gradient written once (4096 rows of 151936 bf16, K = 128: DRAM traffic at the
 // 2.49 GB that there are), 18 instructions per element at 2.6 per cycle.
-// Measured: that case 428 us, 87% of the copy rate (475 us with whole rows per CTA,
+// Measured: that case 424 us, 88% of the copy rate (475 us with whole rows per CTA,
 // which outgrow L2: 1.2 times the traffic; 677 us in quarters, whose ring and
 // target are too much for a part; 463 us with a ring of two steps; first steps again
 // first, a row per CTA: 534 us beside 492); 1024 rows, K = 64, 109 us (81%); 700 fp32
-// rows of 32003 35.7 us; the loss of 32 rows 6.6 us, latency.
+// rows of 32003 34.3 us; the loss of 32 rows 6.6 us, latency.
 //
 // ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
 // that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
@@ -42,7 +42,6 @@ namespace ssv {
 namespace {
 
 constexpr int kThreads = 512;                  // most threads that share a row's part
-constexpr int kParts = kThreads / 32 * kMaxCluster;  // warps of a cluster
 constexpr int kHash = 2 * kLogitsMaxTop;       // places of the table in which repeated tokens meet
 constexpr int kTeam = 2;                       // most warps that bring a target beside those that stream the row
 
@@ -414,10 +413,11 @@ __device__ __forceinline__ void write_zeros(const PartView<T>& part, T* out) {
   write_elements<T>(out, part.lo, part.hi, [](int) { return 0.f; });
 }
 
+template <int THREADS>
 struct Shared {
   Target tg;
   Slope slope;
-  uint32_t part[kParts][4];  // of every warp: maximum and sum (a pair) of its other tokens
+  uint32_t part[THREADS / 32 * kMaxCluster][4];  // of every warp: maximum and sum (a pair) of its other tokens
 };
 
 // Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 452 us, two 463, before the threads were known to the compiler).
@@ -425,12 +425,16 @@ template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
 // LOG_NT: 2^LOG_NT threads share a row, so that a step's addresses are constants apart (4096 rows 444 us where known at the
 // launch alone took 451); 0: as many as the launch says, for rows that are too short for them.  TEAM warps bring the target.
+// most threads that share a row, and how many CTAs of them an SM is to hold (fewer registers would spill)
+constexpr int most_threads(bool grad, int log_nt) { return grad && log_nt == 9 ? kThreads : kThreads / 2; }
+constexpr int ctas_per_sm(bool grad, int log_nt, int team) { return !grad ? 4 : log_nt == 9 ? 2 : team == 1 ? 4 : 3; }
+
 template <typename T, bool GRAD, int LOG_NT, int TEAM>
-__global__ void __launch_bounds__(kThreads + 32 * TEAM, 2) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(most_threads(GRAD, LOG_NT) + 32 * TEAM, ctas_per_sm(GRAD, LOG_NT, TEAM)) distill_kernel(const DistillParams p) {
   // a ring of slots; behind it a word per thread and step, whose bit (vector of the step, element) says that the
   // element is a listed token
   extern __shared__ __align__(128) unsigned char dynamic[];
-  __shared__ Shared sm;
+  __shared__ Shared<most_threads(GRAD, LOG_NT)> sm;
   // NT threads share the row, and the team behind them brings its target; the team's first warp joins the sums
   const int log_nt = LOG_NT ? LOG_NT : p.log_nt;
   const int tid = threadIdx.x, NT = 1 << log_nt, lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
@@ -729,13 +733,13 @@ ssv_status distill_check(const ssv_distill_args* a, DistillParams& p) {
   return SSV_OK;
 }
 
-// A row in parts of at most `bytes`, as far as `most` CTAs go; more of them while there are fewer CTAs than 152 SMs hold
-// at four each and a part has more than one step.  (Loss of 32 rows: 6.8 us at this limit, at half of it and at twice.)
-RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, int threads) {
+// A row in parts of at most `bytes`, as far as `most` CTAs go; more of them while all rows' are no more than `room` and a
+// part has more than one step.  (Loss of 32 rows: 6.6 us with room for four per SM, for two and for eight.)
+RowSplit distill_split(int rows, int V, int element_size, int bytes, int most, int threads, int room) {
   const int vectors = row_vectors(V, element_size);
   int c = 1;
   while (c < most && (vectors + c - 1) / c > bytes / 16) c *= 2;
-  while (c < most && (long long)rows * c * 2 <= 608 && vectors > 4 * c * threads) c *= 2;
+  while (c < most && (long long)rows * c * 2 <= room && vectors > 4 * c * threads) c *= 2;
   return split_of(vectors, c, threads);
 }
 
@@ -746,27 +750,37 @@ cudaError_t distill_launch_as(const DistillParams& p, int n, const RowSplit& sp,
   return e != cudaSuccess ? e : launch_rows(distill_kernel<T, GRAD, LOG_NT, TEAM>, n, sp, sp.threads + 32 * TEAM, smem, st, p);
 }
 
+template <typename T, bool GRAD, int TEAM>
+cudaError_t distill_launch_team(const DistillParams& p, int n, const RowSplit& sp, size_t smem, cudaStream_t st) {
+  if constexpr (GRAD)
+    if (sp.log_nt == 9) return distill_launch_as<T, GRAD, 9, TEAM>(p, n, sp, smem, st);
+  return sp.log_nt == 8 ? distill_launch_as<T, GRAD, 8, TEAM>(p, n, sp, smem, st)
+                        : distill_launch_as<T, GRAD, 0, TEAM>(p, n, sp, smem, st);
+}
+
 template <typename T, bool GRAD>
 cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   // With the gradient parts of 160 KB: two CTAs per SM then have 46 MB of rows on their way, which L2 holds, and 512
-  // threads make the most of a part's fixed cost (4096 rows: see above).  The loss alone reads a row once: no limit, and
-  // 256 threads (32 rows: 6.8 us; 512 threads 8.3 us).
-  const RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 160 * 1024 : 1 << 20, kMaxCluster, GRAD ? 512 : 256);
+  // threads make the most of a part's fixed cost (4096 rows: 426 us; 256 threads 465 us).  Parts of up to 128 KB go to 256
+  // threads, in which steps are shorter and one CTA's barriers are other CTAs' time (rows of 100277 bf16: 147 us with 512
+  // threads, 124 with 256; of 9001 fp32: 27 and 20 us).  The loss alone reads a row once: no limit, and 256 threads (32
+  // rows: 6.6 us; 512 threads 8.3 us).
+  // Short ones are as many as fit an SM at a time (64 rows of 151936 bf16, K = 64: 12.2 us, 18.9 where one fewer fits;
+  // 150, K = 128: 17.9 us, 24.0 with one more).
+  const int per_sm = GRAD && p.K > 64 ? 3 : 4;
+  RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 160 * 1024 : 1 << 20, kMaxCluster, 256, 152 * per_sm);
+  if (GRAD && sp.vectors > 128 * 1024 / 16) sp = split_of(row_vectors(p.V, sizeof(T)), sp.ctas, 512);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
   p.slot_bytes = 16 * kStages<GRAD> * kBatch * sp.threads + kSlotSlack;
   const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
-  constexpr int kWide = GRAD ? 9 : 8;
   // The target is as long on its way as the row's first reading where a warp has four tokens per lane: two warps for more
   // than 64 tokens (4096 rows, K = 128: 428 us; one warp 444, four 435, whose registers do not suffice), one for fewer (1024
   // rows, K = 64: 109 us; two 111) and for the loss, of whose 256 threads two take more room (32 rows, K = 32: 6.6 us; two
   // 7.8).
   if constexpr (GRAD)
-    if (p.K > 64)
-      return sp.log_nt == kWide ? distill_launch_as<T, GRAD, kWide, 2>(p, n, sp, smem, st)
-                                : distill_launch_as<T, GRAD, 0, 2>(p, n, sp, smem, st);
-  return sp.log_nt == kWide ? distill_launch_as<T, GRAD, kWide, 1>(p, n, sp, smem, st)
-                            : distill_launch_as<T, GRAD, 0, 1>(p, n, sp, smem, st);
+    if (p.K > 64) return distill_launch_team<T, GRAD, 2>(p, n, sp, smem, st);
+  return distill_launch_team<T, GRAD, 1>(p, n, sp, smem, st);
 }
 
 template <typename T>
@@ -774,7 +788,7 @@ cudaError_t backward_launch(DistillParams& p, int n, cudaStream_t st) {
   static uint64_t done = 0;
   // (1500 fp32 rows: 248 us in parts of 48 KB and of 24, 276 us in parts of 96; 265 us with 256 threads, for whom a
   // part's fixed cost is too much)
-  const RowSplit sp = distill_split(n, p.V, sizeof(T), 48 * 1024, 64, 128);
+  const RowSplit sp = distill_split(n, p.V, sizeof(T), 48 * 1024, 64, 128, 608);
   p.log_c = sp.log_c;
   p.log_nt = sp.log_nt;
   const size_t smem = 16 * (size_t)sp.vectors + kSlotSlack;

@@ -33,11 +33,11 @@
 // latency in the short ones: one dependent load, the first copies, a step, two
 // cluster barriers and the ranking of the alternatives.  CTAs are small, so
 // that six on an SM keep copies in flight while some rank.
-// Measured: 8192 rows of 151936 bf16 without alternatives 379 us, 98% of the copy
+// Measured: 8192 rows of 151936 bf16 without alternatives 374 us, 99% of the copy
 // rate (391 us with the threads known at the launch alone; then registers for seven
 // CTAs per SM 430 us, loads into registers 403 us, 256 threads 417 us); 960
 // fp32 rows, 30% of them idle, with 32 alternatives 74 us, 84% (256 threads 86 us;
-// rows in halves 92 us); 64 rows with 20 alternatives 13.6 us; one row 9.7 us; 300
+// rows in halves 92 us); 64 rows with 20 alternatives 13.2 us; one row 9.7 us; 300
 // rows of 9001 fp32, nine tenths masked, with 64 alternatives 14 us.
 #include "logits.cuh"
 
@@ -249,8 +249,8 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
   __syncthreads();
 }
 
-// LOG_NT: 2^LOG_NT threads in a CTA, so that a step's addresses are constants apart (8192 rows 379 us; known at the launch
-// alone, 391 us); 0: as many as the launch says, for short rows.
+// LOG_NT: 2^LOG_NT threads in a CTA, so that a step's addresses are constants apart (8192 rows 379 us where known at the
+// launch alone took 391); 0: as many as the launch says, for short rows.
 template <typename T, bool TOP, int LOG_NT>
 __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LogprobsParams p) {
   extern __shared__ __align__(128) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum

@@ -237,6 +237,16 @@ def test_listed_more_than_once(mode):
     check(z, token, value, W.F32, mode)
 
 
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("K", [20, 128])
+def test_long_parts(K, dtype):
+    """Parts above 128 KB: blocks of 512 threads, apart from the logits and in place."""
+    r = np.random.default_rng(K)
+    for v, lead in (((1 << 19) - 3, 3), (1 << 19, 0)):
+        check(*make(r, 1, v, K), dtype, ssv.REST, lead=lead, in_place=True)
+        check(*make(r, 1, v, K), dtype, ssv.RENORM, lead=lead, grad_lead=5, grad_pad=2)
+
+
 @pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("dtype", [W.F32, W.BF16])
 @pytest.mark.parametrize("K", [64, 65, 96, 97, 127, 128])

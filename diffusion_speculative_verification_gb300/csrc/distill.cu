@@ -22,7 +22,7 @@
 // written over what the others' formula left there.
 // Bound by HBM and by instructions alike: each logit is fetched from HBM once and
 // each gradient written once (4096 rows of 151936 bf16, K = 128: DRAM traffic at the
-// 2.49 GB that there are), 18 instructions per element at 2.6 per cycle.
+// 2.49 GB that there are), 18 instructions per element at 2.5 per cycle.
 // Measured: that case 424 us, 88% of the copy rate (475 us with whole rows per CTA,
 // which outgrow L2: 1.2 times the traffic; 677 us in quarters, whose ring and
 // target are too much for a part; 463 us with a ring of two steps; first steps again
@@ -31,8 +31,8 @@
 //
 // ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
 // that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
-// little above a copy (parts of 96 KB 276 us); 2000 rows of 9001 bf16, padded, 12.1
-// us; 32 rows of 151936 bf16 5.4 us.
+// little above a copy (parts of 96 KB 276 us); 2000 rows of 9001 bf16, padded, 12.0
+// us; 32 rows of 151936 bf16 5.2 us.
 #include "logits.cuh"
 
 #include <algorithm>
@@ -420,7 +420,7 @@ struct Shared {
   uint32_t part[THREADS / 32 * kMaxCluster][4];  // of every warp: maximum and sum (a pair) of its other tokens
 };
 
-// Steps in flight: three with the gradient, which find the last 30% of a part of 160 KB there (4096 rows: 452 us, two 463, before the threads were known to the compiler).
+// Steps in flight: three with the gradient, which find the last three fifths of a part of 152 KB there (4096 rows: 428 us; two 433).
 template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
 // LOG_NT: 2^LOG_NT threads share a row, so that a step's addresses are constants apart (4096 rows 444 us where known at the
@@ -430,7 +430,8 @@ constexpr int most_threads(bool grad, int log_nt) { return grad && log_nt == 9 ?
 constexpr int ctas_per_sm(bool grad, int log_nt, int team) { return !grad ? 4 : log_nt == 9 ? 2 : team == 1 ? 4 : 3; }
 
 template <typename T, bool GRAD, int LOG_NT, int TEAM>
-__global__ void __launch_bounds__(most_threads(GRAD, LOG_NT) + 32 * TEAM, ctas_per_sm(GRAD, LOG_NT, TEAM)) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(most_threads(GRAD, LOG_NT) + 32 * TEAM, ctas_per_sm(GRAD, LOG_NT, TEAM))
+    distill_kernel(const DistillParams p) {
   // a ring of slots; behind it a word per thread and step, whose bit (vector of the step, element) says that the
   // element is a listed token
   extern __shared__ __align__(128) unsigned char dynamic[];
@@ -761,11 +762,11 @@ cudaError_t distill_launch_team(const DistillParams& p, int n, const RowSplit& s
 template <typename T, bool GRAD>
 cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   // With the gradient parts of 160 KB: two CTAs per SM then have 46 MB of rows on their way, which L2 holds, and 512
-  // threads make the most of a part's fixed cost (4096 rows: 426 us; 256 threads 465 us).  Parts of up to 128 KB go to 256
+  // threads make the most of a part's fixed cost (4096 rows: 424 us; 256 threads 465 us).  Parts of up to 128 KB go to 256
   // threads, in which steps are shorter and one CTA's barriers are other CTAs' time (rows of 100277 bf16: 147 us with 512
   // threads, 124 with 256; of 9001 fp32: 27 and 20 us).  The loss alone reads a row once: no limit, and 256 threads (32
   // rows: 6.6 us; 512 threads 8.3 us).
-  // Short ones are as many as fit an SM at a time (64 rows of 151936 bf16, K = 64: 12.2 us, 18.9 where one fewer fits;
+  // Short parts are as many as fit an SM at a time (64 rows of 151936 bf16, K = 64: 12.2 us, 18.9 where one fewer fits;
   // 150, K = 128: 17.9 us, 24.0 with one more).
   const int per_sm = GRAD && p.K > 64 ? 3 : 4;
   RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 160 * 1024 : 1 << 20, kMaxCluster, 256, 152 * per_sm);

@@ -192,7 +192,8 @@ struct PartView {
   // behind its first (a row of one vector may have it twice)
   template <typename F>
   __device__ __forceinline__ void edges(const RowView<T>& row, int k, F f) const {
-    const int j = (int)threadIdx.x + NT * kBatch * k, head = i0 < row.lo && i0 < i1 ? 0 : -1, tail = i1 > row.hi ? row.hi - i0 : -1;
+    const int j = (int)threadIdx.x + NT * kBatch * k;
+    const int head = i0 < row.lo && i0 < i1 ? 0 : -1, tail = i1 > row.hi ? row.hi - i0 : -1;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int d = (e ? tail : head) - j;

@@ -32,7 +32,7 @@
 // ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
 // that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
 // little above a copy (parts of 96 KB 276 us); 2000 rows of 9001 bf16, padded, 12.0
-// us; 32 rows of 151936 bf16 5.2 us.
+// us; 32 rows of 151936 bf16 5.6 us.
 #include "logits.cuh"
 
 #include <algorithm>
@@ -119,12 +119,11 @@ __device__ __forceinline__ void team_sync() {
 }
 
 // The team's entries to shared memory: `row` their logits, those of [lo, hi) alone (the others are not asked for).
-// LOSS: with what a loss needs, the rest to more than 32 bits and the sum over the listed tokens.
+// LOSS: with what a loss needs, the sum over the listed tokens.
 template <bool LOSS, typename T, int TEAM>
 __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM>& l, const T* row, int lo, int hi,
                                              Target& tg) {
   constexpr int kEach = Listed<TEAM>::kEach;
-  constexpr bool EXACT = LOSS || sizeof(T) == 4;  // a bf16 gradient would not show it
   const int lane = threadIdx.x & 31;
   float z[kEach];
 #pragma unroll
@@ -148,6 +147,11 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM
   twice = __any_sync(0xffffffffu, twice);
   // probabilities: relative to the largest for a softmax; as they are where they are log-probabilities
   const bool as_is = p.mode == SSV_DISTILL_REST;
+  // What an exponential rounded to 32 bits is off by, from its logarithm: the rest is what the sum leaves of 1, and the other
+  // tokens' gradient is what r leaves of u, so that bf16 shows it too (r of 1e-6 would be off by up to 7%; 32 rows bf16 5.2
+  // us without, 5.6 with it).  Without a rest it is no more than what the drafter's own exponentials are off by (2000 rows
+  // of 9001 bf16: 12.0 us without, 13.0 with it).
+  const bool exact = LOSS || sizeof(T) == 4 || as_is;
   float mx = -INFINITY, top = -INFINITY, e[kEach], off[kEach];
   Pair all = {0.f, 0.f};
 #pragma unroll
@@ -177,9 +181,7 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM
     e[k] = off[k] = 0.f;
     if (l.none(k, p.K)) continue;
     e[k] = expf(l.t[k] - ref);
-    // what an exponential rounded to 32 bits is off by, from its logarithm: the rest is what the sum leaves of 1, and a
-    // gradient what a probability leaves of another
-    if (EXACT && e[k] > 0.f) off[k] = e[k] * value_of(two_sum(l.t[k], -ref) + -log_sum(e[k]));
+    if (exact && e[k] > 0.f) off[k] = e[k] * value_of(two_sum(l.t[k], -ref) + -log_sum(e[k]));
     all = all + Pair{e[k], off[k]};
   }
   all = warp_sum(all);

@@ -1,0 +1,93 @@
+"""The rest of a distillation target to its own digits: r and u far below 1 and next to each other, where the other tokens'
+gradient is a multiple of their small difference.
+
+Tolerances of that gradient, (w / T) (q_v / u) (P u - r), derived before any run (logits_common: a sum is within LN of itself,
+so that the share q_v / u and u are within 2 LN of themselves).  r = 1 - sum p, from exponentials that are off by what their
+logarithms are: below 2^-30, and below 2^-23 of the logarithm itself where that is small (log_sum's series starts with it);
+the pairs' additions by 2^-46; then r is rounded to fp32 and enters a difference that is rounded once."""
+import numpy as np
+import pytest
+import torch
+
+from diffusion_speculative_verification_gb300 import ssv, workloads as W
+import oracle.distill as odist
+from gpu_common import ensure_built
+from logits_common import EPS, LN, near, store
+from test_gpu_distill import half_step
+
+pytestmark = pytest.mark.gpu
+
+
+def setup_module():
+    ensure_built()
+
+
+def rest_error(value):
+    """What the kernel's r is off by, before it is rounded, for a row's fp32 log-probabilities."""
+    t = np.asarray(value, np.float64)
+    t = t[t > -np.inf]
+    return float(np.sum(np.exp(t) * np.minimum(2.0 ** -30, 2.0 ** -23 * np.abs(t))) + 2.0 ** -46)
+
+
+def sharp(r, n, v, K, rest, factor, dtype, T, spread):
+    """Drafter rows whose unlisted tokens have about factor * rest together, and targets that leave them `rest`; `spread`:
+    the listed probability over the first three tokens, else nearly all on the first.  (logits as the dtype has them,
+    token, value)"""
+    z = r.standard_normal((n, v))
+    token = np.stack([r.permutation(v)[:K] for _ in range(n)]).astype(np.int32)
+    p = np.full((n, K), rest / 4 / K)
+    head = min(K, 3) if spread else 1
+    p[:, :head] = (1 - rest - p[:, head:].sum(1, keepdims=True)) * (np.array([0.5, 0.3, 0.2])[:head] / np.array([0.5, 0.3, 0.2])[:head].sum()
+                                                                    if spread else 1.0)
+    others = np.ones((n, v), bool)
+    np.put_along_axis(others, token.astype(np.int64), False, 1)
+    s = np.where(others, np.exp(z / T), 0).sum(1)
+    c = T * np.log(s * (1 - factor * rest) / (factor * rest))
+    np.put_along_axis(z, token.astype(np.int64), T * np.log(p) + c[:, None] + 0.01 * r.standard_normal((n, K)), 1)
+    ref, t = store(z, dtype)
+    # the target again, so that u is `factor` times its rest with the logits as they have been rounded
+    for i in range(n):
+        x = (ref[i] - ref[i].max()) / T
+        u = np.exp(x[others[i]]).sum() / np.exp(x).sum()
+        p[i, head:] = u / factor / 4 / K
+        p[i, :head] *= (1 - u / factor - p[i, head:].sum()) / p[i, :head].sum()
+    return ref, t, token, np.log(p).astype(np.float32)
+
+
+def other_gradient(ref, token, value, T, w):
+    """(gradient [n, V] in 64 bits; of the unlisted tokens its tolerance before the last rounding; how far it may move with
+    the order in which the target's sum is formed; unlisted [n, V])."""
+    n, v = ref.shape
+    grad, tol, same, unlisted = np.zeros((n, v)), np.zeros((n, v)), np.zeros((n, v)), np.ones((n, v), bool)
+    for i in range(n):
+        _, grad[i], stats = odist.row_distill(ref[i], token[i], value[i], T, odist.REST, w)
+        p, listed, r = odist.target(token[i], value[i], odist.REST, v)
+        unlisted[i] = ~listed
+        u, P = np.exp(odist.log_rest(stats, T)), p.sum() + r
+        share = np.exp((ref[i] - stats[2]) / T) / stats[3]
+        tol[i] = share * abs(w / T) * (2 * LN * abs(P * u - r) + 2 * LN * P * u + rest_error(value[i]) + 4 * EPS * (r + u))
+        q = np.exp((ref[i] - stats[0]) / T) / stats[1]
+        same[i] = abs(w / T) * np.where(listed, 4 * EPS * (P * q + p), share * (2.0 ** -45 + 4 * EPS * (r + u)))
+    return grad, tol, same, unlisted
+
+
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("rest", [1e-3, 1e-5, 1e-6])
+def test_gradient_of_a_small_rest(rest, spread, dtype):
+    """Target and drafter leave the others little, one a fifth more than the other: both entry points give the gradient of
+    the difference, and the same one."""
+    r = np.random.default_rng(40)
+    T, w = 1.5, 0.25
+    for v, K, factor in ((500, 2, 1.2), (3001, 20, 0.8), (20000, 100, 1.2), (60000, 128, 2.0)):
+        ref, t, token, value = sharp(r, 4, v, K, rest, factor, dtype, T, spread)
+        want, tol, same, others = other_gradient(ref, token, value.astype(np.float64), T, w)
+        a = [torch.tensor(token, device="cuda"), torch.tensor(value, device="cuda"), T, ssv.REST]
+        wt = torch.full((4,), w, device="cuda")
+        _, stats, fused = ssv.distill(t, *a, wt, grad=True)
+        back = ssv.distill_backward(t, *a[:2], stats, None, *a[2:], wt)
+        for g in (fused, back):
+            g = g.float().cpu().numpy().astype(np.float64)
+            near(g[others], want[others], (tol + half_step(want, dtype))[others])
+        # the same formula on the same statistics
+        near(back.float().cpu().numpy(), fused.float().cpu().numpy().astype(np.float64), same + 2 * half_step(want, dtype))

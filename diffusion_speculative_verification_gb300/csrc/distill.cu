@@ -270,6 +270,12 @@ struct Sums {
   __device__ __forceinline__ bool empty() const { return none() && S == 0.f; }           // the row is all -inf
 };
 
+// e^x: -inf has no low part; NaN stays
+__device__ __forceinline__ float exp_of(Pair x) {
+  const float e = expf(x.hi);
+  return e > 0.f ? fmaf(e, x.lo, e) : e;
+}
+
 // The gradient's coefficients.
 struct Slope {
   float ref, coef;   // other tokens: coef 2^((z - ref) sc)
@@ -283,7 +289,9 @@ __device__ __forceinline__ Slope slope_of(const Sums& s, const Mass& t, const Sc
   Slope k;
   k.wT = w * T.hi;
   k.ref = s.none() ? 0.f : s.mr;
-  k.coef = s.none() ? 0.f : k.wT * (P * (expf((s.mr - s.m) * T.hi) * (s.Sr / s.S)) - rest) / s.Sr;
+  // P u - r is a small difference where the drafter has come near its target: u's exponent to more than 32 bits
+  const float u = exp_of(two_sum(s.mr, -s.m) * Pair{T.hi, T.lo}) * (s.Sr / s.S);
+  k.coef = s.none() ? 0.f : k.wT * fmaf(P, u, -rest) / s.Sr;
   k.top = s.m;
   k.share = P / s.S;
   k.empty = s.empty();
@@ -404,8 +412,7 @@ __device__ __forceinline__ void write_listed(const DistillParams& p, const PartV
   for (int j = threadIdx.x; j < p.K; j += blockDim.x) {
     const int v = tg.token[j];
     if (v < part.lo || v >= part.hi) continue;
-    const Pair x = two_sum(tg.z[j], -k.top) * Pair{p.T.hi, p.T.lo};
-    const float e = expf(x.hi), q = k.share * (e > 0.f ? fmaf(e, x.lo, e) : e);  // -inf has no low part; NaN stays
+    const float q = k.share * exp_of(two_sum(tg.z[j], -k.top) * Pair{p.T.hi, p.T.lo});
     out[v] = Elem<T>::from_f32(k.wT * (q - tg.p[j]));
   }
 }

@@ -91,3 +91,39 @@ def test_gradient_of_a_small_rest(rest, spread, dtype):
             near(g[others], want[others], (tol + half_step(want, dtype))[others])
         # the same formula on the same statistics
         near(back.float().cpu().numpy(), fused.float().cpu().numpy().astype(np.float64), same + 2 * half_step(want, dtype))
+
+
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("T", [0.3, 0.7, 1.0, 1.5, 3.0])
+def test_gradient_next_to_the_target(T, dtype):
+    """One listed token and others that are all equal, 26 T .. 85 T below: sums are whole numbers and probabilities their
+    logarithms' exponentials, so that u = S' e^-gap / S is off by the exponential (2 eps), its low part, S, the quotient, the
+    product and P alone, r = -expm1(t) by its rounding.  They are next to each other, and the gradient is their difference.
+    The exponent is a difference of fp32 numbers times 1 / T: as one product in fp32 it would be off by up to 85 eps."""
+    r = np.random.default_rng(41)
+    n, v, K = 48, 3001, 20
+    T = float(np.float32(T))
+    m = r.standard_normal(n) * 3
+    z = np.repeat((m - T * np.linspace(26, 85, n))[:, None], v, 1)
+    token = np.full((n, K), -1, np.int32)
+    token[:, 7] = r.integers(0, v, n)
+    at = (np.arange(n), token[:, 7])
+    z[at] = m
+    ref, t = store(z, dtype)
+    low = ref[np.arange(n), (token[:, 7] + 1) % v]
+    s = (v - 1) * np.exp((low - ref[at]) / T)
+    u = s / (1 + s)
+    value = np.full((n, K), -1.0, np.float32)
+    apart = 1.001 if dtype == W.F32 else 1.00003        # bf16 shows an error only where it is multiplied by more
+    value[:, 7] = np.log1p(-u / apart)
+    rest = -np.expm1(value[:, 7].astype(np.float64))
+    w = 2.0 ** 60                                       # brings the smallest back into fp32's range
+    want = (u - rest) / (v - 1) * (w / T)
+    tol = ((2 + 5) * EPS * u + 2 * EPS * rest + 4 * EPS * np.abs(u - rest)) / (v - 1) * (w / T) + half_step(want, dtype)
+    a = [torch.tensor(token, device="cuda"), torch.tensor(value, device="cuda")]
+    wt = torch.full((n,), w, device="cuda")
+    _, stats, fused = ssv.distill(t, *a, T, ssv.REST, wt, grad=True)
+    assert (stats[:, 3] == v - 1).all()
+    back = ssv.distill_backward(t, *a, stats, None, T, ssv.REST, wt)
+    for g in (fused, back):
+        near(g.float().cpu().numpy()[np.arange(n), (token[:, 7] + 1) % v], want, tol)

@@ -68,11 +68,12 @@ struct Mass {
   float sum, rest;  // sum p, r
 };
 
-// The target of a row: listed tokens (-1: absent), each once, their probabilities and the logarithms of these, and the
-// drafter's logits of them.
+// The target of a row: listed tokens (-1: absent), each once, their probabilities and (for a loss) the logarithms of these,
+// as pairs, and the drafter's logits of them.
 struct Target {
   int token[kLogitsMaxTop];
-  float p[kLogitsMaxTop], t[kLogitsMaxTop], z[kLogitsMaxTop];
+  float p[kLogitsMaxTop], z[kLogitsMaxTop];
+  Pair t[kLogitsMaxTop];
   int hash[kHash];
   Mass mass;
   float top;        // largest of z
@@ -193,13 +194,14 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM
     for (int o = 1; o < TEAM; ++o) all = all + tg.team_all[o];
   }
   const float s = value_of(all);
-  const float norm = as_is || s == 0.f ? 1.f : s, ln = as_is || s == 0.f ? 0.f : value_of(log_sum(all));
+  const float norm = as_is || s == 0.f ? 1.f : s;
+  const Pair ln = as_is || s == 0.f ? Pair{0.f, 0.f} : log_sum(all);
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     if (l.none(k, p.K)) break;
     const float q = e[k] / norm;
     e[k] = as_is || !(s < INFINITY) ? e[k] + off[k] : q + (fmaf(-q, all.hi, e[k]) + (off[k] - q * all.lo)) / norm;
-    l.t[k] = l.t[k] - ref - ln;
+    if (LOSS) tg.t[l.at(k)] = two_sum(l.t[k], -ref) + -ln;
   }
   if (twice) {  // the first of equal tokens takes the others' probabilities
 #pragma unroll
@@ -219,11 +221,10 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM
           break;
         }
         e[k] += tg.p[o];
-        l.t[k] = logf(e[k]);
+        if (LOSS) tg.t[j] = log_sum(e[k]);
       }
       if (l.v[k] < 0) {
         e[k] = 0.f;
-        l.t[k] = -INFINITY;
         z[k] = -INFINITY;
       }
     }
@@ -235,7 +236,6 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM
     const int j = l.at(k);
     tg.token[j] = l.v[k];
     tg.p[j] = e[k];
-    tg.t[j] = l.t[k];
     tg.z[j] = z[k];
   }
   if (LOSS) {
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(most_threads(GRAD, LOG_NT) + 32 * TEAM, ctas_p
       if (pj > 0.f || pj != pj) {
         // ln p - ln q, a small difference of large numbers: rounded once
         const Pair q = two_sum(tg.z[j], -sums.m) * inv + -lnS;
-        loss = loss + Pair{pj, 0.f} * Pair{value_of(Pair{tg.t[j], 0.f} + -q), 0.f};
+        loss = loss + Pair{pj, 0.f} * Pair{value_of(tg.t[j] + -q), 0.f};
       }
     }
     loss = warp_sum(loss);

@@ -258,16 +258,18 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM
   }
 }
 
-// r, where the drafter leaves the other tokens nothing (every one is listed or masked): there, what the roundings of
-// fp32 log-probabilities leave of 1 is no probability of other tokens.
-__device__ __forceinline__ float rest_of(const Mass& t, bool none) { return none && t.rest < 0x1p-20f ? 0.f : t.rest; }
-
 // What a row's softmax needs: maximum and sum, relative to it, over the row and over the tokens that are not listed.
 struct Sums {
   float m, S, mr, Sr;
 
   __device__ __forceinline__ bool none() const { return mr == -INFINITY && Sr == 0.f; }  // nothing is left to the others
   __device__ __forceinline__ bool empty() const { return none() && S == 0.f; }           // the row is all -inf
+  // r.  Where the drafter leaves the other tokens nothing (every one is listed or masked, with -inf or with a number more
+  // than 100 T below the row's largest: u is below 2^19 e^-100), what the roundings of fp32 log-probabilities leave of 1 is
+  // no probability of theirs: its loss would be the mask's own size.
+  __device__ __forceinline__ float rest_of(const Mass& t, const Scale& T) const {
+    return t.rest < 0x1p-20f && !((mr - m) * T.hi >= -100.f) ? 0.f : t.rest;  // (NaN where the row has nothing, or a NaN)
+  }
 };
 
 // e^x: -inf has no low part; NaN stays
@@ -285,7 +287,7 @@ struct Slope {
 };
 
 __device__ __forceinline__ Slope slope_of(const Sums& s, const Mass& t, const Scale& T, float w) {
-  const float rest = rest_of(t, s.none()), P = t.sum + rest;
+  const float rest = s.rest_of(t, T), P = t.sum + rest;
   Slope k;
   k.wT = w * T.hi;
   k.ref = s.none() ? 0.f : s.mr;
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(most_threads(GRAD, LOG_NT) + 32 * TEAM, ctas_p
     }
     loss = warp_sum(loss);
     if (lane == 0) {
-      const float rest = rest_of(tg.mass, sums.none()), P = tg.mass.sum + rest;
+      const float rest = sums.rest_of(tg.mass, p.T), P = tg.mass.sum + rest;
       // a share of more than half from what is listed: the difference of two logarithms would be off by their rounding
       const Pair ln_u = listed_share < 0.5f ? Pair{log1pf(-listed_share), 0.f}
                         : sums.none()       ? Pair{-INFINITY, 0.f}

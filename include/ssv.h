@@ -942,8 +942,10 @@ SSV_API ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream);
  *   SSV_DISTILL_RENORM: p_j = exp(t_j) / sum exp(t), r = 0 (so that logits
  *                       divided by T serve as well as log-probabilities)
  *   SSV_DISTILL_REST:   p_j = exp(t_j), r = max(0, 1 - sum p): the target's
- *                       probability of all other tokens together (where u = 0, an
- *                       r below 2^-20, left by the roundings of t, counts as 0)
+ *                       probability of all other tokens together (where the drafter
+ *                       leaves them nothing, each being -inf or more than 100 T below
+ *                       the row's largest logit as a masked one is, an r below 2^-20,
+ *                       left by the roundings of t, counts as 0)
  *   q = softmax(z / T), u = sum of q over the tokens that are not listed
  *   loss[i] = w [ sum_j p_j (ln p_j - ln q_j) + r (ln r - ln u) ]
  * (terms of probability 0 add nothing), the divergence of q from p with the

@@ -36,7 +36,7 @@ def row_distill(z: np.ndarray, token: np.ndarray, value: np.ndarray, T: float, m
     if weight == 0:
         return 0.0, np.zeros(V), np.zeros(4)
     p, listed, r = target(np.asarray(token), value, mode, V)
-    if r < 2.0 ** -20 and (z[~listed] == -np.inf).all():
+    if r < 2.0 ** -20 and not (z[~listed] >= z.max() - 100 * T).any():
         r = 0.0                                    # the drafter leaves the others nothing: a rounding of the list
     P = p.sum() + r
     if (z == -np.inf).all():
@@ -48,7 +48,7 @@ def row_distill(z: np.ndarray, token: np.ndarray, value: np.ndarray, T: float, m
     others = z[~listed]
     mo = others.max() if len(others) else -np.inf
     So = np.exp((others - mo) / T).sum() if mo > -np.inf else 0.0
-    with np.errstate(divide="ignore", invalid="ignore"):
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):   # share: of the others alone
         ln_u = (mo - m) / T + np.log(So) - np.log(S)
         loss = np.sum(np.where(p > 0, p * (np.log(np.where(p > 0, p, 1.0)) - logq), 0.0))
         if r > 0:

@@ -127,3 +127,34 @@ def test_gradient_next_to_the_target(T, dtype):
     back = ssv.distill_backward(t, *a, stats, None, T, ssv.REST, wt)
     for g in (fused, back):
         near(g.float().cpu().numpy()[np.arange(n), (token[:, 7] + 1) % v], want, tol)
+
+
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("T", [0.7, 2.0])
+def test_finite_masks(T, dtype):
+    """Tokens masked with a number instead of -inf, on both sides: what the roundings of the target's log-probabilities leave
+    of 1 is nobody's, and loss and gradient are those of the same rows masked with -inf."""
+    r = np.random.default_rng(43)
+    n, v, K = 8, 3001, 6
+    for mask in (-1e3, -1e4, -1e9, -3.3895314e38):
+        z = np.full((n, v), mask)
+        legal = np.stack([r.permutation(v)[:3] for _ in range(n)])
+        np.put_along_axis(z, legal, r.standard_normal((n, 3)) * 2, 1)
+        target = z.copy()
+        np.put_along_axis(target, legal, np.take_along_axis(z, legal, 1) + 0.3 * r.standard_normal((n, 3)), 1)
+        ref, x = store(z, dtype)
+        *_, value, token = ssv.logprobs(store(target, dtype)[1], None, K, T)
+        value[:, :3] += torch.tensor(np.log1p(-5e-7) * r.random((n, 1)), dtype=torch.float32, device="cuda")
+        assert (value.double().exp().sum(1) < 1).any()
+        hidden = torch.where(x < -900, float("-inf"), x)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        want = ssv.distill(hidden, token, value, T, ssv.REST, grad=True, dev_status=status)
+        loss, stats, grad = ssv.distill(x, token, value, T, ssv.REST, grad=True, dev_status=status)
+        back = ssv.distill_backward(x, token, value, stats, None, T, ssv.REST, dev_status=status)
+        assert ssv.get_status(status) == ssv.SSV_OK
+        assert want[0].isfinite().all() and torch.equal(loss, want[0])
+        assert torch.equal(grad, want[2])
+        near(back.float().cpu().numpy(), grad.float().cpu().numpy().astype(np.float64),
+             2 * half_step(grad.float().cpu().numpy().astype(np.float64), dtype) + 2.0 ** -21)
+        own, _, _ = odist.distill_batch(ref, token.cpu().numpy(), value.double().cpu().numpy(), T, odist.REST)
+        near(loss.cpu().numpy(), own, 4 * LN * (1 + np.abs(own)))

@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(most_threads(GRAD, LOG_NT) + 32 * TEAM, ctas_p
       if (rest > 0.f) loss = loss + Pair{rest, 0.f} * Pair{value_of(log_sum(rest) + -ln_u), 0.f};
       float l = w * value_of(loss);
       if (sums.S != sums.S) l = sums.S;
-      if (sums.empty()) l = P == 0.f ? 0.f : w * INFINITY;  // no token of the target has a chance
+      if (sums.empty()) l = P == 0.f ? 0.f : w * (INFINITY * P);  // no token of the target has a chance; NaN stays
       p.loss[entry] = l;
       if (p.stats) {
         float* to = p.stats + 4 * (size_t)entry;

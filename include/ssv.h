@@ -965,11 +965,11 @@ SSV_API ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream);
  * overlaps no other argument; fastest where its rows lie to 16-byte boundaries
  * as the logits' do.  Elements between rows are not written.
  * A row of weight 0 is not read: its loss, statistics and gradient are 0.
- * A row with a NaN (or +inf) in its logits, or a NaN in its target, gives NaN in its loss and
- * gradient.  A listed token with p > 0 and logit -inf, or r > 0 with u = 0,
- * gives the loss +inf (the gradient stays finite); so does a row of nothing but
- * -inf, whose gradient is 0.  A row whose listed tokens are all absent has the
- * loss and gradient 0.
+ * A row with a NaN (or +inf) in its logits, or a NaN in its target, gives NaN in
+ * its loss and gradient.  A listed token with p > 0 and logit -inf, or r > 0 with
+ * u = 0, gives the loss +inf (the gradient stays finite); so does a row of nothing
+ * but -inf, whose gradient is 0 whatever its target.  Any other row whose listed
+ * tokens are all absent has the loss and gradient 0.
  * Sums over a row are fp32 per thread and joined in 48 bits; u is summed from the
  * tokens that are not listed; the loss, a small difference of logarithms, is
  * formed in 48 bits and rounded once.  The gradient is formed in fp32 and

@@ -22,7 +22,7 @@ def target(token: np.ndarray, value: np.ndarray, mode: int, V: int):
         w = np.exp(t)
         r = max(0.0, 1.0 - w.sum())
     else:
-        w = np.exp(t - t.max()) if len(t) and t.max() > -np.inf else np.zeros(len(t))
+        w = np.exp(t - t.max()) if len(t) and t.max() != -np.inf else np.zeros(len(t))
         w = w / w.sum() if w.sum() > 0 else w
         r = 0.0
     np.add.at(p, token[there], w)
@@ -40,7 +40,7 @@ def row_distill(z: np.ndarray, token: np.ndarray, value: np.ndarray, T: float, m
         r = 0.0                                    # the drafter leaves the others nothing: a rounding of the list
     P = p.sum() + r
     if (z == -np.inf).all():
-        return (weight * np.inf if P > 0 else 0.0), np.zeros(V), np.array([-np.inf, 0.0, -np.inf, 0.0])
+        return (weight * np.inf * P if P != 0 else 0.0), np.zeros(V), np.array([-np.inf, 0.0, -np.inf, 0.0])
     m = z.max()
     x = (z - m) / T
     S = np.exp(x).sum()

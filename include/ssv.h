@@ -875,7 +875,9 @@ SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
  * start on 16-byte boundaries are fastest.  1 <= V <= 524288.  T: positive
  * and finite.  No workspace; sums and results are the same from call to call.
  * -inf marks a token that cannot be: it has probability 0.  A result beyond
- * fp32's range (the lse of a row at the type's lowest number, T < 1) is infinite.
+ * fp32's range (the lse of a row at the type's lowest number, T < 1) is infinite,
+ * and so is a difference of two logits of a row beyond it, whatever T: the lower
+ * one then has probability 0 and log-probability -inf, as one of -inf.
  * ---------------------------------------------------------------------- */
 
 /* ------------------------------------------------------------------------

@@ -23,11 +23,12 @@
 // Bound by HBM and by instructions alike: each logit is fetched from HBM once and
 // each gradient written once (4096 rows of 151936 bf16, K = 128: DRAM traffic at the
 // 2.49 GB that there are), 18 instructions per element at 2.5 per cycle.
-// Measured: that case 424 us, 88% of the copy rate (475 us with whole rows per CTA,
-// which outgrow L2: 1.2 times the traffic; 677 us in quarters, whose ring and
-// target are too much for a part; 463 us with a ring of two steps; first steps again
-// first, a row per CTA: 534 us beside 492); 1024 rows, K = 64, 109 us (81%); 700 fp32
-// rows of 32003 34.3 us; the loss of 32 rows 6.6 us, latency.
+// Measured: that case 424 .. 427 us, 87% of the copy rate (at earlier steps: 475 us
+// with whole rows per CTA, which outgrow L2: 1.2 times the traffic; 677 us in
+// quarters, whose ring and target are too much for a part; first steps again first, a
+// row per CTA: 534 us beside 492); 1024 rows, K = 64, 110 us (80%); 700 fp32
+// rows of 32003 34.3 us; the loss of 32 rows 6.6 us, latency, of 4096 rows, K = 128,
+// 194 us (96%), of 1024 rows 55 us (84%).
 //
 // ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
 // that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
@@ -431,15 +432,20 @@ struct Shared {
   uint32_t part[THREADS / 32 * kMaxCluster][4];  // of every warp: maximum and sum (a pair) of its other tokens
 };
 
-// Steps in flight: three with the gradient, which find the last three fifths of a part of 152 KB there (4096 rows: 428 us; two 433).
+// Steps in flight: three with the gradient, which find the last three fifths of a part of 152 KB there (4096 rows, when it was
+// taken: 428 us; two 433).  With 256 threads a ring of two would let a fourth CTA onto an SM for parts above 48 KB (700 fp32
+// rows of 32003: 35.3 us with three, 31.2 with two; other sizes 18.9 -> 14.8, 112 -> 96, but also 47 -> 51 and 125 -> 135).
 template <bool GRAD> constexpr int kStages = GRAD ? 3 : 2;
 
-// LOG_NT: 2^LOG_NT threads share a row, so that a step's addresses are constants apart (4096 rows 444 us where known at the
-// launch alone took 451); 0: as many as the launch says, for rows that are too short for them.  TEAM warps bring the target.
-// most threads that share a row, and how many CTAs of them an SM is to hold (fewer registers would spill)
+// Most threads that share a row, and how many CTAs of them the registers are to leave room for on an SM (one more would
+// spill by tens of bytes; distill_kernel<bf16, true, 0, 1> spills 4 as it is).  Shared memory may hold fewer: of 256 threads
+// with the gradient four only where a part has at most three steps (48 KB), three above.
 constexpr int most_threads(bool grad, int log_nt) { return grad && log_nt == 9 ? kThreads : kThreads / 2; }
 constexpr int ctas_per_sm(bool grad, int log_nt, int team) { return !grad ? 4 : log_nt == 9 ? 2 : team == 1 ? 4 : 3; }
 
+// LOG_NT: 2^LOG_NT threads share a row, so that a step's addresses are constants apart (when it was taken: 4096 rows 444 us,
+// known at the launch alone 451); 0: as many as the launch says, for rows that are too short for them.  TEAM warps bring the
+// target.
 template <typename T, bool GRAD, int LOG_NT, int TEAM>
 __global__ void __launch_bounds__(most_threads(GRAD, LOG_NT) + 32 * TEAM, ctas_per_sm(GRAD, LOG_NT, TEAM))
     distill_kernel(const DistillParams p) {
@@ -777,8 +783,8 @@ cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   // threads, in which steps are shorter and one CTA's barriers are other CTAs' time (rows of 100277 bf16: 147 us with 512
   // threads, 124 with 256; of 9001 fp32: 27 and 20 us).  The loss alone reads a row once: no limit, and 256 threads (32
   // rows: 6.6 us; 512 threads 8.3 us).
-  // Short parts are as many as fit an SM at a time (64 rows of 151936 bf16, K = 64: 12.2 us, 18.9 where one fewer fits;
-  // 150, K = 128: 17.9 us, 24.0 with one more).
+  // Rows are cut further while all parts are no more than an SM holds of short ones at a time, on 152 SMs (64 rows of 151936
+  // bf16, K = 64: 12.2 us, 18.9 where one fewer fits; 150, K = 128: 17.9 us, 24.0 with one more).
   const int per_sm = GRAD && p.K > 64 ? 3 : 4;
   RowSplit sp = distill_split(n, p.V, sizeof(T), GRAD ? 160 * 1024 : 1 << 20, kMaxCluster, 256, 152 * per_sm);
   if (GRAD && sp.vectors > 128 * 1024 / 16) sp = split_of(row_vectors(p.V, sizeof(T)), sp.ctas, 512);
@@ -787,8 +793,8 @@ cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   p.slot_bytes = 16 * kStages<GRAD> * kBatch * sp.threads + kSlotSlack;
   const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
   // The target is as long on its way as the row's first reading where a warp has four tokens per lane: two warps for more
-  // than 64 tokens (4096 rows, K = 128: 428 us; one warp 444, four 435, whose registers do not suffice), one for fewer (1024
-  // rows, K = 64: 109 us; two 111) and for the loss, of whose 256 threads two take more room (32 rows, K = 32: 6.6 us; two
+  // than 64 tokens (when it was taken, 4096 rows, K = 128: 428 us; one warp 444, four 435, whose registers do not suffice),
+  // one for fewer (1024 rows, K = 64: 109 us; two 111) and for the loss, of whose 256 threads two take more room (32 rows, K = 32: 6.6 us; two
   // 7.8).
   if constexpr (GRAD)
     if (p.K > 64) return distill_launch_team<T, GRAD, 2>(p, n, sp, smem, st);

@@ -26,19 +26,29 @@
 // more than K, go to the cluster's first CTA as keys (order of the value above
 // the complemented index: equal values in the order of their indices).  It ranks
 // them by counting.  Where more pass than its list holds (long runs of equal
-// values), it finds the K-th key by bisection over the row.
+// values, and rows masked with a number instead of -inf that leave fewer than K
+// tokens, whose threshold is the mask), it finds the K-th key by bisection over the
+// row: some fifty readings by one CTA.
 //
 // Bound by HBM in the long cases, though 9 instructions per element (the
-// exponential, the sum for the entropy, two maxima, the rank) are close behind, by
-// latency in the short ones: one dependent load, the first copies, a step, two
-// cluster barriers and the ranking of the alternatives.  CTAs are small, so
+// exponential, the sum for the entropy, two maxima, the rank) are close behind.  The
+// short ones are bound by latency, more than half of it behind the pass (of 19200
+// cycles for one row the pass is 5700, the first exchange of the cluster 3400,
+// results and threshold 1900, reading again and listing 2000, the second exchange
+// 2100; of 21900 for a short masked row the pass is 5600, results and threshold
+// 3700, batches 1400, reading again and listing 4900, ranking 1800).  With
+// alternatives a cluster meets three times, without them twice.  CTAs are small, so
 // that six on an SM keep copies in flight while some rank.
-// Measured: 8192 rows of 151936 bf16 without alternatives 374 us, 99% of the copy
-// rate (391 us with the threads known at the launch alone; then registers for seven
-// CTAs per SM 430 us, loads into registers 403 us, 256 threads 417 us); 960
-// fp32 rows, 30% of them idle, with 32 alternatives 74 us, 84% (256 threads 86 us;
-// rows in halves 92 us); 64 rows with 20 alternatives 13.2 us; one row 9.7 us; 300
-// rows of 9001 fp32, nine tenths masked, with 64 alternatives 14 us.
+// Measured: 8192 rows of 151936 bf16 without alternatives 371 us, the copy rate
+// (registers for seven CTAs per SM 430 us, loads into registers 403 us, 256 threads
+// 417 us, each beside 383 .. 391); with tokens at random, whose ranks are long counts,
+// 389 us, with 20 alternatives 434, with 128 588; 960 fp32 rows, 30% of them idle,
+// with 32 alternatives 73 us, 85% (256 threads 86 us, rows in halves 92 us, beside
+// 77); 64 rows with 20 alternatives 13.4 us; one row 9.6 us; 300 rows of 9001 fp32,
+// nine tenths masked, with 64 alternatives 13.6 us.
+// By bisection, all but 3 of 151936 bf16 tokens masked with the type's lowest number
+// and 20 asked for: one row 3.6 ms, 64 rows 3.9 ms, 960 rows 10.7 ms (with -inf 10.8,
+// 13.2 and 59.7 us); rows that are all equal 1.4, 1.5 and 4.2 ms.
 #include "logits.cuh"
 
 #include <algorithm>
@@ -249,8 +259,8 @@ __device__ __noinline__ void bisect_top(const RowView<T>& row, int K, float leas
   __syncthreads();
 }
 
-// LOG_NT: 2^LOG_NT threads in a CTA, so that a step's addresses are constants apart (8192 rows 379 us where known at the
-// launch alone took 391); 0: as many as the launch says, for short rows.
+// LOG_NT: 2^LOG_NT threads in a CTA, so that a step's addresses are constants apart (when it was taken: 8192 rows 379 us,
+// known at the launch alone 391); 0: as many as the launch says, for short rows.
 template <typename T, bool TOP, int LOG_NT>
 __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LogprobsParams p) {
   extern __shared__ __align__(128) unsigned char dynamic[];  // the ring, then the lists; behind them each batch's maximum
@@ -546,8 +556,9 @@ cudaError_t logprobs_launch(const LogprobsParams& p, int n, const RowSplit& sp, 
   return TOP || sp.log_nt == 7 ? logprobs_launch_as<T, TOP, 7>(p, n, sp, st) : logprobs_launch_as<T, TOP, 0>(p, n, sp, st);
 }
 
-// CTAs per row: more of them while they stay below three per SM and a CTA has more than two steps (64 rows of 151936
-// bf16, four CTAs each: 13.4 us; two 17.2 us; eight 15.2 us.  300 rows of 9001 fp32, one each: 12.9 us; two 14.2 us).
+// CTAs per row: more of them while they stay below three per SM (of the 152 that the part has) and a CTA has more than two
+// steps (64 rows of 151936 bf16, four CTAs each: 13.4 us; two 17.2 us; eight 15.2 us.  300 rows of 9001 fp32, one each:
+// 12.9 us when measured beside two, 14.2 us).
 RowSplit logprobs_split(int rows, int V, int element_size, int top_k) {
   // alternatives are ranked by every thread: none of them less for a short row
   const int vectors = std::max(row_vectors(V, element_size), top_k > 0 ? kThreads : 1);

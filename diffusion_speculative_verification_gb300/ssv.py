@@ -860,7 +860,10 @@ def logprobs(logits, tokens=None, top_k: int = 0, T: float = 1.0, rows=None, out
     entry i has logits row rows[i] (int32 [n]; without it row i).  Returns
     (logprob [n], rank [n], entropy [n], lse [n], top_logprob [n, top_k],
     top_token [n, top_k]); logprob and rank are None without tokens, the
-    last two with top_k 0.  ``out``: six tensors (or None) of those shapes."""
+    last two with top_k 0.  ``out``: six tensors (or None) of those shapes,
+    for calls in a loop (making them is most of a short call's time).  Mask
+    with -inf where alternatives are asked for: a row masked with a number
+    that leaves fewer tokens than top_k takes milliseconds."""
     torch = _torch()
     what, f32, i32 = "ssv_logprobs", torch.float32, torch.int32
     stride, dt = _logit_rows(logits, what), _dtype_code(logits)
@@ -936,8 +939,10 @@ def distill(logits, teacher_token, teacher_logprob, T: float = 1.0, mode: int = 
     be strided) against the target's alternatives (teacher_token int32,
     teacher_logprob fp32 [n, K], as logprobs returns them; token -1: absent),
     times weight [n].  Returns (loss [n], stats [n, 4], grad); grad is None
-    unless it is asked for (True) or given (a tensor like the logits, which may
-    be the logits themselves).  stats is what distill_backward takes."""
+    unless it is asked for (True: rows may be strided as the logits' are) or
+    given (a tensor like the logits, which may be the logits themselves).
+    stats is what distill_backward takes.  Not part of autograd: no result has
+    a grad_fn; the gradient goes on with logits.backward(grad)."""
     torch = _torch()
     what = "ssv_distill"
     if logits.dim() != 2:
@@ -962,7 +967,8 @@ def distill_backward(logits, teacher_token, teacher_logprob, stats, grad_loss=No
     """Gradient of sum(grad_loss * loss) for distill's losses on the same
     arguments, from the statistics that it returned; grad_loss [n] fp32 (None:
     ones).  grad: a tensor like the logits, which may be the logits themselves
-    (allocated here when not given).  Returns grad."""
+    (allocated here when not given, rows strided as theirs may be).  Returns
+    grad, for logits.backward(grad)."""
     what = "ssv_distill_backward"
     if logits.dim() != 2:
         raise SsvError(SSV_ERR_INVALID, f"{what}: logits are [rows, V]")

@@ -903,6 +903,10 @@ SSV_API ssv_status ssv_commit_fp8(const ssv_commit_fp8_args* a, void* stream);
  * NaN logits are in no order (never listed, never before another; the rank of
  * such a token is 0).  A row of nothing but -inf gives lse = logprob = -inf,
  * entropy 0 and no alternatives.
+ * Mask with -inf where alternatives are asked for: where a row has more than 512
+ * elements equal to its top_k-th largest (masked with a number, with fewer tokens
+ * left than top_k; or all equal), that one is searched for by reading the row some
+ * fifty times (milliseconds for 151936 tokens instead of microseconds).
  * tokens given: logprob is not NULL; not given: logprob and rank are NULL.
  * rank, entropy, lse may be NULL.  0 <= top_k <= 128; top_logprob, top_token
  * [n, top_k] (NULL for 0).  Outputs overlap no input
@@ -974,8 +978,8 @@ SSV_API ssv_status ssv_logprobs(const ssv_logprobs_args* a, void* stream);
  * tokens are all absent has the loss and gradient 0.
  * Sums over a row are fp32 per thread and joined in 48 bits; u is summed from the
  * tokens that are not listed; the loss, a small difference of logarithms, is
- * formed in 48 bits and rounded once.  The gradient is formed in fp32 and
- * rounded once.
+ * formed in 48 bits and rounded once.  The gradient is formed in fp32, from r and
+ * the exponent of u to 48 bits, and rounded once.
  * 1 <= K <= 128.
  * Errors: SSV_ERR_INVALID, SSV_ERR_NOT_FINITE (T), SSV_ERR_UNSUPPORTED (V, K),
  * SSV_ERR_CUDA; on device SSV_ERR_INVALID for a listed token outside [-1, V)

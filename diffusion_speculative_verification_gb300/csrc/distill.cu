@@ -26,14 +26,14 @@
 // Measured: that case 424 .. 427 us, 87% of the copy rate (at earlier steps: 475 us
 // with whole rows per CTA, which outgrow L2: 1.2 times the traffic; 677 us in
 // quarters, whose ring and target are too much for a part; first steps again first, a
-// row per CTA: 534 us beside 492); 1024 rows, K = 64, 110 us (80%); 700 fp32
+// row per CTA: 534 us beside 492); 1024 rows, K = 64, 109 us (81%); 700 fp32
 // rows of 32003 34.3 us; the loss of 32 rows 6.6 us, latency, of 4096 rows, K = 128,
 // 194 us (96%), of 1024 rows 55 us (84%).
 //
 // ssv_distill_backward.  The same second part from the statistics, in parts of 48 KB
 // that a CTA holds in shared memory: 1500 rows of 151936 fp32 248 us, 7.0 TB/s, a
 // little above a copy (parts of 96 KB 276 us); 2000 rows of 9001 bf16, padded, 12.0
-// us; 32 rows of 151936 bf16 5.6 us.
+// us; 32 rows of 151936 bf16 5.4 us.
 #include "logits.cuh"
 
 #include <algorithm>
@@ -151,8 +151,8 @@ __device__ __forceinline__ void weigh_listed(const DistillParams& p, Listed<TEAM
   const bool as_is = p.mode == SSV_DISTILL_REST;
   // What an exponential rounded to 32 bits is off by, from its logarithm: the rest is what the sum leaves of 1, and the other
   // tokens' gradient is what r leaves of u, so that bf16 shows it too (r of 1e-6 would be off by up to 7%; 32 rows bf16 5.2
-  // us without, 5.6 with it).  Without a rest it is no more than what the drafter's own exponentials are off by (2000 rows
-  // of 9001 bf16: 12.0 us without, 13.0 with it).
+  // us without, 5.4 with it).  Without a rest it is no more than what the drafter's own exponentials are off by (2000 rows
+  // of 9001 bf16: 12.0 us without; with it, when it was taken, 13.0).
   const bool exact = LOSS || sizeof(T) == 4 || as_is;
   float mx = -INFINITY, top = -INFINITY, e[kEach], off[kEach];
   Pair all = {0.f, 0.f};

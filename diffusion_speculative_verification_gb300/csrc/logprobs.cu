@@ -32,8 +32,8 @@
 //
 // Bound by HBM in the long cases, though 9 instructions per element (the
 // exponential, the sum for the entropy, two maxima, the rank) are close behind.  The
-// short ones are bound by latency, more than half of it behind the pass (of 19200
-// cycles for one row the pass is 5700, the first exchange of the cluster 3400,
+// short ones are bound by latency, more than half of it behind the pass (stamps of
+// an earlier, alike form: of 19200 cycles for one row the pass is 5700, the first exchange of the cluster 3400,
 // results and threshold 1900, reading again and listing 2000, the second exchange
 // 2100; of 21900 for a short masked row the pass is 5600, results and threshold
 // 3700, batches 1400, reading again and listing 4900, ranking 1800).  With
@@ -44,8 +44,8 @@
 // 417 us, each beside 383 .. 391); with tokens at random, whose ranks are long counts,
 // 389 us, with 20 alternatives 434, with 128 588; 960 fp32 rows, 30% of them idle,
 // with 32 alternatives 73 us, 85% (256 threads 86 us, rows in halves 92 us, beside
-// 77); 64 rows with 20 alternatives 13.4 us; one row 9.6 us; 300 rows of 9001 fp32,
-// nine tenths masked, with 64 alternatives 13.6 us.
+// 77); 64 rows with 20 alternatives 13.3 us; one row 9.5 us; 300 rows of 9001 fp32,
+// nine tenths masked, with 64 alternatives 12.8 us.
 // By bisection, all but 3 of 151936 bf16 tokens masked with the type's lowest number
 // and 20 asked for: one row 3.6 ms, 64 rows 3.9 ms, 960 rows 10.7 ms (with -inf 10.8,
 // 13.2 and 59.7 us); rows that are all equal 1.4, 1.5 and 4.2 ms.

@@ -33,12 +33,12 @@
 // Bound by HBM in the long cases, though 9 instructions per element (the
 // exponential, the sum for the entropy, two maxima, the rank) are close behind.  The
 // short ones are bound by latency, more than half of it behind the pass (stamps of
-// an earlier, alike form: of 19200 cycles for one row the pass is 5700, the first exchange of the cluster 3400,
-// results and threshold 1900, reading again and listing 2000, the second exchange
-// 2100; of 21900 for a short masked row the pass is 5600, results and threshold
-// 3700, batches 1400, reading again and listing 4900, ranking 1800).  With
-// alternatives a cluster meets three times, without them twice.  CTAs are small, so
-// that six on an SM keep copies in flight while some rank.
+// an earlier, alike form: of 19200 cycles for one row the pass is 5700, the first
+// exchange of the cluster 3400, results and threshold 1900, reading again and
+// listing 2000, the second exchange 2100; of 21900 for a short masked row the pass
+// is 5600, results and threshold 3700, batches 1400, reading again and listing 4900,
+// ranking 1800).  With alternatives a cluster meets three times, without them twice.
+// CTAs are small, so that six on an SM keep copies in flight while some rank.
 // Measured: 8192 rows of 151936 bf16 without alternatives 371 us, the copy rate
 // (registers for seven CTAs per SM 430 us, loads into registers 403 us, 256 threads
 // 417 us, each beside 383 .. 391); with tokens at random, whose ranks are long counts,

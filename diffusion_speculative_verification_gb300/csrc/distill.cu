@@ -794,8 +794,8 @@ cudaError_t distill_launch(DistillParams& p, int n, cudaStream_t st) {
   const size_t smem = p.slot_bytes + sizeof(uint32_t) * (size_t)sp.batches() * sp.threads;
   // The target is as long on its way as the row's first reading where a warp has four tokens per lane: two warps for more
   // than 64 tokens (when it was taken, 4096 rows, K = 128: 428 us; one warp 444, four 435, whose registers do not suffice),
-  // one for fewer (1024 rows, K = 64: 109 us; two 111) and for the loss, of whose 256 threads two take more room (32 rows, K = 32: 6.6 us; two
-  // 7.8).
+  // one for fewer (1024 rows, K = 64: 109 us; two 111) and for the loss, of whose 256 threads two take more room (32 rows,
+  // K = 32: 6.6 us; two 7.8).
   if constexpr (GRAD)
     if (p.K > 64) return distill_launch_team<T, GRAD, 2>(p, n, sp, smem, st);
   return distill_launch_team<T, GRAD, 1>(p, n, sp, smem, st);

@@ -37,8 +37,8 @@ def sharp(r, n, v, K, rest, factor, dtype, T, spread):
     token = np.stack([r.permutation(v)[:K] for _ in range(n)]).astype(np.int32)
     p = np.full((n, K), rest / 4 / K)
     head = min(K, 3) if spread else 1
-    p[:, :head] = (1 - rest - p[:, head:].sum(1, keepdims=True)) * (np.array([0.5, 0.3, 0.2])[:head] / np.array([0.5, 0.3, 0.2])[:head].sum()
-                                                                    if spread else 1.0)
+    share = np.array([0.5, 0.3, 0.2])[:head] if spread else np.ones(1)
+    p[:, :head] = (1 - rest - p[:, head:].sum(1, keepdims=True)) * (share / share.sum())
     others = np.ones((n, v), bool)
     np.put_along_axis(others, token.astype(np.int64), False, 1)
     s = np.where(others, np.exp(z / T), 0).sum(1)

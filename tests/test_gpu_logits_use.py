@@ -1,4 +1,4 @@
-"""The operators on logits as the README shows them: the map of accepted tokens' rows, and a gradient that goes on into the
+"""The operators on logits as a program uses them: the map of accepted tokens' rows, and a gradient that goes on into the
 drafter's own graph."""
 import numpy as np
 import pytest
